@@ -638,6 +638,121 @@ typedef struct {
 size_t moe_backward_mx_workspace_size(int T, int d, int E, int k, int I, int recompute);
 moe_status moe_backward_mx(const moe_bwd_mx_args *args, void *stream);
 
+/* ------------------------------------- FP8 with a scale for each block of 128
+ * ([TTN] outlook: FP8 low-precision compute; the pages fix no format.)  E4M3
+ * elements with one fp32 scale per block: of token rows 1 x 128 along the
+ * contraction, of weights 128 x 128 (a short block at the end of an axis holds
+ * what is left).  An element stands for scale * E4M3(code).  Quantisation, with
+ * amax the block's largest magnitude or 2^-100 if that is more:
+ *   scale = fl32(amax / 448),  code = E4M3( fl32(v * fl32(448 / amax)) )
+ * to the nearest value, ties to even.  A block with a NaN gets scale NaN; one
+ * with an infinity gets scale infinity (so results that depend on it are not
+ * finite).  The matmuls take any scales, not only those of this rule.
+ * Arrays: rows q [rows, K], s [rows, ceil(K/128)]; weights q [G, N, K],
+ * s [G, ceil(N/128), ceil(K/128)]; dense, 16-byte aligned. */
+
+/* Scales per row of K elements: ceil(K / 128). */
+int moe_fp8_scale_cols(int K);
+
+/* Quantises bf16 rows [rows, K] in 1 x 128 blocks.  K % 16 == 0. */
+moe_status moe_fp8_quantize(const uint16_t *src, long long rows, int K, uint8_t *q, float *s,
+                            void *stream);
+
+/* Dispatch gather into FP8 rows ([HP41] §2.3 MegaMoE token dispatch): token row
+ * x[t] is quantised once and written to rows slot_row[t*k + j] (j < k) and
+ * S + t of x_perm_q [S+T, d] / x_perm_s [S+T, ceil(d/128)], S = T*k (slot_row
+ * from moe_permute with x = NULL).  d % 16 == 0, k <= 32. */
+moe_status moe_fp8_gather(const uint16_t *x, const int32_t *slot_row, int T, int d, int k,
+                          uint8_t *x_perm_q, float *x_perm_s, void *stream);
+
+/* Quantises weights [G, N, K] bf16 in 128 x 128 blocks; with qt and st (both or
+ * neither), also writes the transposed copy qt [G, K, N], st [G, ceil(K/128),
+ * ceil(N/128)]: the same codes and scales, the operand of the data gradient.
+ * N % 16 == 0 and K % 16 == 0. */
+moe_status moe_fp8_quantize_weights(const uint16_t *src, int G, int N, int K, uint8_t *q,
+                                    float *s, uint8_t *qt, float *st, void *stream);
+
+/* Grouped matmul: for every group g < G and row r in [offsets[g], offsets[g+1])
+ *   out[r, n] = bf16( w_r sum_b a_s[r, b] b_s[g, n/128, b]
+ *                         sum_{k in block b} a_q[r, k] b_q[g, n, k] )
+ * with fp32 sums, w_r = row_weight[r] for r < w_rows (row_weight NULL or r >=
+ * w_rows: 1).  a_q [R, K], offsets int32 [G+1] on the device with R =
+ * offsets[G] <= max_rows, b_q [G, N, K], out [R, N] bf16.  G = 1 is a dense
+ * product.  The data gradient is the same call with the transposed weight
+ * (N and K exchanged) and the quantised output gradient.  K % 16 == 0,
+ * N % 8 == 0, 1 <= G <= 1025. */
+moe_status moe_fp8_matmul(const uint8_t *a_q, const float *a_s, const int32_t *offsets, int G,
+                          int max_rows, const uint8_t *b_q, const float *b_s,
+                          const float *row_weight, int w_rows, int N, int K, uint16_t *out,
+                          void *stream);
+
+/* Weight gradient of the grouped matmul: for every group g < G
+ *   dW[g, m, n] = sum_b sa[b, m] sb[b, n] sum_{r in block b} aq[r, m] bq[r, n]
+ * where the blocks are 128 rows each from the group's first row and both
+ * operands are quantised here, every column of a block one scale block (the
+ * rule above).  a [R, M], b [R, N] bf16, dW [G, M, N] fp32 (overwritten; zeros
+ * for a group without rows).  M % 8 == 0, N % 8 == 0, 1 <= G <= 1025.
+ * Workspace: moe_fp8_wgrad_workspace_size(G, max_rows, M, N) bytes (0: not
+ * supported). */
+size_t moe_fp8_wgrad_workspace_size(int G, int max_rows, int M, int N);
+moe_status moe_fp8_wgrad(const uint16_t *a, const uint16_t *b, const int32_t *offsets, int G,
+                         int max_rows, int M, int N, float *dW, void *ws, size_t ws_bytes,
+                         void *stream);
+
+/* The expert FFN on FP8 rows: moe_expert_ffn with FP8 operands.
+ *   [g | u] = x~[r] W13~[g]^T
+ *   h~[r]   = FP8( silu(min(g, clamp)) * clamp(u, -clamp, clamp) ) along I
+ *   y[r]    = bf16( row_weight[r] * (h~[r] W2~[g]^T) )
+ * x_perm_q [R, d] / x_perm_s, W13_q [G, 2I, d] / W13_s, W2_q [G, d, I] / W2_s;
+ * outputs h_q [R, I], h_s [R, I/128] and y_perm [R, d] bf16.  d % 128 == 0,
+ * I % 128 == 0 (else MOE_ERR_UNSUPPORTED).  No workspace. */
+moe_status moe_expert_ffn_fp8(const uint8_t *x_perm_q, const float *x_perm_s,
+                              const int32_t *offsets, int G, int max_rows, const uint8_t *W13_q,
+                              const float *W13_s, const uint8_t *W2_q, const float *W2_s,
+                              const float *row_weight, int S, int d, int I, float clamp,
+                              uint8_t *h_q, float *h_s, uint16_t *y_perm, void *stream);
+
+/* ------------------------------------------------ the layer for a few tokens
+ * The whole forward of one layer for 1 <= T <= 32 tokens in two launches, for
+ * decoding: gate and routing as moe_gate_route, then every hit expert's and the
+ * shared expert's weights read once while the tokens' rows go through them,
+ *   h[t,j] = bf16( silu(min(g, clamp)) clamp(u, -clamp, clamp) )
+ *   y[t]   = bf16( h_shared W2[E]^T + sum_j weights[t,j] (h[t,j] W2[e_j]^T) )
+ * with fp32 sums throughout.  The expert weights are bf16 (W13 [E+1, 2I, d] and
+ * W2 [E+1, d, I]) or FP8 in 128 x 128 blocks (W13_q, W13_s, W2_q, W2_s); the
+ * other set is NULL.  Tokens stay bf16 in both.  Supported: d % 128 == 0,
+ * I % 64 == 0, k <= min(8, E), E <= 1024.
+ * Workspace: moe_few_workspace_size bytes (0: not supported), ZERO before its
+ * first use; every call leaves its counters zero again, so a buffer is zeroed
+ * once and then kept for calls of the same sizes (other sizes: zero it again).
+ * Calls that share a workspace must be in order on one stream. */
+typedef struct {
+    int T, d, E, k, I;
+    float scaling, clamp;
+    int mode;                     /* moe_route_mode */
+    int vocab;
+    const uint16_t *x;            /* [T,d] */
+    const uint16_t *W_g;          /* [E,d] */
+    const float *logit_offset;    /* [E] or NULL */
+    const float *bias;            /* [2,E] (top-k mode) */
+    const uint8_t *is_vision;     /* [T] or NULL */
+    const int32_t *input_ids;     /* [T] (hash mode) */
+    const int32_t *tid2eid;       /* [vocab,k] (hash mode) */
+    const uint16_t *W13;          /* bf16 weights ... */
+    const uint16_t *W2;
+    const uint8_t *W13_q;         /* ... or FP8 codes and scales */
+    const float *W13_s;
+    const uint8_t *W2_q;
+    const float *W2_s;
+    uint16_t *y;                  /* [T,d] out */
+    int32_t *ids;                 /* [T,k] out or NULL */
+    float *weights;               /* [T,k] out or NULL */
+    void *ws;
+    size_t ws_bytes;
+} moe_few_args;
+size_t moe_few_workspace_size(int T, int d, int E, int k, int I);
+moe_status moe_layer_few(const moe_few_args *args, void *stream);
+
 /* Text of a status code (static storage). */
 const char *moe_status_string(moe_status s);
 

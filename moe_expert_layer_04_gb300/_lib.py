@@ -42,7 +42,10 @@ EXPORTS = ["moe_workspace_size", "moe_route", "moe_route_logits", "moe_gate_rout
            "moe_set_gemm_pairs", "moe_mx_sf_pitch", "moe_mx_quantize", "moe_mx_gather", "moe_expert_ffn_mx",
            "moe_expert_gemm1_mx", "moe_expert_gemm2_mx", "moe_mx_quantize_t",
            "moe_expert_bwd_mx_workspace_size", "moe_expert_ffn_backward_mx",
-           "moe_backward_mx_workspace_size", "moe_backward_mx", "moe_mx_quantize_both"]
+           "moe_backward_mx_workspace_size", "moe_backward_mx", "moe_mx_quantize_both",
+           "moe_fp8_scale_cols", "moe_fp8_quantize", "moe_fp8_gather", "moe_fp8_quantize_weights",
+           "moe_fp8_matmul", "moe_fp8_wgrad_workspace_size", "moe_fp8_wgrad",
+           "moe_expert_ffn_fp8", "moe_few_workspace_size", "moe_layer_few"]
 
 
 class MoeError(RuntimeError):
@@ -167,6 +170,16 @@ class BwdMxArgs(ctypes.Structure):
                 ("stage_events", ctypes.POINTER(_P))]
 
 
+class FewArgs(ctypes.Structure):
+    """Mirror of moe_few_args."""
+    _fields_ = [("T", _I), ("d", _I), ("E", _I), ("k", _I), ("I", _I),
+                ("scaling", _F), ("clamp", _F), ("mode", _I), ("vocab", _I),
+                ("x", _P), ("W_g", _P), ("logit_offset", _P), ("bias", _P), ("is_vision", _P),
+                ("input_ids", _P), ("tid2eid", _P), ("W13", _P), ("W2", _P), ("W13_q", _P),
+                ("W13_s", _P), ("W2_q", _P), ("W2_s", _P), ("y", _P), ("ids", _P),
+                ("weights", _P), ("ws", _P), ("ws_bytes", _Z)]
+
+
 MOE_BWD_STAGE_NAMES = ["recompute_gather", "recompute_gemm1", "gather_dY", "dgrad2", "wgrad2",
                        "dgrad1", "wgrad1", "router_bwd", "dX", "dW_g"]
 MOE_BWD_STAGES = len(MOE_BWD_STAGE_NAMES)
@@ -216,6 +229,17 @@ _SIGS = {
     "moe_expert_ffn_backward_mx": ([ctypes.POINTER(ExpertBwdMxArgs), _P], _I),
     "moe_backward_mx_workspace_size": ([_I, _I, _I, _I, _I, _I], _Z),
     "moe_backward_mx": ([ctypes.POINTER(BwdMxArgs), _P], _I),
+    "moe_fp8_scale_cols": ([_I], _I),
+    "moe_fp8_quantize": ([_P, _LL, _I, _P, _P, _P], _I),
+    "moe_fp8_gather": ([_P, _P, _I, _I, _I, _P, _P, _P], _I),
+    "moe_fp8_quantize_weights": ([_P, _I, _I, _I, _P, _P, _P, _P, _P], _I),
+    "moe_fp8_matmul": ([_P, _P, _P, _I, _I, _P, _P, _P, _I, _I, _I, _P, _P], _I),
+    "moe_fp8_wgrad_workspace_size": ([_I, _I, _I, _I], _Z),
+    "moe_fp8_wgrad": ([_P, _P, _P, _I, _I, _I, _I, _P, _P, _Z, _P], _I),
+    "moe_expert_ffn_fp8": ([_P, _P, _P, _I, _I, _P, _P, _P, _P, _P, _I, _I, _I, _F, _P, _P, _P,
+                            _P], _I),
+    "moe_few_workspace_size": ([_I, _I, _I, _I, _I], _Z),
+    "moe_layer_few": ([ctypes.POINTER(FewArgs), _P], _I),
     "moe_expert_gemm2_mx": ([_P, _P, _P, _I, _I, _P, _P, _P, _I, _I, _I, _P, _P], _I),
 }
 
@@ -673,3 +697,90 @@ def moe_router_backward(dw_rows, dX_perm, x_perm, offsets, ids, weights, scores_
         _ptr(dlogits, F32, "dlogits"), _ptr(dweights, F32, "dweights"), _ptr(dW_g, F32, "dW_g"),
         _ptr(ws, U8, "ws"), 0 if ws is None else ws.numel(), _stream(stream))
     _check("moe_router_backward", st)
+
+
+# ------------------------------------ FP8 with a scale for each block of 128
+
+def moe_fp8_scale_cols(K) -> int:
+    return int(load().moe_fp8_scale_cols(int(K)))
+
+
+def moe_fp8_quantize(src, rows, K, q, s, stream=None):
+    st = load().moe_fp8_quantize(_ptr(src, BF16, "src"), int(rows), int(K), _ptr(q, U8, "q"),
+                                 _ptr(s, F32, "s"), _stream(stream))
+    _check("moe_fp8_quantize", st)
+
+
+def moe_fp8_gather(x, slot_row, T, d, k, x_perm_q, x_perm_s, stream=None):
+    st = load().moe_fp8_gather(_ptr(x, BF16, "x"), _ptr(slot_row, I32, "slot_row"), T, d, k,
+                               _ptr(x_perm_q, U8, "x_perm_q"), _ptr(x_perm_s, F32, "x_perm_s"),
+                               _stream(stream))
+    _check("moe_fp8_gather", st)
+
+
+def moe_fp8_quantize_weights(src, G, N, K, q, s, qt=None, st=None, stream=None):
+    r = load().moe_fp8_quantize_weights(_ptr(src, BF16, "src"), int(G), int(N), int(K),
+                                        _ptr(q, U8, "q"), _ptr(s, F32, "s"), _ptr(qt, U8, "qt"),
+                                        _ptr(st, F32, "st"), _stream(stream))
+    _check("moe_fp8_quantize_weights", r)
+
+
+def moe_fp8_matmul(a_q, a_s, offsets, G, max_rows, b_q, b_s, row_weight, w_rows, N, K, out,
+                   stream=None):
+    st = load().moe_fp8_matmul(_ptr(a_q, U8, "a_q"), _ptr(a_s, F32, "a_s"),
+                               _ptr(offsets, I32, "offsets"), G, max_rows, _ptr(b_q, U8, "b_q"),
+                               _ptr(b_s, F32, "b_s"), _ptr(row_weight, F32, "row_weight"), w_rows,
+                               N, K, _ptr(out, BF16, "out"), _stream(stream))
+    _check("moe_fp8_matmul", st)
+
+
+def moe_fp8_wgrad_workspace_size(G, max_rows, M, N) -> int:
+    return int(load().moe_fp8_wgrad_workspace_size(G, max_rows, M, N))
+
+
+def moe_fp8_wgrad(a, b, offsets, G, max_rows, M, N, dW, ws, stream=None):
+    st = load().moe_fp8_wgrad(_ptr(a, BF16, "a"), _ptr(b, BF16, "b"),
+                              _ptr(offsets, I32, "offsets"), G, max_rows, M, N,
+                              _ptr(dW, F32, "dW"), _ptr(ws, U8, "ws"),
+                              0 if ws is None else ws.numel(), _stream(stream))
+    _check("moe_fp8_wgrad", st)
+
+
+def moe_expert_ffn_fp8(x_perm_q, x_perm_s, offsets, G, max_rows, W13_q, W13_s, W2_q, W2_s,
+                       row_weight, S, d, I, clamp, h_q, h_s, y_perm, stream=None):
+    st = load().moe_expert_ffn_fp8(_ptr(x_perm_q, U8, "x_perm_q"), _ptr(x_perm_s, F32, "x_perm_s"),
+                                   _ptr(offsets, I32, "offsets"), G, max_rows,
+                                   _ptr(W13_q, U8, "W13_q"), _ptr(W13_s, F32, "W13_s"),
+                                   _ptr(W2_q, U8, "W2_q"), _ptr(W2_s, F32, "W2_s"),
+                                   _ptr(row_weight, F32, "row_weight"), S, d, I, float(clamp),
+                                   _ptr(h_q, U8, "h_q"), _ptr(h_s, F32, "h_s"),
+                                   _ptr(y_perm, BF16, "y_perm"), _stream(stream))
+    _check("moe_expert_ffn_fp8", st)
+
+
+# ------------------------------------------------ the layer for a few tokens
+
+def moe_few_workspace_size(T, d, E, k, I) -> int:
+    return int(load().moe_few_workspace_size(T, d, E, k, I))
+
+
+_FEW_TYPES = dict(x=BF16, W_g=BF16, logit_offset=F32, bias=F32, is_vision=U8, input_ids=I32,
+                  tid2eid=I32, W13=BF16, W2=BF16, W13_q=U8, W13_s=F32, W2_q=U8, W2_s=F32, y=BF16,
+                  ids=I32, weights=F32, ws=U8)
+
+
+def moe_layer_few(args: dict, stream=None):
+    """args: the fields of moe_few_args (tensors for pointers, None for NULL);
+    ws: moe_few_workspace_size bytes, zeroed once before the first call."""
+    a = FewArgs()
+    for name, _ in FewArgs._fields_:
+        if name == "ws_bytes":
+            continue
+        v = args.get(name)
+        if name in _FEW_TYPES:
+            setattr(a, name, _ptr(v, _FEW_TYPES[name], name))
+        else:
+            setattr(a, name, 0 if v is None else v)
+    a.ws_bytes = 0 if args.get("ws") is None else args["ws"].numel()
+    st = load().moe_layer_few(ctypes.byref(a), _stream(stream))
+    _check("moe_layer_few", st)

@@ -7,6 +7,7 @@
 #include <functional>
 #include <mutex>
 
+#include "fp8_common.cuh"
 #include "moe_ptx.cuh"
 #include "mx_common.cuh"
 
@@ -75,6 +76,12 @@ __global__ void wait_timeout_kernel(long long limit, int *status) {
         const WaitCtl wc{&abort_flag, status, limit};
         mbar_wait(&bar, 0, wc);
     }
+}
+
+bool all_aligned16(std::initializer_list<const void *> ptrs) {
+    for (const void *p : ptrs)
+        if (!p || !aligned16(p)) return false;
+    return true;
 }
 
 size_t align256(size_t b) { return (b + 255) / 256 * 256; }
@@ -1195,6 +1202,160 @@ const char *moe_status_string(moe_status s) {
         case MOE_ERR_WORKSPACE: return "workspace missing or too small";
     }
     return "unknown status";
+}
+
+int moe_fp8_scale_cols(int K) { return K > 0 ? fp8_blocks(K) : 0; }
+
+moe_status moe_fp8_quantize(const uint16_t *src, long long rows, int K, uint8_t *q, float *s,
+                            void *stream) {
+    if (rows < 0 || K < 16 || K % 16 != 0) return MOE_ERR_INVALID_ARG;
+    if (rows == 0) return MOE_OK;
+    if (rows > (1LL << 40) / K) return MOE_ERR_UNSUPPORTED;
+    if (!all_aligned16({src, q, s})) return MOE_ERR_INVALID_ARG;
+    return launch_fp8_rows(src, nullptr, rows, K, 0, q, s, static_cast<cudaStream_t>(stream));
+}
+
+moe_status moe_fp8_gather(const uint16_t *x, const int32_t *slot_row, int T, int d, int k,
+                          uint8_t *x_perm_q, float *x_perm_s, void *stream) {
+    if (T < 1 || d < 16 || d % 16 != 0 || k < 1 || k > 32) return MOE_ERR_INVALID_ARG;
+    if ((long long)T * (k + 1) >= (1LL << 31) || (long long)T * (k + 1) > (1LL << 40) / d)
+        return MOE_ERR_UNSUPPORTED;
+    if (!slot_row || !all_aligned16({x, x_perm_q, x_perm_s})) return MOE_ERR_INVALID_ARG;
+    return launch_fp8_rows(x, slot_row, T, d, k, x_perm_q, x_perm_s,
+                           static_cast<cudaStream_t>(stream));
+}
+
+moe_status moe_fp8_quantize_weights(const uint16_t *src, int G, int N, int K, uint8_t *q,
+                                    float *s, uint8_t *qt, float *st, void *stream) {
+    if (G < 1 || N < 16 || K < 16 || N % 16 != 0 || K % 16 != 0) return MOE_ERR_INVALID_ARG;
+    if ((qt == nullptr) != (st == nullptr)) return MOE_ERR_INVALID_ARG;
+    if (!all_aligned16({src, q, s}) || (qt && !all_aligned16({qt, st})))
+        return MOE_ERR_INVALID_ARG;
+    return launch_fp8_weights(src, G, N, K, q, s, qt, st, static_cast<cudaStream_t>(stream));
+}
+
+// Rows times group weights: rows and weight rows are indexed by int in the
+// tensor maps.
+static bool fp8_groups_ok(int G, int max_rows) {
+    return G >= 1 && G <= 1025 && max_rows >= 0 && max_rows < (1 << 30);
+}
+
+moe_status moe_fp8_matmul(const uint8_t *a_q, const float *a_s, const int32_t *offsets, int G,
+                          int max_rows, const uint8_t *b_q, const float *b_s,
+                          const float *row_weight, int w_rows, int N, int K, uint16_t *out,
+                          void *stream) {
+    if (!fp8_groups_ok(G, max_rows) || N < 8 || N % 8 != 0 || K < 16 || K % 16 != 0 || w_rows < 0)
+        return MOE_ERR_INVALID_ARG;
+    if ((long long)G * N >= (1LL << 31)) return MOE_ERR_UNSUPPORTED;
+    if (!offsets || !all_aligned16({a_q, a_s, b_q, b_s, out})) return MOE_ERR_INVALID_ARG;
+    if (max_rows == 0) return MOE_OK;
+    return launch_fp8_matmul(a_q, a_s, offsets, G, max_rows, b_q, b_s, row_weight, w_rows, N, K,
+                             out, static_cast<cudaStream_t>(stream));
+}
+
+// Workspace of moe_fp8_wgrad: the groups' first chunks, and both operands'
+// codes and scales in chunks of 128 rows.
+namespace {
+struct Fp8WgradWorkspace {
+    int32_t *first;
+    uint8_t *aq, *bq;
+    float *as, *bs;
+    int chunks;
+    size_t bytes;
+};
+Fp8WgradWorkspace carve_fp8_wgrad(uint8_t *base, int G, int max_rows, int M, int N) {
+    Fp8WgradWorkspace w;
+    std::memset(&w, 0, sizeof w);
+    size_t off = 0;
+    auto take = [&](size_t bytes) {
+        uint8_t *p = base ? base + off : nullptr;
+        off += align256(bytes);
+        return p;
+    };
+    const int most = max_rows / 128 + G;   // each group rounds up once
+    w.chunks = max_rows < most ? (max_rows > 0 ? max_rows : 1) : most;
+    w.first = reinterpret_cast<int32_t *>(take(((size_t)G + 1) * 4));
+    w.aq = take((size_t)w.chunks * M * 128);
+    w.bq = take((size_t)w.chunks * N * 128);
+    w.as = reinterpret_cast<float *>(take((size_t)w.chunks * M * 4));
+    w.bs = reinterpret_cast<float *>(take((size_t)w.chunks * N * 4));
+    w.bytes = off;
+    return w;
+}
+bool fp8_wgrad_ok(int G, int max_rows, int M, int N) {
+    if (!fp8_groups_ok(G, max_rows) || M < 8 || N < 8 || M % 8 != 0 || N % 8 != 0) return false;
+    const long long chunks = max_rows / 128 + G;
+    return chunks <= 65535 && chunks * (M > N ? M : N) < (1LL << 31);
+}
+}  // namespace
+
+size_t moe_fp8_wgrad_workspace_size(int G, int max_rows, int M, int N) {
+    return fp8_wgrad_ok(G, max_rows, M, N) ? carve_fp8_wgrad(nullptr, G, max_rows, M, N).bytes : 0;
+}
+
+moe_status moe_fp8_wgrad(const uint16_t *a, const uint16_t *b, const int32_t *offsets, int G,
+                         int max_rows, int M, int N, float *dW, void *ws, size_t ws_bytes,
+                         void *stream) {
+    if (!fp8_groups_ok(G, max_rows) || M < 8 || N < 8 || M % 8 != 0 || N % 8 != 0)
+        return MOE_ERR_INVALID_ARG;
+    if (!fp8_wgrad_ok(G, max_rows, M, N)) return MOE_ERR_UNSUPPORTED;
+    if (!offsets || !all_aligned16({dW}) || (max_rows > 0 && !all_aligned16({a, b})))
+        return MOE_ERR_INVALID_ARG;
+    if (!ws || !aligned16(ws) || ws_bytes < carve_fp8_wgrad(nullptr, G, max_rows, M, N).bytes)
+        return MOE_ERR_WORKSPACE;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const Fp8WgradWorkspace w =
+        carve_fp8_wgrad(static_cast<uint8_t *>(ws), G, max_rows, M, N);
+    moe_status r = launch_fp8_chunks(offsets, G, w.first, st);
+    if (r == MOE_OK && max_rows > 0)
+        r = launch_fp8_columns(a, offsets, w.first, G, w.chunks, M, w.aq, w.as, st);
+    if (r == MOE_OK && max_rows > 0)
+        r = launch_fp8_columns(b, offsets, w.first, G, w.chunks, N, w.bq, w.bs, st);
+    if (r == MOE_OK)
+        r = launch_fp8_wgrad(w.aq, w.as, w.bq, w.bs, w.first, G, w.chunks, M, N, dW, st);
+    return r;
+}
+
+moe_status moe_expert_ffn_fp8(const uint8_t *x_perm_q, const float *x_perm_s,
+                              const int32_t *offsets, int G, int max_rows, const uint8_t *W13_q,
+                              const float *W13_s, const uint8_t *W2_q, const float *W2_s,
+                              const float *row_weight, int S, int d, int I, float clamp,
+                              uint8_t *h_q, float *h_s, uint16_t *y_perm, void *stream) {
+    if (!fp8_groups_ok(G, max_rows) || d < 1 || I < 1 || S < 0) return MOE_ERR_INVALID_ARG;
+    if (d % 128 != 0 || I % 128 != 0 || (long long)G * (2LL * I > d ? 2LL * I : d) >= (1LL << 31))
+        return MOE_ERR_UNSUPPORTED;
+    if (!offsets || !(clamp > 0.0f) ||
+        !all_aligned16({x_perm_q, x_perm_s, W13_q, W13_s, W2_q, W2_s, h_q, h_s, y_perm}))
+        return MOE_ERR_INVALID_ARG;
+    if (max_rows == 0) return MOE_OK;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    moe_status r = launch_fp8_ffn1(x_perm_q, x_perm_s, offsets, G, max_rows, W13_q, W13_s, d, I,
+                                   clamp, h_q, h_s, st);
+    if (r != MOE_OK) return r;
+    return launch_fp8_matmul(h_q, h_s, offsets, G, max_rows, W2_q, W2_s, row_weight, S, d, I,
+                             y_perm, st);
+}
+
+size_t moe_few_workspace_size(int T, int d, int E, int k, int I) {
+    return few_supported(T, d, E, k, I) ? few_workspace_bytes(T, d, E, k, I) : 0;
+}
+
+moe_status moe_layer_few(const moe_few_args *a, void *stream) {
+    if (!a || a->T < 1 || a->d < 1 || a->E < 1 || a->k < 1 || a->I < 1) return MOE_ERR_INVALID_ARG;
+    if (a->mode != MOE_ROUTE_TOPK && a->mode != MOE_ROUTE_HASH) return MOE_ERR_INVALID_ARG;
+    if (!few_supported(a->T, a->d, a->E, a->k, a->I)) return MOE_ERR_UNSUPPORTED;
+    if (!(a->clamp > 0.0f) || !all_aligned16({a->x, a->W_g}) || !a->y) return MOE_ERR_INVALID_ARG;
+    const bool any_bf16 = a->W13 || a->W2, any_fp8 = a->W13_q || a->W13_s || a->W2_q || a->W2_s;
+    if (any_bf16 == any_fp8) return MOE_ERR_INVALID_ARG;
+    if (any_bf16 ? !all_aligned16({a->W13, a->W2})
+                 : !all_aligned16({a->W13_q, a->W13_s, a->W2_q, a->W2_s}))
+        return MOE_ERR_INVALID_ARG;
+    if (a->mode == MOE_ROUTE_TOPK ? !a->bias : (!a->input_ids || !a->tid2eid || a->vocab < 1))
+        return MOE_ERR_INVALID_ARG;
+    if (!a->ws || !aligned16(a->ws) ||
+        a->ws_bytes < few_workspace_bytes(a->T, a->d, a->E, a->k, a->I))
+        return MOE_ERR_WORKSPACE;
+    return launch_few(a, static_cast<cudaStream_t>(stream));
 }
 
 moe_status moe_last_device_status(void *stream) {

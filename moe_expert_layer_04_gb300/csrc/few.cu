@@ -1,0 +1,726 @@
+// few.cu -- the whole layer for a few tokens (1 to 32): gate, routing, both
+// expert matmuls around the clamped SwiGLU, the shared expert and the combine,
+// in two launches.
+//
+//   logits = x W_g^T (+ offset);  ids, w = top-k or table routing
+//   h[r] = bf16( silu(min(g, c)) clamp(u, -c, c) ),  [g|u] = x[t] W13[e]^T
+//   y[t] = bf16( h_shared W2[E]^T + sum_j w[t,j] (h[t,j] W2[e_j]^T) )
+// ("HyperParallel加速DeepSeek-V4.1多模态1M长序列训练" §2.3 MegaGate and MegaMoE,
+// "MindSpore HyperParallel一键开箱DeepSeek-V4.1-Flash" §01 shared expert, at the
+// batch sizes of decoding.)
+//
+// Bound: the weights of the experts that the tokens hit cross HBM once (a few
+// rows reuse each of them), so everything else has to hide behind that stream.
+// The second kernel therefore keeps it running from its first cycle to its
+// last: a producer warp copies weight rows into a ring in shared memory
+// (cp.async.bulk) far ahead of the 16 warps that multiply, across the
+// boundaries of the phases, whose dependences only the multiplying warps wait
+// for.  The work comes as items of 16 weight rows in one order for the whole
+// grid, handed out by a counter:
+//   shared expert's W13 | W13 of the hit experts | shared expert's W2 | W2 ...
+// The first part needs no routing result, so the kernel starts on it while the
+// first kernel (gate and routing) still runs (programmatic launch).  An item
+// waits only for items before it in the order, all of which running CTAs hold,
+// so the kernel needs no particular number of resident CTAs.
+//
+// Items: 8 gate rows and the matching 8 up rows of W13 (both land in the same
+// thread, which applies the SwiGLU), or 16 rows of W2.  The 16 warps split the
+// contraction, each with mma.m16n8k16 (weights x 8 tokens, bf16, fp32 sums; at
+// a few rows a weight the matrix pipe is nearly idle, so the 128-row tiles of
+// tcgen05 would only add padding); their partial sums meet in shared memory in
+// a fixed order.  FP8 weights are expanded to bf16 in registers, exactly, and
+// each 128-block's sum takes its scale in fp32.  h is rounded to bf16 (the
+// second matmul's operand), every other sum stays fp32 up to y.  Products of
+// the second matmul go to fp32 rows per (token, slot); the last item of a
+// column group to finish adds them up in slot order, so results do not depend
+// on who finishes when.
+#include "fp8_common.cuh"
+#include "route_common.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int kFewT = 32;              // tokens at most
+constexpr int kFewK = 8;               // experts per token at most
+constexpr int kFewS = kFewT * kFewK;
+constexpr int kFewE = 1024;
+constexpr int kGateWarps = 8;
+constexpr int kGateSplits = 16;        // at most
+constexpr int kMulWarps = 16;
+constexpr int kFewThreads = 32 * (kMulWarps + 1);
+constexpr int kRowBytes = 2048;        // weight bytes of a row in a stage
+constexpr int kRowPitch = kRowBytes + 64;   // eight rows' 64-byte pieces hit all banks
+constexpr int kFewStage = 16 * kRowPitch;
+
+struct FewParams {
+    const uint16_t *x, *W_g;
+    const float *logit_offset, *bias;
+    const uint8_t *is_vision;
+    const int32_t *input_ids, *tid2eid;
+    int vocab, T, d, E, k, I, hash;
+    float scaling, clamp;
+    const void *W13, *W2;              // bf16 or E4M3 codes
+    const float *W13_s, *W2_s;         // FP8: scales
+    uint16_t *y;
+    int32_t *ids_out;                  // or null
+    float *w_out;                      // or null
+    // workspace
+    int *counters;   // [0] gate, [1] ticket, [2] exits, [4 + p] h tiles of pass p,
+                     // then columns' finished items; zero between calls
+    int n_counters;
+    float *part;     // [splits, T, E] partial logits
+    int32_t *ids;    // [T, k]
+    float *w, *ssel; // [T, k]
+    uint16_t *h;     // [S + T, I]
+    float *yp;       // [S + T, d]
+    int splits;
+    int *status;
+    long long wait_limit;
+};
+
+__device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                         uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t bytes,
+                                          uint64_t *bar) {
+    asm volatile(
+        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::
+            "r"(smem_u32(dst)),
+        "l"(src), "r"(bytes), "r"(smem_u32(bar))
+        : "memory");
+}
+
+__device__ __forceinline__ int atom_add_acq_rel(int *p, int v) {
+    int r;
+    asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], %2;" : "=r"(r) : "l"(p), "r"(v) : "memory");
+    return r;
+}
+
+// ------------------------------------------------------------ gate, routing
+//
+// A CTA takes 16 experts and one of `splits` parts of the contraction (all SMs
+// on the few megabytes of W_g), its warps every eighth step of 32; the
+// partial logits go to the workspace, and the CTA that finishes last adds
+// them in order and routes, a warp per token.  mma fragments straight from
+// global memory: a lane's 16 bytes of row l / 4 are eight consecutive k, fed
+// as two k-pairs to each of two MMAs; the token operand is read the same way,
+// so the order of k inside a step is the same on both sides.
+template <int EPL>
+__global__ void __launch_bounds__(kGateWarps * 32) few_gate_kernel(FewParams p) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    __shared__ float red[kGateWarps][4][32];
+    __shared__ int s_last;
+    __shared__ int s_e[kGateWarps][32];
+    __shared__ float s_z[kGateWarps][32], s_b[kGateWarps][32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int e0 = blockIdx.x * 16 + (lane >> 2);
+    const int steps = p.d / 32;
+    const int lo = (int)((long long)steps * blockIdx.y / p.splits);
+    const int hi = (int)((long long)steps * (blockIdx.y + 1) / p.splits);
+    const uint16_t *w0 = p.W_g + (size_t)min(e0, p.E - 1) * p.d + (lane & 3) * 8;
+    const uint16_t *w1 = p.W_g + (size_t)min(e0 + 8, p.E - 1) * p.d + (lane & 3) * 8;
+    for (int t0 = 0; t0 < p.T; t0 += 8) {
+        const int tok = t0 + (lane >> 2);
+        const uint16_t *xr = p.x + (size_t)min(tok, p.T - 1) * p.d + (lane & 3) * 8;
+        float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 4
+        for (int s = lo + warp; s < hi; s += kGateWarps) {
+            const uint4 a = __ldg(reinterpret_cast<const uint4 *>(w0 + s * 32));
+            const uint4 b = __ldg(reinterpret_cast<const uint4 *>(w1 + s * 32));
+            const uint4 v = __ldg(reinterpret_cast<const uint4 *>(xr + s * 32));
+            mma_bf16(acc, a.x, b.x, a.y, b.y, v.x, v.y);
+            mma_bf16(acc, a.z, b.z, a.w, b.w, v.z, v.w);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) red[warp][i][lane] = acc[i];
+        __syncthreads();
+        if (threadIdx.x < 128) {
+            const int l = threadIdx.x & 31, i = threadIdx.x >> 5;
+            float v = 0.0f;
+#pragma unroll
+            for (int w = 0; w < kGateWarps; ++w) v += red[w][i][l];
+            const int e = blockIdx.x * 16 + (l >> 2) + (i >> 1) * 8;
+            const int t = t0 + (l & 3) * 2 + (i & 1);
+            if (e < p.E && t < p.T) p.part[((size_t)blockIdx.y * p.T + t) * p.E + e] = v;
+        }
+        __syncthreads();
+    }
+    if (threadIdx.x == 0)
+        s_last = atom_add_acq_rel(p.counters, 1) == (int)(gridDim.x * gridDim.y) - 1;
+    __syncthreads();
+    if (!s_last) return;
+    __threadfence();
+    if (threadIdx.x == 0) p.counters[0] = 0;
+    for (int t = warp; t < p.T; t += kGateWarps) {
+        auto logit = [&](int e) {
+            float z = 0.0f;
+            for (int s = 0; s < p.splits; ++s)
+                z += __ldcg(p.part + ((size_t)s * p.T + t) * p.E + e);
+            return z + (p.logit_offset ? p.logit_offset[e] : 0.0f);
+        };
+        int my_id = 0;
+        float my_s = 0.0f;
+        if (p.hash) {
+            if (lane < p.k) {
+                int tok = p.input_ids[t];
+                if (tok < 0 || tok >= p.vocab) {
+                    record_status(p.status, MOE_ERR_INVALID_ARG);
+                    tok = 0;
+                }
+                my_id = p.tid2eid[(size_t)tok * p.k + lane];
+                if (my_id < 0 || my_id >= p.E) {
+                    record_status(p.status, MOE_ERR_INVALID_ARG);
+                    my_id = 0;
+                }
+                my_s = sigmoid_exact(logit(my_id));
+            }
+        } else {
+            const float *bt = p.bias + ((p.is_vision && p.is_vision[t]) ? p.E : 0);
+            float zv[EPL], bv[EPL];
+#pragma unroll
+            for (int i = 0; i < EPL; ++i) {
+                const int e = lane + 32 * i;
+                zv[i] = e < p.E ? logit(e) : 0.0f;
+                bv[i] = e < p.E ? bt[e] : 0.0f;
+            }
+            route_topk_token<EPL>(zv, bv, lane, p.E, p.k, s_e[warp], s_z[warp], s_b[warp], my_id,
+                                  my_s);
+        }
+        write_weights(t, p.k, lane, my_id, my_s, p.scaling, p.ids, p.w, p.ssel);
+        if (lane < p.k) {
+            const size_t o = (size_t)t * p.k + lane;
+            if (p.ids_out) p.ids_out[o] = my_id;
+            if (p.w_out) p.w_out[o] = p.w[o];
+        }
+    }
+}
+
+// ------------------------------------------------------------------ experts
+
+// What every role knows about the routing: the hit experts in order, each cut
+// into passes of at most 8 NT rows, and the slots (token * k + j) of each.
+struct FewMeta {
+    int n_pass;                        // routed passes
+    int n_units;                       // column-tile contributions a column group waits for
+    int16_t pass_e[kFewS];
+    int16_t pass_row[kFewS];           // first entry in `slot`
+    int16_t pass_n[kFewS];             // rows
+    int16_t slot[kFewS];
+    int start[kFewE];                  // scratch: rows, then first slot of each expert
+};
+
+struct FewItem {
+    int pass;       // -1 the shared expert
+    bool second;    // W2
+    int tile;
+};
+
+template <bool FP8, int NT>
+struct FewShape {
+    static constexpr int STAGES = NT == 4 ? 5 : 6;
+    static constexpr int RED = NT * kMulWarps * 128 * 4;
+    static constexpr int SMEM = STAGES * kFewStage + RED + (int)sizeof(FewMeta) + 512;
+    static constexpr int ELT = FP8 ? 1 : 2;
+    static constexpr int STAGE_K = kRowBytes / ELT;   // contraction of a stage
+    static constexpr int STEP = FP8 ? 64 : 32;        // of a step (64 bytes of a row)
+};
+
+// Items in order: shared W13, routed W13, shared W2, routed W2.
+__device__ __forceinline__ FewItem few_item(int t, int tiles1, int tiles2, int n_pass) {
+    FewItem it;
+    it.pass = -1;
+    it.second = false;
+    it.tile = t;
+    if (t < tiles1) return it;
+    t -= tiles1;
+    if (t < n_pass * tiles1) {
+        it.pass = t / tiles1;
+        it.tile = t - it.pass * tiles1;
+        return it;
+    }
+    t -= n_pass * tiles1;
+    it.second = true;
+    it.pass = t / tiles2 - 1;
+    it.tile = t % tiles2;
+    return it;
+}
+
+// Eight E4M3 codes' worth: four codes -> two bf16 pairs (exact).
+__device__ __forceinline__ void e4m3x4_bf16(uint32_t w, uint32_t &lo, uint32_t &hi) {
+    uint32_t a, b;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(a) : "h"((uint16_t)(w & 0xFFFFu)));
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(b) : "h"((uint16_t)(w >> 16)));
+    const float2 fa = __half22float2(*reinterpret_cast<const __half2 *>(&a));
+    const float2 fb = __half22float2(*reinterpret_cast<const __half2 *>(&b));
+    lo = pack_bf16x2(fa.x, fa.y);
+    hi = pack_bf16x2(fb.x, fb.y);
+}
+
+template <bool FP8, int NT>
+__global__ void __launch_bounds__(kFewThreads, 1) few_experts_kernel(const FewParams p) {
+    using SH = FewShape<FP8, NT>;
+    extern __shared__ __align__(128) uint8_t smem[];
+    uint8_t *ring = smem;
+    float *red = reinterpret_cast<float *>(smem + SH::STAGES * kFewStage);
+    FewMeta *meta = reinterpret_cast<FewMeta *>(smem + SH::STAGES * kFewStage + SH::RED);
+    uint64_t *full = reinterpret_cast<uint64_t *>(meta + 1);
+    uint64_t *empty = full + SH::STAGES;
+    uint64_t *rfull = empty + SH::STAGES;    // every warp's partial sums are in `red`
+    uint64_t *rempty = rfull + 1;            // ... and have been read
+    volatile int *info = reinterpret_cast<volatile int *>(rempty + 1);   // [STAGES] item, [STAGES] k
+    volatile int *abort_s = info + 2 * SH::STAGES;
+    int *last_s = const_cast<int *>(abort_s) + 1;
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < SH::STAGES; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], kMulWarps);
+        }
+        mbar_init(rfull, kMulWarps);
+        mbar_init(rempty, kMulWarps);
+        *abort_s = 0;
+        fence_barrier_init();
+    }
+    __syncthreads();
+    const WaitCtl wc{abort_s, p.status, p.wait_limit};
+    const int S = p.T * p.k;
+    const int tiles1 = p.I / 8, tiles2 = p.d / 16;
+    int *h_done = p.counters + 4;
+    int *y_done = h_done + 1 + kFewS;
+
+    if (warp == kMulWarps) {
+        // -------------------------------------------------------- producer
+        uint32_t s = 0, ph = 0;
+        int last[SH::STAGES];
+#pragma unroll
+        for (int i = 0; i < SH::STAGES; ++i) last[i] = -1;
+        bool ok = true;
+        int n_pass = -1;
+        while (ok) {
+            int t = 0;
+            if (lane == 0) t = atomicAdd(p.counters + 1, 1);
+            t = __shfl_sync(0xffffffffu, t, 0);
+            if (t >= tiles1 && n_pass < 0) {
+                // routing results: the hit experts, their passes and slots
+                asm volatile("griddepcontrol.wait;" ::: "memory");
+                for (int e = lane; e < p.E; e += 32) meta->start[e] = 0;
+                __syncwarp();
+                int rank[kFewS / 32];
+#pragma unroll
+                for (int j = 0; j < kFewS / 32; ++j) {
+                    const int i = lane + 32 * j;
+                    rank[j] = 0;
+                    if (32 * j < S) {
+                        const int e = i < S ? __ldcg(p.ids + i) : -1 - lane;
+                        const unsigned m = __match_any_sync(0xffffffffu, e);
+                        if (i < S) rank[j] = meta->start[e] + __popc(m & ((1u << lane) - 1u));
+                        __syncwarp();
+                        if (i < S && (m & ((1u << lane) - 1u)) == 0) meta->start[e] += __popc(m);
+                        __syncwarp();
+                    }
+                }
+                int np = 0, ns = 0, units = (p.T + 7) / 8;
+                for (int base = 0; base < p.E; base += 32) {
+                    const int e = base + lane;
+                    const int n = e < p.E ? meta->start[e] : 0;
+                    const int c = (n + 8 * NT - 1) / (8 * NT);
+                    int ip = c, is = n, iu = 0;
+                    // a pass of r rows is ceil(r / 8) units
+                    iu = c > 0 ? (c - 1) * NT + (n - (c - 1) * 8 * NT + 7) / 8 : 0;
+#pragma unroll
+                    for (int o = 1; o < 32; o <<= 1) {
+                        const int a = __shfl_up_sync(0xffffffffu, ip, o);
+                        const int b = __shfl_up_sync(0xffffffffu, is, o);
+                        const int u = __shfl_up_sync(0xffffffffu, iu, o);
+                        if (lane >= o) { ip += a; is += b; iu += u; }
+                    }
+                    if (e < p.E) meta->start[e] = ns + is - n;
+                    for (int j = 0; j < c; ++j) {
+                        const int q = np + ip - c + j;
+                        meta->pass_e[q] = (int16_t)e;
+                        meta->pass_row[q] = (int16_t)(ns + is - n + j * 8 * NT);
+                        meta->pass_n[q] = (int16_t)min(8 * NT, n - j * 8 * NT);
+                    }
+                    np += __shfl_sync(0xffffffffu, ip, 31);
+                    ns += __shfl_sync(0xffffffffu, is, 31);
+                    units += __shfl_sync(0xffffffffu, iu, 31);
+                }
+                __syncwarp();
+#pragma unroll
+                for (int j = 0; j < kFewS / 32; ++j) {
+                    const int i = lane + 32 * j;
+                    if (i < S) meta->slot[meta->start[__ldcg(p.ids + i)] + rank[j]] = (int16_t)i;
+                }
+                n_pass = np;
+                if (lane == 0) {
+                    meta->n_pass = np;
+                    meta->n_units = units;
+                }
+                __syncwarp();
+            }
+            const bool end = n_pass >= 0 && t >= (n_pass + 1) * (tiles1 + tiles2);
+            const FewItem it = few_item(t, tiles1, tiles2, max(n_pass, 0));
+            const int K = it.second ? p.I : p.d;
+            // row `lane` of the item: W13 gate rows then up rows, or W2 rows
+            const uint8_t *src = nullptr;
+            if (!end && lane < 16) {
+                const size_t e = it.pass < 0 ? p.E : meta->pass_e[it.pass];
+                const size_t row =
+                    it.second ? e * p.d + it.tile * 16 + lane
+                              : e * 2 * p.I + it.tile * 8 + (lane & 7) + (lane >> 3) * (size_t)p.I;
+                src = static_cast<const uint8_t *>(it.second ? p.W2 : p.W13) + row * K * SH::ELT;
+            }
+            for (int k0 = 0; k0 < K; k0 += SH::STAGE_K) {
+                if (!mbar_wait_warp(&empty[s], ph ^ 1u, wc)) { ok = false; break; }
+                const int bytes = min(SH::STAGE_K, K - k0) * SH::ELT;
+                if (lane == 0) {
+                    info[s] = end ? -1 : t;
+                    info[SH::STAGES + s] = k0;
+                    if (end) mbar_arrive(&full[s]);
+                    else mbar_arrive_expect_tx(&full[s], 16 * bytes);
+                }
+                __syncwarp();
+                if (end) { ok = false; break; }
+                if (lane < 16)
+                    bulk_load(ring + s * kFewStage + lane * kRowPitch, src + (size_t)k0 * SH::ELT,
+                              bytes, &full[s]);
+                last[s] = (int)ph;
+                if (++s == SH::STAGES) { s = 0; ph ^= 1u; }
+            }
+        }
+        if (*abort_s) {
+            // drain the copies still in flight before the CTA exits
+            for (int i = 0; i < SH::STAGES; ++i)
+                if (last[i] >= 0) mbar_wait_teardown(&full[i], (uint32_t)last[i], p.wait_limit);
+        }
+    } else {
+        // -------------------------------------------------------- multiply
+        uint32_t s = 0, ph = 0, n_item = 0;
+        const int g = lane >> 2, c = lane & 3;
+        float acc[NT][4];
+        const uint16_t *act[NT];   // this lane's token row of each group of 8, or null
+        FewItem it{};
+        int n_rows = 0, row0 = 0, K = 0;
+        const float *sc0 = nullptr, *sc1 = nullptr;
+        while (true) {
+            if (!mbar_wait_warp(&full[s], ph, wc)) break;
+            const int t = info[s], k0 = info[SH::STAGES + s];
+            if (t < 0) break;
+            if (k0 == 0) {
+                it = few_item(t, tiles1, tiles2, t < tiles1 ? 0 : meta->n_pass);
+                K = it.second ? p.I : p.d;
+                n_rows = it.pass < 0 ? p.T : meta->pass_n[it.pass];
+                row0 = it.pass < 0 ? 0 : meta->pass_row[it.pass];
+                const int e = it.pass < 0 ? p.E : meta->pass_e[it.pass];
+                if constexpr (FP8) {
+                    const int kb = fp8_blocks(K);
+                    if (it.second) {
+                        sc0 = p.W2_s + ((size_t)e * fp8_blocks(p.d) + it.tile * 16 / 128) * kb;
+                        sc1 = sc0;
+                    } else {
+                        const float *b = p.W13_s + (size_t)e * fp8_blocks(2 * p.I) * kb;
+                        sc0 = b + (size_t)(it.tile * 8 / 128) * kb;
+                        sc1 = b + (size_t)((p.I + it.tile * 8) / 128) * kb;
+                    }
+                }
+                if (it.second) {
+                    // the h rows of this pass: one signal per column tile and
+                    // group of 8 rows
+                    bool ready = true;
+                    if (lane == 0)
+                        ready = wait_count_geq(h_done + 1 + it.pass, tiles1 * ((n_rows + 7) / 8), wc);
+                    ready = __shfl_sync(0xffffffffu, ready, 0);
+                    __syncwarp();   // orders the h loads of every lane behind the acquire
+                    if (!ready) break;
+                }
+#pragma unroll
+                for (int j = 0; j < NT; ++j) {
+                    const int i = j * 8 + g;
+                    act[j] = nullptr;
+                    if (i < n_rows) {
+                        const int slot = it.pass < 0 ? S + i : meta->slot[row0 + i];
+                        act[j] = it.second ? p.h + (size_t)slot * p.I
+                                           : p.x + (size_t)(it.pass < 0 ? i : slot / p.k) * p.d;
+                    }
+#pragma unroll
+                    for (int i4 = 0; i4 < 4; ++i4) acc[j][i4] = 0.0f;
+                }
+            }
+            const int nt = (n_rows + 7) >> 3;
+            const int steps = min(SH::STAGE_K, K - k0) / SH::STEP;
+            const uint32_t a0 = smem_u32(ring + s * kFewStage) + g * kRowPitch + c * 16;
+            float part[FP8 ? NT : 1][4];   // FP8: sums of this stage, not yet scaled
+            if constexpr (FP8) {
+#pragma unroll
+                for (int j = 0; j < NT; ++j)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) part[j][i] = 0.0f;
+            }
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const int st = warp * 2 + u;
+                if (st < steps) {
+                    const uint4 wa = ld_shared_v4(a0 + st * 64);
+                    const uint4 wb = ld_shared_v4(a0 + 8 * kRowPitch + st * 64);
+                    const int kk = k0 + st * SH::STEP + c * (SH::STEP / 4);
+                    constexpr int NV = FP8 ? 2 : 1;
+#pragma unroll
+                    for (int j = 0; j < NT; ++j) {
+                        if (j >= nt) break;
+                        uint4 v[NV];
+#pragma unroll
+                        for (int i = 0; i < NV; ++i) {
+                            v[i] = make_uint4(0, 0, 0, 0);
+                            if (act[j])
+                                v[i] = __ldcg(reinterpret_cast<const uint4 *>(act[j] + kk + 8 * i));
+                        }
+                        if constexpr (FP8) {
+                            const uint32_t qa[4] = {wa.x, wa.y, wa.z, wa.w};
+                            const uint32_t qb[4] = {wb.x, wb.y, wb.z, wb.w};
+                            const uint32_t bv[8] = {v[0].x, v[0].y, v[0].z, v[0].w,
+                                                    v[1].x, v[1].y, v[1].z, v[1].w};
+#pragma unroll
+                            for (int m = 0; m < 4; ++m) {
+                                uint32_t x0, x1, y0, y1;
+                                e4m3x4_bf16(qa[m], x0, x1);
+                                e4m3x4_bf16(qb[m], y0, y1);
+                                mma_bf16(part[j], x0, y0, x1, y1, bv[2 * m], bv[2 * m + 1]);
+                            }
+                        } else {
+                            mma_bf16(acc[j], wa.x, wb.x, wa.y, wb.y, v[0].x, v[0].y);
+                            mma_bf16(acc[j], wa.z, wb.z, wa.w, wb.w, v[0].z, v[0].w);
+                        }
+                    }
+                }
+            }
+            if constexpr (FP8) {
+                // a warp's two steps are one block of 128
+                if (warp * 2 < steps) {
+                    const int kb = k0 / kFp8Block + warp;
+                    const float f0 = __ldg(sc0 + kb), f1 = __ldg(sc1 + kb);
+#pragma unroll
+                    for (int j = 0; j < NT; ++j) {
+                        acc[j][0] = fmaf(part[j][0], f0, acc[j][0]);
+                        acc[j][1] = fmaf(part[j][1], f0, acc[j][1]);
+                        acc[j][2] = fmaf(part[j][2], f1, acc[j][2]);
+                        acc[j][3] = fmaf(part[j][3], f1, acc[j][3]);
+                    }
+                }
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&empty[s]);
+            if (++s == SH::STAGES) { s = 0; ph ^= 1u; }
+            if (k0 + SH::STAGE_K < K) continue;
+
+            // ------------------------------------ the item's sums over the warps
+            if (!mbar_wait_warp(rempty, (n_item & 1u) ^ 1u, wc)) break;
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    red[((j * kMulWarps + warp) * 4 + i) * 32 + lane] = acc[j][i];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(rfull);
+            if (warp < nt) {
+                if (!mbar_wait_warp(rfull, n_item & 1u, wc)) break;
+                float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                for (int w = 0; w < kMulWarps; ++w)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        v[i] += red[((warp * kMulWarps + w) * 4 + i) * 32 + lane];
+                // v[0], v[1]: weight row g, tokens 2c and 2c + 1; v[2], v[3]: row g + 8
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int r = warp * 8 + 2 * c + i;
+                    if (r >= n_rows) continue;
+                    const int slot = it.pass < 0 ? S + r : meta->slot[row0 + r];
+                    if (it.second) {
+                        const float w = it.pass < 0 ? 1.0f : __ldcg(p.w + slot);
+                        float *o = p.yp + (size_t)slot * p.d + it.tile * 16 + g;
+                        o[0] = w * v[i];
+                        o[8] = w * v[2 + i];
+                    } else {
+                        const float h = swiglu_clamped_nan(v[i], v[2 + i], p.clamp);
+                        p.h[(size_t)slot * p.I + it.tile * 8 + g] =
+                            (uint16_t)(pack_bf16x2(h, 0.0f) & 0xFFFFu);
+                    }
+                }
+                __syncwarp();
+                if (!it.second) {
+                    if (lane == 0) red_release_gpu_add(h_done + 1 + it.pass, 1);
+                } else {
+                    int old = 0;
+                    if (lane == 0) old = atom_add_acq_rel(y_done + it.tile, 1);
+                    old = __shfl_sync(0xffffffffu, old, 0);
+                    __syncwarp();
+                    if (old == meta->n_units - 1) {
+                        // every product of these 16 columns is there
+                        for (int i = lane; i < p.T * 16; i += 32) {
+                            const int tk = i >> 4, n = it.tile * 16 + (i & 15);
+                            float sum = __ldcg(p.yp + (size_t)(S + tk) * p.d + n);
+                            for (int j = 0; j < p.k; ++j)
+                                sum += __ldcg(p.yp + (size_t)(tk * p.k + j) * p.d + n);
+                            p.y[(size_t)tk * p.d + n] =
+                                (uint16_t)(pack_bf16x2(sum, 0.0f) & 0xFFFFu);
+                        }
+                    }
+                }
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(rempty);
+            ++n_item;
+        }
+    }
+
+    // the last CTA to leave puts every counter back to zero
+    __syncthreads();
+    if (threadIdx.x == 0) *last_s = atom_add_acq_rel(p.counters + 2, 1) == (int)gridDim.x - 1;
+    __syncthreads();
+    if (*last_s)
+        for (int i = 1 + threadIdx.x; i < p.n_counters; i += kFewThreads) p.counters[i] = 0;
+}
+
+size_t up256(size_t b) { return (b + 255) / 256 * 256; }
+
+struct FewWorkspace {
+    int *counters;
+    int n_counters;
+    float *part;
+    int32_t *ids;
+    float *w, *ssel;
+    uint16_t *h;
+    float *yp;
+    size_t bytes;
+};
+
+FewWorkspace carve_few(uint8_t *base, int T, int d, int E, int k, int I) {
+    FewWorkspace w;
+    size_t off = 0;
+    auto take = [&](size_t b) {
+        uint8_t *q = base + off;
+        off += up256(b);
+        return q;
+    };
+    const size_t S = (size_t)T * k;
+    w.n_counters = 4 + 1 + kFewS + d / 16;
+    w.counters = reinterpret_cast<int *>(take((size_t)w.n_counters * 4));
+    w.part = reinterpret_cast<float *>(take((size_t)kGateSplits * T * E * 4));
+    w.ids = reinterpret_cast<int32_t *>(take(S * 4));
+    w.w = reinterpret_cast<float *>(take(S * 4));
+    w.ssel = reinterpret_cast<float *>(take(S * 4));
+    w.h = reinterpret_cast<uint16_t *>(take((S + T) * I * 2));
+    w.yp = reinterpret_cast<float *>(take((S + T) * d * 4));
+    w.bytes = off;
+    return w;
+}
+
+template <bool FP8, int NT>
+moe_status launch_experts(const FewParams &p, cudaStream_t st) {
+    using SH = FewShape<FP8, NT>;
+    auto kern = few_experts_kernel<FP8, NT>;
+    static bool attr_set[64] = {};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return MOE_ERR_CUDA;
+    if (dev < 0 || dev >= 64) return MOE_ERR_UNSUPPORTED;
+    if (!attr_set[dev]) {
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SH::SMEM) !=
+            cudaSuccess)
+            return MOE_ERR_CUDA;
+        attr_set[dev] = true;
+    }
+    const long long items = (long long)(p.T * p.k + 1) * (p.I / 8 + p.d / 16);
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = dim3((unsigned)(items < num_sms() ? items : num_sms()), 1, 1);
+    cfg.blockDim = dim3(kFewThreads, 1, 1);
+    cfg.dynamicSmemBytes = SH::SMEM;
+    cfg.stream = st;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, kern, p) != cudaSuccess) return MOE_ERR_CUDA;
+    return cuda_status(cudaGetLastError());
+}
+
+template <bool FP8>
+moe_status launch_experts_nt(const FewParams &p, cudaStream_t st) {
+    // rows of an expert that share one read of its weights: as many groups of
+    // 8 as there can be tokens
+    if (p.T <= 8) return launch_experts<FP8, 1>(p, st);
+    if (p.T <= 16) return launch_experts<FP8, 2>(p, st);
+    return launch_experts<FP8, 4>(p, st);
+}
+
+}  // namespace
+
+bool few_supported(int T, int d, int E, int k, int I) {
+    return T >= 1 && T <= kFewT && d >= 128 && d % 128 == 0 && I >= 64 && I % 64 == 0 && E >= 1 &&
+           E <= kFewE && k >= 1 && k <= kFewK && k <= E && d <= (1 << 20) && I <= (1 << 20);
+}
+
+size_t few_workspace_bytes(int T, int d, int E, int k, int I) {
+    return carve_few(nullptr, T, d, E, k, I).bytes;
+}
+
+moe_status launch_few(const moe_few_args *a, cudaStream_t st) {
+    const FewWorkspace w =
+        carve_few(static_cast<uint8_t *>(a->ws), a->T, a->d, a->E, a->k, a->I);
+    FewParams p{};
+    p.x = a->x;
+    p.W_g = a->W_g;
+    p.logit_offset = a->logit_offset;
+    p.bias = a->bias;
+    p.is_vision = a->is_vision;
+    p.input_ids = a->input_ids;
+    p.tid2eid = a->tid2eid;
+    p.vocab = a->vocab;
+    p.T = a->T;
+    p.d = a->d;
+    p.E = a->E;
+    p.k = a->k;
+    p.I = a->I;
+    p.hash = a->mode == MOE_ROUTE_HASH;
+    p.scaling = a->scaling;
+    p.clamp = a->clamp;
+    const bool fp8 = a->W13_q != nullptr;
+    p.W13 = fp8 ? static_cast<const void *>(a->W13_q) : a->W13;
+    p.W2 = fp8 ? static_cast<const void *>(a->W2_q) : a->W2;
+    p.W13_s = a->W13_s;
+    p.W2_s = a->W2_s;
+    p.y = a->y;
+    p.ids_out = a->ids;
+    p.w_out = a->weights;
+    p.counters = w.counters;
+    p.n_counters = w.n_counters;
+    p.part = w.part;
+    p.ids = w.ids;
+    p.w = w.w;
+    p.ssel = w.ssel;
+    p.h = w.h;
+    p.yp = w.yp;
+    p.status = device_status_ptr();
+    if (!p.status) return MOE_ERR_CUDA;
+    p.wait_limit = kWaitLimitCycles;
+    const int et = (p.E + 15) / 16;
+    int splits = num_sms() / et;
+    splits = splits < 1 ? 1 : splits > kGateSplits ? kGateSplits : splits;
+    if (splits > p.d / 32) splits = p.d / 32;
+    p.splits = splits;
+    const dim3 grid(et, splits);
+    if (p.E <= 128) few_gate_kernel<4><<<grid, kGateWarps * 32, 0, st>>>(p);
+    else if (p.E <= 384) few_gate_kernel<12><<<grid, kGateWarps * 32, 0, st>>>(p);
+    else few_gate_kernel<32><<<grid, kGateWarps * 32, 0, st>>>(p);
+    if (cudaGetLastError() != cudaSuccess) return MOE_ERR_CUDA;
+    return fp8 ? launch_experts_nt<true>(p, st) : launch_experts_nt<false>(p, st);
+}
+
+}  // namespace moe

@@ -1,0 +1,65 @@
+// fp8_common.cuh -- helpers of the FP8 operators whose operands carry one fp32
+// scale per block of 128.
+//
+// A block is 128 consecutive elements along the contraction (of a row: token
+// rows, 1 x 128) or a 128 x 128 tile (weights); a short last block holds what
+// is left.  With amax the block's largest magnitude, at least 2^-100:
+//   s = fl(amax / 448),  r = fl(448 / amax),  code = E4M3(fl(v r))
+// (nearest value, ties to even) and the element stands for s * E4M3(code).
+// One division per block instead of one per element; the floor keeps r finite
+// and the codes of an all-zero block zero.  A block with a NaN has scale NaN,
+// one with an infinity (and no NaN) scale infinity and code NaN at the
+// infinite elements, so neither passes for a number downstream.
+// ("DeepSeek-V4昇腾训练支持：基于 CANN 平台的TorchTitan-NPU + AutoFuse 极简训练优化
+// 实践", 性能结果与未来展望: FP8 low-precision compute; the page fixes no format.)
+#pragma once
+
+#include <cstdint>
+
+#include <cuda_fp16.h>
+
+#include "moe_ptx.cuh"
+
+namespace moe {
+
+constexpr int kFp8Block = 128;
+constexpr float kFp8Max = 448.0f;
+constexpr float kFp8AmaxFloor = 7.888609052210118e-31f;   // 2^-100
+
+__host__ __device__ inline int fp8_blocks(int n) { return (n + kFp8Block - 1) / kFp8Block; }
+
+// Scale s and factor r of a block from the largest magnitude's fp32 bits (sign
+// cleared; as integers NaN > infinity > every number, so an integer maximum
+// over a block keeps a NaN).
+struct Fp8Scale {
+    float s, r;
+};
+__device__ __forceinline__ Fp8Scale fp8_scale(uint32_t amax_bits) {
+    const float a = __uint_as_float(amax_bits);
+    const float m = a < kFp8AmaxFloor ? kFp8AmaxFloor : a;   // a NaN stays
+    return {__fdiv_rn(m, kFp8Max), __fdiv_rn(kFp8Max, m)};
+}
+
+// Two values -> two E4M3 codes, `lo` in the low byte.
+__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
+    uint16_t r;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+__device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
+    return e4m3x2(a, b) | (e4m3x2(c, d) << 16);
+}
+
+// Codes of the bf16 pair `w` times r.
+__device__ __forceinline__ uint32_t e4m3x2_bf16(uint32_t w, float r) {
+    return e4m3x2(bf16_lo(w) * r, bf16_hi(w) * r);
+}
+
+// h = silu(min(g, c)) * clamp(u, -c, c); a NaN in g or u stays a NaN.
+__device__ __forceinline__ float swiglu_clamped_nan(float g, float u, float c) {
+    const float a = g > c ? c : g;
+    const float b = u > c ? c : (u < -c ? -c : u);
+    return a * __fdividef(1.0f, 1.0f + __expf(-a)) * b;
+}
+
+}  // namespace moe

@@ -1,0 +1,518 @@
+// gemm_fp8.cu -- FP8 (E4M3) matmuls whose operands carry one fp32 scale per
+// block of 128 along the contraction (format: fp8_common.cuh).
+//
+//   FP8_ROWS   out[r, n] = w_r sum_b sa[r, b] sb[n / 128, b]
+//                              sum_{k in block b} A[r, k] B[g][n, k]     bf16
+//              rows grouped by expert g; with the transposed weight it is the
+//              data gradient
+//   FP8_FFN1   the same for the gate and up rows of W13, then the clamped
+//              SwiGLU and its quantisation along I (a tile holds the 128 h
+//              columns of one scale block)
+//   FP8_WGRAD  dW[g][m, n] = sum_b sa[b, m] sb[b, n] sum_{r in block b} A B
+//              over the chunks of 128 rows of group g                    fp32
+//
+// The tensor core sums the products of one block exactly as far as fp32 goes
+// (tcgen05.mma kind::f8f6f4: E4M3 operands straight from shared memory, fp32
+// accumulator in tensor memory); the scales differ from block to block, so
+// each block's sum leaves tensor memory, is multiplied by its scales and added
+// to the tile's accumulator in registers, in fp32.  Tiles are 128 x 256: a
+// block costs the tensor core 4 MMAs of 128 x 256 x 32, and the eight epilogue
+// warps 32768 fused multiply-adds, two to an instruction; two tensor memory
+// accumulators let the two overlap.
+//
+// One CTA per SM, persistent, 10 warps: warp 0 TMA producer (48 KB a stage,
+// 128-byte swizzle), warp 1 tensor memory owner and MMA issuer, warps 2-9
+// accumulate (thread = row; two warps per lane quadrant, 128 columns each).
+// Every wait is bounded; on a timeout the CTA records MOE_ERR_TIMEOUT, drains
+// its copies and MMAs, frees tensor memory and returns.
+#include <cstring>
+
+#include "fp8_common.cuh"
+#include "gemm_launch.cuh"
+
+namespace moe {
+namespace {
+
+enum Fp8Mode : int { FP8_ROWS = 0, FP8_FFN1 = 1, FP8_WGRAD = 2 };
+
+struct Fp8Params {
+    CUtensorMap tmA;   // A codes: [rows, K] (WGRAD [chunks * M, 128]), boxes 128 x 128
+    CUtensorMap tmB;   // B codes: [G * N, K] (WGRAD [chunks * N, 128]), boxes 128 x 256 (FFN1 128)
+    const int32_t *offsets;   // [G+1] rows of the groups; WGRAD: their chunks
+    const float *sa, *sb;
+    int G, N, K_blocks, n_tiles;
+    int nb_n;                 // scale rows of one group's B
+    int M;                    // WGRAD: output rows
+    int I;                    // FFN1
+    float clamp;
+    const float *row_w;       // ROWS: weight of rows < w_rows (others 1), or null
+    int w_rows;
+    uint16_t *out;            // ROWS
+    uint8_t *hq;              // FFN1: h codes [rows, I] ...
+    float *hs;                //       ... and scales [rows, I / 128]
+    float *dW;                // WGRAD
+    int *status;
+    long long wait_limit;
+};
+
+constexpr int kF8Stages = 4;
+constexpr int kF8BN = 256;
+constexpr int kF8A = 128 * 128;
+constexpr int kF8Stage = kF8A + kF8BN * 128;
+constexpr int kF8Epi = 8;                       // epilogue warps
+constexpr int kF8Threads = 64 + 32 * kF8Epi;
+constexpr int kF8Bars = 512;
+constexpr int kF8Side = 4096;                   // FFN1: amax exchange; WGRAD: column scales
+constexpr uint32_t kF8Idesc =
+    (1u << 4) | ((uint32_t)(kF8BN >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
+
+inline size_t fp8_smem_bytes(int G) {
+    return 1024 + (size_t)kF8Stages * kF8Stage + kF8Side + kF8Bars + 8 * (size_t)(G + 2);
+}
+
+// D[tmem] (+)= A[smem] B[smem]^T, E4M3 operands (K = 32), fp32 accumulator.
+// Instruction descriptor: D format [4,6) = 1 (fp32), A and B format 0 (E4M3),
+// both K-major, N >> 3 at [17,23), M >> 4 at [24,29).
+__device__ __forceinline__ void umma_f8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                        uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// Pairs of fp32 in one instruction.
+__device__ __forceinline__ uint64_t pair(uint32_t lo, uint32_t hi) {
+    uint64_t v;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "r"(lo), "r"(hi));
+    return v;
+}
+__device__ __forceinline__ uint64_t pair_f(float lo, float hi) {
+    return pair(__float_as_uint(lo), __float_as_uint(hi));
+}
+__device__ __forceinline__ void fma2(uint64_t &acc, uint64_t a, uint64_t b) {
+    asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(acc) : "l"(a), "l"(b));
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ float lo_f(uint64_t v) { return __uint_as_float((uint32_t)v); }
+__device__ __forceinline__ float hi_f(uint64_t v) { return __uint_as_float((uint32_t)(v >> 32)); }
+
+struct F8Tile {
+    int g, nt, row0, rows, kb, k0;   // rows: valid rows from row0; k0: first chunk (WGRAD)
+};
+
+template <int MODE>
+__device__ __forceinline__ F8Tile f8_tile(const Fp8Params &p, int t, const int *mt_start,
+                                          const int *offs) {
+    F8Tile ti;
+    ti.nt = t % p.n_tiles;
+    const int q = t / p.n_tiles;
+    if constexpr (MODE == FP8_WGRAD) {
+        const int mt = (p.M + 127) >> 7;
+        ti.g = q / mt;
+        ti.row0 = (q - ti.g * mt) * 128;
+        ti.rows = min(128, p.M - ti.row0);
+        ti.k0 = offs[ti.g];
+        ti.kb = offs[ti.g + 1] - ti.k0;
+        return ti;
+    }
+    int lo = 0, hi = p.G - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (mt_start[mid] <= q) lo = mid; else hi = mid - 1;
+    }
+    ti.g = lo;
+    ti.row0 = offs[lo] + (q - mt_start[lo]) * 128;
+    ti.rows = min(128, offs[lo + 1] - ti.row0);
+    ti.kb = p.K_blocks;
+    ti.k0 = 0;
+    return ti;
+}
+
+template <int MODE>
+__global__ void __launch_bounds__(kF8Threads, 1) fp8_gemm_kernel(const __grid_constant__ Fp8Params p) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    uint8_t *side = smem + kF8Stages * kF8Stage;
+    uint64_t *full = reinterpret_cast<uint64_t *>(side + kF8Side);
+    uint64_t *empty = full + kF8Stages;
+    uint64_t *tfull = empty + kF8Stages;   // a block's sums are in accumulator 0 / 1
+    uint64_t *tempty = tfull + 2;          // ... and have been read
+    uint64_t *xch = tempty + 2;            // FFN1: both halves' largest |h| are in `side`
+    uint64_t *done = xch + 1;
+    uint32_t *tmem_base_s = reinterpret_cast<uint32_t *>(done + 1);
+    volatile int *abort_s = reinterpret_cast<volatile int *>(tmem_base_s + 1);
+    int *offs = reinterpret_cast<int *>(side + kF8Side + kF8Bars);
+    int *mt_start = offs + (p.G + 1);
+
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kF8Stages; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], 1);
+        }
+        for (int a = 0; a < 2; ++a) {
+            mbar_init(&tfull[a], 1);
+            mbar_init(&tempty[a], kF8Epi);
+        }
+        mbar_init(xch, kF8Epi);
+        mbar_init(done, 1);
+        *abort_s = 0;
+        fence_barrier_init();
+    }
+    if (warp == 0 && lane == 0) {
+        tma_prefetch_desc(&p.tmA);
+        tma_prefetch_desc(&p.tmB);
+    }
+    if (warp == 1) {
+        tmem_alloc(tmem_base_s, 2 * kF8BN);
+        tmem_relinquish();
+    }
+    if (warp == 2) {
+        // group offsets and the exclusive prefix of their 128-row tiles
+        int carry = 0;
+        for (int base = 0; base <= p.G; base += 32) {
+            const int g = base + lane;
+            int o = 0, mt = 0;
+            if (g <= p.G) offs[g] = o = p.offsets[g];
+            if (g < p.G) mt = max(0, (p.offsets[g + 1] - o + 127) >> 7);
+            int incl = mt;
+#pragma unroll
+            for (int sft = 1; sft < 32; sft <<= 1) {
+                const int v = __shfl_up_sync(0xffffffffu, incl, sft);
+                if (lane >= sft) incl += v;
+            }
+            if (g <= p.G) mt_start[g] = carry + incl - mt;
+            carry += __shfl_sync(0xffffffffu, incl, 31);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+
+    const uint32_t tmem_base = *tmem_base_s;
+    const WaitCtl wc{abort_s, p.status, p.wait_limit};
+    const int total =
+        (MODE == FP8_WGRAD ? p.G * ((p.M + 127) >> 7) : mt_start[p.G]) * p.n_tiles;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            int last[kF8Stages];
+#pragma unroll
+            for (int i = 0; i < kF8Stages; ++i) last[i] = -1;
+            uint32_t s = 0, ph = 0;
+            bool ok = true;
+            for (int t = blockIdx.x; ok && t < total; t += gridDim.x) {
+                const F8Tile ti = f8_tile<MODE>(p, t, mt_start, offs);
+                for (int kb = 0; kb < ti.kb; ++kb) {
+                    if (!mbar_wait(&empty[s], ph ^ 1u, wc)) { ok = false; break; }
+                    mbar_arrive_expect_tx(&full[s], kF8Stage);
+                    uint8_t *a = smem + s * kF8Stage;
+                    uint8_t *b = a + kF8A;
+                    if constexpr (MODE == FP8_WGRAD) {
+                        const int c = ti.k0 + kb;
+                        tma_load_2d(a, &p.tmA, &full[s], 0, c * p.M + ti.row0);
+                        tma_load_2d(b, &p.tmB, &full[s], 0, c * p.N + ti.nt * kF8BN);
+                    } else if constexpr (MODE == FP8_FFN1) {
+                        const int br = ti.g * 2 * p.I + ti.nt * 128;
+                        tma_load_2d(a, &p.tmA, &full[s], kb * 128, ti.row0);
+                        tma_load_2d(b, &p.tmB, &full[s], kb * 128, br);
+                        tma_load_2d(b + 128 * 128, &p.tmB, &full[s], kb * 128, br + p.I);
+                    } else {
+                        tma_load_2d(a, &p.tmA, &full[s], kb * 128, ti.row0);
+                        tma_load_2d(b, &p.tmB, &full[s], kb * 128, ti.g * p.N + ti.nt * kF8BN);
+                    }
+                    last[s] = (int)ph;
+                    if (++s == kF8Stages) { s = 0; ph ^= 1u; }
+                }
+            }
+            if (!ok) {
+                // drain the copies still in flight before the CTA exits
+                for (int i = 0; i < kF8Stages; ++i)
+                    if (last[i] >= 0) mbar_wait_teardown(&full[i], (uint32_t)last[i], p.wait_limit);
+            }
+        }
+    } else if (warp == 1) {
+        uint32_t s = 0, ph = 0, blk = 0;
+        bool ok = true;
+        for (int t = blockIdx.x; ok && t < total; t += gridDim.x) {
+            const F8Tile ti = f8_tile<MODE>(p, t, mt_start, offs);
+            for (int kb = 0; kb < ti.kb; ++kb, ++blk) {
+                const uint32_t acc = blk & 1u, aph = (blk >> 1) & 1u;
+                if (!mbar_wait_warp(&tempty[acc], aph ^ 1u, wc)) { ok = false; break; }
+                if (!mbar_wait_warp(&full[s], ph, wc)) { ok = false; break; }
+                tc_fence_after();
+                if (lane == 0) {
+                    const uint32_t a = smem_u32(smem + s * kF8Stage), b = a + kF8A;
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)
+                        umma_f8(tmem_base + acc * kF8BN, sdesc_sw128(a + kk * 32, 16, 1024),
+                                sdesc_sw128(b + kk * 32, 16, 1024), kF8Idesc, kk ? 1u : 0u);
+                    umma_commit(&empty[s]);
+                    umma_commit(&tfull[acc]);
+                }
+                __syncwarp();
+                if (++s == kF8Stages) { s = 0; ph ^= 1u; }
+            }
+        }
+        if (!ok) {
+            // every MMA this thread issued must finish before TMEM is freed
+            if (lane == 0) umma_commit(done);
+            __syncwarp();
+            mbar_wait_teardown(done, 0, p.wait_limit);
+        }
+    } else {
+        // ------------------------------------------------ accumulate and finish
+        const int q = warp & 3;            // TMEM lane quadrant
+        const int part = (warp - 2) >> 2;  // its half of the columns
+        const int r_local = q * 32 + lane;
+        uint32_t blk = 0;
+        int it = 0;
+        bool ok = true;
+        for (int t = blockIdx.x; ok && t < total; t += gridDim.x, ++it) {
+            const F8Tile ti = f8_tile<MODE>(p, t, mt_start, offs);
+            const bool valid = r_local < ti.rows;
+            const int row = ti.row0 + r_local;
+            // this thread's columns of the tile: 128 from cl0, or for FFN1 64
+            // gate columns from 64 part and the 64 up columns 128 further on
+            const int cl0 = MODE == FP8_FFN1 ? 64 * part : 128 * part;
+            constexpr int kHalf = MODE == FP8_FFN1 ? 128 : 64;   // column step between halves
+            const float *sa = nullptr, *sb0 = nullptr, *sb1 = nullptr;
+            int sa_step = 1;
+            bool col_ok = false;
+            if constexpr (MODE == FP8_WGRAD) {
+                sa = p.sa + (size_t)ti.k0 * p.M + row;
+                sa_step = p.M;
+                const int col = ti.nt * kF8BN + cl0 + 4 * lane;
+                col_ok = col < p.N;
+                sb0 = p.sb + (size_t)ti.k0 * p.N + col;
+            } else if constexpr (MODE == FP8_FFN1) {
+                sa = p.sa + (size_t)row * p.K_blocks;
+                sb0 = p.sb + ((size_t)ti.g * p.nb_n + ti.nt) * p.K_blocks;
+                sb1 = sb0 + (size_t)(p.I / 128) * p.K_blocks;
+            } else {
+                sa = p.sa + (size_t)row * p.K_blocks;
+                const int nb = ti.nt * 2 + part;
+                sb0 = p.sb + ((size_t)ti.g * p.nb_n + min(nb, p.nb_n - 1)) * p.K_blocks;
+            }
+            // the next block's scales are loaded a block ahead
+            float na = 0.0f, nb0 = 0.0f, nb1 = 0.0f;
+            float4 ncol = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            auto next_scales = [&](int kb) {
+                if (valid) na = __ldg(sa + (size_t)kb * sa_step);
+                if constexpr (MODE == FP8_WGRAD) {
+                    if (col_ok)
+                        ncol = __ldg(reinterpret_cast<const float4 *>(sb0 + (size_t)kb * p.N));
+                } else {
+                    nb0 = __ldg(sb0 + kb);
+                    if constexpr (MODE == FP8_FFN1) nb1 = __ldg(sb1 + kb);
+                }
+            };
+            if (ti.kb > 0) next_scales(0);
+            uint64_t acc[64];
+#pragma unroll
+            for (int j = 0; j < 64; ++j) acc[j] = 0;
+            for (int kb = 0; kb < ti.kb; ++kb, ++blk) {
+                const float f0 = MODE == FP8_WGRAD ? na : na * nb0, f1 = na * nb1;
+                const uint64_t s0 = pair_f(f0, f0);
+                const uint64_t s1 = MODE == FP8_FFN1 ? pair_f(f1, f1) : s0;
+                float *cs = reinterpret_cast<float *>(side) + (warp - 2) * 128;
+                if constexpr (MODE == FP8_WGRAD) {
+                    __syncwarp();
+                    *reinterpret_cast<float4 *>(cs + 4 * lane) = ncol;
+                    __syncwarp();
+                }
+                if (kb + 1 < ti.kb) next_scales(kb + 1);
+                const uint32_t a = blk & 1u;
+                if (!mbar_wait_warp(&tfull[a], (blk >> 1) & 1u, wc)) { ok = false; break; }
+                tc_fence_after();
+                const uint32_t tb = tmem_base + ((uint32_t)(q * 32) << 16) + a * kF8BN + cl0;
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t r[32];
+                    tmem_ld32(tb + (c >> 1) * kHalf + (c & 1) * 32, r);
+                    tmem_wait_ld();
+                    if (c == 3) {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&tempty[a]);
+                    }
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) {
+                        uint64_t v = pair(r[2 * j], r[2 * j + 1]);
+                        if constexpr (MODE == FP8_WGRAD)
+                            v = mul2(v, *reinterpret_cast<const uint64_t *>(cs + c * 32 + 2 * j));
+                        fma2(acc[c * 16 + j], v, c < 2 ? s0 : s1);
+                    }
+                }
+            }
+            if (!ok) break;
+            if constexpr (MODE == FP8_ROWS) {
+                float w = 1.0f;
+                if (valid && p.row_w && row < p.w_rows) w = p.row_w[row];
+                const int col = ti.nt * kF8BN + cl0;
+                uint16_t *dst = p.out + (size_t)row * p.N + col;
+                if (valid) {
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        if (col + 8 * j < p.N)
+                            st_global_v4(
+                                dst + 8 * j,
+                                pack_bf16x2(w * lo_f(acc[4 * j]), w * hi_f(acc[4 * j])),
+                                pack_bf16x2(w * lo_f(acc[4 * j + 1]), w * hi_f(acc[4 * j + 1])),
+                                pack_bf16x2(w * lo_f(acc[4 * j + 2]), w * hi_f(acc[4 * j + 2])),
+                                pack_bf16x2(w * lo_f(acc[4 * j + 3]), w * hi_f(acc[4 * j + 3])));
+                }
+            } else if constexpr (MODE == FP8_WGRAD) {
+                const int col = ti.nt * kF8BN + cl0;
+                float *dst = p.dW + ((size_t)ti.g * p.M + row) * p.N + col;
+                if (valid) {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j)
+                        if (col + 4 * j < p.N)
+                            st_global_v4(dst + 4 * j, (uint32_t)acc[2 * j],
+                                         (uint32_t)(acc[2 * j] >> 32), (uint32_t)acc[2 * j + 1],
+                                         (uint32_t)(acc[2 * j + 1] >> 32));
+                }
+            } else {
+                // 64 h columns; the other half of the block's 128 is with the
+                // warp of the same quadrant and the other part
+                uint32_t amax = 0;
+                float h[64];
+#pragma unroll
+                for (int j = 0; j < 32; ++j) {
+                    h[2 * j] = swiglu_clamped_nan(lo_f(acc[j]), lo_f(acc[32 + j]), p.clamp);
+                    h[2 * j + 1] = swiglu_clamped_nan(hi_f(acc[j]), hi_f(acc[32 + j]), p.clamp);
+                    amax = max(amax, max(__float_as_uint(h[2 * j]) & 0x7FFFFFFFu,
+                                         __float_as_uint(h[2 * j + 1]) & 0x7FFFFFFFu));
+                }
+                // two buffers in turn: a buffer is rewritten two tiles later,
+                // after a barrier that follows its reads
+                uint32_t *ex = reinterpret_cast<uint32_t *>(side) + (it & 1) * 256;
+                ex[part * 128 + r_local] = amax;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(xch);
+                if (!mbar_wait_warp(xch, (uint32_t)it & 1u, wc)) break;
+                amax = max(amax, ex[(part ^ 1) * 128 + r_local]);
+                const Fp8Scale f = fp8_scale(amax);
+                if (valid) {
+                    uint8_t *dst = p.hq + (size_t)row * p.I + ti.nt * 128 + cl0;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        uint32_t w[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const float *v = h + 16 * j + 4 * e;
+                            w[e] = e4m3x4(v[0] * f.r, v[1] * f.r, v[2] * f.r, v[3] * f.r);
+                        }
+                        st_global_v4(dst + 16 * j, w[0], w[1], w[2], w[3]);
+                    }
+                    if (part == 0) p.hs[(size_t)row * (p.I / 128) + ti.nt] = f.s;
+                }
+            }
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 1) tmem_dealloc(tmem_base, 2 * kF8BN);
+}
+
+template <int MODE>
+moe_status launch_fp8(Fp8Params &p, long long max_tiles, cudaStream_t st) {
+    auto kern = fp8_gemm_kernel<MODE>;
+    static bool attr_set[64] = {};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return MOE_ERR_CUDA;
+    if (dev < 0 || dev >= 64) return MOE_ERR_UNSUPPORTED;
+    if (!attr_set[dev]) {
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 (int)fp8_smem_bytes(kMaxGroups)) != cudaSuccess)
+            return MOE_ERR_CUDA;
+        attr_set[dev] = true;
+    }
+    if (max_tiles <= 0) return MOE_OK;
+    p.status = device_status_ptr();
+    if (!p.status) return MOE_ERR_CUDA;
+    p.wait_limit = kWaitLimitCycles;
+    const int grid = max_tiles < num_sms() ? (int)max_tiles : num_sms();
+    kern<<<grid, kF8Threads, fp8_smem_bytes(p.G), st>>>(p);
+    return cuda_status(cudaGetLastError());
+}
+
+}  // namespace
+
+moe_status launch_fp8_matmul(const uint8_t *aq, const float *as, const int32_t *offsets, int G,
+                             int max_rows, const uint8_t *bq, const float *bs, const float *row_w,
+                             int w_rows, int N, int K, uint16_t *out, cudaStream_t st) {
+    Fp8Params p;
+    std::memset(&p, 0, sizeof p);
+    if (!encode_tmap_u8_2d(&p.tmA, aq, K, max_rows, K, 128, 128, 128) ||
+        !encode_tmap_u8_2d(&p.tmB, bq, K, (uint64_t)G * N, K, 128, kF8BN, 128))
+        return MOE_ERR_CUDA;
+    p.offsets = offsets;
+    p.sa = as;
+    p.sb = bs;
+    p.G = G;
+    p.N = N;
+    p.K_blocks = fp8_blocks(K);
+    p.nb_n = fp8_blocks(N);
+    p.n_tiles = (N + kF8BN - 1) / kF8BN;
+    p.row_w = row_w;
+    p.w_rows = w_rows;
+    p.out = out;
+    return launch_fp8<FP8_ROWS>(p, (long long)row_tile_bound(max_rows, G) * p.n_tiles, st);
+}
+
+moe_status launch_fp8_ffn1(const uint8_t *xq, const float *xs, const int32_t *offsets, int G,
+                           int max_rows, const uint8_t *W13q, const float *W13s, int d, int I,
+                           float clamp, uint8_t *hq, float *hs, cudaStream_t st) {
+    Fp8Params p;
+    std::memset(&p, 0, sizeof p);
+    if (!encode_tmap_u8_2d(&p.tmA, xq, d, max_rows, d, 128, 128, 128) ||
+        !encode_tmap_u8_2d(&p.tmB, W13q, d, (uint64_t)G * 2 * I, d, 128, 128, 128))
+        return MOE_ERR_CUDA;
+    p.offsets = offsets;
+    p.sa = xs;
+    p.sb = W13s;
+    p.G = G;
+    p.N = 2 * I;
+    p.I = I;
+    p.K_blocks = d / 128;
+    p.nb_n = 2 * I / 128;
+    p.n_tiles = I / 128;
+    p.clamp = clamp;
+    p.hq = hq;
+    p.hs = hs;
+    return launch_fp8<FP8_FFN1>(p, (long long)row_tile_bound(max_rows, G) * p.n_tiles, st);
+}
+
+moe_status launch_fp8_wgrad(const uint8_t *aq, const float *as, const uint8_t *bq, const float *bs,
+                            const int32_t *first, int G, int max_chunks, int M, int N, float *dW,
+                            cudaStream_t st) {
+    Fp8Params p;
+    std::memset(&p, 0, sizeof p);
+    if (!encode_tmap_u8_2d(&p.tmA, aq, 128, (uint64_t)max_chunks * M, 128, 128, 128, 128) ||
+        !encode_tmap_u8_2d(&p.tmB, bq, 128, (uint64_t)max_chunks * N, 128, 128, kF8BN, 128))
+        return MOE_ERR_CUDA;
+    p.offsets = first;
+    p.sa = as;
+    p.sb = bs;
+    p.G = G;
+    p.M = M;
+    p.N = N;
+    p.n_tiles = (N + kF8BN - 1) / kF8BN;
+    p.dW = dW;
+    return launch_fp8<FP8_WGRAD>(p, (long long)G * ((M + 127) / 128) * p.n_tiles, st);
+}
+
+}  // namespace moe

@@ -147,6 +147,34 @@ moe_status launch_mx_dgrad2(const uint8_t *dYq, const uint8_t *dYsf, const int32
                             uint8_t *dGUq, uint8_t *dGUsf, uint16_t *hw, float *dw_part,
                             int *n_part, int *tile_counter, cudaStream_t st);
 
+// FP8 with one fp32 scale per block of 128 (fp8.cu, gemm_fp8.cu): quantisation
+// of rows (k > 0: through the dispatch), of weights in both orientations, and
+// of each group's rows along the rows (chunks of 128 rows, first[g] the first
+// chunk of group g); the grouped matmul, expert GEMM 1 with the SwiGLU and the
+// weight gradient.
+moe_status launch_fp8_rows(const uint16_t *x, const int32_t *slot_row, long long T, int K, int k,
+                           uint8_t *q, float *s, cudaStream_t st);
+moe_status launch_fp8_weights(const uint16_t *src, int G, int N, int K, uint8_t *q, float *s,
+                              uint8_t *qt, float *s_t, cudaStream_t st);
+moe_status launch_fp8_chunks(const int32_t *offsets, int G, int32_t *first, cudaStream_t st);
+moe_status launch_fp8_columns(const uint16_t *src, const int32_t *offsets, const int32_t *first,
+                              int G, int max_chunks, int C, uint8_t *qt, float *s_t,
+                              cudaStream_t st);
+moe_status launch_fp8_matmul(const uint8_t *aq, const float *as, const int32_t *offsets, int G,
+                             int max_rows, const uint8_t *bq, const float *bs, const float *row_w,
+                             int w_rows, int N, int K, uint16_t *out, cudaStream_t st);
+moe_status launch_fp8_ffn1(const uint8_t *xq, const float *xs, const int32_t *offsets, int G,
+                           int max_rows, const uint8_t *W13q, const float *W13s, int d, int I,
+                           float clamp, uint8_t *hq, float *hs, cudaStream_t st);
+moe_status launch_fp8_wgrad(const uint8_t *aq, const float *as, const uint8_t *bq, const float *bs,
+                            const int32_t *first, int G, int max_chunks, int M, int N, float *dW,
+                            cudaStream_t st);
+
+// The whole layer for a few tokens (few.cu).
+bool few_supported(int T, int d, int E, int k, int I);
+size_t few_workspace_bytes(int T, int d, int E, int k, int I);
+moe_status launch_few(const moe_few_args *a, cudaStream_t st);
+
 moe_status launch_selftest_timeout(long long limit, cudaStream_t st);
 
 // Row movement around an exchange between GPUs (exchange.cu).

@@ -76,6 +76,12 @@ __device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity, const 
     }
 }
 
+// The same for a whole warp, with one answer for all its lanes (where the limit
+// runs out, lanes could otherwise leave at different times and part).
+__device__ __forceinline__ bool mbar_wait_warp(uint64_t *bar, uint32_t parity, const WaitCtl &w) {
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity, w));
+}
+
 // A wait used only while tearing down after an abort: no abort check, but
 // still bounded.
 __device__ __forceinline__ bool mbar_wait_teardown(uint64_t *bar, uint32_t parity,
