@@ -272,22 +272,25 @@ int num_sms() {
     return g_sms[dev];
 }
 
+static bool have_encode() {
+    std::lock_guard<std::mutex> lk(g_mu);
+    if (!g_encode) {
+        void *fn = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000,
+                                             cudaEnableDefault, &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess || !fn)
+            return false;
+        g_encode = reinterpret_cast<EncodeTiledFn>(fn);
+    }
+    return true;
+}
+
 static bool encode_2d(CUtensorMap *tm, CUtensorMapDataType dt, const void *base, uint64_t inner,
                       uint64_t outer, uint64_t row_pitch_bytes, uint32_t box_inner,
                       uint32_t box_outer,
                       CUtensorMapSwizzle swz = CU_TENSOR_MAP_SWIZZLE_128B) {
-    {
-        std::lock_guard<std::mutex> lk(g_mu);
-        if (!g_encode) {
-            void *fn = nullptr;
-            cudaDriverEntryPointQueryResult q;
-            if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000,
-                                                 cudaEnableDefault, &q) != cudaSuccess ||
-                q != cudaDriverEntryPointSuccess || !fn)
-                return false;
-            g_encode = reinterpret_cast<EncodeTiledFn>(fn);
-        }
-    }
+    if (!have_encode()) return false;
     if (!aligned16(base) || (row_pitch_bytes & 15u) != 0 || inner == 0 || outer == 0) return false;
     const cuuint64_t dims[2] = {inner, outer};
     const cuuint64_t strides[1] = {row_pitch_bytes};
@@ -325,6 +328,21 @@ bool encode_tmap_u8_2d(CUtensorMap *tm, const void *base, uint64_t inner, uint64
                                                          : CU_TENSOR_MAP_SWIZZLE_NONE;
     return encode_2d(tm, CU_TENSOR_MAP_DATA_TYPE_UINT8, base, inner, outer, row_pitch_bytes,
                      box_inner, box_outer, swz);
+}
+
+bool encode_tmap_u8_3d_sw128(CUtensorMap *tm, const void *base, uint64_t n0, uint64_t n1,
+                             uint64_t n2, uint64_t pitch1, uint64_t pitch2, uint32_t b0,
+                             uint32_t b1, uint32_t b2) {
+    if (!have_encode()) return false;
+    if (!aligned16(base) || (pitch1 & 15u) != 0 || (pitch2 & 15u) != 0) return false;
+    const cuuint64_t dims[3] = {n0, n1, n2};
+    const cuuint64_t strides[2] = {pitch1, pitch2};
+    const cuuint32_t box[3] = {b0, b1, b2};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    return g_encode(tm, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void *>(base), dims, strides,
+                    box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 moe_status check_shapes(int T, int d, int E, int k, int I) {

@@ -12,14 +12,16 @@
 // Bound: the weights of the experts that the tokens hit cross HBM once (a few
 // rows reuse each of them), so everything else has to hide behind that stream.
 // The second kernel therefore keeps it running from its first cycle to its
-// last: a producer warp copies weight rows into a ring in shared memory
-// (cp.async.bulk) far ahead of the 16 warps that multiply, across the
-// boundaries of the phases, whose dependences only the multiplying warps wait
-// for.  The work comes as items of 16 weight rows in one order for the whole
+// last: one warp plans (takes items, lists the hit experts), one copies weight
+// rows into a ring in shared memory (two TMA boxes a stage) far ahead of the 16
+// warps that multiply, across the boundaries of the phases, whose dependences
+// only the multiplying warps wait for; four more warps add up the partial sums,
+// apply the SwiGLU or the routing weight and signal, so that no multiplying
+// warp waits for a store or an atomic.  The work comes as items of 16 weight rows in one order for the whole
 // grid, handed out by a counter:
-//   shared expert's W13 | W13 of the hit experts | shared expert's W2 | W2 ...
-// The first part needs no routing result, so the kernel starts on it while the
-// first kernel (gate and routing) still runs (programmatic launch).  An item
+//   shared expert's W13 | its W2 | W13 of the hit experts | their W2
+// The first two parts need no routing result, so the kernel starts on them
+// while the first kernel (gate and routing) still runs (programmatic launch).  An item
 // waits only for items before it in the order, all of which running CTAs hold,
 // so the kernel needs no particular number of resident CTAs.
 //
@@ -47,12 +49,17 @@ constexpr int kFewE = 1024;
 constexpr int kGateWarps = 8;
 constexpr int kGateSplits = 16;        // at most
 constexpr int kMulWarps = 16;
-constexpr int kFewThreads = 32 * (kMulWarps + 1);
-constexpr int kRowBytes = 2048;        // weight bytes of a row in a stage
-constexpr int kRowPitch = kRowBytes + 64;   // eight rows' 64-byte pieces hit all banks
-constexpr int kFewStage = 16 * kRowPitch;
+constexpr int kSumWarps = 4;           // each with a buffer of partial sums of its own
+constexpr int kCopyWarp = kMulWarps, kPlanWarp = kMulWarps + 1, kSumWarp0 = kMulWarps + 2;
+constexpr int kFewThreads = 32 * (kSumWarp0 + kSumWarps);
+constexpr int kPlanSlots = 4;          // items between the planning and the copying warp
+constexpr int kChunk = 128;            // weight bytes of a row for one multiplying warp
+constexpr int kRowBytes = kMulWarps * kChunk;   // weight bytes of a row in a stage
+constexpr int kFewStage = 16 * kRowBytes;       // two boxes of 8 rows
+constexpr int kW2Tiles = 2;            // tiles of 16 rows in an item of W2
 
 struct FewParams {
+    CUtensorMap tm13, tm2;             // weight bytes: [K / 128 B][rows][128 B], boxes 16 x 8 x 128
     const uint16_t *x, *W_g;
     const float *logit_offset, *bias;
     const uint8_t *is_vision;
@@ -65,7 +72,7 @@ struct FewParams {
     int32_t *ids_out;                  // or null
     float *w_out;                      // or null
     // workspace
-    int *counters;   // [0] gate, [1] ticket, [2] exits, [4 + p] h tiles of pass p,
+    int *counters;   // [0] gate, [1] ticket, [2] exits, [4] shared h tiles, [5 + p] those of pass p,
                      // then columns' finished items; zero between calls
     int n_counters;
     float *part;     // [splits, T, E] partial logits
@@ -87,12 +94,12 @@ __device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-__device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t bytes,
-                                          uint64_t *bar) {
+__device__ __forceinline__ void tma_load_3d(void *dst, const CUtensorMap *tm, uint64_t *bar, int c0,
+                                            int c1, int c2) {
     asm volatile(
-        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::
-            "r"(smem_u32(dst)),
-        "l"(src), "r"(bytes), "r"(smem_u32(bar))
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(tm)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2)
         : "memory");
 }
 
@@ -112,7 +119,7 @@ __device__ __forceinline__ int atom_add_acq_rel(int *p, int v) {
 // as two k-pairs to each of two MMAs; the token operand is read the same way,
 // so the order of k inside a step is the same on both sides.
 template <int EPL>
-__global__ void __launch_bounds__(kGateWarps * 32) few_gate_kernel(FewParams p) {
+__global__ void __launch_bounds__(kGateWarps * 32) few_gate_kernel(const __grid_constant__ FewParams p) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     __shared__ float red[kGateWarps][4][32];
     __shared__ int s_last;
@@ -158,12 +165,6 @@ __global__ void __launch_bounds__(kGateWarps * 32) few_gate_kernel(FewParams p) 
     __threadfence();
     if (threadIdx.x == 0) p.counters[0] = 0;
     for (int t = warp; t < p.T; t += kGateWarps) {
-        auto logit = [&](int e) {
-            float z = 0.0f;
-            for (int s = 0; s < p.splits; ++s)
-                z += __ldcg(p.part + ((size_t)s * p.T + t) * p.E + e);
-            return z + (p.logit_offset ? p.logit_offset[e] : 0.0f);
-        };
         int my_id = 0;
         float my_s = 0.0f;
         if (p.hash) {
@@ -178,7 +179,11 @@ __global__ void __launch_bounds__(kGateWarps * 32) few_gate_kernel(FewParams p) 
                     record_status(p.status, MOE_ERR_INVALID_ARG);
                     my_id = 0;
                 }
-                my_s = sigmoid_exact(logit(my_id));
+                float z = 0.0f;
+                for (int s = 0; s < p.splits; ++s)
+                    z += __ldcg(p.part + ((size_t)s * p.T + t) * p.E + my_id);
+                if (p.logit_offset) z += p.logit_offset[my_id];
+                my_s = sigmoid_exact(z);
             }
         } else {
             const float *bt = p.bias + ((p.is_vision && p.is_vision[t]) ? p.E : 0);
@@ -186,8 +191,22 @@ __global__ void __launch_bounds__(kGateWarps * 32) few_gate_kernel(FewParams p) 
 #pragma unroll
             for (int i = 0; i < EPL; ++i) {
                 const int e = lane + 32 * i;
-                zv[i] = e < p.E ? logit(e) : 0.0f;
+                zv[i] = 0.0f;
                 bv[i] = e < p.E ? bt[e] : 0.0f;
+            }
+            // all experts' loads of a split together (their latency, not their
+            // bytes, is what counts here)
+#pragma unroll 2
+            for (int s = 0; s < p.splits; ++s) {
+                const float *z = p.part + ((size_t)s * p.T + t) * p.E;
+#pragma unroll
+                for (int i = 0; i < EPL; ++i)
+                    if (lane + 32 * i < p.E) zv[i] += __ldcg(z + lane + 32 * i);
+            }
+            if (p.logit_offset) {
+#pragma unroll
+                for (int i = 0; i < EPL; ++i)
+                    if (lane + 32 * i < p.E) zv[i] += p.logit_offset[lane + 32 * i];
             }
             route_topk_token<EPL>(zv, bv, lane, p.E, p.k, s_e[warp], s_z[warp], s_b[warp], my_id,
                                   my_s);
@@ -223,31 +242,28 @@ struct FewItem {
 
 template <bool FP8, int NT>
 struct FewShape {
-    static constexpr int STAGES = NT == 4 ? 5 : 6;
-    static constexpr int RED = NT * kMulWarps * 128 * 4;
-    static constexpr int SMEM = STAGES * kFewStage + RED + (int)sizeof(FewMeta) + 512;
+    static constexpr int STAGES = 5;
+    static constexpr int RED = kSumWarps * kMulWarps * 128 * 4;
+    static constexpr int SMEM = 1024 + STAGES * kFewStage + RED + (int)sizeof(FewMeta) + 512;
     static constexpr int ELT = FP8 ? 1 : 2;
     static constexpr int STAGE_K = kRowBytes / ELT;   // contraction of a stage
-    static constexpr int STEP = FP8 ? 64 : 32;        // of a step (64 bytes of a row)
+    static constexpr int STEP = FP8 ? 64 : 32;        // of a step (64 bytes of a row, half a chunk)
 };
 
-// Items in order: shared W13, routed W13, shared W2, routed W2.
+// Tiles in order: shared W13, shared W2, routed W13, routed W2.  An item is one
+// tile of W13 or kW2Tiles of W2 (about the same bytes).
 __device__ __forceinline__ FewItem few_item(int t, int tiles1, int tiles2, int n_pass) {
     FewItem it;
     it.pass = -1;
-    it.second = false;
-    it.tile = t;
-    if (t < tiles1) return it;
-    t -= tiles1;
-    if (t < n_pass * tiles1) {
-        it.pass = t / tiles1;
-        it.tile = t - it.pass * tiles1;
-        return it;
-    }
-    t -= n_pass * tiles1;
-    it.second = true;
-    it.pass = t / tiles2 - 1;
-    it.tile = t % tiles2;
+    it.second = t >= tiles1;
+    it.tile = it.second ? t - tiles1 : t;
+    t -= tiles1 + tiles2;
+    if (t < 0) return it;
+    it.second = t >= n_pass * tiles1;
+    if (it.second) t -= n_pass * tiles1;
+    const int tiles = it.second ? tiles2 : tiles1;
+    it.pass = t / tiles;
+    it.tile = t - it.pass * tiles;
     return it;
 }
 
@@ -263,28 +279,42 @@ __device__ __forceinline__ void e4m3x4_bf16(uint32_t w, uint32_t &lo, uint32_t &
 }
 
 template <bool FP8, int NT>
-__global__ void __launch_bounds__(kFewThreads, 1) few_experts_kernel(const FewParams p) {
+__global__ void __launch_bounds__(kFewThreads, 1) few_experts_kernel(
+    const __grid_constant__ FewParams p) {
     using SH = FewShape<FP8, NT>;
-    extern __shared__ __align__(128) uint8_t smem[];
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     uint8_t *ring = smem;
-    float *red = reinterpret_cast<float *>(smem + SH::STAGES * kFewStage);
+    float4 *red = reinterpret_cast<float4 *>(smem + SH::STAGES * kFewStage);
     FewMeta *meta = reinterpret_cast<FewMeta *>(smem + SH::STAGES * kFewStage + SH::RED);
     uint64_t *full = reinterpret_cast<uint64_t *>(meta + 1);
-    uint64_t *empty = full + SH::STAGES;
-    uint64_t *rfull = empty + SH::STAGES;    // every warp's partial sums are in `red`
-    uint64_t *rempty = rfull + 1;            // ... and have been read
-    volatile int *info = reinterpret_cast<volatile int *>(rempty + 1);   // [STAGES] item, [STAGES] k
-    volatile int *abort_s = info + 2 * SH::STAGES;
+    uint64_t *ifull = full + SH::STAGES;     // `info` of the stage is written (its rows may not be there)
+    uint64_t *empty = ifull + SH::STAGES;
+    uint64_t *rfull = empty + SH::STAGES;    // a buffer of `red` has every warp's partial sums
+    uint64_t *rempty = rfull + kSumWarps;    // ... and has been read
+    uint64_t *qfull = rempty + kSumWarps;    // a planned item is in the queue
+    uint64_t *qempty = qfull + kPlanSlots;
+    volatile int *queue = reinterpret_cast<volatile int *>(qempty + kPlanSlots);   // first tile
+    volatile int *info = queue + kPlanSlots;                          // tile, k per stage
+    volatile int *rinfo = info + 2 * SH::STAGES;                     // tile, group per buffer
+    volatile int *abort_s = rinfo + 2 * kSumWarps;
     int *last_s = const_cast<int *>(abort_s) + 1;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (int s = 0; s < SH::STAGES; ++s) {
             mbar_init(&full[s], 1);
+            mbar_init(&ifull[s], 1);
             mbar_init(&empty[s], kMulWarps);
         }
-        mbar_init(rfull, kMulWarps);
-        mbar_init(rempty, kMulWarps);
+        for (int b = 0; b < kSumWarps; ++b) {
+            mbar_init(&rfull[b], kMulWarps);
+            mbar_init(&rempty[b], 1);
+        }
+        for (int b = 0; b < kPlanSlots; ++b) {
+            mbar_init(&qfull[b], 1);
+            mbar_init(&qempty[b], 1);
+        }
         *abort_s = 0;
         fence_barrier_init();
     }
@@ -295,20 +325,18 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_experts_kernel(const FewPa
     int *h_done = p.counters + 4;
     int *y_done = h_done + 1 + kFewS;
 
-    if (warp == kMulWarps) {
-        // -------------------------------------------------------- producer
-        uint32_t s = 0, ph = 0;
-        int last[SH::STAGES];
-#pragma unroll
-        for (int i = 0; i < SH::STAGES; ++i) last[i] = -1;
-        bool ok = true;
+    if (warp == kPlanWarp) {
+        // ------------------------------------------------------------ plan
+        // Takes items from the grid's counter and passes them on; before the
+        // first routed item, waits for the routing and lists the hit experts.
+        const int shared_items = tiles1 + tiles2 / kW2Tiles;
         int n_pass = -1;
-        while (ok) {
-            int t = 0;
-            if (lane == 0) t = atomicAdd(p.counters + 1, 1);
-            t = __shfl_sync(0xffffffffu, t, 0);
-            if (t >= tiles1 && n_pass < 0) {
-                // routing results: the hit experts, their passes and slots
+        uint32_t n = 0;
+        int ticket = 0;
+        if (lane == 0) ticket = atomicAdd(p.counters + 1, 1);
+        while (true) {
+            int t = __shfl_sync(0xffffffffu, ticket, 0);
+            if (t >= shared_items && n_pass < 0) {
                 asm volatile("griddepcontrol.wait;" ::: "memory");
                 for (int e = lane; e < p.E; e += 32) meta->start[e] = 0;
                 __syncwarp();
@@ -326,31 +354,32 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_experts_kernel(const FewPa
                         __syncwarp();
                     }
                 }
-                int np = 0, ns = 0, units = (p.T + 7) / 8;
+                // prefix sums over the experts of passes, slots and units, in
+                // one word (each at most kFewS = 256: 10 bits)
+                int sum = 0;
                 for (int base = 0; base < p.E; base += 32) {
                     const int e = base + lane;
-                    const int n = e < p.E ? meta->start[e] : 0;
-                    const int c = (n + 8 * NT - 1) / (8 * NT);
-                    int ip = c, is = n, iu = 0;
+                    const int r = e < p.E ? meta->start[e] : 0;
+                    if (!__any_sync(0xffffffffu, r)) continue;
+                    const int c = (r + 8 * NT - 1) / (8 * NT);
                     // a pass of r rows is ceil(r / 8) units
-                    iu = c > 0 ? (c - 1) * NT + (n - (c - 1) * 8 * NT + 7) / 8 : 0;
+                    const int u = c > 0 ? (c - 1) * NT + (r - (c - 1) * 8 * NT + 7) / 8 : 0;
+                    int incl = c | r << 10 | u << 20;
 #pragma unroll
                     for (int o = 1; o < 32; o <<= 1) {
-                        const int a = __shfl_up_sync(0xffffffffu, ip, o);
-                        const int b = __shfl_up_sync(0xffffffffu, is, o);
-                        const int u = __shfl_up_sync(0xffffffffu, iu, o);
-                        if (lane >= o) { ip += a; is += b; iu += u; }
+                        const int v = __shfl_up_sync(0xffffffffu, incl, o);
+                        if (lane >= o) incl += v;
                     }
-                    if (e < p.E) meta->start[e] = ns + is - n;
+                    const int excl = sum + incl - (c | r << 10 | u << 20);
+                    const int first = excl >> 10 & 1023;
+                    if (r > 0) meta->start[e] = first;
                     for (int j = 0; j < c; ++j) {
-                        const int q = np + ip - c + j;
+                        const int q = (excl & 1023) + j;
                         meta->pass_e[q] = (int16_t)e;
-                        meta->pass_row[q] = (int16_t)(ns + is - n + j * 8 * NT);
-                        meta->pass_n[q] = (int16_t)min(8 * NT, n - j * 8 * NT);
+                        meta->pass_row[q] = (int16_t)(first + j * 8 * NT);
+                        meta->pass_n[q] = (int16_t)min(8 * NT, r - j * 8 * NT);
                     }
-                    np += __shfl_sync(0xffffffffu, ip, 31);
-                    ns += __shfl_sync(0xffffffffu, is, 31);
-                    units += __shfl_sync(0xffffffffu, iu, 31);
+                    sum += __shfl_sync(0xffffffffu, incl, 31);
                 }
                 __syncwarp();
 #pragma unroll
@@ -358,63 +387,119 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_experts_kernel(const FewPa
                     const int i = lane + 32 * j;
                     if (i < S) meta->slot[meta->start[__ldcg(p.ids + i)] + rank[j]] = (int16_t)i;
                 }
-                n_pass = np;
+                n_pass = sum & 1023;
                 if (lane == 0) {
-                    meta->n_pass = np;
-                    meta->n_units = units;
+                    meta->n_pass = n_pass;
+                    meta->n_units = (sum >> 20) + (p.T + 7) / 8;
                 }
                 __syncwarp();
             }
-            const bool end = n_pass >= 0 && t >= (n_pass + 1) * (tiles1 + tiles2);
-            const FewItem it = few_item(t, tiles1, tiles2, max(n_pass, 0));
-            const int K = it.second ? p.I : p.d;
-            // row `lane` of the item: W13 gate rows then up rows, or W2 rows
-            const uint8_t *src = nullptr;
-            if (!end && lane < 16) {
-                const size_t e = it.pass < 0 ? p.E : meta->pass_e[it.pass];
-                const size_t row =
-                    it.second ? e * p.d + it.tile * 16 + lane
-                              : e * 2 * p.I + it.tile * 8 + (lane & 7) + (lane >> 3) * (size_t)p.I;
-                src = static_cast<const uint8_t *>(it.second ? p.W2 : p.W13) + row * K * SH::ELT;
+            // the next number comes while this item waits for its place
+            if (lane == 0) ticket = atomicAdd(p.counters + 1, 1);
+            // item -> first tile
+            int tile;
+            if (t < tiles1) tile = t;
+            else if (t < shared_items) tile = tiles1 + (t - tiles1) * kW2Tiles;
+            else {
+                t -= shared_items;
+                const int first2 = n_pass * tiles1;
+                tile = tiles1 + tiles2 + (t < first2 ? t : first2 + (t - first2) * kW2Tiles);
+                if (tile >= (n_pass + 1) * (tiles1 + tiles2)) tile = -1;
             }
-            for (int k0 = 0; k0 < K; k0 += SH::STAGE_K) {
-                if (!mbar_wait_warp(&empty[s], ph ^ 1u, wc)) { ok = false; break; }
-                const int bytes = min(SH::STAGE_K, K - k0) * SH::ELT;
-                if (lane == 0) {
-                    info[s] = end ? -1 : t;
-                    info[SH::STAGES + s] = k0;
-                    if (end) mbar_arrive(&full[s]);
-                    else mbar_arrive_expect_tx(&full[s], 16 * bytes);
+            const uint32_t b = n % kPlanSlots;
+            if (!mbar_wait_warp(&qempty[b], (n / kPlanSlots & 1u) ^ 1u, wc)) break;
+            if (lane == 0) {
+                queue[b] = tile;
+                mbar_arrive(&qfull[b]);
+            }
+            ++n;
+            if (tile < 0) break;
+        }
+    } else if (warp == kCopyWarp) {
+        // ------------------------------------------------------------ copy
+        if (lane == 0) {
+            uint32_t s = 0, ph = 0;
+            int last[SH::STAGES];
+#pragma unroll
+            for (int i = 0; i < SH::STAGES; ++i) last[i] = -1;
+            bool ok = true;
+            for (uint32_t n = 0; ok; ++n) {
+                const uint32_t b = n % kPlanSlots;
+                if (!mbar_wait(&qfull[b], n / kPlanSlots & 1u, wc)) break;
+                const int t = queue[b];
+                mbar_arrive(&qempty[b]);
+                if (t < 0) {
+                    if (mbar_wait(&empty[s], ph ^ 1u, wc)) {
+                        info[s] = -1;
+                        mbar_arrive(&ifull[s]);
+                    }
+                    break;
                 }
-                __syncwarp();
-                if (end) { ok = false; break; }
-                if (lane < 16)
-                    bulk_load(ring + s * kFewStage + lane * kRowPitch, src + (size_t)k0 * SH::ELT,
-                              bytes, &full[s]);
-                last[s] = (int)ph;
-                if (++s == SH::STAGES) { s = 0; ph ^= 1u; }
+                FewItem it = few_item(t, tiles1, tiles2,
+                                      t < tiles1 + tiles2 ? 0 : meta->n_pass);
+                const int e = it.pass < 0 ? p.E : meta->pass_e[it.pass];
+                const int K = it.second ? p.I : p.d;
+                const int chunks = K * SH::ELT / kChunk;   // whole ones; see the tail below
+                const CUtensorMap *tm = it.second ? &p.tm2 : &p.tm13;
+                for (int sub = 0; ok && sub < (it.second ? kW2Tiles : 1); ++sub) {
+                    // 8 gate rows and the matching 8 up rows, or 16 rows of W2
+                    const int r0 = it.second ? e * p.d + (it.tile + sub) * 16
+                                             : e * 2 * p.I + it.tile * 8;
+                    const int r1 = r0 + (it.second ? 8 : p.I);
+                    for (int k0 = 0; k0 < K; k0 += SH::STAGE_K) {
+                        if (!mbar_wait(&empty[s], ph ^ 1u, wc)) { ok = false; break; }
+                        info[s] = t + sub;
+                        info[SH::STAGES + s] = k0;
+                        mbar_arrive(&ifull[s]);
+                        const int c0 = k0 * SH::ELT / kChunk;
+                        if (c0 < chunks) {
+                            uint8_t *dst = ring + s * kFewStage;
+                            mbar_arrive_expect_tx(&full[s], kFewStage);
+                            tma_load_3d(dst, tm, &full[s], 0, r0, c0);
+                            tma_load_3d(dst + kFewStage / 2, tm, &full[s], 0, r1, c0);
+                        } else {
+                            mbar_arrive(&full[s]);
+                        }
+                        last[s] = (int)ph;
+                        if (++s == SH::STAGES) { s = 0; ph ^= 1u; }
+                    }
+                }
+            }
+            if (*abort_s) {
+                // drain the copies still in flight before the CTA exits
+                for (int i = 0; i < SH::STAGES; ++i)
+                    if (last[i] >= 0)
+                        mbar_wait_teardown(&full[i], (uint32_t)last[i], p.wait_limit);
             }
         }
-        if (*abort_s) {
-            // drain the copies still in flight before the CTA exits
-            for (int i = 0; i < SH::STAGES; ++i)
-                if (last[i] >= 0) mbar_wait_teardown(&full[i], (uint32_t)last[i], p.wait_limit);
-        }
-    } else {
+    } else if (warp < kMulWarps) {
         // -------------------------------------------------------- multiply
-        uint32_t s = 0, ph = 0, n_item = 0;
+        // A stage's token operands are loaded as soon as its item is known,
+        // while its weight rows are still on their way.
+        uint32_t s = 0, ph = 0, unit = 0;
         const int g = lane >> 2, c = lane & 3;
         float acc[NT][4];
         const uint16_t *act[NT];   // this lane's token row of each group of 8, or null
         FewItem it{};
         int n_rows = 0, row0 = 0, K = 0;
         const float *sc0 = nullptr, *sc1 = nullptr;
+        constexpr int NV = FP8 ? 2 : 1;
         while (true) {
-            if (!mbar_wait_warp(&full[s], ph, wc)) break;
+            if (!mbar_wait_warp(&ifull[s], ph, wc)) break;
             const int t = info[s], k0 = info[SH::STAGES + s];
-            if (t < 0) break;
+            if (t < 0) {
+                if (lane == 0) {   // tell the sum warps, one buffer each
+                    for (int b = 0; b < kSumWarps; ++b, ++unit) {
+                        const uint32_t buf = unit % kSumWarps;
+                        if (!mbar_wait(&rempty[buf], (unit / kSumWarps & 1u) ^ 1u, wc)) break;
+                        if (warp == 0) rinfo[2 * buf] = -1;
+                        mbar_arrive(&rfull[buf]);
+                    }
+                }
+                break;
+            }
             if (k0 == 0) {
-                it = few_item(t, tiles1, tiles2, t < tiles1 ? 0 : meta->n_pass);
+                it = few_item(t, tiles1, tiles2, t < tiles1 + tiles2 ? 0 : meta->n_pass);
                 K = it.second ? p.I : p.d;
                 n_rows = it.pass < 0 ? p.T : meta->pass_n[it.pass];
                 row0 = it.pass < 0 ? 0 : meta->pass_row[it.pass];
@@ -455,7 +540,61 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_experts_kernel(const FewPa
             }
             const int nt = (n_rows + 7) >> 3;
             const int steps = min(SH::STAGE_K, K - k0) / SH::STEP;
-            const uint32_t a0 = smem_u32(ring + s * kFewStage) + g * kRowPitch + c * 16;
+            const int kk = k0 + warp * 2 * SH::STEP + c * (SH::STEP / 4);
+            // token operand of step u, group j
+            auto load_act = [&](int u, int j, uint4 (&v)[NV]) {
+#pragma unroll
+                for (int i = 0; i < NV; ++i) {
+                    v[i] = make_uint4(0, 0, 0, 0);
+                    if (act[j] && warp * 2 + u < steps)
+                        v[i] = __ldcg(
+                            reinterpret_cast<const uint4 *>(act[j] + kk + u * SH::STEP + 8 * i));
+                }
+            };
+            uint4 v0[2][NV];
+            load_act(0, 0, v0[0]);
+            load_act(1, 0, v0[1]);
+            float f0 = 0.0f, f1 = 0.0f;
+            if constexpr (FP8) {
+                // a warp's two steps are one block of 128
+                if (warp * 2 < steps) {
+                    f0 = __ldg(sc0 + k0 / kFp8Block + warp);
+                    f1 = __ldg(sc1 + k0 / kFp8Block + warp);
+                }
+            }
+            if (!mbar_wait_warp(&full[s], ph, wc)) break;
+            // the warp's chunk: rows g and g + 8, 128 bytes each, 16-byte pieces
+            // exchanged by row (128-byte swizzle).  Lanes of odd rows read their
+            // second half first, so that no two rows of a quarter warp meet in
+            // a bank.
+            uint4 wq[2][2];   // [half][row g / g + 8]
+            {
+                const uint32_t a0 =
+                    smem_u32(ring + s * kFewStage) + warp * (8 * kChunk) + g * kChunk;
+                const uint32_t first = ((uint32_t)((g & 1) * 4 + c) ^ g) << 4;
+                const uint4 p0 = ld_shared_v4(a0 + first), q0 = ld_shared_v4(a0 + (first ^ 64u));
+                const uint4 p1 = ld_shared_v4(a0 + kFewStage / 2 + first);
+                const uint4 q1 = ld_shared_v4(a0 + kFewStage / 2 + (first ^ 64u));
+                const bool odd = g & 1;
+                wq[0][0] = odd ? q0 : p0;
+                wq[1][0] = odd ? p0 : q0;
+                wq[0][1] = odd ? q1 : p1;
+                wq[1][1] = odd ? p1 : q1;
+            }
+            if constexpr (FP8) {
+                // a contraction that ends inside a chunk: its last 64 codes are
+                // not in the stage (a copied row would run into the next one)
+                if ((K & 64) && k0 + warp * 128 + 64 == K) {
+                    const uint8_t *w = static_cast<const uint8_t *>(it.second ? p.W2 : p.W13);
+                    const int e = it.pass < 0 ? p.E : meta->pass_e[it.pass];
+                    const size_t r = it.second ? (size_t)e * p.d + it.tile * 16 + g
+                                               : (size_t)e * 2 * p.I + it.tile * 8 + g;
+                    w += r * K + K - 64 + c * 16;
+                    wq[0][0] = __ldg(reinterpret_cast<const uint4 *>(w));
+                    wq[0][1] = __ldg(reinterpret_cast<const uint4 *>(
+                        w + (size_t)(it.second ? 8 : p.I) * K));
+                }
+            }
             float part[FP8 ? NT : 1][4];   // FP8: sums of this stage, not yet scaled
             if constexpr (FP8) {
 #pragma unroll
@@ -467,116 +606,128 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_experts_kernel(const FewPa
             for (int u = 0; u < 2; ++u) {
                 const int st = warp * 2 + u;
                 if (st < steps) {
-                    const uint4 wa = ld_shared_v4(a0 + st * 64);
-                    const uint4 wb = ld_shared_v4(a0 + 8 * kRowPitch + st * 64);
-                    const int kk = k0 + st * SH::STEP + c * (SH::STEP / 4);
-                    constexpr int NV = FP8 ? 2 : 1;
+                    const uint4 wa = wq[u][0], wb = wq[u][1];
+                    uint32_t x0[4], x1[4], y0[4], y1[4];   // FP8: the codes' values
+                    if constexpr (FP8) {
+                        const uint32_t qa[4] = {wa.x, wa.y, wa.z, wa.w};
+                        const uint32_t qb[4] = {wb.x, wb.y, wb.z, wb.w};
+#pragma unroll
+                        for (int m = 0; m < 4; ++m) {
+                            e4m3x4_bf16(qa[m], x0[m], x1[m]);
+                            e4m3x4_bf16(qb[m], y0[m], y1[m]);
+                        }
+                    }
 #pragma unroll
                     for (int j = 0; j < NT; ++j) {
                         if (j >= nt) break;
                         uint4 v[NV];
-#pragma unroll
-                        for (int i = 0; i < NV; ++i) {
-                            v[i] = make_uint4(0, 0, 0, 0);
-                            if (act[j])
-                                v[i] = __ldcg(reinterpret_cast<const uint4 *>(act[j] + kk + 8 * i));
-                        }
+                        if (j > 0) load_act(u, j, v);
+                        const uint4 *b = j > 0 ? v : v0[u];
                         if constexpr (FP8) {
-                            const uint32_t qa[4] = {wa.x, wa.y, wa.z, wa.w};
-                            const uint32_t qb[4] = {wb.x, wb.y, wb.z, wb.w};
-                            const uint32_t bv[8] = {v[0].x, v[0].y, v[0].z, v[0].w,
-                                                    v[1].x, v[1].y, v[1].z, v[1].w};
+                            const uint32_t bv[8] = {b[0].x, b[0].y, b[0].z, b[0].w,
+                                                    b[NV - 1].x, b[NV - 1].y, b[NV - 1].z,
+                                                    b[NV - 1].w};
 #pragma unroll
-                            for (int m = 0; m < 4; ++m) {
-                                uint32_t x0, x1, y0, y1;
-                                e4m3x4_bf16(qa[m], x0, x1);
-                                e4m3x4_bf16(qb[m], y0, y1);
-                                mma_bf16(part[j], x0, y0, x1, y1, bv[2 * m], bv[2 * m + 1]);
-                            }
+                            for (int m = 0; m < 4; ++m)
+                                mma_bf16(part[j], x0[m], y0[m], x1[m], y1[m], bv[2 * m],
+                                         bv[2 * m + 1]);
                         } else {
-                            mma_bf16(acc[j], wa.x, wb.x, wa.y, wb.y, v[0].x, v[0].y);
-                            mma_bf16(acc[j], wa.z, wb.z, wa.w, wb.w, v[0].z, v[0].w);
+                            mma_bf16(acc[j], wa.x, wb.x, wa.y, wb.y, b[0].x, b[0].y);
+                            mma_bf16(acc[j], wa.z, wb.z, wa.w, wb.w, b[0].z, b[0].w);
                         }
                     }
                 }
             }
             if constexpr (FP8) {
-                // a warp's two steps are one block of 128
-                if (warp * 2 < steps) {
-                    const int kb = k0 / kFp8Block + warp;
-                    const float f0 = __ldg(sc0 + kb), f1 = __ldg(sc1 + kb);
 #pragma unroll
-                    for (int j = 0; j < NT; ++j) {
-                        acc[j][0] = fmaf(part[j][0], f0, acc[j][0]);
-                        acc[j][1] = fmaf(part[j][1], f0, acc[j][1]);
-                        acc[j][2] = fmaf(part[j][2], f1, acc[j][2]);
-                        acc[j][3] = fmaf(part[j][3], f1, acc[j][3]);
-                    }
+                for (int j = 0; j < NT; ++j) {
+                    acc[j][0] = fmaf(part[j][0], f0, acc[j][0]);
+                    acc[j][1] = fmaf(part[j][1], f0, acc[j][1]);
+                    acc[j][2] = fmaf(part[j][2], f1, acc[j][2]);
+                    acc[j][3] = fmaf(part[j][3], f1, acc[j][3]);
                 }
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(&empty[s]);
             if (++s == SH::STAGES) { s = 0; ph ^= 1u; }
             if (k0 + SH::STAGE_K < K) continue;
-
-            // ------------------------------------ the item's sums over the warps
-            if (!mbar_wait_warp(rempty, (n_item & 1u) ^ 1u, wc)) break;
+            // the item's partial sums, one buffer per group of 8 rows
+            bool ok = true;
 #pragma unroll
-            for (int j = 0; j < NT; ++j)
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    red[((j * kMulWarps + warp) * 4 + i) * 32 + lane] = acc[j][i];
-            __syncwarp();
-            if (lane == 0) mbar_arrive(rfull);
-            if (warp < nt) {
-                if (!mbar_wait_warp(rfull, n_item & 1u, wc)) break;
-                float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-                for (int w = 0; w < kMulWarps; ++w)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        v[i] += red[((warp * kMulWarps + w) * 4 + i) * 32 + lane];
-                // v[0], v[1]: weight row g, tokens 2c and 2c + 1; v[2], v[3]: row g + 8
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const int r = warp * 8 + 2 * c + i;
-                    if (r >= n_rows) continue;
-                    const int slot = it.pass < 0 ? S + r : meta->slot[row0 + r];
-                    if (it.second) {
-                        const float w = it.pass < 0 ? 1.0f : __ldcg(p.w + slot);
-                        float *o = p.yp + (size_t)slot * p.d + it.tile * 16 + g;
-                        o[0] = w * v[i];
-                        o[8] = w * v[2 + i];
-                    } else {
-                        const float h = swiglu_clamped_nan(v[i], v[2 + i], p.clamp);
-                        p.h[(size_t)slot * p.I + it.tile * 8 + g] =
-                            (uint16_t)(pack_bf16x2(h, 0.0f) & 0xFFFFu);
-                    }
+            for (int j = 0; j < NT; ++j) {
+                if (j >= nt) break;
+                const uint32_t buf = unit % kSumWarps;
+                ok = mbar_wait_warp(&rempty[buf], (unit / kSumWarps & 1u) ^ 1u, wc);
+                if (!ok) break;
+                red[(buf * kMulWarps + warp) * 32 + lane] =
+                    make_float4(acc[j][0], acc[j][1], acc[j][2], acc[j][3]);
+                if (warp == 0 && lane == 0) {
+                    rinfo[2 * buf] = t;
+                    rinfo[2 * buf + 1] = j;
                 }
                 __syncwarp();
-                if (!it.second) {
-                    if (lane == 0) red_release_gpu_add(h_done + 1 + it.pass, 1);
+                if (lane == 0) mbar_arrive(&rfull[buf]);
+                ++unit;
+            }
+            if (!ok) break;
+        }
+    } else {
+        // ------------------------------------------- sums over the warps
+        const int buf = warp - kSumWarp0;
+        const int g = lane >> 2, c = lane & 3;
+        for (uint32_t n = 0;; ++n) {
+            if (!mbar_wait_warp(&rfull[buf], n & 1u, wc)) break;
+            const int t = rinfo[2 * buf], grp = rinfo[2 * buf + 1];
+            if (t < 0) break;
+            float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int w = 0; w < kMulWarps; ++w) {
+                const float4 r = red[(buf * kMulWarps + w) * 32 + lane];
+                v[0] += r.x;
+                v[1] += r.y;
+                v[2] += r.z;
+                v[3] += r.w;
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&rempty[buf]);
+            const FewItem it = few_item(t, tiles1, tiles2, t < tiles1 + tiles2 ? 0 : meta->n_pass);
+            const int n_rows = it.pass < 0 ? p.T : meta->pass_n[it.pass];
+            const int row0 = it.pass < 0 ? 0 : meta->pass_row[it.pass];
+            // v[0], v[1]: weight row g, tokens 2c and 2c + 1; v[2], v[3]: row g + 8
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int r = grp * 8 + 2 * c + i;
+                if (r >= n_rows) continue;
+                const int slot = it.pass < 0 ? S + r : meta->slot[row0 + r];
+                if (it.second) {
+                    const float w = it.pass < 0 ? 1.0f : __ldcg(p.w + slot);
+                    float *o = p.yp + (size_t)slot * p.d + it.tile * 16 + g;
+                    o[0] = w * v[i];
+                    o[8] = w * v[2 + i];
                 } else {
-                    int old = 0;
-                    if (lane == 0) old = atom_add_acq_rel(y_done + it.tile, 1);
-                    old = __shfl_sync(0xffffffffu, old, 0);
-                    __syncwarp();
-                    if (old == meta->n_units - 1) {
-                        // every product of these 16 columns is there
-                        for (int i = lane; i < p.T * 16; i += 32) {
-                            const int tk = i >> 4, n = it.tile * 16 + (i & 15);
-                            float sum = __ldcg(p.yp + (size_t)(S + tk) * p.d + n);
-                            for (int j = 0; j < p.k; ++j)
-                                sum += __ldcg(p.yp + (size_t)(tk * p.k + j) * p.d + n);
-                            p.y[(size_t)tk * p.d + n] =
-                                (uint16_t)(pack_bf16x2(sum, 0.0f) & 0xFFFFu);
-                        }
-                    }
+                    const float h = swiglu_clamped_nan(v[i], v[2 + i], p.clamp);
+                    p.h[(size_t)slot * p.I + it.tile * 8 + g] =
+                        (uint16_t)(pack_bf16x2(h, 0.0f) & 0xFFFFu);
                 }
             }
             __syncwarp();
-            if (lane == 0) mbar_arrive(rempty);
-            ++n_item;
+            if (!it.second) {
+                if (lane == 0) red_release_gpu_add(h_done + 1 + it.pass, 1);
+                continue;
+            }
+            int old = 0;
+            if (lane == 0) old = atom_add_acq_rel(y_done + it.tile, 1);
+            old = __shfl_sync(0xffffffffu, old, 0);
+            __syncwarp();
+            if (old != meta->n_units - 1) continue;
+            // every product of these 16 columns is there
+            for (int i = lane; i < p.T * 16; i += 32) {
+                const int tk = i >> 4, n16 = it.tile * 16 + (i & 15);
+                float sum = __ldcg(p.yp + (size_t)(S + tk) * p.d + n16);
+                for (int j = 0; j < p.k; ++j)
+                    sum += __ldcg(p.yp + (size_t)(tk * p.k + j) * p.d + n16);
+                p.y[(size_t)tk * p.d + n16] = (uint16_t)(pack_bf16x2(sum, 0.0f) & 0xFFFFu);
+            }
         }
     }
 
@@ -662,6 +813,15 @@ moe_status launch_experts_nt(const FewParams &p, cudaStream_t st) {
 
 }  // namespace
 
+// Rows of `row_bytes` bytes as [row_bytes / 128][rows][128]: a box of 16 x 8 x
+// 128 is 16 whole chunks of eight rows, eight rows of a chunk side by side.
+static bool encode_rows_of_chunks(CUtensorMap *tm, const void *base, uint64_t rows, int row_bytes) {
+    const int chunks = row_bytes / kChunk;
+    return encode_tmap_u8_3d_sw128(tm, base, chunks > 0 ? kChunk : row_bytes, rows,
+                                   chunks > 0 ? chunks : 1, row_bytes, kChunk, kChunk, 8,
+                                   kRowBytes / kChunk);
+}
+
 bool few_supported(int T, int d, int E, int k, int I) {
     return T >= 1 && T <= kFewT && d >= 128 && d % 128 == 0 && I >= 64 && I % 64 == 0 && E >= 1 &&
            E <= kFewE && k >= 1 && k <= kFewK && k <= E && d <= (1 << 20) && I <= (1 << 20);
@@ -710,6 +870,10 @@ moe_status launch_few(const moe_few_args *a, cudaStream_t st) {
     p.status = device_status_ptr();
     if (!p.status) return MOE_ERR_CUDA;
     p.wait_limit = kWaitLimitCycles;
+    const int elt = fp8 ? 1 : 2;
+    if (!encode_rows_of_chunks(&p.tm13, p.W13, (uint64_t)(p.E + 1) * 2 * p.I, p.d * elt) ||
+        !encode_rows_of_chunks(&p.tm2, p.W2, (uint64_t)(p.E + 1) * p.d, p.I * elt))
+        return MOE_ERR_CUDA;
     const int et = (p.E + 15) / 16;
     int splits = num_sms() / et;
     splits = splits < 1 ? 1 : splits > kGateSplits ? kGateSplits : splits;

@@ -40,6 +40,12 @@ bool encode_tmap_u8_2d(CUtensorMap *tm, const void *base, uint64_t inner, uint64
                        uint64_t row_pitch_bytes, uint32_t box_inner, uint32_t box_outer,
                        int swizzle_bytes);
 
+// 3-D byte array [n2][n1][n0] with pitches of dimensions 1 and 2, boxes b2 x b1
+// x b0, 128-byte swizzle.
+bool encode_tmap_u8_3d_sw128(CUtensorMap *tm, const void *base, uint64_t n0, uint64_t n1,
+                             uint64_t n2, uint64_t pitch1, uint64_t pitch2, uint32_t b0,
+                             uint32_t b1, uint32_t b2);
+
 inline moe_status cuda_status(cudaError_t e) { return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA; }
 
 inline bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
