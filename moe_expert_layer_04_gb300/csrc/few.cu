@@ -26,8 +26,8 @@
 // so the kernel needs no particular number of resident CTAs.
 //
 // Items: 8 gate rows and the matching 8 up rows of W13 (both land in the same
-// thread, which applies the SwiGLU), or 16 rows of W2.  The 16 warps split the
-// contraction, each with mma.m16n8k16 (weights x 8 tokens, bf16, fp32 sums; at
+// thread, which applies the SwiGLU), or 16 rows of W2.  Two groups of eight
+// warps take items in turn and split the contraction, each with mma.m16n8k16 (weights x 8 tokens, bf16, fp32 sums; at
 // a few rows a weight the matrix pipe is nearly idle, so the 128-row tiles of
 // tcgen05 would only add padding); their partial sums meet in shared memory in
 // a fixed order.  FP8 weights are expanded to bf16 in registers, exactly, and
@@ -49,12 +49,17 @@ constexpr int kFewE = 1024;
 constexpr int kGateWarps = 8;
 constexpr int kGateSplits = 16;        // at most
 constexpr int kMulWarps = 16;
+constexpr int kGroups = 2;             // of multiplying warps; they take items in turn
+constexpr int kGroupWarps = kMulWarps / kGroups;
 constexpr int kSumWarps = 4;           // each with a buffer of partial sums of its own
+constexpr int kGroupSums = kSumWarps / kGroups;
 constexpr int kCopyWarp = kMulWarps, kPlanWarp = kMulWarps + 1, kSumWarp0 = kMulWarps + 2;
 constexpr int kFewThreads = 32 * (kSumWarp0 + kSumWarps);
 constexpr int kPlanSlots = 4;          // items between the planning and the copying warp
-constexpr int kChunk = 128;            // weight bytes of a row for one multiplying warp
-constexpr int kRowBytes = kMulWarps * kChunk;   // weight bytes of a row in a stage
+constexpr int kChunk = 128;            // weight bytes of a row that a warp takes at a time
+constexpr int kWarpChunks = 2;         // chunks of a stage for one warp
+constexpr int kStageChunks = kGroupWarps * kWarpChunks;
+constexpr int kRowBytes = kStageChunks * kChunk;   // weight bytes of a row in a stage
 constexpr int kFewStage = 16 * kRowBytes;       // two boxes of 8 rows
 constexpr int kW2Tiles = 2;            // tiles of 16 rows in an item of W2
 
@@ -94,12 +99,15 @@ __device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// With an L2 policy: the weights pass through L2 once and must not push out what
+// every call uses again (the kernels' code, W_g, the token rows).
 __device__ __forceinline__ void tma_load_3d(void *dst, const CUtensorMap *tm, uint64_t *bar, int c0,
-                                            int c1, int c2) {
+                                            int c1, int c2, uint64_t policy) {
     asm volatile(
         "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(dst)),
-        "l"(reinterpret_cast<uint64_t>(tm)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2)
+        ".L2::cache_hint [%0], [%1, {%3, %4, %5}], [%2], %6;" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(tm)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2),
+        "l"(policy)
         : "memory");
 }
 
@@ -242,9 +250,11 @@ struct FewItem {
 
 template <bool FP8, int NT>
 struct FewShape {
-    static constexpr int STAGES = 5;
-    static constexpr int RED = kSumWarps * kMulWarps * 128 * 4;
-    static constexpr int SMEM = 1024 + STAGES * kFewStage + RED + (int)sizeof(FewMeta) + 512;
+    static constexpr int STAGES = 6;
+    static constexpr int RED = kSumWarps * kGroupWarps * 128 * 4;
+    static constexpr int SCALES = FP8 ? STAGES * 2 * kStageChunks * 4 : 0;
+    static constexpr int SMEM =
+        1024 + STAGES * kFewStage + RED + SCALES + (int)sizeof(FewMeta) + 512;
     static constexpr int ELT = FP8 ? 1 : 2;
     static constexpr int STAGE_K = kRowBytes / ELT;   // contraction of a stage
     static constexpr int STEP = FP8 ? 64 : 32;        // of a step (64 bytes of a row, half a chunk)
@@ -267,15 +277,37 @@ __device__ __forceinline__ FewItem few_item(int t, int tiles1, int tiles2, int n
     return it;
 }
 
-// Eight E4M3 codes' worth: four codes -> two bf16 pairs (exact).
-__device__ __forceinline__ void e4m3x4_bf16(uint32_t w, uint32_t &lo, uint32_t &hi) {
-    uint32_t a, b;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(a) : "h"((uint16_t)(w & 0xFFFFu)));
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(b) : "h"((uint16_t)(w >> 16)));
-    const float2 fa = __half22float2(*reinterpret_cast<const __half2 *>(&a));
-    const float2 fb = __half22float2(*reinterpret_cast<const __half2 *>(&b));
-    lo = pack_bf16x2(fa.x, fa.y);
-    hi = pack_bf16x2(fb.x, fb.y);
+// Four E4M3 codes -> bf16 pairs (codes 0, 2) and (1, 3), exact: sign and the
+// seven other bits move to their places in bf16, where they read as the value
+// times 2^-120 (the exponent biases differ by 120; subnormal codes become
+// subnormal bf16), and one multiplication puts that right.  Ten instructions
+// for four codes at the full rate; through the converter instruction (f16,
+// fp32, bf16) a stage took 0.55 us of the SM, more than its rows take to
+// arrive.  `top` collects the largest magnitude bits of either half: 0x7F0 is
+// the NaN code, which would otherwise read as 480.
+__device__ __forceinline__ void e4m3x4_bf16(uint32_t w, uint32_t &even, uint32_t &odd,
+                                            uint32_t &top) {
+    const uint32_t a = (w << 4) & 0x07F007F0u, b = (w >> 4) & 0x07F007F0u;
+    top = __vimax3_u16x2(top, a, b);
+    const uint32_t scale = 0x7B807B80u;   // 2^120 twice
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(even) : "r"(a | ((w << 8) & 0x80008000u)), "r"(scale));
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(odd) : "r"(b | (w & 0x80008000u)), "r"(scale));
+}
+
+__device__ __forceinline__ bool e4m3_nan_seen(uint32_t top) {
+    return (top & 0xFFFFu) >= 0x7F0u || (top >> 16) >= 0x7F0u;
+}
+
+__device__ __forceinline__ void cp_async4(void *dst, const void *src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src)
+                 : "memory");
+}
+
+// This lane's arrival on `bar` once its cp.async copies have landed (counted in
+// the barrier's expected arrivals).
+__device__ __forceinline__ void cp_async_arrive(uint64_t *bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar))
+                 : "memory");
 }
 
 template <bool FP8, int NT>
@@ -286,7 +318,10 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_experts_kernel(
     uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     uint8_t *ring = smem;
     float4 *red = reinterpret_cast<float4 *>(smem + SH::STAGES * kFewStage);
-    FewMeta *meta = reinterpret_cast<FewMeta *>(smem + SH::STAGES * kFewStage + SH::RED);
+    // FP8: the stage's scales, of the chunks' gate rows and up rows
+    float *scales = reinterpret_cast<float *>(smem + SH::STAGES * kFewStage + SH::RED);
+    FewMeta *meta =
+        reinterpret_cast<FewMeta *>(smem + SH::STAGES * kFewStage + SH::RED + SH::SCALES);
     uint64_t *full = reinterpret_cast<uint64_t *>(meta + 1);
     uint64_t *ifull = full + SH::STAGES;     // `info` of the stage is written (its rows may not be there)
     uint64_t *empty = ifull + SH::STAGES;
@@ -295,20 +330,20 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_experts_kernel(
     uint64_t *qfull = rempty + kSumWarps;    // a planned item is in the queue
     uint64_t *qempty = qfull + kPlanSlots;
     volatile int *queue = reinterpret_cast<volatile int *>(qempty + kPlanSlots);   // first tile
-    volatile int *info = queue + kPlanSlots;                          // tile, k per stage
-    volatile int *rinfo = info + 2 * SH::STAGES;                     // tile, group per buffer
+    volatile int *info = queue + kPlanSlots;                          // tile, k, group per stage
+    volatile int *rinfo = info + 3 * SH::STAGES;                     // tile, group per buffer
     volatile int *abort_s = rinfo + 2 * kSumWarps;
     int *last_s = const_cast<int *>(abort_s) + 1;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (int s = 0; s < SH::STAGES; ++s) {
-            mbar_init(&full[s], 1);
+            mbar_init(&full[s], FP8 ? 33 : 1);
             mbar_init(&ifull[s], 1);
-            mbar_init(&empty[s], kMulWarps);
+            mbar_init(&empty[s], kMulWarps);   // the other group's too: it has seen the stage
         }
         for (int b = 0; b < kSumWarps; ++b) {
-            mbar_init(&rfull[b], kMulWarps);
+            mbar_init(&rfull[b], kGroupWarps);
             mbar_init(&rempty[b], 1);
         }
         for (int b = 0; b < kPlanSlots; ++b) {
@@ -417,104 +452,122 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_experts_kernel(
         }
     } else if (warp == kCopyWarp) {
         // ------------------------------------------------------------ copy
-        if (lane == 0) {
-            uint32_t s = 0, ph = 0;
-            int last[SH::STAGES];
+        uint32_t s = 0, ph = 0;
+        int last[SH::STAGES];
 #pragma unroll
-            for (int i = 0; i < SH::STAGES; ++i) last[i] = -1;
-            bool ok = true;
-            for (uint32_t n = 0; ok; ++n) {
-                const uint32_t b = n % kPlanSlots;
-                if (!mbar_wait(&qfull[b], n / kPlanSlots & 1u, wc)) break;
-                const int t = queue[b];
-                mbar_arrive(&qempty[b]);
-                if (t < 0) {
-                    if (mbar_wait(&empty[s], ph ^ 1u, wc)) {
-                        info[s] = -1;
-                        mbar_arrive(&ifull[s]);
-                    }
-                    break;
+        for (int i = 0; i < SH::STAGES; ++i) last[i] = -1;
+        const uint64_t policy = policy_evict_first();
+        bool ok = true;
+        for (uint32_t n = 0; ok; ++n) {
+            const uint32_t b = n % kPlanSlots;
+            if (!mbar_wait_warp(&qfull[b], n / kPlanSlots & 1u, wc)) break;
+            const int t = queue[b];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&qempty[b]);
+            if (t < 0) {
+                if (!mbar_wait_warp(&empty[s], ph ^ 1u, wc)) break;
+                if (lane == 0) {
+                    info[s] = -1;
+                    mbar_arrive(&ifull[s]);
                 }
-                FewItem it = few_item(t, tiles1, tiles2,
-                                      t < tiles1 + tiles2 ? 0 : meta->n_pass);
-                const int e = it.pass < 0 ? p.E : meta->pass_e[it.pass];
-                const int K = it.second ? p.I : p.d;
-                const int chunks = K * SH::ELT / kChunk;   // whole ones; see the tail below
-                const CUtensorMap *tm = it.second ? &p.tm2 : &p.tm13;
-                for (int sub = 0; ok && sub < (it.second ? kW2Tiles : 1); ++sub) {
-                    // 8 gate rows and the matching 8 up rows, or 16 rows of W2
-                    const int r0 = it.second ? e * p.d + (it.tile + sub) * 16
-                                             : e * 2 * p.I + it.tile * 8;
-                    const int r1 = r0 + (it.second ? 8 : p.I);
-                    for (int k0 = 0; k0 < K; k0 += SH::STAGE_K) {
-                        if (!mbar_wait(&empty[s], ph ^ 1u, wc)) { ok = false; break; }
+                break;
+            }
+            const FewItem it =
+                few_item(t, tiles1, tiles2, t < tiles1 + tiles2 ? 0 : meta->n_pass);
+            const int e = it.pass < 0 ? p.E : meta->pass_e[it.pass];
+            const int K = it.second ? p.I : p.d;
+            const int chunks = K * SH::ELT / kChunk;   // whole ones
+            const CUtensorMap *tm = it.second ? &p.tm2 : &p.tm13;
+            for (int sub = 0; ok && sub < (it.second ? kW2Tiles : 1); ++sub) {
+                // 8 gate rows and the matching 8 up rows, or 16 rows of W2
+                const int tile = it.tile + sub;
+                const int r0 = it.second ? e * p.d + tile * 16 : e * 2 * p.I + tile * 8;
+                const int r1 = r0 + (it.second ? 8 : p.I);
+                const float *sc = nullptr;   // FP8: this lane's scale of the first stage
+                const int kb = fp8_blocks(K), my_kb = lane & (kStageChunks - 1);
+                if constexpr (FP8) {
+                    const int row = it.second ? tile * 16
+                                              : tile * 8 + (lane >= kStageChunks ? p.I : 0);
+                    const int rows = it.second ? p.d : 2 * p.I;
+                    sc = (it.second ? p.W2_s : p.W13_s) +
+                         ((size_t)e * fp8_blocks(rows) + row / kFp8Block) * kb + my_kb;
+                }
+                for (int k0 = 0; k0 < K; k0 += SH::STAGE_K) {
+                    if (!mbar_wait_warp(&empty[s], ph ^ 1u, wc)) { ok = false; break; }
+                    const int c0 = k0 * SH::ELT / kChunk;
+                    if (lane == 0) {
                         info[s] = t + sub;
                         info[SH::STAGES + s] = k0;
+                        info[2 * SH::STAGES + s] = (int)(n % kGroups);
                         mbar_arrive(&ifull[s]);
-                        const int c0 = k0 * SH::ELT / kChunk;
                         if (c0 < chunks) {
                             uint8_t *dst = ring + s * kFewStage;
                             mbar_arrive_expect_tx(&full[s], kFewStage);
-                            tma_load_3d(dst, tm, &full[s], 0, r0, c0);
-                            tma_load_3d(dst + kFewStage / 2, tm, &full[s], 0, r1, c0);
+                            tma_load_3d(dst, tm, &full[s], 0, r0, c0, policy);
+                            tma_load_3d(dst + kFewStage / 2, tm, &full[s], 0, r1, c0, policy);
                         } else {
                             mbar_arrive(&full[s]);
                         }
-                        last[s] = (int)ph;
-                        if (++s == SH::STAGES) { s = 0; ph ^= 1u; }
                     }
+                    if constexpr (FP8) {
+                        if (c0 + my_kb < kb)
+                            cp_async4(scales + s * 2 * kStageChunks + lane, sc + c0);
+                        cp_async_arrive(&full[s]);
+                    }
+                    last[s] = (int)ph;
+                    if (++s == SH::STAGES) { s = 0; ph ^= 1u; }
                 }
             }
-            if (*abort_s) {
-                // drain the copies still in flight before the CTA exits
-                for (int i = 0; i < SH::STAGES; ++i)
-                    if (last[i] >= 0)
-                        mbar_wait_teardown(&full[i], (uint32_t)last[i], p.wait_limit);
-            }
+        }
+        if (*abort_s) {
+            // drain the copies still in flight before the CTA exits
+            for (int i = 0; i < SH::STAGES; ++i)
+                if (last[i] >= 0) mbar_wait_teardown(&full[i], (uint32_t)last[i], p.wait_limit);
         }
     } else if (warp < kMulWarps) {
         // -------------------------------------------------------- multiply
-        // A stage's token operands are loaded as soon as its item is known,
-        // while its weight rows are still on their way.
+        // Two groups of eight warps take items in turn, so that one's loads of
+        // token operands overlap the other's products.  The operands of a stage
+        // are loaded as soon as its item is known, while its weight rows may
+        // still be on their way.
         uint32_t s = 0, ph = 0, unit = 0;
+        const int group = warp / kGroupWarps, wl = warp % kGroupWarps;
         const int g = lane >> 2, c = lane & 3;
         float acc[NT][4];
         const uint16_t *act[NT];   // this lane's token row of each group of 8, or null
         FewItem it{};
         int n_rows = 0, row0 = 0, K = 0;
-        const float *sc0 = nullptr, *sc1 = nullptr;
         constexpr int NV = FP8 ? 2 : 1;
+        constexpr int STEPS = 2 * kWarpChunks;
+        // steps whose token operands are loaded ahead (registers: the rest on use)
+        constexpr int PRE = FP8 && NT > 1 ? STEPS / 2 : STEPS;
         while (true) {
             if (!mbar_wait_warp(&ifull[s], ph, wc)) break;
             const int t = info[s], k0 = info[SH::STAGES + s];
             if (t < 0) {
-                if (lane == 0) {   // tell the sum warps, one buffer each
-                    for (int b = 0; b < kSumWarps; ++b, ++unit) {
-                        const uint32_t buf = unit % kSumWarps;
-                        if (!mbar_wait(&rempty[buf], (unit / kSumWarps & 1u) ^ 1u, wc)) break;
-                        if (warp == 0) rinfo[2 * buf] = -1;
+                if (lane == 0) {   // tell this group's sum warps, one buffer each
+                    for (int b = 0; b < kGroupSums; ++b, ++unit) {
+                        const uint32_t buf = group * kGroupSums + unit % kGroupSums;
+                        if (!mbar_wait(&rempty[buf], (unit / kGroupSums & 1u) ^ 1u, wc)) break;
+                        if (wl == 0) rinfo[2 * buf] = -1;
                         mbar_arrive(&rfull[buf]);
                     }
                 }
                 break;
+            }
+            if (info[2 * SH::STAGES + s] != group) {
+                // the other group's; both groups release every stage, so that
+                // neither can be a lap behind
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&empty[s]);
+                if (++s == SH::STAGES) { s = 0; ph ^= 1u; }
+                continue;
             }
             if (k0 == 0) {
                 it = few_item(t, tiles1, tiles2, t < tiles1 + tiles2 ? 0 : meta->n_pass);
                 K = it.second ? p.I : p.d;
                 n_rows = it.pass < 0 ? p.T : meta->pass_n[it.pass];
                 row0 = it.pass < 0 ? 0 : meta->pass_row[it.pass];
-                const int e = it.pass < 0 ? p.E : meta->pass_e[it.pass];
-                if constexpr (FP8) {
-                    const int kb = fp8_blocks(K);
-                    if (it.second) {
-                        sc0 = p.W2_s + ((size_t)e * fp8_blocks(p.d) + it.tile * 16 / 128) * kb;
-                        sc1 = sc0;
-                    } else {
-                        const float *b = p.W13_s + (size_t)e * fp8_blocks(2 * p.I) * kb;
-                        sc0 = b + (size_t)(it.tile * 8 / 128) * kb;
-                        sc1 = b + (size_t)((p.I + it.tile * 8) / 128) * kb;
-                    }
-                }
                 if (it.second) {
                     // the h rows of this pass: one signal per column tile and
                     // group of 8 rows
@@ -539,112 +592,122 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_experts_kernel(
                 }
             }
             const int nt = (n_rows + 7) >> 3;
-            const int steps = min(SH::STAGE_K, K - k0) / SH::STEP;
-            const int kk = k0 + warp * 2 * SH::STEP + c * (SH::STEP / 4);
-            // token operand of step u, group j
+            // steps of this warp in this stage: the first `steps` of STEPS
+            const int steps = min(SH::STAGE_K, K - k0) / SH::STEP - wl * STEPS;
+            const int kk = k0 + wl * STEPS * SH::STEP + c * (SH::STEP / 4);
+            // token operand of step u, group j; FP8: pairs (0, 2) and (1, 3) of
+            // each four, as the codes are expanded
             auto load_act = [&](int u, int j, uint4 (&v)[NV]) {
 #pragma unroll
                 for (int i = 0; i < NV; ++i) {
                     v[i] = make_uint4(0, 0, 0, 0);
-                    if (act[j] && warp * 2 + u < steps)
+                    if (act[j] && u < steps)
                         v[i] = __ldcg(
                             reinterpret_cast<const uint4 *>(act[j] + kk + u * SH::STEP + 8 * i));
                 }
             };
-            uint4 v0[2][NV];
-            load_act(0, 0, v0[0]);
-            load_act(1, 0, v0[1]);
-            float f0 = 0.0f, f1 = 0.0f;
-            if constexpr (FP8) {
-                // a warp's two steps are one block of 128
-                if (warp * 2 < steps) {
-                    f0 = __ldg(sc0 + k0 / kFp8Block + warp);
-                    f1 = __ldg(sc1 + k0 / kFp8Block + warp);
-                }
-            }
+            uint4 v0[PRE][NV];
+#pragma unroll
+            for (int u = 0; u < PRE; ++u) load_act(u, 0, v0[u]);
             if (!mbar_wait_warp(&full[s], ph, wc)) break;
-            // the warp's chunk: rows g and g + 8, 128 bytes each, 16-byte pieces
-            // exchanged by row (128-byte swizzle).  Lanes of odd rows read their
-            // second half first, so that no two rows of a quarter warp meet in
-            // a bank.
-            uint4 wq[2][2];   // [half][row g / g + 8]
-            {
-                const uint32_t a0 =
-                    smem_u32(ring + s * kFewStage) + warp * (8 * kChunk) + g * kChunk;
-                const uint32_t first = ((uint32_t)((g & 1) * 4 + c) ^ g) << 4;
-                const uint4 p0 = ld_shared_v4(a0 + first), q0 = ld_shared_v4(a0 + (first ^ 64u));
-                const uint4 p1 = ld_shared_v4(a0 + kFewStage / 2 + first);
-                const uint4 q1 = ld_shared_v4(a0 + kFewStage / 2 + (first ^ 64u));
-                const bool odd = g & 1;
-                wq[0][0] = odd ? q0 : p0;
-                wq[1][0] = odd ? p0 : q0;
-                wq[0][1] = odd ? q1 : p1;
-                wq[1][1] = odd ? p1 : q1;
-            }
-            if constexpr (FP8) {
-                // a contraction that ends inside a chunk: its last 64 codes are
-                // not in the stage (a copied row would run into the next one)
-                if ((K & 64) && k0 + warp * 128 + 64 == K) {
-                    const uint8_t *w = static_cast<const uint8_t *>(it.second ? p.W2 : p.W13);
-                    const int e = it.pass < 0 ? p.E : meta->pass_e[it.pass];
-                    const size_t r = it.second ? (size_t)e * p.d + it.tile * 16 + g
-                                               : (size_t)e * 2 * p.I + it.tile * 8 + g;
-                    w += r * K + K - 64 + c * 16;
-                    wq[0][0] = __ldg(reinterpret_cast<const uint4 *>(w));
-                    wq[0][1] = __ldg(reinterpret_cast<const uint4 *>(
-                        w + (size_t)(it.second ? 8 : p.I) * K));
+#pragma unroll
+            for (int ch = 0; ch < kWarpChunks; ++ch) {
+                if (2 * ch >= steps) break;
+                const int chunk = wl * kWarpChunks + ch;
+                // rows g and g + 8 of the chunk, 128 bytes each, 16-byte pieces
+                // exchanged by row (128-byte swizzle).  Lanes of odd rows read
+                // their second half first, so that no two rows of a quarter warp
+                // meet in a bank.
+                uint4 wq[2][2];   // [half][row g / g + 8]
+                {
+                    const uint32_t a0 =
+                        smem_u32(ring + s * kFewStage) + chunk * (8 * kChunk) + g * kChunk;
+                    const uint32_t first = ((uint32_t)((g & 1) * 4 + c) ^ g) << 4;
+                    const uint4 p0 = ld_shared_v4(a0 + first), q0 = ld_shared_v4(a0 + (first ^ 64u));
+                    const uint4 p1 = ld_shared_v4(a0 + kFewStage / 2 + first);
+                    const uint4 q1 = ld_shared_v4(a0 + kFewStage / 2 + (first ^ 64u));
+                    const bool odd = g & 1;
+                    wq[0][0] = odd ? q0 : p0;
+                    wq[1][0] = odd ? p0 : q0;
+                    wq[0][1] = odd ? q1 : p1;
+                    wq[1][1] = odd ? p1 : q1;
                 }
-            }
-            float part[FP8 ? NT : 1][4];   // FP8: sums of this stage, not yet scaled
-            if constexpr (FP8) {
+                if constexpr (!FP8) {
 #pragma unroll
-                for (int j = 0; j < NT; ++j)
+                    for (int h = 0; h < 2; ++h) {
+                        const uint4 wa = wq[h][0], wb = wq[h][1];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) part[j][i] = 0.0f;
-            }
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                const int st = warp * 2 + u;
-                if (st < steps) {
-                    const uint4 wa = wq[u][0], wb = wq[u][1];
-                    uint32_t x0[4], x1[4], y0[4], y1[4];   // FP8: the codes' values
-                    if constexpr (FP8) {
-                        const uint32_t qa[4] = {wa.x, wa.y, wa.z, wa.w};
-                        const uint32_t qb[4] = {wb.x, wb.y, wb.z, wb.w};
-#pragma unroll
-                        for (int m = 0; m < 4; ++m) {
-                            e4m3x4_bf16(qa[m], x0[m], x1[m]);
-                            e4m3x4_bf16(qb[m], y0[m], y1[m]);
+                        for (int j = 0; j < NT; ++j) {
+                            if (j >= nt) break;
+                            uint4 v[NV];
+                            if (j > 0) load_act(2 * ch + h, j, v);
+                            const uint4 b = j > 0 ? v[0] : v0[2 * ch + h][0];
+                            mma_bf16(acc[j], wa.x, wb.x, wa.y, wb.y, b.x, b.y);
+                            mma_bf16(acc[j], wa.z, wb.z, wa.w, wb.w, b.z, b.w);
                         }
                     }
+                } else {
+                    // a contraction that ends inside a chunk: its last 64 codes
+                    // are not in the stage (a copied row would run into the next)
+                    if ((K & 64) && k0 + chunk * 128 + 64 == K) {
+                        const uint8_t *w = static_cast<const uint8_t *>(it.second ? p.W2 : p.W13);
+                        const int e = it.pass < 0 ? p.E : meta->pass_e[it.pass];
+                        const size_t r = it.second ? (size_t)e * p.d + it.tile * 16 + g
+                                                   : (size_t)e * 2 * p.I + it.tile * 8 + g;
+                        w += r * K + K - 64 + c * 16;
+                        wq[0][0] = __ldg(reinterpret_cast<const uint4 *>(w));
+                        wq[0][1] = __ldg(reinterpret_cast<const uint4 *>(
+                            w + (size_t)(it.second ? 8 : p.I) * K));
+                    }
+                    float part[NT][4];   // this block of 128, not yet scaled
 #pragma unroll
-                    for (int j = 0; j < NT; ++j) {
-                        if (j >= nt) break;
-                        uint4 v[NV];
-                        if (j > 0) load_act(u, j, v);
-                        const uint4 *b = j > 0 ? v : v0[u];
-                        if constexpr (FP8) {
+                    for (int j = 0; j < NT; ++j)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) part[j][i] = 0.0f;
+                    uint32_t top0 = 0, top1 = 0;
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        if (2 * ch + h >= steps) break;
+                        const uint32_t qa[4] = {wq[h][0].x, wq[h][0].y, wq[h][0].z, wq[h][0].w};
+                        const uint32_t qb[4] = {wq[h][1].x, wq[h][1].y, wq[h][1].z, wq[h][1].w};
+                        uint32_t x0[4], x1[4], y0[4], y1[4];
+#pragma unroll
+                        for (int m = 0; m < 4; ++m) {
+                            e4m3x4_bf16(qa[m], x0[m], x1[m], top0);
+                            e4m3x4_bf16(qb[m], y0[m], y1[m], top1);
+                        }
+#pragma unroll
+                        for (int j = 0; j < NT; ++j) {
+                            if (j >= nt) break;
+                            uint4 v[NV];
+                            const bool ahead = j == 0 && 2 * ch + h < PRE;
+                            if (!ahead) load_act(2 * ch + h, j, v);
+                            const uint4 *b = ahead ? v0[(2 * ch + h) % PRE] : v;
                             const uint32_t bv[8] = {b[0].x, b[0].y, b[0].z, b[0].w,
                                                     b[NV - 1].x, b[NV - 1].y, b[NV - 1].z,
                                                     b[NV - 1].w};
 #pragma unroll
                             for (int m = 0; m < 4; ++m)
-                                mma_bf16(part[j], x0[m], y0[m], x1[m], y1[m], bv[2 * m],
-                                         bv[2 * m + 1]);
-                        } else {
-                            mma_bf16(acc[j], wa.x, wb.x, wa.y, wb.y, b[0].x, b[0].y);
-                            mma_bf16(acc[j], wa.z, wb.z, wa.w, wb.w, b[0].z, b[0].w);
+                                mma_bf16(part[j], x0[m], y0[m], x1[m], y1[m],
+                                         __byte_perm(bv[2 * m], bv[2 * m + 1], 0x5410),
+                                         __byte_perm(bv[2 * m], bv[2 * m + 1], 0x7632));
                         }
                     }
-                }
-            }
-            if constexpr (FP8) {
+                    // a NaN code in a row of the block: NaN for every token
+                    float f0 = scales[s * 2 * kStageChunks + chunk];
+                    float f1 = scales[(s * 2 + 1) * kStageChunks + chunk];
+                    const unsigned quad = 0xFu << (lane & 28);
+                    if (__ballot_sync(0xffffffffu, e4m3_nan_seen(top0)) & quad)
+                        f0 = __int_as_float(0x7FFFFFFF);
+                    if (__ballot_sync(0xffffffffu, e4m3_nan_seen(top1)) & quad)
+                        f1 = __int_as_float(0x7FFFFFFF);
 #pragma unroll
-                for (int j = 0; j < NT; ++j) {
-                    acc[j][0] = fmaf(part[j][0], f0, acc[j][0]);
-                    acc[j][1] = fmaf(part[j][1], f0, acc[j][1]);
-                    acc[j][2] = fmaf(part[j][2], f1, acc[j][2]);
-                    acc[j][3] = fmaf(part[j][3], f1, acc[j][3]);
+                    for (int j = 0; j < NT; ++j) {
+                        acc[j][0] = fmaf(part[j][0], f0, acc[j][0]);
+                        acc[j][1] = fmaf(part[j][1], f0, acc[j][1]);
+                        acc[j][2] = fmaf(part[j][2], f1, acc[j][2]);
+                        acc[j][3] = fmaf(part[j][3], f1, acc[j][3]);
+                    }
                 }
             }
             __syncwarp();
@@ -656,12 +719,12 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_experts_kernel(
 #pragma unroll
             for (int j = 0; j < NT; ++j) {
                 if (j >= nt) break;
-                const uint32_t buf = unit % kSumWarps;
-                ok = mbar_wait_warp(&rempty[buf], (unit / kSumWarps & 1u) ^ 1u, wc);
+                const uint32_t buf = group * kGroupSums + unit % kGroupSums;
+                ok = mbar_wait_warp(&rempty[buf], (unit / kGroupSums & 1u) ^ 1u, wc);
                 if (!ok) break;
-                red[(buf * kMulWarps + warp) * 32 + lane] =
+                red[(buf * kGroupWarps + wl) * 32 + lane] =
                     make_float4(acc[j][0], acc[j][1], acc[j][2], acc[j][3]);
-                if (warp == 0 && lane == 0) {
+                if (wl == 0 && lane == 0) {
                     rinfo[2 * buf] = t;
                     rinfo[2 * buf + 1] = j;
                 }
@@ -681,8 +744,8 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_experts_kernel(
             if (t < 0) break;
             float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-            for (int w = 0; w < kMulWarps; ++w) {
-                const float4 r = red[(buf * kMulWarps + w) * 32 + lane];
+            for (int w = 0; w < kGroupWarps; ++w) {
+                const float4 r = red[(buf * kGroupWarps + w) * 32 + lane];
                 v[0] += r.x;
                 v[1] += r.y;
                 v[2] += r.z;
