@@ -36,8 +36,10 @@
 // the second matmul go to fp32 rows per (token, slot); the last item of a
 // column group to finish adds them up in slot order, so results do not depend
 // on who finishes when.
+#include <cfloat>
+#include <climits>
+
 #include "fp8_common.cuh"
-#include "route_common.cuh"
 
 namespace moe {
 namespace {
@@ -82,7 +84,7 @@ struct FewParams {
     int n_counters;
     float *part;     // [splits, T, E] partial logits
     int32_t *ids;    // [T, k]
-    float *w, *ssel; // [T, k]
+    float *w;        // [T, k]
     uint16_t *h;     // [S + T, I]
     float *yp;       // [S + T, d]
     int splits;
@@ -126,13 +128,29 @@ __device__ __forceinline__ int atom_add_acq_rel(int *p, int v) {
 // global memory: a lane's 16 bytes of row l / 4 are eight consecutive k, fed
 // as two k-pairs to each of two MMAs; the token operand is read the same way,
 // so the order of k inside a step is the same on both sides.
+// Scores and keys are fp32 here (moe_route evaluates the sigmoid in fp64 and
+// rounds it): the logits' own sums differ between the two calls by more than
+// the fp32 sigmoid's error, and fp64 costs 6 us of latency that nothing hides.
+// Largest key of the warp and its id; equal keys: the lower id.
+__device__ __forceinline__ void warp_best(float &key, int &id) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        const float k2 = __shfl_xor_sync(0xffffffffu, key, o);
+        const int i2 = __shfl_xor_sync(0xffffffffu, id, o);
+        if (k2 > key || (k2 == key && i2 < id)) {
+            key = k2;
+            id = i2;
+        }
+    }
+}
+
+__device__ __forceinline__ float sigmoid_f32(float z) { return 1.0f / (1.0f + expf(-z)); }
+
 template <int EPL>
 __global__ void __launch_bounds__(kGateWarps * 32) few_gate_kernel(const __grid_constant__ FewParams p) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     __shared__ float red[kGateWarps][4][32];
     __shared__ int s_last;
-    __shared__ int s_e[kGateWarps][32];
-    __shared__ float s_z[kGateWarps][32], s_b[kGateWarps][32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int e0 = blockIdx.x * 16 + (lane >> 2);
     const int steps = p.d / 32;
@@ -174,7 +192,7 @@ __global__ void __launch_bounds__(kGateWarps * 32) few_gate_kernel(const __grid_
     if (threadIdx.x == 0) p.counters[0] = 0;
     for (int t = warp; t < p.T; t += kGateWarps) {
         int my_id = 0;
-        float my_s = 0.0f;
+        float my_s = 0.0f;   // lane j < k: expert and score of slot j
         if (p.hash) {
             if (lane < p.k) {
                 int tok = p.input_ids[t];
@@ -191,16 +209,16 @@ __global__ void __launch_bounds__(kGateWarps * 32) few_gate_kernel(const __grid_
                 for (int s = 0; s < p.splits; ++s)
                     z += __ldcg(p.part + ((size_t)s * p.T + t) * p.E + my_id);
                 if (p.logit_offset) z += p.logit_offset[my_id];
-                my_s = sigmoid_exact(z);
+                my_s = sigmoid_f32(z);
             }
         } else {
             const float *bt = p.bias + ((p.is_vision && p.is_vision[t]) ? p.E : 0);
-            float zv[EPL], bv[EPL];
+            float zv[EPL], key[EPL];
 #pragma unroll
             for (int i = 0; i < EPL; ++i) {
                 const int e = lane + 32 * i;
-                zv[i] = 0.0f;
-                bv[i] = e < p.E ? bt[e] : 0.0f;
+                zv[i] = e < p.E && p.logit_offset ? p.logit_offset[e] : 0.0f;
+                key[i] = e < p.E ? bt[e] : 0.0f;
             }
             // all experts' loads of a split together (their latency, not their
             // bytes, is what counts here)
@@ -211,19 +229,47 @@ __global__ void __launch_bounds__(kGateWarps * 32) few_gate_kernel(const __grid_
                 for (int i = 0; i < EPL; ++i)
                     if (lane + 32 * i < p.E) zv[i] += __ldcg(z + lane + 32 * i);
             }
-            if (p.logit_offset) {
 #pragma unroll
-                for (int i = 0; i < EPL; ++i)
-                    if (lane + 32 * i < p.E) zv[i] += p.logit_offset[lane + 32 * i];
+            for (int i = 0; i < EPL; ++i) {
+                zv[i] = sigmoid_f32(zv[i]);
+                const float kk = zv[i] + key[i];
+                key[i] = lane + 32 * i >= p.E ? -INFINITY : kk == kk ? kk : -FLT_MAX;
             }
-            route_topk_token<EPL>(zv, bv, lane, p.E, p.k, s_e[warp], s_z[warp], s_b[warp], my_id,
-                                  my_s);
+            for (int j = 0; j < p.k; ++j) {
+                float bk = -INFINITY, bs = 0.0f;
+                int be = INT_MAX;
+#pragma unroll
+                for (int i = 0; i < EPL; ++i) {   // ids grow with i: the first of equals stays
+                    if (key[i] > bk) {
+                        bk = key[i];
+                        bs = zv[i];
+                        be = lane + 32 * i;
+                    }
+                }
+                const int mine = be;
+                warp_best(bk, be);
+                const unsigned m = __ballot_sync(0xffffffffu, mine == be && be != INT_MAX);
+                bs = __shfl_sync(0xffffffffu, bs, m ? __ffs(m) - 1 : 0);
+                if (mine == be) {
+#pragma unroll
+                    for (int i = 0; i < EPL; ++i)
+                        if (lane + 32 * i == be) key[i] = -INFINITY;
+                }
+                if (lane == j) {
+                    my_id = be == INT_MAX ? 0 : be;
+                    my_s = bs;
+                }
+            }
         }
-        write_weights(t, p.k, lane, my_id, my_s, p.scaling, p.ids, p.w, p.ssel);
+        float sum = 0.0f;
+        for (int j = 0; j < p.k; ++j) sum += __shfl_sync(0xffffffffu, my_s, j);
         if (lane < p.k) {
             const size_t o = (size_t)t * p.k + lane;
+            const float w = sum > 0.0f ? p.scaling * my_s / sum : 0.0f;
+            p.ids[o] = my_id;
+            p.w[o] = w;
             if (p.ids_out) p.ids_out[o] = my_id;
-            if (p.w_out) p.w_out[o] = p.w[o];
+            if (p.w_out) p.w_out[o] = w;
         }
     }
 }
@@ -309,6 +355,11 @@ __device__ __forceinline__ void cp_async_arrive(uint64_t *bar) {
     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar))
                  : "memory");
 }
+
+// Weight row of a tile's eight that the MMA's row g takes: rows 0, 4, 1, 5, ...
+// The two rows that a quarter warp reads then lie in different halves of the
+// swizzled 128 bytes, so that no two of its loads meet in a bank.
+__device__ __forceinline__ int few_row(int g) { return (g >> 1) | (g & 1) << 2; }
 
 template <bool FP8, int NT>
 __global__ void __launch_bounds__(kFewThreads, 1) few_experts_kernel(
@@ -533,6 +584,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_experts_kernel(
         uint32_t s = 0, ph = 0, unit = 0;
         const int group = warp / kGroupWarps, wl = warp % kGroupWarps;
         const int g = lane >> 2, c = lane & 3;
+        const int pr = few_row(g);
         float acc[NT][4];
         const uint16_t *act[NT];   // this lane's token row of each group of 8, or null
         FewItem it{};
@@ -614,23 +666,17 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_experts_kernel(
             for (int ch = 0; ch < kWarpChunks; ++ch) {
                 if (2 * ch >= steps) break;
                 const int chunk = wl * kWarpChunks + ch;
-                // rows g and g + 8 of the chunk, 128 bytes each, 16-byte pieces
-                // exchanged by row (128-byte swizzle).  Lanes of odd rows read
-                // their second half first, so that no two rows of a quarter warp
-                // meet in a bank.
-                uint4 wq[2][2];   // [half][row g / g + 8]
+                // rows pr and pr + 8 of the chunk, 128 bytes each, 16-byte pieces
+                // exchanged by row (128-byte swizzle)
+                uint4 wq[2][2];   // [half][row pr / pr + 8]
                 {
                     const uint32_t a0 =
-                        smem_u32(ring + s * kFewStage) + chunk * (8 * kChunk) + g * kChunk;
-                    const uint32_t first = ((uint32_t)((g & 1) * 4 + c) ^ g) << 4;
-                    const uint4 p0 = ld_shared_v4(a0 + first), q0 = ld_shared_v4(a0 + (first ^ 64u));
-                    const uint4 p1 = ld_shared_v4(a0 + kFewStage / 2 + first);
-                    const uint4 q1 = ld_shared_v4(a0 + kFewStage / 2 + (first ^ 64u));
-                    const bool odd = g & 1;
-                    wq[0][0] = odd ? q0 : p0;
-                    wq[1][0] = odd ? p0 : q0;
-                    wq[0][1] = odd ? q1 : p1;
-                    wq[1][1] = odd ? p1 : q1;
+                        smem_u32(ring + s * kFewStage) + chunk * (8 * kChunk) + pr * kChunk;
+                    const uint32_t first = (uint32_t)(c ^ pr) << 4;
+                    wq[0][0] = ld_shared_v4(a0 + first);
+                    wq[1][0] = ld_shared_v4(a0 + (first ^ 64u));
+                    wq[0][1] = ld_shared_v4(a0 + kFewStage / 2 + first);
+                    wq[1][1] = ld_shared_v4(a0 + kFewStage / 2 + (first ^ 64u));
                 }
                 if constexpr (!FP8) {
 #pragma unroll
@@ -652,8 +698,8 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_experts_kernel(
                     if ((K & 64) && k0 + chunk * 128 + 64 == K) {
                         const uint8_t *w = static_cast<const uint8_t *>(it.second ? p.W2 : p.W13);
                         const int e = it.pass < 0 ? p.E : meta->pass_e[it.pass];
-                        const size_t r = it.second ? (size_t)e * p.d + it.tile * 16 + g
-                                                   : (size_t)e * 2 * p.I + it.tile * 8 + g;
+                        const size_t r = it.second ? (size_t)e * p.d + it.tile * 16 + pr
+                                                   : (size_t)e * 2 * p.I + it.tile * 8 + pr;
                         w += r * K + K - 64 + c * 16;
                         wq[0][0] = __ldg(reinterpret_cast<const uint4 *>(w));
                         wq[0][1] = __ldg(reinterpret_cast<const uint4 *>(
@@ -737,7 +783,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_experts_kernel(
     } else {
         // ------------------------------------------- sums over the warps
         const int buf = warp - kSumWarp0;
-        const int g = lane >> 2, c = lane & 3;
+        const int g = few_row(lane >> 2), c = lane & 3;
         for (uint32_t n = 0;; ++n) {
             if (!mbar_wait_warp(&rfull[buf], n & 1u, wc)) break;
             const int t = rinfo[2 * buf], grp = rinfo[2 * buf + 1];
@@ -809,7 +855,7 @@ struct FewWorkspace {
     int n_counters;
     float *part;
     int32_t *ids;
-    float *w, *ssel;
+    float *w;
     uint16_t *h;
     float *yp;
     size_t bytes;
@@ -829,7 +875,6 @@ FewWorkspace carve_few(uint8_t *base, int T, int d, int E, int k, int I) {
     w.part = reinterpret_cast<float *>(take((size_t)kGateSplits * T * E * 4));
     w.ids = reinterpret_cast<int32_t *>(take(S * 4));
     w.w = reinterpret_cast<float *>(take(S * 4));
-    w.ssel = reinterpret_cast<float *>(take(S * 4));
     w.h = reinterpret_cast<uint16_t *>(take((S + T) * I * 2));
     w.yp = reinterpret_cast<float *>(take((S + T) * d * 4));
     w.bytes = off;
@@ -927,7 +972,6 @@ moe_status launch_few(const moe_few_args *a, cudaStream_t st) {
     p.part = w.part;
     p.ids = w.ids;
     p.w = w.w;
-    p.ssel = w.ssel;
     p.h = w.h;
     p.yp = w.yp;
     p.status = device_status_ptr();

@@ -19,12 +19,45 @@
 //      rate here, and a warp pays for every fp64 sequence any lane needs.
 // Ties go to the lower expert id.  Weights: w_j = scaling * s_j / sum_i s_i
 // with the sum and quotient in fp64, rounded to fp32.
-#include "route_common.cuh"
+#include <cfloat>
+#include <climits>
+
+#include "moe_ptx.cuh"
 
 namespace moe {
 namespace {
 
 constexpr int kRouteWarps = 8;
+
+// Warp argmax of (key, id): larger key wins, equal keys go to the lower id.
+__device__ __forceinline__ void warp_argmax(float &key, int &id) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        const float k2 = __shfl_xor_sync(0xffffffffu, key, o);
+        const int i2 = __shfl_xor_sync(0xffffffffu, id, o);
+        if (k2 > key || (k2 == key && i2 < id)) {
+            key = k2;
+            id = i2;
+        }
+    }
+}
+
+__device__ __forceinline__ float sigmoid_exact(float z) {
+    return (float)(1.0 / (1.0 + exp(-(double)z)));
+}
+
+// Fills slot j = lane (< k) of token t from the selected id and its score.
+__device__ __forceinline__ void write_weights(int t, int k, int lane, int my_id, float my_s,
+                                             float scaling, int32_t *ids, float *w, float *ssel) {
+    double S = 0.0;
+    for (int j = 0; j < k; ++j) S += (double)__shfl_sync(0xffffffffu, my_s, j);
+    if (lane < k) {
+        const size_t o = (size_t)t * k + lane;
+        ids[o] = my_id;
+        ssel[o] = my_s;
+        w[o] = S > 0.0 ? (float)((double)scaling * (double)my_s / S) : 0.0f;
+    }
+}
 
 template <int EPL>
 __global__ void __launch_bounds__(kRouteWarps * 32) route_topk_kernel(
@@ -42,16 +75,138 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_topk_kernel(
     for (int t = gw; t < T; t += nw) {
         const float *zt = z + (size_t)t * E;
         const float *bt = bias + ((is_vision && is_vision[t]) ? E : 0);
-        float zv[EPL], bv[EPL];
+        float zv[EPL], key[EPL], bv[EPL];
 #pragma unroll
         for (int i = 0; i < EPL; ++i) {
             const int e = lane + 32 * i;
-            zv[i] = e < E ? zt[e] : 0.0f;
-            bv[i] = e < E ? bt[e] : 0.0f;
+            if (e < E) {
+                zv[i] = zt[e];
+                bv[i] = bt[e];
+                const float s = 1.0f / (1.0f + expf(-zv[i]));
+                const float kk = s + bv[i];
+                key[i] = (kk == kk) ? kk : -FLT_MAX;  // NaN ranks last
+            } else {
+                zv[i] = 0.0f;
+                bv[i] = 0.0f;
+                key[i] = -INFINITY;
+            }
         }
-        int my_id;
-        float my_s;
-        route_topk_token<EPL>(zv, bv, lane, E, k, lst_e, lst_z, lst_b, my_id, my_s);
+        // pass 1: approximate k-th key
+        uint32_t taken = 0;
+        float kth = INFINITY;
+        for (int j = 0; j < k; ++j) {
+            float bk = -INFINITY;
+            int be = INT_MAX;
+#pragma unroll
+            for (int i = 0; i < EPL; ++i) {
+                const int e = lane + 32 * i;
+                if (e < E && !(taken >> i & 1u) && (key[i] > bk || (key[i] == bk && e < be))) {
+                    bk = key[i];
+                    be = e;
+                }
+            }
+            warp_argmax(bk, be);
+            if (be != INT_MAX && (be & 31) == lane) taken |= 1u << (be >> 5);
+            kth = bk;
+        }
+        // error bound of the approximate key: expf, 1+e and the division add a
+        // few ulp of the score; the two key additions half an ulp of the key each
+        const float tol = 4e-6f * fmaxf(1.0f, fabsf(kth));
+        const float thr = kth - 2.0f * tol;
+        // pass 2: exact keys inside the window, then the exact top-k.  The
+        // window's experts are first packed one per lane, so that the warp
+        // evaluates the fp64 sigmoid once for all of them.
+        bool cand[EPL];
+        int ncand = 0;
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) {
+            const int e = lane + 32 * i;
+            cand[i] = e < E && key[i] >= thr;
+            ncand += __popc(__ballot_sync(0xffffffffu, cand[i]));
+        }
+        int my_id = 0;
+        float my_s = 0.0f;
+        if (ncand <= 32) {
+            int base = 0;
+#pragma unroll
+            for (int i = 0; i < EPL; ++i) {
+                const unsigned m = __ballot_sync(0xffffffffu, cand[i]);
+                if (cand[i]) {
+                    const int pos = base + __popc(m & ((1u << lane) - 1u));
+                    lst_e[pos] = lane + 32 * i;
+                    lst_z[pos] = zv[i];
+                    lst_b[pos] = bv[i];
+                }
+                base += __popc(m);
+            }
+            __syncwarp();
+            int ce = INT_MAX;
+            float cs = 0.0f, ck = -INFINITY;
+            if (lane < ncand) {
+                ce = lst_e[lane];
+                cs = sigmoid_exact(lst_z[lane]);
+                const float kk = __fadd_rn(cs, lst_b[lane]);
+                ck = (kk == kk) ? kk : -FLT_MAX;
+            }
+            __syncwarp();
+            for (int j = 0; j < k; ++j) {
+                float bk = ck;
+                int be = ce;
+                warp_argmax(bk, be);
+                const unsigned owner = __ballot_sync(0xffffffffu, ce == be && be != INT_MAX);
+                const int ol = owner ? __ffs(owner) - 1 : 0;
+                const float sv = __shfl_sync(0xffffffffu, cs, ol);
+                if (lane == ol) {
+                    ck = -INFINITY;
+                    ce = INT_MAX;
+                }
+                if (lane == j) {
+                    my_id = be == INT_MAX ? 0 : be;
+                    my_s = sv;
+                }
+            }
+        } else {
+            // many exact ties in the window: every lane evaluates its own experts
+            float ek[EPL], es[EPL];
+#pragma unroll
+            for (int i = 0; i < EPL; ++i) {
+                es[i] = 0.0f;
+                ek[i] = -INFINITY;
+                if (cand[i]) {
+                    es[i] = sigmoid_exact(zv[i]);
+                    const float kk = __fadd_rn(es[i], bv[i]);
+                    ek[i] = (kk == kk) ? kk : -FLT_MAX;
+                }
+            }
+            taken = 0;
+            for (int j = 0; j < k; ++j) {
+                float bk = -INFINITY;
+                int be = INT_MAX;
+#pragma unroll
+                for (int i = 0; i < EPL; ++i) {
+                    const int e = lane + 32 * i;
+                    if (e < E && !(taken >> i & 1u) && (ek[i] > bk || (ek[i] == bk && e < be))) {
+                        bk = ek[i];
+                        be = e;
+                    }
+                }
+                warp_argmax(bk, be);
+                float sv = 0.0f;
+                if (be != INT_MAX && (be & 31) == lane) {
+                    const int i = be >> 5;
+                    taken |= 1u << i;
+#pragma unroll
+                    for (int ii = 0; ii < EPL; ++ii)
+                        if (ii == i) sv = es[ii];
+                }
+                const int owner = be == INT_MAX ? 0 : (be & 31);
+                sv = __shfl_sync(0xffffffffu, sv, owner);
+                if (lane == j) {
+                    my_id = be == INT_MAX ? 0 : be;
+                    my_s = sv;
+                }
+            }
+        }
         write_weights(t, k, lane, my_id, my_s, scaling, ids, w, ssel);
     }
 }
