@@ -12,10 +12,10 @@
 // Bound: the weights of the experts that the tokens hit cross HBM once (a few
 // rows reuse each of them), so everything else has to hide behind that stream.
 // The second kernel therefore keeps it running from its first cycle to its
-// last: one warp plans (takes items, lists the hit experts), one copies weight
-// rows into a ring in shared memory (two TMA boxes a stage) far ahead of the 16
-// warps that multiply, across the boundaries of the phases, whose dependences
-// only the multiplying warps wait for; four more warps add up the partial sums,
+// last: one warp takes items, lists the hit experts and copies weight rows into
+// a ring in shared memory (two TMA boxes a stage) far ahead of the 16 warps that
+// multiply, across the boundaries of the phases, whose dependences
+// only the multiplying warps wait for; three more warps add up the partial sums,
 // apply the SwiGLU or the routing weight and signal, so that no multiplying
 // warp waits for a store or an atomic.  The work comes as items of 16 weight rows in one order for the whole
 // grid, handed out by a counter:
@@ -26,13 +26,15 @@
 // so the kernel needs no particular number of resident CTAs.
 //
 // Items: 8 gate rows and the matching 8 up rows of W13 (both land in the same
-// thread, which applies the SwiGLU), or 16 rows of W2.  Two groups of eight
-// warps take items in turn and split the contraction, each with mma.m16n8k16 (weights x 8 tokens, bf16, fp32 sums; at
+// thread, which applies the SwiGLU), or 16 rows of W2.  Four groups of four
+// warps take the stages in turn and so split the contraction, each with mma.m16n8k16 (weights x 8 tokens, bf16, fp32 sums; at
 // a few rows a weight the matrix pipe is nearly idle, so the 128-row tiles of
 // tcgen05 would only add padding); their partial sums meet in shared memory in
-// a fixed order.  FP8 weights are expanded to bf16 in registers, exactly, and
-// each 128-block's sum takes its scale in fp32.  h is rounded to bf16 (the
-// second matmul's operand), every other sum stays fp32 up to y.  Products of
+// a fixed order.  FP8 weights are expanded to f16 in registers, exactly, and
+// each 128-block's sum takes its scale in fp32; the tokens are then f16 as well,
+// each scaled by a power of two (a few CTAs of the first kernel).  h is rounded
+// to 16 bits (the second matmul's operand: bf16, or with FP8 weights f16), every
+// other sum stays fp32 up to y.  Products of
 // the second matmul go to fp32 rows per (token, slot); the last item of a
 // column group to finish adds them up in slot order, so results do not depend
 // on who finishes when.
@@ -48,21 +50,18 @@ constexpr int kFewT = 32;              // tokens at most
 constexpr int kFewK = 8;               // experts per token at most
 constexpr int kFewS = kFewT * kFewK;
 constexpr int kFewE = 1024;
-constexpr int kGateWarps = 8;
+constexpr int kGateWarps = 16;
 constexpr int kGateSplits = 16;        // at most
 constexpr int kMulWarps = 16;
-constexpr int kGroups = 2;             // of multiplying warps; they take items in turn
+constexpr int kGroups = 4;             // of multiplying warps; they take stages in turn
 constexpr int kGroupWarps = kMulWarps / kGroups;
-constexpr int kSumWarps = 4;           // each with a buffer of partial sums of its own
-constexpr int kGroupSums = kSumWarps / kGroups;
-constexpr int kCopyWarp = kMulWarps, kPlanWarp = kMulWarps + 1, kSumWarp0 = kMulWarps + 2;
+constexpr int kSumWarps = 3;           // each with a buffer of partial sums of its own
+constexpr int kCopyWarp = kMulWarps, kSumWarp0 = kMulWarps + 1;
 constexpr int kFewThreads = 32 * (kSumWarp0 + kSumWarps);
-constexpr int kPlanSlots = 4;          // items between the planning and the copying warp
 constexpr int kChunk = 128;            // weight bytes of a row that a warp takes at a time
-constexpr int kWarpChunks = 2;         // chunks of a stage for one warp
-constexpr int kStageChunks = kGroupWarps * kWarpChunks;
-constexpr int kRowBytes = kStageChunks * kChunk;   // weight bytes of a row in a stage
-constexpr int kFewStage = 16 * kRowBytes;       // two boxes of 8 rows
+constexpr int kStageChunks = 16;       // chunks of a row in a stage, at most
+constexpr int kWarpChunks = kStageChunks / kGroupWarps;
+constexpr int kFewStage = 16 * kStageChunks * kChunk;   // two boxes of 8 rows
 constexpr int kW2Tiles = 2;            // tiles of 16 rows in an item of W2
 
 struct FewParams {
@@ -79,15 +78,19 @@ struct FewParams {
     int32_t *ids_out;                  // or null
     float *w_out;                      // or null
     // workspace
-    int *counters;   // [0] gate, [1] ticket, [2] exits, [4] shared h tiles, [5 + p] those of pass p,
+    int *counters;   // [0] gate, [1] ticket, [2] exits, [3] f16 tokens, [4] shared h tiles, [5 + p] those of pass p,
                      // then columns' finished items; zero between calls
     int n_counters;
     float *part;     // [splits, T, E] partial logits
+    uint16_t *x16;   // FP8 weights: [T, d] f16 tokens, each scaled by a power of two ...
+    float *x16_s;    // ... whose inverse this is [T]
+    int h_exp;       // FP8 weights: h is f16, times 2^h_exp
     int32_t *ids;    // [T, k]
     float *w;        // [T, k]
-    uint16_t *h;     // [S + T, I]
+    uint16_t *h;     // [S + T, I] bf16, or f16 (FP8 weights)
     float *yp;       // [S + T, d]
     int splits;
+    int cps13, cps2;   // chunks of a row in a stage
     int *status;
     long long wait_limit;
 };
@@ -96,6 +99,15 @@ __device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1
                                          uint32_t a3, uint32_t b0, uint32_t b1) {
     asm volatile(
         "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                        uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
         "{%8,%9}, {%0,%1,%2,%3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
@@ -146,9 +158,57 @@ __device__ __forceinline__ void warp_best(float &key, int &id) {
 
 __device__ __forceinline__ float sigmoid_f32(float z) { return 1.0f / (1.0f + expf(-z)); }
 
+// Token t in f16 (for FP8 weights): times the power of two that brings its
+// largest magnitude to [2^14, 2^15), so that bf16's eight bits survive down to
+// 2^-28 of that magnitude and lose at most 2^-40 of it below.  One CTA.
+__device__ void few_token_f16(const FewParams &p, int t, uint32_t *warp_top) {
+    const uint4 *src = reinterpret_cast<const uint4 *>(p.x + (size_t)t * p.d);
+    uint32_t m = 0;
+    for (int i = threadIdx.x; i < p.d / 8; i += blockDim.x) {
+        const uint4 v = __ldg(src + i);
+        m = __vmaxu2(m, v.x & 0x7FFF7FFFu);
+        m = __vmaxu2(m, v.y & 0x7FFF7FFFu);
+        m = __vmaxu2(m, v.z & 0x7FFF7FFFu);
+        m = __vmaxu2(m, v.w & 0x7FFF7FFFu);
+    }
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, o));
+    if ((threadIdx.x & 31) == 0) warp_top[threadIdx.x >> 5] = m;
+    __syncthreads();
+    for (int w = 0; w < kGateWarps; ++w) m = __vmaxu2(m, warp_top[w]);
+    __syncthreads();
+    const uint32_t top = max(m & 0xFFFFu, m >> 16);
+    // exponent of the largest; an infinity or NaN among the values stays one
+    // under any scale
+    const int e = top >= 0x7F80u ? 0 : max((int)(top >> 7) - 127, -86);
+    const float f = __uint_as_float((uint32_t)(127 + 14 - e) << 23);
+    uint4 *dst = reinterpret_cast<uint4 *>(p.x16 + (size_t)t * p.d);
+    for (int i = threadIdx.x; i < p.d / 8; i += blockDim.x) {
+        const uint4 v = __ldg(src + i);
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        uint32_t r[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const __half2 h = __floats2half2_rn(bf16_lo(w[j]) * f, bf16_hi(w[j]) * f);
+            r[j] = *reinterpret_cast<const uint32_t *>(&h);
+        }
+        dst[i] = make_uint4(r[0], r[1], r[2], r[3]);
+    }
+    if (threadIdx.x == 0) p.x16_s[t] = __uint_as_float((uint32_t)(127 - 14 + e) << 23);
+    __syncthreads();
+    if (threadIdx.x == 0) red_release_gpu_add(p.counters + 3, 1);
+}
+
 template <int EPL>
 __global__ void __launch_bounds__(kGateWarps * 32) few_gate_kernel(const __grid_constant__ FewParams p) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if ((int)blockIdx.y >= p.splits) {
+        __shared__ uint32_t warp_top[kGateWarps];
+        const int n = (gridDim.y - p.splits) * gridDim.x;
+        for (int t = (blockIdx.y - p.splits) * gridDim.x + blockIdx.x; t < p.T; t += n)
+            few_token_f16(p, t, warp_top);
+        return;
+    }
     __shared__ float red[kGateWarps][4][32];
     __shared__ int s_last;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -185,7 +245,7 @@ __global__ void __launch_bounds__(kGateWarps * 32) few_gate_kernel(const __grid_
         __syncthreads();
     }
     if (threadIdx.x == 0)
-        s_last = atom_add_acq_rel(p.counters, 1) == (int)(gridDim.x * gridDim.y) - 1;
+        s_last = atom_add_acq_rel(p.counters, 1) == (int)gridDim.x * p.splits - 1;
     __syncthreads();
     if (!s_last) return;
     __threadfence();
@@ -220,14 +280,23 @@ __global__ void __launch_bounds__(kGateWarps * 32) few_gate_kernel(const __grid_
                 zv[i] = e < p.E && p.logit_offset ? p.logit_offset[e] : 0.0f;
                 key[i] = e < p.E ? bt[e] : 0.0f;
             }
-            // all experts' loads of a split together (their latency, not their
-            // bytes, is what counts here)
-#pragma unroll 2
-            for (int s = 0; s < p.splits; ++s) {
-                const float *z = p.part + ((size_t)s * p.T + t) * p.E;
+            // many loads together: their latency, not their bytes, counts here
+            constexpr int U = EPL <= 4 ? 8 : EPL <= 12 ? 4 : 1;
+            for (int s0 = 0; s0 < p.splits; s0 += U) {
+                float z[U][EPL];
 #pragma unroll
-                for (int i = 0; i < EPL; ++i)
-                    if (lane + 32 * i < p.E) zv[i] += __ldcg(z + lane + 32 * i);
+                for (int u = 0; u < U; ++u)
+#pragma unroll
+                    for (int i = 0; i < EPL; ++i) {
+                        const int e = lane + 32 * i;
+                        z[u][i] = e < p.E && s0 + u < p.splits
+                                      ? __ldcg(p.part + ((size_t)(s0 + u) * p.T + t) * p.E + e)
+                                      : 0.0f;
+                    }
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+#pragma unroll
+                    for (int i = 0; i < EPL; ++i) zv[i] += z[u][i];
             }
 #pragma unroll
             for (int i = 0; i < EPL; ++i) {
@@ -297,13 +366,12 @@ struct FewItem {
 template <bool FP8, int NT>
 struct FewShape {
     static constexpr int STAGES = 6;
-    static constexpr int RED = kSumWarps * kGroupWarps * 128 * 4;
+    static constexpr int RED = kSumWarps * kMulWarps * 128 * 4;
     static constexpr int SCALES = FP8 ? STAGES * 2 * kStageChunks * 4 : 0;
     static constexpr int SMEM =
         1024 + STAGES * kFewStage + RED + SCALES + (int)sizeof(FewMeta) + 512;
     static constexpr int ELT = FP8 ? 1 : 2;
-    static constexpr int STAGE_K = kRowBytes / ELT;   // contraction of a stage
-    static constexpr int STEP = FP8 ? 64 : 32;        // of a step (64 bytes of a row, half a chunk)
+    static constexpr int STEP = FP8 ? 64 : 32;   // contraction of a step (half a chunk)
 };
 
 // Tiles in order: shared W13, shared W2, routed W13, routed W2.  An item is one
@@ -323,26 +391,16 @@ __device__ __forceinline__ FewItem few_item(int t, int tiles1, int tiles2, int n
     return it;
 }
 
-// Four E4M3 codes -> bf16 pairs (codes 0, 2) and (1, 3), exact: sign and the
-// seven other bits move to their places in bf16, where they read as the value
-// times 2^-120 (the exponent biases differ by 120; subnormal codes become
-// subnormal bf16), and one multiplication puts that right.  Ten instructions
-// for four codes at the full rate; through the converter instruction (f16,
-// fp32, bf16) a stage took 0.55 us of the SM, more than its rows take to
-// arrive.  `top` collects the largest magnitude bits of either half: 0x7F0 is
-// the NaN code, which would otherwise read as 480.
-__device__ __forceinline__ void e4m3x4_bf16(uint32_t w, uint32_t &even, uint32_t &odd,
-                                            uint32_t &top) {
-    const uint32_t a = (w << 4) & 0x07F007F0u, b = (w >> 4) & 0x07F007F0u;
-    top = __vimax3_u16x2(top, a, b);
-    const uint32_t scale = 0x7B807B80u;   // 2^120 twice
-    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(even) : "r"(a | ((w << 8) & 0x80008000u)), "r"(scale));
-    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(odd) : "r"(b | (w & 0x80008000u)), "r"(scale));
+// Four E4M3 codes -> two f16 pairs, exact, a NaN code to a NaN: two conversion
+// instructions.  (To bf16 there is none: through fp32 it takes eight, and by
+// moving bits ten on the integer pipe, 0.75 us of the SM for the 32 KB of a
+// stage, as long as they take to arrive.)  So the token operand is f16 too.
+__device__ __forceinline__ void e4m3x4_f16(uint32_t w, uint32_t &lo, uint32_t &hi) {
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(lo) : "h"((uint16_t)(w & 0xFFFFu)));
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(hi) : "h"((uint16_t)(w >> 16)));
 }
 
-__device__ __forceinline__ bool e4m3_nan_seen(uint32_t top) {
-    return (top & 0xFFFFu) >= 0x7F0u || (top >> 16) >= 0x7F0u;
-}
+__device__ __forceinline__ float exp2i(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
 
 __device__ __forceinline__ void cp_async4(void *dst, const void *src) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src)
@@ -378,11 +436,9 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_experts_kernel(
     uint64_t *empty = ifull + SH::STAGES;
     uint64_t *rfull = empty + SH::STAGES;    // a buffer of `red` has every warp's partial sums
     uint64_t *rempty = rfull + kSumWarps;    // ... and has been read
-    uint64_t *qfull = rempty + kSumWarps;    // a planned item is in the queue
-    uint64_t *qempty = qfull + kPlanSlots;
-    volatile int *queue = reinterpret_cast<volatile int *>(qempty + kPlanSlots);   // first tile
-    volatile int *info = queue + kPlanSlots;                          // tile, k, group per stage
-    volatile int *rinfo = info + 3 * SH::STAGES;                     // tile, group per buffer
+    volatile int *info =
+        reinterpret_cast<volatile int *>(rempty + kSumWarps);   // per stage: tile, first chunk
+    volatile int *rinfo = info + 2 * SH::STAGES;    // per buffer: tile, group of 8 rows
     volatile int *abort_s = rinfo + 2 * kSumWarps;
     int *last_s = const_cast<int *>(abort_s) + 1;
 
@@ -391,15 +447,11 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_experts_kernel(
         for (int s = 0; s < SH::STAGES; ++s) {
             mbar_init(&full[s], FP8 ? 33 : 1);
             mbar_init(&ifull[s], 1);
-            mbar_init(&empty[s], kMulWarps);   // the other group's too: it has seen the stage
+            mbar_init(&empty[s], kMulWarps);   // the other groups' too: they have seen the stage
         }
         for (int b = 0; b < kSumWarps; ++b) {
-            mbar_init(&rfull[b], kGroupWarps);
+            mbar_init(&rfull[b], kMulWarps);
             mbar_init(&rempty[b], 1);
-        }
-        for (int b = 0; b < kPlanSlots; ++b) {
-            mbar_init(&qfull[b], 1);
-            mbar_init(&qempty[b], 1);
         }
         *abort_s = 0;
         fence_barrier_init();
@@ -411,17 +463,22 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_experts_kernel(
     int *h_done = p.counters + 4;
     int *y_done = h_done + 1 + kFewS;
 
-    if (warp == kPlanWarp) {
-        // ------------------------------------------------------------ plan
-        // Takes items from the grid's counter and passes them on; before the
+    if (warp == kCopyWarp) {
+        // ---------------------------------------------------- plan and copy
+        // Takes items from the grid's counter and copies their rows; before the
         // first routed item, waits for the routing and lists the hit experts.
         const int shared_items = tiles1 + tiles2 / kW2Tiles;
+        uint32_t s = 0, ph = 0;
+        int last[SH::STAGES];
+#pragma unroll
+        for (int i = 0; i < SH::STAGES; ++i) last[i] = -1;
+        const uint64_t policy = policy_evict_first();
+        bool ok = true;
         int n_pass = -1;
-        uint32_t n = 0;
-        int ticket = 0;
-        if (lane == 0) ticket = atomicAdd(p.counters + 1, 1);
-        while (true) {
-            int t = __shfl_sync(0xffffffffu, ticket, 0);
+        while (ok) {
+            int t = 0;
+            if (lane == 0) t = atomicAdd(p.counters + 1, 1);
+            t = __shfl_sync(0xffffffffu, t, 0);
             if (t >= shared_items && n_pass < 0) {
                 asm volatile("griddepcontrol.wait;" ::: "memory");
                 for (int e = lane; e < p.E; e += 32) meta->start[e] = 0;
@@ -480,42 +537,17 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_experts_kernel(
                 }
                 __syncwarp();
             }
-            // the next number comes while this item waits for its place
-            if (lane == 0) ticket = atomicAdd(p.counters + 1, 1);
             // item -> first tile
-            int tile;
-            if (t < tiles1) tile = t;
-            else if (t < shared_items) tile = tiles1 + (t - tiles1) * kW2Tiles;
+            int first;
+            if (t < tiles1) first = t;
+            else if (t < shared_items) first = tiles1 + (t - tiles1) * kW2Tiles;
             else {
                 t -= shared_items;
                 const int first2 = n_pass * tiles1;
-                tile = tiles1 + tiles2 + (t < first2 ? t : first2 + (t - first2) * kW2Tiles);
-                if (tile >= (n_pass + 1) * (tiles1 + tiles2)) tile = -1;
+                first = tiles1 + tiles2 + (t < first2 ? t : first2 + (t - first2) * kW2Tiles);
+                if (first >= (n_pass + 1) * (tiles1 + tiles2)) first = -1;
             }
-            const uint32_t b = n % kPlanSlots;
-            if (!mbar_wait_warp(&qempty[b], (n / kPlanSlots & 1u) ^ 1u, wc)) break;
-            if (lane == 0) {
-                queue[b] = tile;
-                mbar_arrive(&qfull[b]);
-            }
-            ++n;
-            if (tile < 0) break;
-        }
-    } else if (warp == kCopyWarp) {
-        // ------------------------------------------------------------ copy
-        uint32_t s = 0, ph = 0;
-        int last[SH::STAGES];
-#pragma unroll
-        for (int i = 0; i < SH::STAGES; ++i) last[i] = -1;
-        const uint64_t policy = policy_evict_first();
-        bool ok = true;
-        for (uint32_t n = 0; ok; ++n) {
-            const uint32_t b = n % kPlanSlots;
-            if (!mbar_wait_warp(&qfull[b], n / kPlanSlots & 1u, wc)) break;
-            const int t = queue[b];
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&qempty[b]);
-            if (t < 0) {
+            if (first < 0) {
                 if (!mbar_wait_warp(&empty[s], ph ^ 1u, wc)) break;
                 if (lane == 0) {
                     info[s] = -1;
@@ -523,11 +555,12 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_experts_kernel(
                 }
                 break;
             }
-            const FewItem it =
-                few_item(t, tiles1, tiles2, t < tiles1 + tiles2 ? 0 : meta->n_pass);
+            const FewItem it = few_item(first, tiles1, tiles2, max(n_pass, 0));
             const int e = it.pass < 0 ? p.E : meta->pass_e[it.pass];
             const int K = it.second ? p.I : p.d;
-            const int chunks = K * SH::ELT / kChunk;   // whole ones
+            const int whole = K * SH::ELT / kChunk;   // chunks
+            const int chunks = (K * SH::ELT + kChunk - 1) / kChunk;
+            const int cps = it.second ? p.cps2 : p.cps13;
             const CUtensorMap *tm = it.second ? &p.tm2 : &p.tm13;
             for (int sub = 0; ok && sub < (it.second ? kW2Tiles : 1); ++sub) {
                 // 8 gate rows and the matching 8 up rows, or 16 rows of W2
@@ -543,17 +576,15 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_experts_kernel(
                     sc = (it.second ? p.W2_s : p.W13_s) +
                          ((size_t)e * fp8_blocks(rows) + row / kFp8Block) * kb + my_kb;
                 }
-                for (int k0 = 0; k0 < K; k0 += SH::STAGE_K) {
+                for (int c0 = 0; c0 < chunks; c0 += cps) {
                     if (!mbar_wait_warp(&empty[s], ph ^ 1u, wc)) { ok = false; break; }
-                    const int c0 = k0 * SH::ELT / kChunk;
                     if (lane == 0) {
-                        info[s] = t + sub;
-                        info[SH::STAGES + s] = k0;
-                        info[2 * SH::STAGES + s] = (int)(n % kGroups);
+                        info[s] = first + sub;
+                        info[SH::STAGES + s] = c0;
                         mbar_arrive(&ifull[s]);
-                        if (c0 < chunks) {
+                        if (c0 < whole) {
                             uint8_t *dst = ring + s * kFewStage;
-                            mbar_arrive_expect_tx(&full[s], kFewStage);
+                            mbar_arrive_expect_tx(&full[s], 16 * kChunk * cps);
                             tma_load_3d(dst, tm, &full[s], 0, r0, c0, policy);
                             tma_load_3d(dst + kFewStage / 2, tm, &full[s], 0, r1, c0, policy);
                         } else {
@@ -561,7 +592,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_experts_kernel(
                         }
                     }
                     if constexpr (FP8) {
-                        if (c0 + my_kb < kb)
+                        if (my_kb < cps && c0 + my_kb < kb)
                             cp_async4(scales + s * 2 * kStageChunks + lane, sc + c0);
                         cp_async_arrive(&full[s]);
                     }
@@ -577,11 +608,13 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_experts_kernel(
         }
     } else if (warp < kMulWarps) {
         // -------------------------------------------------------- multiply
-        // Two groups of eight warps take items in turn, so that one's loads of
-        // token operands overlap the other's products.  The operands of a stage
+        // Four groups of four warps take stages in turn, so that one's loads of
+        // token operands overlap the others' products.  The operands of a stage
         // are loaded as soon as its item is known, while its weight rows may
         // still be on their way.
-        uint32_t s = 0, ph = 0, unit = 0;
+        uint32_t s = 0, ph = 0, unit = 0, n_stage = 0;
+        int item = -1;   // tile of `it`
+        bool have_x = false;
         const int group = warp / kGroupWarps, wl = warp % kGroupWarps;
         const int g = lane >> 2, c = lane & 3;
         const int pr = few_row(g);
@@ -592,40 +625,46 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_experts_kernel(
         constexpr int NV = FP8 ? 2 : 1;
         constexpr int STEPS = 2 * kWarpChunks;
         // steps whose token operands are loaded ahead (registers: the rest on use)
-        constexpr int PRE = FP8 && NT > 1 ? STEPS / 2 : STEPS;
+        constexpr int PRE = !FP8 ? STEPS : NT > 1 ? 2 : 4;
         while (true) {
             if (!mbar_wait_warp(&ifull[s], ph, wc)) break;
-            const int t = info[s], k0 = info[SH::STAGES + s];
+            const int t = info[s], c0 = info[SH::STAGES + s];
             if (t < 0) {
-                if (lane == 0) {   // tell this group's sum warps, one buffer each
-                    for (int b = 0; b < kGroupSums; ++b, ++unit) {
-                        const uint32_t buf = group * kGroupSums + unit % kGroupSums;
-                        if (!mbar_wait(&rempty[buf], (unit / kGroupSums & 1u) ^ 1u, wc)) break;
-                        if (wl == 0) rinfo[2 * buf] = -1;
+                if (lane == 0) {   // tell the sum warps, one buffer each
+                    for (int b = 0; b < kSumWarps; ++b, ++unit) {
+                        const uint32_t buf = unit % kSumWarps;
+                        if (!mbar_wait(&rempty[buf], (unit / kSumWarps & 1u) ^ 1u, wc)) break;
+                        if (warp == 0) rinfo[2 * buf] = -1;
                         mbar_arrive(&rfull[buf]);
                     }
                 }
                 break;
             }
-            if (info[2 * SH::STAGES + s] != group) {
-                // the other group's; both groups release every stage, so that
-                // neither can be a lap behind
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&empty[s]);
-                if (++s == SH::STAGES) { s = 0; ph ^= 1u; }
-                continue;
-            }
-            if (k0 == 0) {
+            if (c0 == 0) {
                 it = few_item(t, tiles1, tiles2, t < tiles1 + tiles2 ? 0 : meta->n_pass);
                 K = it.second ? p.I : p.d;
                 n_rows = it.pass < 0 ? p.T : meta->pass_n[it.pass];
                 row0 = it.pass < 0 ? 0 : meta->pass_row[it.pass];
-                if (it.second) {
+#pragma unroll
+                for (int j = 0; j < NT; ++j)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) acc[j][i] = 0.0f;
+            }
+            const int nt = (n_rows + 7) >> 3;
+            const int chunks = (K * SH::ELT + kChunk - 1) / kChunk;
+            const int cps = it.second ? p.cps2 : p.cps13;
+            if (n_stage++ % kGroups == (uint32_t)group) {
+            if (item != t) {
+                item = t;
+                if (it.second || (FP8 && !have_x)) {
                     // the h rows of this pass: one signal per column tile and
-                    // group of 8 rows
+                    // group of 8 rows; or the tokens in f16, from the first kernel
                     bool ready = true;
                     if (lane == 0)
-                        ready = wait_count_geq(h_done + 1 + it.pass, tiles1 * ((n_rows + 7) / 8), wc);
+                        ready = it.second ? wait_count_geq(h_done + 1 + it.pass,
+                                                           tiles1 * ((n_rows + 7) / 8), wc)
+                                          : wait_count_geq(p.counters + 3, p.T, wc);
+                    have_x = have_x || !it.second;
                     ready = __shfl_sync(0xffffffffu, ready, 0);
                     __syncwarp();   // orders the h loads of every lane behind the acquire
                     if (!ready) break;
@@ -637,25 +676,25 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_experts_kernel(
                     if (i < n_rows) {
                         const int slot = it.pass < 0 ? S + i : meta->slot[row0 + i];
                         act[j] = it.second ? p.h + (size_t)slot * p.I
-                                           : p.x + (size_t)(it.pass < 0 ? i : slot / p.k) * p.d;
+                                           : (FP8 ? p.x16 : p.x) +
+                                                 (size_t)(it.pass < 0 ? i : slot / p.k) * p.d;
                     }
-#pragma unroll
-                    for (int i4 = 0; i4 < 4; ++i4) acc[j][i4] = 0.0f;
                 }
             }
-            const int nt = (n_rows + 7) >> 3;
-            // steps of this warp in this stage: the first `steps` of STEPS
-            const int steps = min(SH::STAGE_K, K - k0) / SH::STEP - wl * STEPS;
-            const int kk = k0 + wl * STEPS * SH::STEP + c * (SH::STEP / 4);
-            // token operand of step u, group j; FP8: pairs (0, 2) and (1, 3) of
-            // each four, as the codes are expanded
+            // this warp's chunks of the stage: wl, wl + 4, ...
+            const int n_c = min(cps, chunks - c0);
+            // token operand of half u % 2 of the warp's chunk u / 2, group j (x
+            // through L1; what is written while this kernel runs, from L2)
             auto load_act = [&](int u, int j, uint4 (&v)[NV]) {
+                const int cl = wl + kGroupWarps * (u / 2);
+                const int kk = (2 * (c0 + cl) + u % 2) * SH::STEP + c * (SH::STEP / 4);
 #pragma unroll
                 for (int i = 0; i < NV; ++i) {
                     v[i] = make_uint4(0, 0, 0, 0);
-                    if (act[j] && u < steps)
-                        v[i] = __ldcg(
-                            reinterpret_cast<const uint4 *>(act[j] + kk + u * SH::STEP + 8 * i));
+                    if (act[j] && cl < n_c && kk < K) {
+                        const uint4 *a = reinterpret_cast<const uint4 *>(act[j] + kk) + i;
+                        v[i] = FP8 || it.second ? __ldcg(a) : __ldg(a);
+                    }
                 }
             };
             uint4 v0[PRE][NV];
@@ -664,8 +703,8 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_experts_kernel(
             if (!mbar_wait_warp(&full[s], ph, wc)) break;
 #pragma unroll
             for (int ch = 0; ch < kWarpChunks; ++ch) {
-                if (2 * ch >= steps) break;
-                const int chunk = wl * kWarpChunks + ch;
+                const int chunk = wl + kGroupWarps * ch;
+                if (chunk >= n_c) break;
                 // rows pr and pr + 8 of the chunk, 128 bytes each, 16-byte pieces
                 // exchanged by row (128-byte swizzle)
                 uint4 wq[2][2];   // [half][row pr / pr + 8]
@@ -695,7 +734,8 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_experts_kernel(
                 } else {
                     // a contraction that ends inside a chunk: its last 64 codes
                     // are not in the stage (a copied row would run into the next)
-                    if ((K & 64) && k0 + chunk * 128 + 64 == K) {
+                    const bool tail = (K & 64) && (c0 + chunk) * 128 + 64 == K;
+                    if (tail) {
                         const uint8_t *w = static_cast<const uint8_t *>(it.second ? p.W2 : p.W13);
                         const int e = it.pass < 0 ? p.E : meta->pass_e[it.pass];
                         const size_t r = it.second ? (size_t)e * p.d + it.tile * 16 + pr
@@ -710,17 +750,16 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_experts_kernel(
                     for (int j = 0; j < NT; ++j)
 #pragma unroll
                         for (int i = 0; i < 4; ++i) part[j][i] = 0.0f;
-                    uint32_t top0 = 0, top1 = 0;
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        if (2 * ch + h >= steps) break;
+                        if (h == 1 && tail) break;
                         const uint32_t qa[4] = {wq[h][0].x, wq[h][0].y, wq[h][0].z, wq[h][0].w};
                         const uint32_t qb[4] = {wq[h][1].x, wq[h][1].y, wq[h][1].z, wq[h][1].w};
                         uint32_t x0[4], x1[4], y0[4], y1[4];
 #pragma unroll
                         for (int m = 0; m < 4; ++m) {
-                            e4m3x4_bf16(qa[m], x0[m], x1[m], top0);
-                            e4m3x4_bf16(qb[m], y0[m], y1[m], top1);
+                            e4m3x4_f16(qa[m], x0[m], x1[m]);
+                            e4m3x4_f16(qb[m], y0[m], y1[m]);
                         }
 #pragma unroll
                         for (int j = 0; j < NT; ++j) {
@@ -734,19 +773,12 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_experts_kernel(
                                                     b[NV - 1].w};
 #pragma unroll
                             for (int m = 0; m < 4; ++m)
-                                mma_bf16(part[j], x0[m], y0[m], x1[m], y1[m],
-                                         __byte_perm(bv[2 * m], bv[2 * m + 1], 0x5410),
-                                         __byte_perm(bv[2 * m], bv[2 * m + 1], 0x7632));
+                                mma_f16(part[j], x0[m], y0[m], x1[m], y1[m], bv[2 * m],
+                                        bv[2 * m + 1]);
                         }
                     }
-                    // a NaN code in a row of the block: NaN for every token
-                    float f0 = scales[s * 2 * kStageChunks + chunk];
-                    float f1 = scales[(s * 2 + 1) * kStageChunks + chunk];
-                    const unsigned quad = 0xFu << (lane & 28);
-                    if (__ballot_sync(0xffffffffu, e4m3_nan_seen(top0)) & quad)
-                        f0 = __int_as_float(0x7FFFFFFF);
-                    if (__ballot_sync(0xffffffffu, e4m3_nan_seen(top1)) & quad)
-                        f1 = __int_as_float(0x7FFFFFFF);
+                    const float f0 = scales[s * 2 * kStageChunks + chunk];
+                    const float f1 = scales[(s * 2 + 1) * kStageChunks + chunk];
 #pragma unroll
                     for (int j = 0; j < NT; ++j) {
                         acc[j][0] = fmaf(part[j][0], f0, acc[j][0]);
@@ -756,21 +788,24 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_experts_kernel(
                     }
                 }
             }
+            }
+            // every group releases every stage, so that none can be a lap behind
             __syncwarp();
             if (lane == 0) mbar_arrive(&empty[s]);
             if (++s == SH::STAGES) { s = 0; ph ^= 1u; }
-            if (k0 + SH::STAGE_K < K) continue;
-            // the item's partial sums, one buffer per group of 8 rows
+            if (c0 + cps < chunks) continue;
+            // the tile's partial sums, one buffer per group of 8 rows (zeros from
+            // a warp that had no stage of it)
             bool ok = true;
 #pragma unroll
             for (int j = 0; j < NT; ++j) {
                 if (j >= nt) break;
-                const uint32_t buf = group * kGroupSums + unit % kGroupSums;
-                ok = mbar_wait_warp(&rempty[buf], (unit / kGroupSums & 1u) ^ 1u, wc);
+                const uint32_t buf = unit % kSumWarps;
+                ok = mbar_wait_warp(&rempty[buf], (unit / kSumWarps & 1u) ^ 1u, wc);
                 if (!ok) break;
-                red[(buf * kGroupWarps + wl) * 32 + lane] =
+                red[(buf * kMulWarps + warp) * 32 + lane] =
                     make_float4(acc[j][0], acc[j][1], acc[j][2], acc[j][3]);
-                if (wl == 0 && lane == 0) {
+                if (warp == 0 && lane == 0) {
                     rinfo[2 * buf] = t;
                     rinfo[2 * buf + 1] = j;
                 }
@@ -790,8 +825,8 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_experts_kernel(
             if (t < 0) break;
             float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-            for (int w = 0; w < kGroupWarps; ++w) {
-                const float4 r = red[(buf * kGroupWarps + w) * 32 + lane];
+            for (int w = 0; w < kMulWarps; ++w) {
+                const float4 r = red[(buf * kMulWarps + w) * 32 + lane];
                 v[0] += r.x;
                 v[1] += r.y;
                 v[2] += r.z;
@@ -809,14 +844,18 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_experts_kernel(
                 if (r >= n_rows) continue;
                 const int slot = it.pass < 0 ? S + r : meta->slot[row0 + r];
                 if (it.second) {
-                    const float w = it.pass < 0 ? 1.0f : __ldcg(p.w + slot);
+                    const float w = (it.pass < 0 ? 1.0f : __ldcg(p.w + slot)) *
+                                    (FP8 ? exp2i(-p.h_exp) : 1.0f);
                     float *o = p.yp + (size_t)slot * p.d + it.tile * 16 + g;
                     o[0] = w * v[i];
                     o[8] = w * v[2 + i];
                 } else {
-                    const float h = swiglu_clamped_nan(v[i], v[2 + i], p.clamp);
+                    float up = 1.0f;
+                    if constexpr (FP8) up = __ldcg(p.x16_s + (it.pass < 0 ? r : slot / p.k));
+                    const float h = swiglu_clamped_nan(v[i] * up, v[2 + i] * up, p.clamp);
                     p.h[(size_t)slot * p.I + it.tile * 8 + g] =
-                        (uint16_t)(pack_bf16x2(h, 0.0f) & 0xFFFFu);
+                        FP8 ? __half_as_ushort(__float2half_rn(h * exp2i(p.h_exp)))
+                            : (uint16_t)(pack_bf16x2(h, 0.0f) & 0xFFFFu);
                 }
             }
             __syncwarp();
@@ -854,6 +893,8 @@ struct FewWorkspace {
     int *counters;
     int n_counters;
     float *part;
+    uint16_t *x16;
+    float *x16_s;
     int32_t *ids;
     float *w;
     uint16_t *h;
@@ -873,6 +914,8 @@ FewWorkspace carve_few(uint8_t *base, int T, int d, int E, int k, int I) {
     w.n_counters = 4 + 1 + kFewS + d / 16;
     w.counters = reinterpret_cast<int *>(take((size_t)w.n_counters * 4));
     w.part = reinterpret_cast<float *>(take((size_t)kGateSplits * T * E * 4));
+    w.x16 = reinterpret_cast<uint16_t *>(take((size_t)T * d * 2));
+    w.x16_s = reinterpret_cast<float *>(take((size_t)T * 4));
     w.ids = reinterpret_cast<int32_t *>(take(S * 4));
     w.w = reinterpret_cast<float *>(take(S * 4));
     w.h = reinterpret_cast<uint16_t *>(take((S + T) * I * 2));
@@ -923,11 +966,15 @@ moe_status launch_experts_nt(const FewParams &p, cudaStream_t st) {
 
 // Rows of `row_bytes` bytes as [row_bytes / 128][rows][128]: a box of 16 x 8 x
 // 128 is 16 whole chunks of eight rows, eight rows of a chunk side by side.
-static bool encode_rows_of_chunks(CUtensorMap *tm, const void *base, uint64_t rows, int row_bytes) {
+// `cps`: chunks of a row in a stage -- the fewest stages, evenly filled.
+static bool encode_rows_of_chunks(CUtensorMap *tm, const void *base, uint64_t rows, int row_bytes,
+                                  int *cps) {
+    const int all = (row_bytes + kChunk - 1) / kChunk;
+    const int stages = (all + kStageChunks - 1) / kStageChunks;
+    *cps = (all + stages - 1) / stages;
     const int chunks = row_bytes / kChunk;
     return encode_tmap_u8_3d_sw128(tm, base, chunks > 0 ? kChunk : row_bytes, rows,
-                                   chunks > 0 ? chunks : 1, row_bytes, kChunk, kChunk, 8,
-                                   kRowBytes / kChunk);
+                                   chunks > 0 ? chunks : 1, row_bytes, kChunk, kChunk, 8, *cps);
 }
 
 bool few_supported(int T, int d, int E, int k, int I) {
@@ -970,6 +1017,8 @@ moe_status launch_few(const moe_few_args *a, cudaStream_t st) {
     p.counters = w.counters;
     p.n_counters = w.n_counters;
     p.part = w.part;
+    p.x16 = w.x16;
+    p.x16_s = w.x16_s;
     p.ids = w.ids;
     p.w = w.w;
     p.h = w.h;
@@ -978,15 +1027,19 @@ moe_status launch_few(const moe_few_args *a, cudaStream_t st) {
     if (!p.status) return MOE_ERR_CUDA;
     p.wait_limit = kWaitLimitCycles;
     const int elt = fp8 ? 1 : 2;
-    if (!encode_rows_of_chunks(&p.tm13, p.W13, (uint64_t)(p.E + 1) * 2 * p.I, p.d * elt) ||
-        !encode_rows_of_chunks(&p.tm2, p.W2, (uint64_t)(p.E + 1) * p.d, p.I * elt))
+    if (!encode_rows_of_chunks(&p.tm13, p.W13, (uint64_t)(p.E + 1) * 2 * p.I, p.d * elt,
+                               &p.cps13) ||
+        !encode_rows_of_chunks(&p.tm2, p.W2, (uint64_t)(p.E + 1) * p.d, p.I * elt, &p.cps2))
         return MOE_ERR_CUDA;
     const int et = (p.E + 15) / 16;
-    int splits = num_sms() / et;
+    int splits = (num_sms() + et - 1) / et;   // every SM has a part
     splits = splits < 1 ? 1 : splits > kGateSplits ? kGateSplits : splits;
     if (splits > p.d / 32) splits = p.d / 32;
     p.splits = splits;
-    const dim3 grid(et, splits);
+    // |h| <= clamp^2: the power of two that keeps it inside f16
+    p.h_exp = 0;
+    while (p.h_exp < 24 && p.clamp * p.clamp * (float)(2 << p.h_exp) <= 65504.0f) ++p.h_exp;
+    const dim3 grid(et, splits + (fp8 ? (p.T + et - 1) / et : 0));
     if (p.E <= 128) few_gate_kernel<4><<<grid, kGateWarps * 32, 0, st>>>(p);
     else if (p.E <= 384) few_gate_kernel<12><<<grid, kGateWarps * 32, 0, st>>>(p);
     else few_gate_kernel<32><<<grid, kGateWarps * 32, 0, st>>>(p);
