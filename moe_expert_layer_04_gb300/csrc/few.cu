@@ -53,14 +53,11 @@ constexpr int kFewE = 1024;
 constexpr int kGateWarps = 16;
 constexpr int kGateSplits = 16;        // at most
 constexpr int kMulWarps = 16;
-constexpr int kGroups = 4;             // of multiplying warps; they take stages in turn
-constexpr int kGroupWarps = kMulWarps / kGroups;
-constexpr int kSumWarps = 3;           // each with a buffer of partial sums of its own
-constexpr int kCopyWarp = kMulWarps, kSumWarp0 = kMulWarps + 1;
+constexpr int kSumWarps = 2;           // each with a buffer of partial sums of its own
+constexpr int kCopyWarp = kMulWarps, kActWarp = kMulWarps + 1, kSumWarp0 = kMulWarps + 2;
 constexpr int kFewThreads = 32 * (kSumWarp0 + kSumWarps);
-constexpr int kChunk = 128;            // weight bytes of a row that a warp takes at a time
-constexpr int kStageChunks = 16;       // chunks of a row in a stage, at most
-constexpr int kWarpChunks = kStageChunks / kGroupWarps;
+constexpr int kChunk = 128;            // weight bytes of a row that a warp takes
+constexpr int kStageChunks = kMulWarps;         // chunks of a row in a stage, at most
 constexpr int kFewStage = 16 * kStageChunks * kChunk;   // two boxes of 8 rows
 constexpr int kW2Tiles = 2;            // tiles of 16 rows in an item of W2
 
@@ -111,6 +108,15 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1,
         "{%8,%9}, {%0,%1,%2,%3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t bytes,
+                                          uint64_t *bar) {
+    asm volatile(
+        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::
+            "r"(smem_u32(dst)),
+        "l"(src), "r"(bytes), "r"(smem_u32(bar))
+        : "memory");
 }
 
 // With an L2 policy: the weights pass through L2 once and must not push out what
@@ -347,35 +353,58 @@ __global__ void __launch_bounds__(kGateWarps * 32) few_gate_kernel(const __grid_
 
 // What every role knows about the routing: the hit experts in order, each cut
 // into passes of at most 8 NT rows, and the slots (token * k + j) of each.
-struct FewMeta {
-    int n_pass;                        // routed passes
-    int n_units;                       // column-tile contributions a column group waits for
+struct alignas(8) FewMeta {
+    int n_units;                       // contributions that a column tile waits for
+    float w[kFewS];                    // routing weight of each slot
     int16_t pass_e[kFewS];
     int16_t pass_row[kFewS];           // first entry in `slot`
     int16_t pass_n[kFewS];             // rows
     int16_t slot[kFewS];
-    int start[kFewE];                  // scratch: rows, then first slot of each expert
+    int16_t start[kFewE];              // scratch: rows, then first slot of each expert
 };
 
+// One tile's place in the work, as the copying warp hands it on with each stage.
+struct FewTile {
+    int tile;      // of 16 weight rows
+    int pass;      // -1 the shared expert
+    int rows;      // tokens of the pass | first entry in `slot` << 16
+    int flags;     // first chunk | kSecond | kLast
+};
+constexpr int kSecond = 1 << 30;       // W2
+constexpr int kLast = 1 << 29;         // the tile's last stage
+constexpr int kChunkMask = (1 << 29) - 1;
+
+__device__ __forceinline__ int4 ld_tile(const FewTile *p) {
+    const uint4 v = ld_shared_v4(smem_u32(p));
+    return make_int4((int)v.x, (int)v.y, (int)v.z, (int)v.w);
+}
+
 struct FewItem {
-    int pass;       // -1 the shared expert
-    bool second;    // W2
+    int pass;
+    bool second;
     int tile;
 };
 
 template <bool FP8, int NT>
 struct FewShape {
-    static constexpr int STAGES = 6;
-    static constexpr int RED = kSumWarps * kMulWarps * 128 * 4;
-    static constexpr int SCALES = FP8 ? STAGES * 2 * kStageChunks * 4 : 0;
-    static constexpr int SMEM =
-        1024 + STAGES * kFewStage + RED + SCALES + (int)sizeof(FewMeta) + 512;
+    static constexpr int STAGES = 5;
     static constexpr int ELT = FP8 ? 1 : 2;
-    static constexpr int STEP = FP8 ? 64 : 32;   // contraction of a step (half a chunk)
+    static constexpr int CHUNK_K = kChunk / ELT;       // contraction of a chunk
+    // token operands of a stage: rows of 16 bits an element, pitched so that the
+    // rows of a quarter warp's loads meet in no bank; passes of more rows are
+    // read from global memory
+    static constexpr int ACT_ROWS = FP8 ? 2 : 4;
+    static constexpr int ACT_PITCH = 2 * CHUNK_K * kStageChunks + (FP8 ? 16 : 64);
+    static constexpr int ACT = ACT_ROWS * ACT_PITCH;
+    static constexpr int RED = kSumWarps * kMulWarps * 128 * 4;
+    static constexpr int SCALES = FP8 ? 2 * kStageChunks * 4 : 0;
+    static constexpr int SMEM = 1024 + STAGES * (kFewStage + ACT + SCALES + 16 /* FewTile */) +
+                                RED + kSumWarps * 16 + (int)sizeof(FewMeta) + 512;
+    static_assert(SMEM <= 232448, "shared memory of a CTA");
 };
 
 // Tiles in order: shared W13, shared W2, routed W13, routed W2.  An item is one
-// tile of W13 or kW2Tiles of W2 (about the same bytes).
+// tile of W13 or kW2Tiles of W2.
 __device__ __forceinline__ FewItem few_item(int t, int tiles1, int tiles2, int n_pass) {
     FewItem it;
     it.pass = -1;
@@ -423,31 +452,31 @@ template <bool FP8, int NT>
 __global__ void __launch_bounds__(kFewThreads, 1) few_experts_kernel(
     const __grid_constant__ FewParams p) {
     using SH = FewShape<FP8, NT>;
+    constexpr int STAGES = SH::STAGES;
     extern __shared__ uint8_t smem_raw[];
-    uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-    uint8_t *ring = smem;
-    float4 *red = reinterpret_cast<float4 *>(smem + SH::STAGES * kFewStage);
-    // FP8: the stage's scales, of the chunks' gate rows and up rows
-    float *scales = reinterpret_cast<float *>(smem + SH::STAGES * kFewStage + SH::RED);
+    uint8_t *ring = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    uint8_t *acts = ring + STAGES * kFewStage;
+    float4 *red = reinterpret_cast<float4 *>(acts + STAGES * SH::ACT);
+    FewTile *info = reinterpret_cast<FewTile *>(reinterpret_cast<uint8_t *>(red) + SH::RED);
+    FewTile *rinfo = info + STAGES;          // per buffer of `red`; flags: group of 8 rows | kSecond
+    float *scales = reinterpret_cast<float *>(rinfo + kSumWarps);   // FP8: per stage gate, up
     FewMeta *meta =
-        reinterpret_cast<FewMeta *>(smem + SH::STAGES * kFewStage + SH::RED + SH::SCALES);
+        reinterpret_cast<FewMeta *>(reinterpret_cast<uint8_t *>(scales) + STAGES * SH::SCALES);
     uint64_t *full = reinterpret_cast<uint64_t *>(meta + 1);
-    uint64_t *ifull = full + SH::STAGES;     // `info` of the stage is written (its rows may not be there)
-    uint64_t *empty = ifull + SH::STAGES;
-    uint64_t *rfull = empty + SH::STAGES;    // a buffer of `red` has every warp's partial sums
+    uint64_t *ifull = full + STAGES;         // `info` of the stage is written
+    uint64_t *empty = ifull + STAGES;
+    uint64_t *rfull = empty + STAGES;        // a buffer of `red` has every warp's partial sums
     uint64_t *rempty = rfull + kSumWarps;    // ... and has been read
-    volatile int *info =
-        reinterpret_cast<volatile int *>(rempty + kSumWarps);   // per stage: tile, first chunk
-    volatile int *rinfo = info + 2 * SH::STAGES;    // per buffer: tile, group of 8 rows
-    volatile int *abort_s = rinfo + 2 * kSumWarps;
+    volatile int *abort_s = reinterpret_cast<volatile int *>(rempty + kSumWarps);
     int *last_s = const_cast<int *>(abort_s) + 1;
+    static_assert(sizeof(FewMeta) % 8 == 0, "the barriers behind it are 8-byte aligned");
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
-        for (int s = 0; s < SH::STAGES; ++s) {
-            mbar_init(&full[s], FP8 ? 33 : 1);
+        for (int s = 0; s < STAGES; ++s) {
+            mbar_init(&full[s], 2 + (FP8 ? 32 : 0));
             mbar_init(&ifull[s], 1);
-            mbar_init(&empty[s], kMulWarps);   // the other groups' too: they have seen the stage
+            mbar_init(&empty[s], kMulWarps);
         }
         for (int b = 0; b < kSumWarps; ++b) {
             mbar_init(&rfull[b], kMulWarps);
@@ -469,9 +498,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_experts_kernel(
         // first routed item, waits for the routing and lists the hit experts.
         const int shared_items = tiles1 + tiles2 / kW2Tiles;
         uint32_t s = 0, ph = 0;
-        int last[SH::STAGES];
-#pragma unroll
-        for (int i = 0; i < SH::STAGES; ++i) last[i] = -1;
+        uint32_t begun = 0;                // stages that a copy was issued to, and its parity
         const uint64_t policy = policy_evict_first();
         bool ok = true;
         int n_pass = -1;
@@ -515,7 +542,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_experts_kernel(
                     }
                     const int excl = sum + incl - (c | r << 10 | u << 20);
                     const int first = excl >> 10 & 1023;
-                    if (r > 0) meta->start[e] = first;
+                    if (r > 0) meta->start[e] = (int16_t)first;
                     for (int j = 0; j < c; ++j) {
                         const int q = (excl & 1023) + j;
                         meta->pass_e[q] = (int16_t)e;
@@ -528,13 +555,13 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_experts_kernel(
 #pragma unroll
                 for (int j = 0; j < kFewS / 32; ++j) {
                     const int i = lane + 32 * j;
-                    if (i < S) meta->slot[meta->start[__ldcg(p.ids + i)] + rank[j]] = (int16_t)i;
+                    if (i < S) {
+                        meta->slot[meta->start[__ldcg(p.ids + i)] + rank[j]] = (int16_t)i;
+                        meta->w[i] = __ldcg(p.w + i);
+                    }
                 }
                 n_pass = sum & 1023;
-                if (lane == 0) {
-                    meta->n_pass = n_pass;
-                    meta->n_units = (sum >> 20) + (p.T + 7) / 8;
-                }
+                if (lane == 0) meta->n_units = (sum >> 20) + (p.T + 7) / 8;
                 __syncwarp();
             }
             // item -> first tile
@@ -550,13 +577,16 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_experts_kernel(
             if (first < 0) {
                 if (!mbar_wait_warp(&empty[s], ph ^ 1u, wc)) break;
                 if (lane == 0) {
-                    info[s] = -1;
+                    info[s].tile = -1;
                     mbar_arrive(&ifull[s]);
+                    mbar_arrive(&full[s]);
                 }
+                if constexpr (FP8) mbar_arrive(&full[s]);
                 break;
             }
             const FewItem it = few_item(first, tiles1, tiles2, max(n_pass, 0));
             const int e = it.pass < 0 ? p.E : meta->pass_e[it.pass];
+            const int rows = it.pass < 0 ? p.T : meta->pass_n[it.pass] | meta->pass_row[it.pass] << 16;
             const int K = it.second ? p.I : p.d;
             const int whole = K * SH::ELT / kChunk;   // chunks
             const int chunks = (K * SH::ELT + kChunk - 1) / kChunk;
@@ -572,15 +602,16 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_experts_kernel(
                 if constexpr (FP8) {
                     const int row = it.second ? tile * 16
                                               : tile * 8 + (lane >= kStageChunks ? p.I : 0);
-                    const int rows = it.second ? p.d : 2 * p.I;
+                    const int all = it.second ? p.d : 2 * p.I;
                     sc = (it.second ? p.W2_s : p.W13_s) +
-                         ((size_t)e * fp8_blocks(rows) + row / kFp8Block) * kb + my_kb;
+                         ((size_t)e * fp8_blocks(all) + row / kFp8Block) * kb + my_kb;
                 }
                 for (int c0 = 0; c0 < chunks; c0 += cps) {
                     if (!mbar_wait_warp(&empty[s], ph ^ 1u, wc)) { ok = false; break; }
                     if (lane == 0) {
-                        info[s] = first + sub;
-                        info[SH::STAGES + s] = c0;
+                        const int flags = c0 | (it.second ? kSecond : 0) |
+                                          (c0 + cps >= chunks ? kLast : 0);
+                        *reinterpret_cast<int4 *>(&info[s]) = make_int4(tile, it.pass, rows, flags);
                         mbar_arrive(&ifull[s]);
                         if (c0 < whole) {
                             uint8_t *dst = ring + s * kFewStage;
@@ -596,126 +627,150 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_experts_kernel(
                             cp_async4(scales + s * 2 * kStageChunks + lane, sc + c0);
                         cp_async_arrive(&full[s]);
                     }
-                    last[s] = (int)ph;
-                    if (++s == SH::STAGES) { s = 0; ph ^= 1u; }
+                    begun = (begun & ~(0x10001u << s)) | (0x10000u << s) | (ph << s);
+                    if (++s == STAGES) { s = 0; ph ^= 1u; }
                 }
             }
         }
         if (*abort_s) {
             // drain the copies still in flight before the CTA exits
-            for (int i = 0; i < SH::STAGES; ++i)
-                if (last[i] >= 0) mbar_wait_teardown(&full[i], (uint32_t)last[i], p.wait_limit);
+            for (int i = 0; i < STAGES; ++i)
+                if (begun >> (16 + i) & 1u)
+                    mbar_wait_teardown(&full[i], begun >> i & 1u, p.wait_limit);
+        }
+    } else if (warp == kActWarp) {
+        // ------------------------------------------- token operands of a stage
+        // Waits until they exist (the tokens in f16 come from the first kernel,
+        // a pass's h from the tiles before it) and copies the rows of passes
+        // that have few; whoever multiplies waits for nothing else.
+        uint32_t s = 0, ph = 0;
+        bool have_x = !FP8;
+        while (mbar_wait_warp(&ifull[s], ph, wc)) {
+            const int4 q = ld_tile(&info[s]);
+            if (q.x < 0) {
+                if (lane == 0) mbar_arrive(&full[s]);
+                break;
+            }
+            const int n = q.z & 0xFFFF, row0 = q.z >> 16, c0 = q.w & kChunkMask;
+            const bool second = q.w & kSecond;
+            bool ready = true;
+            if (lane == 0) {
+                if (second) {
+                    // one signal per column tile and group of 8 rows
+                    if (c0 == 0)
+                        ready = wait_count_geq(h_done + 1 + q.y, tiles1 * ((n + 7) / 8), wc);
+                } else if (!have_x) {
+                    ready = wait_count_geq(p.counters + 3, p.T, wc);
+                }
+                fence_proxy_async_global();   // the copies read what others stored
+            }
+            have_x = have_x || !second;
+            if (!__shfl_sync(0xffffffffu, ready, 0)) break;
+            __syncwarp();
+            const int K = second ? p.I : p.d;
+            const int k0 = c0 * SH::CHUNK_K;
+            const int cps = second ? p.cps2 : p.cps13;
+            const int bytes = 2 * min(cps * SH::CHUNK_K, K - k0);
+            const bool copy = n <= SH::ACT_ROWS;
+            if (lane == 0) {
+                if (copy) mbar_arrive_expect_tx(&full[s], n * bytes);
+                else mbar_arrive(&full[s]);
+            }
+            __syncwarp();
+            if (copy && lane < n) {
+                const int slot = q.y < 0 ? S + lane : meta->slot[row0 + lane];
+                const uint16_t *src =
+                    second ? p.h + (size_t)slot * p.I
+                           : (FP8 ? p.x16 : p.x) + (size_t)(q.y < 0 ? lane : slot / p.k) * p.d;
+                bulk_load(acts + s * SH::ACT + lane * SH::ACT_PITCH, src + k0, bytes, &full[s]);
+            }
+            if (++s == STAGES) { s = 0; ph ^= 1u; }
         }
     } else if (warp < kMulWarps) {
         // -------------------------------------------------------- multiply
-        // Four groups of four warps take stages in turn, so that one's loads of
-        // token operands overlap the others' products.  The operands of a stage
-        // are loaded as soon as its item is known, while its weight rows may
-        // still be on their way.
-        uint32_t s = 0, ph = 0, unit = 0, n_stage = 0;
-        int item = -1;   // tile of `it`
-        bool have_x = false;
-        const int group = warp / kGroupWarps, wl = warp % kGroupWarps;
+        // Warp w takes chunk w of every stage: its 16 rows x 128 bytes against
+        // the tokens, fragments straight from the row-wise tiles (a lane's 16
+        // bytes are consecutive k, fed as k-pairs to successive MMAs, on both
+        // sides alike).
+        uint32_t s = 0, ph = 0, unit = 0;
         const int g = lane >> 2, c = lane & 3;
         const int pr = few_row(g);
         float acc[NT][4];
-        const uint16_t *act[NT];   // this lane's token row of each group of 8, or null
-        FewItem it{};
-        int n_rows = 0, row0 = 0, K = 0;
+        const uint16_t *act[NT];   // passes of many rows: this lane's token row of each group
         constexpr int NV = FP8 ? 2 : 1;
-        constexpr int STEPS = 2 * kWarpChunks;
-        // steps whose token operands are loaded ahead (registers: the rest on use)
-        constexpr int PRE = !FP8 ? STEPS : NT > 1 ? 2 : 4;
         while (true) {
-            if (!mbar_wait_warp(&ifull[s], ph, wc)) break;
-            const int t = info[s], c0 = info[SH::STAGES + s];
-            if (t < 0) {
+            if (!mbar_wait_warp(&full[s], ph, wc)) break;
+            const int4 q = ld_tile(&info[s]);
+            if (q.x < 0) {
                 if (lane == 0) {   // tell the sum warps, one buffer each
                     for (int b = 0; b < kSumWarps; ++b, ++unit) {
                         const uint32_t buf = unit % kSumWarps;
                         if (!mbar_wait(&rempty[buf], (unit / kSumWarps & 1u) ^ 1u, wc)) break;
-                        if (warp == 0) rinfo[2 * buf] = -1;
+                        if (warp == 0) rinfo[buf].tile = -1;
                         mbar_arrive(&rfull[buf]);
                     }
                 }
                 break;
             }
+            const int n = q.z & 0xFFFF, row0 = q.z >> 16, c0 = q.w & kChunkMask;
+            const bool second = q.w & kSecond;
+            const int K = second ? p.I : p.d;
+            const int nt = NT == 1 ? 1 : (n + 7) >> 3;
+            const bool in_smem = n <= SH::ACT_ROWS;
             if (c0 == 0) {
-                it = few_item(t, tiles1, tiles2, t < tiles1 + tiles2 ? 0 : meta->n_pass);
-                K = it.second ? p.I : p.d;
-                n_rows = it.pass < 0 ? p.T : meta->pass_n[it.pass];
-                row0 = it.pass < 0 ? 0 : meta->pass_row[it.pass];
-#pragma unroll
-                for (int j = 0; j < NT; ++j)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) acc[j][i] = 0.0f;
-            }
-            const int nt = (n_rows + 7) >> 3;
-            const int chunks = (K * SH::ELT + kChunk - 1) / kChunk;
-            const int cps = it.second ? p.cps2 : p.cps13;
-            if (n_stage++ % kGroups == (uint32_t)group) {
-            if (item != t) {
-                item = t;
-                if (it.second || (FP8 && !have_x)) {
-                    // the h rows of this pass: one signal per column tile and
-                    // group of 8 rows; or the tokens in f16, from the first kernel
-                    bool ready = true;
-                    if (lane == 0)
-                        ready = it.second ? wait_count_geq(h_done + 1 + it.pass,
-                                                           tiles1 * ((n_rows + 7) / 8), wc)
-                                          : wait_count_geq(p.counters + 3, p.T, wc);
-                    have_x = have_x || !it.second;
-                    ready = __shfl_sync(0xffffffffu, ready, 0);
-                    __syncwarp();   // orders the h loads of every lane behind the acquire
-                    if (!ready) break;
-                }
 #pragma unroll
                 for (int j = 0; j < NT; ++j) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) acc[j][i] = 0.0f;
                     const int i = j * 8 + g;
                     act[j] = nullptr;
-                    if (i < n_rows) {
-                        const int slot = it.pass < 0 ? S + i : meta->slot[row0 + i];
-                        act[j] = it.second ? p.h + (size_t)slot * p.I
-                                           : (FP8 ? p.x16 : p.x) +
-                                                 (size_t)(it.pass < 0 ? i : slot / p.k) * p.d;
+                    if (!in_smem && i < n) {
+                        const int slot = q.y < 0 ? S + i : meta->slot[row0 + i];
+                        act[j] = second ? p.h + (size_t)slot * p.I
+                                        : (FP8 ? p.x16 : p.x) +
+                                              (size_t)(q.y < 0 ? i : slot / p.k) * p.d;
                     }
                 }
             }
-            // this warp's chunks of the stage: wl, wl + 4, ...
-            const int n_c = min(cps, chunks - c0);
-            // token operand of half u % 2 of the warp's chunk u / 2, group j (x
-            // through L1; what is written while this kernel runs, from L2)
-            auto load_act = [&](int u, int j, uint4 (&v)[NV]) {
-                const int cl = wl + kGroupWarps * (u / 2);
-                const int kk = (2 * (c0 + cl) + u % 2) * SH::STEP + c * (SH::STEP / 4);
+            const int chunk = c0 + warp;
+            const int cps = second ? p.cps2 : p.cps13;
+            if (warp < cps && chunk * SH::CHUNK_K < K) {
+                // token operand of the chunk's half h, group j
+                auto load_act = [&](int h, int j, uint4 (&v)[NV]) {
+                    const int kk = (2 * chunk + h) * (SH::CHUNK_K / 2) + c * (SH::CHUNK_K / 8);
 #pragma unroll
-                for (int i = 0; i < NV; ++i) {
-                    v[i] = make_uint4(0, 0, 0, 0);
-                    if (act[j] && cl < n_c && kk < K) {
-                        const uint4 *a = reinterpret_cast<const uint4 *>(act[j] + kk) + i;
-                        v[i] = FP8 || it.second ? __ldcg(a) : __ldg(a);
+                    for (int i = 0; i < NV; ++i) {
+                        v[i] = make_uint4(0, 0, 0, 0);
+                        if (act[j] && kk < K)
+                            v[i] = __ldcg(reinterpret_cast<const uint4 *>(act[j] + kk) + i);
                     }
+                };
+                uint4 v0[2][NV];   // group 0
+                if (in_smem) {
+                    const uint32_t a = smem_u32(acts + s * SH::ACT) + g * SH::ACT_PITCH +
+                                       warp * (2 * SH::CHUNK_K) + c * (SH::CHUNK_K / 4);
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+#pragma unroll
+                        for (int i = 0; i < NV; ++i)
+                            v0[h][i] = g < n ? ld_shared_v4(a + h * SH::CHUNK_K + 16 * i)
+                                             : make_uint4(0, 0, 0, 0);
+                } else {
+                    load_act(0, 0, v0[0]);
+                    load_act(1, 0, v0[1]);
                 }
-            };
-            uint4 v0[PRE][NV];
-#pragma unroll
-            for (int u = 0; u < PRE; ++u) load_act(u, 0, v0[u]);
-            if (!mbar_wait_warp(&full[s], ph, wc)) break;
-#pragma unroll
-            for (int ch = 0; ch < kWarpChunks; ++ch) {
-                const int chunk = wl + kGroupWarps * ch;
-                if (chunk >= n_c) break;
                 // rows pr and pr + 8 of the chunk, 128 bytes each, 16-byte pieces
                 // exchanged by row (128-byte swizzle)
                 uint4 wq[2][2];   // [half][row pr / pr + 8]
                 {
                     const uint32_t a0 =
-                        smem_u32(ring + s * kFewStage) + chunk * (8 * kChunk) + pr * kChunk;
+                        smem_u32(ring + s * kFewStage) + warp * (8 * kChunk) + pr * kChunk;
+                    const uint32_t b0 = a0 + kFewStage / 2;
                     const uint32_t first = (uint32_t)(c ^ pr) << 4;
                     wq[0][0] = ld_shared_v4(a0 + first);
+                    wq[0][1] = ld_shared_v4(b0 + first);
                     wq[1][0] = ld_shared_v4(a0 + (first ^ 64u));
-                    wq[0][1] = ld_shared_v4(a0 + kFewStage / 2 + first);
-                    wq[1][1] = ld_shared_v4(a0 + kFewStage / 2 + (first ^ 64u));
+                    wq[1][1] = ld_shared_v4(b0 + (first ^ 64u));
                 }
                 if constexpr (!FP8) {
 #pragma unroll
@@ -725,8 +780,8 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_experts_kernel(
                         for (int j = 0; j < NT; ++j) {
                             if (j >= nt) break;
                             uint4 v[NV];
-                            if (j > 0) load_act(2 * ch + h, j, v);
-                            const uint4 b = j > 0 ? v[0] : v0[2 * ch + h][0];
+                            if (j > 0) load_act(h, j, v);
+                            const uint4 b = j > 0 ? v[0] : v0[h][0];
                             mma_bf16(acc[j], wa.x, wb.x, wa.y, wb.y, b.x, b.y);
                             mma_bf16(acc[j], wa.z, wb.z, wa.w, wb.w, b.z, b.w);
                         }
@@ -734,25 +789,28 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_experts_kernel(
                 } else {
                     // a contraction that ends inside a chunk: its last 64 codes
                     // are not in the stage (a copied row would run into the next)
-                    const bool tail = (K & 64) && (c0 + chunk) * 128 + 64 == K;
+                    const bool tail = chunk * 128 + 64 == K;
                     if (tail) {
-                        const uint8_t *w = static_cast<const uint8_t *>(it.second ? p.W2 : p.W13);
-                        const int e = it.pass < 0 ? p.E : meta->pass_e[it.pass];
-                        const size_t r = it.second ? (size_t)e * p.d + it.tile * 16 + pr
-                                                   : (size_t)e * 2 * p.I + it.tile * 8 + pr;
+                        const uint8_t *w = static_cast<const uint8_t *>(second ? p.W2 : p.W13);
+                        const int e = q.y < 0 ? p.E : meta->pass_e[q.y];
+                        const size_t r = second ? (size_t)e * p.d + q.x * 16 + pr
+                                                : (size_t)e * 2 * p.I + q.x * 8 + pr;
                         w += r * K + K - 64 + c * 16;
                         wq[0][0] = __ldg(reinterpret_cast<const uint4 *>(w));
-                        wq[0][1] = __ldg(reinterpret_cast<const uint4 *>(
-                            w + (size_t)(it.second ? 8 : p.I) * K));
+                        wq[0][1] = __ldg(
+                            reinterpret_cast<const uint4 *>(w + (size_t)(second ? 8 : p.I) * K));
+                        wq[1][0] = wq[1][1] = make_uint4(0, 0, 0, 0);
+                        v0[1][0] = v0[1][NV - 1] = make_uint4(0, 0, 0, 0);
                     }
-                    float part[NT][4];   // this block of 128, not yet scaled
+                    // the block of 128, not yet scaled; two sums, so that each
+                    // MMA need not wait for the one before it
+                    float part[NT][2][4];
 #pragma unroll
                     for (int j = 0; j < NT; ++j)
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) part[j][i] = 0.0f;
+                        for (int i = 0; i < 4; ++i) part[j][0][i] = part[j][1][i] = 0.0f;
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        if (h == 1 && tail) break;
                         const uint32_t qa[4] = {wq[h][0].x, wq[h][0].y, wq[h][0].z, wq[h][0].w};
                         const uint32_t qb[4] = {wq[h][1].x, wq[h][1].y, wq[h][1].z, wq[h][1].w};
                         uint32_t x0[4], x1[4], y0[4], y1[4];
@@ -765,37 +823,33 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_experts_kernel(
                         for (int j = 0; j < NT; ++j) {
                             if (j >= nt) break;
                             uint4 v[NV];
-                            const bool ahead = j == 0 && 2 * ch + h < PRE;
-                            if (!ahead) load_act(2 * ch + h, j, v);
-                            const uint4 *b = ahead ? v0[(2 * ch + h) % PRE] : v;
+                            if (j > 0) load_act(h, j, v);
+                            const uint4 *b = j > 0 ? v : v0[h];
                             const uint32_t bv[8] = {b[0].x, b[0].y, b[0].z, b[0].w,
                                                     b[NV - 1].x, b[NV - 1].y, b[NV - 1].z,
                                                     b[NV - 1].w};
 #pragma unroll
                             for (int m = 0; m < 4; ++m)
-                                mma_f16(part[j], x0[m], y0[m], x1[m], y1[m], bv[2 * m],
+                                mma_f16(part[j][m & 1], x0[m], y0[m], x1[m], y1[m], bv[2 * m],
                                         bv[2 * m + 1]);
                         }
                     }
-                    const float f0 = scales[s * 2 * kStageChunks + chunk];
-                    const float f1 = scales[(s * 2 + 1) * kStageChunks + chunk];
+                    const float f0 = scales[s * 2 * kStageChunks + warp];
+                    const float f1 = scales[(s * 2 + 1) * kStageChunks + warp];
 #pragma unroll
                     for (int j = 0; j < NT; ++j) {
-                        acc[j][0] = fmaf(part[j][0], f0, acc[j][0]);
-                        acc[j][1] = fmaf(part[j][1], f0, acc[j][1]);
-                        acc[j][2] = fmaf(part[j][2], f1, acc[j][2]);
-                        acc[j][3] = fmaf(part[j][3], f1, acc[j][3]);
+                        acc[j][0] = fmaf(part[j][0][0] + part[j][1][0], f0, acc[j][0]);
+                        acc[j][1] = fmaf(part[j][0][1] + part[j][1][1], f0, acc[j][1]);
+                        acc[j][2] = fmaf(part[j][0][2] + part[j][1][2], f1, acc[j][2]);
+                        acc[j][3] = fmaf(part[j][0][3] + part[j][1][3], f1, acc[j][3]);
                     }
                 }
             }
-            }
-            // every group releases every stage, so that none can be a lap behind
             __syncwarp();
             if (lane == 0) mbar_arrive(&empty[s]);
-            if (++s == SH::STAGES) { s = 0; ph ^= 1u; }
-            if (c0 + cps < chunks) continue;
-            // the tile's partial sums, one buffer per group of 8 rows (zeros from
-            // a warp that had no stage of it)
+            if (++s == STAGES) { s = 0; ph ^= 1u; }
+            if (!(q.w & kLast)) continue;
+            // the tile's partial sums, one buffer per group of 8 rows
             bool ok = true;
 #pragma unroll
             for (int j = 0; j < NT; ++j) {
@@ -805,10 +859,9 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_experts_kernel(
                 if (!ok) break;
                 red[(buf * kMulWarps + warp) * 32 + lane] =
                     make_float4(acc[j][0], acc[j][1], acc[j][2], acc[j][3]);
-                if (warp == 0 && lane == 0) {
-                    rinfo[2 * buf] = t;
-                    rinfo[2 * buf + 1] = j;
-                }
+                if (warp == 0 && lane == 0)
+                    *reinterpret_cast<int4 *>(&rinfo[buf]) =
+                        make_int4(q.x, q.y, q.z, j | (q.w & kSecond));
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&rfull[buf]);
                 ++unit;
@@ -819,10 +872,10 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_experts_kernel(
         // ------------------------------------------- sums over the warps
         const int buf = warp - kSumWarp0;
         const int g = few_row(lane >> 2), c = lane & 3;
-        for (uint32_t n = 0;; ++n) {
-            if (!mbar_wait_warp(&rfull[buf], n & 1u, wc)) break;
-            const int t = rinfo[2 * buf], grp = rinfo[2 * buf + 1];
-            if (t < 0) break;
+        for (uint32_t m = 0;; ++m) {
+            if (!mbar_wait_warp(&rfull[buf], m & 1u, wc)) break;
+            const int4 q = ld_tile(&rinfo[buf]);
+            if (q.x < 0) break;
             float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
             for (int w = 0; w < kMulWarps; ++w) {
@@ -834,43 +887,45 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_experts_kernel(
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(&rempty[buf]);
-            const FewItem it = few_item(t, tiles1, tiles2, t < tiles1 + tiles2 ? 0 : meta->n_pass);
-            const int n_rows = it.pass < 0 ? p.T : meta->pass_n[it.pass];
-            const int row0 = it.pass < 0 ? 0 : meta->pass_row[it.pass];
+            const int n = q.z & 0xFFFF, row0 = q.z >> 16, grp = q.w & kChunkMask;
+            const bool second = q.w & kSecond;
             // v[0], v[1]: weight row g, tokens 2c and 2c + 1; v[2], v[3]: row g + 8
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const int r = grp * 8 + 2 * c + i;
-                if (r >= n_rows) continue;
-                const int slot = it.pass < 0 ? S + r : meta->slot[row0 + r];
-                if (it.second) {
-                    const float w = (it.pass < 0 ? 1.0f : __ldcg(p.w + slot)) *
+                if (r >= n) continue;
+                const int slot = q.y < 0 ? S + r : meta->slot[row0 + r];
+                if (second) {
+                    const float w = (q.y < 0 ? 1.0f : meta->w[slot]) *
                                     (FP8 ? exp2i(-p.h_exp) : 1.0f);
-                    float *o = p.yp + (size_t)slot * p.d + it.tile * 16 + g;
+                    float *o = p.yp + (size_t)slot * p.d + q.x * 16 + g;
                     o[0] = w * v[i];
                     o[8] = w * v[2 + i];
                 } else {
                     float up = 1.0f;
-                    if constexpr (FP8) up = __ldcg(p.x16_s + (it.pass < 0 ? r : slot / p.k));
+                    if constexpr (FP8) up = __ldcg(p.x16_s + (q.y < 0 ? r : slot / p.k));
                     const float h = swiglu_clamped_nan(v[i] * up, v[2 + i] * up, p.clamp);
-                    p.h[(size_t)slot * p.I + it.tile * 8 + g] =
+                    p.h[(size_t)slot * p.I + q.x * 8 + g] =
                         FP8 ? __half_as_ushort(__float2half_rn(h * exp2i(p.h_exp)))
                             : (uint16_t)(pack_bf16x2(h, 0.0f) & 0xFFFFu);
                 }
             }
             __syncwarp();
-            if (!it.second) {
-                if (lane == 0) red_release_gpu_add(h_done + 1 + it.pass, 1);
+            if (!second) {
+                if (lane == 0) {
+                    fence_proxy_async_global();   // copies will read h
+                    red_release_gpu_add(h_done + 1 + q.y, 1);
+                }
                 continue;
             }
             int old = 0;
-            if (lane == 0) old = atom_add_acq_rel(y_done + it.tile, 1);
+            if (lane == 0) old = atom_add_acq_rel(y_done + q.x, 1);
             old = __shfl_sync(0xffffffffu, old, 0);
             __syncwarp();
             if (old != meta->n_units - 1) continue;
             // every product of these 16 columns is there
             for (int i = lane; i < p.T * 16; i += 32) {
-                const int tk = i >> 4, n16 = it.tile * 16 + (i & 15);
+                const int tk = i >> 4, n16 = q.x * 16 + (i & 15);
                 float sum = __ldcg(p.yp + (size_t)(S + tk) * p.d + n16);
                 for (int j = 0; j < p.k; ++j)
                     sum += __ldcg(p.yp + (size_t)(tk * p.k + j) * p.d + n16);
