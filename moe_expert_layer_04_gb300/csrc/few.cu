@@ -207,6 +207,10 @@ __device__ void few_token_f16(const FewParams &p, int t, uint32_t *warp_top) {
 
 template <int EPL>
 __global__ void __launch_bounds__(kGateWarps * 32) few_gate_kernel(const __grid_constant__ FewParams p) {
+    // The launch may precede the end of the kernel before it (which hides its
+    // latency); nothing is read before that end.  The second kernel may start
+    // from here on, never before: it shares the workspace with the call before.
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if ((int)blockIdx.y >= p.splits) {
         __shared__ uint32_t warp_top[kGateWarps];
@@ -486,6 +490,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_experts_kernel(
         fence_barrier_init();
     }
     __syncthreads();
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // a next call's first kernel
     const WaitCtl wc{abort_s, p.status, p.wait_limit};
     const int S = p.T * p.k;
     const int tiles1 = p.I / 8, tiles2 = p.d / 16;
@@ -502,10 +507,10 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_experts_kernel(
         const uint64_t policy = policy_evict_first();
         bool ok = true;
         int n_pass = -1;
+        int ticket = 0;
+        if (lane == 31) ticket = atomicAdd(p.counters + 1, 1);
         while (ok) {
-            int t = 0;
-            if (lane == 0) t = atomicAdd(p.counters + 1, 1);
-            t = __shfl_sync(0xffffffffu, t, 0);
+            int t = __shfl_sync(0xffffffffu, ticket, 31);
             if (t >= shared_items && n_pass < 0) {
                 asm volatile("griddepcontrol.wait;" ::: "memory");
                 for (int e = lane; e < p.E; e += 32) meta->start[e] = 0;
@@ -584,6 +589,8 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_experts_kernel(
                 if constexpr (FP8) mbar_arrive(&full[s]);
                 break;
             }
+            // the next item's number comes while this one's copies are issued
+            if (lane == 31) ticket = atomicAdd(p.counters + 1, 1);
             const FewItem it = few_item(first, tiles1, tiles2, max(n_pass, 0));
             const int e = it.pass < 0 ? p.E : meta->pass_e[it.pass];
             const int rows = it.pass < 0 ? p.T : meta->pass_n[it.pass] | meta->pass_row[it.pass] << 16;
@@ -979,6 +986,24 @@ FewWorkspace carve_few(uint8_t *base, int T, int d, int E, int k, int I) {
     return w;
 }
 
+// A launch that may begin before the kernel ahead of it in the stream ends
+// (programmatic dependent launch).
+moe_status launch_early(void (*kern)(FewParams), dim3 grid, int threads, int smem,
+                        const FewParams &p, cudaStream_t st) {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads, 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, kern, p) != cudaSuccess) return MOE_ERR_CUDA;
+    return cuda_status(cudaGetLastError());
+}
+
 template <bool FP8, int NT>
 moe_status launch_experts(const FewParams &p, cudaStream_t st) {
     using SH = FewShape<FP8, NT>;
@@ -994,18 +1019,8 @@ moe_status launch_experts(const FewParams &p, cudaStream_t st) {
         attr_set[dev] = true;
     }
     const long long items = (long long)(p.T * p.k + 1) * (p.I / 8 + p.d / 16);
-    cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.gridDim = dim3((unsigned)(items < num_sms() ? items : num_sms()), 1, 1);
-    cfg.blockDim = dim3(kFewThreads, 1, 1);
-    cfg.dynamicSmemBytes = SH::SMEM;
-    cfg.stream = st;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, kern, p) != cudaSuccess) return MOE_ERR_CUDA;
-    return cuda_status(cudaGetLastError());
+    return launch_early(kern, dim3((unsigned)(items < num_sms() ? items : num_sms())), kFewThreads,
+                        SH::SMEM, p, st);
 }
 
 template <bool FP8>
@@ -1095,10 +1110,12 @@ moe_status launch_few(const moe_few_args *a, cudaStream_t st) {
     p.h_exp = 0;
     while (p.h_exp < 24 && p.clamp * p.clamp * (float)(2 << p.h_exp) <= 65504.0f) ++p.h_exp;
     const dim3 grid(et, splits + (fp8 ? (p.T + et - 1) / et : 0));
-    if (p.E <= 128) few_gate_kernel<4><<<grid, kGateWarps * 32, 0, st>>>(p);
-    else if (p.E <= 384) few_gate_kernel<12><<<grid, kGateWarps * 32, 0, st>>>(p);
-    else few_gate_kernel<32><<<grid, kGateWarps * 32, 0, st>>>(p);
-    if (cudaGetLastError() != cudaSuccess) return MOE_ERR_CUDA;
+    const moe_status s =
+        launch_early(p.E <= 128   ? few_gate_kernel<4>
+                     : p.E <= 384 ? few_gate_kernel<12>
+                                  : few_gate_kernel<32>,
+                     grid, kGateWarps * 32, 0, p, st);
+    if (s != MOE_OK) return s;
     return fp8 ? launch_experts_nt<true>(p, st) : launch_experts_nt<false>(p, st);
 }
 
