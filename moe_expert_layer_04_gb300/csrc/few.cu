@@ -15,9 +15,10 @@
 // last: one warp takes items, lists the hit experts and copies weight rows into
 // a ring in shared memory (two TMA boxes a stage) far ahead of the 16 warps that
 // multiply, across the boundaries of the phases, whose dependences
-// only the multiplying warps wait for; three more warps add up the partial sums,
+// only the multiplying warps wait for; another brings the
+// token operands, and two add up the partial sums,
 // apply the SwiGLU or the routing weight and signal, so that no multiplying
-// warp waits for a store or an atomic.  The work comes as items of 16 weight rows in one order for the whole
+// warp waits for a store or a signal.  The work comes as items of 16 weight rows in one order for the whole
 // grid, handed out by a counter:
 //   shared expert's W13 | its W2 | W13 of the hit experts | their W2
 // The first two parts need no routing result, so the kernel starts on them
@@ -26,7 +27,7 @@
 // so the kernel needs no particular number of resident CTAs.
 //
 // Items: 8 gate rows and the matching 8 up rows of W13 (both land in the same
-// thread, which applies the SwiGLU), or 16 rows of W2.  Four groups of four
+// thread, which applies the SwiGLU), or 16 rows of W2.  Two groups of eight
 // warps take the stages in turn and so split the contraction, each with mma.m16n8k16 (weights x 8 tokens, bf16, fp32 sums; at
 // a few rows a weight the matrix pipe is nearly idle, so the 128-row tiles of
 // tcgen05 would only add padding); their partial sums meet in shared memory in
@@ -35,9 +36,9 @@
 // each scaled by a power of two (a few CTAs of the first kernel).  h is rounded
 // to 16 bits (the second matmul's operand: bf16, or with FP8 weights f16), every
 // other sum stays fp32 up to y.  Products of
-// the second matmul go to fp32 rows per (token, slot); the last item of a
-// column group to finish adds them up in slot order, so results do not depend
-// on who finishes when.
+// the second matmul go to fp32 rows per (token, slot); at the end
+// each CTA adds up its share of the columns in slot order, so results do not
+// depend on who finishes when.
 #include <cfloat>
 #include <climits>
 
@@ -57,7 +58,10 @@ constexpr int kSumWarps = 2;           // each with a buffer of partial sums of 
 constexpr int kCopyWarp = kMulWarps, kActWarp = kMulWarps + 1, kSumWarp0 = kMulWarps + 2;
 constexpr int kFewThreads = 32 * (kSumWarp0 + kSumWarps);
 constexpr int kChunk = 128;            // weight bytes of a row that a warp takes
-constexpr int kStageChunks = kMulWarps;         // chunks of a row in a stage, at most
+constexpr int kGroups = 2;             // of multiplying warps; they take stages in turn
+constexpr int kGroupWarps = kMulWarps / kGroups;
+constexpr int kWarpChunks = 2;         // chunks of a stage for one warp
+constexpr int kStageChunks = kGroupWarps * kWarpChunks;   // of a row in a stage, at most
 constexpr int kFewStage = 16 * kStageChunks * kChunk;   // two boxes of 8 rows
 constexpr int kW2Tiles = 2;            // tiles of 16 rows in an item of W2
 
@@ -372,11 +376,12 @@ struct FewTile {
     int tile;      // of 16 weight rows
     int pass;      // -1 the shared expert
     int rows;      // tokens of the pass | first entry in `slot` << 16
-    int flags;     // first chunk | kSecond | kLast
+    int flags;     // first chunk | kSecond | kLast | kItem
 };
 constexpr int kSecond = 1 << 30;       // W2
 constexpr int kLast = 1 << 29;         // the tile's last stage
-constexpr int kChunkMask = (1 << 29) - 1;
+constexpr int kItem = 1 << 28;         // the item's first stage
+constexpr int kChunkMask = (1 << 28) - 1;
 
 __device__ __forceinline__ int4 ld_tile(const FewTile *p) {
     const uint4 v = ld_shared_v4(smem_u32(p));
@@ -471,7 +476,9 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_experts_kernel(
     uint64_t *empty = ifull + STAGES;
     uint64_t *rfull = empty + STAGES;        // a buffer of `red` has every warp's partial sums
     uint64_t *rempty = rfull + kSumWarps;    // ... and has been read
-    volatile int *abort_s = reinterpret_cast<volatile int *>(rempty + kSumWarps);
+    uint64_t *qfull = rempty + kSumWarps;    // an item's number is in `queue`
+    volatile int *queue = reinterpret_cast<volatile int *>(qfull + 2);
+    volatile int *abort_s = queue + 2;
     int *last_s = const_cast<int *>(abort_s) + 1;
     static_assert(sizeof(FewMeta) % 8 == 0, "the barriers behind it are 8-byte aligned");
 
@@ -486,6 +493,8 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_experts_kernel(
             mbar_init(&rfull[b], kMulWarps);
             mbar_init(&rempty[b], 1);
         }
+        mbar_init(&qfull[0], 1);
+        mbar_init(&qfull[1], 1);
         *abort_s = 0;
         fence_barrier_init();
     }
@@ -507,10 +516,9 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_experts_kernel(
         const uint64_t policy = policy_evict_first();
         bool ok = true;
         int n_pass = -1;
-        int ticket = 0;
-        if (lane == 31) ticket = atomicAdd(p.counters + 1, 1);
-        while (ok) {
-            int t = __shfl_sync(0xffffffffu, ticket, 31);
+        for (uint32_t n = 0; ok; ++n) {
+            if (!mbar_wait_warp(&qfull[n & 1], n >> 1 & 1u, wc)) break;
+            int t = queue[n & 1];
             if (t >= shared_items && n_pass < 0) {
                 asm volatile("griddepcontrol.wait;" ::: "memory");
                 for (int e = lane; e < p.E; e += 32) meta->start[e] = 0;
@@ -584,13 +592,9 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_experts_kernel(
                 if (lane == 0) {
                     info[s].tile = -1;
                     mbar_arrive(&ifull[s]);
-                    mbar_arrive(&full[s]);
                 }
-                if constexpr (FP8) mbar_arrive(&full[s]);
                 break;
             }
-            // the next item's number comes while this one's copies are issued
-            if (lane == 31) ticket = atomicAdd(p.counters + 1, 1);
             const FewItem it = few_item(first, tiles1, tiles2, max(n_pass, 0));
             const int e = it.pass < 0 ? p.E : meta->pass_e[it.pass];
             const int rows = it.pass < 0 ? p.T : meta->pass_n[it.pass] | meta->pass_row[it.pass] << 16;
@@ -617,7 +621,8 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_experts_kernel(
                     if (!mbar_wait_warp(&empty[s], ph ^ 1u, wc)) { ok = false; break; }
                     if (lane == 0) {
                         const int flags = c0 | (it.second ? kSecond : 0) |
-                                          (c0 + cps >= chunks ? kLast : 0);
+                                          (c0 + cps >= chunks ? kLast : 0) |
+                                          (c0 == 0 && sub == 0 ? kItem : 0);
                         *reinterpret_cast<int4 *>(&info[s]) = make_int4(tile, it.pass, rows, flags);
                         mbar_arrive(&ifull[s]);
                         if (c0 < whole) {
@@ -650,14 +655,23 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_experts_kernel(
         // Waits until they exist (the tokens in f16 come from the first kernel,
         // a pass's h from the tiles before it) and copies the rows of passes
         // that have few; whoever multiplies waits for nothing else.
-        uint32_t s = 0, ph = 0;
+        // It also takes the item numbers from the grid's counter, two ahead of
+        // the copies (the copying warp's arrivals would wait for its own
+        // outstanding atomics).
+        uint32_t s = 0, ph = 0, n_item = 0;
         bool have_x = !FP8;
+        auto take_item = [&]() {
+            if (lane == 0) {
+                queue[n_item & 1] = atomicAdd(p.counters + 1, 1);
+                mbar_arrive(&qfull[n_item & 1]);
+            }
+            ++n_item;
+        };
+        take_item();
+        take_item();
         while (mbar_wait_warp(&ifull[s], ph, wc)) {
             const int4 q = ld_tile(&info[s]);
-            if (q.x < 0) {
-                if (lane == 0) mbar_arrive(&full[s]);
-                break;
-            }
+            if (q.x < 0) break;
             const int n = q.z & 0xFFFF, row0 = q.z >> 16, c0 = q.w & kChunkMask;
             const bool second = q.w & kSecond;
             bool ready = true;
@@ -677,8 +691,8 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_experts_kernel(
             const int K = second ? p.I : p.d;
             const int k0 = c0 * SH::CHUNK_K;
             const int cps = second ? p.cps2 : p.cps13;
-            const int bytes = 2 * min(cps * SH::CHUNK_K, K - k0);
-            const bool copy = n <= SH::ACT_ROWS;
+            const int bytes = 2 * min(cps * SH::CHUNK_K, K - k0);   // none behind the end
+            const bool copy = n <= SH::ACT_ROWS && bytes > 0;
             if (lane == 0) {
                 if (copy) mbar_arrive_expect_tx(&full[s], n * bytes);
                 else mbar_arrive(&full[s]);
@@ -691,22 +705,29 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_experts_kernel(
                            : (FP8 ? p.x16 : p.x) + (size_t)(q.y < 0 ? lane : slot / p.k) * p.d;
                 bulk_load(acts + s * SH::ACT + lane * SH::ACT_PITCH, src + k0, bytes, &full[s]);
             }
+            // the copying warp has read this item's number: its place is free
+            if (q.w & kItem) take_item();
             if (++s == STAGES) { s = 0; ph ^= 1u; }
         }
     } else if (warp < kMulWarps) {
         // -------------------------------------------------------- multiply
-        // Warp w takes chunk w of every stage: its 16 rows x 128 bytes against
-        // the tokens, fragments straight from the row-wise tiles (a lane's 16
-        // bytes are consecutive k, fed as k-pairs to successive MMAs, on both
-        // sides alike).
-        uint32_t s = 0, ph = 0, unit = 0;
+        // Two groups of eight warps take the stages in turn, so that one's waits
+        // and loads overlap the other's products; warp w of a group takes chunks
+        // w and w + 8 of its stage: 16 rows x 128 bytes against the tokens,
+        // fragments straight from the row-wise tiles (a lane's 16 bytes are
+        // consecutive k, fed as k-pairs to successive MMAs, on both sides alike).
+        const int group = warp / kGroupWarps, wl = warp % kGroupWarps;
+        uint32_t s = 0, ph = 0, unit = 0, n_stage = 0;
         const int g = lane >> 2, c = lane & 3;
         const int pr = few_row(g);
         float acc[NT][4];
         const uint16_t *act[NT];   // passes of many rows: this lane's token row of each group
         constexpr int NV = FP8 ? 2 : 1;
         while (true) {
-            if (!mbar_wait_warp(&full[s], ph, wc)) break;
+            // Every warp goes through every stage in order and releases it, also
+            // the other group's: with parity waits, whoever skipped stages could
+            // take one lap of the ring for another.
+            if (!mbar_wait_warp(&ifull[s], ph, wc)) break;
             const int4 q = ld_tile(&info[s]);
             if (q.x < 0) {
                 if (lane == 0) {   // tell the sum warps, one buffer each
@@ -739,9 +760,14 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_experts_kernel(
                     }
                 }
             }
-            const int chunk = c0 + warp;
             const int cps = second ? p.cps2 : p.cps13;
-            if (warp < cps && chunk * SH::CHUNK_K < K) {
+            const bool mine = (n_stage++ & (kGroups - 1)) == (uint32_t)group;
+            if (mine && !mbar_wait_warp(&full[s], ph, wc)) break;
+#pragma unroll
+            for (int ch = 0; ch < kWarpChunks; ++ch) {
+                const int cl = wl + kGroupWarps * ch;   // in the stage
+                const int chunk = c0 + cl;              // in the row
+                if (!mine || cl >= cps || chunk * SH::CHUNK_K >= K) break;
                 // token operand of the chunk's half h, group j
                 auto load_act = [&](int h, int j, uint4 (&v)[NV]) {
                     const int kk = (2 * chunk + h) * (SH::CHUNK_K / 2) + c * (SH::CHUNK_K / 8);
@@ -755,7 +781,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_experts_kernel(
                 uint4 v0[2][NV];   // group 0
                 if (in_smem) {
                     const uint32_t a = smem_u32(acts + s * SH::ACT) + g * SH::ACT_PITCH +
-                                       warp * (2 * SH::CHUNK_K) + c * (SH::CHUNK_K / 4);
+                                       cl * (2 * SH::CHUNK_K) + c * (SH::CHUNK_K / 4);
 #pragma unroll
                     for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -771,7 +797,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_experts_kernel(
                 uint4 wq[2][2];   // [half][row pr / pr + 8]
                 {
                     const uint32_t a0 =
-                        smem_u32(ring + s * kFewStage) + warp * (8 * kChunk) + pr * kChunk;
+                        smem_u32(ring + s * kFewStage) + cl * (8 * kChunk) + pr * kChunk;
                     const uint32_t b0 = a0 + kFewStage / 2;
                     const uint32_t first = (uint32_t)(c ^ pr) << 4;
                     wq[0][0] = ld_shared_v4(a0 + first);
@@ -841,8 +867,8 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_experts_kernel(
                                         bv[2 * m + 1]);
                         }
                     }
-                    const float f0 = scales[s * 2 * kStageChunks + warp];
-                    const float f1 = scales[(s * 2 + 1) * kStageChunks + warp];
+                    const float f0 = scales[s * 2 * kStageChunks + cl];
+                    const float f1 = scales[(s * 2 + 1) * kStageChunks + cl];
 #pragma unroll
                     for (int j = 0; j < NT; ++j) {
                         acc[j][0] = fmaf(part[j][0][0] + part[j][1][0], f0, acc[j][0]);
@@ -856,7 +882,8 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_experts_kernel(
             if (lane == 0) mbar_arrive(&empty[s]);
             if (++s == STAGES) { s = 0; ph ^= 1u; }
             if (!(q.w & kLast)) continue;
-            // the tile's partial sums, one buffer per group of 8 rows
+            // the tile's partial sums, one buffer per group of 8 rows (zeros where
+            // the other group had all its stages)
             bool ok = true;
 #pragma unroll
             for (int j = 0; j < NT; ++j) {
@@ -918,26 +945,30 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_experts_kernel(
                 }
             }
             __syncwarp();
-            if (!second) {
-                if (lane == 0) {
-                    fence_proxy_async_global();   // copies will read h
-                    red_release_gpu_add(h_done + 1 + q.y, 1);
-                }
-                continue;
+            if (lane == 0) {
+                fence_proxy_async_global();   // copies will read h
+                red_release_gpu_add(second ? y_done + q.x : h_done + 1 + q.y, 1);
             }
-            int old = 0;
-            if (lane == 0) old = atom_add_acq_rel(y_done + q.x, 1);
-            old = __shfl_sync(0xffffffffu, old, 0);
-            __syncwarp();
-            if (old != meta->n_units - 1) continue;
-            // every product of these 16 columns is there
-            for (int i = lane; i < p.T * 16; i += 32) {
-                const int tk = i >> 4, n16 = q.x * 16 + (i & 15);
-                float sum = __ldcg(p.yp + (size_t)(S + tk) * p.d + n16);
-                for (int j = 0; j < p.k; ++j)
-                    sum += __ldcg(p.yp + (size_t)(tk * p.k + j) * p.d + n16);
-                p.y[(size_t)tk * p.d + n16] = (uint16_t)(pack_bf16x2(sum, 0.0f) & 0xFFFFu);
-            }
+        }
+    }
+
+    // The columns of this CTA: every product of a tile's 16 columns is there once
+    // all its items have signalled; they are added up in slot order.
+    __syncthreads();
+    for (int tile = blockIdx.x; tile < tiles2; tile += gridDim.x) {
+        if (threadIdx.x == 0) wait_count_geq(y_done + tile, meta->n_units, wc);
+        __syncthreads();
+        for (int i = threadIdx.x; i < p.T * 16; i += kFewThreads) {
+            const int tk = i >> 4, n16 = tile * 16 + (i & 15);
+            float v[kFewK + 1];
+            v[0] = __ldcg(p.yp + (size_t)(S + tk) * p.d + n16);
+#pragma unroll
+            for (int j = 0; j < kFewK; ++j)
+                v[j + 1] = j < p.k ? __ldcg(p.yp + (size_t)(tk * p.k + j) * p.d + n16) : 0.0f;
+            float sum = v[0];
+#pragma unroll
+            for (int j = 0; j < kFewK; ++j) sum += v[j + 1];
+            p.y[(size_t)tk * p.d + n16] = (uint16_t)(pack_bf16x2(sum, 0.0f) & 0xFFFFu);
         }
     }
 
