@@ -20,8 +20,8 @@
 // warps 32768 fused multiply-adds, two to an instruction; two tensor memory
 // accumulators let the two overlap.
 //
-// One CTA per SM, persistent, 10 warps: warp 0 TMA producer (48 KB a stage,
-// 128-byte swizzle), warp 1 tensor memory owner and MMA issuer, warps 2-9
+// One CTA per SM, persistent, 12 warps: warp 0 TMA producer (48 KB a stage,
+// 128-byte swizzle), warp 1 tensor memory owner and MMA issuer, warps 4-11
 // accumulate (thread = row; two warps per lane quadrant, 128 columns each).
 // Every wait is bounded; on a timeout the CTA records MOE_ERR_TIMEOUT, drains
 // its copies and MMAs, frees tensor memory and returns.
@@ -37,6 +37,7 @@ enum Fp8Mode : int { FP8_ROWS = 0, FP8_FFN1 = 1, FP8_WGRAD = 2 };
 
 struct Fp8Params {
     CUtensorMap tmA;   // A codes: [rows, K] (WGRAD [chunks * M, 128]), boxes 128 x 128
+    CUtensorMap tmO;   // ROWS: out [rows, N] bf16; WGRAD: dW [G * M, N] fp32; boxes 32 x 32
     CUtensorMap tmB;   // B codes: [G * N, K] (WGRAD [chunks * N, 128]), boxes 128 x 256 (FFN1 128)
     const int32_t *offsets;   // [G+1] rows of the groups; WGRAD: their chunks
     const float *sa, *sb;
@@ -55,19 +56,37 @@ struct Fp8Params {
     long long wait_limit;
 };
 
-constexpr int kF8Stages = 4;
 constexpr int kF8BN = 256;
 constexpr int kF8A = 128 * 128;
 constexpr int kF8Stage = kF8A + kF8BN * 128;
 constexpr int kF8Epi = 8;                       // epilogue warps
-constexpr int kF8Threads = 64 + 32 * kF8Epi;
+constexpr int kF8Epi0 = 4;                      // the first of them
+constexpr int kF8Threads = 32 * (kF8Epi0 + kF8Epi);
 constexpr int kF8Bars = 512;
-constexpr int kF8Side = 4096;                   // FFN1: amax exchange; WGRAD: column scales
 constexpr uint32_t kF8Idesc =
     (1u << 4) | ((uint32_t)(kF8BN >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
 
+// Registers: the four warps that copy and issue hand most of theirs to the
+// eight that hold the accumulators (128 a thread, and 64 in flight from tensor
+// memory); 4 x 40 + 8 x 232 is what the block is launched with, 12 x 168.
+constexpr int kF8RegsFew = 40, kF8RegsMany = 232;
+static_assert(4 * kF8RegsFew + 8 * kF8RegsMany <= 12 * 168, "register split");
+
+template <int MODE>
+struct F8Shape {
+    // the weight gradient stages more output and has short contractions
+    static constexpr int STAGES = MODE == FP8_WGRAD ? 3 : 4;
+    // per epilogue warp: output blocks of 32 x 32 on their way out (bf16: one,
+    // fp32: two)
+    static constexpr int OUT = MODE == FP8_ROWS ? 2048 : MODE == FP8_WGRAD ? 2 * 4096 : 0;
+    // FFN1: exchange of the largest |h|; WGRAD: column scales
+    static constexpr int SIDE = MODE == FP8_FFN1 ? 2048 : MODE == FP8_WGRAD ? 4096 : 0;
+    static constexpr int FIXED = STAGES * kF8Stage + kF8Epi * OUT + SIDE;
+};
+
+template <int MODE>
 inline size_t fp8_smem_bytes(int G) {
-    return 1024 + (size_t)kF8Stages * kF8Stage + kF8Side + kF8Bars + 8 * (size_t)(G + 2);
+    return 1024 + (size_t)F8Shape<MODE>::FIXED + kF8Bars + 8 * (size_t)(G + 2);
 }
 
 // D[tmem] (+)= A[smem] B[smem]^T, E4M3 operands (K = 32), fp32 accumulator.
@@ -93,7 +112,8 @@ __device__ __forceinline__ uint64_t pair_f(float lo, float hi) {
     return pair(__float_as_uint(lo), __float_as_uint(hi));
 }
 __device__ __forceinline__ void fma2(uint64_t &acc, uint64_t a, uint64_t b) {
-    asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(acc) : "l"(a), "l"(b));
+    // volatile: stays between the tensor memory loads that it is meant to cover
+    asm volatile("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(acc) : "l"(a), "l"(b));
 }
 __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
     uint64_t r;
@@ -139,23 +159,26 @@ template <int MODE>
 __global__ void __launch_bounds__(kF8Threads, 1) fp8_gemm_kernel(const __grid_constant__ Fp8Params p) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-    uint8_t *side = smem + kF8Stages * kF8Stage;
-    uint64_t *full = reinterpret_cast<uint64_t *>(side + kF8Side);
-    uint64_t *empty = full + kF8Stages;
-    uint64_t *tfull = empty + kF8Stages;   // a block's sums are in accumulator 0 / 1
+    using SH = F8Shape<MODE>;
+    constexpr int STAGES = SH::STAGES;
+    uint8_t *out_s = smem + STAGES * kF8Stage;
+    uint8_t *side = out_s + kF8Epi * SH::OUT;
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + SH::FIXED);
+    uint64_t *empty = full + STAGES;
+    uint64_t *tfull = empty + STAGES;   // a block's sums are in accumulator 0 / 1
     uint64_t *tempty = tfull + 2;          // ... and have been read
     uint64_t *xch = tempty + 2;            // FFN1: both halves' largest |h| are in `side`
     uint64_t *done = xch + 1;
     uint32_t *tmem_base_s = reinterpret_cast<uint32_t *>(done + 1);
     volatile int *abort_s = reinterpret_cast<volatile int *>(tmem_base_s + 1);
-    int *offs = reinterpret_cast<int *>(side + kF8Side + kF8Bars);
+    int *offs = reinterpret_cast<int *>(smem + SH::FIXED + kF8Bars);
     int *mt_start = offs + (p.G + 1);
 
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
-        for (int s = 0; s < kF8Stages; ++s) {
+        for (int s = 0; s < STAGES; ++s) {
             mbar_init(&full[s], 1);
             mbar_init(&empty[s], 1);
         }
@@ -203,11 +226,13 @@ __global__ void __launch_bounds__(kF8Threads, 1) fp8_gemm_kernel(const __grid_co
     const int total =
         (MODE == FP8_WGRAD ? p.G * ((p.M + 127) >> 7) : mt_start[p.G]) * p.n_tiles;
 
+    if (warp < kF8Epi0) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kF8RegsFew));
     if (warp == 0) {
         if (lane == 0) {
-            int last[kF8Stages];
+            int last[STAGES];
 #pragma unroll
-            for (int i = 0; i < kF8Stages; ++i) last[i] = -1;
+            for (int i = 0; i < STAGES; ++i) last[i] = -1;
             uint32_t s = 0, ph = 0;
             bool ok = true;
             for (int t = blockIdx.x; ok && t < total; t += gridDim.x) {
@@ -231,12 +256,12 @@ __global__ void __launch_bounds__(kF8Threads, 1) fp8_gemm_kernel(const __grid_co
                         tma_load_2d(b, &p.tmB, &full[s], kb * 128, ti.g * p.N + ti.nt * kF8BN);
                     }
                     last[s] = (int)ph;
-                    if (++s == kF8Stages) { s = 0; ph ^= 1u; }
+                    if (++s == STAGES) { s = 0; ph ^= 1u; }
                 }
             }
             if (!ok) {
                 // drain the copies still in flight before the CTA exits
-                for (int i = 0; i < kF8Stages; ++i)
+                for (int i = 0; i < STAGES; ++i)
                     if (last[i] >= 0) mbar_wait_teardown(&full[i], (uint32_t)last[i], p.wait_limit);
             }
         }
@@ -260,7 +285,7 @@ __global__ void __launch_bounds__(kF8Threads, 1) fp8_gemm_kernel(const __grid_co
                     umma_commit(&tfull[acc]);
                 }
                 __syncwarp();
-                if (++s == kF8Stages) { s = 0; ph ^= 1u; }
+                if (++s == STAGES) { s = 0; ph ^= 1u; }
             }
         }
         if (!ok) {
@@ -269,10 +294,12 @@ __global__ void __launch_bounds__(kF8Threads, 1) fp8_gemm_kernel(const __grid_co
             __syncwarp();
             mbar_wait_teardown(done, 0, p.wait_limit);
         }
+    }
     } else {
         // ------------------------------------------------ accumulate and finish
-        const int q = warp & 3;            // TMEM lane quadrant
-        const int part = (warp - 2) >> 2;  // its half of the columns
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kF8RegsMany));
+        const int q = warp & 3;                  // TMEM lane quadrant
+        const int part = (warp - kF8Epi0) >> 2;  // its half of the columns
         const int r_local = q * 32 + lane;
         uint32_t blk = 0;
         int it = 0;
@@ -324,7 +351,7 @@ __global__ void __launch_bounds__(kF8Threads, 1) fp8_gemm_kernel(const __grid_co
                 const float f0 = MODE == FP8_WGRAD ? na : na * nb0, f1 = na * nb1;
                 const uint64_t s0 = pair_f(f0, f0);
                 const uint64_t s1 = MODE == FP8_FFN1 ? pair_f(f1, f1) : s0;
-                float *cs = reinterpret_cast<float *>(side) + (warp - 2) * 128;
+                float *cs = reinterpret_cast<float *>(side) + (warp - kF8Epi0) * 128;
                 if constexpr (MODE == FP8_WGRAD) {
                     __syncwarp();
                     *reinterpret_cast<float4 *>(cs + 4 * lane) = ncol;
@@ -335,22 +362,25 @@ __global__ void __launch_bounds__(kF8Threads, 1) fp8_gemm_kernel(const __grid_co
                 if (!mbar_wait_warp(&tfull[a], (blk >> 1) & 1u, wc)) { ok = false; break; }
                 tc_fence_after();
                 const uint32_t tb = tmem_base + ((uint32_t)(q * 32) << 16) + a * kF8BN + cl0;
+                // 32 columns at a time, the next ones on their way meanwhile
+                uint32_t r[2][32];
+                tmem_ld32(tb, r[0]);
+                tmem_wait_ld();
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
-                    uint32_t r[32];
-                    tmem_ld32(tb + (c >> 1) * kHalf + (c & 1) * 32, r);
-                    tmem_wait_ld();
-                    if (c == 3) {
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&tempty[a]);
-                    }
+                    if (c < 3) tmem_ld32(tb + ((c + 1) >> 1) * kHalf + ((c + 1) & 1) * 32, r[(c + 1) & 1]);
 #pragma unroll
                     for (int j = 0; j < 16; ++j) {
-                        uint64_t v = pair(r[2 * j], r[2 * j + 1]);
+                        uint64_t v = pair(r[c & 1][2 * j], r[c & 1][2 * j + 1]);
                         if constexpr (MODE == FP8_WGRAD)
                             v = mul2(v, *reinterpret_cast<const uint64_t *>(cs + c * 32 + 2 * j));
                         fma2(acc[c * 16 + j], v, c < 2 ? s0 : s1);
+                    }
+                    if (c < 3) tmem_wait_ld();
+                    if (c == 2) {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&tempty[a]);
                     }
                 }
             }
@@ -358,29 +388,78 @@ __global__ void __launch_bounds__(kF8Threads, 1) fp8_gemm_kernel(const __grid_co
             if constexpr (MODE == FP8_ROWS) {
                 float w = 1.0f;
                 if (valid && p.row_w && row < p.w_rows) w = p.row_w[row];
-                const int col = ti.nt * kF8BN + cl0;
-                uint16_t *dst = p.out + (size_t)row * p.N + col;
-                if (valid) {
+                // a warp whose 32 rows all exist writes 32 x 32 blocks through
+                // shared memory and TMA (whole sectors); a ragged one must not
+                // touch the next group's rows
+                const int col0 = ti.nt * kF8BN + cl0;
+                const bool whole = q * 32 + 32 <= ti.rows;
+                uint8_t *stg = out_s + (warp - kF8Epi0) * SH::OUT;
+                const uint32_t sa_row = smem_u32(stg) + lane * 64;
+                uint16_t *dst = p.out + (size_t)row * p.N + col0;
 #pragma unroll
-                    for (int j = 0; j < 16; ++j)
-                        if (col + 8 * j < p.N)
-                            st_global_v4(
-                                dst + 8 * j,
-                                pack_bf16x2(w * lo_f(acc[4 * j]), w * hi_f(acc[4 * j])),
-                                pack_bf16x2(w * lo_f(acc[4 * j + 1]), w * hi_f(acc[4 * j + 1])),
-                                pack_bf16x2(w * lo_f(acc[4 * j + 2]), w * hi_f(acc[4 * j + 2])),
-                                pack_bf16x2(w * lo_f(acc[4 * j + 3]), w * hi_f(acc[4 * j + 3])));
+                for (int b = 0; b < 4; ++b) {
+                    if (col0 + 32 * b >= p.N) break;
+                    if (whole) {
+                        if (lane == 0) bulk_wait_group_read<0>();
+                        __syncwarp();
+                    }
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        uint32_t w4[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const uint64_t v = acc[16 * b + 4 * j + e];
+                            w4[e] = pack_bf16x2(w * lo_f(v), w * hi_f(v));
+                        }
+                        if (whole)
+                            st_shared_v4(sa_row + (((uint32_t)j ^ ((lane >> 1) & 3u)) << 4), w4[0],
+                                         w4[1], w4[2], w4[3]);
+                        else if (valid && col0 + 32 * b + 8 * j < p.N)
+                            st_global_v4(dst + 32 * b + 8 * j, w4[0], w4[1], w4[2], w4[3]);
+                    }
+                    if (whole) {
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) {
+                            tma_store_2d(&p.tmO, stg, col0 + 32 * b, ti.row0 + q * 32);
+                            bulk_commit_group();
+                        }
+                    }
                 }
             } else if constexpr (MODE == FP8_WGRAD) {
-                const int col = ti.nt * kF8BN + cl0;
-                float *dst = p.dW + ((size_t)ti.g * p.M + row) * p.N + col;
-                if (valid) {
+                const int col0 = ti.nt * kF8BN + cl0;
+                const bool whole = q * 32 + 32 <= ti.rows;
+                uint8_t *stg = out_s + (warp - kF8Epi0) * SH::OUT;
+                float *dst = p.dW + ((size_t)ti.g * p.M + row) * p.N + col0;
 #pragma unroll
-                    for (int j = 0; j < 32; ++j)
-                        if (col + 4 * j < p.N)
-                            st_global_v4(dst + 4 * j, (uint32_t)acc[2 * j],
-                                         (uint32_t)(acc[2 * j] >> 32), (uint32_t)acc[2 * j + 1],
-                                         (uint32_t)(acc[2 * j + 1] >> 32));
+                for (int b = 0; b < 4; ++b) {
+                    if (col0 + 32 * b >= p.N) break;
+                    uint8_t *blk = stg + (b & 1) * 4096;
+                    if (whole) {
+                        if (lane == 0) bulk_wait_group_read<1>();
+                        __syncwarp();
+                    }
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const uint64_t v0 = acc[16 * b + 2 * j], v1 = acc[16 * b + 2 * j + 1];
+                        if (whole)
+                            st_shared_v4(smem_u32(blk) + lane * 128 +
+                                             (((uint32_t)j ^ (lane & 7u)) << 4),
+                                         (uint32_t)v0, (uint32_t)(v0 >> 32), (uint32_t)v1,
+                                         (uint32_t)(v1 >> 32));
+                        else if (valid && col0 + 32 * b + 4 * j < p.N)
+                            st_global_v4(dst + 32 * b + 4 * j, (uint32_t)v0, (uint32_t)(v0 >> 32),
+                                         (uint32_t)v1, (uint32_t)(v1 >> 32));
+                    }
+                    if (whole) {
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) {
+                            tma_store_2d(&p.tmO, blk, col0 + 32 * b,
+                                         ti.g * p.M + ti.row0 + q * 32);
+                            bulk_commit_group();
+                        }
+                    }
                 }
             } else {
                 // 64 h columns; the other half of the block's 128 is with the
@@ -419,6 +498,8 @@ __global__ void __launch_bounds__(kF8Threads, 1) fp8_gemm_kernel(const __grid_co
                 }
             }
         }
+        // the output blocks have left shared memory (and landed) before the exit
+        if (MODE != FP8_FFN1 && lane == 0) bulk_wait_group_all();
     }
 
     tc_fence_before();
@@ -436,7 +517,7 @@ moe_status launch_fp8(Fp8Params &p, long long max_tiles, cudaStream_t st) {
     if (dev < 0 || dev >= 64) return MOE_ERR_UNSUPPORTED;
     if (!attr_set[dev]) {
         if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 (int)fp8_smem_bytes(kMaxGroups)) != cudaSuccess)
+                                 (int)fp8_smem_bytes<MODE>(kMaxGroups)) != cudaSuccess)
             return MOE_ERR_CUDA;
         attr_set[dev] = true;
     }
@@ -445,7 +526,7 @@ moe_status launch_fp8(Fp8Params &p, long long max_tiles, cudaStream_t st) {
     if (!p.status) return MOE_ERR_CUDA;
     p.wait_limit = kWaitLimitCycles;
     const int grid = max_tiles < num_sms() ? (int)max_tiles : num_sms();
-    kern<<<grid, kF8Threads, fp8_smem_bytes(p.G), st>>>(p);
+    kern<<<grid, kF8Threads, fp8_smem_bytes<MODE>(p.G), st>>>(p);
     return cuda_status(cudaGetLastError());
 }
 
@@ -457,7 +538,8 @@ moe_status launch_fp8_matmul(const uint8_t *aq, const float *as, const int32_t *
     Fp8Params p;
     std::memset(&p, 0, sizeof p);
     if (!encode_tmap_u8_2d(&p.tmA, aq, K, max_rows, K, 128, 128, 128) ||
-        !encode_tmap_u8_2d(&p.tmB, bq, K, (uint64_t)G * N, K, 128, kF8BN, 128))
+        !encode_tmap_u8_2d(&p.tmB, bq, K, (uint64_t)G * N, K, 128, kF8BN, 128) ||
+        !encode_tmap_bf16_2d_sw64(&p.tmO, out, N, max_rows, (uint64_t)N * 2, 32, 32))
         return MOE_ERR_CUDA;
     p.offsets = offsets;
     p.sa = as;
@@ -502,7 +584,8 @@ moe_status launch_fp8_wgrad(const uint8_t *aq, const float *as, const uint8_t *b
     Fp8Params p;
     std::memset(&p, 0, sizeof p);
     if (!encode_tmap_u8_2d(&p.tmA, aq, 128, (uint64_t)max_chunks * M, 128, 128, 128, 128) ||
-        !encode_tmap_u8_2d(&p.tmB, bq, 128, (uint64_t)max_chunks * N, 128, 128, kF8BN, 128))
+        !encode_tmap_u8_2d(&p.tmB, bq, 128, (uint64_t)max_chunks * N, 128, 128, kF8BN, 128) ||
+        !encode_tmap_f32_2d(&p.tmO, dW, N, (uint64_t)G * M, (uint64_t)N * 4, 32, 32))
         return MOE_ERR_CUDA;
     p.offsets = first;
     p.sa = as;
