@@ -52,6 +52,7 @@ struct Fp8Params {
     uint8_t *hq;              // FFN1: h codes [rows, I] ...
     float *hs;                //       ... and scales [rows, I / 128]
     float *dW;                // WGRAD
+    int out_bufs;             // output blocks of an epilogue warp
     int *status;
     long long wait_limit;
 };
@@ -76,17 +77,23 @@ template <int MODE>
 struct F8Shape {
     // the weight gradient stages more output and has short contractions
     static constexpr int STAGES = MODE == FP8_WGRAD ? 3 : 4;
-    // per epilogue warp: output blocks of 32 x 32 on their way out (bf16: one,
-    // fp32: two)
-    static constexpr int OUT = MODE == FP8_ROWS ? 2048 : MODE == FP8_WGRAD ? 2 * 4096 : 0;
+    // an output block of 32 x 32 on its way out; every epilogue warp has two (one
+    // where the offsets of many groups need the room)
+    static constexpr int OUT = MODE == FP8_ROWS ? 2048 : MODE == FP8_WGRAD ? 4096 : 0;
     // FFN1: exchange of the largest |h|; WGRAD: column scales
     static constexpr int SIDE = MODE == FP8_FFN1 ? 2048 : MODE == FP8_WGRAD ? 4096 : 0;
-    static constexpr int FIXED = STAGES * kF8Stage + kF8Epi * OUT + SIDE;
+    static constexpr int FIXED = STAGES * kF8Stage + SIDE;
 };
+constexpr int kF8Smem = 232448;   // shared memory that a CTA can have
 
 template <int MODE>
-inline size_t fp8_smem_bytes(int G) {
-    return 1024 + (size_t)F8Shape<MODE>::FIXED + kF8Bars + 8 * (size_t)(G + 2);
+inline int fp8_smem_bytes(int G, int out_bufs) {
+    return 1024 + F8Shape<MODE>::FIXED + kF8Epi * F8Shape<MODE>::OUT * out_bufs + kF8Bars +
+           8 * (G + 2);
+}
+template <int MODE>
+inline int fp8_out_bufs(int G) {
+    return fp8_smem_bytes<MODE>(G, 2) <= kF8Smem ? 2 : 1;
 }
 
 // D[tmem] (+)= A[smem] B[smem]^T, E4M3 operands (K = 32), fp32 accumulator.
@@ -161,9 +168,10 @@ __global__ void __launch_bounds__(kF8Threads, 1) fp8_gemm_kernel(const __grid_co
     uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     using SH = F8Shape<MODE>;
     constexpr int STAGES = SH::STAGES;
-    uint8_t *out_s = smem + STAGES * kF8Stage;
-    uint8_t *side = out_s + kF8Epi * SH::OUT;
-    uint64_t *full = reinterpret_cast<uint64_t *>(smem + SH::FIXED);
+    uint8_t *side = smem + STAGES * kF8Stage;
+    uint8_t *out_s = smem + SH::FIXED;
+    uint8_t *fixed_end = out_s + kF8Epi * SH::OUT * p.out_bufs;
+    uint64_t *full = reinterpret_cast<uint64_t *>(fixed_end);
     uint64_t *empty = full + STAGES;
     uint64_t *tfull = empty + STAGES;   // a block's sums are in accumulator 0 / 1
     uint64_t *tempty = tfull + 2;          // ... and have been read
@@ -171,7 +179,7 @@ __global__ void __launch_bounds__(kF8Threads, 1) fp8_gemm_kernel(const __grid_co
     uint64_t *done = xch + 1;
     uint32_t *tmem_base_s = reinterpret_cast<uint32_t *>(done + 1);
     volatile int *abort_s = reinterpret_cast<volatile int *>(tmem_base_s + 1);
-    int *offs = reinterpret_cast<int *>(smem + SH::FIXED + kF8Bars);
+    int *offs = reinterpret_cast<int *>(fixed_end + kF8Bars);
     int *mt_start = offs + (p.G + 1);
 
     const int warp = threadIdx.x >> 5;
@@ -347,6 +355,16 @@ __global__ void __launch_bounds__(kF8Threads, 1) fp8_gemm_kernel(const __grid_co
             uint64_t acc[64];
 #pragma unroll
             for (int j = 0; j < 64; ++j) acc[j] = 0;
+            // 32 columns at a time, the next ones (also those of the next block) on
+            // their way from tensor memory during the products
+            uint32_t r[2][32];
+            const uint32_t tq = tmem_base + ((uint32_t)(q * 32) << 16) + cl0;
+            if (ti.kb > 0) {
+                ok = mbar_wait_warp(&tfull[blk & 1u], (blk >> 1) & 1u, wc);
+                if (!ok) break;
+                tc_fence_after();
+                tmem_ld32(tq + (blk & 1u) * kF8BN, r[0]);
+            }
             for (int kb = 0; kb < ti.kb; ++kb, ++blk) {
                 const float f0 = MODE == FP8_WGRAD ? na : na * nb0, f1 = na * nb1;
                 const uint64_t s0 = pair_f(f0, f0);
@@ -359,16 +377,23 @@ __global__ void __launch_bounds__(kF8Threads, 1) fp8_gemm_kernel(const __grid_co
                 }
                 if (kb + 1 < ti.kb) next_scales(kb + 1);
                 const uint32_t a = blk & 1u;
-                if (!mbar_wait_warp(&tfull[a], (blk >> 1) & 1u, wc)) { ok = false; break; }
-                tc_fence_after();
-                const uint32_t tb = tmem_base + ((uint32_t)(q * 32) << 16) + a * kF8BN + cl0;
-                // 32 columns at a time, the next ones on their way meanwhile
-                uint32_t r[2][32];
-                tmem_ld32(tb, r[0]);
-                tmem_wait_ld();
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
-                    if (c < 3) tmem_ld32(tb + ((c + 1) >> 1) * kHalf + ((c + 1) & 1) * 32, r[(c + 1) & 1]);
+                    tmem_wait_ld();
+                    if (c < 3) {
+                        tmem_ld32(tq + a * kF8BN + ((c + 1) >> 1) * kHalf + ((c + 1) & 1) * 32,
+                                  r[(c + 1) & 1]);
+                    } else {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&tempty[a]);
+                        if (kb + 1 < ti.kb) {
+                            ok = mbar_wait_warp(&tfull[a ^ 1u], ((blk + 1) >> 1) & 1u, wc);
+                            if (!ok) break;
+                            tc_fence_after();
+                            tmem_ld32(tq + (a ^ 1u) * kF8BN, r[0]);
+                        }
+                    }
 #pragma unroll
                     for (int j = 0; j < 16; ++j) {
                         uint64_t v = pair(r[c & 1][2 * j], r[c & 1][2 * j + 1]);
@@ -376,13 +401,8 @@ __global__ void __launch_bounds__(kF8Threads, 1) fp8_gemm_kernel(const __grid_co
                             v = mul2(v, *reinterpret_cast<const uint64_t *>(cs + c * 32 + 2 * j));
                         fma2(acc[c * 16 + j], v, c < 2 ? s0 : s1);
                     }
-                    if (c < 3) tmem_wait_ld();
-                    if (c == 2) {
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&tempty[a]);
-                    }
                 }
+                if (!ok) break;
             }
             if (!ok) break;
             if constexpr (MODE == FP8_ROWS) {
@@ -393,14 +413,17 @@ __global__ void __launch_bounds__(kF8Threads, 1) fp8_gemm_kernel(const __grid_co
                 // touch the next group's rows
                 const int col0 = ti.nt * kF8BN + cl0;
                 const bool whole = q * 32 + 32 <= ti.rows;
-                uint8_t *stg = out_s + (warp - kF8Epi0) * SH::OUT;
-                const uint32_t sa_row = smem_u32(stg) + lane * 64;
+                uint8_t *stg = out_s + (warp - kF8Epi0) * SH::OUT * p.out_bufs;
                 uint16_t *dst = p.out + (size_t)row * p.N + col0;
 #pragma unroll
                 for (int b = 0; b < 4; ++b) {
                     if (col0 + 32 * b >= p.N) break;
+                    uint8_t *blk_s = stg + (b & (p.out_bufs - 1)) * SH::OUT;
                     if (whole) {
-                        if (lane == 0) bulk_wait_group_read<0>();
+                        if (lane == 0) {
+                            if (p.out_bufs == 2) bulk_wait_group_read<1>();
+                            else bulk_wait_group_read<0>();
+                        }
                         __syncwarp();
                     }
 #pragma unroll
@@ -412,8 +435,9 @@ __global__ void __launch_bounds__(kF8Threads, 1) fp8_gemm_kernel(const __grid_co
                             w4[e] = pack_bf16x2(w * lo_f(v), w * hi_f(v));
                         }
                         if (whole)
-                            st_shared_v4(sa_row + (((uint32_t)j ^ ((lane >> 1) & 3u)) << 4), w4[0],
-                                         w4[1], w4[2], w4[3]);
+                            st_shared_v4(smem_u32(blk_s) + lane * 64 +
+                                             (((uint32_t)j ^ ((lane >> 1) & 3u)) << 4),
+                                         w4[0], w4[1], w4[2], w4[3]);
                         else if (valid && col0 + 32 * b + 8 * j < p.N)
                             st_global_v4(dst + 32 * b + 8 * j, w4[0], w4[1], w4[2], w4[3]);
                     }
@@ -421,7 +445,7 @@ __global__ void __launch_bounds__(kF8Threads, 1) fp8_gemm_kernel(const __grid_co
                         fence_proxy_async_smem();
                         __syncwarp();
                         if (lane == 0) {
-                            tma_store_2d(&p.tmO, stg, col0 + 32 * b, ti.row0 + q * 32);
+                            tma_store_2d(&p.tmO, blk_s, col0 + 32 * b, ti.row0 + q * 32);
                             bulk_commit_group();
                         }
                     }
@@ -429,14 +453,17 @@ __global__ void __launch_bounds__(kF8Threads, 1) fp8_gemm_kernel(const __grid_co
             } else if constexpr (MODE == FP8_WGRAD) {
                 const int col0 = ti.nt * kF8BN + cl0;
                 const bool whole = q * 32 + 32 <= ti.rows;
-                uint8_t *stg = out_s + (warp - kF8Epi0) * SH::OUT;
+                uint8_t *stg = out_s + (warp - kF8Epi0) * SH::OUT * p.out_bufs;
                 float *dst = p.dW + ((size_t)ti.g * p.M + row) * p.N + col0;
 #pragma unroll
                 for (int b = 0; b < 4; ++b) {
                     if (col0 + 32 * b >= p.N) break;
-                    uint8_t *blk = stg + (b & 1) * 4096;
+                    uint8_t *blk = stg + (b & (p.out_bufs - 1)) * SH::OUT;
                     if (whole) {
-                        if (lane == 0) bulk_wait_group_read<1>();
+                        if (lane == 0) {
+                            if (p.out_bufs == 2) bulk_wait_group_read<1>();
+                            else bulk_wait_group_read<0>();
+                        }
                         __syncwarp();
                     }
 #pragma unroll
@@ -517,7 +544,7 @@ moe_status launch_fp8(Fp8Params &p, long long max_tiles, cudaStream_t st) {
     if (dev < 0 || dev >= 64) return MOE_ERR_UNSUPPORTED;
     if (!attr_set[dev]) {
         if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 (int)fp8_smem_bytes<MODE>(kMaxGroups)) != cudaSuccess)
+                                 kF8Smem) != cudaSuccess)
             return MOE_ERR_CUDA;
         attr_set[dev] = true;
     }
@@ -526,7 +553,10 @@ moe_status launch_fp8(Fp8Params &p, long long max_tiles, cudaStream_t st) {
     if (!p.status) return MOE_ERR_CUDA;
     p.wait_limit = kWaitLimitCycles;
     const int grid = max_tiles < num_sms() ? (int)max_tiles : num_sms();
-    kern<<<grid, kF8Threads, fp8_smem_bytes<MODE>(p.G), st>>>(p);
+    p.out_bufs = fp8_out_bufs<MODE>(p.G);
+    const int smem = fp8_smem_bytes<MODE>(p.G, p.out_bufs);
+    if (smem > kF8Smem) return MOE_ERR_UNSUPPORTED;
+    kern<<<grid, kF8Threads, smem, st>>>(p);
     return cuda_status(cudaGetLastError());
 }
 
