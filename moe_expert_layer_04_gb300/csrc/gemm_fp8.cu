@@ -57,15 +57,11 @@ struct Fp8Params {
     long long wait_limit;
 };
 
-constexpr int kF8BN = 256;
 constexpr int kF8A = 128 * 128;
-constexpr int kF8Stage = kF8A + kF8BN * 128;
 constexpr int kF8Epi = 8;                       // epilogue warps
 constexpr int kF8Epi0 = 4;                      // the first of them
 constexpr int kF8Threads = 32 * (kF8Epi0 + kF8Epi);
 constexpr int kF8Bars = 512;
-constexpr uint32_t kF8Idesc =
-    (1u << 4) | ((uint32_t)(kF8BN >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
 
 // Registers: the four warps that copy and issue hand most of theirs to the
 // eight that hold the accumulators (128 a thread, and 64 in flight from tensor
@@ -73,27 +69,33 @@ constexpr uint32_t kF8Idesc =
 constexpr int kF8RegsFew = 40, kF8RegsMany = 232;
 static_assert(4 * kF8RegsFew + 8 * kF8RegsMany <= 12 * 168, "register split");
 
-template <int MODE>
+template <int MODE, int BN>
 struct F8Shape {
-    // the weight gradient stages more output and has short contractions
-    static constexpr int STAGES = MODE == FP8_WGRAD ? 3 : 4;
+    static constexpr int STAGE = kF8A + BN * 128;
+    static constexpr int NACC = 512 / BN;            // accumulators in tensor memory
+    static constexpr int CW = BN / 2;                // columns of an epilogue warp
+    static constexpr int CH = MODE == FP8_WGRAD ? 16 : 32;   // of them in flight at a time
+    static constexpr uint32_t IDESC =
+        (1u << 4) | ((uint32_t)(BN >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
+    static constexpr int STAGES = BN == 256 ? 4 : MODE == FP8_WGRAD ? 4 : 6;
     // an output block of 32 x 32 on its way out; every epilogue warp has two (one
     // where the offsets of many groups need the room)
     static constexpr int OUT = MODE == FP8_ROWS ? 2048 : MODE == FP8_WGRAD ? 4096 : 0;
     // FFN1: exchange of the largest |h|; WGRAD: column scales
-    static constexpr int SIDE = MODE == FP8_FFN1 ? 2048 : MODE == FP8_WGRAD ? 4096 : 0;
-    static constexpr int FIXED = STAGES * kF8Stage + SIDE;
+    static constexpr int SIDE = MODE == FP8_FFN1 ? 2048 : MODE == FP8_WGRAD ? kF8Epi * CW * 4 : 0;
+    static constexpr int FIXED = STAGES * STAGE + SIDE;
 };
 constexpr int kF8Smem = 232448;   // shared memory that a CTA can have
 
-template <int MODE>
+template <int MODE, int BN>
 inline int fp8_smem_bytes(int G, int out_bufs) {
-    return 1024 + F8Shape<MODE>::FIXED + kF8Epi * F8Shape<MODE>::OUT * out_bufs + kF8Bars +
+    using SH = F8Shape<MODE, BN>;
+    return 1024 + SH::FIXED + kF8Epi * SH::OUT * out_bufs + kF8Bars +
            8 * (G + 2);
 }
-template <int MODE>
+template <int MODE, int BN>
 inline int fp8_out_bufs(int G) {
-    return fp8_smem_bytes<MODE>(G, 2) <= kF8Smem ? 2 : 1;
+    return fp8_smem_bytes<MODE, BN>(G, 2) <= kF8Smem ? 2 : 1;
 }
 
 // D[tmem] (+)= A[smem] B[smem]^T, E4M3 operands (K = 32), fp32 accumulator.
@@ -106,6 +108,18 @@ __device__ __forceinline__ void umma_f8(uint32_t d_tmem, uint64_t a_desc, uint64
         "setp.ne.b32 p, %4, 0;\n\t"
         "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
         "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[32]) { tmem_ld32(taddr, r); }
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
+          "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr)
         : "memory");
 }
 
@@ -162,20 +176,20 @@ __device__ __forceinline__ F8Tile f8_tile(const Fp8Params &p, int t, const int *
     return ti;
 }
 
-template <int MODE>
+template <int MODE, int BN>
 __global__ void __launch_bounds__(kF8Threads, 1) fp8_gemm_kernel(const __grid_constant__ Fp8Params p) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-    using SH = F8Shape<MODE>;
-    constexpr int STAGES = SH::STAGES;
-    uint8_t *side = smem + STAGES * kF8Stage;
+    using SH = F8Shape<MODE, BN>;
+    constexpr int STAGES = SH::STAGES, NACC = SH::NACC, CW = SH::CW, CH = SH::CH;
+    uint8_t *side = smem + STAGES * SH::STAGE;
     uint8_t *out_s = smem + SH::FIXED;
     uint8_t *fixed_end = out_s + kF8Epi * SH::OUT * p.out_bufs;
     uint64_t *full = reinterpret_cast<uint64_t *>(fixed_end);
     uint64_t *empty = full + STAGES;
-    uint64_t *tfull = empty + STAGES;   // a block's sums are in accumulator 0 / 1
-    uint64_t *tempty = tfull + 2;          // ... and have been read
-    uint64_t *xch = tempty + 2;            // FFN1: both halves' largest |h| are in `side`
+    uint64_t *tfull = empty + STAGES;   // a block's sums are in an accumulator
+    uint64_t *tempty = tfull + NACC;          // ... and have been read
+    uint64_t *xch = tempty + NACC;            // FFN1: both halves' largest |h| are in `side`
     uint64_t *done = xch + 1;
     uint32_t *tmem_base_s = reinterpret_cast<uint32_t *>(done + 1);
     volatile int *abort_s = reinterpret_cast<volatile int *>(tmem_base_s + 1);
@@ -190,7 +204,7 @@ __global__ void __launch_bounds__(kF8Threads, 1) fp8_gemm_kernel(const __grid_co
             mbar_init(&full[s], 1);
             mbar_init(&empty[s], 1);
         }
-        for (int a = 0; a < 2; ++a) {
+        for (int a = 0; a < NACC; ++a) {
             mbar_init(&tfull[a], 1);
             mbar_init(&tempty[a], kF8Epi);
         }
@@ -204,7 +218,7 @@ __global__ void __launch_bounds__(kF8Threads, 1) fp8_gemm_kernel(const __grid_co
         tma_prefetch_desc(&p.tmB);
     }
     if (warp == 1) {
-        tmem_alloc(tmem_base_s, 2 * kF8BN);
+        tmem_alloc(tmem_base_s, NACC * BN);
         tmem_relinquish();
     }
     if (warp == 2) {
@@ -247,13 +261,13 @@ __global__ void __launch_bounds__(kF8Threads, 1) fp8_gemm_kernel(const __grid_co
                 const F8Tile ti = f8_tile<MODE>(p, t, mt_start, offs);
                 for (int kb = 0; kb < ti.kb; ++kb) {
                     if (!mbar_wait(&empty[s], ph ^ 1u, wc)) { ok = false; break; }
-                    mbar_arrive_expect_tx(&full[s], kF8Stage);
-                    uint8_t *a = smem + s * kF8Stage;
+                    mbar_arrive_expect_tx(&full[s], SH::STAGE);
+                    uint8_t *a = smem + s * SH::STAGE;
                     uint8_t *b = a + kF8A;
                     if constexpr (MODE == FP8_WGRAD) {
                         const int c = ti.k0 + kb;
                         tma_load_2d(a, &p.tmA, &full[s], 0, c * p.M + ti.row0);
-                        tma_load_2d(b, &p.tmB, &full[s], 0, c * p.N + ti.nt * kF8BN);
+                        tma_load_2d(b, &p.tmB, &full[s], 0, c * p.N + ti.nt * BN);
                     } else if constexpr (MODE == FP8_FFN1) {
                         const int br = ti.g * 2 * p.I + ti.nt * 128;
                         tma_load_2d(a, &p.tmA, &full[s], kb * 128, ti.row0);
@@ -261,7 +275,7 @@ __global__ void __launch_bounds__(kF8Threads, 1) fp8_gemm_kernel(const __grid_co
                         tma_load_2d(b + 128 * 128, &p.tmB, &full[s], kb * 128, br + p.I);
                     } else {
                         tma_load_2d(a, &p.tmA, &full[s], kb * 128, ti.row0);
-                        tma_load_2d(b, &p.tmB, &full[s], kb * 128, ti.g * p.N + ti.nt * kF8BN);
+                        tma_load_2d(b, &p.tmB, &full[s], kb * 128, ti.g * p.N + ti.nt * BN);
                     }
                     last[s] = (int)ph;
                     if (++s == STAGES) { s = 0; ph ^= 1u; }
@@ -279,16 +293,16 @@ __global__ void __launch_bounds__(kF8Threads, 1) fp8_gemm_kernel(const __grid_co
         for (int t = blockIdx.x; ok && t < total; t += gridDim.x) {
             const F8Tile ti = f8_tile<MODE>(p, t, mt_start, offs);
             for (int kb = 0; kb < ti.kb; ++kb, ++blk) {
-                const uint32_t acc = blk & 1u, aph = (blk >> 1) & 1u;
+                const uint32_t acc = blk % NACC, aph = (blk / NACC) & 1u;
                 if (!mbar_wait_warp(&tempty[acc], aph ^ 1u, wc)) { ok = false; break; }
                 if (!mbar_wait_warp(&full[s], ph, wc)) { ok = false; break; }
                 tc_fence_after();
                 if (lane == 0) {
-                    const uint32_t a = smem_u32(smem + s * kF8Stage), b = a + kF8A;
+                    const uint32_t a = smem_u32(smem + s * SH::STAGE), b = a + kF8A;
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk)
-                        umma_f8(tmem_base + acc * kF8BN, sdesc_sw128(a + kk * 32, 16, 1024),
-                                sdesc_sw128(b + kk * 32, 16, 1024), kF8Idesc, kk ? 1u : 0u);
+                        umma_f8(tmem_base + acc * BN, sdesc_sw128(a + kk * 32, 16, 1024),
+                                sdesc_sw128(b + kk * 32, 16, 1024), SH::IDESC, kk ? 1u : 0u);
                     umma_commit(&empty[s]);
                     umma_commit(&tfull[acc]);
                 }
@@ -312,22 +326,36 @@ __global__ void __launch_bounds__(kF8Threads, 1) fp8_gemm_kernel(const __grid_co
         uint32_t blk = 0;
         int it = 0;
         bool ok = true;
-        for (int t = blockIdx.x; ok && t < total; t += gridDim.x, ++it) {
-            const F8Tile ti = f8_tile<MODE>(p, t, mt_start, offs);
-            const bool valid = r_local < ti.rows;
+        // this thread's columns of a tile: CW from cl0, or for FFN1 64 gate
+        // columns from 64 part and the 64 up columns 128 further on
+        const int cl0 = MODE == FP8_FFN1 ? 64 * part : CW * part;
+        constexpr int kHalf = MODE == FP8_FFN1 ? 128 : CW / 2;   // column step between halves
+        // scales of the tile; the next block's are loaded a block ahead, a tile's
+        // first ones (and its row weight) before the tile before it is written
+        const float *sa = nullptr, *sb0 = nullptr, *sb1 = nullptr;
+        int sa_step = 1;
+        bool col_ok = false, valid = false;
+        float na = 0.0f, nb0 = 0.0f, nb1 = 0.0f, nw = 1.0f;
+        float4 ncol = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        auto next_scales = [&](int kb) {
+            if (valid) na = __ldg(sa + (size_t)kb * sa_step);
+            if constexpr (MODE == FP8_WGRAD) {
+                if (col_ok) ncol = __ldg(reinterpret_cast<const float4 *>(sb0 + (size_t)kb * p.N));
+            } else {
+                nb0 = __ldg(sb0 + kb);
+                if constexpr (MODE == FP8_FFN1) nb1 = __ldg(sb1 + kb);
+            }
+        };
+        F8Tile ti{};
+        auto begin_tile = [&](int t) {
+            ti = f8_tile<MODE>(p, t, mt_start, offs);
+            valid = r_local < ti.rows;
             const int row = ti.row0 + r_local;
-            // this thread's columns of the tile: 128 from cl0, or for FFN1 64
-            // gate columns from 64 part and the 64 up columns 128 further on
-            const int cl0 = MODE == FP8_FFN1 ? 64 * part : 128 * part;
-            constexpr int kHalf = MODE == FP8_FFN1 ? 128 : 64;   // column step between halves
-            const float *sa = nullptr, *sb0 = nullptr, *sb1 = nullptr;
-            int sa_step = 1;
-            bool col_ok = false;
             if constexpr (MODE == FP8_WGRAD) {
                 sa = p.sa + (size_t)ti.k0 * p.M + row;
                 sa_step = p.M;
-                const int col = ti.nt * kF8BN + cl0 + 4 * lane;
-                col_ok = col < p.N;
+                const int col = ti.nt * BN + cl0 + 4 * lane;
+                col_ok = 4 * lane < CW && col < p.N;
                 sb0 = p.sb + (size_t)ti.k0 * p.N + col;
             } else if constexpr (MODE == FP8_FFN1) {
                 sa = p.sa + (size_t)row * p.K_blocks;
@@ -335,88 +363,98 @@ __global__ void __launch_bounds__(kF8Threads, 1) fp8_gemm_kernel(const __grid_co
                 sb1 = sb0 + (size_t)(p.I / 128) * p.K_blocks;
             } else {
                 sa = p.sa + (size_t)row * p.K_blocks;
-                const int nb = ti.nt * 2 + part;
+                const int nb = (ti.nt * BN + cl0) / kFp8Block;
                 sb0 = p.sb + ((size_t)ti.g * p.nb_n + min(nb, p.nb_n - 1)) * p.K_blocks;
+                nw = valid && p.row_w && row < p.w_rows ? __ldg(p.row_w + row) : 1.0f;
             }
-            // the next block's scales are loaded a block ahead
-            float na = 0.0f, nb0 = 0.0f, nb1 = 0.0f;
-            float4 ncol = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            auto next_scales = [&](int kb) {
-                if (valid) na = __ldg(sa + (size_t)kb * sa_step);
-                if constexpr (MODE == FP8_WGRAD) {
-                    if (col_ok)
-                        ncol = __ldg(reinterpret_cast<const float4 *>(sb0 + (size_t)kb * p.N));
-                } else {
-                    nb0 = __ldg(sb0 + kb);
-                    if constexpr (MODE == FP8_FFN1) nb1 = __ldg(sb1 + kb);
-                }
-            };
             if (ti.kb > 0) next_scales(0);
-            uint64_t acc[64];
+        };
+        if ((int)blockIdx.x < total) begin_tile(blockIdx.x);
+        for (int t = blockIdx.x; ok && t < total; t += gridDim.x, ++it) {
+            uint64_t acc[CW / 2];
 #pragma unroll
-            for (int j = 0; j < 64; ++j) acc[j] = 0;
-            // 32 columns at a time, the next ones (also those of the next block) on
+            for (int j = 0; j < CW / 2; ++j) acc[j] = 0;
+            // CH columns at a time, the next ones (also those of the next block) on
             // their way from tensor memory during the products
-            uint32_t r[2][32];
+            constexpr int NCH = CW / CH;
+            uint32_t r[2][CH];
             const uint32_t tq = tmem_base + ((uint32_t)(q * 32) << 16) + cl0;
+            float *cs = reinterpret_cast<float *>(side) + (warp - kF8Epi0) * CW;
             if (ti.kb > 0) {
-                ok = mbar_wait_warp(&tfull[blk & 1u], (blk >> 1) & 1u, wc);
+                ok = mbar_wait_warp(&tfull[blk % NACC], (blk / NACC) & 1u, wc);
                 if (!ok) break;
                 tc_fence_after();
-                tmem_ld32(tq + (blk & 1u) * kF8BN, r[0]);
+                tmem_ld(tq + (blk % NACC) * BN, r[0]);
             }
             for (int kb = 0; kb < ti.kb; ++kb, ++blk) {
                 const float f0 = MODE == FP8_WGRAD ? na : na * nb0, f1 = na * nb1;
                 const uint64_t s0 = pair_f(f0, f0);
                 const uint64_t s1 = MODE == FP8_FFN1 ? pair_f(f1, f1) : s0;
-                float *cs = reinterpret_cast<float *>(side) + (warp - kF8Epi0) * 128;
+                float4 f[2][CH / 4];   // WGRAD: column scales of two chunks
+                auto load_cs = [&](int c) {
+#pragma unroll
+                    for (int j = 0; j < CH / 4; ++j)
+                        f[c & 1][j] = *reinterpret_cast<const float4 *>(cs + c * CH + 4 * j);
+                };
                 if constexpr (MODE == FP8_WGRAD) {
                     __syncwarp();
-                    *reinterpret_cast<float4 *>(cs + 4 * lane) = ncol;
+                    if (4 * lane < CW) *reinterpret_cast<float4 *>(cs + 4 * lane) = ncol;
                     __syncwarp();
+                    load_cs(0);
                 }
                 if (kb + 1 < ti.kb) next_scales(kb + 1);
-                const uint32_t a = blk & 1u;
+                const uint32_t a = blk % NACC;
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
+                for (int c = 0; c < NCH; ++c) {
                     tmem_wait_ld();
-                    if (c < 3) {
-                        tmem_ld32(tq + a * kF8BN + ((c + 1) >> 1) * kHalf + ((c + 1) & 1) * 32,
-                                  r[(c + 1) & 1]);
+                    if (c < NCH - 1) {
+                        constexpr int kPer = NCH / 2;   // chunks of a half
+                        tmem_ld(tq + a * BN + (c + 1) / kPer * kHalf + (c + 1) % kPer * CH,
+                                r[(c + 1) & 1]);
+                        if constexpr (MODE == FP8_WGRAD) load_cs(c + 1);
                     } else {
                         tc_fence_before();
                         __syncwarp();
                         if (lane == 0) mbar_arrive(&tempty[a]);
                         if (kb + 1 < ti.kb) {
-                            ok = mbar_wait_warp(&tfull[a ^ 1u], ((blk + 1) >> 1) & 1u, wc);
+                            const uint32_t b1 = blk + 1;
+                            ok = mbar_wait_warp(&tfull[b1 % NACC], (b1 / NACC) & 1u, wc);
                             if (!ok) break;
                             tc_fence_after();
-                            tmem_ld32(tq + (a ^ 1u) * kF8BN, r[0]);
+                            tmem_ld(tq + (b1 % NACC) * BN, r[0]);
                         }
                     }
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) {
-                        uint64_t v = pair(r[c & 1][2 * j], r[c & 1][2 * j + 1]);
-                        if constexpr (MODE == FP8_WGRAD)
-                            v = mul2(v, *reinterpret_cast<const uint64_t *>(cs + c * 32 + 2 * j));
-                        fma2(acc[c * 16 + j], v, c < 2 ? s0 : s1);
+                    for (int j = 0; j < CH / 2; j += 2) {
+                        uint64_t v0 = pair(r[c & 1][2 * j], r[c & 1][2 * j + 1]);
+                        uint64_t v1 = pair(r[c & 1][2 * j + 2], r[c & 1][2 * j + 3]);
+                        if constexpr (MODE == FP8_WGRAD) {
+                            const float4 s = f[c & 1][j / 2];
+                            v0 = mul2(v0, pair_f(s.x, s.y));
+                            v1 = mul2(v1, pair_f(s.z, s.w));
+                        }
+                        fma2(acc[c * (CH / 2) + j], v0, c < NCH / 2 ? s0 : s1);
+                        fma2(acc[c * (CH / 2) + j + 1], v1, c < NCH / 2 ? s0 : s1);
                     }
                 }
                 if (!ok) break;
             }
             if (!ok) break;
+            const F8Tile cur = ti;
+            const bool cur_valid = valid;
+            const int row = cur.row0 + r_local;
+            const float w = nw;
+            if (t + (int)gridDim.x < total) begin_tile(t + gridDim.x);
             if constexpr (MODE == FP8_ROWS) {
-                float w = 1.0f;
-                if (valid && p.row_w && row < p.w_rows) w = p.row_w[row];
                 // a warp whose 32 rows all exist writes 32 x 32 blocks through
                 // shared memory and TMA (whole sectors); a ragged one must not
                 // touch the next group's rows
-                const int col0 = ti.nt * kF8BN + cl0;
-                const bool whole = q * 32 + 32 <= ti.rows;
+                const int col0 = cur.nt * BN + cl0;
+                const bool whole = q * 32 + 32 <= cur.rows;
                 uint8_t *stg = out_s + (warp - kF8Epi0) * SH::OUT * p.out_bufs;
                 uint16_t *dst = p.out + (size_t)row * p.N + col0;
 #pragma unroll
-                for (int b = 0; b < 4; ++b) {
+                for (int b = 0; b < CW / 32; ++b) {
                     if (col0 + 32 * b >= p.N) break;
                     uint8_t *blk_s = stg + (b & (p.out_bufs - 1)) * SH::OUT;
                     if (whole) {
@@ -438,25 +476,25 @@ __global__ void __launch_bounds__(kF8Threads, 1) fp8_gemm_kernel(const __grid_co
                             st_shared_v4(smem_u32(blk_s) + lane * 64 +
                                              (((uint32_t)j ^ ((lane >> 1) & 3u)) << 4),
                                          w4[0], w4[1], w4[2], w4[3]);
-                        else if (valid && col0 + 32 * b + 8 * j < p.N)
+                        else if (cur_valid && col0 + 32 * b + 8 * j < p.N)
                             st_global_v4(dst + 32 * b + 8 * j, w4[0], w4[1], w4[2], w4[3]);
                     }
                     if (whole) {
                         fence_proxy_async_smem();
                         __syncwarp();
                         if (lane == 0) {
-                            tma_store_2d(&p.tmO, blk_s, col0 + 32 * b, ti.row0 + q * 32);
+                            tma_store_2d(&p.tmO, blk_s, col0 + 32 * b, cur.row0 + q * 32);
                             bulk_commit_group();
                         }
                     }
                 }
             } else if constexpr (MODE == FP8_WGRAD) {
-                const int col0 = ti.nt * kF8BN + cl0;
-                const bool whole = q * 32 + 32 <= ti.rows;
+                const int col0 = cur.nt * BN + cl0;
+                const bool whole = q * 32 + 32 <= cur.rows;
                 uint8_t *stg = out_s + (warp - kF8Epi0) * SH::OUT * p.out_bufs;
-                float *dst = p.dW + ((size_t)ti.g * p.M + row) * p.N + col0;
+                float *dst = p.dW + ((size_t)cur.g * p.M + row) * p.N + col0;
 #pragma unroll
-                for (int b = 0; b < 4; ++b) {
+                for (int b = 0; b < CW / 32; ++b) {
                     if (col0 + 32 * b >= p.N) break;
                     uint8_t *blk = stg + (b & (p.out_bufs - 1)) * SH::OUT;
                     if (whole) {
@@ -474,7 +512,7 @@ __global__ void __launch_bounds__(kF8Threads, 1) fp8_gemm_kernel(const __grid_co
                                              (((uint32_t)j ^ (lane & 7u)) << 4),
                                          (uint32_t)v0, (uint32_t)(v0 >> 32), (uint32_t)v1,
                                          (uint32_t)(v1 >> 32));
-                        else if (valid && col0 + 32 * b + 4 * j < p.N)
+                        else if (cur_valid && col0 + 32 * b + 4 * j < p.N)
                             st_global_v4(dst + 32 * b + 4 * j, (uint32_t)v0, (uint32_t)(v0 >> 32),
                                          (uint32_t)v1, (uint32_t)(v1 >> 32));
                     }
@@ -483,7 +521,7 @@ __global__ void __launch_bounds__(kF8Threads, 1) fp8_gemm_kernel(const __grid_co
                         __syncwarp();
                         if (lane == 0) {
                             tma_store_2d(&p.tmO, blk, col0 + 32 * b,
-                                         ti.g * p.M + ti.row0 + q * 32);
+                                         cur.g * p.M + cur.row0 + q * 32);
                             bulk_commit_group();
                         }
                     }
@@ -509,8 +547,8 @@ __global__ void __launch_bounds__(kF8Threads, 1) fp8_gemm_kernel(const __grid_co
                 if (!mbar_wait_warp(xch, (uint32_t)it & 1u, wc)) break;
                 amax = max(amax, ex[(part ^ 1) * 128 + r_local]);
                 const Fp8Scale f = fp8_scale(amax);
-                if (valid) {
-                    uint8_t *dst = p.hq + (size_t)row * p.I + ti.nt * 128 + cl0;
+                if (cur_valid) {
+                    uint8_t *dst = p.hq + (size_t)row * p.I + cur.nt * 128 + cl0;
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         uint32_t w[4];
@@ -521,7 +559,7 @@ __global__ void __launch_bounds__(kF8Threads, 1) fp8_gemm_kernel(const __grid_co
                         }
                         st_global_v4(dst + 16 * j, w[0], w[1], w[2], w[3]);
                     }
-                    if (part == 0) p.hs[(size_t)row * (p.I / 128) + ti.nt] = f.s;
+                    if (part == 0) p.hs[(size_t)row * (p.I / 128) + cur.nt] = f.s;
                 }
             }
         }
@@ -532,12 +570,12 @@ __global__ void __launch_bounds__(kF8Threads, 1) fp8_gemm_kernel(const __grid_co
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == 1) tmem_dealloc(tmem_base, 2 * kF8BN);
+    if (warp == 1) tmem_dealloc(tmem_base, NACC * BN);
 }
 
-template <int MODE>
+template <int MODE, int BN>
 moe_status launch_fp8(Fp8Params &p, long long max_tiles, cudaStream_t st) {
-    auto kern = fp8_gemm_kernel<MODE>;
+    auto kern = fp8_gemm_kernel<MODE, BN>;
     static bool attr_set[64] = {};
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return MOE_ERR_CUDA;
@@ -553,8 +591,8 @@ moe_status launch_fp8(Fp8Params &p, long long max_tiles, cudaStream_t st) {
     if (!p.status) return MOE_ERR_CUDA;
     p.wait_limit = kWaitLimitCycles;
     const int grid = max_tiles < num_sms() ? (int)max_tiles : num_sms();
-    p.out_bufs = fp8_out_bufs<MODE>(p.G);
-    const int smem = fp8_smem_bytes<MODE>(p.G, p.out_bufs);
+    p.out_bufs = fp8_out_bufs<MODE, BN>(p.G);
+    const int smem = fp8_smem_bytes<MODE, BN>(p.G, p.out_bufs);
     if (smem > kF8Smem) return MOE_ERR_UNSUPPORTED;
     kern<<<grid, kF8Threads, smem, st>>>(p);
     return cuda_status(cudaGetLastError());
@@ -562,13 +600,21 @@ moe_status launch_fp8(Fp8Params &p, long long max_tiles, cudaStream_t st) {
 
 }  // namespace
 
+// 256-wide tiles read fewer operand bytes for a product; 128-wide ones spread
+// over the SMs where there are few of them.
+static int rows_bn(int max_rows, int G, int N) {
+    const long long rows = (max_rows + 127) / 128 + (G < max_rows ? G : max_rows) - 1;
+    return rows * ((N + 255) / 256) >= 4LL * num_sms() ? 256 : 128;
+}
+
 moe_status launch_fp8_matmul(const uint8_t *aq, const float *as, const int32_t *offsets, int G,
                              int max_rows, const uint8_t *bq, const float *bs, const float *row_w,
                              int w_rows, int N, int K, uint16_t *out, cudaStream_t st) {
     Fp8Params p;
     std::memset(&p, 0, sizeof p);
+    const int BN = rows_bn(max_rows, G, N);
     if (!encode_tmap_u8_2d(&p.tmA, aq, K, max_rows, K, 128, 128, 128) ||
-        !encode_tmap_u8_2d(&p.tmB, bq, K, (uint64_t)G * N, K, 128, kF8BN, 128) ||
+        !encode_tmap_u8_2d(&p.tmB, bq, K, (uint64_t)G * N, K, 128, BN, 128) ||
         !encode_tmap_bf16_2d_sw64(&p.tmO, out, N, max_rows, (uint64_t)N * 2, 32, 32))
         return MOE_ERR_CUDA;
     p.offsets = offsets;
@@ -578,11 +624,13 @@ moe_status launch_fp8_matmul(const uint8_t *aq, const float *as, const int32_t *
     p.N = N;
     p.K_blocks = fp8_blocks(K);
     p.nb_n = fp8_blocks(N);
-    p.n_tiles = (N + kF8BN - 1) / kF8BN;
+    p.n_tiles = (N + BN - 1) / BN;
     p.row_w = row_w;
     p.w_rows = w_rows;
     p.out = out;
-    return launch_fp8<FP8_ROWS>(p, (long long)row_tile_bound(max_rows, G) * p.n_tiles, st);
+    const long long tiles = (long long)row_tile_bound(max_rows, G) * p.n_tiles;
+    return BN == 256 ? launch_fp8<FP8_ROWS, 256>(p, tiles, st)
+                     : launch_fp8<FP8_ROWS, 128>(p, tiles, st);
 }
 
 moe_status launch_fp8_ffn1(const uint8_t *xq, const float *xs, const int32_t *offsets, int G,
@@ -605,16 +653,17 @@ moe_status launch_fp8_ffn1(const uint8_t *xq, const float *xs, const int32_t *of
     p.clamp = clamp;
     p.hq = hq;
     p.hs = hs;
-    return launch_fp8<FP8_FFN1>(p, (long long)row_tile_bound(max_rows, G) * p.n_tiles, st);
+    return launch_fp8<FP8_FFN1, 256>(p, (long long)row_tile_bound(max_rows, G) * p.n_tiles, st);
 }
 
 moe_status launch_fp8_wgrad(const uint8_t *aq, const float *as, const uint8_t *bq, const float *bs,
                             const int32_t *first, int G, int max_chunks, int M, int N, float *dW,
                             cudaStream_t st) {
+    constexpr int BN = 128;   // a tile's output fits the staging blocks: see the top
     Fp8Params p;
     std::memset(&p, 0, sizeof p);
     if (!encode_tmap_u8_2d(&p.tmA, aq, 128, (uint64_t)max_chunks * M, 128, 128, 128, 128) ||
-        !encode_tmap_u8_2d(&p.tmB, bq, 128, (uint64_t)max_chunks * N, 128, 128, kF8BN, 128) ||
+        !encode_tmap_u8_2d(&p.tmB, bq, 128, (uint64_t)max_chunks * N, 128, 128, BN, 128) ||
         !encode_tmap_f32_2d(&p.tmO, dW, N, (uint64_t)G * M, (uint64_t)N * 4, 32, 32))
         return MOE_ERR_CUDA;
     p.offsets = first;
@@ -623,9 +672,9 @@ moe_status launch_fp8_wgrad(const uint8_t *aq, const float *as, const uint8_t *b
     p.G = G;
     p.M = M;
     p.N = N;
-    p.n_tiles = (N + kF8BN - 1) / kF8BN;
+    p.n_tiles = (N + BN - 1) / BN;
     p.dW = dW;
-    return launch_fp8<FP8_WGRAD>(p, (long long)G * ((M + 127) / 128) * p.n_tiles, st);
+    return launch_fp8<FP8_WGRAD, 128>(p, (long long)G * ((M + 127) / 128) * p.n_tiles, st);
 }
 
 }  // namespace moe
