@@ -37,7 +37,6 @@ enum Fp8Mode : int { FP8_ROWS = 0, FP8_FFN1 = 1, FP8_WGRAD = 2 };
 
 struct Fp8Params {
     CUtensorMap tmA;   // A codes: [rows, K] (WGRAD [chunks * M, 128]), boxes 128 x 128
-    CUtensorMap tmO;   // ROWS: out [rows, N] bf16; WGRAD: dW [G * M, N] fp32; boxes 32 x 32
     CUtensorMap tmB;   // B codes: [G * N, K] (WGRAD [chunks * N, 128]), boxes 128 x 256 (FFN1 128)
     const int32_t *offsets;   // [G+1] rows of the groups; WGRAD: their chunks
     const float *sa, *sb;
@@ -52,7 +51,6 @@ struct Fp8Params {
     uint8_t *hq;              // FFN1: h codes [rows, I] ...
     float *hs;                //       ... and scales [rows, I / 128]
     float *dW;                // WGRAD
-    int out_bufs;             // output blocks of an epilogue warp
     int *status;
     long long wait_limit;
 };
@@ -78,24 +76,17 @@ struct F8Shape {
     static constexpr uint32_t IDESC =
         (1u << 4) | ((uint32_t)(BN >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
     static constexpr int STAGES = BN == 256 ? 4 : MODE == FP8_WGRAD ? 4 : 6;
-    // an output block of 32 x 32 on its way out; every epilogue warp has two (one
-    // where the offsets of many groups need the room)
+    // an output block of 32 x 32 for each epilogue warp
     static constexpr int OUT = MODE == FP8_ROWS ? 2048 : MODE == FP8_WGRAD ? 4096 : 0;
     // FFN1: exchange of the largest |h|; WGRAD: column scales
     static constexpr int SIDE = MODE == FP8_FFN1 ? 2048 : MODE == FP8_WGRAD ? kF8Epi * CW * 4 : 0;
-    static constexpr int FIXED = STAGES * STAGE + SIDE;
+    static constexpr int FIXED = STAGES * STAGE + SIDE + kF8Epi * OUT;
+    static_assert(1024 + FIXED + kF8Bars + 8 * (kMaxGroups + 2) <= 232448, "shared memory");
 };
-constexpr int kF8Smem = 232448;   // shared memory that a CTA can have
 
 template <int MODE, int BN>
-inline int fp8_smem_bytes(int G, int out_bufs) {
-    using SH = F8Shape<MODE, BN>;
-    return 1024 + SH::FIXED + kF8Epi * SH::OUT * out_bufs + kF8Bars +
-           8 * (G + 2);
-}
-template <int MODE, int BN>
-inline int fp8_out_bufs(int G) {
-    return fp8_smem_bytes<MODE, BN>(G, 2) <= kF8Smem ? 2 : 1;
+inline int fp8_smem_bytes(int G) {
+    return 1024 + F8Shape<MODE, BN>::FIXED + kF8Bars + 8 * (G + 2);
 }
 
 // D[tmem] (+)= A[smem] B[smem]^T, E4M3 operands (K = 32), fp32 accumulator.
@@ -148,12 +139,14 @@ struct F8Tile {
     int g, nt, row0, rows, kb, k0;   // rows: valid rows from row0; k0: first chunk (WGRAD)
 };
 
+// Tile t of the schedule, found by a whole warp (a ballot over 32 groups at a
+// time, from the group of the tile before it: tiles come in order).
 template <int MODE>
 __device__ __forceinline__ F8Tile f8_tile(const Fp8Params &p, int t, const int *mt_start,
-                                          const int *offs) {
+                                          const int *offs, int from) {
     F8Tile ti;
-    ti.nt = t % p.n_tiles;
     const int q = t / p.n_tiles;
+    ti.nt = t - q * p.n_tiles;
     if constexpr (MODE == FP8_WGRAD) {
         const int mt = (p.M + 127) >> 7;
         ti.g = q / mt;
@@ -163,14 +156,18 @@ __device__ __forceinline__ F8Tile f8_tile(const Fp8Params &p, int t, const int *
         ti.kb = offs[ti.g + 1] - ti.k0;
         return ti;
     }
-    int lo = 0, hi = p.G - 1;
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (mt_start[mid] <= q) lo = mid; else hi = mid - 1;
+    // the last group that starts at or before row tile q (empty groups start
+    // where the next one does)
+    int g = from;
+    while (true) {
+        const int i = g + 1 + (threadIdx.x & 31);
+        const unsigned m = __ballot_sync(0xffffffffu, i < p.G && mt_start[min(i, p.G)] <= q);
+        g += __popc(m);
+        if (m != 0xffffffffu) break;
     }
-    ti.g = lo;
-    ti.row0 = offs[lo] + (q - mt_start[lo]) * 128;
-    ti.rows = min(128, offs[lo + 1] - ti.row0);
+    ti.g = g;
+    ti.row0 = offs[g] + (q - mt_start[g]) * 128;
+    ti.rows = min(128, offs[g + 1] - ti.row0);
     ti.kb = p.K_blocks;
     ti.k0 = 0;
     return ti;
@@ -183,9 +180,8 @@ __global__ void __launch_bounds__(kF8Threads, 1) fp8_gemm_kernel(const __grid_co
     using SH = F8Shape<MODE, BN>;
     constexpr int STAGES = SH::STAGES, NACC = SH::NACC, CW = SH::CW, CH = SH::CH;
     uint8_t *side = smem + STAGES * SH::STAGE;
-    uint8_t *out_s = smem + SH::FIXED;
-    uint8_t *fixed_end = out_s + kF8Epi * SH::OUT * p.out_bufs;
-    uint64_t *full = reinterpret_cast<uint64_t *>(fixed_end);
+    uint8_t *out_s = side + SH::SIDE;
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + SH::FIXED);
     uint64_t *empty = full + STAGES;
     uint64_t *tfull = empty + STAGES;   // a block's sums are in an accumulator
     uint64_t *tempty = tfull + NACC;          // ... and have been read
@@ -193,7 +189,7 @@ __global__ void __launch_bounds__(kF8Threads, 1) fp8_gemm_kernel(const __grid_co
     uint64_t *done = xch + 1;
     uint32_t *tmem_base_s = reinterpret_cast<uint32_t *>(done + 1);
     volatile int *abort_s = reinterpret_cast<volatile int *>(tmem_base_s + 1);
-    int *offs = reinterpret_cast<int *>(fixed_end + kF8Bars);
+    int *offs = reinterpret_cast<int *>(smem + SH::FIXED + kF8Bars);
     int *mt_start = offs + (p.G + 1);
 
     const int warp = threadIdx.x >> 5;
@@ -251,16 +247,16 @@ __global__ void __launch_bounds__(kF8Threads, 1) fp8_gemm_kernel(const __grid_co
     if (warp < kF8Epi0) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kF8RegsFew));
     if (warp == 0) {
-        if (lane == 0) {
-            int last[STAGES];
-#pragma unroll
-            for (int i = 0; i < STAGES; ++i) last[i] = -1;
-            uint32_t s = 0, ph = 0;
-            bool ok = true;
-            for (int t = blockIdx.x; ok && t < total; t += gridDim.x) {
-                const F8Tile ti = f8_tile<MODE>(p, t, mt_start, offs);
-                for (int kb = 0; kb < ti.kb; ++kb) {
-                    if (!mbar_wait(&empty[s], ph ^ 1u, wc)) { ok = false; break; }
+        uint32_t s = 0, ph = 0;
+        uint32_t begun = 0;   // stages with a copy, and its parity
+        bool ok = true;
+        int g = 0;
+        for (int t = blockIdx.x; ok && t < total; t += gridDim.x) {
+            const F8Tile ti = f8_tile<MODE>(p, t, mt_start, offs, g);
+            g = ti.g;
+            for (int kb = 0; kb < ti.kb; ++kb) {
+                if (!mbar_wait_warp(&empty[s], ph ^ 1u, wc)) { ok = false; break; }
+                if (lane == 0) {
                     mbar_arrive_expect_tx(&full[s], SH::STAGE);
                     uint8_t *a = smem + s * SH::STAGE;
                     uint8_t *b = a + kF8A;
@@ -277,21 +273,24 @@ __global__ void __launch_bounds__(kF8Threads, 1) fp8_gemm_kernel(const __grid_co
                         tma_load_2d(a, &p.tmA, &full[s], kb * 128, ti.row0);
                         tma_load_2d(b, &p.tmB, &full[s], kb * 128, ti.g * p.N + ti.nt * BN);
                     }
-                    last[s] = (int)ph;
-                    if (++s == STAGES) { s = 0; ph ^= 1u; }
                 }
+                begun = (begun & ~(0x10001u << s)) | (0x10000u << s) | (ph << s);
+                if (++s == STAGES) { s = 0; ph ^= 1u; }
             }
-            if (!ok) {
-                // drain the copies still in flight before the CTA exits
-                for (int i = 0; i < STAGES; ++i)
-                    if (last[i] >= 0) mbar_wait_teardown(&full[i], (uint32_t)last[i], p.wait_limit);
-            }
+        }
+        if (!ok) {
+            // drain the copies still in flight before the CTA exits
+            for (int i = 0; i < STAGES; ++i)
+                if (begun >> (16 + i) & 1u)
+                    mbar_wait_teardown(&full[i], begun >> i & 1u, p.wait_limit);
         }
     } else if (warp == 1) {
         uint32_t s = 0, ph = 0, blk = 0;
         bool ok = true;
+        int g = 0;
         for (int t = blockIdx.x; ok && t < total; t += gridDim.x) {
-            const F8Tile ti = f8_tile<MODE>(p, t, mt_start, offs);
+            const F8Tile ti = f8_tile<MODE>(p, t, mt_start, offs, g);
+            g = ti.g;
             for (int kb = 0; kb < ti.kb; ++kb, ++blk) {
                 const uint32_t acc = blk % NACC, aph = (blk / NACC) & 1u;
                 if (!mbar_wait_warp(&tempty[acc], aph ^ 1u, wc)) { ok = false; break; }
@@ -348,7 +347,7 @@ __global__ void __launch_bounds__(kF8Threads, 1) fp8_gemm_kernel(const __grid_co
         };
         F8Tile ti{};
         auto begin_tile = [&](int t) {
-            ti = f8_tile<MODE>(p, t, mt_start, offs);
+            ti = f8_tile<MODE>(p, t, mt_start, offs, ti.g);
             valid = r_local < ti.rows;
             const int row = ti.row0 + r_local;
             if constexpr (MODE == FP8_WGRAD) {
@@ -446,24 +445,16 @@ __global__ void __launch_bounds__(kF8Threads, 1) fp8_gemm_kernel(const __grid_co
             const float w = nw;
             if (t + (int)gridDim.x < total) begin_tile(t + gridDim.x);
             if constexpr (MODE == FP8_ROWS) {
-                // a warp whose 32 rows all exist writes 32 x 32 blocks through
-                // shared memory and TMA (whole sectors); a ragged one must not
-                // touch the next group's rows
+                // 32 x 32 blocks turned in shared memory (16-byte pieces exchanged
+                // by row against bank conflicts), so that four lanes write the 64
+                // bytes of a row together
                 const int col0 = cur.nt * BN + cl0;
-                const bool whole = q * 32 + 32 <= cur.rows;
-                uint8_t *stg = out_s + (warp - kF8Epi0) * SH::OUT * p.out_bufs;
-                uint16_t *dst = p.out + (size_t)row * p.N + col0;
+                const uint32_t blk_s = smem_u32(out_s) + (warp - kF8Epi0) * SH::OUT;
+                const int wr = lane >> 2, wc4 = lane & 3;
 #pragma unroll
                 for (int b = 0; b < CW / 32; ++b) {
                     if (col0 + 32 * b >= p.N) break;
-                    uint8_t *blk_s = stg + (b & (p.out_bufs - 1)) * SH::OUT;
-                    if (whole) {
-                        if (lane == 0) {
-                            if (p.out_bufs == 2) bulk_wait_group_read<1>();
-                            else bulk_wait_group_read<0>();
-                        }
-                        __syncwarp();
-                    }
+                    __syncwarp();
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         uint32_t w4[4];
@@ -472,58 +463,48 @@ __global__ void __launch_bounds__(kF8Threads, 1) fp8_gemm_kernel(const __grid_co
                             const uint64_t v = acc[16 * b + 4 * j + e];
                             w4[e] = pack_bf16x2(w * lo_f(v), w * hi_f(v));
                         }
-                        if (whole)
-                            st_shared_v4(smem_u32(blk_s) + lane * 64 +
-                                             (((uint32_t)j ^ ((lane >> 1) & 3u)) << 4),
-                                         w4[0], w4[1], w4[2], w4[3]);
-                        else if (cur_valid && col0 + 32 * b + 8 * j < p.N)
-                            st_global_v4(dst + 32 * b + 8 * j, w4[0], w4[1], w4[2], w4[3]);
+                        st_shared_v4(blk_s + lane * 64 + (((uint32_t)j ^ ((lane >> 1) & 3u)) << 4),
+                                     w4[0], w4[1], w4[2], w4[3]);
                     }
-                    if (whole) {
-                        fence_proxy_async_smem();
-                        __syncwarp();
-                        if (lane == 0) {
-                            tma_store_2d(&p.tmO, blk_s, col0 + 32 * b, cur.row0 + q * 32);
-                            bulk_commit_group();
-                        }
+                    __syncwarp();
+                    const int col = col0 + 32 * b + 8 * wc4;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int rr = 8 * i + wr;
+                        const uint4 v = ld_shared_v4(
+                            blk_s + rr * 64 + (((uint32_t)wc4 ^ ((rr >> 1) & 3u)) << 4));
+                        if (q * 32 + rr < cur.rows && col < p.N)
+                            st_global_v4(p.out + (size_t)(cur.row0 + q * 32 + rr) * p.N + col, v.x,
+                                         v.y, v.z, v.w);
                     }
                 }
             } else if constexpr (MODE == FP8_WGRAD) {
+                // likewise, eight lanes to the 128 bytes of a row
                 const int col0 = cur.nt * BN + cl0;
-                const bool whole = q * 32 + 32 <= cur.rows;
-                uint8_t *stg = out_s + (warp - kF8Epi0) * SH::OUT * p.out_bufs;
-                float *dst = p.dW + ((size_t)cur.g * p.M + row) * p.N + col0;
+                const uint32_t blk_s = smem_u32(out_s) + (warp - kF8Epi0) * SH::OUT;
+                const int wr = lane >> 3, wc8 = lane & 7;
 #pragma unroll
                 for (int b = 0; b < CW / 32; ++b) {
                     if (col0 + 32 * b >= p.N) break;
-                    uint8_t *blk = stg + (b & (p.out_bufs - 1)) * SH::OUT;
-                    if (whole) {
-                        if (lane == 0) {
-                            if (p.out_bufs == 2) bulk_wait_group_read<1>();
-                            else bulk_wait_group_read<0>();
-                        }
-                        __syncwarp();
-                    }
+                    __syncwarp();
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {
                         const uint64_t v0 = acc[16 * b + 2 * j], v1 = acc[16 * b + 2 * j + 1];
-                        if (whole)
-                            st_shared_v4(smem_u32(blk) + lane * 128 +
-                                             (((uint32_t)j ^ (lane & 7u)) << 4),
-                                         (uint32_t)v0, (uint32_t)(v0 >> 32), (uint32_t)v1,
-                                         (uint32_t)(v1 >> 32));
-                        else if (cur_valid && col0 + 32 * b + 4 * j < p.N)
-                            st_global_v4(dst + 32 * b + 4 * j, (uint32_t)v0, (uint32_t)(v0 >> 32),
-                                         (uint32_t)v1, (uint32_t)(v1 >> 32));
+                        st_shared_v4(blk_s + lane * 128 + (((uint32_t)j ^ (lane & 7u)) << 4),
+                                     (uint32_t)v0, (uint32_t)(v0 >> 32), (uint32_t)v1,
+                                     (uint32_t)(v1 >> 32));
                     }
-                    if (whole) {
-                        fence_proxy_async_smem();
-                        __syncwarp();
-                        if (lane == 0) {
-                            tma_store_2d(&p.tmO, blk, col0 + 32 * b,
-                                         cur.g * p.M + cur.row0 + q * 32);
-                            bulk_commit_group();
-                        }
+                    __syncwarp();
+                    const int col = col0 + 32 * b + 4 * wc8;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int rr = 4 * i + wr;
+                        const uint4 v =
+                            ld_shared_v4(blk_s + rr * 128 + (((uint32_t)wc8 ^ (rr & 7u)) << 4));
+                        if (q * 32 + rr < cur.rows && col < p.N)
+                            st_global_v4(p.dW + ((size_t)cur.g * p.M + cur.row0 + q * 32 + rr) * p.N +
+                                             col,
+                                         v.x, v.y, v.z, v.w);
                     }
                 }
             } else {
@@ -563,8 +544,6 @@ __global__ void __launch_bounds__(kF8Threads, 1) fp8_gemm_kernel(const __grid_co
                 }
             }
         }
-        // the output blocks have left shared memory (and landed) before the exit
-        if (MODE != FP8_FFN1 && lane == 0) bulk_wait_group_all();
     }
 
     tc_fence_before();
@@ -582,7 +561,7 @@ moe_status launch_fp8(Fp8Params &p, long long max_tiles, cudaStream_t st) {
     if (dev < 0 || dev >= 64) return MOE_ERR_UNSUPPORTED;
     if (!attr_set[dev]) {
         if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 kF8Smem) != cudaSuccess)
+                                 fp8_smem_bytes<MODE, BN>(kMaxGroups)) != cudaSuccess)
             return MOE_ERR_CUDA;
         attr_set[dev] = true;
     }
@@ -591,10 +570,7 @@ moe_status launch_fp8(Fp8Params &p, long long max_tiles, cudaStream_t st) {
     if (!p.status) return MOE_ERR_CUDA;
     p.wait_limit = kWaitLimitCycles;
     const int grid = max_tiles < num_sms() ? (int)max_tiles : num_sms();
-    p.out_bufs = fp8_out_bufs<MODE, BN>(p.G);
-    const int smem = fp8_smem_bytes<MODE, BN>(p.G, p.out_bufs);
-    if (smem > kF8Smem) return MOE_ERR_UNSUPPORTED;
-    kern<<<grid, kF8Threads, smem, st>>>(p);
+    kern<<<grid, kF8Threads, fp8_smem_bytes<MODE, BN>(p.G), st>>>(p);
     return cuda_status(cudaGetLastError());
 }
 
@@ -614,8 +590,7 @@ moe_status launch_fp8_matmul(const uint8_t *aq, const float *as, const int32_t *
     std::memset(&p, 0, sizeof p);
     const int BN = rows_bn(max_rows, G, N);
     if (!encode_tmap_u8_2d(&p.tmA, aq, K, max_rows, K, 128, 128, 128) ||
-        !encode_tmap_u8_2d(&p.tmB, bq, K, (uint64_t)G * N, K, 128, BN, 128) ||
-        !encode_tmap_bf16_2d_sw64(&p.tmO, out, N, max_rows, (uint64_t)N * 2, 32, 32))
+        !encode_tmap_u8_2d(&p.tmB, bq, K, (uint64_t)G * N, K, 128, BN, 128))
         return MOE_ERR_CUDA;
     p.offsets = offsets;
     p.sa = as;
@@ -663,8 +638,7 @@ moe_status launch_fp8_wgrad(const uint8_t *aq, const float *as, const uint8_t *b
     Fp8Params p;
     std::memset(&p, 0, sizeof p);
     if (!encode_tmap_u8_2d(&p.tmA, aq, 128, (uint64_t)max_chunks * M, 128, 128, 128, 128) ||
-        !encode_tmap_u8_2d(&p.tmB, bq, 128, (uint64_t)max_chunks * N, 128, 128, BN, 128) ||
-        !encode_tmap_f32_2d(&p.tmO, dW, N, (uint64_t)G * M, (uint64_t)N * 4, 32, 32))
+        !encode_tmap_u8_2d(&p.tmB, bq, 128, (uint64_t)max_chunks * N, 128, 128, BN, 128))
         return MOE_ERR_CUDA;
     p.offsets = first;
     p.sa = as;
