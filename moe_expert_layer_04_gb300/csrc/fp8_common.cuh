@@ -62,4 +62,15 @@ __device__ __forceinline__ float swiglu_clamped_nan(float g, float u, float c) {
     return a * __fdividef(1.0f, 1.0f + __expf(-a)) * b;
 }
 
+// Contiguous bytes into shared memory (both 16-byte aligned, bytes a multiple of
+// 16), counted on an mbarrier.
+__device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t bytes,
+                                          uint64_t *bar) {
+    asm volatile(
+        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::
+            "r"(smem_u32(dst)),
+        "l"(src), "r"(bytes), "r"(smem_u32(bar))
+        : "memory");
+}
+
 }  // namespace moe

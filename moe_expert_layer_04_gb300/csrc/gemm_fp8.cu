@@ -38,6 +38,7 @@ enum Fp8Mode : int { FP8_ROWS = 0, FP8_FFN1 = 1, FP8_WGRAD = 2 };
 struct Fp8Params {
     CUtensorMap tmA;   // A codes: [rows, K] (WGRAD [chunks * M, 128]), boxes 128 x 128
     CUtensorMap tmB;   // B codes: [G * N, K] (WGRAD [chunks * N, 128]), boxes 128 x 256 (FFN1 128)
+    CUtensorMap tmO;   // ROWS, WGRAD: output, boxes of 32 rows x 128 bytes
     const int32_t *offsets;   // [G+1] rows of the groups; WGRAD: their chunks
     const float *sa, *sb;
     int G, N, K_blocks, n_tiles;
@@ -59,7 +60,14 @@ constexpr int kF8A = 128 * 128;
 constexpr int kF8Epi = 8;                       // epilogue warps
 constexpr int kF8Epi0 = 4;                      // the first of them
 constexpr int kF8Threads = 32 * (kF8Epi0 + kF8Epi);
-constexpr int kF8Bars = 512;
+constexpr int kF8Bars = 256;
+constexpr int kF8Smem = 232448;                 // of a CTA at most
+// Scales of a block are overwritten six blocks on: its copy is sent when the MMAs
+// of the block three or more before it are done, which began after the sums of the
+// block two before that one were read, and with them its scales.
+constexpr int kF8Scales = 6;
+// 128 bytes of 32 rows on their way out, 128-byte swizzle
+constexpr int kF8OutPiece = 32 * 128;
 
 // Registers: the four warps that copy and issue hand most of theirs to the
 // eight that hold the accumulators (128 a thread, and 64 in flight from tensor
@@ -67,7 +75,7 @@ constexpr int kF8Bars = 512;
 constexpr int kF8RegsFew = 40, kF8RegsMany = 232;
 static_assert(4 * kF8RegsFew + 8 * kF8RegsMany <= 12 * 168, "register split");
 
-template <int MODE, int BN>
+template <int MODE, int BN, int ST>
 struct F8Shape {
     static constexpr int STAGE = kF8A + BN * 128;
     static constexpr int NACC = 512 / BN;            // accumulators in tensor memory
@@ -75,19 +83,16 @@ struct F8Shape {
     static constexpr int CH = MODE == FP8_WGRAD ? 16 : 32;   // of them in flight at a time
     static constexpr uint32_t IDESC =
         (1u << 4) | ((uint32_t)(BN >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
-    static constexpr int STAGES = BN == 256 ? 4 : MODE == FP8_WGRAD ? 4 : 6;
-    // an output block of 32 x 32 for each epilogue warp
-    static constexpr int OUT = MODE == FP8_ROWS ? 2048 : MODE == FP8_WGRAD ? 4096 : 0;
-    // FFN1: exchange of the largest |h|; WGRAD: column scales
-    static constexpr int SIDE = MODE == FP8_FFN1 ? 2048 : MODE == FP8_WGRAD ? kF8Epi * CW * 4 : 0;
-    static constexpr int FIXED = STAGES * STAGE + SIDE + kF8Epi * OUT;
-    static_assert(1024 + FIXED + kF8Bars + 8 * (kMaxGroups + 2) <= 232448, "shared memory");
+    // FFN1: exchange of the largest |h|; WGRAD: ring of both operands' scales
+    static constexpr int SIDE =
+        MODE == FP8_FFN1 ? 2048 : MODE == FP8_WGRAD ? kF8Scales * (128 + BN) * 4 : 0;
+    // pieces of output on their way to memory, for each epilogue warp
+    static constexpr int OUTS = MODE == FP8_FFN1 ? 0 : BN == 256 ? 2 : 1;
+    static constexpr int OUT = kF8Epi * OUTS * kF8OutPiece;
+    static constexpr int GROUP = MODE == FP8_WGRAD ? 4 : 8;   // bytes of a group's offset and first tile
+    static constexpr int FIXED = ST * STAGE + OUT + SIDE + kF8Bars;
+    static constexpr int smem(int G) { return 1024 + FIXED + GROUP * (G + 2); }
 };
-
-template <int MODE, int BN>
-inline int fp8_smem_bytes(int G) {
-    return 1024 + F8Shape<MODE, BN>::FIXED + kF8Bars + 8 * (G + 2);
-}
 
 // D[tmem] (+)= A[smem] B[smem]^T, E4M3 operands (K = 32), fp32 accumulator.
 // Instruction descriptor: D format [4,6) = 1 (fp32), A and B format 0 (E4M3),
@@ -139,14 +144,28 @@ struct F8Tile {
     int g, nt, row0, rows, kb, k0;   // rows: valid rows from row0; k0: first chunk (WGRAD)
 };
 
-// Tile t of the schedule, found by a whole warp (a ballot over 32 groups at a
+// The tiles of a CTA, gridDim.x apart: tile t = q n_tiles + nt.
+struct F8Walk {
+    int q, nt, dq, dn, n;
+    __device__ explicit F8Walk(int n_tiles)
+        : q(blockIdx.x / n_tiles), dq(gridDim.x / n_tiles), n(n_tiles) {
+        nt = blockIdx.x - q * n;
+        dn = gridDim.x - dq * n;
+    }
+    __device__ void next() {
+        q += dq;
+        nt += dn;
+        if (nt >= n) { nt -= n; ++q; }
+    }
+};
+
+// Row tile q, column tile nt, found by a whole warp (a ballot over 32 groups at a
 // time, from the group of the tile before it: tiles come in order).
 template <int MODE>
-__device__ __forceinline__ F8Tile f8_tile(const Fp8Params &p, int t, const int *mt_start,
+__device__ __forceinline__ F8Tile f8_tile(const Fp8Params &p, int q, int nt, const int *mt_start,
                                           const int *offs, int from) {
     F8Tile ti;
-    const int q = t / p.n_tiles;
-    ti.nt = t - q * p.n_tiles;
+    ti.nt = nt;
     if constexpr (MODE == FP8_WGRAD) {
         const int mt = (p.M + 127) >> 7;
         ti.g = q / mt;
@@ -173,30 +192,30 @@ __device__ __forceinline__ F8Tile f8_tile(const Fp8Params &p, int t, const int *
     return ti;
 }
 
-template <int MODE, int BN>
+template <int MODE, int BN, int ST>   // ST: stages of operands in shared memory
 __global__ void __launch_bounds__(kF8Threads, 1) fp8_gemm_kernel(const __grid_constant__ Fp8Params p) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-    using SH = F8Shape<MODE, BN>;
-    constexpr int STAGES = SH::STAGES, NACC = SH::NACC, CW = SH::CW, CH = SH::CH;
-    uint8_t *side = smem + STAGES * SH::STAGE;
-    uint8_t *out_s = side + SH::SIDE;
-    uint64_t *full = reinterpret_cast<uint64_t *>(smem + SH::FIXED);
-    uint64_t *empty = full + STAGES;
-    uint64_t *tfull = empty + STAGES;   // a block's sums are in an accumulator
+    using SH = F8Shape<MODE, BN, ST>;
+    constexpr int NACC = SH::NACC, CW = SH::CW, CH = SH::CH;
+    uint8_t *out_s = smem + ST * SH::STAGE;   // 1024-aligned
+    uint8_t *side = out_s + SH::OUT;
+    uint64_t *full = reinterpret_cast<uint64_t *>(side + SH::SIDE);
+    uint64_t *empty = full + ST;
+    uint64_t *tfull = empty + ST;   // a block's sums are in an accumulator
     uint64_t *tempty = tfull + NACC;          // ... and have been read
     uint64_t *xch = tempty + NACC;            // FFN1: both halves' largest |h| are in `side`
     uint64_t *done = xch + 1;
     uint32_t *tmem_base_s = reinterpret_cast<uint32_t *>(done + 1);
     volatile int *abort_s = reinterpret_cast<volatile int *>(tmem_base_s + 1);
-    int *offs = reinterpret_cast<int *>(smem + SH::FIXED + kF8Bars);
+    int *offs = reinterpret_cast<int *>(side + SH::SIDE + kF8Bars);
     int *mt_start = offs + (p.G + 1);
 
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
-        for (int s = 0; s < STAGES; ++s) {
+        for (int s = 0; s < ST; ++s) {
             mbar_init(&full[s], 1);
             mbar_init(&empty[s], 1);
         }
@@ -231,7 +250,7 @@ __global__ void __launch_bounds__(kF8Threads, 1) fp8_gemm_kernel(const __grid_co
                 const int v = __shfl_up_sync(0xffffffffu, incl, sft);
                 if (lane >= sft) incl += v;
             }
-            if (g <= p.G) mt_start[g] = carry + incl - mt;
+            if (MODE != FP8_WGRAD && g <= p.G) mt_start[g] = carry + incl - mt;
             carry += __shfl_sync(0xffffffffu, incl, 31);
         }
     }
@@ -247,23 +266,33 @@ __global__ void __launch_bounds__(kF8Threads, 1) fp8_gemm_kernel(const __grid_co
     if (warp < kF8Epi0) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kF8RegsFew));
     if (warp == 0) {
-        uint32_t s = 0, ph = 0;
+        uint32_t s = 0, ph = 0, sc = 0;
         uint32_t begun = 0;   // stages with a copy, and its parity
         bool ok = true;
         int g = 0;
-        for (int t = blockIdx.x; ok && t < total; t += gridDim.x) {
-            const F8Tile ti = f8_tile<MODE>(p, t, mt_start, offs, g);
+        F8Walk at(p.n_tiles);
+        for (int t = blockIdx.x; ok && t < total; t += gridDim.x, at.next()) {
+            const F8Tile ti = f8_tile<MODE>(p, at.q, at.nt, mt_start, offs, g);
             g = ti.g;
             for (int kb = 0; kb < ti.kb; ++kb) {
                 if (!mbar_wait_warp(&empty[s], ph ^ 1u, wc)) { ok = false; break; }
                 if (lane == 0) {
-                    mbar_arrive_expect_tx(&full[s], SH::STAGE);
+                    uint32_t sa_bytes = 0, sb_bytes = 0;
+                    if constexpr (MODE == FP8_WGRAD) {
+                        sa_bytes = 4 * min(128, p.M - ti.row0);
+                        sb_bytes = 4 * min(BN, p.N - ti.nt * BN);
+                    }
+                    mbar_arrive_expect_tx(&full[s], SH::STAGE + sa_bytes + sb_bytes);
                     uint8_t *a = smem + s * SH::STAGE;
                     uint8_t *b = a + kF8A;
                     if constexpr (MODE == FP8_WGRAD) {
                         const int c = ti.k0 + kb;
                         tma_load_2d(a, &p.tmA, &full[s], 0, c * p.M + ti.row0);
                         tma_load_2d(b, &p.tmB, &full[s], 0, c * p.N + ti.nt * BN);
+                        float *f = reinterpret_cast<float *>(side) + sc * (128 + BN);
+                        bulk_load(f, p.sa + (size_t)c * p.M + ti.row0, sa_bytes, &full[s]);
+                        bulk_load(f + 128, p.sb + (size_t)c * p.N + ti.nt * BN, sb_bytes,
+                                  &full[s]);
                     } else if constexpr (MODE == FP8_FFN1) {
                         const int br = ti.g * 2 * p.I + ti.nt * 128;
                         tma_load_2d(a, &p.tmA, &full[s], kb * 128, ti.row0);
@@ -274,41 +303,52 @@ __global__ void __launch_bounds__(kF8Threads, 1) fp8_gemm_kernel(const __grid_co
                         tma_load_2d(b, &p.tmB, &full[s], kb * 128, ti.g * p.N + ti.nt * BN);
                     }
                 }
+                if (++sc == kF8Scales) sc = 0;
                 begun = (begun & ~(0x10001u << s)) | (0x10000u << s) | (ph << s);
-                if (++s == STAGES) { s = 0; ph ^= 1u; }
+                if (++s == ST) { s = 0; ph ^= 1u; }
             }
         }
         if (!ok) {
             // drain the copies still in flight before the CTA exits
-            for (int i = 0; i < STAGES; ++i)
+            for (int i = 0; i < ST; ++i)
                 if (begun >> (16 + i) & 1u)
                     mbar_wait_teardown(&full[i], begun >> i & 1u, p.wait_limit);
         }
     } else if (warp == 1) {
-        uint32_t s = 0, ph = 0, blk = 0;
+        // One thread: what it costs from the release of an accumulator to its next
+        // MMA is time in which the tensor core has nothing to do.
         bool ok = true;
-        int g = 0;
-        for (int t = blockIdx.x; ok && t < total; t += gridDim.x) {
-            const F8Tile ti = f8_tile<MODE>(p, t, mt_start, offs, g);
-            g = ti.g;
-            for (int kb = 0; kb < ti.kb; ++kb, ++blk) {
-                const uint32_t acc = blk % NACC, aph = (blk / NACC) & 1u;
-                if (!mbar_wait_warp(&tempty[acc], aph ^ 1u, wc)) { ok = false; break; }
-                if (!mbar_wait_warp(&full[s], ph, wc)) { ok = false; break; }
-                tc_fence_after();
-                if (lane == 0) {
-                    const uint32_t a = smem_u32(smem + s * SH::STAGE), b = a + kF8A;
-#pragma unroll
-                    for (int kk = 0; kk < 4; ++kk)
-                        umma_f8(tmem_base + acc * BN, sdesc_sw128(a + kk * 32, 16, 1024),
-                                sdesc_sw128(b + kk * 32, 16, 1024), SH::IDESC, kk ? 1u : 0u);
-                    umma_commit(&empty[s]);
-                    umma_commit(&tfull[acc]);
+        if (lane == 0) {
+            const uint64_t ad0 = sdesc_sw128(smem_u32(smem), 16, 1024);
+            uint64_t ad = ad0;
+            uint32_t s = 0, ph = 0, blk = 0;
+            F8Walk at(p.n_tiles);
+            for (int t = blockIdx.x; ok && t < total; t += gridDim.x, at.next()) {
+                int n = p.K_blocks;
+                if constexpr (MODE == FP8_WGRAD) {
+                    const int g = at.q / ((p.M + 127) >> 7);
+                    n = offs[g + 1] - offs[g];
                 }
-                __syncwarp();
-                if (++s == STAGES) { s = 0; ph ^= 1u; }
+                for (int kb = 0; kb < n; ++kb, ++blk) {
+                    const uint32_t acc = blk % NACC, aph = (blk / NACC) & 1u;
+                    // (the operands are there long before the accumulator)
+                    if (!mbar_wait(&full[s], ph, wc) || !mbar_wait(&tempty[acc], aph ^ 1u, wc)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)   // descriptors count 16 bytes
+                        umma_f8(tmem_base + acc * BN, ad + 2 * kk, ad + kF8A / 16 + 2 * kk,
+                                SH::IDESC, kk ? 1u : 0u);
+                    umma_commit(&tfull[acc]);
+                    umma_commit(&empty[s]);
+                    ad += SH::STAGE / 16;
+                    if (++s == ST) { s = 0; ph ^= 1u; ad = ad0; }
+                }
             }
         }
+        ok = __shfl_sync(0xffffffffu, (int)ok, 0);
         if (!ok) {
             // every MMA this thread issued must finish before TMEM is freed
             if (lane == 0) umma_commit(done);
@@ -321,6 +361,7 @@ __global__ void __launch_bounds__(kF8Threads, 1) fp8_gemm_kernel(const __grid_co
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kF8RegsMany));
         const int q = warp & 3;                  // TMEM lane quadrant
         const int part = (warp - kF8Epi0) >> 2;  // its half of the columns
+        out_s += (warp - kF8Epi0) * SH::OUTS * kF8OutPiece;
         const int r_local = q * 32 + lane;
         uint32_t blk = 0;
         int it = 0;
@@ -329,34 +370,27 @@ __global__ void __launch_bounds__(kF8Threads, 1) fp8_gemm_kernel(const __grid_co
         // columns from 64 part and the 64 up columns 128 further on
         const int cl0 = MODE == FP8_FFN1 ? 64 * part : CW * part;
         constexpr int kHalf = MODE == FP8_FFN1 ? 128 : CW / 2;   // column step between halves
-        // scales of the tile; the next block's are loaded a block ahead, a tile's
-        // first ones (and its row weight) before the tile before it is written
+        // Scales.  Those of WGRAD come with the operands; the others of the next block
+        // are loaded a block ahead, a tile's first ones (and its row weight) before the
+        // tile before it is written.
         const float *sa = nullptr, *sb0 = nullptr, *sb1 = nullptr;
-        int sa_step = 1;
-        bool col_ok = false, valid = false;
+        bool valid = false;
         float na = 0.0f, nb0 = 0.0f, nb1 = 0.0f, nw = 1.0f;
-        float4 ncol = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         auto next_scales = [&](int kb) {
-            if (valid) na = __ldg(sa + (size_t)kb * sa_step);
-            if constexpr (MODE == FP8_WGRAD) {
-                if (col_ok) ncol = __ldg(reinterpret_cast<const float4 *>(sb0 + (size_t)kb * p.N));
-            } else {
-                nb0 = __ldg(sb0 + kb);
-                if constexpr (MODE == FP8_FFN1) nb1 = __ldg(sb1 + kb);
-            }
+            if (valid) na = __ldg(sa + kb);
+            nb0 = __ldg(sb0 + kb);
+            if constexpr (MODE == FP8_FFN1) nb1 = __ldg(sb1 + kb);
         };
+        uint32_t sc = 0;   // WGRAD: slot of the block's scales
         F8Tile ti{};
-        auto begin_tile = [&](int t) {
-            ti = f8_tile<MODE>(p, t, mt_start, offs, ti.g);
+        F8Walk at(p.n_tiles);
+        auto begin_tile = [&] {
+            ti = f8_tile<MODE>(p, at.q, at.nt, mt_start, offs, ti.g);
+            at.next();
             valid = r_local < ti.rows;
             const int row = ti.row0 + r_local;
-            if constexpr (MODE == FP8_WGRAD) {
-                sa = p.sa + (size_t)ti.k0 * p.M + row;
-                sa_step = p.M;
-                const int col = ti.nt * BN + cl0 + 4 * lane;
-                col_ok = 4 * lane < CW && col < p.N;
-                sb0 = p.sb + (size_t)ti.k0 * p.N + col;
-            } else if constexpr (MODE == FP8_FFN1) {
+            if constexpr (MODE == FP8_WGRAD) return;
+            if constexpr (MODE == FP8_FFN1) {
                 sa = p.sa + (size_t)row * p.K_blocks;
                 sb0 = p.sb + ((size_t)ti.g * p.nb_n + ti.nt) * p.K_blocks;
                 sb1 = sb0 + (size_t)(p.I / 128) * p.K_blocks;
@@ -366,9 +400,9 @@ __global__ void __launch_bounds__(kF8Threads, 1) fp8_gemm_kernel(const __grid_co
                 sb0 = p.sb + ((size_t)ti.g * p.nb_n + min(nb, p.nb_n - 1)) * p.K_blocks;
                 nw = valid && p.row_w && row < p.w_rows ? __ldg(p.row_w + row) : 1.0f;
             }
-            if (ti.kb > 0) next_scales(0);
+            next_scales(0);
         };
-        if ((int)blockIdx.x < total) begin_tile(blockIdx.x);
+        if ((int)blockIdx.x < total) begin_tile();
         for (int t = blockIdx.x; ok && t < total; t += gridDim.x, ++it) {
             uint64_t acc[CW / 2];
 #pragma unroll
@@ -378,7 +412,6 @@ __global__ void __launch_bounds__(kF8Threads, 1) fp8_gemm_kernel(const __grid_co
             constexpr int NCH = CW / CH;
             uint32_t r[2][CH];
             const uint32_t tq = tmem_base + ((uint32_t)(q * 32) << 16) + cl0;
-            float *cs = reinterpret_cast<float *>(side) + (warp - kF8Epi0) * CW;
             if (ti.kb > 0) {
                 ok = mbar_wait_warp(&tfull[blk % NACC], (blk / NACC) & 1u, wc);
                 if (!ok) break;
@@ -386,7 +419,17 @@ __global__ void __launch_bounds__(kF8Threads, 1) fp8_gemm_kernel(const __grid_co
                 tmem_ld(tq + (blk % NACC) * BN, r[0]);
             }
             for (int kb = 0; kb < ti.kb; ++kb, ++blk) {
-                const float f0 = MODE == FP8_WGRAD ? na : na * nb0, f1 = na * nb1;
+                const float *cs = reinterpret_cast<const float *>(side) + sc * (128 + BN);
+                float f0, f1;
+                if constexpr (MODE == FP8_WGRAD) {
+                    f0 = f1 = cs[r_local];
+                    cs += 128 + cl0;
+                    if (++sc == kF8Scales) sc = 0;
+                } else {
+                    f0 = na * nb0;
+                    f1 = na * nb1;
+                    if (kb + 1 < ti.kb) next_scales(kb + 1);
+                }
                 const uint64_t s0 = pair_f(f0, f0);
                 const uint64_t s1 = MODE == FP8_FFN1 ? pair_f(f1, f1) : s0;
                 float4 f[2][CH / 4];   // WGRAD: column scales of two chunks
@@ -395,13 +438,7 @@ __global__ void __launch_bounds__(kF8Threads, 1) fp8_gemm_kernel(const __grid_co
                     for (int j = 0; j < CH / 4; ++j)
                         f[c & 1][j] = *reinterpret_cast<const float4 *>(cs + c * CH + 4 * j);
                 };
-                if constexpr (MODE == FP8_WGRAD) {
-                    __syncwarp();
-                    if (4 * lane < CW) *reinterpret_cast<float4 *>(cs + 4 * lane) = ncol;
-                    __syncwarp();
-                    load_cs(0);
-                }
-                if (kb + 1 < ti.kb) next_scales(kb + 1);
+                if constexpr (MODE == FP8_WGRAD) load_cs(0);
                 const uint32_t a = blk % NACC;
 #pragma unroll
                 for (int c = 0; c < NCH; ++c) {
@@ -443,68 +480,59 @@ __global__ void __launch_bounds__(kF8Threads, 1) fp8_gemm_kernel(const __grid_co
             const bool cur_valid = valid;
             const int row = cur.row0 + r_local;
             const float w = nw;
-            if (t + (int)gridDim.x < total) begin_tile(t + gridDim.x);
-            if constexpr (MODE == FP8_ROWS) {
-                // 32 x 32 blocks turned in shared memory (16-byte pieces exchanged
-                // by row against bank conflicts), so that four lanes write the 64
-                // bytes of a row together
+            if (t + (int)gridDim.x < total) begin_tile();
+            if constexpr (MODE != FP8_FFN1) {
+                // 128 bytes of each row at a time: through shared memory, from where one
+                // thread's TMA store takes all 32 rows during the next tile; rows at a
+                // group's end that are not 32 straight from the registers
+                constexpr int EB = MODE == FP8_ROWS ? 2 : 4;   // bytes of a value
+                constexpr int PC = 128 / EB;                   // values of a piece
                 const int col0 = cur.nt * BN + cl0;
-                const uint32_t blk_s = smem_u32(out_s) + (warp - kF8Epi0) * SH::OUT;
-                const int wr = lane >> 2, wc4 = lane & 3;
+                const bool whole = q * 32 + 32 <= cur.rows;
+                auto sixteen = [&](int i) {   // bytes 16 i .. of this thread's row
+                    uint4 v;
+                    if constexpr (MODE == FP8_ROWS) {
+                        const uint64_t *a = acc + 4 * i;
+                        v.x = pack_bf16x2(w * lo_f(a[0]), w * hi_f(a[0]));
+                        v.y = pack_bf16x2(w * lo_f(a[1]), w * hi_f(a[1]));
+                        v.z = pack_bf16x2(w * lo_f(a[2]), w * hi_f(a[2]));
+                        v.w = pack_bf16x2(w * lo_f(a[3]), w * hi_f(a[3]));
+                    } else {
+                        const uint64_t *a = acc + 2 * i;
+                        v = make_uint4((uint32_t)a[0], (uint32_t)(a[0] >> 32), (uint32_t)a[1],
+                                       (uint32_t)(a[1] >> 32));
+                    }
+                    return v;
+                };
+                const size_t out_row = MODE == FP8_ROWS ? row : (size_t)cur.g * p.M + row;
+                if (whole) {
 #pragma unroll
-                for (int b = 0; b < CW / 32; ++b) {
-                    if (col0 + 32 * b >= p.N) break;
-                    __syncwarp();
+                    for (int s = 0; s < CW / PC; ++s) {
+                        uint8_t *o = out_s + s % SH::OUTS * kF8OutPiece;
+                        // this buffer's last store has been read
+                        if (lane == 0) bulk_wait_group_read<SH::OUTS - 1>();
+                        __syncwarp();
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        uint32_t w4[4];
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const uint64_t v = acc[16 * b + 4 * j + e];
-                            w4[e] = pack_bf16x2(w * lo_f(v), w * hi_f(v));
+                        for (int j = 0; j < 8; ++j)
+                            *reinterpret_cast<uint4 *>(o + lane * 128 + ((j ^ (lane & 7)) << 4)) =
+                                sixteen(8 * s + j);
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) {
+                            if (col0 + PC * s < p.N)
+                                tma_store_2d(&p.tmO, o, col0 + PC * s, (int)out_row);
+                            bulk_commit_group();   // empty past the last column
                         }
-                        st_shared_v4(blk_s + lane * 64 + (((uint32_t)j ^ ((lane >> 1) & 3u)) << 4),
-                                     w4[0], w4[1], w4[2], w4[3]);
                     }
-                    __syncwarp();
-                    const int col = col0 + 32 * b + 8 * wc4;
+                } else if (cur_valid) {
+                    uint8_t *dst = (MODE == FP8_ROWS ? reinterpret_cast<uint8_t *>(p.out)
+                                                     : reinterpret_cast<uint8_t *>(p.dW)) +
+                                   (out_row * p.N + col0) * EB;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int rr = 8 * i + wr;
-                        const uint4 v = ld_shared_v4(
-                            blk_s + rr * 64 + (((uint32_t)wc4 ^ ((rr >> 1) & 3u)) << 4));
-                        if (q * 32 + rr < cur.rows && col < p.N)
-                            st_global_v4(p.out + (size_t)(cur.row0 + q * 32 + rr) * p.N + col, v.x,
-                                         v.y, v.z, v.w);
-                    }
-                }
-            } else if constexpr (MODE == FP8_WGRAD) {
-                // likewise, eight lanes to the 128 bytes of a row
-                const int col0 = cur.nt * BN + cl0;
-                const uint32_t blk_s = smem_u32(out_s) + (warp - kF8Epi0) * SH::OUT;
-                const int wr = lane >> 3, wc8 = lane & 7;
-#pragma unroll
-                for (int b = 0; b < CW / 32; ++b) {
-                    if (col0 + 32 * b >= p.N) break;
-                    __syncwarp();
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const uint64_t v0 = acc[16 * b + 2 * j], v1 = acc[16 * b + 2 * j + 1];
-                        st_shared_v4(blk_s + lane * 128 + (((uint32_t)j ^ (lane & 7u)) << 4),
-                                     (uint32_t)v0, (uint32_t)(v0 >> 32), (uint32_t)v1,
-                                     (uint32_t)(v1 >> 32));
-                    }
-                    __syncwarp();
-                    const int col = col0 + 32 * b + 4 * wc8;
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const int rr = 4 * i + wr;
-                        const uint4 v =
-                            ld_shared_v4(blk_s + rr * 128 + (((uint32_t)wc8 ^ (rr & 7u)) << 4));
-                        if (q * 32 + rr < cur.rows && col < p.N)
-                            st_global_v4(p.dW + ((size_t)cur.g * p.M + cur.row0 + q * 32 + rr) * p.N +
-                                             col,
-                                         v.x, v.y, v.z, v.w);
+                    for (int i = 0; i < CW * EB / 16; ++i) {
+                        const uint4 v = sixteen(i);
+                        if (col0 + i * (16 / EB) < p.N)
+                            st_global_v4(dst + 16 * i, v.x, v.y, v.z, v.w);
                     }
                 }
             } else {
@@ -546,31 +574,34 @@ __global__ void __launch_bounds__(kF8Threads, 1) fp8_gemm_kernel(const __grid_co
         }
     }
 
+    // a thread's last pieces have left shared memory
+    if (MODE != FP8_FFN1 && lane == 0) bulk_wait_group_all();
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     if (warp == 1) tmem_dealloc(tmem_base, NACC * BN);
 }
 
-template <int MODE, int BN>
+template <int MODE, int BN, int ST>
 moe_status launch_fp8(Fp8Params &p, long long max_tiles, cudaStream_t st) {
-    auto kern = fp8_gemm_kernel<MODE, BN>;
+    auto kern = fp8_gemm_kernel<MODE, BN, ST>;
     static bool attr_set[64] = {};
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return MOE_ERR_CUDA;
     if (dev < 0 || dev >= 64) return MOE_ERR_UNSUPPORTED;
     if (!attr_set[dev]) {
         if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 fp8_smem_bytes<MODE, BN>(kMaxGroups)) != cudaSuccess)
+                                 kF8Smem) != cudaSuccess)
             return MOE_ERR_CUDA;
         attr_set[dev] = true;
     }
+    static_assert(F8Shape<MODE, BN, ST>::smem(kMaxGroups) <= kF8Smem, "shared memory");
     if (max_tiles <= 0) return MOE_OK;
     p.status = device_status_ptr();
     if (!p.status) return MOE_ERR_CUDA;
     p.wait_limit = kWaitLimitCycles;
     const int grid = max_tiles < num_sms() ? (int)max_tiles : num_sms();
-    kern<<<grid, kF8Threads, fp8_smem_bytes<MODE, BN>(p.G), st>>>(p);
+    kern<<<grid, kF8Threads, F8Shape<MODE, BN, ST>::smem(p.G), st>>>(p);
     return cuda_status(cudaGetLastError());
 }
 
@@ -590,7 +621,8 @@ moe_status launch_fp8_matmul(const uint8_t *aq, const float *as, const int32_t *
     std::memset(&p, 0, sizeof p);
     const int BN = rows_bn(max_rows, G, N);
     if (!encode_tmap_u8_2d(&p.tmA, aq, K, max_rows, K, 128, 128, 128) ||
-        !encode_tmap_u8_2d(&p.tmB, bq, K, (uint64_t)G * N, K, 128, BN, 128))
+        !encode_tmap_u8_2d(&p.tmB, bq, K, (uint64_t)G * N, K, 128, BN, 128) ||
+        !encode_tmap_bf16_2d(&p.tmO, out, N, max_rows, 2ULL * N, 64, 32))
         return MOE_ERR_CUDA;
     p.offsets = offsets;
     p.sa = as;
@@ -604,8 +636,8 @@ moe_status launch_fp8_matmul(const uint8_t *aq, const float *as, const int32_t *
     p.w_rows = w_rows;
     p.out = out;
     const long long tiles = (long long)row_tile_bound(max_rows, G) * p.n_tiles;
-    return BN == 256 ? launch_fp8<FP8_ROWS, 256>(p, tiles, st)
-                     : launch_fp8<FP8_ROWS, 128>(p, tiles, st);
+    return BN == 256 ? launch_fp8<FP8_ROWS, 256, 3>(p, tiles, st)
+                     : launch_fp8<FP8_ROWS, 128, 5>(p, tiles, st);
 }
 
 moe_status launch_fp8_ffn1(const uint8_t *xq, const float *xs, const int32_t *offsets, int G,
@@ -628,17 +660,18 @@ moe_status launch_fp8_ffn1(const uint8_t *xq, const float *xs, const int32_t *of
     p.clamp = clamp;
     p.hq = hq;
     p.hs = hs;
-    return launch_fp8<FP8_FFN1, 256>(p, (long long)row_tile_bound(max_rows, G) * p.n_tiles, st);
+    return launch_fp8<FP8_FFN1, 256, 4>(p, (long long)row_tile_bound(max_rows, G) * p.n_tiles, st);
 }
 
 moe_status launch_fp8_wgrad(const uint8_t *aq, const float *as, const uint8_t *bq, const float *bs,
                             const int32_t *first, int G, int max_chunks, int M, int N, float *dW,
                             cudaStream_t st) {
-    constexpr int BN = 128;   // a tile's output fits the staging blocks: see the top
+    constexpr int BN = 256;
     Fp8Params p;
     std::memset(&p, 0, sizeof p);
     if (!encode_tmap_u8_2d(&p.tmA, aq, 128, (uint64_t)max_chunks * M, 128, 128, 128, 128) ||
-        !encode_tmap_u8_2d(&p.tmB, bq, 128, (uint64_t)max_chunks * N, 128, 128, BN, 128))
+        !encode_tmap_u8_2d(&p.tmB, bq, 128, (uint64_t)max_chunks * N, 128, 128, BN, 128) ||
+        !encode_tmap_f32_2d(&p.tmO, dW, N, (uint64_t)G * M, 4ULL * N, 32, 32))
         return MOE_ERR_CUDA;
     p.offsets = first;
     p.sa = as;
@@ -648,7 +681,7 @@ moe_status launch_fp8_wgrad(const uint8_t *aq, const float *as, const uint8_t *b
     p.N = N;
     p.n_tiles = (N + BN - 1) / BN;
     p.dW = dW;
-    return launch_fp8<FP8_WGRAD, 128>(p, (long long)G * ((M + 127) / 128) * p.n_tiles, st);
+    return launch_fp8<FP8_WGRAD, BN, 3>(p, (long long)G * ((M + 127) / 128) * p.n_tiles, st);
 }
 
 }  // namespace moe

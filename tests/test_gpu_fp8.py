@@ -151,7 +151,8 @@ def check(got, ref, absdot, K, bf16_out, what):
 
 MATMULS = [([1], 8, 16), ([1], 512, 4096), ([3], 136, 400), ([128], 256, 128), ([129, 0, 1, 260], 264, 272),
            ([17, 40, 0, 200, 5], 640, 1152), ([0, 0], 64, 64), ([300], 1000, 2048), ([2] * 40, 72, 144),
-           ([32], 384, 512), ([33], 384, 512), ([31, 0, 1], 264, 656)]
+           ([32], 384, 512), ([33], 384, 512), ([31, 0, 1], 264, 656),
+           ([650, 100, 0, 700], 520, 400), ([513], 264, 1040)]
 
 
 @pytest.mark.parametrize("counts,N,K", MATMULS)
@@ -293,7 +294,7 @@ def test_linear_and_its_gradients():
 # ---------------------------------------------------------------------- FFN
 
 @pytest.mark.parametrize("counts,d,I", [([1], 128, 128), ([130, 0, 1, 77], 256, 128),
-                                        ([64, 200], 384, 640), ([3, 2, 9], 512, 256)])
+                                        ([64, 200], 384, 640), ([3, 2, 9], 512, 256), ([520, 129, 385], 256, 384)])
 def test_ffn(counts, d, I):
     rng = np.random.default_rng(d + I)
     G, rows, clamp = len(counts), sum(counts), 2.0
