@@ -1008,24 +1008,6 @@ FewWorkspace carve_few(uint8_t *base, int T, int d, int E, int k, int I) {
     return w;
 }
 
-// A launch that may begin before the kernel ahead of it in the stream ends
-// (programmatic dependent launch).
-moe_status launch_early(void (*kern)(FewParams), dim3 grid, int threads, int smem,
-                        const FewParams &p, cudaStream_t st) {
-    cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3(threads, 1, 1);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = st;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, kern, p) != cudaSuccess) return MOE_ERR_CUDA;
-    return cuda_status(cudaGetLastError());
-}
-
 template <bool FP8, int NT>
 moe_status launch_experts(const FewParams &p, cudaStream_t st) {
     using SH = FewShape<FP8, NT>;
@@ -1042,7 +1024,7 @@ moe_status launch_experts(const FewParams &p, cudaStream_t st) {
     }
     const long long items = (long long)(p.T * p.k + 1) * (p.I / 8 + p.d / 16);
     return launch_early(kern, dim3((unsigned)(items < num_sms() ? items : num_sms())), kFewThreads,
-                        SH::SMEM, p, st);
+                        SH::SMEM, st, p);
 }
 
 template <bool FP8>
@@ -1136,7 +1118,7 @@ moe_status launch_few(const moe_few_args *a, cudaStream_t st) {
         launch_early(p.E <= 128   ? few_gate_kernel<4>
                      : p.E <= 384 ? few_gate_kernel<12>
                                   : few_gate_kernel<32>,
-                     grid, kGateWarps * 32, 0, p, st);
+                     grid, kGateWarps * 32, 0, st, p);
     if (s != MOE_OK) return s;
     return fp8 ? launch_experts_nt<true>(p, st) : launch_experts_nt<false>(p, st);
 }

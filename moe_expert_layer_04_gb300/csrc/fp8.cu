@@ -29,6 +29,8 @@ constexpr int kRowU = 2;
 __global__ void __launch_bounds__(256)
     fp8_rows_kernel(const uint16_t *__restrict__ x, const int32_t *__restrict__ slot_row,
                     long long T, int K, int k, uint8_t *__restrict__ q, float *__restrict__ s) {
+    wait_for_kernels_ahead();
+    let_kernels_behind_begin();
     const int lane = threadIdx.x & 31;
     const int nb = fp8_blocks(K);
     const int chunks = (K + kRowU * 512 - 1) / (kRowU * 512);
@@ -145,6 +147,8 @@ __global__ void __launch_bounds__(256)
                        float *__restrict__ s, uint8_t *__restrict__ qt, float *__restrict__ st) {
     __shared__ __align__(16) uint32_t stage[128 * 32];
     __shared__ uint32_t part[8];
+    wait_for_kernels_ahead();
+    let_kernels_behind_begin();
     const int nbn = fp8_blocks(N), nbk = fp8_blocks(K);
     const int bk = blockIdx.x % nbk;
     const long long rest = blockIdx.x / nbk;
@@ -211,6 +215,8 @@ __global__ void __launch_bounds__(256)
     __shared__ __align__(16) uint32_t stage[128 * 32];
     __shared__ __align__(16) uint32_t part[8][64];   // per warp: bf16 pair maxima of 128 columns
     __shared__ __align__(16) float factor[128];
+    wait_for_kernels_ahead();
+    let_kernels_behind_begin();
     const int b = blockIdx.y;
     if (b >= first[G]) return;
     int lo = 0, hi = G - 1;                          // the chunk's group
@@ -270,6 +276,8 @@ __global__ void __launch_bounds__(256)
 // first[g]: chunks of 128 rows before group g; first[G] their number.  One warp.
 __global__ void fp8_chunks_kernel(const int32_t *__restrict__ offsets, int G,
                                   int32_t *__restrict__ first) {
+    wait_for_kernels_ahead();
+    let_kernels_behind_begin();
     const int lane = threadIdx.x;
     int carry = 0;
     for (int base = 0; base <= G; base += 32) {
@@ -293,29 +301,27 @@ moe_status launch_fp8_rows(const uint16_t *x, const int32_t *slot_row, long long
     const long long units = T * ((K + kRowU * 512 - 1) / (kRowU * 512));
     const long long want = (units + 7) / 8;
     const long long most = (long long)num_sms() * 64;
-    fp8_rows_kernel<<<(int)(want < most ? want : most), 256, 0, st>>>(x, slot_row, T, K, k, q, s);
-    return cuda_status(cudaGetLastError());
+    return launch_early(fp8_rows_kernel, dim3((unsigned)(want < most ? want : most)), 256, 0, st, x,
+                        slot_row, T, K, k, q, s);
 }
 
 moe_status launch_fp8_weights(const uint16_t *src, int G, int N, int K, uint8_t *q, float *s,
                               uint8_t *qt, float *s_t, cudaStream_t st) {
     const long long tiles = (long long)G * fp8_blocks(N) * fp8_blocks(K);
     if (tiles > 0x7FFFFFFFLL) return MOE_ERR_UNSUPPORTED;
-    fp8_weights_kernel<<<(int)tiles, 256, 0, st>>>(src, N, K, q, s, qt, s_t);
-    return cuda_status(cudaGetLastError());
+    return launch_early(fp8_weights_kernel, dim3((unsigned)tiles), 256, 0, st, src, N, K, q, s, qt,
+                        s_t);
 }
 
 moe_status launch_fp8_chunks(const int32_t *offsets, int G, int32_t *first, cudaStream_t st) {
-    fp8_chunks_kernel<<<1, 32, 0, st>>>(offsets, G, first);
-    return cuda_status(cudaGetLastError());
+    return launch_early(fp8_chunks_kernel, dim3(1), 32, 0, st, offsets, G, first);
 }
 
 moe_status launch_fp8_columns(const uint16_t *src, const int32_t *offsets, const int32_t *first,
                               int G, int max_chunks, int C, uint8_t *qt, float *s_t,
                               cudaStream_t st) {
     const dim3 grid(fp8_blocks(C), max_chunks);
-    fp8_columns_kernel<<<grid, 256, 0, st>>>(src, offsets, first, G, C, qt, s_t);
-    return cuda_status(cudaGetLastError());
+    return launch_early(fp8_columns_kernel, grid, 256, 0, st, src, offsets, first, G, C, qt, s_t);
 }
 
 }  // namespace moe

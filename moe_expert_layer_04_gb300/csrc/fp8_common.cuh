@@ -18,6 +18,7 @@
 
 #include <cuda_fp16.h>
 
+#include "moe_internal.h"
 #include "moe_ptx.cuh"
 
 namespace moe {
@@ -71,6 +72,32 @@ __device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t b
             "r"(smem_u32(dst)),
         "l"(src), "r"(bytes), "r"(smem_u32(bar))
         : "memory");
+}
+
+// A launch that may begin before the kernel ahead of it in the stream ends
+// (programmatic dependent launch), which hides its latency; such a kernel touches
+// nothing in memory before wait_for_kernels_ahead().
+template <typename... P, typename... A>
+inline moe_status launch_early(void (*kern)(P...), dim3 grid, int threads, int smem,
+                               cudaStream_t st, A... args) {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads, 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, kern, P(args)...) != cudaSuccess) return MOE_ERR_CUDA;
+    return cuda_status(cudaGetLastError());
+}
+__device__ __forceinline__ void wait_for_kernels_ahead() {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+__device__ __forceinline__ void let_kernels_behind_begin() {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
 }  // namespace moe

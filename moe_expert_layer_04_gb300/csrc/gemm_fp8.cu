@@ -26,6 +26,7 @@
 // Every wait is bounded; on a timeout the CTA records MOE_ERR_TIMEOUT, drains
 // its copies and MMAs, frees tensor memory and returns.
 #include <cstring>
+#include <type_traits>
 
 #include "fp8_common.cuh"
 #include "gemm_launch.cuh"
@@ -36,13 +37,14 @@ namespace {
 enum Fp8Mode : int { FP8_ROWS = 0, FP8_FFN1 = 1, FP8_WGRAD = 2 };
 
 struct Fp8Params {
-    CUtensorMap tmA;   // A codes: [rows, K] (WGRAD [chunks * M, 128]), boxes 128 x 128
+    CUtensorMap tmA;   // A codes: [rows, K] (WGRAD [chunks * M, 128]), boxes a_rows x 128
     CUtensorMap tmB;   // B codes: [G * N, K] (WGRAD [chunks * N, 128]), boxes 128 x 256 (FFN1 128)
     CUtensorMap tmO;   // ROWS, WGRAD: output, boxes of 32 rows x 128 bytes
     const int32_t *offsets;   // [G+1] rows of the groups; WGRAD: their chunks
     const float *sa, *sb;
     int G, N, K_blocks, n_tiles;
     int nb_n;                 // scale rows of one group's B
+    int a_rows;               // of A's boxes
     int M;                    // WGRAD: output rows
     int I;                    // FFN1
     float clamp;
@@ -78,32 +80,56 @@ static_assert(4 * kF8RegsFew + 8 * kF8RegsMany <= 12 * 168, "register split");
 template <int MODE, int BN, int ST>
 struct F8Shape {
     static constexpr int STAGE = kF8A + BN * 128;
-    static constexpr int NACC = 512 / BN;            // accumulators in tensor memory
+    static constexpr int NACC = BN == 256 ? 2 : 4;   // accumulators in tensor memory
     static constexpr int CW = BN / 2;                // columns of an epilogue warp
-    static constexpr int CH = MODE == FP8_WGRAD ? 16 : 32;   // of them in flight at a time
+    static constexpr int CH = MODE == FP8_WGRAD ? 16 : BN < 128 ? CW : 32;   // of them in flight at a time
     static constexpr uint32_t IDESC =
         (1u << 4) | ((uint32_t)(BN >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
     // FFN1: exchange of the largest |h|; WGRAD: ring of both operands' scales
     static constexpr int SIDE =
         MODE == FP8_FFN1 ? 2048 : MODE == FP8_WGRAD ? kF8Scales * (128 + BN) * 4 : 0;
     // pieces of output on their way to memory, for each epilogue warp
-    static constexpr int OUTS = MODE == FP8_FFN1 ? 0 : BN == 256 ? 2 : 1;
+    static constexpr int OUTS = MODE == FP8_FFN1 || BN < 128 ? 0 : BN / 128;
     static constexpr int OUT = kF8Epi * OUTS * kF8OutPiece;
     static constexpr int GROUP = MODE == FP8_WGRAD ? 4 : 8;   // bytes of a group's offset and first tile
     static constexpr int FIXED = ST * STAGE + OUT + SIDE + kF8Bars;
     static constexpr int smem(int G) { return 1024 + FIXED + GROUP * (G + 2); }
 };
 
-// D[tmem] (+)= A[smem] B[smem]^T, E4M3 operands (K = 32), fp32 accumulator.
+// One block of 128: D[tmem] = A[smem] B[smem]^T in four steps of K = 32, E4M3
+// operands, fp32 accumulator; then both barriers are to hear of its end.  Called by a
+// whole warp, which elects the issuing thread here: with uniform control flow around
+// it the descriptors stay in uniform registers (inside `if (lane == 0)` the six
+// instructions took 400 cycles, time that the tensor core waited for).
 // Instruction descriptor: D format [4,6) = 1 (fp32), A and B format 0 (E4M3),
-// both K-major, N >> 3 at [17,23), M >> 4 at [24,29).
-__device__ __forceinline__ void umma_f8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
-                                        uint32_t idesc, uint32_t accumulate) {
+// both K-major, N >> 3 at [17,23), M >> 4 at [24,29).  Matrix descriptors count 16 bytes.
+__device__ __forceinline__ void umma_f8_block(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                              uint32_t idesc, uint64_t *bar0, uint64_t *bar1) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        "{\n\t.reg .pred e, f, t;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "setp.ne.b32 f, 0, 0;\n\t"
+        "setp.eq.b32 t, 0, 0;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %5, %9, f;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %2, %6, %9, t;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %3, %7, %9, t;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %4, %8, %9, t;\n\t"
+        "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%10];\n\t"
+        "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%11];\n\t}" ::"r"(
+            d_tmem),
+        "l"(a_desc), "l"(a_desc + 2), "l"(a_desc + 4), "l"(a_desc + 6), "l"(b_desc),
+        "l"(b_desc + 2), "l"(b_desc + 4), "l"(b_desc + 6), "r"(idesc), "r"(smem_u32(bar0)),
+        "r"(smem_u32(bar1))
+        : "memory");
+}
+
+// (the same thread, as a warp's election has one outcome)
+__device__ __forceinline__ void umma_commit_elected(uint64_t *bar) {
+    asm volatile(
+        "{\n\t.reg .pred e;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(
+            smem_u32(bar))
         : "memory");
 }
 
@@ -211,7 +237,7 @@ __global__ void __launch_bounds__(kF8Threads, 1) fp8_gemm_kernel(const __grid_co
     int *offs = reinterpret_cast<int *>(side + SH::SIDE + kF8Bars);
     int *mt_start = offs + (p.G + 1);
 
-    const int warp = threadIdx.x >> 5;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);   // uniform, to the compiler too
     const int lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
@@ -236,6 +262,7 @@ __global__ void __launch_bounds__(kF8Threads, 1) fp8_gemm_kernel(const __grid_co
         tmem_alloc(tmem_base_s, NACC * BN);
         tmem_relinquish();
     }
+    wait_for_kernels_ahead();
     if (warp == 2) {
         // group offsets and the exclusive prefix of their 128-row tiles
         int carry = 0;
@@ -257,6 +284,7 @@ __global__ void __launch_bounds__(kF8Threads, 1) fp8_gemm_kernel(const __grid_co
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    let_kernels_behind_begin();
 
     const uint32_t tmem_base = *tmem_base_s;
     const WaitCtl wc{abort_s, p.status, p.wait_limit};
@@ -282,7 +310,7 @@ __global__ void __launch_bounds__(kF8Threads, 1) fp8_gemm_kernel(const __grid_co
                         sa_bytes = 4 * min(128, p.M - ti.row0);
                         sb_bytes = 4 * min(BN, p.N - ti.nt * BN);
                     }
-                    mbar_arrive_expect_tx(&full[s], SH::STAGE + sa_bytes + sb_bytes);
+                    mbar_arrive_expect_tx(&full[s], p.a_rows * 128 + BN * 128 + sa_bytes + sb_bytes);
                     uint8_t *a = smem + s * SH::STAGE;
                     uint8_t *b = a + kF8A;
                     if constexpr (MODE == FP8_WGRAD) {
@@ -315,44 +343,37 @@ __global__ void __launch_bounds__(kF8Threads, 1) fp8_gemm_kernel(const __grid_co
                     mbar_wait_teardown(&full[i], begun >> i & 1u, p.wait_limit);
         }
     } else if (warp == 1) {
-        // One thread: what it costs from the release of an accumulator to its next
-        // MMA is time in which the tensor core has nothing to do.
+        // What it costs from the release of an accumulator to its next MMA is time
+        // in which the tensor core has nothing to do.
+        const uint64_t ad0 = sdesc_sw128(smem_u32(smem), 16, 1024);
+        uint64_t ad = ad0;
+        uint32_t s = 0, ph = 0, blk = 0;
         bool ok = true;
-        if (lane == 0) {
-            const uint64_t ad0 = sdesc_sw128(smem_u32(smem), 16, 1024);
-            uint64_t ad = ad0;
-            uint32_t s = 0, ph = 0, blk = 0;
-            F8Walk at(p.n_tiles);
-            for (int t = blockIdx.x; ok && t < total; t += gridDim.x, at.next()) {
-                int n = p.K_blocks;
-                if constexpr (MODE == FP8_WGRAD) {
-                    const int g = at.q / ((p.M + 127) >> 7);
-                    n = offs[g + 1] - offs[g];
+        F8Walk at(p.n_tiles);
+        for (int t = blockIdx.x; ok && t < total; t += gridDim.x, at.next()) {
+            int n = p.K_blocks;
+            if constexpr (MODE == FP8_WGRAD) {
+                const int g = at.q / ((p.M + 127) >> 7);
+                n = __shfl_sync(0xffffffffu, offs[g + 1] - offs[g], 0);
+            }
+            for (int kb = 0; kb < n; ++kb, ++blk) {
+                const uint32_t acc = blk % NACC, aph = (blk / NACC) & 1u;
+                // (the operands are there long before the accumulator)
+                if (!mbar_wait_warp(&full[s], ph, wc) ||
+                    !mbar_wait_warp(&tempty[acc], aph ^ 1u, wc)) {
+                    ok = false;
+                    break;
                 }
-                for (int kb = 0; kb < n; ++kb, ++blk) {
-                    const uint32_t acc = blk % NACC, aph = (blk / NACC) & 1u;
-                    // (the operands are there long before the accumulator)
-                    if (!mbar_wait(&full[s], ph, wc) || !mbar_wait(&tempty[acc], aph ^ 1u, wc)) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
-#pragma unroll
-                    for (int kk = 0; kk < 4; ++kk)   // descriptors count 16 bytes
-                        umma_f8(tmem_base + acc * BN, ad + 2 * kk, ad + kF8A / 16 + 2 * kk,
-                                SH::IDESC, kk ? 1u : 0u);
-                    umma_commit(&tfull[acc]);
-                    umma_commit(&empty[s]);
-                    ad += SH::STAGE / 16;
-                    if (++s == ST) { s = 0; ph ^= 1u; ad = ad0; }
-                }
+                tc_fence_after();
+                umma_f8_block(tmem_base + acc * BN, ad, ad + kF8A / 16, SH::IDESC, &tfull[acc],
+                              &empty[s]);
+                ad += SH::STAGE / 16;
+                if (++s == ST) { s = 0; ph ^= 1u; ad = ad0; }
             }
         }
-        ok = __shfl_sync(0xffffffffu, (int)ok, 0);
         if (!ok) {
             // every MMA this thread issued must finish before TMEM is freed
-            if (lane == 0) umma_commit(done);
-            __syncwarp();
+            umma_commit_elected(done);
             mbar_wait_teardown(done, 0, p.wait_limit);
         }
     }
@@ -418,7 +439,9 @@ __global__ void __launch_bounds__(kF8Threads, 1) fp8_gemm_kernel(const __grid_co
                 tc_fence_after();
                 tmem_ld(tq + (blk % NACC) * BN, r[0]);
             }
-            for (int kb = 0; kb < ti.kb; ++kb, ++blk) {
+            // block kb, its first chunk in r[b0]
+            auto block = [&](int kb, auto b0c) {
+                constexpr int b0 = decltype(b0c)::value;
                 const float *cs = reinterpret_cast<const float *>(side) + sc * (128 + BN);
                 float f0, f1;
                 if constexpr (MODE == FP8_WGRAD) {
@@ -439,41 +462,44 @@ __global__ void __launch_bounds__(kF8Threads, 1) fp8_gemm_kernel(const __grid_co
                         f[c & 1][j] = *reinterpret_cast<const float4 *>(cs + c * CH + 4 * j);
                 };
                 if constexpr (MODE == FP8_WGRAD) load_cs(0);
-                const uint32_t a = blk % NACC;
+                const uint32_t a = blk++ % NACC;
 #pragma unroll
                 for (int c = 0; c < NCH; ++c) {
+                    uint32_t(&now)[CH] = r[(b0 + c) & 1], (&next)[CH] = r[(b0 + c + 1) & 1];
                     tmem_wait_ld();
                     if (c < NCH - 1) {
-                        constexpr int kPer = NCH / 2;   // chunks of a half
-                        tmem_ld(tq + a * BN + (c + 1) / kPer * kHalf + (c + 1) % kPer * CH,
-                                r[(c + 1) & 1]);
+                        constexpr int kPer = MODE == FP8_FFN1 ? NCH / 2 : NCH;   // to kHalf
+                        tmem_ld(tq + a * BN + (c + 1) / kPer * kHalf + (c + 1) % kPer * CH, next);
                         if constexpr (MODE == FP8_WGRAD) load_cs(c + 1);
                     } else {
                         tc_fence_before();
                         __syncwarp();
                         if (lane == 0) mbar_arrive(&tempty[a]);
                         if (kb + 1 < ti.kb) {
-                            const uint32_t b1 = blk + 1;
-                            ok = mbar_wait_warp(&tfull[b1 % NACC], (b1 / NACC) & 1u, wc);
-                            if (!ok) break;
+                            ok = mbar_wait_warp(&tfull[blk % NACC], (blk / NACC) & 1u, wc);
+                            if (!ok) return;
                             tc_fence_after();
-                            tmem_ld(tq + (b1 % NACC) * BN, r[0]);
+                            tmem_ld(tq + (blk % NACC) * BN, next);
                         }
                     }
 #pragma unroll
                     for (int j = 0; j < CH / 2; j += 2) {
-                        uint64_t v0 = pair(r[c & 1][2 * j], r[c & 1][2 * j + 1]);
-                        uint64_t v1 = pair(r[c & 1][2 * j + 2], r[c & 1][2 * j + 3]);
+                        uint64_t v0 = pair(now[2 * j], now[2 * j + 1]);
+                        uint64_t v1 = pair(now[2 * j + 2], now[2 * j + 3]);
                         if constexpr (MODE == FP8_WGRAD) {
                             const float4 s = f[c & 1][j / 2];
                             v0 = mul2(v0, pair_f(s.x, s.y));
                             v1 = mul2(v1, pair_f(s.z, s.w));
                         }
-                        fma2(acc[c * (CH / 2) + j], v0, c < NCH / 2 ? s0 : s1);
-                        fma2(acc[c * (CH / 2) + j + 1], v1, c < NCH / 2 ? s0 : s1);
+                        const uint64_t s = MODE == FP8_FFN1 && c >= NCH / 2 ? s1 : s0;
+                        fma2(acc[c * (CH / 2) + j], v0, s);
+                        fma2(acc[c * (CH / 2) + j + 1], v1, s);
                     }
                 }
-                if (!ok) break;
+            };
+            for (int kb = 0; ok && kb < ti.kb;) {
+                block(kb++, std::integral_constant<int, 0>());
+                if (NCH % 2 == 1 && ok && kb < ti.kb) block(kb++, std::integral_constant<int, 1>());
             }
             if (!ok) break;
             const F8Tile cur = ti;
@@ -488,7 +514,7 @@ __global__ void __launch_bounds__(kF8Threads, 1) fp8_gemm_kernel(const __grid_co
                 constexpr int EB = MODE == FP8_ROWS ? 2 : 4;   // bytes of a value
                 constexpr int PC = 128 / EB;                   // values of a piece
                 const int col0 = cur.nt * BN + cl0;
-                const bool whole = q * 32 + 32 <= cur.rows;
+                const bool whole = SH::OUTS > 0 && q * 32 + 32 <= cur.rows;
                 auto sixteen = [&](int i) {   // bytes 16 i .. of this thread's row
                     uint4 v;
                     if constexpr (MODE == FP8_ROWS) {
@@ -506,11 +532,12 @@ __global__ void __launch_bounds__(kF8Threads, 1) fp8_gemm_kernel(const __grid_co
                 };
                 const size_t out_row = MODE == FP8_ROWS ? row : (size_t)cur.g * p.M + row;
                 if (whole) {
+                    constexpr int OUTS = SH::OUTS > 0 ? SH::OUTS : 1;
 #pragma unroll
                     for (int s = 0; s < CW / PC; ++s) {
-                        uint8_t *o = out_s + s % SH::OUTS * kF8OutPiece;
+                        uint8_t *o = out_s + s % OUTS * kF8OutPiece;
                         // this buffer's last store has been read
-                        if (lane == 0) bulk_wait_group_read<SH::OUTS - 1>();
+                        if (lane == 0) bulk_wait_group_read<OUTS - 1>();
                         __syncwarp();
 #pragma unroll
                         for (int j = 0; j < 8; ++j)
@@ -575,7 +602,7 @@ __global__ void __launch_bounds__(kF8Threads, 1) fp8_gemm_kernel(const __grid_co
     }
 
     // a thread's last pieces have left shared memory
-    if (MODE != FP8_FFN1 && lane == 0) bulk_wait_group_all();
+    if (SH::OUTS > 0 && lane == 0) bulk_wait_group_all();
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -601,17 +628,32 @@ moe_status launch_fp8(Fp8Params &p, long long max_tiles, cudaStream_t st) {
     if (!p.status) return MOE_ERR_CUDA;
     p.wait_limit = kWaitLimitCycles;
     const int grid = max_tiles < num_sms() ? (int)max_tiles : num_sms();
-    kern<<<grid, kF8Threads, F8Shape<MODE, BN, ST>::smem(p.G), st>>>(p);
-    return cuda_status(cudaGetLastError());
+    return launch_early(kern, dim3(grid), kF8Threads, F8Shape<MODE, BN, ST>::smem(p.G), st, p);
 }
 
 }  // namespace
 
-// 256-wide tiles read fewer operand bytes for a product; 128-wide ones spread
-// over the SMs where there are few of them.
+// Rows of A's boxes: no more than there are (the MMAs' other rows take whatever the
+// stage holds, and what comes of them is not written).
+static int box_rows(int max_rows) { return max_rows < 128 ? (max_rows + 7) & ~7 : 128; }
+
+// Column width of a tile: wide ones read fewer operand bytes for a product, narrow
+// ones spread over the SMs where there are few.  The least of (rounds of tiles over
+// the SMs) x (cycles of a block of 128 along the contraction).
 static int rows_bn(int max_rows, int G, int N) {
     const long long rows = (max_rows + 127) / 128 + (G < max_rows ? G : max_rows) - 1;
-    return rows * ((N + 255) / 256) >= 4LL * num_sms() ? 256 : 128;
+    int best = 256;
+    long long least = -1;
+    const int width[4] = {256, 128, 64, 32}, cycles[4] = {850, 520, 384, 320};
+    for (int i = 0; i < 4; ++i) {
+        const long long tiles = rows * ((N + width[i] - 1) / width[i]);
+        const long long cost = (tiles + num_sms() - 1) / num_sms() * cycles[i];
+        if (least < 0 || cost < least) {
+            least = cost;
+            best = width[i];
+        }
+    }
+    return best;
 }
 
 moe_status launch_fp8_matmul(const uint8_t *aq, const float *as, const int32_t *offsets, int G,
@@ -620,7 +662,8 @@ moe_status launch_fp8_matmul(const uint8_t *aq, const float *as, const int32_t *
     Fp8Params p;
     std::memset(&p, 0, sizeof p);
     const int BN = rows_bn(max_rows, G, N);
-    if (!encode_tmap_u8_2d(&p.tmA, aq, K, max_rows, K, 128, 128, 128) ||
+    p.a_rows = box_rows(max_rows);
+    if (!encode_tmap_u8_2d(&p.tmA, aq, K, max_rows, K, 128, p.a_rows, 128) ||
         !encode_tmap_u8_2d(&p.tmB, bq, K, (uint64_t)G * N, K, 128, BN, 128) ||
         !encode_tmap_bf16_2d(&p.tmO, out, N, max_rows, 2ULL * N, 64, 32))
         return MOE_ERR_CUDA;
@@ -636,8 +679,12 @@ moe_status launch_fp8_matmul(const uint8_t *aq, const float *as, const int32_t *
     p.w_rows = w_rows;
     p.out = out;
     const long long tiles = (long long)row_tile_bound(max_rows, G) * p.n_tiles;
-    return BN == 256 ? launch_fp8<FP8_ROWS, 256, 3>(p, tiles, st)
-                     : launch_fp8<FP8_ROWS, 128, 5>(p, tiles, st);
+    switch (BN) {
+    case 256: return launch_fp8<FP8_ROWS, 256, 3>(p, tiles, st);
+    case 128: return launch_fp8<FP8_ROWS, 128, 5>(p, tiles, st);
+    case 64: return launch_fp8<FP8_ROWS, 64, 7>(p, tiles, st);
+    default: return launch_fp8<FP8_ROWS, 32, 8>(p, tiles, st);
+    }
 }
 
 moe_status launch_fp8_ffn1(const uint8_t *xq, const float *xs, const int32_t *offsets, int G,
@@ -645,7 +692,8 @@ moe_status launch_fp8_ffn1(const uint8_t *xq, const float *xs, const int32_t *of
                            float clamp, uint8_t *hq, float *hs, cudaStream_t st) {
     Fp8Params p;
     std::memset(&p, 0, sizeof p);
-    if (!encode_tmap_u8_2d(&p.tmA, xq, d, max_rows, d, 128, 128, 128) ||
+    p.a_rows = box_rows(max_rows);
+    if (!encode_tmap_u8_2d(&p.tmA, xq, d, max_rows, d, 128, p.a_rows, 128) ||
         !encode_tmap_u8_2d(&p.tmB, W13q, d, (uint64_t)G * 2 * I, d, 128, 128, 128))
         return MOE_ERR_CUDA;
     p.offsets = offsets;
@@ -669,6 +717,7 @@ moe_status launch_fp8_wgrad(const uint8_t *aq, const float *as, const uint8_t *b
     constexpr int BN = 256;
     Fp8Params p;
     std::memset(&p, 0, sizeof p);
+    p.a_rows = 128;
     if (!encode_tmap_u8_2d(&p.tmA, aq, 128, (uint64_t)max_chunks * M, 128, 128, 128, 128) ||
         !encode_tmap_u8_2d(&p.tmB, bq, 128, (uint64_t)max_chunks * N, 128, 128, BN, 128) ||
         !encode_tmap_f32_2d(&p.tmO, dW, N, (uint64_t)G * M, 4ULL * N, 32, 32))
