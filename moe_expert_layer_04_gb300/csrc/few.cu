@@ -114,15 +114,24 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1,
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// With an L2 policy: the weights pass through L2 once and must not push out what
-// every call uses again (the kernels' code, W_g, the token rows).
-__device__ __forceinline__ void tma_load_3d(void *dst, const CUtensorMap *tm, uint64_t *bar, int c0,
-                                            int c1, int c2, uint64_t policy) {
+// A stage's two boxes of eight rows and the bytes that `bar` is to count.  With an L2
+// policy: the weights pass through L2 once and must not push out what every call uses
+// again (the kernels' code, W_g, the token rows).  Called by a whole warp, which elects
+// the issuing thread here: with uniform control flow around it the operands stay in
+// uniform registers.
+__device__ __forceinline__ void copy_stage(void *dst, int half, const CUtensorMap *tm,
+                                           uint64_t *bar, int bytes, int r0, int r1, int c0,
+                                           uint64_t policy) {
     asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
-        ".L2::cache_hint [%0], [%1, {%3, %4, %5}], [%2], %6;" ::"r"(smem_u32(dst)),
-        "l"(reinterpret_cast<uint64_t>(tm)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2),
-        "l"(policy)
+        "{\n\t.reg .pred e;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "@e mbarrier.arrive.expect_tx.shared::cta.b64 _, [%3], %4;\n\t"
+        "@e cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
+        ".L2::cache_hint [%0], [%2, {%8, %5, %7}], [%3], %9;\n\t"
+        "@e cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
+        ".L2::cache_hint [%1], [%2, {%8, %6, %7}], [%3], %9;\n\t}" ::"r"(smem_u32(dst)),
+        "r"(smem_u32(dst) + half), "l"(reinterpret_cast<uint64_t>(tm)), "r"(smem_u32(bar)),
+        "r"(bytes), "r"(r0), "r"(r1), "r"(c0), "r"(0), "l"(policy)
         : "memory");
 }
 
@@ -405,7 +414,9 @@ struct FewShape {
 
 // Tiles in order: shared W13, shared W2, routed W13, routed W2.  An item is one
 // tile of W13 or kW2Tiles of W2.
-__device__ __forceinline__ FewItem few_item(int t, int tiles1, int tiles2, int n_pass) {
+// r1, r2: 1 / tiles1, 1 / tiles2 (what rounding leaves wrong is put right).
+__device__ __forceinline__ FewItem few_item(int t, int tiles1, int tiles2, float r1, float r2,
+                                            int n_pass) {
     FewItem it;
     it.pass = -1;
     it.second = t >= tiles1;
@@ -415,8 +426,10 @@ __device__ __forceinline__ FewItem few_item(int t, int tiles1, int tiles2, int n
     it.second = t >= n_pass * tiles1;
     if (it.second) t -= n_pass * tiles1;
     const int tiles = it.second ? tiles2 : tiles1;
-    it.pass = t / tiles;
+    it.pass = (int)((float)t * (it.second ? r2 : r1));
     it.tile = t - it.pass * tiles;
+    if (it.tile < 0) { --it.pass; it.tile += tiles; }
+    if (it.tile >= tiles) { ++it.pass; it.tile -= tiles; }
     return it;
 }
 
@@ -473,7 +486,8 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_experts_kernel(
     int *last_s = const_cast<int *>(abort_s) + 1;
     static_assert(sizeof(FewMeta) % 8 == 0, "the barriers behind it are 8-byte aligned");
 
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    // (the warp's number is uniform, to the compiler too)
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES; ++s) {
             mbar_init(&full[s], 2 + (FP8 ? 32 : 0));
@@ -505,11 +519,12 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_experts_kernel(
         uint32_t s = 0, ph = 0;
         uint32_t begun = 0;                // stages that a copy was issued to, and its parity
         const uint64_t policy = policy_evict_first();
+        const float rcp1 = 1.0f / (float)tiles1, rcp2 = 1.0f / (float)tiles2;
         bool ok = true;
         int n_pass = -1;
         for (uint32_t n = 0; ok; ++n) {
             if (!mbar_wait_warp(&qfull[n & 1], n >> 1 & 1u, wc)) break;
-            int t = queue[n & 1];
+            int t = __shfl_sync(0xffffffffu, queue[n & 1], 0);
             if (t >= shared_items && n_pass < 0) {
                 asm volatile("griddepcontrol.wait;" ::: "memory");
                 for (int e = lane; e < p.E; e += 32) meta->start[e] = 0;
@@ -586,7 +601,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_experts_kernel(
                 }
                 break;
             }
-            const FewItem it = few_item(first, tiles1, tiles2, max(n_pass, 0));
+            const FewItem it = few_item(first, tiles1, tiles2, rcp1, rcp2, max(n_pass, 0));
             const int e = it.pass < 0 ? p.E : meta->pass_e[it.pass];
             const int rows = it.pass < 0 ? p.T : meta->pass_n[it.pass] | meta->pass_row[it.pass] << 16;
             const int K = it.second ? p.I : p.d;
@@ -616,15 +631,12 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_experts_kernel(
                                           (c0 == 0 && sub == 0 ? kItem : 0);
                         *reinterpret_cast<int4 *>(&info[s]) = make_int4(tile, it.pass, rows, flags);
                         mbar_arrive(&ifull[s]);
-                        if (c0 < whole) {
-                            uint8_t *dst = ring + s * kFewStage;
-                            mbar_arrive_expect_tx(&full[s], 16 * kChunk * cps);
-                            tma_load_3d(dst, tm, &full[s], 0, r0, c0, policy);
-                            tma_load_3d(dst + kFewStage / 2, tm, &full[s], 0, r1, c0, policy);
-                        } else {
-                            mbar_arrive(&full[s]);
-                        }
+                        if (c0 >= whole) mbar_arrive(&full[s]);
                     }
+                    __syncwarp();
+                    if (c0 < whole)
+                        copy_stage(ring + s * kFewStage, kFewStage / 2, tm, &full[s],
+                                   16 * kChunk * cps, r0, r1, c0, policy);
                     if constexpr (FP8) {
                         if (my_kb < cps && c0 + my_kb < kb)
                             cp_async4(scales + s * 2 * kStageChunks + lane, sc + c0);
