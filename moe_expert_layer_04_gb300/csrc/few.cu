@@ -56,7 +56,8 @@ constexpr int kGateSplits = 16;        // at most
 constexpr int kMulWarps = 16;
 constexpr int kSumWarps = 2;           // each with a buffer of partial sums of its own
 constexpr int kCopyWarp = kMulWarps, kActWarp = kMulWarps + 1, kSumWarp0 = kMulWarps + 2;
-constexpr int kFewThreads = 32 * (kSumWarp0 + kSumWarps);
+constexpr int kTicketWarp = kSumWarp0 + kSumWarps;
+constexpr int kFewThreads = 32 * (kTicketWarp + 1);
 constexpr int kChunk = 128;            // weight bytes of a row that a warp takes
 constexpr int kGroups = 2;             // of multiplying warps; they take stages in turn
 constexpr int kGroupWarps = kMulWarps / kGroups;
@@ -376,11 +377,10 @@ struct FewTile {
     int tile;      // of 16 weight rows
     int pass;      // -1 the shared expert
     int rows;      // tokens of the pass | first entry in `slot` << 16
-    int flags;     // first chunk | kSecond | kLast | kItem
+    int flags;     // first chunk | kSecond | kLast
 };
 constexpr int kSecond = 1 << 30;       // W2
 constexpr int kLast = 1 << 29;         // the tile's last stage
-constexpr int kItem = 1 << 28;         // the item's first stage
 constexpr int kChunkMask = (1 << 28) - 1;
 
 __device__ __forceinline__ int4 ld_tile(const FewTile *p) {
@@ -481,9 +481,11 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_experts_kernel(
     uint64_t *rfull = empty + STAGES;        // a buffer of `red` has every warp's partial sums
     uint64_t *rempty = rfull + kSumWarps;    // ... and has been read
     uint64_t *qfull = rempty + kSumWarps;    // an item's number is in `queue`
-    volatile int *queue = reinterpret_cast<volatile int *>(qfull + 2);
+    uint64_t *qempty = qfull + 2;            // ... and has been taken
+    volatile int *queue = reinterpret_cast<volatile int *>(qempty + 2);
     volatile int *abort_s = queue + 2;
     int *last_s = const_cast<int *>(abort_s) + 1;
+    volatile int *stop_s = last_s + 1;       // no more items are wanted
     static_assert(sizeof(FewMeta) % 8 == 0, "the barriers behind it are 8-byte aligned");
 
     // (the warp's number is uniform, to the compiler too)
@@ -500,7 +502,10 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_experts_kernel(
         }
         mbar_init(&qfull[0], 1);
         mbar_init(&qfull[1], 1);
+        mbar_init(&qempty[0], 1);
+        mbar_init(&qempty[1], 1);
         *abort_s = 0;
+        *stop_s = 0;
         fence_barrier_init();
     }
     __syncthreads();
@@ -593,6 +598,11 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_experts_kernel(
                 first = tiles1 + tiles2 + (t < first2 ? t : first2 + (t - first2) * kW2Tiles);
                 if (first >= (n_pass + 1) * (tiles1 + tiles2)) first = -1;
             }
+            if (lane == 0) {
+                if (first < 0) *stop_s = 1;
+                mbar_arrive(&qempty[n & 1]);
+            }
+            __syncwarp();
             if (first < 0) {
                 if (!mbar_wait_warp(&empty[s], ph ^ 1u, wc)) break;
                 if (lane == 0) {
@@ -627,8 +637,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_experts_kernel(
                     if (!mbar_wait_warp(&empty[s], ph ^ 1u, wc)) { ok = false; break; }
                     if (lane == 0) {
                         const int flags = c0 | (it.second ? kSecond : 0) |
-                                          (c0 + cps >= chunks ? kLast : 0) |
-                                          (c0 == 0 && sub == 0 ? kItem : 0);
+                                          (c0 + cps >= chunks ? kLast : 0);
                         *reinterpret_cast<int4 *>(&info[s]) = make_int4(tile, it.pass, rows, flags);
                         mbar_arrive(&ifull[s]);
                         if (c0 >= whole) mbar_arrive(&full[s]);
@@ -658,20 +667,8 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_experts_kernel(
         // Waits until they exist (the tokens in f16 come from the first kernel,
         // a pass's h from the tiles before it) and copies the rows of passes
         // that have few; whoever multiplies waits for nothing else.
-        // It also takes the item numbers from the grid's counter, two ahead of
-        // the copies (the copying warp's arrivals would wait for its own
-        // outstanding atomics).
-        uint32_t s = 0, ph = 0, n_item = 0;
+        uint32_t s = 0, ph = 0;
         bool have_x = !FP8;
-        auto take_item = [&]() {
-            if (lane == 0) {
-                queue[n_item & 1] = atomicAdd(p.counters + 1, 1);
-                mbar_arrive(&qfull[n_item & 1]);
-            }
-            ++n_item;
-        };
-        take_item();
-        take_item();
         while (mbar_wait_warp(&ifull[s], ph, wc)) {
             const int4 q = ld_tile(&info[s]);
             if (q.x < 0) break;
@@ -708,8 +705,6 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_experts_kernel(
                            : (FP8 ? p.x16 : p.x) + (size_t)(q.y < 0 ? lane : slot / p.k) * p.d;
                 bulk_load(acts + s * SH::ACT + lane * SH::ACT_PITCH, src + k0, bytes, &full[s]);
             }
-            // the copying warp has read this item's number: its place is free
-            if (q.w & kItem) take_item();
             if (++s == STAGES) { s = 0; ph ^= 1u; }
         }
     } else if (warp < kMulWarps) {
@@ -765,12 +760,22 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_experts_kernel(
             }
             const int cps = second ? p.cps2 : p.cps13;
             const bool mine = (n_stage++ & (kGroups - 1)) == (uint32_t)group;
+            // this warp's chunks of the stage, which it releases once the last one's
+            // weights are in its registers
+            const int left = min(cps, (K + SH::CHUNK_K - 1) / SH::CHUNK_K - c0) - wl;
+            const int n_ch = !mine || left <= 0 ? 0 : left > kGroupWarps ? 2 : 1;
+            static_assert(kWarpChunks == 2, "chunks of a stage for one warp");
+            auto release = [&] {
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&empty[s]);
+            };
             if (mine && !mbar_wait_warp(&full[s], ph, wc)) break;
+            if (n_ch == 0) release();
 #pragma unroll
             for (int ch = 0; ch < kWarpChunks; ++ch) {
                 const int cl = wl + kGroupWarps * ch;   // in the stage
                 const int chunk = c0 + cl;              // in the row
-                if (!mine || cl >= cps || chunk * SH::CHUNK_K >= K) break;
+                if (ch >= n_ch) break;
                 // token operand of the chunk's half h, group j
                 auto load_act = [&](int h, int j, uint4 (&v)[NV]) {
                     const int kk = (2 * chunk + h) * (SH::CHUNK_K / 2) + c * (SH::CHUNK_K / 8);
@@ -808,6 +813,12 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_experts_kernel(
                     wq[1][0] = ld_shared_v4(a0 + (first ^ 64u));
                     wq[1][1] = ld_shared_v4(b0 + (first ^ 64u));
                 }
+                float f0 = 1.0f, f1 = 1.0f;
+                if constexpr (FP8) {
+                    f0 = scales[s * 2 * kStageChunks + cl];
+                    f1 = scales[(s * 2 + 1) * kStageChunks + cl];
+                }
+                if (ch == n_ch - 1) release();
                 if constexpr (!FP8) {
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
@@ -870,8 +881,6 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_experts_kernel(
                                         bv[2 * m + 1]);
                         }
                     }
-                    const float f0 = scales[s * 2 * kStageChunks + cl];
-                    const float f1 = scales[(s * 2 + 1) * kStageChunks + cl];
 #pragma unroll
                     for (int j = 0; j < NT; ++j) {
                         acc[j][0] = fmaf(part[j][0][0] + part[j][1][0], f0, acc[j][0]);
@@ -881,8 +890,6 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_experts_kernel(
                     }
                 }
             }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&empty[s]);
             if (++s == STAGES) { s = 0; ph ^= 1u; }
             if (!(q.w & kLast)) continue;
             // the tile's partial sums, one buffer per group of 8 rows (zeros where
@@ -904,6 +911,19 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_experts_kernel(
                 ++unit;
             }
             if (!ok) break;
+        }
+    } else if (warp == kTicketWarp) {
+        // ------------------------------------------------------ item numbers
+        // from the grid's counter, two ahead of the copies.  A warp of its own: the
+        // counter answers after a microsecond, and whoever waits for it does nothing
+        // else (a warp's arrivals on barriers wait for its outstanding atomics too).
+        for (uint32_t n = 0;; ++n) {
+            if (!mbar_wait_warp(&qempty[n & 1], (n >> 1 & 1u) ^ 1u, wc) || *stop_s) break;
+            if (lane == 0) {
+                queue[n & 1] = atomicAdd(p.counters + 1, 1);
+                mbar_arrive(&qfull[n & 1]);
+            }
+            __syncwarp();
         }
     } else {
         // ------------------------------------------- sums over the warps
