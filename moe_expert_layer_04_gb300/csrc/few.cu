@@ -93,6 +93,7 @@ struct FewParams {
     float *yp;       // [S + T, d]
     int splits;
     int cps13, cps2;   // chunks of a row in a stage
+    int by_tile;       // the groups of multiplying warps take tiles in turn (0: stages)
     int *status;
     long long wait_limit;
 };
@@ -369,6 +370,7 @@ struct alignas(8) FewMeta {
     int16_t pass_row[kFewS];           // first entry in `slot`
     int16_t pass_n[kFewS];             // rows
     int16_t slot[kFewS];
+    int16_t token[kFewS];              // of each entry of `slot`
     int16_t start[kFewE];              // scratch: rows, then first slot of each expert
 };
 
@@ -408,7 +410,7 @@ struct FewShape {
     static constexpr int RED = kSumWarps * kMulWarps * 128 * 4;
     static constexpr int SCALES = FP8 ? 2 * kStageChunks * 4 : 0;
     static constexpr int SMEM = 1024 + STAGES * (kFewStage + ACT + SCALES + 16 /* FewTile */) +
-                                RED + kSumWarps * 16 + (int)sizeof(FewMeta) + 512;
+                                RED + 2 * kSumWarps * 16 + (int)sizeof(FewMeta) + 512;
     static_assert(SMEM <= 232448, "shared memory of a CTA");
 };
 
@@ -471,16 +473,20 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_experts_kernel(
     uint8_t *acts = ring + STAGES * kFewStage;
     float4 *red = reinterpret_cast<float4 *>(acts + STAGES * SH::ACT);
     FewTile *info = reinterpret_cast<FewTile *>(reinterpret_cast<uint8_t *>(red) + SH::RED);
+    // `red`: a buffer of 16 warps' sums for each sum warp; where the groups take tiles
+    // in turn, two of 8 for each group and its sum warp
+    constexpr int BUFS = 2 * kSumWarps;
+    static_assert(kSumWarps == kGroups && kMulWarps == 2 * kGroupWarps, "halves of a buffer");
     FewTile *rinfo = info + STAGES;          // per buffer of `red`; flags: group of 8 rows | kSecond
-    float *scales = reinterpret_cast<float *>(rinfo + kSumWarps);   // FP8: per stage gate, up
+    float *scales = reinterpret_cast<float *>(rinfo + BUFS);   // FP8: per stage gate, up
     FewMeta *meta =
         reinterpret_cast<FewMeta *>(reinterpret_cast<uint8_t *>(scales) + STAGES * SH::SCALES);
     uint64_t *full = reinterpret_cast<uint64_t *>(meta + 1);
     uint64_t *ifull = full + STAGES;         // `info` of the stage is written
     uint64_t *empty = ifull + STAGES;
     uint64_t *rfull = empty + STAGES;        // a buffer of `red` has every warp's partial sums
-    uint64_t *rempty = rfull + kSumWarps;    // ... and has been read
-    uint64_t *qfull = rempty + kSumWarps;    // an item's number is in `queue`
+    uint64_t *rempty = rfull + BUFS;         // ... and has been read
+    uint64_t *qfull = rempty + BUFS;         // an item's number is in `queue`
     uint64_t *qempty = qfull + 2;            // ... and has been taken
     volatile int *queue = reinterpret_cast<volatile int *>(qempty + 2);
     volatile int *abort_s = queue + 2;
@@ -496,8 +502,8 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_experts_kernel(
             mbar_init(&ifull[s], 1);
             mbar_init(&empty[s], kMulWarps);
         }
-        for (int b = 0; b < kSumWarps; ++b) {
-            mbar_init(&rfull[b], kMulWarps);
+        for (int b = 0; b < BUFS; ++b) {
+            mbar_init(&rfull[b], p.by_tile ? kGroupWarps : kMulWarps);
             mbar_init(&rempty[b], 1);
         }
         mbar_init(&qfull[0], 1);
@@ -534,13 +540,20 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_experts_kernel(
                 asm volatile("griddepcontrol.wait;" ::: "memory");
                 for (int e = lane; e < p.E; e += 32) meta->start[e] = 0;
                 __syncwarp();
-                int rank[kFewS / 32];
+                int rank[kFewS / 32], id[kFewS / 32];
+                float w[kFewS / 32];
+#pragma unroll
+                for (int j = 0; j < kFewS / 32; ++j) {
+                    const int i = lane + 32 * j;
+                    id[j] = i < S ? __ldcg(p.ids + i) : -1 - lane;
+                    w[j] = i < S ? __ldcg(p.w + i) : 0.0f;
+                }
 #pragma unroll
                 for (int j = 0; j < kFewS / 32; ++j) {
                     const int i = lane + 32 * j;
                     rank[j] = 0;
                     if (32 * j < S) {
-                        const int e = i < S ? __ldcg(p.ids + i) : -1 - lane;
+                        const int e = id[j];
                         const unsigned m = __match_any_sync(0xffffffffu, e);
                         if (i < S) rank[j] = meta->start[e] + __popc(m & ((1u << lane) - 1u));
                         __syncwarp();
@@ -580,8 +593,10 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_experts_kernel(
                 for (int j = 0; j < kFewS / 32; ++j) {
                     const int i = lane + 32 * j;
                     if (i < S) {
-                        meta->slot[meta->start[__ldcg(p.ids + i)] + rank[j]] = (int16_t)i;
-                        meta->w[i] = __ldcg(p.w + i);
+                        const int at = meta->start[id[j]] + rank[j];
+                        meta->slot[at] = (int16_t)i;
+                        meta->token[at] = (int16_t)(i / p.k);
+                        meta->w[i] = w[j];
                     }
                 }
                 n_pass = sum & 1023;
@@ -699,10 +714,11 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_experts_kernel(
             }
             __syncwarp();
             if (copy && lane < n) {
-                const int slot = q.y < 0 ? S + lane : meta->slot[row0 + lane];
-                const uint16_t *src =
-                    second ? p.h + (size_t)slot * p.I
-                           : (FP8 ? p.x16 : p.x) + (size_t)(q.y < 0 ? lane : slot / p.k) * p.d;
+                const int row = q.y < 0    ? (second ? S + lane : lane)
+                                : second ? meta->slot[row0 + lane]
+                                         : meta->token[row0 + lane];
+                const uint16_t *src = second ? p.h + (size_t)row * p.I
+                                             : (FP8 ? p.x16 : p.x) + (size_t)row * p.d;
                 bulk_load(acts + s * SH::ACT + lane * SH::ACT_PITCH, src + k0, bytes, &full[s]);
             }
             if (++s == STAGES) { s = 0; ph ^= 1u; }
@@ -715,7 +731,13 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_experts_kernel(
         // fragments straight from the row-wise tiles (a lane's 16 bytes are
         // consecutive k, fed as k-pairs to successive MMAs, on both sides alike).
         const int group = warp / kGroupWarps, wl = warp % kGroupWarps;
-        uint32_t s = 0, ph = 0, unit = 0, n_stage = 0;
+        // Where a tile is one or two stages long, the groups take tiles in turn instead,
+        // and the other group neither writes nor signals anything for it.  In either
+        // case `role` says which of a tile's stages a group has (0 the first one), so
+        // that sums do not depend on which group it is.
+        uint32_t s = 0, ph = 0, unit = 0, turn = 0;
+        int role = 0;
+        auto buffer = [&](uint32_t u) { return (p.by_tile ? 2 * group : 0) + (u & 1u); };
         const int g = lane >> 2, c = lane & 3;
         const int pr = few_row(g);
         float acc[NT][4];
@@ -728,11 +750,11 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_experts_kernel(
             if (!mbar_wait_warp(&ifull[s], ph, wc)) break;
             const int4 q = ld_tile(&info[s]);
             if (q.x < 0) {
-                if (lane == 0) {   // tell the sum warps, one buffer each
-                    for (int b = 0; b < kSumWarps; ++b, ++unit) {
-                        const uint32_t buf = unit % kSumWarps;
-                        if (!mbar_wait(&rempty[buf], (unit / kSumWarps & 1u) ^ 1u, wc)) break;
-                        if (warp == 0) rinfo[buf].tile = -1;
+                if (lane == 0) {   // tell the sum warps: each its own, or both
+                    for (int b = 0; b < (p.by_tile ? 1 : kSumWarps); ++b, ++unit) {
+                        const uint32_t buf = buffer(unit);
+                        if (!mbar_wait(&rempty[buf], (unit >> 1 & 1u) ^ 1u, wc)) break;
+                        if (wl == 0 && (p.by_tile || group == 0)) rinfo[buf].tile = -1;
                         mbar_arrive(&rfull[buf]);
                     }
                 }
@@ -743,7 +765,10 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_experts_kernel(
             const int K = second ? p.I : p.d;
             const int nt = NT == 1 ? 1 : (n + 7) >> 3;
             const bool in_smem = n <= SH::ACT_ROWS;
-            if (c0 == 0) {
+            const bool mine = (turn & (kGroups - 1)) == (uint32_t)group;
+            if (c0 == 0) role = mine ? 0 : 1;
+            if (!p.by_tile || (q.w & kLast)) ++turn;
+            if (c0 == 0 && (mine || !p.by_tile)) {
 #pragma unroll
                 for (int j = 0; j < NT; ++j) {
 #pragma unroll
@@ -751,15 +776,15 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_experts_kernel(
                     const int i = j * 8 + g;
                     act[j] = nullptr;
                     if (!in_smem && i < n) {
-                        const int slot = q.y < 0 ? S + i : meta->slot[row0 + i];
-                        act[j] = second ? p.h + (size_t)slot * p.I
-                                        : (FP8 ? p.x16 : p.x) +
-                                              (size_t)(q.y < 0 ? i : slot / p.k) * p.d;
+                        const int row = q.y < 0    ? (second ? S + i : i)
+                                        : second ? meta->slot[row0 + i]
+                                                 : meta->token[row0 + i];
+                        act[j] = second ? p.h + (size_t)row * p.I
+                                        : (FP8 ? p.x16 : p.x) + (size_t)row * p.d;
                     }
                 }
             }
             const int cps = second ? p.cps2 : p.cps13;
-            const bool mine = (n_stage++ & (kGroups - 1)) == (uint32_t)group;
             // this warp's chunks of the stage, which it releases once the last one's
             // weights are in its registers
             const int left = min(cps, (K + SH::CHUNK_K - 1) / SH::CHUNK_K - c0) - wl;
@@ -892,18 +917,19 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_experts_kernel(
             }
             if (++s == STAGES) { s = 0; ph ^= 1u; }
             if (!(q.w & kLast)) continue;
-            // the tile's partial sums, one buffer per group of 8 rows (zeros where
-            // the other group had all its stages)
+            if (p.by_tile && !mine) continue;
+            // the tile's partial sums, one buffer per group of 8 rows
             bool ok = true;
 #pragma unroll
             for (int j = 0; j < NT; ++j) {
                 if (j >= nt) break;
-                const uint32_t buf = unit % kSumWarps;
-                ok = mbar_wait_warp(&rempty[buf], (unit / kSumWarps & 1u) ^ 1u, wc);
+                const uint32_t buf = buffer(unit);
+                ok = mbar_wait_warp(&rempty[buf], (unit >> 1 & 1u) ^ 1u, wc);
                 if (!ok) break;
-                red[(buf * kMulWarps + warp) * 32 + lane] =
+                const int w0 = p.by_tile ? buf * kGroupWarps : buf * kMulWarps + role * kGroupWarps;
+                red[(w0 + wl) * 32 + lane] =
                     make_float4(acc[j][0], acc[j][1], acc[j][2], acc[j][3]);
-                if (warp == 0 && lane == 0)
+                if (role == 0 && wl == 0 && lane == 0)
                     *reinterpret_cast<int4 *>(&rinfo[buf]) =
                         make_int4(q.x, q.y, q.z, j | (q.w & kSecond));
                 __syncwarp();
@@ -927,16 +953,19 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_experts_kernel(
         }
     } else {
         // ------------------------------------------- sums over the warps
-        const int buf = warp - kSumWarp0;
+        const int me = warp - kSumWarp0;
         const int g = few_row(lane >> 2), c = lane & 3;
         for (uint32_t m = 0;; ++m) {
-            if (!mbar_wait_warp(&rfull[buf], m & 1u, wc)) break;
+            const uint32_t buf = p.by_tile ? 2 * me + (m & 1u) : me;
+            if (!mbar_wait_warp(&rfull[buf], (p.by_tile ? m >> 1 : m) & 1u, wc)) break;
             const int4 q = ld_tile(&rinfo[buf]);
             if (q.x < 0) break;
+            const float4 *from = red + buf * (p.by_tile ? kGroupWarps : kMulWarps) * 32 + lane;
             float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
             for (int w = 0; w < kMulWarps; ++w) {
-                const float4 r = red[(buf * kMulWarps + w) * 32 + lane];
+                if (w == kGroupWarps && p.by_tile) break;
+                const float4 r = from[w * 32];
                 v[0] += r.x;
                 v[1] += r.y;
                 v[2] += r.z;
@@ -960,7 +989,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_experts_kernel(
                     o[8] = w * v[2 + i];
                 } else {
                     float up = 1.0f;
-                    if constexpr (FP8) up = __ldcg(p.x16_s + (q.y < 0 ? r : slot / p.k));
+                    if constexpr (FP8) up = __ldcg(p.x16_s + (q.y < 0 ? r : meta->token[row0 + r]));
                     const float h = swiglu_clamped_nan(v[i] * up, v[2 + i] * up, p.clamp);
                     p.h[(size_t)slot * p.I + q.x * 8 + g] =
                         FP8 ? __half_as_ushort(__float2half_rn(h * exp2i(p.h_exp)))
@@ -1137,6 +1166,8 @@ moe_status launch_few(const moe_few_args *a, cudaStream_t st) {
                                &p.cps13) ||
         !encode_rows_of_chunks(&p.tm2, p.W2, (uint64_t)(p.E + 1) * p.d, p.I * elt, &p.cps2))
         return MOE_ERR_CUDA;
+    // tiles of one or two stages: see the multiplying warps
+    p.by_tile = p.d * elt <= 2 * p.cps13 * kChunk && p.I * elt <= 2 * p.cps2 * kChunk;
     const int et = (p.E + 15) / 16;
     int splits = (num_sms() + et - 1) / et;   // every SM has a part
     splits = splits < 1 ? 1 : splits > kGateSplits ? kGateSplits : splits;
