@@ -87,8 +87,8 @@ struct FewParams {
     uint16_t *x16;   // FP8 weights: [T, d] f16 tokens, each scaled by a power of two ...
     float *x16_s;    // ... whose inverse this is [T]
     int h_exp;       // FP8 weights: h is f16, times 2^h_exp
-    int32_t *ids;    // [T, k]
-    float *w;        // [T, k]
+    uint64_t *routed;   // [T, k] (expert + 1) << 32 | its weight's bits; zero between calls, so
+                        // that a slot's word is its own signal
     uint16_t *h;     // [S + T, I] bf16, or f16 (FP8 weights)
     float *yp;       // [S + T, d]
     int splits;
@@ -143,6 +143,30 @@ __device__ __forceinline__ int atom_add_acq_rel(int *p, int v) {
     return r;
 }
 
+// A routed slot's word, which says itself that it is there: whoever lists the experts
+// needs neither a flag nor the end of the first kernel, each a round trip more.
+__device__ __forceinline__ void st_slot(uint64_t *p, uint64_t v) {
+    asm volatile("st.relaxed.gpu.global.u64 [%0], %1;" ::"l"(p), "l"(v) : "memory");
+}
+__device__ __forceinline__ uint64_t ld_slot(const uint64_t *p) {
+    uint64_t v;
+    asm volatile("ld.relaxed.gpu.global.u64 %0, [%1];" : "=l"(v) : "l"(p) : "memory");
+    return v;
+}
+// Bounded like mbar_wait; 0 once the CTA has aborted or the limit ran out.
+__device__ __forceinline__ uint64_t wait_slot(const uint64_t *p, const WaitCtl &w) {
+    uint64_t v = ld_slot(p);
+    const long long t0 = clock64();
+    while (v == 0 && !*w.abort) {
+        v = ld_slot(p);
+        if (clock64() - t0 > w.limit) {
+            *w.abort = 1;
+            atomicExch(w.status, (int)MOE_ERR_TIMEOUT);
+        }
+    }
+    return v;
+}
+
 // ------------------------------------------------------------ gate, routing
 //
 // A CTA takes 16 experts and one of `splits` parts of the contraction (all SMs
@@ -155,17 +179,14 @@ __device__ __forceinline__ int atom_add_acq_rel(int *p, int v) {
 // Scores and keys are fp32 here (moe_route evaluates the sigmoid in fp64 and
 // rounds it): the logits' own sums differ between the two calls by more than
 // the fp32 sigmoid's error, and fp64 costs 6 us of latency that nothing hides.
-// Largest key of the warp and its id; equal keys: the lower id.
-__device__ __forceinline__ void warp_best(float &key, int &id) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        const float k2 = __shfl_xor_sync(0xffffffffu, key, o);
-        const int i2 = __shfl_xor_sync(0xffffffffu, id, o);
-        if (k2 > key || (k2 == key && i2 < id)) {
-            key = k2;
-            id = i2;
-        }
-    }
+//
+// What follows the gate matmul is latency alone, and the routed experts wait for it: so
+// all of the last CTA's threads add up the partial logits where they fit its shared
+// memory, and the largest key of a round is found by two reductions of the warp over
+// keys in the order of unsigned integers.
+__device__ __forceinline__ uint32_t ordered(float v) {
+    const uint32_t u = __float_as_uint(v);
+    return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
 }
 
 __device__ __forceinline__ float sigmoid_f32(float z) { return 1.0f / (1.0f + expf(-z)); }
@@ -225,7 +246,7 @@ __global__ void __launch_bounds__(kGateWarps * 32) few_gate_kernel(const __grid_
             few_token_f16(p, t, warp_top);
         return;
     }
-    __shared__ float red[kGateWarps][4][32];
+    __shared__ float red[kGateWarps][4][32], keys[kGateWarps * 4 * 32];
     __shared__ int s_last;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int e0 = blockIdx.x * 16 + (lane >> 2);
@@ -266,6 +287,25 @@ __global__ void __launch_bounds__(kGateWarps * 32) few_gate_kernel(const __grid_
     if (!s_last) return;
     __threadfence();
     if (threadIdx.x == 0) p.counters[0] = 0;
+    float *scores = &red[0][0][0];
+    const bool all = !p.hash && p.T * p.E <= kGateWarps * 4 * 32;
+    if (all) {
+        for (int i = threadIdx.x; i < p.T * p.E; i += kGateWarps * 32) {
+            const int t = i / p.E, e = i - t * p.E;
+            float z[kGateSplits];
+#pragma unroll
+            for (int s = 0; s < kGateSplits; ++s)
+                z[s] = s < p.splits ? __ldcg(p.part + (size_t)s * p.T * p.E + i) : 0.0f;
+            float v = p.logit_offset ? p.logit_offset[e] : 0.0f;
+            const float b = p.bias[e + ((p.is_vision && p.is_vision[t]) ? p.E : 0)];
+#pragma unroll
+            for (int s = 0; s < kGateSplits; ++s) v += z[s];
+            v = sigmoid_f32(v);
+            scores[i] = v;
+            keys[i] = v + b;
+        }
+        __syncthreads();
+    }
     for (int t = warp; t < p.T; t += kGateWarps) {
         int my_id = 0;
         float my_s = 0.0f;   // lane j < k: expert and score of slot j
@@ -289,39 +329,56 @@ __global__ void __launch_bounds__(kGateWarps * 32) few_gate_kernel(const __grid_
             }
         } else {
             const float *bt = p.bias + ((p.is_vision && p.is_vision[t]) ? p.E : 0);
-            float zv[EPL], key[EPL];
+            float zv[EPL];
+            uint32_t key[EPL];
+            if (all) {
+#pragma unroll
+                for (int i = 0; i < EPL; ++i) {
+                    const int e = lane + 32 * i;
+                    zv[i] = e < p.E ? scores[t * p.E + e] : 0.0f;
+                    key[i] = __float_as_uint(e < p.E ? keys[t * p.E + e] : 0.0f);
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < EPL; ++i) {
+                    const int e = lane + 32 * i;
+                    zv[i] = e < p.E && p.logit_offset ? p.logit_offset[e] : 0.0f;
+                    key[i] = __float_as_uint(e < p.E ? bt[e] : 0.0f);
+                }
+                // many loads together: their latency, not their bytes, counts here
+                constexpr int U = EPL <= 4 ? 8 : EPL <= 12 ? 4 : 1;
+                for (int s0 = 0; s0 < p.splits; s0 += U) {
+                    float z[U][EPL];
+#pragma unroll
+                    for (int u = 0; u < U; ++u)
+#pragma unroll
+                        for (int i = 0; i < EPL; ++i) {
+                            const int e = lane + 32 * i;
+                            z[u][i] = e < p.E && s0 + u < p.splits
+                                          ? __ldcg(p.part + ((size_t)(s0 + u) * p.T + t) * p.E + e)
+                                          : 0.0f;
+                        }
+#pragma unroll
+                    for (int u = 0; u < U; ++u)
+#pragma unroll
+                        for (int i = 0; i < EPL; ++i) zv[i] += z[u][i];
+                }
+#pragma unroll
+                for (int i = 0; i < EPL; ++i) {
+                    zv[i] = sigmoid_f32(zv[i]);
+                    key[i] = __float_as_uint(zv[i] + __uint_as_float(key[i]));
+                }
+            }
+            // in the integers' order: no expert 0, a NaN the smallest number
 #pragma unroll
             for (int i = 0; i < EPL; ++i) {
-                const int e = lane + 32 * i;
-                zv[i] = e < p.E && p.logit_offset ? p.logit_offset[e] : 0.0f;
-                key[i] = e < p.E ? bt[e] : 0.0f;
+                const float kk = __uint_as_float(key[i]);
+                key[i] = lane + 32 * i >= p.E ? 0u : ordered(kk == kk ? kk : -FLT_MAX);
             }
-            // many loads together: their latency, not their bytes, counts here
-            constexpr int U = EPL <= 4 ? 8 : EPL <= 12 ? 4 : 1;
-            for (int s0 = 0; s0 < p.splits; s0 += U) {
-                float z[U][EPL];
-#pragma unroll
-                for (int u = 0; u < U; ++u)
-#pragma unroll
-                    for (int i = 0; i < EPL; ++i) {
-                        const int e = lane + 32 * i;
-                        z[u][i] = e < p.E && s0 + u < p.splits
-                                      ? __ldcg(p.part + ((size_t)(s0 + u) * p.T + t) * p.E + e)
-                                      : 0.0f;
-                    }
-#pragma unroll
-                for (int u = 0; u < U; ++u)
-#pragma unroll
-                    for (int i = 0; i < EPL; ++i) zv[i] += z[u][i];
-            }
-#pragma unroll
-            for (int i = 0; i < EPL; ++i) {
-                zv[i] = sigmoid_f32(zv[i]);
-                const float kk = zv[i] + key[i];
-                key[i] = lane + 32 * i >= p.E ? -INFINITY : kk == kk ? kk : -FLT_MAX;
-            }
+            const uint32_t none = ordered(-INFINITY);
             for (int j = 0; j < p.k; ++j) {
-                float bk = -INFINITY, bs = 0.0f;
+                uint32_t bk = none;
+                float bs = 0.0f;
                 int be = INT_MAX;
 #pragma unroll
                 for (int i = 0; i < EPL; ++i) {   // ids grow with i: the first of equals stays
@@ -331,18 +388,18 @@ __global__ void __launch_bounds__(kGateWarps * 32) few_gate_kernel(const __grid_
                         be = lane + 32 * i;
                     }
                 }
-                const int mine = be;
-                warp_best(bk, be);
-                const unsigned m = __ballot_sync(0xffffffffu, mine == be && be != INT_MAX);
-                bs = __shfl_sync(0xffffffffu, bs, m ? __ffs(m) - 1 : 0);
-                if (mine == be) {
+                const uint32_t top = __reduce_max_sync(0xffffffffu, bk);
+                const int first =
+                    (int)__reduce_min_sync(0xffffffffu, bk == top ? (unsigned)be : INT_MAX);
+                bs = __shfl_sync(0xffffffffu, bs, first & 31);
+                if (be == first) {
 #pragma unroll
                     for (int i = 0; i < EPL; ++i)
-                        if (lane + 32 * i == be) key[i] = -INFINITY;
+                        if (lane + 32 * i == first) key[i] = 0u;
                 }
                 if (lane == j) {
-                    my_id = be == INT_MAX ? 0 : be;
-                    my_s = bs;
+                    my_id = first == INT_MAX ? 0 : first;
+                    my_s = first == INT_MAX ? 0.0f : bs;
                 }
             }
         }
@@ -351,8 +408,7 @@ __global__ void __launch_bounds__(kGateWarps * 32) few_gate_kernel(const __grid_
         if (lane < p.k) {
             const size_t o = (size_t)t * p.k + lane;
             const float w = sum > 0.0f ? p.scaling * my_s / sum : 0.0f;
-            p.ids[o] = my_id;
-            p.w[o] = w;
+            st_slot(p.routed + o, (uint64_t)(my_id + 1) << 32 | __float_as_uint(w));
             if (p.ids_out) p.ids_out[o] = my_id;
             if (p.w_out) p.w_out[o] = w;
         }
@@ -371,7 +427,8 @@ struct alignas(8) FewMeta {
     int16_t pass_n[kFewS];             // rows
     int16_t slot[kFewS];
     int16_t token[kFewS];              // of each entry of `slot`
-    int16_t start[kFewE];              // scratch: rows, then first slot of each expert
+    // scratch: of each slot, and rows, then first slot of each expert
+    int16_t expert[kFewS], rank[kFewS], start[kFewE];
 };
 
 // One tile's place in the work, as the copying warp hands it on with each stage.
@@ -463,6 +520,111 @@ __device__ __forceinline__ void cp_async_arrive(uint64_t *bar) {
 // swizzled 128 bytes, so that no two of its loads meet in a bank.
 __device__ __forceinline__ int few_row(int g) { return (g >> 1) | (g & 1) << 2; }
 
+// The routing as `meta` says it, listed by one warp; the number of passes, or -1 after
+// a wait that ran out.  An expert with r rows has ceil(r / (8 NT)) passes, and a pass
+// as many units as it has groups of 8 rows.
+template <int NT>
+__device__ __forceinline__ int few_units(int r, int passes) {
+    return passes > 0 ? (passes - 1) * NT + (r - (passes - 1) * 8 * NT + 7) / 8 : 0;
+}
+template <int NT>
+__device__ __forceinline__ void few_passes(FewMeta *meta, int e, int r, int first_row, int first,
+                                           int passes) {
+    for (int j = 0; j < passes; ++j) {
+        meta->pass_e[first + j] = (int16_t)e;
+        meta->pass_row[first + j] = (int16_t)(first_row + j * 8 * NT);
+        meta->pass_n[first + j] = (int16_t)min(8 * NT, r - j * 8 * NT);
+    }
+}
+
+// At most 32 slots, one a lane: a slot's place is the number of slots with a smaller
+// expert.  Little code, run once from a cold instruction cache, with the routed experts
+// waiting for it.
+template <int NT>
+__device__ __noinline__ int few_list_short(const FewParams &p, int S, FewMeta *meta, int lane,
+                                           const WaitCtl &wc) {
+    const uint64_t v = lane < S ? wait_slot(p.routed + lane, wc) : 1;
+    if (!__all_sync(0xffffffffu, v != 0)) return -1;
+    const int e = lane < S ? (int)(v >> 32) - 1 : INT_MAX;
+    const unsigned same = __match_any_sync(0xffffffffu, e), before = same & ((1u << lane) - 1u);
+    const int r = __popc(same), passes = (r + 8 * NT - 1) / (8 * NT);
+    const bool lead = lane < S && before == 0;
+    const int mine = lead ? passes | few_units<NT>(r, passes) << 16 : 0;
+    int place = 0, sum = 0, all = 0;
+    for (int i = 0; i < S; ++i) {
+        const int ei = __shfl_sync(0xffffffffu, e, i), c = __shfl_sync(0xffffffffu, mine, i);
+        place += ei < e;
+        sum += ei < e ? c : 0;
+        all += c;
+    }
+    if (lane < S) {
+        const int at = place + __popc(before);
+        meta->slot[at] = (int16_t)lane;
+        meta->token[at] = (int16_t)(lane / p.k);
+        meta->w[lane] = __uint_as_float((uint32_t)v);
+    }
+    if (lead) few_passes<NT>(meta, e, r, place, sum & 0xFFFF, passes);
+    if (lane == 0) meta->n_units = (all >> 16) + (p.T + 7) / 8;
+    __syncwarp();
+    return all & 0xFFFF;
+}
+
+template <int NT>
+__device__ __noinline__ int few_list(const FewParams &p, int S, FewMeta *meta, int lane,
+                                     const WaitCtl &wc) {
+    for (int e = lane; e < p.E; e += 32) meta->start[e] = 0;
+    __syncwarp();
+    // slot by slot: its expert, and its rank among the expert's rows
+    for (int i0 = 0; i0 < S; i0 += 32) {
+        const int i = i0 + lane;
+        const uint64_t v = i < S ? wait_slot(p.routed + i, wc) : 1;
+        if (!__all_sync(0xffffffffu, v != 0)) return -1;
+        const int e = i < S ? (int)(v >> 32) - 1 : -1 - lane;
+        const unsigned same = __match_any_sync(0xffffffffu, e), before = same & ((1u << lane) - 1u);
+        int rank = 0;
+        if (i < S) rank = meta->start[e] + __popc(before);
+        __syncwarp();
+        if (i < S) {
+            if (before == 0) meta->start[e] += __popc(same);
+            meta->w[i] = __uint_as_float((uint32_t)v);
+            meta->rank[i] = (int16_t)rank;
+            meta->expert[i] = (int16_t)e;
+        }
+        __syncwarp();
+    }
+    // prefix sums over the experts of passes, slots and units, in one word (each at
+    // most kFewS = 256: 10 bits)
+    int sum = 0;
+    for (int base = 0; base < p.E; base += 32) {
+        const int e = base + lane;
+        const int r = e < p.E ? meta->start[e] : 0;
+        if (!__any_sync(0xffffffffu, r)) continue;
+        const int passes = (r + 8 * NT - 1) / (8 * NT);
+        const int mine = passes | r << 10 | few_units<NT>(r, passes) << 20;
+        int incl = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += v;
+        }
+        const int excl = sum + incl - mine;
+        if (r > 0) {
+            meta->start[e] = (int16_t)(excl >> 10 & 1023);
+            few_passes<NT>(meta, e, r, excl >> 10 & 1023, excl & 1023, passes);
+        }
+        sum += __shfl_sync(0xffffffffu, incl, 31);
+    }
+    __syncwarp();
+    for (int i = lane; i < S; i += 32) {
+        const int at = meta->start[meta->expert[i]] + meta->rank[i];
+        meta->slot[at] = (int16_t)i;
+        meta->token[at] = (int16_t)(i / p.k);
+    }
+    if (lane == 0) meta->n_units = (sum >> 20) + (p.T + 7) / 8;
+    __syncwarp();
+    return sum & 1023;
+}
+
 template <bool FP8, int NT>
 __global__ void __launch_bounds__(kFewThreads, 1) few_experts_kernel(
     const __grid_constant__ FewParams p) {
@@ -537,71 +699,9 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_experts_kernel(
             if (!mbar_wait_warp(&qfull[n & 1], n >> 1 & 1u, wc)) break;
             int t = __shfl_sync(0xffffffffu, queue[n & 1], 0);
             if (t >= shared_items && n_pass < 0) {
-                asm volatile("griddepcontrol.wait;" ::: "memory");
-                for (int e = lane; e < p.E; e += 32) meta->start[e] = 0;
-                __syncwarp();
-                int rank[kFewS / 32], id[kFewS / 32];
-                float w[kFewS / 32];
-#pragma unroll
-                for (int j = 0; j < kFewS / 32; ++j) {
-                    const int i = lane + 32 * j;
-                    id[j] = i < S ? __ldcg(p.ids + i) : -1 - lane;
-                    w[j] = i < S ? __ldcg(p.w + i) : 0.0f;
-                }
-#pragma unroll
-                for (int j = 0; j < kFewS / 32; ++j) {
-                    const int i = lane + 32 * j;
-                    rank[j] = 0;
-                    if (32 * j < S) {
-                        const int e = id[j];
-                        const unsigned m = __match_any_sync(0xffffffffu, e);
-                        if (i < S) rank[j] = meta->start[e] + __popc(m & ((1u << lane) - 1u));
-                        __syncwarp();
-                        if (i < S && (m & ((1u << lane) - 1u)) == 0) meta->start[e] += __popc(m);
-                        __syncwarp();
-                    }
-                }
-                // prefix sums over the experts of passes, slots and units, in
-                // one word (each at most kFewS = 256: 10 bits)
-                int sum = 0;
-                for (int base = 0; base < p.E; base += 32) {
-                    const int e = base + lane;
-                    const int r = e < p.E ? meta->start[e] : 0;
-                    if (!__any_sync(0xffffffffu, r)) continue;
-                    const int c = (r + 8 * NT - 1) / (8 * NT);
-                    // a pass of r rows is ceil(r / 8) units
-                    const int u = c > 0 ? (c - 1) * NT + (r - (c - 1) * 8 * NT + 7) / 8 : 0;
-                    int incl = c | r << 10 | u << 20;
-#pragma unroll
-                    for (int o = 1; o < 32; o <<= 1) {
-                        const int v = __shfl_up_sync(0xffffffffu, incl, o);
-                        if (lane >= o) incl += v;
-                    }
-                    const int excl = sum + incl - (c | r << 10 | u << 20);
-                    const int first = excl >> 10 & 1023;
-                    if (r > 0) meta->start[e] = (int16_t)first;
-                    for (int j = 0; j < c; ++j) {
-                        const int q = (excl & 1023) + j;
-                        meta->pass_e[q] = (int16_t)e;
-                        meta->pass_row[q] = (int16_t)(first + j * 8 * NT);
-                        meta->pass_n[q] = (int16_t)min(8 * NT, r - j * 8 * NT);
-                    }
-                    sum += __shfl_sync(0xffffffffu, incl, 31);
-                }
-                __syncwarp();
-#pragma unroll
-                for (int j = 0; j < kFewS / 32; ++j) {
-                    const int i = lane + 32 * j;
-                    if (i < S) {
-                        const int at = meta->start[id[j]] + rank[j];
-                        meta->slot[at] = (int16_t)i;
-                        meta->token[at] = (int16_t)(i / p.k);
-                        meta->w[i] = w[j];
-                    }
-                }
-                n_pass = sum & 1023;
-                if (lane == 0) meta->n_units = (sum >> 20) + (p.T + 7) / 8;
-                __syncwarp();
+                n_pass = S <= 32 ? few_list_short<NT>(p, S, meta, lane, wc)
+                                 : few_list<NT>(p, S, meta, lane, wc);
+                if (n_pass < 0) break;
             }
             // item -> first tile
             int first;
@@ -1024,12 +1124,14 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_experts_kernel(
         }
     }
 
-    // the last CTA to leave puts every counter back to zero
+    // the last CTA to leave puts every counter and slot back to zero
     __syncthreads();
     if (threadIdx.x == 0) *last_s = atom_add_acq_rel(p.counters + 2, 1) == (int)gridDim.x - 1;
     __syncthreads();
-    if (*last_s)
+    if (*last_s) {
         for (int i = 1 + threadIdx.x; i < p.n_counters; i += kFewThreads) p.counters[i] = 0;
+        for (int i = threadIdx.x; i < S; i += kFewThreads) p.routed[i] = 0;
+    }
 }
 
 size_t up256(size_t b) { return (b + 255) / 256 * 256; }
@@ -1040,8 +1142,7 @@ struct FewWorkspace {
     float *part;
     uint16_t *x16;
     float *x16_s;
-    int32_t *ids;
-    float *w;
+    uint64_t *routed;
     uint16_t *h;
     float *yp;
     size_t bytes;
@@ -1061,8 +1162,7 @@ FewWorkspace carve_few(uint8_t *base, int T, int d, int E, int k, int I) {
     w.part = reinterpret_cast<float *>(take((size_t)kGateSplits * T * E * 4));
     w.x16 = reinterpret_cast<uint16_t *>(take((size_t)T * d * 2));
     w.x16_s = reinterpret_cast<float *>(take((size_t)T * 4));
-    w.ids = reinterpret_cast<int32_t *>(take(S * 4));
-    w.w = reinterpret_cast<float *>(take(S * 4));
+    w.routed = reinterpret_cast<uint64_t *>(take(S * 8));
     w.h = reinterpret_cast<uint16_t *>(take((S + T) * I * 2));
     w.yp = reinterpret_cast<float *>(take((S + T) * d * 4));
     w.bytes = off;
@@ -1154,8 +1254,7 @@ moe_status launch_few(const moe_few_args *a, cudaStream_t st) {
     p.part = w.part;
     p.x16 = w.x16;
     p.x16_s = w.x16_s;
-    p.ids = w.ids;
-    p.w = w.w;
+    p.routed = w.routed;
     p.h = w.h;
     p.yp = w.yp;
     p.status = device_status_ptr();
