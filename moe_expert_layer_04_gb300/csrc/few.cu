@@ -471,24 +471,21 @@ struct FewShape {
     static_assert(SMEM <= 232448, "shared memory of a CTA");
 };
 
-// Tiles in order: shared W13, shared W2, routed W13, routed W2.  An item is one
-// tile of W13 or kW2Tiles of W2.
-// r1, r2: 1 / tiles1, 1 / tiles2 (what rounding leaves wrong is put right).
+// Item t: shared W13 | W13 of the passes | shared W2 | W2 of the passes, one tile of W13
+// or kW2Tiles of W2.  r1, r2: 1 / tiles1, 1 / tiles2 (what rounding leaves wrong is put
+// right).  tile < 0: none.
 __device__ __forceinline__ FewItem few_item(int t, int tiles1, int tiles2, float r1, float r2,
                                             int n_pass) {
     FewItem it;
-    it.pass = -1;
-    it.second = t >= tiles1;
-    it.tile = it.second ? t - tiles1 : t;
-    t -= tiles1 + tiles2;
-    if (t < 0) return it;
-    it.second = t >= n_pass * tiles1;
-    if (it.second) t -= n_pass * tiles1;
+    it.second = t >= (n_pass + 1) * tiles1;
+    if (it.second) t = (t - (n_pass + 1) * tiles1) * kW2Tiles;
     const int tiles = it.second ? tiles2 : tiles1;
-    it.pass = (int)((float)t * (it.second ? r2 : r1));
-    it.tile = t - it.pass * tiles;
-    if (it.tile < 0) { --it.pass; it.tile += tiles; }
-    if (it.tile >= tiles) { ++it.pass; it.tile -= tiles; }
+    int q = (int)((float)t * (it.second ? r2 : r1));
+    it.tile = t - q * tiles;
+    if (it.tile < 0) { --q; it.tile += tiles; }
+    if (it.tile >= tiles) { ++q; it.tile -= tiles; }
+    it.pass = q - 1;
+    if (q > n_pass) it.tile = -1;
     return it;
 }
 
@@ -688,7 +685,6 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_experts_kernel(
         // ---------------------------------------------------- plan and copy
         // Takes items from the grid's counter and copies their rows; before the
         // first routed item, waits for the routing and lists the hit experts.
-        const int shared_items = tiles1 + tiles2 / kW2Tiles;
         uint32_t s = 0, ph = 0;
         uint32_t begun = 0;                // stages that a copy was issued to, and its parity
         const uint64_t policy = policy_evict_first();
@@ -697,28 +693,19 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_experts_kernel(
         int n_pass = -1;
         for (uint32_t n = 0; ok; ++n) {
             if (!mbar_wait_warp(&qfull[n & 1], n >> 1 & 1u, wc)) break;
-            int t = __shfl_sync(0xffffffffu, queue[n & 1], 0);
-            if (t >= shared_items && n_pass < 0) {
+            const int t = __shfl_sync(0xffffffffu, queue[n & 1], 0);
+            if (t >= tiles1 && n_pass < 0) {
                 n_pass = S <= 32 ? few_list_short<NT>(p, S, meta, lane, wc)
                                  : few_list<NT>(p, S, meta, lane, wc);
                 if (n_pass < 0) break;
             }
-            // item -> first tile
-            int first;
-            if (t < tiles1) first = t;
-            else if (t < shared_items) first = tiles1 + (t - tiles1) * kW2Tiles;
-            else {
-                t -= shared_items;
-                const int first2 = n_pass * tiles1;
-                first = tiles1 + tiles2 + (t < first2 ? t : first2 + (t - first2) * kW2Tiles);
-                if (first >= (n_pass + 1) * (tiles1 + tiles2)) first = -1;
-            }
+            const FewItem it = few_item(t, tiles1, tiles2, rcp1, rcp2, max(n_pass, 0));
             if (lane == 0) {
-                if (first < 0) *stop_s = 1;
+                if (it.tile < 0) *stop_s = 1;
                 mbar_arrive(&qempty[n & 1]);
             }
             __syncwarp();
-            if (first < 0) {
+            if (it.tile < 0) {
                 if (!mbar_wait_warp(&empty[s], ph ^ 1u, wc)) break;
                 if (lane == 0) {
                     info[s].tile = -1;
@@ -726,7 +713,6 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_experts_kernel(
                 }
                 break;
             }
-            const FewItem it = few_item(first, tiles1, tiles2, rcp1, rcp2, max(n_pass, 0));
             const int e = it.pass < 0 ? p.E : meta->pass_e[it.pass];
             const int rows = it.pass < 0 ? p.T : meta->pass_n[it.pass] | meta->pass_row[it.pass] << 16;
             const int K = it.second ? p.I : p.d;
