@@ -6,6 +6,7 @@ library in order; every step of the layer runs in the library's kernels:
   forward   moe_gate_route (or moe_route) -> moe_permute -> moe_expert_ffn
             (or the one-launch moe_expert_ffn_fused) -> moe_combine
   backward  moe_backward
+  decoding  moe_layer_few (at most 32 tokens, two launches)
 
 ("HyperParallel加速DeepSeek-V4.1多模态1M长序列训练" §2.3: MegaGate routing
 pipeline, then MegaMoE dispatch, two expert matmuls around the clamped
@@ -31,6 +32,11 @@ def gate_route_supported(d: int, E: int, k: int) -> bool:
 def mx_supported(d: int, I: int) -> bool:
     """Shapes the MXFP8 expert matmuls (moe_expert_ffn_mx) take."""
     return d % 256 == 0 and I % 128 == 0
+
+
+def fp8_supported(d: int, I: int) -> bool:
+    """Shapes the expert FFN on FP8 rows (moe_expert_ffn_fp8) takes."""
+    return d % 128 == 0 and I % 128 == 0
 
 
 def ffn_fused_supported(d: int, I: int) -> bool:
@@ -73,12 +79,23 @@ class MoELayer:
     is MXFP8 too.  With backward, the weights also get copies quantised along
     their other axis (moe_mx_quantize_t) and the backward runs the MX dgrad
     matmuls (moe_backward_mx).  Two launches (not fused_ffn).
+    fp8: the serving variant whose expert weights are FP8 (E4M3) with one fp32
+    scale per 128 x 128 block, quantised here (moe_fp8_quantize_weights; again
+    with quantize_weights() after they change).  forward() quantises each
+    step's token rows in the dispatch (moe_fp8_gather) and runs
+    moe_expert_ffn_fp8; forward_few() decodes from the same weights.  Forward
+    only (GroupedLinearFP8 has the matmul's gradients).
     """
 
     def __init__(self, dims: Dims, weights: dict, scaling: float, clamp: float = 7.0,
                  backward: bool = False, recompute: bool = False, device="cuda",
-                 fused_route: bool | None = None, fused_ffn: bool = False, mx: bool = False):
+                 fused_route: bool | None = None, fused_ffn: bool = False, mx: bool = False,
+                 fp8: bool = False):
         self.dims = dims
+        if fp8 and (mx or fused_ffn or backward or not fp8_supported(dims.d, dims.I)):
+            raise ValueError(f"the FP8 layer runs the forward in two launches and needs "
+                             f"d % 128 == 0, I % 128 == 0 (got {dims})")
+        self.fp8 = bool(fp8)
         if mx and (fused_ffn or not mx_supported(dims.d, dims.I)):
             raise ValueError(f"the MXFP8 layer runs two launches and needs "
                              f"d % 256 == 0, I % 128 == 0 (got {dims})")
@@ -112,6 +129,8 @@ class MoELayer:
         self.row_weight = torch.empty(D.S, dtype=torch.float32, **e)
         if self.mx:
             self._init_mx(weights, e)
+        elif self.fp8:
+            self._init_fp8(e)
         else:
             self.x_perm = torch.empty(D.R, D.d, dtype=torch.bfloat16, **e)
             self.h_perm = torch.empty(D.R, D.I, dtype=torch.bfloat16, **e)
@@ -138,6 +157,22 @@ class MoELayer:
             self.dW2 = torch.empty(D.E + 1, D.d, D.I, dtype=torch.float32, **e)
             self.dlogits = None
             self.dweights = None
+        self._few_ws = {}   # forward_few: a workspace for each number of tokens
+
+    def _init_fp8(self, e):
+        D = self.dims
+        f32, u8 = dict(dtype=torch.float32, **e), dict(dtype=torch.uint8, **e)
+        bd, bi = _lib.moe_fp8_scale_cols(D.d), _lib.moe_fp8_scale_cols(D.I)
+        G = D.E + 1
+        self.W13_q = torch.empty(G, 2 * D.I, D.d, **u8)
+        self.W13_s = torch.empty(G, 2 * bi, bd, **f32)
+        self.W2_q = torch.empty(G, D.d, D.I, **u8)
+        self.W2_s = torch.empty(G, bd, bi, **f32)
+        self.quantize_weights()
+        self.x_perm_q = torch.empty(D.R, D.d, **u8)
+        self.x_perm_s = torch.empty(D.R, bd, **f32)
+        self.h_q = torch.empty(D.R, D.I, **u8)
+        self.h_s = torch.empty(D.R, bi, **f32)
 
     def _init_mx(self, weights, e):
         D = self.dims
@@ -161,12 +196,17 @@ class MoELayer:
         self.h_sf = torch.empty(D.R, pi, **u8)
 
     def quantize_weights(self, stream=None):
-        """(MX layer) Quantise the expert weights from self.w into the MX
-        copies the matmuls read: along d and I for the forward, and with
+        """(MX and FP8 layers) Quantise the expert weights from self.w into the
+        copies the matmuls read.  MX: along d and I for the forward, and with
         backward also along d (W2) and 2I (W13) for the dgrad matmuls."""
         D = self.dims
         G = D.E + 1
         W13, W2 = self.w["W13"], self.w["W2"]
+        if self.fp8:
+            _lib.moe_fp8_quantize_weights(W13, G, 2 * D.I, D.d, self.W13_q, self.W13_s,
+                                          stream=stream)
+            _lib.moe_fp8_quantize_weights(W2, G, D.d, D.I, self.W2_q, self.W2_s, stream=stream)
+            return
         if self.backward_enabled:
             # one pass over each weight for both copies
             _lib.moe_mx_quantize_both(W13, G, 2 * D.I, D.d, self.W13_q, self.W13_sf,
@@ -194,9 +234,13 @@ class MoELayer:
 
     def dispatch(self, x, stream=None):
         D = self.dims
-        _lib.moe_permute(self.ids, self.weights, None if self.mx else x, D.T, D.d, D.E, D.k,
+        low = self.mx or self.fp8
+        _lib.moe_permute(self.ids, self.weights, None if low else x, D.T, D.d, D.E, D.k,
                          self.counts, self.offsets, self.row_token, self.slot_row,
-                         self.row_weight, None if self.mx else self.x_perm, self.ws, stream)
+                         self.row_weight, None if low else self.x_perm, self.ws, stream)
+        if self.fp8:
+            _lib.moe_fp8_gather(x, self.slot_row, D.T, D.d, D.k, self.x_perm_q, self.x_perm_s,
+                                stream)
         if self.mx:
             _lib.moe_mx_gather(x, self.slot_row, D.T, D.d, D.k, self.x_perm_q, self.x_perm_sf,
                                stream)
@@ -209,6 +253,12 @@ class MoELayer:
                                    self.row_weight, D.S, D.d, D.I, self.clamp, self.h_q,
                                    self.h_sf, self.y_perm, self.gu_save, stream)
             return
+        if self.fp8:
+            _lib.moe_expert_ffn_fp8(self.x_perm_q, self.x_perm_s, self.offsets, D.E + 1, D.R,
+                                    self.W13_q, self.W13_s, self.W2_q, self.W2_s,
+                                    self.row_weight, D.S, D.d, D.I, self.clamp, self.h_q,
+                                    self.h_s, self.y_perm, stream)
+            return
         if self.fused_ffn:
             _lib.moe_expert_ffn_fused(self.x_perm, self.offsets, D.E + 1, D.R, self.w["W13"],
                                       self.w["W2"], self.row_weight, D.S, D.d, D.I, self.clamp,
@@ -220,6 +270,8 @@ class MoELayer:
 
     def expert_gemm1(self, stream=None):
         D = self.dims
+        if self.fp8:
+            raise RuntimeError("the FP8 layer's expert matmuls are one call (experts())")
         if self.mx:
             _lib.moe_expert_gemm1_mx(self.x_perm_q, self.x_perm_sf, self.offsets, D.E + 1, D.R,
                                      self.W13_q, self.W13_sf, D.d, D.I, self.clamp, self.h_q,
@@ -230,6 +282,8 @@ class MoELayer:
 
     def expert_gemm2(self, stream=None):
         D = self.dims
+        if self.fp8:
+            raise RuntimeError("the FP8 layer's expert matmuls are one call (experts())")
         if self.mx:
             _lib.moe_expert_gemm2_mx(self.h_q, self.h_sf, self.offsets, D.E + 1, D.R, self.W2_q,
                                      self.W2_sf, self.row_weight, D.S, D.d, D.I, self.y_perm,
@@ -253,6 +307,35 @@ class MoELayer:
         self.experts(stream)
         self.combine(stream, y)
         return self.y if y is None else y
+
+    def forward_few(self, x, bias, is_vision=None, logit_offset=None, mode=MOE_ROUTE_TOPK,
+                    input_ids=None, tid2eid=None, stream=None, y=None):
+        """The forward of 1 to 32 tokens x [T, d] (any T, not dims.T) through
+        moe_layer_few, from the layer's bf16 or FP8 weights; returns y [T, d]
+        (a new tensor unless given).  It routes into buffers of its own: ids and
+        weights of the last forward() stay.  The workspace of a T is made at
+        its first call and kept, so calls of one T go to one stream."""
+        D = self.dims
+        if self.mx:
+            raise RuntimeError("moe_layer_few takes bf16 or FP8 weights")
+        T = int(x.shape[0])
+        if T not in self._few_ws:
+            n = _lib.moe_few_workspace_size(T, D.d, D.E, D.k, D.I)
+            if n == 0:
+                raise ValueError(f"moe_layer_few does not take {T} tokens of {D}")
+            # zero before its first use, whatever stream the calls then run on
+            self._few_ws[T] = torch.zeros(n, dtype=torch.uint8, device=x.device)
+            torch.cuda.current_stream(x.device).synchronize()
+        if y is None:
+            y = torch.empty(T, D.d, dtype=torch.bfloat16, device=x.device)
+        w = (dict(W13_q=self.W13_q, W13_s=self.W13_s, W2_q=self.W2_q, W2_s=self.W2_s)
+             if self.fp8 else dict(W13=self.w["W13"], W2=self.w["W2"]))
+        _lib.moe_layer_few(dict(
+            T=T, d=D.d, E=D.E, k=D.k, I=D.I, scaling=self.scaling, clamp=self.clamp,
+            mode=int(mode), vocab=0 if tid2eid is None else int(tid2eid.shape[0]), x=x,
+            W_g=self.w["W_g"], logit_offset=logit_offset, bias=bias, is_vision=is_vision,
+            input_ids=input_ids, tid2eid=tid2eid, y=y, ws=self._few_ws[T], **w), stream)
+        return y
 
     # ----------------------------------------------------------- backward
     def backward(self, dY, want_dlogits=False, want_dweights=False, stream=None,
@@ -332,7 +415,7 @@ class MoELayer:
     def _ensure_host_struct(self, train, bias, is_vision, logit_offset, mode, input_ids,
                             tid2eid):
         D = self.dims
-        if self.mx:
+        if self.mx or self.fp8:
             raise RuntimeError("the host-memory steps run the bf16 layer")
         if train and not self.backward_enabled:
             raise RuntimeError("layer built without backward buffers")
@@ -363,7 +446,68 @@ class MoELayer:
             self._host_key = key
 
 
-__all__ = ["Dims", "MoELayer", "MOE_ROUTE_TOPK", "MOE_ROUTE_HASH"]
+class GroupedLinearFP8:
+    """One projection per group (expert), y[r] = x[r] W[g]^T for the rows of
+    group g, with its three products in FP8 (E4M3, one fp32 scale per 128): the
+    forward, the data gradient (the same matmul on the weight's transposed
+    copy) and the weight gradient.
+
+    weight: bf16 [G, N, K] (CUDA), quantised here in both orientations; again
+    with quantize_weights() after it changes.  G = 1 is a dense layer.  rows:
+    the most rows of a call.  offsets: int32 [G+1] on the device, the groups'
+    first rows (as moe_permute writes them).
+    """
+
+    def __init__(self, weight, rows: int):
+        self.weight = weight
+        G, N, K = self.G, self.N, self.K = tuple(map(int, weight.shape))
+        self.rows = int(rows)
+        n = _lib.moe_fp8_wgrad_workspace_size(G, self.rows, N, K)
+        if N % 16 or K % 16 or n == 0:
+            raise ValueError(f"unsupported FP8 projection [{G}, {N}, {K}] of {rows} rows")
+        bn, bk = _lib.moe_fp8_scale_cols(N), _lib.moe_fp8_scale_cols(K)
+        dev = weight.device
+        u8, f32 = dict(dtype=torch.uint8, device=dev), dict(dtype=torch.float32, device=dev)
+        self.w_q, self.w_s = torch.empty(G, N, K, **u8), torch.empty(G, bn, bk, **f32)
+        self.wt_q, self.wt_s = torch.empty(G, K, N, **u8), torch.empty(G, bk, bn, **f32)
+        self.x_q, self.x_s = torch.empty(rows, K, **u8), torch.empty(rows, bk, **f32)
+        self.dy_q, self.dy_s = torch.empty(rows, N, **u8), torch.empty(rows, bn, **f32)
+        self.dW = torch.empty(G, N, K, **f32)
+        self.ws = torch.empty(n, **u8)
+        self.quantize_weights()
+
+    def quantize_weights(self, stream=None):
+        _lib.moe_fp8_quantize_weights(self.weight, self.G, self.N, self.K, self.w_q, self.w_s,
+                                      self.wt_q, self.wt_s, stream)
+
+    def forward(self, x, offsets, stream=None):
+        """y [R, N] bf16 of the rows x [R, K] bf16, R <= rows."""
+        R = int(x.shape[0])
+        self.x, self.offsets = x, offsets   # the backward reads them
+        y = torch.empty(R, self.N, dtype=torch.bfloat16, device=x.device)
+        if R == 0:
+            return y
+        _lib.moe_fp8_quantize(x, R, self.K, self.x_q, self.x_s, stream)
+        _lib.moe_fp8_matmul(self.x_q, self.x_s, offsets, self.G, R, self.w_q, self.w_s, None, 0,
+                            self.N, self.K, y, stream)
+        return y
+
+    def backward(self, dy, stream=None):
+        """dX [R, K] bf16 of the last forward; self.dW [G, N, K] fp32."""
+        R = int(dy.shape[0])
+        dx = torch.empty(R, self.K, dtype=torch.bfloat16, device=dy.device)
+        if R == 0:
+            self.dW.zero_()
+            return dx
+        _lib.moe_fp8_quantize(dy, R, self.N, self.dy_q, self.dy_s, stream)
+        _lib.moe_fp8_matmul(self.dy_q, self.dy_s, self.offsets, self.G, R, self.wt_q, self.wt_s,
+                            None, 0, self.K, self.N, dx, stream)
+        _lib.moe_fp8_wgrad(dy, self.x, self.offsets, self.G, R, self.N, self.K, self.dW, self.ws,
+                           stream)
+        return dx
+
+
+__all__ = ["Dims", "GroupedLinearFP8", "MoELayer", "MOE_ROUTE_TOPK", "MOE_ROUTE_HASH"]
 
 
 class HostPipeline:

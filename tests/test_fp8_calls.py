@@ -144,3 +144,13 @@ def test_reference_few_layer_against_dense_sum():
             gu = W13[e] @ x[t]
             want += f * (W2[e] @ R.silu_clamped(gu[:I], gu[I:], 7.0))
         assert np.allclose(want, y[t], rtol=1e-12, atol=1e-12)
+
+
+def test_layer_refusals():
+    from moe_expert_layer_04_gb300.layer import Dims, MoELayer
+    for kw in (dict(backward=True), dict(mx=True), dict(fused_ffn=True)):
+        with pytest.raises(ValueError):
+            MoELayer(Dims(8, 256, 32, 2, 128), {}, 1.0, fp8=True, device="cpu", **kw)
+    for d, I in ((192, 128), (256, 64)):
+        with pytest.raises(ValueError):
+            MoELayer(Dims(8, d, 32, 2, I), {}, 1.0, fp8=True, device="cpu")
