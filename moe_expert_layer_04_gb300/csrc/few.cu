@@ -107,15 +107,6 @@ __device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                        uint32_t a3, uint32_t b0, uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
-        "{%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
 // A stage's two boxes of eight rows and the bytes that `bar` is to count.  With an L2
 // policy: the weights pass through L2 once and must not push out what every call uses
 // again (the kernels' code, W_g, the token rows).  Called by a whole warp, which elects
@@ -487,15 +478,6 @@ __device__ __forceinline__ FewItem few_item(int t, int tiles1, int tiles2, float
     it.pass = q - 1;
     if (q > n_pass) it.tile = -1;
     return it;
-}
-
-// Four E4M3 codes -> two f16 pairs, exact, a NaN code to a NaN: two conversion
-// instructions.  (To bf16 there is none: through fp32 it takes eight, and by
-// moving bits ten on the integer pipe, 0.75 us of the SM for the 32 KB of a
-// stage, as long as they take to arrive.)  So the token operand is f16 too.
-__device__ __forceinline__ void e4m3x4_f16(uint32_t w, uint32_t &lo, uint32_t &hi) {
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(lo) : "h"((uint16_t)(w & 0xFFFFu)));
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(hi) : "h"((uint16_t)(w >> 16)));
 }
 
 __device__ __forceinline__ float exp2i(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }

@@ -169,6 +169,9 @@ moe_status launch_fp8_columns(const uint16_t *src, const int32_t *offsets, const
 moe_status launch_fp8_matmul(const uint8_t *aq, const float *as, const int32_t *offsets, int G,
                              int max_rows, const uint8_t *bq, const float *bs, const float *row_w,
                              int w_rows, int N, int K, uint16_t *out, cudaStream_t st);
+moe_status launch_fp8_thin(const uint8_t *aq, const float *as, const int32_t *offsets, int max_rows,
+                           const uint8_t *bq, const float *bs, const float *row_w, int w_rows,
+                           int N, int K, uint16_t *out, cudaStream_t st);
 moe_status launch_fp8_ffn1(const uint8_t *xq, const float *xs, const int32_t *offsets, int G,
                            int max_rows, const uint8_t *W13q, const float *W13s, int d, int I,
                            float clamp, uint8_t *hq, float *hs, cudaStream_t st);

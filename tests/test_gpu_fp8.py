@@ -152,7 +152,8 @@ def check(got, ref, absdot, K, bf16_out, what):
 MATMULS = [([1], 8, 16), ([1], 512, 4096), ([3], 136, 400), ([128], 256, 128), ([129, 0, 1, 260], 264, 272),
            ([17, 40, 0, 200, 5], 640, 1152), ([0, 0], 64, 64), ([300], 1000, 2048), ([2] * 40, 72, 144),
            ([32], 384, 512), ([33], 384, 512), ([31, 0, 1], 264, 656),
-           ([650, 100, 0, 700], 520, 400), ([513], 264, 1040)]
+           ([650, 100, 0, 700], 520, 400), ([513], 264, 1040), ([8], 24, 4112), ([5], 520, 1040),
+           ([9], 264, 272)]
 
 
 @pytest.mark.parametrize("counts,N,K", MATMULS)
