@@ -23,7 +23,8 @@ __device__ __forceinline__ uint32_t amax_bits_of(uint32_t m) {
 // elements of one token at a time, all loads issued before the first use.
 // k = 0: plain quantisation, row t to row t; k > 0: row t goes to its k
 // permuted rows and to row T*k + t, quantised once.  Bound by HBM: 2 bytes
-// read an element, 1 + 1/32 written for each copy.
+// read an element, 1 + 1/32 written for each copy.  4096 tokens of 4096 to seven
+// rows each: 24.3 us, 6.4 TB/s.
 constexpr int kRowU = 2;
 
 __global__ void __launch_bounds__(256)
@@ -206,7 +207,10 @@ __global__ void __launch_bounds__(256)
 // group's first row (the last block filled with zeros), every column of a
 // block one scale block.  Block b of all groups together ("chunk") is written
 // transposed: code (c, r) at (b C + c) 128 + r, scale (b, c) at b C + c, so
-// that a matmul stage is one contiguous run of rows of 128 codes.
+// that a matmul stage is one contiguous run of rows of 128 codes.  Bound by HBM in
+// principle; 6789 rows of 4096 in 9 groups take 19.5 us (4.3 TB/s: 2.6 rounds of CTAs,
+// each of which loads once and then stores).  Both operands in one launch measured
+// 243 us for the whole gradient against 234: the second launch begins during the first.
 // first[g] is the group's first chunk (fp8_chunks_kernel); blockIdx.y = chunk.
 __global__ void __launch_bounds__(256)
     fp8_columns_kernel(const uint16_t *__restrict__ src, const int32_t *__restrict__ offsets,

@@ -11,20 +11,36 @@
 //   FP8_WGRAD  dW[g][m, n] = sum_b sa[b, m] sb[b, n] sum_{r in block b} A B
 //              over the chunks of 128 rows of group g                    fp32
 //
-// The tensor core sums the products of one block exactly as far as fp32 goes
-// (tcgen05.mma kind::f8f6f4: E4M3 operands straight from shared memory, fp32
-// accumulator in tensor memory); the scales differ from block to block, so
-// each block's sum leaves tensor memory, is multiplied by its scales and added
-// to the tile's accumulator in registers, in fp32.  Tiles are 128 x 256: a
-// block costs the tensor core 4 MMAs of 128 x 256 x 32, and the eight epilogue
-// warps 32768 fused multiply-adds, two to an instruction; two tensor memory
-// accumulators let the two overlap.
+// The tensor core sums the products of one block in fp32 (tcgen05.mma
+// kind::f8f6f4: E4M3 operands straight from shared memory, accumulator in tensor
+// memory); the scales differ from block to block, so each block's sum leaves tensor
+// memory, is multiplied by its scales and added to the tile's accumulator in
+// registers, in fp32.
 //
-// One CTA per SM, persistent, 12 warps: warp 0 TMA producer (48 KB a stage,
-// 128-byte swizzle), warp 1 tensor memory owner and MMA issuer, warps 4-11
-// accumulate (thread = row; two warps per lane quadrant, 128 columns each).
-// Every wait is bounded; on a timeout the CTA records MOE_ERR_TIMEOUT, drains
-// its copies and MMAs, frees tensor memory and returns.
+// What bounds it: for a 128 x 256 tile a block costs the tensor core 537 cycles,
+// measured alone, and reading its sums 256 more on the same tensor memory port, which
+// the two cannot share: 793 cycles a block, whatever feeds it (a pair of SMs on one
+// 256 x 256 tile measured 1120-1220; its operands cross shared memory half as often,
+// but that is not the limit).  The loop below takes 770-850.  At that rate the
+// products of a long run of blocks go at 2.0 PFLOP/s, half of what the tensor core
+// does on FP8 without block scales.  The rest is what a tile costs outside its loop:
+// the first operands of the next tile and two blocks of products run during it, then
+// the tensor core waits.  So the output leaves through shared memory by TMA stores that
+// run during the next tile (ROWS: 1500 cycles a tile, 3000 straight from the registers),
+// the next tile's place and scales are found before it, and the weight gradient, whose
+// loops are short (a group of 900 rows has 7 blocks) and whose fp32 output is 128 KB a
+// tile, writes two pieces while two wait: 4000 cycles a tile, a third of its time.
+//
+// Measured (time of the call): 12345 rows in 33 uneven groups, 4096 x 2048 weights: 114-118
+// us, 1.8 PFLOP/s; expert FFN of 32768 rows over 33 groups, d = 4096, I = 2048: 794-818 us,
+// 2.0-2.1 PFLOP/s; of 777 rows over 9: 66 us, where the weights alone are 36 us of HBM
+// (160-190 tiles on 152 SMs); weight gradient 4096 x 4096 of 6789 rows in 9 groups: 234 us
+// with the quantisation of both operands (39 us), 604 MB of output.
+//
+// One CTA per SM, persistent, 12 warps: warp 0 TMA producer, warp 1 tensor memory owner
+// and MMA issuer, warps 4-11 accumulate (thread = row; two warps per lane quadrant, half
+// of the columns each).  Every wait is bounded; on a timeout the CTA records
+// MOE_ERR_TIMEOUT, drains its copies and MMAs, frees tensor memory and returns.
 #include <cstring>
 #include <type_traits>
 
@@ -82,7 +98,8 @@ struct F8Shape {
     static constexpr int STAGE = kF8A + BN * 128;
     static constexpr int NACC = BN == 256 ? 2 : 4;   // accumulators in tensor memory
     static constexpr int CW = BN / 2;                // columns of an epilogue warp
-    static constexpr int CH = MODE == FP8_WGRAD ? 16 : BN < 128 ? CW : 32;   // of them in flight at a time
+    // of them in flight from tensor memory at a time
+    static constexpr int CH = MODE == FP8_WGRAD ? 16 : BN < 128 ? CW : 32;
     static constexpr uint32_t IDESC =
         (1u << 4) | ((uint32_t)(BN >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
     // FFN1: exchange of the largest |h|; WGRAD: ring of both operands' scales
@@ -91,7 +108,8 @@ struct F8Shape {
     // pieces of output on their way to memory, for each epilogue warp
     static constexpr int OUTS = MODE == FP8_FFN1 || BN < 128 ? 0 : BN / 128;
     static constexpr int OUT = kF8Epi * OUTS * kF8OutPiece;
-    static constexpr int GROUP = MODE == FP8_WGRAD ? 4 : 8;   // bytes of a group's offset and first tile
+    // bytes of a group's offset and first tile
+    static constexpr int GROUP = MODE == FP8_WGRAD ? 4 : 8;
     static constexpr int FIXED = ST * STAGE + OUT + SIDE + kF8Bars;
     static constexpr int smem(int G) { return 1024 + FIXED + GROUP * (G + 2); }
 };
@@ -639,7 +657,11 @@ static int box_rows(int max_rows) { return max_rows < 128 ? (max_rows + 7) & ~7 
 
 // Column width of a tile: wide ones read fewer operand bytes for a product, narrow
 // ones spread over the SMs where there are few.  The least of (rounds of tiles over
-// the SMs) x (cycles of a block of 128 along the contraction).
+// the SMs) x (cycles of a block of 128 along the contraction), the cycles measured with
+// one round of tiles.  Widths 256 / 128 / 64 / 32 with 4096 x 4096 weights: 128 rows 17.9
+// / 11.7 / 10.3 / 9.4 us, 512 rows 17.6 / 11.9 / 17.5 / 29.0, 1024 rows 18.0 / 20.2 / 32.0 /
+// 48.5, 4096 rows 60.3 / 60.7 / 105 / 179; 288 rows in 9 groups, 4096 x 2048 weights: 15.4 /
+// 14.9 / 17.2 / 27.8.  (For each of these the rule takes the fastest.)
 static int rows_bn(int max_rows, int G, int N) {
     const long long rows = (max_rows + 127) / 128 + (G < max_rows ? G : max_rows) - 1;
     int best = 256;

@@ -366,3 +366,43 @@ def test_other_stream_and_graph():
     graph.replay()
     ok()
     assert torch.equal(outs[0], outs[1]) and torch.equal(outs[0], outs[2])
+
+
+def test_places_behind_32_bits():
+    """Weights of more than 2^32 bytes and codes of more than 2^31: the last
+    group's products and the last rows' codes."""
+    G, N, K, rows = 520, 2048, 4096, 37
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    w = torch.zeros(G, N, K, dtype=torch.bfloat16, device="cuda")
+    assert w.numel() * 2 > 2 ** 32 and w.numel() > 2 ** 31
+    last = (torch.randn(N, K, generator=gen, device="cuda") * K ** -0.5).to(torch.bfloat16)
+    w[-1] = last
+    q, qt = (torch.empty(G, *s, dtype=torch.uint8, device="cuda") for s in ((N, K), (K, N)))
+    s = torch.empty(G, N // 128, K // 128, device="cuda")
+    st = torch.empty(G, K // 128, N // 128, device="cuda")
+    _lib.moe_fp8_quantize_weights(w, G, N, K, q, s, qt, st)
+    one = [torch.empty(1, *t.shape[1:], dtype=t.dtype, device="cuda") for t in (q, s, qt, st)]
+    _lib.moe_fp8_quantize_weights(last[None].contiguous(), 1, N, K, *one)
+    for t, o in zip((q, s, qt, st), one):
+        assert torch.equal(t[-1], o[0]) and not (t[-2].float() * (t.dtype == torch.uint8)).any()
+    # the same rows as the last group's and as a group of its own
+    x = torch.randn(rows, K, generator=gen, device="cuda").to(torch.bfloat16)
+    xq, xs = torch.empty(rows, K, dtype=torch.uint8, device="cuda"), torch.empty(rows, K // 128,
+                                                                                 device="cuda")
+    _lib.moe_fp8_quantize(x, rows, K, xq, xs)
+    offsets = torch.zeros(G + 1, dtype=torch.int32, device="cuda")
+    offsets[-1] = rows
+    a, b = (torch.empty(rows, N, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    _lib.moe_fp8_matmul(xq, xs, offsets, G, rows, q, s, None, 0, N, K, a)
+    _lib.moe_fp8_matmul(xq, xs, offsets[-2:].contiguous(), 1, rows, one[0], one[1], None, 0, N, K, b)
+    # (each one bf16 rounding of the same sums)
+    torch.testing.assert_close(a, b, rtol=2.0 ** -7, atol=1e-4)
+    assert float(a.float().std()) > 0.5
+    # rows quantised in place: the last of more than 2^31 elements
+    flat = w.view(-1, 128)
+    _lib.moe_fp8_quantize(flat, flat.shape[0], 128, q.view(-1, 128), torch.empty(
+        flat.shape[0], 1, device="cuda"))
+    tail = torch.empty(N * K // 128, 128, dtype=torch.uint8, device="cuda")
+    _lib.moe_fp8_quantize(last, N * K // 128, 128, tail, torch.empty(N * K // 128, 1, device="cuda"))
+    assert torch.equal(q[-1].view(-1, 128), tail)
+    ok()
