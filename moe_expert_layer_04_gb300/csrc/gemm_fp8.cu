@@ -661,9 +661,12 @@ static int box_rows(int max_rows) { return max_rows < 128 ? (max_rows + 7) & ~7 
 // one round of tiles.  Widths 256 / 128 / 64 / 32 with 4096 x 4096 weights: 128 rows 17.9
 // / 11.7 / 10.3 / 9.4 us, 512 rows 17.6 / 11.9 / 17.5 / 29.0, 1024 rows 18.0 / 20.2 / 32.0 /
 // 48.5, 4096 rows 60.3 / 60.7 / 105 / 179; 288 rows in 9 groups, 4096 x 2048 weights: 15.4 /
-// 14.9 / 17.2 / 27.8.  (For each of these the rule takes the fastest.)
+// 14.9 / 17.2 / 27.8.  (The rule takes the fastest, in the last case the next.)
 static int rows_bn(int max_rows, int G, int N) {
-    const long long rows = (max_rows + 127) / 128 + (G < max_rows ? G : max_rows) - 1;
+    // row tiles: one for each group, or half a tile more than its rows fill
+    const int groups = G < max_rows ? G : max_rows;
+    const long long filled = (max_rows + 127) / 128 + (groups - 1) / 2;
+    const long long rows = filled > groups ? filled : groups;
     int best = 256;
     long long least = -1;
     const int width[4] = {256, 128, 64, 32}, cycles[4] = {850, 520, 384, 320};
