@@ -776,18 +776,18 @@ _FEW_TYPES = dict(x=BF16, W_g=BF16, logit_offset=F32, bias=F32, is_vision=U8, in
                   ids=I32, weights=F32, ws=U8)
 
 
+_FEW_FIELDS = [(name, _FEW_TYPES.get(name)) for name, _ in FewArgs._fields_ if name != "ws_bytes"]
+assert FewArgs._fields_[-1][0] == "ws_bytes"
+
+
 def moe_layer_few(args: dict, stream=None):
     """args: the fields of moe_few_args (tensors for pointers, None for NULL);
     ws: moe_few_workspace_size bytes, zeroed once before the first call."""
-    a = FewArgs()
-    for name, _ in FewArgs._fields_:
-        if name == "ws_bytes":
-            continue
+    vals = []
+    for name, dtype in _FEW_FIELDS:
         v = args.get(name)
-        if name in _FEW_TYPES:
-            setattr(a, name, _ptr(v, _FEW_TYPES[name], name))
-        else:
-            setattr(a, name, 0 if v is None else v)
-    a.ws_bytes = 0 if args.get("ws") is None else args["ws"].numel()
+        vals.append(_ptr(v, dtype, name) if dtype is not None else 0 if v is None else v)
+    ws = args.get("ws")
+    a = FewArgs(*vals, 0 if ws is None else ws.numel())
     st = load().moe_layer_few(ctypes.byref(a), _stream(stream))
     _check("moe_layer_few", st)

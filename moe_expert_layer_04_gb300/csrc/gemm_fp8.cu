@@ -29,12 +29,13 @@
 // run during the next tile (ROWS: 1500 cycles a tile, 3000 straight from the registers),
 // the next tile's place and scales are found before it, and the weight gradient, whose
 // loops are short (a group of 900 rows has 7 blocks) and whose fp32 output is 128 KB a
-// tile, writes two pieces while two wait: 4000 cycles a tile, a third of its time.
+// tile, takes 4000 cycles for it, a third of its time: the output crosses shared memory
+// twice (2048 cycles) while the next tile's first products do (1536).
 //
 // Measured (time of the call): 12345 rows in 33 uneven groups, 4096 x 2048 weights: 114-118
 // us, 1.8 PFLOP/s; expert FFN of 32768 rows over 33 groups, d = 4096, I = 2048: 794-818 us,
-// 2.0-2.1 PFLOP/s; of 777 rows over 9: 66 us, where the weights alone are 36 us of HBM
-// (160-190 tiles on 152 SMs); weight gradient 4096 x 4096 of 6789 rows in 9 groups: 234 us
+// 2.0-2.1 PFLOP/s; of 777 rows over 9: 63 us, where the weights alone are 30 us of HBM
+// (176 tiles on 152 SMs); weight gradient 4096 x 4096 of 6789 rows in 9 groups: 234 us
 // with the quantisation of both operands (39 us), 604 MB of output.
 //
 // One CTA per SM, persistent, 12 warps: warp 0 TMA producer, warp 1 tensor memory owner
