@@ -726,7 +726,8 @@ moe_status moe_expert_ffn_fp8(const uint8_t *x_perm_q, const float *x_perm_s,
  * I % 64 == 0, k <= min(8, E), E <= 1024.
  * Workspace: moe_few_workspace_size bytes (0: not supported), ZERO before its
  * first use; every call leaves its counters zero again, so a buffer is zeroed
- * once and then kept for calls of the same sizes (other sizes: zero it again).
+ * once and then kept for calls of the same sizes (other sizes, or a call that
+ * recorded MOE_ERR_TIMEOUT: zero it again).
  * Calls that share a workspace must be in order on one stream. */
 typedef struct {
     int T, d, E, k, I;

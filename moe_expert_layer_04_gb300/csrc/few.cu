@@ -1254,7 +1254,7 @@ moe_status launch_few(const moe_few_args *a, cudaStream_t st) {
     // tiles of one or two stages: see the multiplying warps
     p.by_tile = p.d * elt <= 2 * p.cps13 * kChunk && p.I * elt <= 2 * p.cps2 * kChunk;
     const int et = (p.E + 15) / 16;
-    int splits = (num_sms() + et - 1) / et;   // every SM has a part
+    int splits = num_sms() / et;   // one round: an SM takes one CTA of many experts
     splits = splits < 1 ? 1 : splits > kGateSplits ? kGateSplits : splits;
     if (splits > p.d / 32) splits = p.d / 32;
     p.splits = splits;

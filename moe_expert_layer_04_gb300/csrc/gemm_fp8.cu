@@ -697,7 +697,7 @@ moe_status launch_fp8_matmul(const uint8_t *aq, const float *as, const int32_t *
     p.a_rows = box_rows(max_rows);
     if (!encode_tmap_u8_2d(&p.tmA, aq, K, max_rows, K, 128, p.a_rows, 128) ||
         !encode_tmap_u8_2d(&p.tmB, bq, K, (uint64_t)G * N, K, 128, BN, 128) ||
-        !encode_tmap_bf16_2d(&p.tmO, out, N, max_rows, 2ULL * N, 64, 32))
+        (BN >= 128 && !encode_tmap_bf16_2d(&p.tmO, out, N, max_rows, 2ULL * N, 64, 32)))
         return MOE_ERR_CUDA;
     p.offsets = offsets;
     p.sa = as;
