@@ -186,6 +186,9 @@ __device__ __forceinline__ uint64_t wait_slot(const uint64_t *p, const WaitCtl &
 // all of the last CTA's threads add up the partial logits where they fit its shared
 // memory, and the largest key of a round is found by two reductions of the warp over
 // keys in the order of unsigned integers.
+__device__ __forceinline__ void prefetch_l2(const void *p) {
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
+}
 __device__ __forceinline__ uint32_t ordered(float v) {
     const uint32_t u = __float_as_uint(v);
     return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
@@ -249,6 +252,20 @@ __global__ void __launch_bounds__(kGateWarps * 32) few_gate_kernel(const __grid_
             few_token_f16(p, t, warp_top);
         return;
     }
+    // what the last CTA will read once more, into L2 in the meantime
+    if (blockIdx.x == 0 && blockIdx.y == 0) {
+        for (int i = threadIdx.x * 32; i < p.E; i += kGateWarps * 32 * 32) {
+            if (p.logit_offset) prefetch_l2(p.logit_offset + i);
+            if (!p.hash) {
+                prefetch_l2(p.bias + i);
+                if (p.is_vision) prefetch_l2(p.bias + p.E + i);
+            }
+        }
+        if (p.hash && (int)threadIdx.x < p.T) {
+            const int tok = p.input_ids[threadIdx.x];
+            if (tok >= 0 && tok < p.vocab) prefetch_l2(p.tid2eid + (size_t)tok * p.k);
+        }
+    }
     __shared__ float red[kGateWarps][4][32], keys[kGateWarps * 4 * 32];
     __shared__ int s_last;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -288,7 +305,6 @@ __global__ void __launch_bounds__(kGateWarps * 32) few_gate_kernel(const __grid_
         s_last = atom_add_acq_rel(p.counters, 1) == (int)gridDim.x * p.splits - 1;
     __syncthreads();
     if (!s_last) return;
-    __threadfence();
     float *scores = &red[0][0][0];
     const bool all = !p.hash && p.T * p.E <= kGateWarps * 4 * 32;
     if (all) {
