@@ -14,9 +14,10 @@
 // and what cannot hide is the start (launch, gate, routing) and the two places
 // where one matmul needs all of the one before it.  The second kernel keeps the
 // stream running with a warp for each of the things that wait:
-//   1 takes item numbers from the grid's counter, two ahead
-//   1 lists the hit experts and copies weight rows into a ring in shared memory
-//     (two TMA boxes a stage, 32 KB), across the boundaries of the phases
+//   1 takes item numbers from the grid's counter, two ahead, and lists the hit
+//     experts once they are known
+//   1 copies weight rows into a ring in shared memory (two TMA boxes a stage, 32
+//     KB), across the boundaries of the phases
 //   1 waits for a stage's token operands (a phase's dependence on the one before)
 //     and brings them
 //  16 multiply, in two groups that take stages, or short tiles, in turn
@@ -437,12 +438,14 @@ __global__ void __launch_bounds__(kGateWarps * 32) few_gate_kernel(const __grid_
 
 // What every role knows about the routing: the hit experts in order, each cut
 // into passes of at most 8 NT rows, and the slots (token * k + j) of each.
+struct alignas(8) FewPass {
+    int e;                             // expert
+    int rows;                          // rows | first entry in `slot` << 16
+};
 struct alignas(8) FewMeta {
-    int n_units;                       // contributions that a column tile waits for
+    int n_units, n_pass;               // contributions that a column tile waits for; passes
     float w[kFewS];                    // routing weight of each slot
-    int16_t pass_e[kFewS];
-    int16_t pass_row[kFewS];           // first entry in `slot`
-    int16_t pass_n[kFewS];             // rows
+    FewPass pass[kFewS];
     int16_t slot[kFewS];
     int16_t token[kFewS];              // of each entry of `slot`
     // scratch: of each slot, and rows, then first slot of each expert
@@ -537,9 +540,8 @@ template <int NT>
 __device__ __forceinline__ void few_passes(FewMeta *meta, int e, int r, int first_row, int first,
                                            int passes) {
     for (int j = 0; j < passes; ++j) {
-        meta->pass_e[first + j] = (int16_t)e;
-        meta->pass_row[first + j] = (int16_t)(first_row + j * 8 * NT);
-        meta->pass_n[first + j] = (int16_t)min(8 * NT, r - j * 8 * NT);
+        const int row = first_row + j * 8 * NT;
+        meta->pass[first + j] = {e, min(8 * NT, r - j * 8 * NT) | row << 16};
     }
 }
 
@@ -691,9 +693,8 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_experts_kernel(
     int *y_done = h_done + 1 + kFewS;
 
     if (warp == kCopyWarp) {
-        // ---------------------------------------------------- plan and copy
-        // Takes items from the grid's counter and copies their rows; before the
-        // first routed item, waits for the routing and lists the hit experts.
+        // ------------------------------------------------------------- copy
+        // the rows of the items whose numbers it is given.
         uint32_t s = 0, ph = 0;
         uint32_t begun = 0;                // stages that a copy was issued to, and its parity
         const uint64_t policy = policy_evict_first();
@@ -703,11 +704,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_experts_kernel(
         for (uint32_t n = 0; ok; ++n) {
             if (!mbar_wait_warp(&qfull[n & 1], n >> 1 & 1u, wc)) break;
             const int t = __shfl_sync(0xffffffffu, queue[n & 1], 0);
-            if (t >= tiles1 && n_pass < 0) {
-                n_pass = S <= 32 ? few_list_short<NT>(p, S, meta, lane, wc)
-                                 : few_list<NT>(p, S, meta, lane, wc);
-                if (n_pass < 0) break;
-            }
+            if (t >= tiles1 && n_pass < 0) n_pass = meta->n_pass;   // listed before this number
             const FewItem it = few_item(t, tiles1, tiles2, rcp1, rcp2, max(n_pass, 0));
             if (lane == 0) {
                 if (it.tile < 0) *stop_s = 1;
@@ -722,8 +719,9 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_experts_kernel(
                 }
                 break;
             }
-            const int e = it.pass < 0 ? p.E : meta->pass_e[it.pass];
-            const int rows = it.pass < 0 ? p.T : meta->pass_n[it.pass] | meta->pass_row[it.pass] << 16;
+            FewPass ps = {p.E, p.T};
+            if (it.pass >= 0) ps = meta->pass[it.pass];
+            const int e = ps.e, rows = ps.rows;
             const int K = it.second ? p.I : p.d;
             const int whole = K * SH::ELT / kChunk;   // chunks
             const int chunks = (K * SH::ELT + kChunk - 1) / kChunk;
@@ -740,8 +738,9 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_experts_kernel(
                     const int row = it.second ? tile * 16
                                               : tile * 8 + (lane >= kStageChunks ? p.I : 0);
                     const int all = it.second ? p.d : 2 * p.I;
+                    // (a scale stands for 2^14 weights: their number is an int)
                     sc = (it.second ? p.W2_s : p.W13_s) +
-                         ((size_t)e * fp8_blocks(all) + row / kFp8Block) * kb + my_kb;
+                         (e * fp8_blocks(all) + row / kFp8Block) * kb + my_kb;
                 }
                 for (int c0 = 0; c0 < chunks; c0 += cps) {
                     if (!mbar_wait_warp(&empty[s], ph ^ 1u, wc)) { ok = false; break; }
@@ -966,7 +965,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_experts_kernel(
                     const bool tail = chunk * 128 + 64 == K;
                     if (tail) {
                         const uint8_t *w = static_cast<const uint8_t *>(second ? p.W2 : p.W13);
-                        const int e = q.y < 0 ? p.E : meta->pass_e[q.y];
+                        const int e = q.y < 0 ? p.E : meta->pass[q.y].e;
                         const size_t r = second ? (size_t)e * p.d + q.x * 16 + pr
                                                 : (size_t)e * 2 * p.I + q.x * 8 + pr;
                         w += r * K + K - 64 + c * 16;
@@ -1042,13 +1041,25 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_experts_kernel(
         }
     } else if (warp == kTicketWarp) {
         // ------------------------------------------------------ item numbers
-        // from the grid's counter, two ahead of the copies.  A warp of its own: the
-        // counter answers after a microsecond, and whoever waits for it does nothing
-        // else (a warp's arrivals on barriers wait for its outstanding atomics too).
+        // from the grid's counter, two ahead of the copies; before the first routed one,
+        // waits for the routing and lists the hit experts, while the copies of the items
+        // ahead of it go out.  A warp of its own: the counter answers after a microsecond,
+        // and whoever waits for it does nothing else (a warp's arrivals on barriers wait
+        // for its outstanding atomics too).
+        int n_pass = -1;
         for (uint32_t n = 0;; ++n) {
             if (!mbar_wait_warp(&qempty[n & 1], (n >> 1 & 1u) ^ 1u, wc) || *stop_s) break;
+            int t = 0;
+            if (lane == 0) t = atomicAdd(p.counters + 1, 1);
+            t = __shfl_sync(0xffffffffu, t, 0);
+            if (t >= tiles1 && n_pass < 0) {
+                n_pass = S <= 32 ? few_list_short<NT>(p, S, meta, lane, wc)
+                                 : few_list<NT>(p, S, meta, lane, wc);
+                if (n_pass < 0) break;
+                if (lane == 0) meta->n_pass = n_pass;
+            }
             if (lane == 0) {
-                queue[n & 1] = atomicAdd(p.counters + 1, 1);
+                queue[n & 1] = t;
                 mbar_arrive(&qfull[n & 1]);
             }
             __syncwarp();
