@@ -14,8 +14,7 @@
 // and what cannot hide is the start (launch, gate, routing) and the two places
 // where one matmul needs all of the one before it.  The second kernel keeps the
 // stream running with a warp for each of the things that wait:
-//   1 takes item numbers from the grid's counter, two ahead, and lists the hit
-//     experts once they are known
+//   1 takes item numbers from the grid's counter, one ahead of the copies
 //   1 copies weight rows into a ring in shared memory (two TMA boxes a stage, 32
 //     KB), across the boundaries of the phases
 //   1 waits for a stage's token operands (a phase's dependence on the one before)
@@ -657,9 +656,9 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_experts_kernel(
     uint64_t *rfull = empty + STAGES;        // a buffer of `red` has every warp's partial sums
     uint64_t *rempty = rfull + BUFS;         // ... and has been read
     uint64_t *qfull = rempty + BUFS;         // an item's number is in `queue`
-    uint64_t *qempty = qfull + 2;            // ... and has been taken
-    volatile int *queue = reinterpret_cast<volatile int *>(qempty + 2);
-    volatile int *abort_s = queue + 2;
+    uint64_t *qempty = qfull + 1;            // ... and has been taken
+    volatile int *queue = reinterpret_cast<volatile int *>(qempty + 1);
+    volatile int *abort_s = queue + 1;
     int *last_s = const_cast<int *>(abort_s) + 1;
     volatile int *stop_s = last_s + 1;       // no more items are wanted
     static_assert(sizeof(FewMeta) % 8 == 0, "the barriers behind it are 8-byte aligned");
@@ -676,10 +675,8 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_experts_kernel(
             mbar_init(&rfull[b], p.by_tile ? kGroupWarps : kMulWarps);
             mbar_init(&rempty[b], 1);
         }
-        mbar_init(&qfull[0], 1);
-        mbar_init(&qfull[1], 1);
-        mbar_init(&qempty[0], 1);
-        mbar_init(&qempty[1], 1);
+        mbar_init(qfull, 1);
+        mbar_init(qempty, 1);
         *abort_s = 0;
         *stop_s = 0;
         fence_barrier_init();
@@ -702,13 +699,19 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_experts_kernel(
         bool ok = true;
         int n_pass = -1;
         for (uint32_t n = 0; ok; ++n) {
-            if (!mbar_wait_warp(&qfull[n & 1], n >> 1 & 1u, wc)) break;
-            const int t = __shfl_sync(0xffffffffu, queue[n & 1], 0);
-            if (t >= tiles1 && n_pass < 0) n_pass = meta->n_pass;   // listed before this number
+            if (!mbar_wait_warp(qfull, n & 1u, wc)) break;
+            const int t = __shfl_sync(0xffffffffu, *queue, 0);
+            // A long list is made ahead by the warp that takes the numbers (23 tokens of
+            // 5 experts 86 -> 82 us); a short one here, as late as it is needed (one
+            // token 37.8 us, 38.5 if made there).
+            if (t >= tiles1 && n_pass < 0) {
+                n_pass = S <= 32 ? few_list_short<NT>(p, S, meta, lane, wc) : meta->n_pass;
+                if (n_pass < 0) break;
+            }
             const FewItem it = few_item(t, tiles1, tiles2, rcp1, rcp2, max(n_pass, 0));
             if (lane == 0) {
                 if (it.tile < 0) *stop_s = 1;
-                mbar_arrive(&qempty[n & 1]);
+                mbar_arrive(qempty);
             }
             __syncwarp();
             if (it.tile < 0) {
@@ -1041,26 +1044,24 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_experts_kernel(
         }
     } else if (warp == kTicketWarp) {
         // ------------------------------------------------------ item numbers
-        // from the grid's counter, two ahead of the copies; before the first routed one,
-        // waits for the routing and lists the hit experts, while the copies of the items
-        // ahead of it go out.  A warp of its own: the counter answers after a microsecond,
-        // and whoever waits for it does nothing else (a warp's arrivals on barriers wait
-        // for its outstanding atomics too).
+        // from the grid's counter, one ahead of the copies (two ahead left the CTAs less
+        // even at the end: one token 58.0 us, 57.7 so).  A warp of its own: the counter
+        // answers after a microsecond, and whoever waits for it does nothing else (a
+        // warp's arrivals on barriers wait for its outstanding atomics too).
         int n_pass = -1;
         for (uint32_t n = 0;; ++n) {
-            if (!mbar_wait_warp(&qempty[n & 1], (n >> 1 & 1u) ^ 1u, wc) || *stop_s) break;
+            if (!mbar_wait_warp(qempty, (n & 1u) ^ 1u, wc) || *stop_s) break;
             int t = 0;
             if (lane == 0) t = atomicAdd(p.counters + 1, 1);
             t = __shfl_sync(0xffffffffu, t, 0);
-            if (t >= tiles1 && n_pass < 0) {
-                n_pass = S <= 32 ? few_list_short<NT>(p, S, meta, lane, wc)
-                                 : few_list<NT>(p, S, meta, lane, wc);
+            if (S > 32 && t >= tiles1 && n_pass < 0) {
+                n_pass = few_list<NT>(p, S, meta, lane, wc);
                 if (n_pass < 0) break;
                 if (lane == 0) meta->n_pass = n_pass;
             }
             if (lane == 0) {
-                queue[n & 1] = t;
-                mbar_arrive(&qfull[n & 1]);
+                *queue = t;
+                mbar_arrive(qfull);
             }
             __syncwarp();
         }
