@@ -43,12 +43,13 @@
 // slot order, so results do not depend on who finishes when.
 //
 // Measured (time of the call; of the copy bandwidth in brackets), d = 4096, I =
-// 2048, 384 experts, top 6: one token 61 us (86 %), 32 tokens 1.03-1.07 ms (7.2-7.4
-// TB/s of the 7.7 GB of weights they hit); FP8, one token 40.5 us (65 %), 16 tokens
-// 358-373 us (87-90 %).  23 tokens through a table of 97 experts, d = 1152, I = 704: 85
-// us (59 %).  A token's 40.5 us: its expert list is there after 9.3 us, of which the
-// shared W13 hides 5; from then on the stream runs at 5.6 TB/s, held back by the
-// time that a stage stays in the ring (2 us on its way, 1.5 until it is read).
+// 2048, 384 experts, top 6: one token 58 us (90 %), 32 tokens 1.03-1.07 ms (7.2-7.4
+// TB/s of the 7.7 GB of weights they hit); FP8, one token 37.7 us (70 %), 16 tokens
+// 357-376 us (86-90 %).  23 tokens through a table of 97 experts, d = 1152, I = 704: 83-86
+// us (58-60 %).  A token's 37.7 us: routed 5 us after the start, first routed copies
+// after 8, of which the shared W13 hides 4; then the stream runs at 5.5-6 TB/s, held
+// back by the copying warp (1.2 us an item of 64 KB) and by the time that a stage
+// stays in the ring (2 us on its way, 1.5 until it is read), and two dependences.
 #include <cfloat>
 #include <climits>
 
