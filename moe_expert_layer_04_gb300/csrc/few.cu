@@ -119,6 +119,20 @@ __device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// The warp's arrival on a barrier that lets others overwrite what it has loaded from
+// shared memory: after the loads have come back, not after they were issued.  `loaded`
+// depends on all of them (a load comes back for all lanes at once) and the address on
+// `loaded`; loads that queue behind stalled ones to global memory were seen to read
+// what came after them otherwise.
+__device__ __forceinline__ void arrive_after(uint64_t *bar, uint32_t loaded, uint32_t zero,
+                                             int lane) {
+    __syncwarp();
+    if (lane == 0)
+        asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar) +
+                                                                     (loaded & zero))
+                     : "memory");
+}
+
 // A stage's two boxes of eight rows and the bytes that `bar` is to count.  With an L2
 // policy: the weights pass through L2 once and must not push out what every call uses
 // again (the kernels' code, W_g, the token rows).  Called by a whole warp, which elects
@@ -685,6 +699,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_experts_kernel(
     __syncthreads();
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // a next call's first kernel
     const WaitCtl wc{abort_s, p.status, p.wait_limit};
+    const uint32_t zero = (uint32_t)p.hash >> 1;   // which the compiler does not know
     const int S = p.T * p.k;
     const int tiles1 = p.I / 8, tiles2 = p.d / 16;
     int *h_done = p.counters + 4;
@@ -895,10 +910,8 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_experts_kernel(
             const int left = min(cps, (K + SH::CHUNK_K - 1) / SH::CHUNK_K - c0) - w_at;
             const int n_ch = !mine || left <= 0 ? 0 : left > kGroupWarps ? 2 : 1;
             static_assert(kWarpChunks == 2, "chunks of a stage for one warp");
-            auto release = [&] {
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&empty[s]);
-            };
+            uint32_t loaded = 0;   // something of every load from the stage
+            auto release = [&] { arrive_after(&empty[s], loaded, zero, lane); };
             if (mine && !mbar_wait_warp(&full[s], ph, wc)) break;
             if (n_ch == 0) release();
 #pragma unroll
@@ -948,6 +961,10 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_experts_kernel(
                     f0 = scales[s * 2 * kStageChunks + cl];
                     f1 = scales[(s * 2 + 1) * kStageChunks + cl];
                 }
+                loaded ^= wq[0][0].x ^ wq[0][1].x ^ wq[1][0].x ^ wq[1][1].x;
+#pragma unroll
+                for (int i = 0; i < NV; ++i) loaded ^= v0[0][i].x ^ v0[1][i].x;
+                if constexpr (FP8) loaded ^= __float_as_uint(f0) ^ __float_as_uint(f1);
                 if (ch == n_ch - 1) release();
                 if constexpr (!FP8) {
 #pragma unroll
@@ -1086,8 +1103,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_experts_kernel(
                 v[2] += r.z;
                 v[3] += r.w;
             }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&rempty[buf]);
+            arrive_after(&rempty[buf], __float_as_uint(v[0]), zero, lane);
             const int n = q.z & 0xFFFF, row0 = q.z >> 16, grp = q.w & kChunkMask;
             const bool second = q.w & kSecond;
             // v[0], v[1]: weight row g, tokens 2c and 2c + 1; v[2], v[3]: row g + 8

@@ -208,3 +208,24 @@ def test_out_of_range_table_entry_is_recorded():
     a["tid2eid"][:, 1] = 0
     run(a)
     check(a)
+
+
+@pytest.mark.parametrize("T,d,E,k,I,fp8", [(14, 2048, 2, 1, 1024, False), (23, 1152, 33, 4, 704, False),
+                                           (14, 2048, 2, 1, 1024, True), (9, 640, 5, 2, 192, True)])
+def test_calls_back_to_back_on_one_workspace(T, d, E, k, I, fp8):
+    """Two inputs in turn, nothing waited for in between: every call gives what it
+    gives alone, bit for bit (a part of the ring rewritten before it is read, a sum
+    overtaken by the next or a row of the call before would show)."""
+    a = make(T, d, E, k, I, fp8)
+    b = dict(a, x=make(T, d, E, k, I, fp8, seed=1)["x"])
+    alone = []
+    for c in (a, b):
+        run(c)
+        alone.append(c["y"].clone())
+    wrong = []
+    for i in range(600):
+        w = (i * 7 // 3) % 2
+        _lib.moe_layer_few((a, b)[w])
+        wrong.append((a["y"] != alone[w]).any())
+    assert _lib.moe_last_device_status() == _lib.MOE_OK
+    assert not torch.stack(wrong).any()
