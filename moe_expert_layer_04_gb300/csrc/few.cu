@@ -910,10 +910,9 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_experts_kernel(
             const int left = min(cps, (K + SH::CHUNK_K - 1) / SH::CHUNK_K - c0) - w_at;
             const int n_ch = !mine || left <= 0 ? 0 : left > kGroupWarps ? 2 : 1;
             static_assert(kWarpChunks == 2, "chunks of a stage for one warp");
-            uint32_t loaded = 0;   // something of every load from the stage
-            auto release = [&] { arrive_after(&empty[s], loaded, zero, lane); };
+            auto release = [&](uint32_t loaded) { arrive_after(&empty[s], loaded, zero, lane); };
             if (mine && !mbar_wait_warp(&full[s], ph, wc)) break;
-            if (n_ch == 0) release();
+            if (n_ch == 0) release(0);
 #pragma unroll
             for (int ch = 0; ch < kWarpChunks; ++ch) {
                 const int cl = w_at + kGroupWarps * ch;   // in the stage
@@ -961,11 +960,17 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_experts_kernel(
                     f0 = scales[s * 2 * kStageChunks + cl];
                     f1 = scales[(s * 2 + 1) * kStageChunks + cl];
                 }
-                loaded ^= wq[0][0].x ^ wq[0][1].x ^ wq[1][0].x ^ wq[1][1].x;
+                if (ch == n_ch - 1) {
+                    // something of every load from the stage: of this chunk's, and what
+                    // became of the one before
+                    uint32_t loaded = wq[0][0].x ^ wq[0][1].x ^ wq[1][0].x ^ wq[1][1].x;
 #pragma unroll
-                for (int i = 0; i < NV; ++i) loaded ^= v0[0][i].x ^ v0[1][i].x;
-                if constexpr (FP8) loaded ^= __float_as_uint(f0) ^ __float_as_uint(f1);
-                if (ch == n_ch - 1) release();
+                    for (int i = 0; i < NV; ++i) loaded ^= v0[0][i].x ^ v0[1][i].x;
+                    if constexpr (FP8) loaded ^= __float_as_uint(f0) ^ __float_as_uint(f1);
+                    if (ch > 0)
+                        loaded ^= __float_as_uint(acc[0][0]) ^ __float_as_uint(acc[0][2]);
+                    release(loaded);
+                }
                 if constexpr (!FP8) {
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
