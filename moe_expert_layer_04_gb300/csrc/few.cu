@@ -45,7 +45,7 @@
 // Measured (time of the call; of the copy bandwidth in brackets), d = 4096, I =
 // 2048, 384 experts, top 6: one token 58 us (90 %), 32 tokens 1.03-1.07 ms (7.2-7.4
 // TB/s of the 7.7 GB of weights they hit); FP8, one token 37.7 us (70 %), 16 tokens
-// 357-376 us (86-90 %).  23 tokens through a table of 97 experts, d = 1152, I = 704: 83-86
+// 357-380 us (85-90 %).  23 tokens through a table of 97 experts, d = 1152, I = 704: 83-86
 // us (58-60 %).  A token's 37.7 us: routed 5 us after the start, first routed copies
 // after 8, of which the shared W13 hides 4; then the stream runs at 5.5-6 TB/s, held
 // back by the copying warp (1.2 us an item of 64 KB) and by the time that a stage

@@ -33,7 +33,7 @@
 // twice (2048 cycles) while the next tile's first products do (1536).
 //
 // Measured (time of the call): 12345 rows in 33 uneven groups, 4096 x 2048 weights: 114-118
-// us, 1.8 PFLOP/s; expert FFN of 32768 rows over 33 groups, d = 4096, I = 2048: 794-818 us,
+// us, 1.8 PFLOP/s; expert FFN of 32768 rows over 33 groups, d = 4096, I = 2048: 794-823 us,
 // 2.0-2.1 PFLOP/s; of 777 rows over 9: 63 us, where the weights alone are 30 us of HBM
 // (176 tiles on 152 SMs); weight gradient 4096 x 4096 of 6789 rows in 9 groups: 234 us
 // with the quantisation of both operands (39 us), 604 MB of output.
