@@ -1160,9 +1160,15 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_experts_kernel(
         }
     }
 
-    // the last CTA to leave puts every counter and slot back to zero
+    // The first kernel stores ids and weights after the slots that say they are there.
+    // It has long ended, but only this wait makes its end, and those stores, come before
+    // the end of this kernel, which is what whoever runs next on the stream waits for.
+    // The last CTA to leave puts every counter and slot back to zero.
     __syncthreads();
-    if (threadIdx.x == 0) *last_s = atom_add_acq_rel(p.counters + 2, 1) == (int)gridDim.x - 1;
+    if (threadIdx.x == 0) {
+        wait_for_kernels_ahead();
+        *last_s = atom_add_acq_rel(p.counters + 2, 1) == (int)gridDim.x - 1;
+    }
     __syncthreads();
     if (*last_s) {
         for (int i = threadIdx.x; i < p.n_counters; i += kFewThreads) p.counters[i] = 0;

@@ -94,7 +94,10 @@ __device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t b
 
 // A launch that may begin before the kernel ahead of it in the stream ends
 // (programmatic dependent launch), which hides its latency; such a kernel touches
-// nothing in memory before wait_for_kernels_ahead().
+// nothing in memory before wait_for_kernels_ahead().  (few_experts_kernel alone works
+// beside the kernel ahead, its own gate, through signals in the workspace, and waits for
+// its end before it ends itself: every kernel launched so must, as the one behind it
+// waits for no other.)
 template <typename... P, typename... A>
 inline moe_status launch_early(void (*kern)(P...), dim3 grid, int threads, int smem,
                                cudaStream_t st, A... args) {
