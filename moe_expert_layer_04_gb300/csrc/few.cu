@@ -811,11 +811,12 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_experts_kernel(
                 } else if (!have_x) {
                     ready = wait_count_geq(p.counters + 3, p.T, wc);
                 }
-                fence_proxy_async_global();   // the copies read what others stored
             }
             have_x = have_x || !second;
             if (!__shfl_sync(0xffffffffu, ready, 0)) break;
             __syncwarp();
+            // the copies read what others stored: every lane that issues one needs it
+            fence_proxy_async_global();
             const int K = second ? p.I : p.d;
             const int k0 = c0 * SH::CHUNK_K;
             const int cps = second ? p.cps2 : p.cps13;
@@ -1132,11 +1133,9 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_experts_kernel(
                             : (uint16_t)(pack_bf16x2(h, 0.0f) & 0xFFFFu);
                 }
             }
+            fence_proxy_async_global();   // copies will read h
             __syncwarp();
-            if (lane == 0) {
-                fence_proxy_async_global();   // copies will read h
-                red_release_gpu_add(second ? y_done + q.x : h_done + 1 + q.y, 1);
-            }
+            if (lane == 0) red_release_gpu_add(second ? y_done + q.x : h_done + 1 + q.y, 1);
         }
     }
 

@@ -45,6 +45,57 @@ def test_who_lets_the_kernel_behind_begin_waits_for_the_one_ahead():
     assert not missing
 
 
+def blocks_around(body, at):
+    """Opening braces of the blocks around place `at`."""
+    stack = []
+    for i, c in enumerate(body[:at]):
+        if c == "{":
+            stack.append(i)
+        elif c == "}":
+            stack.pop()
+    return stack
+
+
+def test_who_issues_a_bulk_copy_of_others_stores_has_the_proxy_fence():
+    """The fence between generic stores and asynchronous copies works for the
+    thread that executes it: it stands in a block around the copy, not in a branch
+    that other lanes than the copying ones take."""
+    body = next(b for _, n, b in kernels() if n == "few_experts_kernel")
+    copies = [m.start() for m in re.finditer(r"\bbulk_load\(", body)]
+    assert copies
+    for at in copies:
+        around = set(blocks_around(body, at))
+        fences = [m.start() for m in re.finditer(r"fence_proxy_async_global\(", body[:at])]
+        assert any(set(blocks_around(body, f)) <= around for f in fences)
+    # and the lanes that store what is copied
+    at = body.index("p.h[")
+    after = body.index("fence_proxy_async_global(", at)
+    assert set(blocks_around(body, after)) <= set(blocks_around(body, at))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,E,k,fp8", [(1, 6, 2, False), (4, 64, 6, False), (2, 96, 8, True), (1, 4, 4, True)])
+def test_rows_that_lanes_copy_are_the_ones_stored(T, E, k, fp8):
+    """Passes of few rows, whose h each lane copies to shared memory for itself:
+    two inputs in turn on one workspace, every call as it is alone."""
+    from moe_expert_layer_04_gb300 import _lib
+    from tests.test_gpu_few import check, make, run
+    a = make(T, 256, E, k, 576, fp8)
+    b = dict(a, x=make(T, 256, E, k, 576, fp8, seed=1)["x"])
+    alone = []
+    for c in (a, b):
+        run(c)
+        check(c)
+        alone.append(c["y"].clone())
+    wrong = []
+    for i in range(300):
+        w = (i * 7 // 3) % 2
+        _lib.moe_layer_few((a, b)[w])
+        wrong.append((a["y"] != alone[w]).any())
+    assert _lib.moe_last_device_status() == _lib.MOE_OK
+    assert not torch.stack(wrong).any()
+
+
 @pytest.mark.gpu
 def test_early_kernel_behind_the_few_token_layer_reads_its_weights():
     """A matmul launched early behind the call takes the call's routing weights
