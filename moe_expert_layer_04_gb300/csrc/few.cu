@@ -121,15 +121,15 @@ __device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1
 
 // The warp's arrival on a barrier that lets others overwrite what it has loaded from
 // shared memory: after the loads have come back, not after they were issued.  `loaded`
-// depends on all of them (a load comes back for all lanes at once) and the address on
-// `loaded`; loads that queue behind stalled ones to global memory were seen to read
-// what came after them otherwise.
+// depends on all of this lane's, the vote on every lane's `loaded`, and the address on
+// the vote (which is 0, as `zero` is); loads that queue behind stalled ones to global
+// memory were seen to read what came after them otherwise.
 __device__ __forceinline__ void arrive_after(uint64_t *bar, uint32_t loaded, uint32_t zero,
                                              int lane) {
+    const uint32_t none = __any_sync(0xffffffffu, (loaded & zero) != 0);
     __syncwarp();
     if (lane == 0)
-        asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar) +
-                                                                     (loaded & zero))
+        asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar) + none)
                      : "memory");
 }
 

@@ -73,6 +73,17 @@ def test_who_issues_a_bulk_copy_of_others_stores_has_the_proxy_fence():
     assert set(blocks_around(body, after)) <= set(blocks_around(body, at))
 
 
+def test_the_arrival_that_frees_shared_memory_takes_every_lanes_loads():
+    """One lane arrives for the warp: what it arrives with depends on the values
+    that all lanes have loaded (a vote), not on its own alone."""
+    text = open(os.path.join(CSRC, "few.cu")).read()
+    at = text.index("void arrive_after(")
+    body = text[at:text.index("\n}\n", at)]
+    voted = re.search(r"(\w+) = __any_sync\(0xffffffffu, \(loaded & zero\) != 0\)", body)
+    assert voted
+    assert re.search(r"smem_u32\(bar\) \+ " + voted.group(1), re.sub(r"\s+", " ", body))
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("T,E,k,fp8", [(1, 6, 2, False), (4, 64, 6, False), (2, 96, 8, True), (1, 4, 4, True)])
 def test_rows_that_lanes_copy_are_the_ones_stored(T, E, k, fp8):
