@@ -716,12 +716,13 @@ moe_status moe_expert_ffn_fp8(const uint8_t *x_perm_q, const float *x_perm_s,
  * The whole forward of one layer for 1 <= T <= 32 tokens in two launches, for
  * decoding: gate and routing as moe_gate_route, then every hit expert's and the
  * shared expert's weights read once while the tokens' rows go through them,
- *   h[t,j] = silu(min(g, clamp)) clamp(u, -clamp, clamp), rounded to bf16
+ *   h[t,j] = silu(min(g, clamp)) clamp(u, -clamp, clamp)
  *   y[t]   = bf16( h_shared W2[E]^T + sum_j weights[t,j] (h[t,j] W2[e_j]^T) )
  * with fp32 sums throughout.  The expert weights are bf16 (W13 [E+1, 2I, d] and
  * W2 [E+1, d, I]) or FP8 in 128 x 128 blocks (W13_q, W13_s, W2_q, W2_s); the
- * other set is NULL.  Tokens are not quantised in either.  With FP8 weights h is
- * f16 instead of bf16, times a power of two that keeps clamp^2 inside f16's
+ * other set is NULL.  Tokens are not quantised in either.  With bf16 weights h is
+ * the sum of two bf16 terms (2^-16 of itself); with FP8 weights it is
+ * f16, times a power of two that keeps clamp^2 inside f16's
  * range: for clamp > 255 an |h| above 65504 becomes infinite.  Supported: d % 128 == 0,
  * I % 64 == 0, k <= min(8, E), E <= 1024.
  * Workspace: moe_few_workspace_size bytes (0: not supported), ZERO before its

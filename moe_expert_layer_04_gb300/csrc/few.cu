@@ -3,7 +3,7 @@
 // in two launches.
 //
 //   logits = x W_g^T (+ offset);  ids, w = top-k or table routing
-//   h[r] = bf16( silu(min(g, c)) clamp(u, -c, c) ),  [g|u] = x[t] W13[e]^T
+//   h[r] = silu(min(g, c)) clamp(u, -c, c),  [g|u] = x[t] W13[e]^T
 //   y[t] = bf16( h_shared W2[E]^T + sum_j w[t,j] (h[t,j] W2[e_j]^T) )
 // ("HyperParallel加速DeepSeek-V4.1多模态1M长序列训练" §2.3 MegaGate and MegaMoE,
 // "MindSpore HyperParallel一键开箱DeepSeek-V4.1-Flash" §01 shared expert, at the
@@ -36,9 +36,14 @@
 // tiles of tcgen05 would only add padding); their partial sums meet in shared
 // memory in a fixed order.  FP8 weights are expanded to f16 in registers, exactly,
 // and each 128-block's sum takes its scale in fp32; the tokens are then f16 as
-// well, each scaled by a power of two (a few CTAs of the first kernel).  h is
-// rounded to 16 bits (the second matmul's operand: bf16, or with FP8 weights f16),
-// every other sum stays fp32 up to y.  Products of the second matmul go to fp32
+// well, each scaled by a power of two (a few CTAs of the first kernel).  The second
+// matmul's operand h is f16 with FP8 weights (2^-11 of itself), and with bf16 weights
+// the sum of two bf16 terms (2^-16; one term, 2^-8, makes the error of y 1.4 times what
+// its own rounding to bf16 leaves).  The terms of up to four rows lie side by side in the
+// MMA's eight columns; for more rows the second one is another MMA for the same weights,
+// in a loop of its own (inside the first one it cost registers: 32 tokens 1.05 -> 1.16
+// ms, so 1.08).  One term measured 58.4 us (so 58.7) for one token, 88 (91) for 23.
+// Every sum stays fp32 up to y.  Products of the second matmul go to fp32
 // rows per (token, slot); at the end each CTA adds up its share of the columns in
 // slot order, so results do not depend on who finishes when.
 //
@@ -101,7 +106,7 @@ struct FewParams {
     int h_exp;       // FP8 weights: h is f16, times 2^h_exp
     uint64_t *routed;   // [T, k] (expert + 1) << 32 | its weight's bits; zero between calls, so
                         // that a slot's word is its own signal
-    uint16_t *h;     // [S + T, I] bf16, or f16 (FP8 weights)
+    uint16_t *h;     // FP8 weights: [S + T, I] f16; else [S + T, 2, I], bf16 terms of h
     float *yp;       // [S + T, d]
     int splits;
     int cps13, cps2;   // chunks of a row in a stage
@@ -497,6 +502,7 @@ struct FewShape {
     // rows of a quarter warp's loads meet in no bank; passes of more rows are
     // read from global memory
     static constexpr int ACT_ROWS = FP8 ? 2 : 4;
+    static constexpr int TERMS = FP8 ? 1 : 2;          // of h
     static constexpr int ACT_PITCH = 2 * CHUNK_K * kStageChunks + (FP8 ? 16 : 64);
     static constexpr int ACT = ACT_ROWS * ACT_PITCH;
     static constexpr int RED = kSumWarps * kMulWarps * 128 * 4;
@@ -821,17 +827,20 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_experts_kernel(
             const int k0 = c0 * SH::CHUNK_K;
             const int cps = second ? p.cps2 : p.cps13;
             const int bytes = 2 * min(cps * SH::CHUNK_K, K - k0);   // none behind the end
-            const bool copy = n <= SH::ACT_ROWS && bytes > 0;
+            const bool terms = SH::TERMS == 2 && second;   // h: row by row, its two terms
+            const int copies = terms ? 2 * n : n;
+            const bool copy = copies <= SH::ACT_ROWS && bytes > 0;
             if (lane == 0) {
-                if (copy) mbar_arrive_expect_tx(&full[s], n * bytes);
+                if (copy) mbar_arrive_expect_tx(&full[s], copies * bytes);
                 else mbar_arrive(&full[s]);
             }
             __syncwarp();
-            if (copy && lane < n) {
-                const int row = q.y < 0    ? (second ? S + lane : lane)
-                                : second ? meta->slot[row0 + lane]
-                                         : meta->token[row0 + lane];
-                const uint16_t *src = second ? p.h + (size_t)row * p.I
+            if (copy && lane < copies) {
+                const int r = terms ? lane >> 1 : lane, term = terms ? lane & 1 : 0;
+                const int row = q.y < 0    ? (second ? S + r : r)
+                                : second ? meta->slot[row0 + r]
+                                         : meta->token[row0 + r];
+                const uint16_t *src = second ? p.h + ((size_t)row * SH::TERMS + term) * p.I
                                              : (FP8 ? p.x16 : p.x) + (size_t)row * p.d;
                 bulk_load(acts + s * SH::ACT + lane * SH::ACT_PITCH, src + k0, bytes, &full[s]);
             }
@@ -880,7 +889,11 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_experts_kernel(
             const bool second = q.w & kSecond;
             const int K = second ? p.I : p.d;
             const int nt = NT == 1 ? 1 : (n + 7) >> 3;
-            const bool in_smem = n <= SH::ACT_ROWS;
+            const bool terms = SH::TERMS == 2 && second;
+            const bool in_smem = (terms ? 2 * n : n) <= SH::ACT_ROWS;
+            // a row's two terms of h in columns side by side
+            const bool beside = terms && n <= 4;
+            const int col = beside ? g >> 1 : g, term = beside ? g & 1 : 0;   // row, term
             const bool mine = (turn & (kGroups - 1)) == (uint32_t)group;
             if (c0 == 0) role = mine ? 0 : 1;
             if (!p.by_tile || (q.w & kLast)) ++turn;
@@ -889,13 +902,13 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_experts_kernel(
                 for (int j = 0; j < NT; ++j) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i) acc[j][i] = 0.0f;
-                    const int i = j * 8 + g;
+                    const int i = j * 8 + col;
                     act[j] = nullptr;
                     if (!in_smem && i < n) {
                         const int row = q.y < 0    ? (second ? S + i : i)
                                         : second ? meta->slot[row0 + i]
                                                  : meta->token[row0 + i];
-                        act[j] = second ? p.h + (size_t)row * p.I
+                        act[j] = second ? p.h + ((size_t)row * SH::TERMS + term) * p.I
                                         : (FP8 ? p.x16 : p.x) + (size_t)row * p.d;
                     }
                 }
@@ -919,14 +932,14 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_experts_kernel(
                 const int cl = w_at + kGroupWarps * ch;   // in the stage
                 const int chunk = c0 + cl;              // in the row
                 if (ch >= n_ch) break;
-                // token operand of the chunk's half h, group j
-                auto load_act = [&](int h, int j, uint4 (&v)[NV]) {
+                // token operand of the chunk's half h, group j (`at` elements further on)
+                auto load_act = [&](int h, int j, uint4 (&v)[NV], int at = 0) {
                     const int kk = (2 * chunk + h) * (SH::CHUNK_K / 2) + c * (SH::CHUNK_K / 8);
 #pragma unroll
                     for (int i = 0; i < NV; ++i) {
                         v[i] = make_uint4(0, 0, 0, 0);
                         if (act[j] && kk < K)
-                            v[i] = __ldcg(reinterpret_cast<const uint4 *>(act[j] + kk) + i);
+                            v[i] = __ldcg(reinterpret_cast<const uint4 *>(act[j] + at + kk) + i);
                     }
                 };
                 uint4 v0[2][NV];   // group 0
@@ -937,8 +950,8 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_experts_kernel(
                     for (int h = 0; h < 2; ++h)
 #pragma unroll
                         for (int i = 0; i < NV; ++i)
-                            v0[h][i] = g < n ? ld_shared_v4(a + h * SH::CHUNK_K + 16 * i)
-                                             : make_uint4(0, 0, 0, 0);
+                            v0[h][i] = col < n ? ld_shared_v4(a + h * SH::CHUNK_K + 16 * i)
+                                               : make_uint4(0, 0, 0, 0);
                 } else {
                     load_act(0, 0, v0[0]);
                     load_act(1, 0, v0[1]);
@@ -984,6 +997,20 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_experts_kernel(
                             const uint4 b = j > 0 ? v[0] : v0[h][0];
                             mma_bf16(acc[j], wa.x, wb.x, wa.y, wb.y, b.x, b.y);
                             mma_bf16(acc[j], wa.z, wb.z, wa.w, wb.w, b.z, b.w);
+                        }
+                    }
+                    if (terms && !beside) {   // the second terms of h
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const uint4 wa = wq[h][0], wb = wq[h][1];
+#pragma unroll
+                            for (int j = 0; j < NT; ++j) {
+                                if (j >= nt) break;
+                                uint4 v[NV];
+                                load_act(h, j, v, p.I);
+                                mma_bf16(acc[j], wa.x, wb.x, wa.y, wb.y, v[0].x, v[0].y);
+                                mma_bf16(acc[j], wa.z, wb.z, wa.w, wb.w, v[0].z, v[0].w);
+                            }
                         }
                     }
                 } else {
@@ -1113,10 +1140,16 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_experts_kernel(
             const int n = q.z & 0xFFFF, row0 = q.z >> 16, grp = q.w & kChunkMask;
             const bool second = q.w & kSecond;
             // v[0], v[1]: weight row g, tokens 2c and 2c + 1; v[2], v[3]: row g + 8
+            // (or token c's two terms of h)
+            const bool beside = SH::TERMS == 2 && second && n <= 4;
+            if (beside) {
+                v[0] += v[1];
+                v[2] += v[3];
+            }
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                const int r = grp * 8 + 2 * c + i;
-                if (r >= n) continue;
+                const int r = beside ? c : grp * 8 + 2 * c + i;
+                if (r >= n || (beside && i > 0)) continue;
                 const int slot = q.y < 0 ? S + r : meta->slot[row0 + r];
                 if (second) {
                     const float w = (q.y < 0 ? 1.0f : meta->w[slot]) *
@@ -1128,9 +1161,16 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_experts_kernel(
                     float up = 1.0f;
                     if constexpr (FP8) up = __ldcg(p.x16_s + (q.y < 0 ? r : meta->token[row0 + r]));
                     const float h = swiglu_clamped_nan(v[i] * up, v[2 + i] * up, p.clamp);
-                    p.h[(size_t)slot * p.I + q.x * 8 + g] =
-                        FP8 ? __half_as_ushort(__float2half_rn(h * exp2i(p.h_exp)))
-                            : (uint16_t)(pack_bf16x2(h, 0.0f) & 0xFFFFu);
+                    const size_t o = (size_t)slot * SH::TERMS * p.I + q.x * 8 + g;
+                    if constexpr (FP8) {
+                        p.h[o] = __half_as_ushort(__float2half_rn(h * exp2i(p.h_exp)));
+                    } else {
+                        const uint32_t top = pack_bf16x2(h, 0.0f) & 0xFFFFu;
+                        const float rest = h - bf16_lo(top);   // exact, or not finite
+                        p.h[o] = (uint16_t)top;
+                        p.h[o + p.I] =
+                            isfinite(rest) ? (uint16_t)(pack_bf16x2(rest, 0.0f) & 0xFFFFu) : 0;
+                    }
                 }
             }
             fence_proxy_async_global();   // copies will read h
@@ -1204,7 +1244,7 @@ FewWorkspace carve_few(uint8_t *base, int T, int d, int E, int k, int I) {
     w.x16 = reinterpret_cast<uint16_t *>(take((size_t)T * d * 2));
     w.x16_s = reinterpret_cast<float *>(take((size_t)T * 4));
     w.routed = reinterpret_cast<uint64_t *>(take(S * 8));
-    w.h = reinterpret_cast<uint16_t *>(take((S + T) * I * 2));
+    w.h = reinterpret_cast<uint16_t *>(take((S + T) * I * 4));   // two terms, with bf16 weights
     w.yp = reinterpret_cast<float *>(take((S + T) * d * 4));
     w.bytes = off;
     return w;
