@@ -721,10 +721,10 @@ moe_status moe_expert_ffn_fp8(const uint8_t *x_perm_q, const float *x_perm_s,
  * with fp32 sums throughout.  The expert weights are bf16 (W13 [E+1, 2I, d] and
  * W2 [E+1, d, I]) or FP8 in 128 x 128 blocks (W13_q, W13_s, W2_q, W2_s); the
  * other set is NULL.  Tokens are not quantised in either.  With bf16 weights h is
- * the sum of two bf16 terms (2^-16 of itself); with FP8 weights it is
- * f16, times a power of two that keeps clamp^2 inside f16's
- * range: for clamp > 255 an |h| above 65504 becomes infinite.  Supported: d % 128 == 0,
- * I % 64 == 0, k <= min(8, E), E <= 1024.
+ * the sum of two bf16 terms (2^-16 of itself); with FP8 weights it is f16, times a
+ * power of two that keeps clamp^2 inside f16's range (2^-11 of itself), and two bf16
+ * terms where none does (clamp > 255.9).
+ * Supported: d % 128 == 0, I % 64 == 0, k <= min(8, E), E <= 1024.
  * Workspace: moe_few_workspace_size bytes (0: not supported), ZERO before its
  * first use; every call leaves its counters zero again, so a buffer is zeroed
  * once and then kept for calls of the same sizes (other sizes, or a call that

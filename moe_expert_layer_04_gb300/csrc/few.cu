@@ -37,8 +37,8 @@
 // memory in a fixed order.  FP8 weights are expanded to f16 in registers, exactly,
 // and each 128-block's sum takes its scale in fp32; the tokens are then f16 as
 // well, each scaled by a power of two (a few CTAs of the first kernel).  The second
-// matmul's operand h is f16 with FP8 weights (2^-11 of itself), and with bf16 weights
-// the sum of two bf16 terms (2^-16; one term, 2^-8, makes the error of y 1.4 times what
+// matmul's operand h is f16 with FP8 weights (2^-11 of itself; for a clamp whose square
+// f16 does not hold, as with bf16 weights), and with bf16 weights the sum of two bf16 terms (2^-16; one term, 2^-8, makes the error of y 1.4 times what
 // its own rounding to bf16 leaves).  The terms of up to four rows lie side by side in the
 // MMA's eight columns; for more rows the second one is another MMA for the same weights,
 // in a loop of its own (inside the first one it cost registers: 32 tokens 1.05 -> 1.16
@@ -103,10 +103,11 @@ struct FewParams {
     float *part;     // [splits, T, E] partial logits
     uint16_t *x16;   // FP8 weights: [T, d] f16 tokens, each scaled by a power of two ...
     float *x16_s;    // ... whose inverse this is [T]
-    int h_exp;       // FP8 weights: h is f16, times 2^h_exp
+    int h_exp;       // where h is f16, it is times 2^h_exp
     uint64_t *routed;   // [T, k] (expert + 1) << 32 | its weight's bits; zero between calls, so
                         // that a slot's word is its own signal
-    uint16_t *h;     // FP8 weights: [S + T, I] f16; else [S + T, 2, I], bf16 terms of h
+    uint16_t *h;     // FP8 weights, clamp^2 inside f16: [S + T, I] f16; else [S + T, 2, I],
+                     // bf16 terms of h
     float *yp;       // [S + T, d]
     int splits;
     int cps13, cps2;   // chunks of a row in a stage
@@ -493,7 +494,8 @@ struct FewItem {
     int tile;
 };
 
-template <bool FP8, int NT>
+// WIDE: FP8 weights and a clamp whose square f16 does not hold
+template <bool FP8, int NT, bool WIDE>
 struct FewShape {
     static constexpr int STAGES = 5;
     static constexpr int ELT = FP8 ? 1 : 2;
@@ -502,7 +504,7 @@ struct FewShape {
     // rows of a quarter warp's loads meet in no bank; passes of more rows are
     // read from global memory
     static constexpr int ACT_ROWS = FP8 ? 2 : 4;
-    static constexpr int TERMS = FP8 ? 1 : 2;          // of h
+    static constexpr int TERMS = FP8 && !WIDE ? 1 : 2;   // of h
     static constexpr int ACT_PITCH = 2 * CHUNK_K * kStageChunks + (FP8 ? 16 : 64);
     static constexpr int ACT = ACT_ROWS * ACT_PITCH;
     static constexpr int RED = kSumWarps * kMulWarps * 128 * 4;
@@ -653,10 +655,10 @@ __device__ __noinline__ int few_list(const FewParams &p, int S, FewMeta *meta, i
     return sum & 1023;
 }
 
-template <bool FP8, int NT>
+template <bool FP8, int NT, bool WIDE>
 __global__ void __launch_bounds__(kFewThreads, 1) few_experts_kernel(
     const __grid_constant__ FewParams p) {
-    using SH = FewShape<FP8, NT>;
+    using SH = FewShape<FP8, NT, WIDE>;
     constexpr int STAGES = SH::STAGES;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *ring = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -1045,6 +1047,12 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_experts_kernel(
                         for (int m = 0; m < 4; ++m) {
                             e4m3x4_f16(qa[m], x0[m], x1[m]);
                             e4m3x4_f16(qb[m], y0[m], y1[m]);
+                            if (WIDE && second) {   // h is bf16: so are they, exactly
+                                x0[m] = f16x2_bf16x2(x0[m]);
+                                x1[m] = f16x2_bf16x2(x1[m]);
+                                y0[m] = f16x2_bf16x2(y0[m]);
+                                y1[m] = f16x2_bf16x2(y1[m]);
+                            }
                         }
 #pragma unroll
                         for (int j = 0; j < NT; ++j) {
@@ -1056,9 +1064,24 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_experts_kernel(
                                                     b[NV - 1].x, b[NV - 1].y, b[NV - 1].z,
                                                     b[NV - 1].w};
 #pragma unroll
-                            for (int m = 0; m < 4; ++m)
-                                mma_f16(part[j][m & 1], x0[m], y0[m], x1[m], y1[m], bv[2 * m],
-                                        bv[2 * m + 1]);
+                            for (int m = 0; m < 4; ++m) {
+                                if (WIDE && second)
+                                    mma_bf16(part[j][m & 1], x0[m], y0[m], x1[m], y1[m], bv[2 * m],
+                                             bv[2 * m + 1]);
+                                else
+                                    mma_f16(part[j][m & 1], x0[m], y0[m], x1[m], y1[m], bv[2 * m],
+                                            bv[2 * m + 1]);
+                            }
+                            if (WIDE && terms && !beside) {   // the second terms of h
+                                load_act(h, j, v, p.I);
+                                const uint32_t lo[8] = {v[0].x, v[0].y, v[0].z, v[0].w,
+                                                        v[NV - 1].x, v[NV - 1].y, v[NV - 1].z,
+                                                        v[NV - 1].w};
+#pragma unroll
+                                for (int m = 0; m < 4; ++m)
+                                    mma_bf16(part[j][m & 1], x0[m], y0[m], x1[m], y1[m], lo[2 * m],
+                                             lo[2 * m + 1]);
+                            }
                         }
                     }
 #pragma unroll
@@ -1162,7 +1185,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_experts_kernel(
                     if constexpr (FP8) up = __ldcg(p.x16_s + (q.y < 0 ? r : meta->token[row0 + r]));
                     const float h = swiglu_clamped_nan(v[i] * up, v[2 + i] * up, p.clamp);
                     const size_t o = (size_t)slot * SH::TERMS * p.I + q.x * 8 + g;
-                    if constexpr (FP8) {
+                    if constexpr (SH::TERMS == 1) {
                         p.h[o] = __half_as_ushort(__float2half_rn(h * exp2i(p.h_exp)));
                     } else {
                         const uint32_t top = pack_bf16x2(h, 0.0f) & 0xFFFFu;
@@ -1244,16 +1267,16 @@ FewWorkspace carve_few(uint8_t *base, int T, int d, int E, int k, int I) {
     w.x16 = reinterpret_cast<uint16_t *>(take((size_t)T * d * 2));
     w.x16_s = reinterpret_cast<float *>(take((size_t)T * 4));
     w.routed = reinterpret_cast<uint64_t *>(take(S * 8));
-    w.h = reinterpret_cast<uint16_t *>(take((S + T) * I * 4));   // two terms, with bf16 weights
+    w.h = reinterpret_cast<uint16_t *>(take((S + T) * I * 4));   // of two terms, or half of it
     w.yp = reinterpret_cast<float *>(take((S + T) * d * 4));
     w.bytes = off;
     return w;
 }
 
-template <bool FP8, int NT>
+template <bool FP8, int NT, bool WIDE>
 moe_status launch_experts(const FewParams &p, cudaStream_t st) {
-    using SH = FewShape<FP8, NT>;
-    auto kern = few_experts_kernel<FP8, NT>;
+    using SH = FewShape<FP8, NT, WIDE>;
+    auto kern = few_experts_kernel<FP8, NT, WIDE>;
     static bool attr_set[64] = {};
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return MOE_ERR_CUDA;
@@ -1269,13 +1292,13 @@ moe_status launch_experts(const FewParams &p, cudaStream_t st) {
                         SH::SMEM, st, p);
 }
 
-template <bool FP8>
+template <bool FP8, bool WIDE>
 moe_status launch_experts_nt(const FewParams &p, cudaStream_t st) {
     // rows of an expert that share one read of its weights: as many groups of
     // 8 as there can be tokens
-    if (p.T <= 8) return launch_experts<FP8, 1>(p, st);
-    if (p.T <= 16) return launch_experts<FP8, 2>(p, st);
-    return launch_experts<FP8, 4>(p, st);
+    if (p.T <= 8) return launch_experts<FP8, 1, WIDE>(p, st);
+    if (p.T <= 16) return launch_experts<FP8, 2, WIDE>(p, st);
+    return launch_experts<FP8, 4, WIDE>(p, st);
 }
 
 }  // namespace
@@ -1353,7 +1376,10 @@ moe_status launch_few(const moe_few_args *a, cudaStream_t st) {
     splits = splits < 1 ? 1 : splits > kGateSplits ? kGateSplits : splits;
     if (splits > p.d / 32) splits = p.d / 32;
     p.splits = splits;
-    // |h| <= clamp^2: the power of two that keeps it inside f16
+    // |h| <= clamp^2: the power of two that keeps it inside f16.  Where none does, h is
+    // two bf16 terms as with bf16 weights, and the codes become bf16 too (through fp32:
+    // eight more instructions for eight of them).
+    const bool wide = !(p.clamp * p.clamp <= 65504.0f);
     p.h_exp = 0;
     while (p.h_exp < 24 && p.clamp * p.clamp * (float)(2 << p.h_exp) <= 65504.0f) ++p.h_exp;
     const dim3 grid(et, splits + (fp8 ? (p.T + et - 1) / et : 0));
@@ -1363,7 +1389,9 @@ moe_status launch_few(const moe_few_args *a, cudaStream_t st) {
                                   : few_gate_kernel<32>,
                      grid, kGateWarps * 32, 0, st, p);
     if (s != MOE_OK) return s;
-    return fp8 ? launch_experts_nt<true>(p, st) : launch_experts_nt<false>(p, st);
+    return !fp8   ? launch_experts_nt<false, false>(p, st)
+           : wide ? launch_experts_nt<true, true>(p, st)
+                  : launch_experts_nt<true, false>(p, st);
 }
 
 }  // namespace moe

@@ -72,6 +72,12 @@ __device__ __forceinline__ void e4m3x4_f16(uint32_t w, uint32_t &lo, uint32_t &h
     asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(hi) : "h"((uint16_t)(w >> 16)));
 }
 
+// Two f16 that bf16 holds (E4M3 values) -> bf16, exact.
+__device__ __forceinline__ uint32_t f16x2_bf16x2(uint32_t w) {
+    const float2 v = __half22float2(*reinterpret_cast<const __half2 *>(&w));
+    return pack_bf16x2(v.x, v.y);
+}
+
 __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                         uint32_t a3, uint32_t b0, uint32_t b1) {
     asm volatile(

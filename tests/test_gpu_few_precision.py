@@ -48,3 +48,27 @@ def test_infinite_h_stays_infinite(T):
     a["W2"].fill_(1.0)
     run(a)
     assert torch.isinf(a["y"][:T].float()).all() and (a["y"][:T] > 0).all()
+
+
+@pytest.mark.parametrize("T,d,E,k,I,clamp", [(1, 256, 8, 2, 128, 256.5), (3, 256, 2, 1, 192, 1.0e4),
+                                             (2, 128, 1, 1, 64, float("inf")), (7, 384, 3, 2, 320, 1.0e4),
+                                             (8, 2048, 40, 6, 704, float("inf")), (13, 640, 5, 2, 448, 1.0e4),
+                                             (32, 256, 4, 4, 128, 1.0e30)])
+def test_fp8_weights_with_h_beyond_f16(T, d, E, k, I, clamp):
+    """A clamp whose square f16 does not hold: |h| goes beyond 65504 here."""
+    a = make(T, d, E, k, I, True)
+    a["clamp"] = clamp
+    a["W13_s"] *= 400.0          # g and u of some 500 without a clamp
+    run(a)
+    check(a)
+    one_rounding(a)
+
+
+@pytest.mark.parametrize("clamp", [255.0, 255.9, 256.0, 300.0])
+def test_fp8_weights_around_the_clamp_that_f16_holds(clamp):
+    a = make(6, 256, 5, 2, 192, True)
+    a["clamp"] = clamp
+    a["W13_s"] *= 400.0
+    run(a)
+    check(a)
+    one_rounding(a)
