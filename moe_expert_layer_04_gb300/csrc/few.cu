@@ -199,9 +199,9 @@ __device__ __forceinline__ uint64_t wait_slot(const uint64_t *p, const WaitCtl &
 // global memory: a lane's 16 bytes of row l / 4 are eight consecutive k, fed
 // as two k-pairs to each of two MMAs; the token operand is read the same way,
 // so the order of k inside a step is the same on both sides.
-// Scores and keys are fp32 here (moe_route evaluates the sigmoid in fp64 and
-// rounds it): the logits' own sums differ between the two calls by more than
-// the fp32 sigmoid's error, and fp64 costs 6 us of latency that nothing hides.
+// Scores and weights are rounded once, as moe_route rounds the fp64 values; here the
+// values before the rounding are pairs of fp32 (0.2 us for one token and 384 experts),
+// as fp64 costs 6 us of latency that nothing hides.
 //
 // What follows the gate matmul is latency alone, and the routed experts wait for it: so
 // all of the last CTA's threads add up the partial logits where they fit its shared
@@ -215,7 +215,67 @@ __device__ __forceinline__ uint32_t ordered(float v) {
     return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
 }
 
-__device__ __forceinline__ float sigmoid_f32(float z) { return 1.0f / (1.0f + expf(-z)); }
+__device__ __forceinline__ float exp2i(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
+
+// A value as the sum of two fp32 numbers, the second at most half a spacing of the first.
+// Sums and products by the error-free transformations of Knuth and Dekker.
+struct Pair {
+    float h, l;
+};
+__device__ __forceinline__ Pair two_sum(float a, float b) {
+    const float s = __fadd_rn(a, b), t = __fsub_rn(s, a);
+    return {s, __fadd_rn(__fsub_rn(a, __fsub_rn(s, t)), __fsub_rn(b, t))};
+}
+// |a| >= |b|
+__device__ __forceinline__ Pair fast_two_sum(float a, float b) {
+    const float s = __fadd_rn(a, b);
+    return {s, __fsub_rn(b, __fsub_rn(s, a))};
+}
+// c + r p, |c| >= |r p|, to the accuracy of a pair
+__device__ __forceinline__ Pair horner(float c, Pair r, Pair p) {
+    const float v = __fmul_rn(r.h, p.h);
+    const float e = __fmaf_rn(r.l, p.h, __fmaf_rn(r.h, p.l, __fmaf_rn(r.h, p.h, -v)));
+    Pair s = fast_two_sum(c, v);
+    s.l = __fadd_rn(s.l, e);
+    return s;
+}
+// (a.h + a.l) / (b.h + b.l), one rounding
+__device__ __forceinline__ float quotient(Pair a, Pair b) {
+    const float q = __fdiv_rn(a.h, b.h);
+    const float rest = __fadd_rn(__fmaf_rn(-q, b.h, a.h), __fmaf_rn(-q, b.l, a.l));
+    return __fadd_rn(q, __fdiv_rn(rest, b.h));
+}
+
+// 1 / (1 + e^-z), rounded to fp32: the nearest value but for 3 of 100000 logits, whose
+// neighbour it is (values within 2^-33 of the middle between two).  With e = e^-|z| it
+// is 1 / (1 + e) or e / (1 + e).  e = 2^n e^r, r = -|z| - n ln 2 with ln 2 as the sum of
+// three numbers of which the first has 12 bits (Cody and Waite), e^r by its series up to
+// r^9, the terms up to r^3 in pairs.
+__device__ __forceinline__ float sigmoid_rounded(float z) {
+    const float t = -fminf(fabsf(z), 110.0f);   // (e^-110 is 0 in fp32; a NaN: below)
+    const float n = rintf(t * 1.44269504f);
+    const Pair d = {__fmul_rn(n, 3.1946183e-5f), __fmaf_rn(n, 3.1946183e-5f, -__fmul_rn(n, 3.1946183e-5f))};
+    Pair r = two_sum(__fmaf_rn(n, -0.693115234375f, t), -d.h);
+    r = fast_two_sum(r.h, __fsub_rn(r.l, __fmaf_rn(n, 1.646595e-12f, d.l)));
+    float p = 1.0f / 362880.0f;
+    p = __fmaf_rn(p, r.h, 1.0f / 40320.0f);
+    p = __fmaf_rn(p, r.h, 1.0f / 5040.0f);
+    p = __fmaf_rn(p, r.h, 1.0f / 720.0f);
+    p = __fmaf_rn(p, r.h, 1.0f / 120.0f);
+    p = __fmaf_rn(p, r.h, 1.0f / 24.0f);
+    Pair e = fast_two_sum(1.0f / 6.0f, __fmul_rn(r.h, p));
+    e.l = __fadd_rn(e.l, -4.967054e-9f);        // 1/6 less its fp32 value
+    e = horner(0.5f, r, e);
+    e = horner(1.0f, r, e);
+    e = horner(1.0f, r, e);
+    const int k = (int)n;
+    const float f = exp2i(max(k, -100));
+    Pair den = fast_two_sum(1.0f, __fmul_rn(e.h, f));
+    den.l = __fmaf_rn(e.l, f, den.l);
+    float s = quotient(z >= 0.0f ? Pair{1.0f, 0.0f} : e, den);
+    if (z < 0.0f) s = s * exp2i(max(k, -126)) * exp2i(min(k + 126, 0));
+    return z == z ? s : z;
+}
 
 // Token t in f16 (for FP8 weights): times the power of two that brings its
 // largest magnitude to [2^14, 2^15), so that bf16's eight bits survive down to
@@ -339,7 +399,7 @@ __global__ void __launch_bounds__(kGateWarps * 32) few_gate_kernel(const __grid_
             const float b = p.bias[e + ((p.is_vision && p.is_vision[t]) ? p.E : 0)];
 #pragma unroll
             for (int s = 0; s < kGateSplits; ++s) v += z[s];
-            v = sigmoid_f32(v);
+            v = sigmoid_rounded(v);
             scores[i] = v;
             keys[i] = v + b;
         }
@@ -364,7 +424,7 @@ __global__ void __launch_bounds__(kGateWarps * 32) few_gate_kernel(const __grid_
                 for (int s = 0; s < p.splits; ++s)
                     z += __ldcg(p.part + ((size_t)s * p.T + t) * p.E + my_id);
                 if (p.logit_offset) z += p.logit_offset[my_id];
-                my_s = sigmoid_f32(z);
+                my_s = sigmoid_rounded(z);
             }
         } else {
             const float *bt = p.bias + ((p.is_vision && p.is_vision[t]) ? p.E : 0);
@@ -404,7 +464,7 @@ __global__ void __launch_bounds__(kGateWarps * 32) few_gate_kernel(const __grid_
                 }
 #pragma unroll
                 for (int i = 0; i < EPL; ++i) {
-                    zv[i] = sigmoid_f32(zv[i]);
+                    zv[i] = sigmoid_rounded(zv[i]);
                     key[i] = __float_as_uint(zv[i] + __uint_as_float(key[i]));
                 }
             }
@@ -442,11 +502,19 @@ __global__ void __launch_bounds__(kGateWarps * 32) few_gate_kernel(const __grid_
                 }
             }
         }
-        float sum = 0.0f;
-        for (int j = 0; j < p.k; ++j) sum += __shfl_sync(0xffffffffu, my_s, j);
+        Pair sum = {0.0f, 0.0f};
+        for (int j = 0; j < p.k; ++j) {
+            const Pair a = two_sum(sum.h, __shfl_sync(0xffffffffu, my_s, j));
+            sum = fast_two_sum(a.h, __fadd_rn(a.l, sum.l));
+        }
         if (lane < p.k) {
             const size_t o = (size_t)t * p.k + lane;
-            const float w = sum > 0.0f ? p.scaling * my_s / sum : 0.0f;
+            // (tiny scores by a power of two, which cancels, so that no product is subnormal)
+            const float up = sum.h < 1.0e-20f ? exp2i(100) : 1.0f;
+            const float v = my_s * up, num = __fmul_rn(p.scaling, v);
+            float w = 0.0f;
+            if (sum.h > 0.0f)
+                w = quotient({num, __fmaf_rn(p.scaling, v, -num)}, {sum.h * up, sum.l * up});
             st_slot(p.routed + o, (uint64_t)(my_id + 1) << 32 | __float_as_uint(w));
             if (p.ids_out) p.ids_out[o] = my_id;
             if (p.w_out) p.w_out[o] = w;
@@ -531,8 +599,6 @@ __device__ __forceinline__ FewItem few_item(int t, int tiles1, int tiles2, float
     if (q > n_pass) it.tile = -1;
     return it;
 }
-
-__device__ __forceinline__ float exp2i(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
 
 __device__ __forceinline__ void cp_async4(void *dst, const void *src) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src)
