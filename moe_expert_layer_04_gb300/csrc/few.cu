@@ -474,9 +474,8 @@ __global__ void __launch_bounds__(kGateWarps * 32) few_gate_kernel(const __grid_
                 const float kk = __uint_as_float(key[i]);
                 key[i] = lane + 32 * i >= p.E ? 0u : ordered(kk == kk ? kk : -FLT_MAX);
             }
-            const uint32_t none = ordered(-INFINITY);
             for (int j = 0; j < p.k; ++j) {
-                uint32_t bk = none;
+                uint32_t bk = 0u;   // below every key, minus infinity's too
                 float bs = 0.0f;
                 int be = INT_MAX;
 #pragma unroll
@@ -496,9 +495,9 @@ __global__ void __launch_bounds__(kGateWarps * 32) few_gate_kernel(const __grid_
                     for (int i = 0; i < EPL; ++i)
                         if (lane + 32 * i == first) key[i] = 0u;
                 }
-                if (lane == j) {
-                    my_id = first == INT_MAX ? 0 : first;
-                    my_s = first == INT_MAX ? 0.0f : bs;
+                if (lane == j) {   // (there is always one: k <= E)
+                    my_id = first;
+                    my_s = bs;
                 }
             }
         }
