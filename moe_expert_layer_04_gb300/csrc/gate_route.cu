@@ -565,12 +565,13 @@ __global__ void __launch_bounds__(kGrThreads, 1)
                         if (!(approx_key(z, bt[e]) >= thr)) continue;
                         const float se = sigmoid_exact_f(z);
                         float key = exact_key(se, bt[e]);
-                        // ids arrive in increasing order: an equal key goes after
                         int id = e;
                         float sv = se;
 #pragma unroll
                         for (int q2 = 0; q2 < kGrKmax; ++q2) {
-                            if (q2 < k && key > ek[q2]) {
+                            // (an entry pushed down goes before equal keys of higher
+                            // ids, and any goes before a place not taken yet)
+                            if (q2 < k && (key > ek[q2] || (key == ek[q2] && id < ei[q2]))) {
                                 const float tk = ek[q2];
                                 const int ti = ei[q2];
                                 const float ts = es[q2];
