@@ -533,8 +533,9 @@ __global__ void __launch_bounds__(kGrThreads, 1)
                 if (j < k) kth = fminf(kth, kv[j]);
             // error bound of the approximate key: see approx_key; the two key
             // additions add half an ulp of the key each
+            // (an infinite key is the only one in its window)
             const float tol = 4e-6f * fmaxf(1.0f, fabsf(kth));
-            const float thr = kth - 2.0f * tol;
+            const float thr = fabsf(kth) == INFINITY ? kth : kth - 2.0f * tol;
             const bool rescan = topk && valid && !(kv[L - 1] < thr);
             if (topk) {
                 // the exact keys start from the logits in global memory (the

@@ -111,8 +111,9 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_topk_kernel(
         }
         // error bound of the approximate key: expf, 1+e and the division add a
         // few ulp of the score; the two key additions half an ulp of the key each
+        // (an infinite key is the only one in its window)
         const float tol = 4e-6f * fmaxf(1.0f, fabsf(kth));
-        const float thr = kth - 2.0f * tol;
+        const float thr = fabsf(kth) == INFINITY ? kth : kth - 2.0f * tol;
         // pass 2: exact keys inside the window, then the exact top-k.  The
         // window's experts are first packed one per lane, so that the warp
         // evaluates the fp64 sigmoid once for all of them.

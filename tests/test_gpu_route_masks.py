@@ -116,6 +116,6 @@ def test_masked_experts(call, T, E, k, mask):
 
 @pytest.mark.parametrize("mask", list(FORCED))
 @pytest.mark.parametrize("T,E,k", SIZES)
-@pytest.mark.parametrize("call", ["few"])
+@pytest.mark.parametrize("call", list(CALLS))
 def test_forced_experts(call, T, E, k, mask):
     check(call, T, E, k, FORCED[mask])
