@@ -15,6 +15,7 @@ SwiGLU, and result return; the shared expert of "MindSpore HyperParallel
 """
 from __future__ import annotations
 
+import math
 from dataclasses import dataclass
 
 import torch
@@ -37,6 +38,12 @@ def mx_supported(d: int, I: int) -> bool:
 def fp8_supported(d: int, I: int) -> bool:
     """Shapes the expert FFN on FP8 rows (moe_expert_ffn_fp8) takes."""
     return d % 128 == 0 and I % 128 == 0
+
+
+def _expect(name, t, *shape):
+    """A tensor, where it is given, has the elements that a call reads or writes."""
+    if t is not None and t.numel() != math.prod(shape):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {shape}")
 
 
 def ffn_fused_supported(d: int, I: int) -> bool:
@@ -319,13 +326,16 @@ class MoELayer:
         if self.mx:
             raise RuntimeError("moe_layer_few takes bf16 or FP8 weights")
         T = int(x.shape[0])
-        if T not in self._few_ws:
-            n = _lib.moe_few_workspace_size(T, D.d, D.E, D.k, D.I)
-            if n == 0:
-                raise ValueError(f"moe_layer_few does not take {T} tokens of {D}")
-            # zero before its first use, whatever stream the calls then run on
-            self._few_ws[T] = torch.zeros(n, dtype=torch.uint8, device=x.device)
-            torch.cuda.current_stream(x.device).synchronize()
+        _expect("x", x, T, D.d)
+        _expect("logit_offset", logit_offset, D.E)
+        if int(mode) == MOE_ROUTE_TOPK:
+            _expect("bias", bias, 2, D.E)
+            _expect("is_vision", is_vision, T)
+        elif tid2eid is not None:
+            _expect("input_ids", input_ids, T)
+            _expect("tid2eid", tid2eid, tid2eid.shape[0], D.k)
+        _expect("y", y, T, D.d)
+        ws = self._few_workspace(T, x.device)
         if y is None:
             y = torch.empty(T, D.d, dtype=torch.bfloat16, device=x.device)
         w = (dict(W13_q=self.W13_q, W13_s=self.W13_s, W2_q=self.W2_q, W2_s=self.W2_s)
@@ -334,8 +344,19 @@ class MoELayer:
             T=T, d=D.d, E=D.E, k=D.k, I=D.I, scaling=self.scaling, clamp=self.clamp,
             mode=int(mode), vocab=0 if tid2eid is None else int(tid2eid.shape[0]), x=x,
             W_g=self.w["W_g"], logit_offset=logit_offset, bias=bias, is_vision=is_vision,
-            input_ids=input_ids, tid2eid=tid2eid, y=y, ws=self._few_ws[T], **w), stream)
+            input_ids=input_ids, tid2eid=tid2eid, y=y, ws=ws, **w), stream)
         return y
+
+    def _few_workspace(self, T, device):
+        if T not in self._few_ws:
+            D = self.dims
+            n = _lib.moe_few_workspace_size(T, D.d, D.E, D.k, D.I)
+            if n == 0:
+                raise ValueError(f"moe_layer_few does not take {T} tokens of {D}")
+            # zero before its first use, whatever stream the calls then run on
+            self._few_ws[T] = torch.zeros(n, dtype=torch.uint8, device=device)
+            torch.cuda.current_stream(device).synchronize()
+        return self._few_ws[T]
 
     # ----------------------------------------------------------- backward
     def backward(self, dY, want_dlogits=False, want_dweights=False, stream=None,
@@ -455,7 +476,7 @@ class GroupedLinearFP8:
     weight: bf16 [G, N, K] (CUDA), quantised here in both orientations; again
     with quantize_weights() after it changes.  G = 1 is a dense layer.  rows:
     the most rows of a call.  offsets: int32 [G+1] on the device, the groups'
-    first rows (as moe_permute writes them).
+    first rows (as moe_permute writes them), the last one the number of rows.
     """
 
     def __init__(self, weight, rows: int):
@@ -474,6 +495,7 @@ class GroupedLinearFP8:
         self.dy_q, self.dy_s = torch.empty(rows, N, **u8), torch.empty(rows, bn, **f32)
         self.dW = torch.empty(G, N, K, **f32)
         self.ws = torch.empty(n, **u8)
+        self.x = self.offsets = None
         self.quantize_weights()
 
     def quantize_weights(self, stream=None):
@@ -483,6 +505,10 @@ class GroupedLinearFP8:
     def forward(self, x, offsets, stream=None):
         """y [R, N] bf16 of the rows x [R, K] bf16, R <= rows."""
         R = int(x.shape[0])
+        _expect("x", x, R, self.K)
+        _expect("offsets", offsets, self.G + 1)
+        if R > self.rows:
+            raise ValueError(f"{R} rows, the buffers hold {self.rows}")
         self.x, self.offsets = x, offsets   # the backward reads them
         y = torch.empty(R, self.N, dtype=torch.bfloat16, device=x.device)
         if R == 0:
@@ -494,7 +520,12 @@ class GroupedLinearFP8:
 
     def backward(self, dy, stream=None):
         """dX [R, K] bf16 of the last forward; self.dW [G, N, K] fp32."""
-        R = int(dy.shape[0])
+        if self.x is None:
+            raise RuntimeError("backward() before a forward()")
+        R = int(self.x.shape[0])
+        _expect("dy", dy, R, self.N)
+        if int(dy.shape[0]) != R:
+            raise ValueError(f"dy: {int(dy.shape[0])} rows, the forward had {R}")
         dx = torch.empty(R, self.K, dtype=torch.bfloat16, device=dy.device)
         if R == 0:
             self.dW.zero_()
