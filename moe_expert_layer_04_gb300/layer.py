@@ -46,6 +46,17 @@ def _expect(name, t, *shape):
         raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {shape}")
 
 
+def _result(stream, device, *shape):
+    """A bf16 tensor that a call on `stream` (None: the current one) writes and the
+    caller reads on the current stream: memory of the first, kept for both."""
+    if stream is None:
+        return torch.empty(*shape, dtype=torch.bfloat16, device=device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(*shape, dtype=torch.bfloat16, device=device)
+    t.record_stream(torch.cuda.current_stream(device))
+    return t
+
+
 def ffn_fused_supported(d: int, I: int) -> bool:
     """Shapes the one-launch expert FFN (moe_expert_ffn_fused) takes: 256-wide
     tiles in both matmuls."""
@@ -319,7 +330,7 @@ class MoELayer:
                     input_ids=None, tid2eid=None, stream=None, y=None):
         """The forward of 1 to 32 tokens x [T, d] (any T, not dims.T) through
         moe_layer_few, from the layer's bf16 or FP8 weights; returns y [T, d]
-        (a new tensor unless given).  It routes into buffers of its own: ids and
+        (a new tensor unless given, of the memory of `stream`).  It routes into buffers of its own: ids and
         weights of the last forward() stay.  The workspace of a T is made at
         its first call and kept, so calls of one T go to one stream."""
         D = self.dims
@@ -337,7 +348,7 @@ class MoELayer:
         _expect("y", y, T, D.d)
         ws = self._few_workspace(T, x.device)
         if y is None:
-            y = torch.empty(T, D.d, dtype=torch.bfloat16, device=x.device)
+            y = _result(stream, x.device, T, D.d)
         w = (dict(W13_q=self.W13_q, W13_s=self.W13_s, W2_q=self.W2_q, W2_s=self.W2_s)
              if self.fp8 else dict(W13=self.w["W13"], W2=self.w["W2"]))
         _lib.moe_layer_few(dict(
@@ -503,14 +514,15 @@ class GroupedLinearFP8:
                                       self.wt_q, self.wt_s, stream)
 
     def forward(self, x, offsets, stream=None):
-        """y [R, N] bf16 of the rows x [R, K] bf16, R <= rows."""
+        """y [R, N] bf16 of the rows x [R, K] bf16, R <= rows.  With `stream` the work and
+        y's memory belong to that stream; the backward too then takes it."""
         R = int(x.shape[0])
         _expect("x", x, R, self.K)
         _expect("offsets", offsets, self.G + 1)
         if R > self.rows:
             raise ValueError(f"{R} rows, the buffers hold {self.rows}")
         self.x, self.offsets = x, offsets   # the backward reads them
-        y = torch.empty(R, self.N, dtype=torch.bfloat16, device=x.device)
+        y = _result(stream, x.device, R, self.N)
         if R == 0:
             return y
         _lib.moe_fp8_quantize(x, R, self.K, self.x_q, self.x_s, stream)
@@ -526,9 +538,10 @@ class GroupedLinearFP8:
         _expect("dy", dy, R, self.N)
         if int(dy.shape[0]) != R:
             raise ValueError(f"dy: {int(dy.shape[0])} rows, the forward had {R}")
-        dx = torch.empty(R, self.K, dtype=torch.bfloat16, device=dy.device)
+        dx = _result(stream, dy.device, R, self.K)
         if R == 0:
-            self.dW.zero_()
+            with torch.cuda.stream(stream):   # (None: the current one)
+                self.dW.zero_()
             return dx
         _lib.moe_fp8_quantize(dy, R, self.N, self.dy_q, self.dy_s, stream)
         _lib.moe_fp8_matmul(self.dy_q, self.dy_s, self.offsets, self.G, R, self.wt_q, self.wt_s,
