@@ -175,7 +175,7 @@ class MoELayer:
             self.dW2 = torch.empty(D.E + 1, D.d, D.I, dtype=torch.float32, **e)
             self.dlogits = None
             self.dweights = None
-        self._few_ws = {}   # forward_few: a workspace for each number of tokens
+        self._few_ws = {}   # forward_few: a workspace for each number of tokens and stream
 
     def _init_fp8(self, e):
         D = self.dims
@@ -330,9 +330,12 @@ class MoELayer:
                     input_ids=None, tid2eid=None, stream=None, y=None):
         """The forward of 1 to 32 tokens x [T, d] (any T, not dims.T) through
         moe_layer_few, from the layer's bf16 or FP8 weights; returns y [T, d]
-        (a new tensor unless given, of the memory of `stream`).  It routes into buffers of its own: ids and
-        weights of the last forward() stay.  The workspace of a T is made at
-        its first call and kept, so calls of one T go to one stream."""
+        (a new tensor unless given, of the memory of `stream`).  It routes into
+        buffers of its own: ids and weights of the last forward() stay.
+        The workspace of a T and a stream is made at its first call and kept.  A
+        captured call whose stream has one takes it (replay such a graph in turn
+        with that stream's calls); else the graph gets its own, which it zeroes on
+        every replay.  See reset_few()."""
         D = self.dims
         if self.mx:
             raise RuntimeError("moe_layer_few takes bf16 or FP8 weights")
@@ -346,7 +349,7 @@ class MoELayer:
             _expect("input_ids", input_ids, T)
             _expect("tid2eid", tid2eid, tid2eid.shape[0], D.k)
         _expect("y", y, T, D.d)
-        ws = self._few_workspace(T, x.device)
+        ws = self._few_workspace(T, x.device, stream)
         if y is None:
             y = _result(stream, x.device, T, D.d)
         w = (dict(W13_q=self.W13_q, W13_s=self.W13_s, W2_q=self.W2_q, W2_s=self.W2_s)
@@ -358,16 +361,25 @@ class MoELayer:
             input_ids=input_ids, tid2eid=tid2eid, y=y, ws=ws, **w), stream)
         return y
 
-    def _few_workspace(self, T, device):
-        if T not in self._few_ws:
+    def _few_workspace(self, T, device, stream=None):
+        key = T, _lib._stream(stream)
+        ws = self._few_ws.get(key)
+        if ws is None:
             D = self.dims
             n = _lib.moe_few_workspace_size(T, D.d, D.E, D.k, D.I)
             if n == 0:
                 raise ValueError(f"moe_layer_few does not take {T} tokens of {D}")
-            # zero before its first use, whatever stream the calls then run on
-            self._few_ws[T] = torch.zeros(n, dtype=torch.uint8, device=device)
-            torch.cuda.current_stream(device).synchronize()
-        return self._few_ws[T]
+            with torch.cuda.stream(stream):   # (None: the current one)
+                ws = torch.zeros(n, dtype=torch.uint8, device=device)
+                if not torch.cuda.is_current_stream_capturing():
+                    self._few_ws[key] = ws
+        return ws
+
+    def reset_few(self):
+        """Drops the workspaces of forward_few(), so that its next calls start from
+        zeroed ones: after a call that recorded MOE_ERR_TIMEOUT
+        (moe_last_device_status), which can leave counters that are not zero."""
+        self._few_ws.clear()
 
     # ----------------------------------------------------------- backward
     def backward(self, dY, want_dlogits=False, want_dweights=False, stream=None,
