@@ -99,7 +99,10 @@ class MoELayer:
     matmuls (moe_backward_mx).  Two launches (not fused_ffn).
     fp8: the serving variant whose expert weights are FP8 (E4M3) with one fp32
     scale per 128 x 128 block, quantised here (moe_fp8_quantize_weights; again
-    with quantize_weights() after they change).  forward() quantises each
+    with quantize_weights() after they change), or given so, as checkpoints hold
+    them: weights then has W13_q [E+1,2I,d], W2_q [E+1,d,I] (E4M3 codes, as
+    float8_e4m3fn or uint8) and W13_s [E+1,2I/128,d/128], W2_s [E+1,d/128,I/128]
+    (fp32) in place of W13 and W2.  forward() quantises each
     step's token rows in the dispatch (moe_fp8_gather) and runs
     moe_expert_ffn_fp8; forward_few() decodes from the same weights.  Forward
     only (GroupedLinearFP8 has the matmul's gradients).
@@ -182,11 +185,24 @@ class MoELayer:
         f32, u8 = dict(dtype=torch.float32, **e), dict(dtype=torch.uint8, **e)
         bd, bi = _lib.moe_fp8_scale_cols(D.d), _lib.moe_fp8_scale_cols(D.I)
         G = D.E + 1
-        self.W13_q = torch.empty(G, 2 * D.I, D.d, **u8)
-        self.W13_s = torch.empty(G, 2 * bi, bd, **f32)
-        self.W2_q = torch.empty(G, D.d, D.I, **u8)
-        self.W2_s = torch.empty(G, bd, bi, **f32)
-        self.quantize_weights()
+        shapes = dict(W13_q=(G, 2 * D.I, D.d), W13_s=(G, 2 * bi, bd), W2_q=(G, D.d, D.I),
+                      W2_s=(G, bd, bi))
+        given = [n for n in shapes if n in self.w]
+        if given and (len(given) < 4 or "W13" in self.w or "W2" in self.w):
+            raise ValueError("FP8 weights are W13 and W2, or W13_q, W13_s, W2_q and W2_s")
+        for name, shape in shapes.items():
+            codes = name.endswith("_q")
+            if given:
+                t = self.w[name]
+                if codes and t.dtype == torch.float8_e4m3fn:
+                    t = t.view(torch.uint8)
+                if tuple(t.shape) != shape or t.dtype != (torch.uint8 if codes else torch.float32):
+                    raise ValueError(f"{name}: {t.dtype} {tuple(t.shape)}, expected {shape}")
+            else:
+                t = torch.empty(*shape, **(u8 if codes else f32))
+            setattr(self, name, t)
+        if not given:
+            self.quantize_weights()
         self.x_perm_q = torch.empty(D.R, D.d, **u8)
         self.x_perm_s = torch.empty(D.R, bd, **f32)
         self.h_q = torch.empty(D.R, D.I, **u8)
@@ -219,6 +235,8 @@ class MoELayer:
         backward also along d (W2) and 2I (W13) for the dgrad matmuls."""
         D = self.dims
         G = D.E + 1
+        if "W13" not in self.w:
+            raise RuntimeError("the layer was given FP8 weights: there are none to quantise")
         W13, W2 = self.w["W13"], self.w["W2"]
         if self.fp8:
             _lib.moe_fp8_quantize_weights(W13, G, 2 * D.I, D.d, self.W13_q, self.W13_s,
