@@ -193,7 +193,7 @@ __device__ __forceinline__ uint64_t wait_slot(const uint64_t *p, const WaitCtl &
 // ------------------------------------------------------------ gate, routing
 //
 // A CTA takes 16 experts and one of `splits` parts of the contraction (all SMs
-// on the few megabytes of W_g), its warps every eighth step of 32; the
+// on the few megabytes of W_g), its warps every sixteenth step of 32; the
 // partial logits go to the workspace, and the CTA that finishes last adds
 // them in order and routes, a warp per token.  mma fragments straight from
 // global memory: a lane's 16 bytes of row l / 4 are eight consecutive k, fed
@@ -279,7 +279,8 @@ __device__ __forceinline__ float sigmoid_rounded(float z) {
 
 // Token t in f16 (for FP8 weights): times the power of two that brings its
 // largest magnitude to [2^14, 2^15), so that bf16's eight bits survive down to
-// 2^-28 of that magnitude and lose at most 2^-40 of it below.  One CTA.
+// 2^-31 of that magnitude and lose at most 2^-39 of it below.  By no more than 2^100,
+// as the first matmul's sums grow with it and have to stay inside fp32.  One CTA.
 __device__ void few_token_f16(const FewParams &p, int t, uint32_t *warp_top) {
     const uint4 *src = reinterpret_cast<const uint4 *>(p.x + (size_t)t * p.d);
     uint32_t m = 0;
