@@ -48,13 +48,16 @@
 // slot order, so results do not depend on who finishes when.
 //
 // Measured (time of the call; of the copy bandwidth in brackets), d = 4096, I =
-// 2048, 384 experts, top 6: one token 58 us (90 %), 32 tokens 1.03-1.07 ms (7.2-7.4
-// TB/s of the 7.7 GB of weights they hit); FP8, one token 37.7 us (70 %), 16 tokens
-// 357-380 us (85-90 %).  23 tokens through a table of 97 experts, d = 1152, I = 704: 83-86
-// us (58-60 %).  A token's 37.7 us: routed 5 us after the start, first routed copies
-// after 8, of which the shared W13 hides 4; then the stream runs at 5.5-6 TB/s, held
-// back by the copying warp (1.2 us an item of 64 KB) and by the time that a stage
-// stays in the ring (2 us on its way, 1.5 until it is read), and two dependences.
+// 2048, 384 experts, top 6: one token 58.9 us (89 %); 32 tokens 1.08 ms with 149 experts
+// hit on average (7.0 TB/s of their 7.5 GB); FP8, one token 38.2 us (69 %), 16 tokens 375-390
+// us with 87 experts hit (5.7-5.9 TB/s of 2.2 GB).  23 tokens through a table of 97 experts, d
+// = 1152, I = 704: 89-92 us with 66 hit (3.6 TB/s).  What holds the last one back is not HBM
+// but what a tile of 16 short weight rows costs the multiplying warps whatever it brings
+// (waits, the hand-over of sums, a signal).  A token's 38 us: routed 5 us after the
+// start, first routed copies after 8, of which the shared W13 hides 4; then the stream
+// runs at 5.5-6 TB/s, held back by the copying warp (1.2 us an item of 64 KB) and by the
+// time that a stage stays in the ring (2 us on its way, 1.5 until it is read), and two
+// dependences.
 #include <cfloat>
 #include <climits>
 
@@ -791,9 +794,9 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_experts_kernel(
         for (uint32_t n = 0; ok; ++n) {
             if (!mbar_wait_warp(qfull, n & 1u, wc)) break;
             const int t = __shfl_sync(0xffffffffu, *queue, 0);
-            // A long list is made ahead by the warp that takes the numbers (23 tokens of
-            // 5 experts 86 -> 82 us); a short one here, as late as it is needed (one
-            // token 37.8 us, 38.5 if made there).
+            // A long list is made ahead by the warp that takes the numbers (which took 4 us
+            // off 23 tokens of 5 experts); a short one here, as late as it is needed (made
+            // there, one token takes 0.7 us more).
             if (t >= tiles1 && n_pass < 0) {
                 n_pass = S <= 32 ? few_list_short<NT>(p, S, meta, lane, wc) : meta->n_pass;
                 if (n_pass < 0) break;

@@ -17,20 +17,22 @@
 // memory, is multiplied by its scales and added to the tile's accumulator in
 // registers, in fp32.
 //
-// What bounds it: for a 128 x 256 tile a block costs the tensor core 537 cycles,
-// measured alone, and reading its sums 256 more on the same tensor memory port, which
-// the two cannot share: 793 cycles a block, whatever feeds it (a pair of SMs on one
-// 256 x 256 tile measured 1120-1220; its operands cross shared memory half as often,
-// but that is not the limit).  The loop below takes 770-850.  At that rate the
-// products of a long run of blocks go at 2.0 PFLOP/s, half of what the tensor core
-// does on FP8 without block scales.  The rest is what a tile costs outside its loop:
+// What bounds it: a block of a 128 x 256 tile takes the tensor core 512 cycles, the
+// reading of its sums by eight warps 320, the copies of its 48 KB of operands out of L2
+// 570, each on its own; side by side the three do not slow one another (512, 355, 570).
+// What does cost is their order: with two accumulators, each read between its MMAs and
+// its next ones, 580 cycles a block without any scales, and the loop below takes 806
+// (FFN1 835, WGRAD with a product for the column scales 1080), measured as the
+// difference of long and short contractions.  At that rate the products of a long run of
+// blocks go at 2.0 PFLOP/s, half of what the tensor core does on FP8 without block
+// scales.  The rest is what a tile costs outside its loop:
 // the first operands of the next tile and two blocks of products run during it, then
 // the tensor core waits.  So the output leaves through shared memory by TMA stores that
 // run during the next tile (ROWS: 1500 cycles a tile, 3000 straight from the registers),
 // the next tile's place and scales are found before it, and the weight gradient, whose
 // loops are short (a group of 900 rows has 7 blocks) and whose fp32 output is 128 KB a
-// tile, takes 4000 cycles for it, a third of its time: the output crosses shared memory
-// twice (2048 cycles) while the next tile's first products do (1536).
+// tile, takes 4000 cycles for it, a third of its time: the same warps accumulate and
+// store, and the output crosses shared memory twice (2048 cycles).
 //
 // Measured (time of the call): 12345 rows in 33 uneven groups, 4096 x 2048 weights: 114-118
 // us, 1.8 PFLOP/s; expert FFN of 32768 rows over 33 groups, d = 4096, I = 2048: 794-823 us,
@@ -685,7 +687,8 @@ static int rows_bn(int max_rows, int G, int N) {
 moe_status launch_fp8_matmul(const uint8_t *aq, const float *as, const int32_t *offsets, int G,
                              int max_rows, const uint8_t *bq, const float *bs, const float *row_w,
                              int w_rows, int N, int K, uint16_t *out, cudaStream_t st) {
-    // A few rows of one matrix: 6.6 us there against 8.9 here at 4096 x 4096 and one row,
+    // A few rows of one matrix (calls in a graph, each on other weights than the one before,
+    // from HBM): 6.6 us there against 8.9 here at 4096 x 4096 and one row,
     // 1.9 against 3.1 at 1024 x 512, 7.6 against 25 at 128 x 16384 (few tiles to spread),
     // 14.4 against 13.9 at 16384 x 4096; with 16 rows the products cost it as much as it
     // gains (8.7 against 8.9).
