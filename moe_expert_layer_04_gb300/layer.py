@@ -257,6 +257,7 @@ class MoELayer:
     def route(self, x, bias, is_vision=None, logit_offset=None, mode=MOE_ROUTE_TOPK,
               input_ids=None, tid2eid=None, stream=None):
         D = self.dims
+        self._rows("x", x)
         self.x = x       # the backward reads the forward's input
         if self.fused_route:
             _lib.moe_gate_route(x, self.w["W_g"], logit_offset, bias, is_vision, input_ids,
@@ -268,8 +269,16 @@ class MoELayer:
                            D.T, D.d, D.E, D.k, self.scaling, mode, self.logits, self.ids,
                            self.weights, self.scores_sel, stream)
 
+    def _rows(self, name, t):
+        """T rows of d elements at least, where the tensor is given: what the calls read
+        or write, whatever its shape says."""
+        D = self.dims
+        if t is not None and t.numel() < D.T * D.d:
+            raise ValueError(f"{name}: shape {tuple(t.shape)}, the layer has T = {D.T}, d = {D.d}")
+
     def dispatch(self, x, stream=None):
         D = self.dims
+        self._rows("x", x)
         low = self.mx or self.fp8
         _lib.moe_permute(self.ids, self.weights, None if low else x, D.T, D.d, D.E, D.k,
                          self.counts, self.offsets, self.row_token, self.slot_row,
@@ -330,6 +339,7 @@ class MoELayer:
 
     def combine(self, stream=None, y=None):
         D = self.dims
+        self._rows("y", y)
         _lib.moe_combine(self.y_perm, self.slot_row, D.T, D.d, D.k, 1,
                          self.y if y is None else y, stream)
 
@@ -337,7 +347,7 @@ class MoELayer:
                 input_ids=None, tid2eid=None, stream=None, y=None):
         """One forward pass; the output goes to self.y, or to `y` ([T, d] bf16)
         when given."""
-        self.x = x
+        self._rows("y", y)
         self.route(x, bias, is_vision, logit_offset, mode, input_ids, tid2eid, stream)
         self.dispatch(x, stream)
         self.experts(stream)
@@ -408,6 +418,7 @@ class MoELayer:
         D = self.dims
         if not self.backward_enabled:
             raise RuntimeError("layer built without backward buffers")
+        self._rows("dY", dY)
         if want_dlogits and self.dlogits is None:
             self.dlogits = torch.empty(D.T, D.E, dtype=torch.float32, device=dY.device)
         if want_dweights and self.dweights is None:
