@@ -677,7 +677,8 @@ moe_status moe_fp8_quantize_weights(const uint16_t *src, int G, int N, int K, ui
  *                         sum_{k in block b} a_q[r, k] b_q[g, n, k] )
  * with fp32 sums, w_r = row_weight[r] for r < w_rows (row_weight NULL or r >=
  * w_rows: 1).  a_q [R, K], offsets int32 [G+1] on the device with R =
- * offsets[G] <= max_rows, b_q [G, N, K], out [R, N] bf16.  G = 1 is a dense
+ * offsets[G] <= max_rows (in this and the calls below, offsets that descend or leave
+ * [0, max_rows] are cut to it and recorded as MOE_ERR_INVALID_ARG on the device), b_q [G, N, K], out [R, N] bf16.  G = 1 is a dense
  * product.  The data gradient is the same call with the transposed weight
  * (N and K exchanged) and the quantised output gradient.  K % 16 == 0,
  * N % 8 == 0, 1 <= G <= 1025. */

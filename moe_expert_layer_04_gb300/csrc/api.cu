@@ -1324,11 +1324,11 @@ moe_status moe_fp8_wgrad(const uint16_t *a, const uint16_t *b, const int32_t *of
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const Fp8WgradWorkspace w =
         carve_fp8_wgrad(static_cast<uint8_t *>(ws), G, max_rows, M, N);
-    moe_status r = launch_fp8_chunks(offsets, G, w.first, st);
+    moe_status r = launch_fp8_chunks(offsets, G, max_rows, w.chunks, w.first, st);
     if (r == MOE_OK && max_rows > 0)
-        r = launch_fp8_columns(a, offsets, w.first, G, w.chunks, M, w.aq, w.as, st);
+        r = launch_fp8_columns(a, offsets, w.first, G, max_rows, w.chunks, M, w.aq, w.as, st);
     if (r == MOE_OK && max_rows > 0)
-        r = launch_fp8_columns(b, offsets, w.first, G, w.chunks, N, w.bq, w.bs, st);
+        r = launch_fp8_columns(b, offsets, w.first, G, max_rows, w.chunks, N, w.bq, w.bs, st);
     if (r == MOE_OK)
         r = launch_fp8_wgrad(w.aq, w.as, w.bq, w.bs, w.first, G, w.chunks, M, N, dW, st);
     return r;

@@ -214,8 +214,8 @@ __global__ void __launch_bounds__(256)
 // first[g] is the group's first chunk (fp8_chunks_kernel); blockIdx.y = chunk.
 __global__ void __launch_bounds__(256)
     fp8_columns_kernel(const uint16_t *__restrict__ src, const int32_t *__restrict__ offsets,
-                       const int32_t *__restrict__ first, int G, int C, uint8_t *__restrict__ qt,
-                       float *__restrict__ st) {
+                       const int32_t *__restrict__ first, int G, int max_rows, int C,
+                       uint8_t *__restrict__ qt, float *__restrict__ st) {
     __shared__ __align__(16) uint32_t stage[128 * 32];
     __shared__ __align__(16) uint32_t part[8][64];   // per warp: bf16 pair maxima of 128 columns
     __shared__ __align__(16) float factor[128];
@@ -228,8 +228,8 @@ __global__ void __launch_bounds__(256)
         const int mid = (lo + hi + 1) >> 1;
         if (first[mid] <= b) lo = mid; else hi = mid - 1;
     }
-    const int row0 = offsets[lo] + (b - first[lo]) * 128;
-    const int rows = min(128, offsets[lo + 1] - row0);
+    const int row0 = row_offset(offsets[lo], max_rows) + (b - first[lo]) * 128;
+    const int rows = min(128, row_offset(offsets[lo + 1], max_rows) - row0);
     const int col0 = blockIdx.x * 128, cols = min(128, C - col0);
     const int t = threadIdx.x, c0 = (t & 7) * 16;
     Tile a;
@@ -277,23 +277,31 @@ __global__ void __launch_bounds__(256)
     }
 }
 
-// first[g]: chunks of 128 rows before group g; first[G] their number.  One warp.
-__global__ void fp8_chunks_kernel(const int32_t *__restrict__ offsets, int G,
-                                  int32_t *__restrict__ first) {
+// first[g]: chunks of 128 rows before group g, first[G] their number, at most max_chunks
+// (which offsets that do not descend never exceed).  One warp.
+__global__ void fp8_chunks_kernel(const int32_t *__restrict__ offsets, int G, int max_rows,
+                                  int max_chunks, int32_t *__restrict__ first, int *status) {
     wait_for_kernels_ahead();
     let_kernels_behind_begin();
     const int lane = threadIdx.x;
     int carry = 0;
     for (int base = 0; base <= G; base += 32) {
         const int g = base + lane;
-        int n = g < G ? max(0, (offsets[g + 1] - offsets[g] + 127) >> 7) : 0;
+        int n = 0;
+        if (g < G) {
+            const int o = row_offset(offsets[g], max_rows);
+            const int end = row_offset(offsets[g + 1], max_rows);
+            if (o != offsets[g] || end != offsets[g + 1] || end < o)
+                record_status(status, MOE_ERR_INVALID_ARG);
+            n = max(0, (end - o + 127) >> 7);
+        }
         int incl = n;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const int v = __shfl_up_sync(0xffffffffu, incl, o);
             if (lane >= o) incl += v;
         }
-        if (g <= G) first[g] = carry + incl - n;
+        if (g <= G) first[g] = min(carry + incl - n, max_chunks);
         carry += __shfl_sync(0xffffffffu, incl, 31);
     }
 }
@@ -317,15 +325,20 @@ moe_status launch_fp8_weights(const uint16_t *src, int G, int N, int K, uint8_t 
                         s_t);
 }
 
-moe_status launch_fp8_chunks(const int32_t *offsets, int G, int32_t *first, cudaStream_t st) {
-    return launch_early(fp8_chunks_kernel, dim3(1), 32, 0, st, offsets, G, first);
+moe_status launch_fp8_chunks(const int32_t *offsets, int G, int max_rows, int max_chunks,
+                             int32_t *first, cudaStream_t st) {
+    int *status = device_status_ptr();
+    if (!status) return MOE_ERR_CUDA;
+    return launch_early(fp8_chunks_kernel, dim3(1), 32, 0, st, offsets, G, max_rows, max_chunks,
+                        first, status);
 }
 
 moe_status launch_fp8_columns(const uint16_t *src, const int32_t *offsets, const int32_t *first,
-                              int G, int max_chunks, int C, uint8_t *qt, float *s_t,
-                              cudaStream_t st) {
+                              int G, int max_rows, int max_chunks, int C, uint8_t *qt,
+                              float *s_t, cudaStream_t st) {
     const dim3 grid(fp8_blocks(C), max_chunks);
-    return launch_early(fp8_columns_kernel, grid, 256, 0, st, src, offsets, first, G, C, qt, s_t);
+    return launch_early(fp8_columns_kernel, grid, 256, 0, st, src, offsets, first, G, max_rows, C, qt,
+                        s_t);
 }
 
 }  // namespace moe

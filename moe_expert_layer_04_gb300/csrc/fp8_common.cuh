@@ -87,6 +87,10 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1,
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// A group's first row as the rows of the call allow it: offsets come from the device,
+// where the host cannot check them, and nothing may be read or written past the rows.
+__device__ __forceinline__ int row_offset(int o, int max_rows) { return min(max(o, 0), max_rows); }
+
 // Contiguous bytes into shared memory (both 16-byte aligned, bytes a multiple of
 // 16), counted on an mbarrier.
 __device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t bytes,

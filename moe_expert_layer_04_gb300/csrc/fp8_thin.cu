@@ -34,6 +34,7 @@ struct ThinParams {
     const float *row_w;       // of rows < w_rows (others 1), or null
     int w_rows;
     uint16_t *out;
+    int *status;
 };
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
@@ -53,7 +54,10 @@ __global__ void __launch_bounds__(kThinWarps * 32) fp8_thin_kernel(const ThinPar
     const float *sb = p.sb + (size_t)(n0 / kFp8Block) * K_blocks;
     // piece j (row r4 or r4 + 8, half of the block) of block u, this lane's
     const uint32_t mine = smem_u32(stage) + warp * (U * 2048) + lane * 16;
-    const int row0 = p.offsets[0], n = min(p.offsets[1], p.max_rows) - row0;
+    const int row0 = row_offset(p.offsets[0], p.max_rows);
+    const int n = row_offset(p.offsets[1], p.max_rows) - row0;
+    if (blockIdx.x == 0 && threadIdx.x == 0 && (row0 != p.offsets[0] || row0 + n != p.offsets[1] || n < 0))
+        record_status(p.status, MOE_ERR_INVALID_ARG);
     // this lane's row as an operand, and the first of its two rows of sums
     const int c0 = 2 * t4;
     const bool row_ok = r4 < n;
@@ -144,7 +148,9 @@ __global__ void __launch_bounds__(kThinWarps * 32) fp8_thin_kernel(const ThinPar
 moe_status launch_fp8_thin(const uint8_t *aq, const float *as, const int32_t *offsets, int max_rows,
                            const uint8_t *bq, const float *bs, const float *row_w, int w_rows,
                            int N, int K, uint16_t *out, cudaStream_t st) {
-    const ThinParams p = {aq, bq, as, bs, offsets, max_rows, N, K, row_w, w_rows, out};
+    int *status = device_status_ptr();
+    if (!status) return MOE_ERR_CUDA;
+    const ThinParams p = {aq, bq, as, bs, offsets, max_rows, N, K, row_w, w_rows, out, status};
     static bool attr_set[64] = {};
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return MOE_ERR_CUDA;

@@ -62,6 +62,7 @@ struct Fp8Params {
     const int32_t *offsets;   // [G+1] rows of the groups; WGRAD: their chunks
     const float *sa, *sb;
     int G, N, K_blocks, n_tiles;
+    int max_rows;             // (not WGRAD)
     int nb_n;                 // scale rows of one group's B
     int a_rows;               // of A's boxes
     int M;                    // WGRAD: output rows
@@ -290,8 +291,21 @@ __global__ void __launch_bounds__(kF8Threads, 1) fp8_gemm_kernel(const __grid_co
         for (int base = 0; base <= p.G; base += 32) {
             const int g = base + lane;
             int o = 0, mt = 0;
-            if (g <= p.G) offs[g] = o = p.offsets[g];
-            if (g < p.G) mt = max(0, (p.offsets[g + 1] - o + 127) >> 7);
+            if constexpr (MODE == FP8_WGRAD) {   // checked where they were made
+                if (g <= p.G) offs[g] = p.offsets[g];
+            } else {
+                bool ok = true;
+                if (g <= p.G) {
+                    offs[g] = o = row_offset(p.offsets[g], p.max_rows);
+                    ok = o == p.offsets[g];
+                }
+                if (g < p.G) {
+                    const int end = row_offset(p.offsets[g + 1], p.max_rows);
+                    ok = ok && end >= o;
+                    mt = max(0, (end - o + 127) >> 7);
+                }
+                if (!ok && blockIdx.x == 0) record_status(p.status, MOE_ERR_INVALID_ARG);
+            }
             int incl = mt;
 #pragma unroll
             for (int sft = 1; sft < 32; sft <<= 1) {
@@ -707,6 +721,7 @@ moe_status launch_fp8_matmul(const uint8_t *aq, const float *as, const int32_t *
     p.sb = bs;
     p.G = G;
     p.N = N;
+    p.max_rows = max_rows;
     p.K_blocks = fp8_blocks(K);
     p.nb_n = fp8_blocks(N);
     p.n_tiles = (N + BN - 1) / BN;
@@ -737,6 +752,7 @@ moe_status launch_fp8_ffn1(const uint8_t *xq, const float *xs, const int32_t *of
     p.G = G;
     p.N = 2 * I;
     p.I = I;
+    p.max_rows = max_rows;
     p.K_blocks = d / 128;
     p.nb_n = 2 * I / 128;
     p.n_tiles = I / 128;

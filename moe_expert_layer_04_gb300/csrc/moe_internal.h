@@ -162,10 +162,11 @@ moe_status launch_fp8_rows(const uint16_t *x, const int32_t *slot_row, long long
                            uint8_t *q, float *s, cudaStream_t st);
 moe_status launch_fp8_weights(const uint16_t *src, int G, int N, int K, uint8_t *q, float *s,
                               uint8_t *qt, float *s_t, cudaStream_t st);
-moe_status launch_fp8_chunks(const int32_t *offsets, int G, int32_t *first, cudaStream_t st);
+moe_status launch_fp8_chunks(const int32_t *offsets, int G, int max_rows, int max_chunks,
+                             int32_t *first, cudaStream_t st);
 moe_status launch_fp8_columns(const uint16_t *src, const int32_t *offsets, const int32_t *first,
-                              int G, int max_chunks, int C, uint8_t *qt, float *s_t,
-                              cudaStream_t st);
+                              int G, int max_rows, int max_chunks, int C, uint8_t *qt,
+                              float *s_t, cudaStream_t st);
 moe_status launch_fp8_matmul(const uint8_t *aq, const float *as, const int32_t *offsets, int G,
                              int max_rows, const uint8_t *bq, const float *bs, const float *row_w,
                              int w_rows, int N, int K, uint16_t *out, cudaStream_t st);
