@@ -14,7 +14,7 @@
 // row and of a token row hold the same 16 places along the contraction; which of them an
 // instruction takes together does not matter, so both are used as they lie in memory.
 // Measured, calls in a graph, each on other weights than the one before (from HBM): 4096 x
-// 4096 with one row 6.5 us (2.6 TB/s, 1.7 us of them what an empty call takes), 16384 x
+// 4096 with one row 6.1 us (2.7 TB/s, 1.7 us of them what an empty call takes), 16384 x
 // 4096 14.4-15.1 us (4.4-4.7 TB/s); on the same weights again, from L2: 5.1 and 10.3 us, 1024 x
 // 512 2.0 us.  A call by itself, from the host: 7.0-7.5 us at 4096 x 4096.
 #include "fp8_common.cuh"

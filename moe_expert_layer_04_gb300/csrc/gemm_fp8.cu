@@ -702,7 +702,7 @@ moe_status launch_fp8_matmul(const uint8_t *aq, const float *as, const int32_t *
                              int max_rows, const uint8_t *bq, const float *bs, const float *row_w,
                              int w_rows, int N, int K, uint16_t *out, cudaStream_t st) {
     // A few rows of one matrix (calls in a graph, each on other weights than the one before,
-    // from HBM): 6.6 us there against 8.9 here at 4096 x 4096 and one row,
+    // from HBM): 6.1 us there against 8.9 here at 4096 x 4096 and one row,
     // 1.9 against 3.1 at 1024 x 512, 7.6 against 25 at 128 x 16384 (few tiles to spread),
     // 14.4 against 13.9 at 16384 x 4096; with 16 rows the products cost it as much as it
     // gains (8.7 against 8.9).
