@@ -758,6 +758,165 @@ typedef struct {
 size_t moe_few_workspace_size(int T, int d, int E, int k, int I);
 moe_status moe_layer_few(const moe_few_args *args, void *stream);
 
+/* ------------------------------------------------------------------ MXFP4
+ * Expert weights in 4 bits ([TTN] outlook: A8W4, MxFP4; the pages fix no format).  OCP
+ * Microscaling (MX) v1.0 with E2M1 elements (0, 0.5, 1, 1.5, 2, 3, 4, 6 and their
+ * negatives): blocks of 32 consecutive elements along the contraction, one E8M0 scale
+ * X = 2^(c-127) each.  Quantisation: X = 2^(floor(log2 max|v|) - 2), the exponent at least
+ * -127 (code 0 for an all-zero block); element = v / X rounded to the nearest E2M1 value,
+ * ties to the even code, magnitudes above 6 to 6, the sign kept.  E2M1 has no NaN: a block
+ * that holds a NaN or an infinity gets scale code 255 (NaN), and results that depend on it
+ * are NaN.  A quantised [rows, K] matrix is a pair of byte arrays:
+ *   q  [rows, K/2]                two codes a byte, the even element in the low nibble
+ *   sf [rows, moe_mx_sf_pitch(K)] E8M0 codes as for MXFP8 (padding neither read for
+ *                                 results nor written)
+ * dense, 16-byte aligned; K % 32 == 0. */
+
+/* bf16 [rows, K] -> MXFP4 along the rows (weights: W13 as [G*2I, d], W2 as [G*d, I]). */
+moe_status moe_mx4_quantize(const uint16_t *src, long long rows, int K, uint8_t *q, uint8_t *sf,
+                            void *stream);
+
+/* The values of an MXFP4 matrix in bf16 (exact), out [rows, K]. */
+moe_status moe_mx4_dequantize(const uint8_t *q, const uint8_t *sf, long long rows, int K,
+                              uint16_t *out, void *stream);
+
+/* Dispatch gather into MXFP4 rows, as moe_mx_gather: x [T, d] bf16 quantised once and
+ * written to rows slot_row[t*k + j] (j < k) and S + t of x_perm_q [S+T, d/2] / x_perm_sf.
+ * d % 32 == 0, k <= 32. */
+moe_status moe_mx4_gather(const uint16_t *x, const int32_t *slot_row, int T, int d, int k,
+                          uint8_t *x_perm_q, uint8_t *x_perm_sf, void *stream);
+
+/* Grouped matmul with MXFP4 weights: for every group g < G and row r in
+ * [offsets[g], offsets[g+1])
+ *   out[r, n] = bf16( w_r sum_k a~[r, k] b~[g, n, k] )      (exact products, fp32 sums)
+ * w_r = row_weight[r] for r < w_rows (row_weight NULL or r >= w_rows: 1).  The rows are
+ * MXFP4 (a_bits 4: a_q [R, K/2]) or MXFP8 (a_bits 8: a_q [R, K] as moe_mx_quantize writes
+ * them), a_sf [R, moe_mx_sf_pitch(K)]; b_q [G, N, K/2], b_sf [G, N, moe_mx_sf_pitch(K)];
+ * offsets int32 [G+1] on the device with R = offsets[G] <= max_rows (offsets that descend
+ * or leave [0, max_rows] are cut to it and recorded as MOE_ERR_INVALID_ARG on the device);
+ * out [R, N] bf16, rows outside every group are left as they were.  G = 1 is a dense
+ * product.  N % 8 == 0, 1 <= G <= 1025, K % 32 == 0; with a_bits 8 also K % 128 == 0 (else
+ * MOE_ERR_UNSUPPORTED) and b_q 32-byte aligned. */
+moe_status moe_mx4_matmul(const uint8_t *a_q, const uint8_t *a_sf, int a_bits,
+                          const int32_t *offsets, int G, int max_rows, const uint8_t *b_q,
+                          const uint8_t *b_sf, const float *row_weight, int w_rows, int N, int K,
+                          uint16_t *out, void *stream);
+
+/* The expert FFN with MXFP4 weights on MXFP8 rows: moe_expert_ffn_mx with 4-bit weights.
+ *   [g | u] = x~[r] W13~[g]^T
+ *   h~[r]   = MXFP8( silu(min(g, clamp)) * clamp(u, -clamp, clamp) )  along I
+ *   y[r]    = bf16( row_weight[r] * (h~[r] W2~[g]^T) )
+ * x_perm_q [R, d] / x_perm_sf (moe_mx_gather); W13_q [G, 2I, d/2] / W13_sf, W2_q
+ * [G, d, I/2] / W2_sf (MXFP4, codes 32-byte aligned); outputs h_q [R, I], h_sf, y_perm
+ * [R, d] bf16.  d % 128 == 0, I % 128 == 0 (else MOE_ERR_UNSUPPORTED).  No workspace. */
+moe_status moe_expert_ffn_mx4(const uint8_t *x_perm_q, const uint8_t *x_perm_sf,
+                              const int32_t *offsets, int G, int max_rows, const uint8_t *W13_q,
+                              const uint8_t *W13_sf, const uint8_t *W2_q, const uint8_t *W2_sf,
+                              const float *row_weight, int S, int d, int I, float clamp,
+                              uint8_t *h_q, uint8_t *h_sf, uint16_t *y_perm, void *stream);
+
+/* --------------------------------------------------- the norm ahead of the layer
+ * Root-mean-square norm of the rows with the residual's addition before it ([HP41] §2.3,
+ * MegaMHC: residual update and norm) and the rows' quantisation behind it.
+ *   v    = bf16(x + residual)                       (residual NULL: v = x)
+ *   rstd = 1 / sqrt( mean_i v[t,i]^2 + eps )        (fp32)
+ *   u    = v rstd weight                            (fp32)
+ *   y    = bf16(u);  q, scales = u in the format's blocks (not of the rounded y)
+ * x, residual, residual_out, y [T, d] bf16; weight [d] fp32; rstd [T] fp32.  residual and
+ * residual_out (= v) are both given or both NULL; residual_out may be x or residual.
+ * y and rstd may be NULL, and y too may be x.  format: MOE_ROWS_NONE (q and scales
+ * NULL), MOE_ROWS_FP8 (q [T, d], scales fp32 [T, ceil(d/128)], the rule of
+ * moe_fp8_quantize), MOE_ROWS_MXFP8 (q [T, d], scales uint8 [T, moe_mx_sf_pitch(d)], as
+ * moe_mx_quantize) or MOE_ROWS_MXFP4 (q [T, d/2], scales likewise, as moe_mx4_quantize).
+ * T >= 0; d % 8 == 0, with FP8 d % 16 == 0, with MX d % 32 == 0; d <= 32768 (else
+ * MOE_ERR_UNSUPPORTED); eps > 0, finite.  A row whose squares leave fp32's range has
+ * rstd 0. */
+typedef enum {
+    MOE_ROWS_NONE = 0, MOE_ROWS_FP8 = 1, MOE_ROWS_MXFP8 = 2, MOE_ROWS_MXFP4 = 3
+} moe_row_format;
+typedef struct {
+    int T, d;
+    float eps;
+    int format;                   /* moe_row_format */
+    const uint16_t *x;            /* [T,d] */
+    const uint16_t *residual;     /* [T,d] or NULL */
+    const float *weight;          /* [d] */
+    uint16_t *residual_out;       /* [T,d] out, or NULL */
+    uint16_t *y;                  /* [T,d] out, or NULL */
+    float *rstd;                  /* [T] out, or NULL */
+    uint8_t *q;                   /* out, or NULL */
+    void *scales;                 /* out, or NULL */
+} moe_norm_args;
+moe_status moe_rmsnorm(const moe_norm_args *args, void *stream);
+
+/* Its backward, through y: with vh = x rstd and a = weight dy
+ *   dx       = bf16( d_residual + rstd (a - vh mean_i(a_i vh_i)) )
+ *   d_weight = sum_t dy vh                          (overwritten; zeros for T = 0)
+ * x is the forward's v (residual_out, or x without a residual), rstd the forward's;
+ * d_residual [T,d] bf16 or NULL is the gradient that reaches residual_out past the layer.
+ * dx is the gradient of both x and residual; it may be dy or d_residual.  Workspace:
+ * moe_rmsnorm_bwd_workspace_size(T, d) bytes, 16-byte aligned (0: not supported, or T = 0). */
+typedef struct {
+    int T, d;
+    const uint16_t *x;            /* [T,d] */
+    const float *weight;          /* [d] */
+    const float *rstd;            /* [T] */
+    const uint16_t *dy;           /* [T,d] */
+    const uint16_t *d_residual;   /* [T,d] or NULL */
+    uint16_t *dx;                 /* [T,d] out */
+    float *d_weight;              /* [d] fp32 out */
+    void *ws;
+    size_t ws_bytes;
+} moe_norm_bwd_args;
+size_t moe_rmsnorm_bwd_workspace_size(int T, int d);
+moe_status moe_rmsnorm_backward(const moe_norm_bwd_args *args, void *stream);
+
+/* ------------------------------------------------------------ balance loss
+ * Sequence-wise balance loss of the router, each expert's load, and the gradient at the
+ * gate's logits ([HP41] §01 item 5: balance feedback, text and vision kept apart -- give
+ * each as sequences of its own, or mask the other with `valid`).  For sequence q, the
+ * tokens seq_offsets[q] .. seq_offsets[q+1] - 1, N of them valid:
+ *   counts[q,e] = slots (t,j) of valid tokens with ids[t,j] = e;   tokens[q] = N
+ *   load[q,e]   = E counts[q,e] / (k N)              (a constant of the gradient)
+ *   p[t,e]      = s[t,e] / sum_e s[t,e],  s = sigmoid(logits) or exp(logits)
+ *                 (zeros for a token all of whose logits are -infinity)
+ *   seq_loss[q] = sum_e load[q,e] mean_t p[t,e]      (0 for a sequence without valid tokens)
+ *   loss        = alpha / n_seq sum_q seq_loss[q]
+ *   dlogits[t,j] = dloss alpha / (n_seq N) p_j (load_j - sum_e load_e p_e) (1 - s_j)
+ *                 (softmax: without the last factor); zeros for tokens that are not valid
+ *                 or in no sequence
+ * moe_balance_loss writes counts, tokens, load, seq_loss and loss (dloss and dlogits are
+ * not read); moe_balance_loss_backward reads tokens and load of it and writes dlogits (ids,
+ * counts, seq_loss, loss and ws are not read).
+ * T >= 0, n_seq >= 1, 1 <= E <= 1024, 1 <= k <= 32 (else MOE_ERR_UNSUPPORTED),
+ * (T + n_seq) E < 2^40.  seq_offsets int32 [n_seq+1] on the device, or NULL: one sequence of
+ * all T tokens (n_seq = 1).  Offsets that descend or leave [0, T] are cut to it and recorded
+ * as MOE_ERR_INVALID_ARG on the device, as are ids outside [0, E), which are not counted.
+ * logits and dlogits 16-byte aligned; dlogits may be logits.  Workspace:
+ * moe_balance_workspace_size(T, E, n_seq) bytes, 16-byte aligned (0: not supported). */
+typedef enum { MOE_SCORE_SIGMOID = 0, MOE_SCORE_SOFTMAX = 1 } moe_score;
+typedef struct {
+    int T, E, k, n_seq;
+    int score;                    /* moe_score */
+    float alpha;
+    const float *logits;          /* [T,E] */
+    const int32_t *ids;           /* [T,k] */
+    const int32_t *seq_offsets;   /* [n_seq+1] or NULL */
+    const uint8_t *valid;         /* [T], zero: padding; or NULL (all valid) */
+    int32_t *counts;              /* [n_seq,E] out */
+    int32_t *tokens;              /* [n_seq] out */
+    float *load;                  /* [n_seq,E] out */
+    float *seq_loss;              /* [n_seq] out */
+    float *loss;                  /* [1] out */
+    const float *dloss;           /* [1] gradient of loss, or NULL (1) */
+    float *dlogits;               /* [T,E] out (backward) */
+    void *ws;
+    size_t ws_bytes;
+} moe_balance_args;
+size_t moe_balance_workspace_size(int T, int E, int n_seq);
+moe_status moe_balance_loss(const moe_balance_args *args, void *stream);
+moe_status moe_balance_loss_backward(const moe_balance_args *args, void *stream);
+
 /* Text of a status code (static storage). */
 const char *moe_status_string(moe_status s);
 

@@ -28,6 +28,8 @@ MOE_OK, MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED, MOE_ERR_CUDA, MOE_ERR_TIMEOUT,
     MOE_ERR_WORKSPACE = range(6)
 MOE_ROUTE_TOPK, MOE_ROUTE_HASH = 0, 1
 MOE_FLAG_BACKWARD, MOE_FLAG_RECOMPUTE = 1, 2
+MOE_ROWS_NONE, MOE_ROWS_FP8, MOE_ROWS_MXFP8, MOE_ROWS_MXFP4 = range(4)
+MOE_SCORE_SIGMOID, MOE_SCORE_SOFTMAX = 0, 1
 MOE_PAIR_EXPERT_GEMM1, MOE_PAIR_EXPERT_GEMM2, MOE_PAIR_DGRAD2, MOE_PAIR_DGRAD1, MOE_PAIR_WGRAD = \
     1 << 1, 1 << 2, 1 << 3, 1 << 4, 1 << 5
 MOE_PAIR_ALL = (MOE_PAIR_EXPERT_GEMM1 | MOE_PAIR_EXPERT_GEMM2 | MOE_PAIR_DGRAD2 | MOE_PAIR_DGRAD1
@@ -45,7 +47,11 @@ EXPORTS = ["moe_workspace_size", "moe_route", "moe_route_logits", "moe_gate_rout
            "moe_backward_mx_workspace_size", "moe_backward_mx", "moe_mx_quantize_both",
            "moe_fp8_scale_cols", "moe_fp8_quantize", "moe_fp8_gather", "moe_fp8_quantize_weights",
            "moe_fp8_matmul", "moe_fp8_wgrad_workspace_size", "moe_fp8_wgrad",
-           "moe_expert_ffn_fp8", "moe_few_workspace_size", "moe_layer_few"]
+           "moe_expert_ffn_fp8", "moe_few_workspace_size", "moe_layer_few",
+           "moe_mx4_quantize", "moe_mx4_dequantize", "moe_mx4_gather", "moe_mx4_matmul",
+           "moe_expert_ffn_mx4", "moe_rmsnorm", "moe_rmsnorm_bwd_workspace_size",
+           "moe_rmsnorm_backward", "moe_balance_workspace_size", "moe_balance_loss",
+           "moe_balance_loss_backward"]
 
 
 class MoeError(RuntimeError):
@@ -180,6 +186,27 @@ class FewArgs(ctypes.Structure):
                 ("weights", _P), ("ws", _P), ("ws_bytes", _Z)]
 
 
+class NormArgs(ctypes.Structure):
+    """Mirror of moe_norm_args."""
+    _fields_ = [("T", _I), ("d", _I), ("eps", _F), ("format", _I), ("x", _P), ("residual", _P),
+                ("weight", _P), ("residual_out", _P), ("y", _P), ("rstd", _P), ("q", _P),
+                ("scales", _P)]
+
+
+class NormBwdArgs(ctypes.Structure):
+    """Mirror of moe_norm_bwd_args."""
+    _fields_ = [("T", _I), ("d", _I), ("x", _P), ("weight", _P), ("rstd", _P), ("dy", _P),
+                ("d_residual", _P), ("dx", _P), ("d_weight", _P), ("ws", _P), ("ws_bytes", _Z)]
+
+
+class BalanceArgs(ctypes.Structure):
+    """Mirror of moe_balance_args."""
+    _fields_ = [("T", _I), ("E", _I), ("k", _I), ("n_seq", _I), ("score", _I), ("alpha", _F),
+                ("logits", _P), ("ids", _P), ("seq_offsets", _P), ("valid", _P), ("counts", _P),
+                ("tokens", _P), ("load", _P), ("seq_loss", _P), ("loss", _P), ("dloss", _P),
+                ("dlogits", _P), ("ws", _P), ("ws_bytes", _Z)]
+
+
 MOE_BWD_STAGE_NAMES = ["recompute_gather", "recompute_gemm1", "gather_dY", "dgrad2", "wgrad2",
                        "dgrad1", "wgrad1", "router_bwd", "dX", "dW_g"]
 MOE_BWD_STAGES = len(MOE_BWD_STAGE_NAMES)
@@ -240,6 +267,18 @@ _SIGS = {
                             _P], _I),
     "moe_few_workspace_size": ([_I, _I, _I, _I, _I], _Z),
     "moe_layer_few": ([ctypes.POINTER(FewArgs), _P], _I),
+    "moe_mx4_quantize": ([_P, _LL, _I, _P, _P, _P], _I),
+    "moe_mx4_dequantize": ([_P, _P, _LL, _I, _P, _P], _I),
+    "moe_mx4_gather": ([_P, _P, _I, _I, _I, _P, _P, _P], _I),
+    "moe_mx4_matmul": ([_P, _P, _I, _P, _I, _I, _P, _P, _P, _I, _I, _I, _P, _P], _I),
+    "moe_expert_ffn_mx4": ([_P, _P, _P, _I, _I, _P, _P, _P, _P, _P, _I, _I, _I, _F, _P, _P, _P,
+                            _P], _I),
+    "moe_rmsnorm": ([ctypes.POINTER(NormArgs), _P], _I),
+    "moe_rmsnorm_bwd_workspace_size": ([_I, _I], _Z),
+    "moe_rmsnorm_backward": ([ctypes.POINTER(NormBwdArgs), _P], _I),
+    "moe_balance_workspace_size": ([_I, _I, _I], _Z),
+    "moe_balance_loss": ([ctypes.POINTER(BalanceArgs), _P], _I),
+    "moe_balance_loss_backward": ([ctypes.POINTER(BalanceArgs), _P], _I),
     "moe_expert_gemm2_mx": ([_P, _P, _P, _I, _I, _P, _P, _P, _I, _I, _I, _P, _P], _I),
 }
 
@@ -791,3 +830,106 @@ def moe_layer_few(args: dict, stream=None):
     a = FewArgs(*vals, 0 if ws is None else ws.numel())
     st = load().moe_layer_few(ctypes.byref(a), _stream(stream))
     _check("moe_layer_few", st)
+
+
+# ------------------------------------------------------------------- MXFP4
+
+def moe_mx4_quantize(src, rows, K, q, sf, stream=None):
+    st = load().moe_mx4_quantize(_ptr(src, BF16, "src"), int(rows), int(K), _ptr(q, U8, "q"),
+                                 _ptr(sf, U8, "sf"), _stream(stream))
+    _check("moe_mx4_quantize", st)
+
+
+def moe_mx4_dequantize(q, sf, rows, K, out, stream=None):
+    st = load().moe_mx4_dequantize(_ptr(q, U8, "q"), _ptr(sf, U8, "sf"), int(rows), int(K),
+                                   _ptr(out, BF16, "out"), _stream(stream))
+    _check("moe_mx4_dequantize", st)
+
+
+def moe_mx4_gather(x, slot_row, T, d, k, x_perm_q, x_perm_sf, stream=None):
+    st = load().moe_mx4_gather(_ptr(x, BF16, "x"), _ptr(slot_row, I32, "slot_row"), T, d, k,
+                               _ptr(x_perm_q, U8, "x_perm_q"), _ptr(x_perm_sf, U8, "x_perm_sf"),
+                               _stream(stream))
+    _check("moe_mx4_gather", st)
+
+
+def moe_mx4_matmul(a_q, a_sf, a_bits, offsets, G, max_rows, b_q, b_sf, row_weight, w_rows, N, K,
+                   out, stream=None):
+    st = load().moe_mx4_matmul(_ptr(a_q, U8, "a_q"), _ptr(a_sf, U8, "a_sf"), a_bits,
+                               _ptr(offsets, I32, "offsets"), G, max_rows, _ptr(b_q, U8, "b_q"),
+                               _ptr(b_sf, U8, "b_sf"), _ptr(row_weight, F32, "row_weight"),
+                               w_rows, N, K, _ptr(out, BF16, "out"), _stream(stream))
+    _check("moe_mx4_matmul", st)
+
+
+def moe_expert_ffn_mx4(x_perm_q, x_perm_sf, offsets, G, max_rows, W13_q, W13_sf, W2_q, W2_sf,
+                       row_weight, S, d, I, clamp, h_q, h_sf, y_perm, stream=None):
+    st = load().moe_expert_ffn_mx4(_ptr(x_perm_q, U8, "x_perm_q"), _ptr(x_perm_sf, U8, "x_perm_sf"),
+                                   _ptr(offsets, I32, "offsets"), G, max_rows,
+                                   _ptr(W13_q, U8, "W13_q"), _ptr(W13_sf, U8, "W13_sf"),
+                                   _ptr(W2_q, U8, "W2_q"), _ptr(W2_sf, U8, "W2_sf"),
+                                   _ptr(row_weight, F32, "row_weight"), S, d, I, float(clamp),
+                                   _ptr(h_q, U8, "h_q"), _ptr(h_sf, U8, "h_sf"),
+                                   _ptr(y_perm, BF16, "y_perm"), _stream(stream))
+    _check("moe_expert_ffn_mx4", st)
+
+
+# ------------------------------------- calls that take their fields as a dict
+
+def _fields(struct, **types):
+    """(name, dtype or None) of a struct's fields; ws_bytes, where there is one, comes last."""
+    return [(n, types.get(n)) for n, _ in struct._fields_ if n != "ws_bytes"]
+
+
+def _struct(struct, fields, args):
+    vals = []
+    for name, dtype in fields:
+        v = args.get(name)
+        vals.append(_ptr(v, dtype, name) if dtype is not None else 0 if v is None else v)
+    if struct._fields_[-1][0] == "ws_bytes":
+        ws = args.get("ws")
+        vals.append(0 if ws is None else ws.numel())
+    return struct(*vals)
+
+
+_NORM = _fields(NormArgs, x=BF16, residual=BF16, weight=F32, residual_out=BF16, y=BF16, rstd=F32,
+                q=U8)[:-1]
+_NORM_BWD = _fields(NormBwdArgs, x=BF16, weight=F32, rstd=F32, dy=BF16, d_residual=BF16, dx=BF16,
+                    d_weight=F32, ws=U8)
+_BALANCE = _fields(BalanceArgs, logits=F32, ids=I32, seq_offsets=I32, valid=U8, counts=I32,
+                   tokens=I32, load=F32, seq_loss=F32, loss=F32, dloss=F32, dlogits=F32, ws=U8)
+
+
+def moe_rmsnorm(args: dict, stream=None):
+    """args: the fields of moe_norm_args (tensors for pointers, None for NULL); scales is
+    fp32 with MOE_ROWS_FP8 and uint8 with the MX formats."""
+    a = _struct(NormArgs, _NORM, args)
+    a.scales = _ptr(args.get("scales"), F32 if a.format == MOE_ROWS_FP8 else U8, "scales")
+    _check("moe_rmsnorm", load().moe_rmsnorm(ctypes.byref(a), _stream(stream)))
+
+
+def moe_rmsnorm_bwd_workspace_size(T, d) -> int:
+    return int(load().moe_rmsnorm_bwd_workspace_size(T, d))
+
+
+def moe_rmsnorm_backward(args: dict, stream=None):
+    """args: the fields of moe_norm_bwd_args."""
+    a = _struct(NormBwdArgs, _NORM_BWD, args)
+    _check("moe_rmsnorm_backward", load().moe_rmsnorm_backward(ctypes.byref(a), _stream(stream)))
+
+
+def moe_balance_workspace_size(T, E, n_seq=1) -> int:
+    return int(load().moe_balance_workspace_size(T, E, n_seq))
+
+
+def moe_balance_loss(args: dict, stream=None):
+    """args: the fields of moe_balance_args."""
+    a = _struct(BalanceArgs, _BALANCE, args)
+    _check("moe_balance_loss", load().moe_balance_loss(ctypes.byref(a), _stream(stream)))
+
+
+def moe_balance_loss_backward(args: dict, stream=None):
+    """args: the fields of moe_balance_args (of the forward)."""
+    a = _struct(BalanceArgs, _BALANCE, args)
+    _check("moe_balance_loss_backward",
+           load().moe_balance_loss_backward(ctypes.byref(a), _stream(stream)))

@@ -330,6 +330,13 @@ bool encode_tmap_u8_2d(CUtensorMap *tm, const void *base, uint64_t inner, uint64
                      box_inner, box_outer, swz);
 }
 
+bool encode_tmap_u4_expand_2d(CUtensorMap *tm, const void *base, uint64_t inner, uint64_t outer,
+                              uint32_t box_outer) {
+    if (inner % 128 != 0 || (reinterpret_cast<uintptr_t>(base) & 31u) != 0) return false;
+    return encode_2d(tm, CU_TENSOR_MAP_DATA_TYPE_16U4_ALIGN16B, base, inner, outer, inner / 2, 128,
+                     box_outer, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
 bool encode_tmap_u8_3d_sw128(CUtensorMap *tm, const void *base, uint64_t n0, uint64_t n1,
                              uint64_t n2, uint64_t pitch1, uint64_t pitch2, uint32_t b0,
                              uint32_t b1, uint32_t b2) {
@@ -1352,6 +1359,153 @@ moe_status moe_expert_ffn_fp8(const uint8_t *x_perm_q, const float *x_perm_s,
     if (r != MOE_OK) return r;
     return launch_fp8_matmul(h_q, h_s, offsets, G, max_rows, W2_q, W2_s, row_weight, S, d, I,
                              y_perm, st);
+}
+
+moe_status moe_mx4_quantize(const uint16_t *src, long long rows, int K, uint8_t *q, uint8_t *sf,
+                            void *stream) {
+    if (rows < 0 || K < 32 || K % 32 != 0) return MOE_ERR_INVALID_ARG;
+    if (rows == 0) return MOE_OK;
+    if (rows > (1LL << 40) / K) return MOE_ERR_UNSUPPORTED;
+    if (!all_aligned16({src, q, sf})) return MOE_ERR_INVALID_ARG;
+    return launch_mx4_quantize(src, rows, K, q, sf, static_cast<cudaStream_t>(stream));
+}
+
+moe_status moe_mx4_dequantize(const uint8_t *q, const uint8_t *sf, long long rows, int K,
+                              uint16_t *out, void *stream) {
+    if (rows < 0 || K < 32 || K % 32 != 0) return MOE_ERR_INVALID_ARG;
+    if (rows == 0) return MOE_OK;
+    if (rows > (1LL << 40) / K) return MOE_ERR_UNSUPPORTED;
+    if (!all_aligned16({q, sf, out})) return MOE_ERR_INVALID_ARG;
+    return launch_mx4_dequantize(q, sf, rows, K, out, static_cast<cudaStream_t>(stream));
+}
+
+moe_status moe_mx4_gather(const uint16_t *x, const int32_t *slot_row, int T, int d, int k,
+                          uint8_t *x_perm_q, uint8_t *x_perm_sf, void *stream) {
+    if (T < 1 || d < 32 || d % 32 != 0 || k < 1 || k > 32) return MOE_ERR_INVALID_ARG;
+    if ((long long)T * (k + 1) >= (1LL << 31) || (long long)T * (k + 1) > (1LL << 40) / d)
+        return MOE_ERR_UNSUPPORTED;
+    if (!slot_row || !all_aligned16({x, x_perm_q, x_perm_sf})) return MOE_ERR_INVALID_ARG;
+    return launch_mx4_gather(x, slot_row, T, d, k, x_perm_q, x_perm_sf,
+                             static_cast<cudaStream_t>(stream));
+}
+
+static bool aligned32(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 31u) == 0; }
+
+moe_status moe_mx4_matmul(const uint8_t *a_q, const uint8_t *a_sf, int a_bits,
+                          const int32_t *offsets, int G, int max_rows, const uint8_t *b_q,
+                          const uint8_t *b_sf, const float *row_weight, int w_rows, int N, int K,
+                          uint16_t *out, void *stream) {
+    if (!fp8_groups_ok(G, max_rows) || N < 8 || N % 8 != 0 || K < 32 || K % 32 != 0 ||
+        w_rows < 0 || (a_bits != 4 && a_bits != 8))
+        return MOE_ERR_INVALID_ARG;
+    if ((long long)G * N >= (1LL << 31) || (a_bits == 8 && K % 128 != 0))
+        return MOE_ERR_UNSUPPORTED;
+    if (!offsets || !all_aligned16({a_q, a_sf, b_q, b_sf, out}) || (a_bits == 8 && !aligned32(b_q)))
+        return MOE_ERR_INVALID_ARG;
+    if (max_rows == 0) return MOE_OK;
+    return launch_mx4_matmul(a_q, a_sf, a_bits, offsets, G, max_rows, b_q, b_sf, row_weight,
+                             w_rows, N, K, out, static_cast<cudaStream_t>(stream));
+}
+
+moe_status moe_expert_ffn_mx4(const uint8_t *x_perm_q, const uint8_t *x_perm_sf,
+                              const int32_t *offsets, int G, int max_rows, const uint8_t *W13_q,
+                              const uint8_t *W13_sf, const uint8_t *W2_q, const uint8_t *W2_sf,
+                              const float *row_weight, int S, int d, int I, float clamp,
+                              uint8_t *h_q, uint8_t *h_sf, uint16_t *y_perm, void *stream) {
+    if (!fp8_groups_ok(G, max_rows) || d < 1 || I < 1 || S < 0) return MOE_ERR_INVALID_ARG;
+    if (d % 128 != 0 || I % 128 != 0 || (long long)G * (2LL * I > d ? 2LL * I : d) >= (1LL << 31))
+        return MOE_ERR_UNSUPPORTED;
+    if (!offsets || !(clamp > 0.0f) || !aligned32(W13_q) || !aligned32(W2_q) ||
+        !all_aligned16({x_perm_q, x_perm_sf, W13_q, W13_sf, W2_q, W2_sf, h_q, h_sf, y_perm}))
+        return MOE_ERR_INVALID_ARG;
+    if (max_rows == 0) return MOE_OK;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    moe_status r = launch_mx4_ffn1(x_perm_q, x_perm_sf, offsets, G, max_rows, W13_q, W13_sf, d, I,
+                                   clamp, h_q, h_sf, st);
+    if (r != MOE_OK) return r;
+    return launch_mx4_matmul(h_q, h_sf, 8, offsets, G, max_rows, W2_q, W2_sf, row_weight, S, d, I,
+                             y_perm, st);
+}
+
+moe_status moe_rmsnorm(const moe_norm_args *a, void *stream) {
+    if (!a || a->T < 0 || a->d < 8 || a->d % 8 != 0 || !(a->eps > 0.0f) || !(a->eps < 1e30f))
+        return MOE_ERR_INVALID_ARG;
+    const bool coded = a->format != MOE_ROWS_NONE;
+    if (a->format < MOE_ROWS_NONE || a->format > MOE_ROWS_MXFP4 ||
+        a->d % (a->format == MOE_ROWS_FP8 ? 16 : coded ? 32 : 8) != 0)
+        return MOE_ERR_INVALID_ARG;
+    if (a->d > 32768) return MOE_ERR_UNSUPPORTED;
+    if ((a->residual == nullptr) != (a->residual_out == nullptr) || (a->q != nullptr) != coded ||
+        (a->scales != nullptr) != coded)
+        return MOE_ERR_INVALID_ARG;
+    if (a->T == 0) return MOE_OK;
+    if (!all_aligned16({a->x, a->weight}) || !aligned16(a->residual) ||
+        !aligned16(a->residual_out) || !aligned16(a->y) || !aligned16(a->q) ||
+        !aligned16(a->scales))
+        return MOE_ERR_INVALID_ARG;
+    return launch_rmsnorm(a, static_cast<cudaStream_t>(stream));
+}
+
+static bool norm_bwd_ok(int T, int d) { return T >= 0 && d >= 8 && d % 8 == 0 && d <= 32768; }
+
+size_t moe_rmsnorm_bwd_workspace_size(int T, int d) {
+    return norm_bwd_ok(T, d) ? rmsnorm_bwd_workspace_bytes(T, d) : 0;
+}
+
+moe_status moe_rmsnorm_backward(const moe_norm_bwd_args *a, void *stream) {
+    if (!a || a->T < 0 || a->d < 8 || a->d % 8 != 0) return MOE_ERR_INVALID_ARG;
+    if (!norm_bwd_ok(a->T, a->d)) return MOE_ERR_UNSUPPORTED;
+    if (!all_aligned16({a->d_weight})) return MOE_ERR_INVALID_ARG;
+    if (a->T > 0) {
+        if (!all_aligned16({a->x, a->weight, a->dy, a->dx}) || !a->rstd ||
+            !aligned16(a->d_residual))
+            return MOE_ERR_INVALID_ARG;
+        if (!a->ws || !aligned16(a->ws) || a->ws_bytes < rmsnorm_bwd_workspace_bytes(a->T, a->d))
+            return MOE_ERR_WORKSPACE;
+    }
+    return launch_rmsnorm_bwd(a, static_cast<cudaStream_t>(stream));
+}
+
+// Shapes of the balance loss: MOE_OK, or why not.
+static moe_status balance_shape(int T, int E, int k, int n_seq) {
+    if (T < 0 || E < 1 || k < 1 || n_seq < 1) return MOE_ERR_INVALID_ARG;
+    if (E > 1024 || k > 32 || ((long long)T + n_seq) * E >= (1LL << 40))
+        return MOE_ERR_UNSUPPORTED;
+    return MOE_OK;
+}
+
+static moe_status balance_check(const moe_balance_args *a) {
+    if (!a) return MOE_ERR_INVALID_ARG;
+    const moe_status s = balance_shape(a->T, a->E, a->k, a->n_seq);
+    if (s != MOE_OK) return s;
+    if ((a->score != MOE_SCORE_SIGMOID && a->score != MOE_SCORE_SOFTMAX) ||
+        (!a->seq_offsets && a->n_seq != 1) || !a->tokens || !a->load || !aligned16(a->load))
+        return MOE_ERR_INVALID_ARG;
+    if (a->T > 0 && !all_aligned16({a->logits})) return MOE_ERR_INVALID_ARG;
+    return MOE_OK;
+}
+
+size_t moe_balance_workspace_size(int T, int E, int n_seq) {
+    return balance_shape(T, E, 1, n_seq) == MOE_OK ? balance_workspace_bytes(T, E, n_seq) : 0;
+}
+
+moe_status moe_balance_loss(const moe_balance_args *a, void *stream) {
+    const moe_status s = balance_check(a);
+    if (s != MOE_OK) return s;
+    if (!a->counts || !a->seq_loss || !a->loss || (a->T > 0 && !a->ids))
+        return MOE_ERR_INVALID_ARG;
+    if (!a->ws || !aligned16(a->ws) ||
+        a->ws_bytes < balance_workspace_bytes(a->T, a->E, a->n_seq))
+        return MOE_ERR_WORKSPACE;
+    return launch_balance(a, static_cast<cudaStream_t>(stream));
+}
+
+moe_status moe_balance_loss_backward(const moe_balance_args *a, void *stream) {
+    const moe_status s = balance_check(a);
+    if (s != MOE_OK) return s;
+    if (a->T == 0) return MOE_OK;
+    if (!all_aligned16({a->dlogits})) return MOE_ERR_INVALID_ARG;
+    return launch_balance_bwd(a, static_cast<cudaStream_t>(stream));
 }
 
 size_t moe_few_workspace_size(int T, int d, int E, int k, int I) {

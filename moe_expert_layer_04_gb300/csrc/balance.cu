@@ -1,0 +1,421 @@
+// balance.cu -- the balance loss of the router with each expert's load, and its
+// gradient at the gate's logits.
+//
+// For sequence q with N valid tokens (f is a constant of the gradient, as is usual):
+//   count[e] = slots of the valid tokens that chose e,  f[e] = E count[e] / (k N)
+//   s = sigmoid(z) or exp(z - max z),  p = s / sum_e s  (zeros where the sum is zero)
+//   seq_loss = sum_e f[e] mean_t p[t, e],  loss = alpha / n_seq sum_q seq_loss
+//   dz[t, j] = dloss alpha / (n_seq N) p_j (f_j - sum_e f_e p_e) (1 - s_j for sigmoid)
+// (Text and vision, or any other share of the tokens, are balanced apart by giving each
+// as sequences of its own: "HyperParallel加速DeepSeek-V4.1多模态1M长序列训练" §01 item 5.)
+//
+// Sums are fp32 within a chunk of tokens and fp64 over the chunks, in a fixed order, so
+// that results do not depend on the schedule.  Bound by HBM: the logits are read once in
+// each direction, and their gradient is written once.
+#include <cstring>
+
+#include "fp8_common.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int kWarps = 8;
+
+struct BalanceParams {
+    int T, E, k, n_seq, chunk, n_chunks;
+    float alpha;
+    const float *logits;
+    const int32_t *ids, *seq_offsets;
+    const uint8_t *valid;
+    int32_t *counts, *tokens;
+    float *load, *seq_loss, *loss;
+    const float *dloss;
+    float *dlogits;
+    // partial sums: one slot for each (chunk, sequence) that meet, at chunk + sequence,
+    // which is another number for every such pair
+    float *part_p;     // [slots, E]
+    int32_t *part_c;   // [slots, E]
+    int32_t *part_n;   // [slots]
+    int *status;
+};
+
+__device__ __forceinline__ int seq_begin(const BalanceParams &p, int q) {
+    return p.seq_offsets ? min(max(__ldg(p.seq_offsets + q), 0), p.T) : q == 0 ? 0 : p.T;
+}
+
+// The first sequence that ends behind token t (n_seq: none).
+__device__ __forceinline__ int first_seq(const BalanceParams &p, int t) {
+    int lo = 0, hi = p.n_seq;
+    while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (seq_begin(p, mid + 1) <= t) lo = mid + 1; else hi = mid;
+    }
+    return lo;
+}
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+
+// A lane's columns: VEC consecutive ones from VEC (lane + 32 i), i < N.
+template <int VEC, int N>
+struct Row {
+    float z[N][VEC];
+
+    __device__ __forceinline__ void load(const float *src, int E) {
+        const int lane = threadIdx.x & 31;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int c = VEC * (lane + 32 * i);
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) z[i][j] = -INFINITY;
+            if (c < E) {
+                if constexpr (VEC == 4) {
+                    const float4 v = __ldg(reinterpret_cast<const float4 *>(src + c));
+                    z[i][0] = v.x;
+                    z[i][1] = v.y;
+                    z[i][2] = v.z;
+                    z[i][3] = v.w;
+                } else {
+                    z[i][0] = __ldg(src + c);
+                }
+            }
+        }
+    }
+};
+
+// z -> p (columns outside E: zeros); slope = 1 - s for the sigmoid, 1 otherwise.
+template <bool SOFTMAX, int VEC, int N>
+__device__ __forceinline__ void shares(const Row<VEC, N> &r, float (&p)[N][VEC],
+                                       float (&slope)[N][VEC]) {
+    float sum = 0.0f;
+    if constexpr (SOFTMAX) {
+        float m = -INFINITY;   // (a NaN makes the sum one)
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) m = fmaxf(m, r.z[i][j]);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        if (m == -INFINITY) m = 0.0f;   // nothing is left: every term is zero
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) {
+                p[i][j] = __expf(r.z[i][j] - m);
+                slope[i][j] = 1.0f;
+                sum += p[i][j];
+            }
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) {
+                // both s and 1 - s without cancellation or overflow
+                const float z = r.z[i][j], t = __expf(-fabsf(z));
+                const float big = __fdividef(1.0f, 1.0f + t), small = t * big;
+                p[i][j] = z < 0.0f ? small : big;
+                slope[i][j] = z < 0.0f ? big : small;
+                sum += p[i][j];
+            }
+    }
+    sum = warp_sum(sum);
+    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) p[i][j] *= inv;
+}
+
+// CTA: one chunk of tokens, sequence by sequence; its warps take tokens in turn, a lane
+// sums its columns' shares in registers.
+template <bool SOFTMAX, int VEC, int N>
+__global__ void __launch_bounds__(32 * kWarps) balance_part_kernel(const BalanceParams p) {
+    extern __shared__ float sm[];   // [kWarps, E] shares, [E] counts
+    __shared__ int n_valid;
+    wait_for_kernels_ahead();
+    let_kernels_behind_begin();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int32_t *hist = reinterpret_cast<int32_t *>(sm + kWarps * p.E);
+    if (blockIdx.x == 0 && p.seq_offsets) {
+        for (int q = threadIdx.x; q <= p.n_seq; q += blockDim.x) {
+            const int o = p.seq_offsets[q];
+            if (o < 0 || o > p.T || (q > 0 && p.seq_offsets[q - 1] > o))
+                record_status(p.status, MOE_ERR_INVALID_ARG);
+        }
+    }
+    const int end = min(p.T, (int)(blockIdx.x + 1) * p.chunk);
+    int a = blockIdx.x * p.chunk;
+    for (int q = first_seq(p, a); q < p.n_seq && a < end; ++q) {
+        const int b = min(end, seq_begin(p, q + 1));
+        a = max(a, seq_begin(p, q));
+        if (a >= b) continue;
+        __syncthreads();   // the last sequence's sums have been read
+        for (int e = threadIdx.x; e < p.E; e += blockDim.x) hist[e] = 0;
+        if (threadIdx.x == 0) n_valid = 0;
+        __syncthreads();
+        float acc[N][VEC] = {};
+        int n = 0;
+        for (int t = a + warp; t < b; t += kWarps) {
+            if (p.valid && !__ldg(p.valid + t)) continue;
+            ++n;
+            Row<VEC, N> r;
+            r.load(p.logits + (size_t)t * p.E, p.E);
+            float s[N][VEC], slope[N][VEC];
+            shares<SOFTMAX>(r, s, slope);
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+#pragma unroll
+                for (int j = 0; j < VEC; ++j) acc[i][j] += s[i][j];
+            if (lane < p.k) {
+                const int e = __ldg(p.ids + (size_t)t * p.k + lane);
+                if ((unsigned)e < (unsigned)p.E) atomicAdd(hist + e, 1);
+                else record_status(p.status, MOE_ERR_INVALID_ARG);
+            }
+        }
+        if (lane == 0 && n) atomicAdd(&n_valid, n);
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) {
+                const int c = VEC * (lane + 32 * i) + j;
+                if (c < p.E) sm[warp * p.E + c] = acc[i][j];
+            }
+        __syncthreads();
+        const size_t slot = (size_t)blockIdx.x + q;
+        for (int e = threadIdx.x; e < p.E; e += blockDim.x) {
+            float s = 0.0f;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) s += sm[w * p.E + e];
+            p.part_p[slot * p.E + e] = s;
+            p.part_c[slot * p.E + e] = hist[e];
+        }
+        if (threadIdx.x == 0) p.part_n[slot] = n_valid;
+        a = b;
+    }
+}
+
+// One CTA for each sequence: its slots in order.
+__global__ void __launch_bounds__(1024) balance_seq_kernel(const BalanceParams p) {
+    __shared__ double term[32];
+    __shared__ int n_all;
+    wait_for_kernels_ahead();
+    let_kernels_behind_begin();
+    const int q = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int a = seq_begin(p, q), b = seq_begin(p, q + 1);
+    const int c0 = a / p.chunk, c1 = b > a ? (b - 1) / p.chunk : c0 - 1;
+    if (threadIdx.x == 0) n_all = 0;
+    __syncthreads();
+    int n = 0;
+    for (int c = c0 + threadIdx.x; c <= c1; c += blockDim.x) n += p.part_n[c + q];
+    if (n) atomicAdd(&n_all, n);
+    __syncthreads();
+    n = n_all;
+    double mine = 0.0;
+    for (int e = threadIdx.x; e < p.E; e += blockDim.x) {
+        double s = 0.0;
+        int cnt = 0;
+        for (int c = c0; c <= c1; ++c) {
+            s += p.part_p[(size_t)(c + q) * p.E + e];
+            cnt += p.part_c[(size_t)(c + q) * p.E + e];
+        }
+        const float f = n ? (float)((double)cnt * p.E / ((double)p.k * n)) : 0.0f;
+        p.counts[(size_t)q * p.E + e] = cnt;
+        p.load[(size_t)q * p.E + e] = f;
+        if (n) mine += f * (s / n);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
+    if (lane == 0) term[warp] = mine;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        double s = 0.0;
+        for (int w = 0; w < (int)(blockDim.x >> 5); ++w) s += term[w];
+        p.seq_loss[q] = (float)s;
+        p.tokens[q] = n;
+        if (p.n_seq == 1) p.loss[0] = (float)(p.alpha * s);
+    }
+}
+
+// The mean of the sequences' losses; one warp.
+__global__ void balance_loss_kernel(const BalanceParams p) {
+    wait_for_kernels_ahead();
+    let_kernels_behind_begin();
+    double s = 0.0;
+    for (int q = threadIdx.x; q < p.n_seq; q += 32) s += p.seq_loss[q];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if (threadIdx.x == 0) p.loss[0] = (float)(p.alpha * s / p.n_seq);
+}
+
+// A warp takes `chunk` consecutive tokens; a sequence's load stays in its registers.
+template <bool SOFTMAX, int VEC, int N>
+__global__ void __launch_bounds__(32 * kWarps) balance_bwd_kernel(const BalanceParams p) {
+    wait_for_kernels_ahead();
+    let_kernels_behind_begin();
+    const int lane = threadIdx.x & 31;
+    const long long first =
+        ((long long)blockIdx.x * kWarps + (threadIdx.x >> 5)) * p.chunk;
+    if (first >= p.T) return;
+    const int a = (int)first, b = (int)min((long long)p.T, first + p.chunk);
+    int q = first_seq(p, a);
+    int begin = q < p.n_seq ? seq_begin(p, q) : p.T;
+    int end = q < p.n_seq ? seq_begin(p, q + 1) : p.T;
+    const float g = (p.dloss ? __ldg(p.dloss) : 1.0f) * p.alpha;
+    float f[N][VEC], coef = 0.0f;
+    bool loaded = false;
+    for (int t = a; t < b; ++t) {
+        while (q < p.n_seq && t >= end) {
+            ++q;
+            loaded = false;
+            begin = q < p.n_seq ? seq_begin(p, q) : p.T;
+            end = q < p.n_seq ? seq_begin(p, q + 1) : p.T;
+        }
+        float *dst = p.dlogits + (size_t)t * p.E;
+        const bool live = q < p.n_seq && t >= begin && (!p.valid || __ldg(p.valid + t));
+        float out[N][VEC] = {};
+        if (live) {
+            if (!loaded) {
+                Row<VEC, N> l;
+                l.load(p.load + (size_t)q * p.E, p.E);
+#pragma unroll
+                for (int i = 0; i < N; ++i)
+#pragma unroll
+                    for (int j = 0; j < VEC; ++j)
+                        f[i][j] = VEC * (lane + 32 * i) + j < p.E ? l.z[i][j] : 0.0f;
+                coef = g / ((float)p.n_seq * (float)max(1, __ldg(p.tokens + q)));
+                loaded = true;
+            }
+            Row<VEC, N> r;
+            r.load(p.logits + (size_t)t * p.E, p.E);
+            float s[N][VEC], slope[N][VEC];
+            shares<SOFTMAX>(r, s, slope);
+            float dot = 0.0f;
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+#pragma unroll
+                for (int j = 0; j < VEC; ++j) dot = fmaf(f[i][j], s[i][j], dot);
+            dot = warp_sum(dot);
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+#pragma unroll
+                for (int j = 0; j < VEC; ++j)
+                    out[i][j] = coef * (s[i][j] * (f[i][j] - dot) * slope[i][j]);
+        }
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int c = VEC * (lane + 32 * i);
+            if (c >= p.E) continue;
+            if constexpr (VEC == 4)
+                *reinterpret_cast<float4 *>(dst + c) =
+                    make_float4(out[i][0], out[i][1], out[i][2], out[i][3]);
+            else
+                dst[c] = out[i][0];
+        }
+    }
+}
+
+// Tokens of a chunk: four CTAs an SM, at least a token for each warp.
+int part_chunk(int T) {
+    const int c = (int)(((long long)T + 4LL * num_sms() - 1) / (4LL * num_sms()));
+    return c < 2 * kWarps ? 2 * kWarps : c;
+}
+
+BalanceParams params(const moe_balance_args *a) {
+    BalanceParams p;
+    std::memset(&p, 0, sizeof p);
+    p.T = a->T;
+    p.E = a->E;
+    p.k = a->k;
+    p.n_seq = a->n_seq;
+    p.alpha = a->alpha;
+    p.logits = a->logits;
+    p.ids = a->ids;
+    p.seq_offsets = a->seq_offsets;
+    p.valid = a->valid;
+    p.counts = a->counts;
+    p.tokens = a->tokens;
+    p.load = a->load;
+    p.seq_loss = a->seq_loss;
+    p.loss = a->loss;
+    p.dloss = a->dloss;
+    p.dlogits = a->dlogits;
+    return p;
+}
+
+// Instances by the columns of a lane: four at a time where rows are whole 16 bytes.
+template <template <bool, int, int> class L>
+moe_status by_columns(const moe_balance_args *a, const BalanceParams &p, cudaStream_t st) {
+    const bool soft = a->score == MOE_SCORE_SOFTMAX;
+    const int E = a->E;
+#define MOE_BALANCE(V, N) return soft ? L<true, V, N>::go(p, st) : L<false, V, N>::go(p, st)
+    if (E % 4 == 0) {
+        if (E <= 128) MOE_BALANCE(4, 1);
+        if (E <= 256) MOE_BALANCE(4, 2);
+        if (E <= 384) MOE_BALANCE(4, 3);
+        if (E <= 512) MOE_BALANCE(4, 4);
+        MOE_BALANCE(4, 8);
+    }
+    if (E <= 32) MOE_BALANCE(1, 1);
+    if (E <= 128) MOE_BALANCE(1, 4);
+    if (E <= 256) MOE_BALANCE(1, 8);
+    if (E <= 512) MOE_BALANCE(1, 16);
+    MOE_BALANCE(1, 32);
+#undef MOE_BALANCE
+}
+
+template <bool S, int V, int N>
+struct PartLaunch {
+    static moe_status go(const BalanceParams &p, cudaStream_t st) {
+        return launch_early(balance_part_kernel<S, V, N>, dim3(p.n_chunks), 32 * kWarps,
+                            (kWarps + 1) * p.E * 4, st, p);
+    }
+};
+template <bool S, int V, int N>
+struct BwdLaunch {
+    static moe_status go(const BalanceParams &p, cudaStream_t st) {
+        const long long ctas = ((long long)p.T + (long long)p.chunk * kWarps - 1) /
+                               ((long long)p.chunk * kWarps);
+        return launch_early(balance_bwd_kernel<S, V, N>, dim3((unsigned)ctas), 32 * kWarps, 0, st,
+                            p);
+    }
+};
+
+}  // namespace
+
+size_t balance_workspace_bytes(int T, int E, int n_seq) {
+    const int C = part_chunk(T);
+    const size_t slots = (size_t)((T + C - 1) / C) + n_seq;
+    return slots * E * 8 + slots * 4;
+}
+
+moe_status launch_balance(const moe_balance_args *a, cudaStream_t st) {
+    BalanceParams p = params(a);
+    p.status = device_status_ptr();
+    if (!p.status) return MOE_ERR_CUDA;
+    p.chunk = part_chunk(a->T);
+    p.n_chunks = (a->T + p.chunk - 1) / p.chunk;
+    const size_t slots = (size_t)p.n_chunks + a->n_seq;
+    p.part_p = static_cast<float *>(a->ws);
+    p.part_c = reinterpret_cast<int32_t *>(p.part_p + slots * a->E);
+    p.part_n = p.part_c + slots * a->E;
+    if (p.n_chunks > 0) {
+        const moe_status s = by_columns<PartLaunch>(a, p, st);
+        if (s != MOE_OK) return s;
+    }
+    const int threads = a->E < 1024 ? (a->E + 31) / 32 * 32 : 1024;
+    const moe_status s = launch_early(balance_seq_kernel, dim3(a->n_seq), threads, 0, st, p);
+    if (s != MOE_OK || a->n_seq == 1) return s;
+    return launch_early(balance_loss_kernel, dim3(1), 32, 0, st, p);
+}
+
+moe_status launch_balance_bwd(const moe_balance_args *a, cudaStream_t st) {
+    BalanceParams p = params(a);
+    const long long warps = (long long)num_sms() * 4 * kWarps;
+    p.chunk = (int)(((long long)a->T + warps - 1) / warps);
+    return by_columns<BwdLaunch>(a, p, st);
+}
+
+}  // namespace moe

@@ -46,6 +46,12 @@ bool encode_tmap_u8_3d_sw128(CUtensorMap *tm, const void *base, uint64_t n0, uin
                              uint64_t n2, uint64_t pitch1, uint64_t pitch2, uint32_t b0,
                              uint32_t b1, uint32_t b2);
 
+// MXFP4 codes [outer, inner] (inner elements of 4 bits, a multiple of 128; base and rows
+// 32-byte aligned) copied in boxes of 128 elements x box_outer rows, sixteen elements to
+// eight bytes and eight bytes of padding in shared memory, 128-byte swizzle.
+bool encode_tmap_u4_expand_2d(CUtensorMap *tm, const void *base, uint64_t inner, uint64_t outer,
+                              uint32_t box_outer);
+
 inline moe_status cuda_status(cudaError_t e) { return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA; }
 
 inline bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -179,6 +185,31 @@ moe_status launch_fp8_ffn1(const uint8_t *xq, const float *xs, const int32_t *of
 moe_status launch_fp8_wgrad(const uint8_t *aq, const float *as, const uint8_t *bq, const float *bs,
                             const int32_t *first, int G, int max_chunks, int M, int N, float *dW,
                             cudaStream_t st);
+
+// MXFP4 (mx4.cu, gemm_mx4.cu): quantisation of rows, their values, the quantising
+// dispatch gather; the grouped matmul on rows of `bits` bits (8: K % 128 == 0) and expert
+// GEMM 1 on MXFP8 rows with the SwiGLU.
+moe_status launch_mx4_quantize(const uint16_t *src, long long rows, int K, uint8_t *q, uint8_t *sf,
+                               cudaStream_t st);
+moe_status launch_mx4_dequantize(const uint8_t *q, const uint8_t *sf, long long rows, int K,
+                                 uint16_t *out, cudaStream_t st);
+moe_status launch_mx4_gather(const uint16_t *x, const int32_t *slot_row, int T, int d, int k,
+                             uint8_t *q, uint8_t *sf, cudaStream_t st);
+moe_status launch_mx4_matmul(const uint8_t *aq, const uint8_t *asf, int bits,
+                             const int32_t *offsets, int G, int max_rows, const uint8_t *bq,
+                             const uint8_t *bsf, const float *row_w, int w_rows, int N, int K,
+                             uint16_t *out, cudaStream_t st);
+moe_status launch_mx4_ffn1(const uint8_t *xq, const uint8_t *xsf, const int32_t *offsets, int G,
+                           int max_rows, const uint8_t *W13q, const uint8_t *W13sf, int d, int I,
+                           float clamp, uint8_t *hq, uint8_t *hsf, cudaStream_t st);
+
+// The norm ahead of the layer (norm.cu) and the balance loss (balance.cu).
+moe_status launch_rmsnorm(const moe_norm_args *a, cudaStream_t st);
+size_t rmsnorm_bwd_workspace_bytes(int T, int d);
+moe_status launch_rmsnorm_bwd(const moe_norm_bwd_args *a, cudaStream_t st);
+size_t balance_workspace_bytes(int T, int E, int n_seq);
+moe_status launch_balance(const moe_balance_args *a, cudaStream_t st);
+moe_status launch_balance_bwd(const moe_balance_args *a, cudaStream_t st);
 
 // The whole layer for a few tokens (few.cu).
 bool few_supported(int T, int d, int E, int k, int I);

@@ -1,0 +1,178 @@
+// mx4.cu -- MXFP4 quantisation of bf16 rows (weights, or token rows in place and through
+// the dispatch), and the values of quantised rows in bf16.  Format: mx_common.cuh; codes
+// q [rows, K/2], scales sf [rows, mx_sf_pitch(K)] as for MXFP8.
+//
+// A lane owns eight consecutive elements, 16 bytes of bf16 and a word of codes, four
+// lanes a block: every load and store of a warp is contiguous, and a block's largest
+// magnitude is two shuffles away.  All loads of a lane are issued before the first use.
+// Bound by HBM: 2 bytes read, 1/2 + 1/32 written an element, and the reverse.
+#include "fp8_common.cuh"
+#include "mx_common.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int kU = 4;   // vectors of eight elements of a lane
+
+// Codes and scale code of a vector; every lane of the warp calls it.
+__device__ __forceinline__ uint32_t quantise8(const uint4 v, uint32_t &code) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) m = __vmaxu2(m, w[i] & 0x7FFF7FFFu);
+    m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, 1));
+    m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, 2));
+    const uint32_t lo = m & 0xFFFFu, hi = m >> 16;
+    code = mx4_scale_code((lo > hi ? lo : hi) << 16);   // bf16 bits order as magnitudes
+    float f[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        f[2 * i] = bf16_lo(w[i]);
+        f[2 * i + 1] = bf16_hi(w[i]);
+    }
+    return e2m1x8(f, mx4_inv_scale(code));
+}
+
+// n8 = all vectors of the matrix; kb = blocks of a row.
+__global__ void __launch_bounds__(256)
+    mx4_quantize_kernel(const uint4 *__restrict__ src, long long n8, int kb, int sfp,
+                        uint32_t *__restrict__ q, uint8_t *__restrict__ sf) {
+    wait_for_kernels_ahead();
+    let_kernels_behind_begin();
+    const int lane = threadIdx.x & 31;
+    const long long step = (long long)gridDim.x * 8 * 32 * kU;
+    // whole warps take the same steps: the shuffles need every lane
+    for (long long w0 = ((long long)blockIdx.x * 8 + (threadIdx.x >> 5)) * 32 * kU; w0 < n8;
+         w0 += step) {
+        uint4 v[kU];
+#pragma unroll
+        for (int u = 0; u < kU; ++u) {
+            const long long i = w0 + 32 * u + lane;
+            v[u] = i < n8 ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
+        }
+#pragma unroll
+        for (int u = 0; u < kU; ++u) {
+            const long long i = w0 + 32 * u + lane;
+            uint32_t code;
+            const uint32_t w = quantise8(v[u], code);
+            if (i >= n8) continue;
+            q[i] = w;
+            if ((lane & 3) == 0) {
+                const long long b = i >> 2, r = b / kb;
+                sf[r * sfp + (b - r * kb)] = (uint8_t)code;
+            }
+        }
+    }
+}
+
+__global__ void __launch_bounds__(256)
+    mx4_dequantize_kernel(const uint32_t *__restrict__ q, const uint8_t *__restrict__ sf,
+                          long long n8, int kb, int sfp, uint4 *__restrict__ out) {
+    wait_for_kernels_ahead();
+    let_kernels_behind_begin();
+    const int lane = threadIdx.x & 31;
+    const long long step = (long long)gridDim.x * 8 * 32 * kU;
+    for (long long w0 = ((long long)blockIdx.x * 8 + (threadIdx.x >> 5)) * 32 * kU; w0 < n8;
+         w0 += step) {
+        uint32_t w[kU], code[kU];
+#pragma unroll
+        for (int u = 0; u < kU; ++u) {
+            const long long i = w0 + 32 * u + lane;
+            w[u] = code[u] = 0;
+            if (i < n8) {
+                const long long b = i >> 2, r = b / kb;
+                w[u] = __ldg(q + i);
+                code[u] = __ldg(sf + r * sfp + (b - r * kb));
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < kU; ++u) {
+            const long long i = w0 + 32 * u + lane;
+            if (i >= n8) continue;
+            uint32_t h[4], o[4];
+            e2m1x8_f16(w[u], h);
+            const float x = mx4_scale(code[u]);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h[j]));
+                o[j] = pack_bf16x2(f.x * x, f.y * x);
+            }
+            out[i] = make_uint4(o[0], o[1], o[2], o[3]);
+        }
+    }
+}
+
+// The dispatch: a warp takes kU * 256 elements of one token, quantises them once and
+// writes them to the token's k routed rows and to row T k + t.
+__global__ void __launch_bounds__(256)
+    mx4_gather_kernel(const uint4 *__restrict__ x, const int32_t *__restrict__ slot_row, int T,
+                      int d8, int k, int sfp, uint32_t *__restrict__ q,
+                      uint8_t *__restrict__ sf) {
+    wait_for_kernels_ahead();
+    let_kernels_behind_begin();
+    const int lane = threadIdx.x & 31;
+    const int chunks = (d8 + 32 * kU - 1) / (32 * kU);
+    const long long units = (long long)T * chunks, S = (long long)T * k;
+    for (long long i = (long long)blockIdx.x * 8 + (threadIdx.x >> 5); i < units;
+         i += (long long)gridDim.x * 8) {
+        const long long t = i / chunks;
+        const int c0 = (int)(i - t * chunks) * (32 * kU) + lane;
+        long long row = 0;
+        if (lane < k) row = slot_row[t * k + lane];
+        uint4 v[kU];
+#pragma unroll
+        for (int u = 0; u < kU; ++u) {
+            const int c = c0 + 32 * u;
+            v[u] = c < d8 ? __ldg(x + t * d8 + c) : make_uint4(0, 0, 0, 0);
+        }
+        uint32_t w[kU], code[kU];
+#pragma unroll
+        for (int u = 0; u < kU; ++u) w[u] = quantise8(v[u], code[u]);
+        for (int j = 0; j <= k; ++j) {
+            long long r = __shfl_sync(0xffffffffu, row, j & 31);
+            if (j == k) r = S + t;
+            else if (r < 0 || r >= S) continue;   // not a routed row
+#pragma unroll
+            for (int u = 0; u < kU; ++u) {
+                const int c = c0 + 32 * u;
+                if (c >= d8) continue;
+                q[r * d8 + c] = w[u];
+                if ((lane & 3) == 0) sf[r * sfp + (c >> 2)] = (uint8_t)code[u];
+            }
+        }
+    }
+}
+
+unsigned blocks_for(long long warps) {
+    const long long want = (warps + 7) / 8, most = (long long)num_sms() * 64;
+    return (unsigned)(want < most ? want : most);
+}
+
+}  // namespace
+
+moe_status launch_mx4_quantize(const uint16_t *src, long long rows, int K, uint8_t *q, uint8_t *sf,
+                               cudaStream_t st) {
+    const long long n8 = rows * (K / 8);
+    return launch_early(mx4_quantize_kernel, dim3(blocks_for((n8 + 32 * kU - 1) / (32 * kU))), 256,
+                        0, st, reinterpret_cast<const uint4 *>(src), n8, K / 32, mx_sf_pitch(K),
+                        reinterpret_cast<uint32_t *>(q), sf);
+}
+
+moe_status launch_mx4_dequantize(const uint8_t *q, const uint8_t *sf, long long rows, int K,
+                                 uint16_t *out, cudaStream_t st) {
+    const long long n8 = rows * (K / 8);
+    return launch_early(mx4_dequantize_kernel, dim3(blocks_for((n8 + 32 * kU - 1) / (32 * kU))),
+                        256, 0, st, reinterpret_cast<const uint32_t *>(q), sf, n8, K / 32,
+                        mx_sf_pitch(K), reinterpret_cast<uint4 *>(out));
+}
+
+moe_status launch_mx4_gather(const uint16_t *x, const int32_t *slot_row, int T, int d, int k,
+                             uint8_t *q, uint8_t *sf, cudaStream_t st) {
+    const int d8 = d / 8;
+    const long long units = (long long)T * ((d8 + 32 * kU - 1) / (32 * kU));
+    return launch_early(mx4_gather_kernel, dim3(blocks_for(units)), 256, 0, st,
+                        reinterpret_cast<const uint4 *>(x), slot_row, T, d8, k, mx_sf_pitch(d),
+                        reinterpret_cast<uint32_t *>(q), sf);
+}
+
+}  // namespace moe

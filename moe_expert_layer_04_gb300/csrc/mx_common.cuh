@@ -67,4 +67,56 @@ __device__ __forceinline__ uint32_t mx_quantize_block(const float (&v)[32], uint
     return code;
 }
 
+// MXFP4: the same blocks with E2M1 elements (sign, 2 exponent bits with bias 1, 1
+// mantissa bit: 0, 0.5, 1, 1.5, 2, 3, 4, 6), X = 2^(floor(log2 amax) - 2), two codes a
+// byte, the even element in the low nibble.  E2M1 has neither NaN nor infinity: a block
+// that holds one gets the scale's NaN code, 255, so that it does not pass for a number.
+
+// E8M0 code from the largest magnitude's fp32 bits (sign cleared; NaN and infinity order
+// above every number).
+__device__ __forceinline__ uint32_t mx4_scale_code(uint32_t amax_bits) {
+    if (amax_bits >= 0x7F800000u) return 255u;
+    if (amax_bits == 0u) return 0u;
+    const int se = floor_log2_f32(__uint_as_float(amax_bits)) - 2;
+    return (uint32_t)((se < -127 ? -127 : se) + 127);
+}
+
+// 1 / X; for the NaN code any finite factor does.
+__device__ __forceinline__ float mx4_inv_scale(uint32_t code) {
+    return code == 255u ? 0.0f : exp2_int(127 - (int)code);
+}
+
+// X, a NaN for the NaN code.
+__device__ __forceinline__ float mx4_scale(uint32_t code) {
+    return code == 255u ? __uint_as_float(0x7FC00000u) : exp2_int((int)code - 127);
+}
+
+// Eight values times r -> eight E2M1 codes, the first in the lowest nibble (nearest, ties
+// to the even code, magnitudes above 6 to 6, the sign kept).
+__device__ __forceinline__ uint32_t e2m1x8(const float (&v)[8], float r) {
+    uint32_t w;
+    asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b2, %6, %5;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n\t"
+        "mov.b32 %0, {b0, b1, b2, b3};\n\t}"
+        : "=r"(w)
+        : "f"(v[0] * r), "f"(v[1] * r), "f"(v[2] * r), "f"(v[3] * r), "f"(v[4] * r),
+          "f"(v[5] * r), "f"(v[6] * r), "f"(v[7] * r));
+    return w;
+}
+
+// Eight E2M1 codes -> four f16 pairs, exact.
+__device__ __forceinline__ void e2m1x8_f16(uint32_t w, uint32_t (&h)[4]) {
+    asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+        "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %2, b2;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
+        : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+        : "r"(w));
+}
+
 }  // namespace moe

@@ -1,0 +1,387 @@
+// norm.cu -- the root-mean-square norm ahead of the layer, with the residual's
+// addition before it and the rows' quantisation behind it, and its backward.
+//
+//   v    = bf16(x + residual)                    (x alone without a residual)
+//   rstd = 1 / sqrt( mean_i v_i^2 + eps )
+//   u    = v rstd w                              fp32
+//   y    = bf16(u),  codes and scales of u in FP8 (1 x 128), MXFP8 or MXFP4
+//
+//   vh = v rstd,  a = w dy
+//   dx = bf16( d_residual + rstd (a - vh mean_i(a_i vh_i)) )   (for x and the residual)
+//   dw = sum over the rows of dy vh
+//
+// (The rows are those of the MoE layer: "HyperParallel加速DeepSeek-V4.1多模态1M长序列
+// 训练" §2.3, MegaMHC's residual update and norm ahead of it.)  Sums are fp32 in a
+// fixed order.  Both directions are bound by HBM: each row is held in registers
+// between its sum and its use, so that every value crosses once.
+#include <cstring>
+
+#include "fp8_common.cuh"
+#include "mx_common.cuh"
+
+namespace moe {
+namespace {
+
+__device__ __forceinline__ void unpack8(const uint4 v, float (&f)[8]) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        f[2 * i] = bf16_lo(w[i]);
+        f[2 * i + 1] = bf16_hi(w[i]);
+    }
+}
+__device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
+    return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
+                      pack_bf16x2(f[6], f[7]));
+}
+
+// Sum over the `warps` warps that share a row (all of the CTA's rows at once); `part`
+// holds a float for each warp of the CTA.
+__device__ __forceinline__ float row_sum(float s, int warps, float *part) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if (warps == 1) return s;
+    const int warp = threadIdx.x >> 5;
+    if ((threadIdx.x & 31) == 0) part[warp] = s;
+    __syncthreads();
+    const int first = warp / warps * warps;
+    s = 0.0f;
+    for (int i = 0; i < warps; ++i) s += part[first + i];
+    return s;
+}
+
+struct NormRows {
+    int T, d8, threads;   // threads of a row, a multiple of 32
+    float eps, inv_d;
+    int format;
+    const uint4 *x, *residual;
+    const float *weight;
+    uint4 *residual_out, *y;
+    float *rstd;
+    uint8_t *q;
+    void *scales;
+    int scale_pitch;      // scales of a row
+};
+
+// Codes and scales of the eight values u, elements 8 c .. of row `row`; called by
+// whole warps, whose lanes hold consecutive vectors (a block of 128 is sixteen lanes,
+// one of 32 four).
+__device__ __forceinline__ void store_codes(const NormRows &p, size_t row, int c, bool live,
+                                            const float (&u)[8]) {
+    if (p.format == MOE_ROWS_FP8) {
+        uint32_t m = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(u[i]) & 0x7FFFFFFFu);
+#pragma unroll
+        for (int o = 1; o < 16; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+        const Fp8Scale f = fp8_scale(m);
+        if (!live) return;
+        uint2 w;
+        w.x = e4m3x4(u[0] * f.r, u[1] * f.r, u[2] * f.r, u[3] * f.r);
+        w.y = e4m3x4(u[4] * f.r, u[5] * f.r, u[6] * f.r, u[7] * f.r);
+        *reinterpret_cast<uint2 *>(p.q + (row * p.d8 + c) * 8) = w;
+        if ((c & 15) == 0)
+            static_cast<float *>(p.scales)[row * p.scale_pitch + (c >> 4)] = f.s;
+        return;
+    }
+    if (p.format == MOE_ROWS_MXFP8) {
+        float m = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(u[i]));
+#pragma unroll
+        for (int o = 1; o < 4; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        const uint32_t code = mx_scale_code(m);
+        const float r = mx_inv_scale(code);
+        if (!live) return;
+        uint2 w;
+        w.x = e4m3x4(u[0] * r, u[1] * r, u[2] * r, u[3] * r);
+        w.y = e4m3x4(u[4] * r, u[5] * r, u[6] * r, u[7] * r);
+        *reinterpret_cast<uint2 *>(p.q + (row * p.d8 + c) * 8) = w;
+        if ((c & 3) == 0)
+            static_cast<uint8_t *>(p.scales)[row * p.scale_pitch + (c >> 2)] = (uint8_t)code;
+        return;
+    }
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(u[i]) & 0x7FFFFFFFu);
+#pragma unroll
+    for (int o = 1; o < 4; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+    const uint32_t code = mx4_scale_code(m);
+    if (!live) return;
+    *reinterpret_cast<uint32_t *>(p.q + (row * p.d8 + c) * 4) = e2m1x8(u, mx4_inv_scale(code));
+    if ((c & 3) == 0)
+        static_cast<uint8_t *>(p.scales)[row * p.scale_pitch + (c >> 2)] = (uint8_t)code;
+}
+
+// A row's `threads` threads hold V vectors of eight elements each.
+template <int V>
+__global__ void __launch_bounds__(1024) rmsnorm_kernel(const NormRows p) {
+    __shared__ float part[32];
+    wait_for_kernels_ahead();
+    let_kernels_behind_begin();
+    const int in_row = threadIdx.x % p.threads;
+    const long long row = (long long)blockIdx.x * (blockDim.x / p.threads) +
+                          threadIdx.x / p.threads;
+    const bool has = row < p.T;
+    uint4 v[V];
+    float ss = 0.0f;
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+        const int c = in_row + j * p.threads;
+        v[j] = make_uint4(0, 0, 0, 0);
+        if (has && c < p.d8) {
+            v[j] = __ldg(p.x + row * p.d8 + c);
+            if (p.residual) {
+                const uint4 b = __ldg(p.residual + row * p.d8 + c);
+                float f[8], g[8];
+                unpack8(v[j], f);
+                unpack8(b, g);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) f[i] += g[i];
+                v[j] = pack8(f);
+                p.residual_out[row * p.d8 + c] = v[j];
+            }
+        }
+        float f[8];
+        unpack8(v[j], f);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) ss = fmaf(f[i], f[i], ss);
+    }
+    ss = row_sum(ss, p.threads >> 5, part);
+    const float r = 1.0f / sqrtf(fmaf(ss, p.inv_d, p.eps));
+    if (has && in_row == 0 && p.rstd) p.rstd[row] = r;
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+        const int c = in_row + j * p.threads;
+        const bool live = has && c < p.d8;
+        float f[8];
+        unpack8(v[j], f);
+        if (live) {
+            const float4 w0 = __ldg(reinterpret_cast<const float4 *>(p.weight) + 2 * c);
+            const float4 w1 = __ldg(reinterpret_cast<const float4 *>(p.weight) + 2 * c + 1);
+            const float w[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
+#pragma unroll
+            for (int i = 0; i < 8; ++i) f[i] = f[i] * r * w[i];
+            if (p.y) p.y[row * p.d8 + c] = pack8(f);
+        }
+        if (p.format != MOE_ROWS_NONE) store_codes(p, (size_t)row, c, live, f);
+    }
+}
+
+struct NormBwd {
+    int T, d8, threads;
+    float inv_d;
+    const uint4 *x, *dy, *d_residual;
+    const float *weight, *rstd;
+    uint4 *dx;
+    float *part;   // [slots, d]: a row of partial sums for each row in flight
+};
+
+// The rows slot, slot + slots, ... of one slot; the next row's loads are issued before
+// this row's sum.
+template <int V>
+__global__ void __launch_bounds__(512) rmsnorm_bwd_kernel(const NormBwd p) {
+    __shared__ float part[2][32];
+    wait_for_kernels_ahead();
+    let_kernels_behind_begin();
+    const int in_row = threadIdx.x % p.threads;
+    const int per = blockDim.x / p.threads;
+    const long long slots = (long long)gridDim.x * per;
+    const long long slot = (long long)blockIdx.x * per + threadIdx.x / p.threads;
+    float w[V][8], dw[V][8];
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+        const int c = in_row + j * p.threads;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            w[j][i] = c < p.d8 ? __ldg(p.weight + 8 * c + i) : 0.0f;
+            dw[j][i] = 0.0f;
+        }
+    }
+    const uint4 zero = make_uint4(0, 0, 0, 0);
+    uint4 nv[V], nd[V], nr[V];
+    float nrstd = 0.0f;
+    auto load = [&](long long row) {
+        const bool has = row < p.T;
+        nrstd = has ? __ldg(p.rstd + row) : 0.0f;
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            const int c = in_row + j * p.threads;
+            const bool live = has && c < p.d8;
+            nv[j] = live ? __ldg(p.x + row * p.d8 + c) : zero;
+            nd[j] = live ? __ldg(p.dy + row * p.d8 + c) : zero;
+            nr[j] = live && p.d_residual ? __ldg(p.d_residual + row * p.d8 + c) : zero;
+        }
+    };
+    load(slot);
+    // all rows of a CTA take the same number of steps (its sums are barriers)
+    const long long first = (long long)blockIdx.x * per;
+    int turn = 0;
+    for (long long base = first; base < p.T; base += slots, turn ^= 1) {
+        const long long row = base + threadIdx.x / p.threads;
+        const float r = nrstd;
+        uint4 v[V], dr[V];
+        float a[V][8];
+        float dot = 0.0f;
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            v[j] = nv[j];
+            dr[j] = nr[j];
+            float f[8], g[8];
+            unpack8(nv[j], f);
+            unpack8(nd[j], g);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float vh = f[i] * r;
+                dw[j][i] = fmaf(g[i], vh, dw[j][i]);
+                a[j][i] = g[i] * w[j][i];
+                dot = fmaf(a[j][i], vh, dot);
+            }
+        }
+        load(row + slots);
+        const float m = row_sum(dot, p.threads >> 5, part[turn]) * p.inv_d;
+        if (row < p.T) {
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                const int c = in_row + j * p.threads;
+                if (c >= p.d8) continue;
+                float f[8], g[8];
+                unpack8(v[j], f);
+                unpack8(dr[j], g);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) g[i] += r * (a[j][i] - f[i] * r * m);
+                p.dx[row * p.d8 + c] = pack8(g);
+            }
+        }
+    }
+    float4 *dst = reinterpret_cast<float4 *>(p.part + slot * p.d8 * 8);
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+        const int c = in_row + j * p.threads;
+        if (c >= p.d8) continue;
+        dst[2 * c] = make_float4(dw[j][0], dw[j][1], dw[j][2], dw[j][3]);
+        dst[2 * c + 1] = make_float4(dw[j][4], dw[j][5], dw[j][6], dw[j][7]);
+    }
+}
+
+// dw = the sum of the slots' rows: a CTA takes 128 columns, its eight warps every
+// eighth slot, added up in order.
+__global__ void __launch_bounds__(256)
+    rmsnorm_dw_kernel(const float4 *__restrict__ part, int slots, int d4, float4 *__restrict__ dw) {
+    __shared__ float4 sums[8][32];
+    wait_for_kernels_ahead();
+    let_kernels_behind_begin();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int c = blockIdx.x * 32 + lane;
+    float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (c < d4) {
+#pragma unroll 8
+        for (int i = warp; i < slots; i += 8) {
+            const float4 v = part[(size_t)i * d4 + c];
+            s.x += v.x;
+            s.y += v.y;
+            s.z += v.z;
+            s.w += v.w;
+        }
+    }
+    sums[warp][lane] = s;
+    __syncthreads();
+    if (warp != 0 || c >= d4) return;
+#pragma unroll
+    for (int i = 1; i < 8; ++i) {
+        const float4 v = sums[i][lane];
+        s.x += v.x;
+        s.y += v.y;
+        s.z += v.z;
+        s.w += v.w;
+    }
+    dw[c] = s;
+}
+
+// Threads of a row of d8 vectors, V each, and rows of a CTA.
+struct RowShape {
+    int V, threads, rows;
+};
+RowShape row_shape(int d8, int most, int cta) {
+    RowShape s;
+    s.V = 1;
+    while (d8 > s.V * most) s.V *= 2;
+    s.threads = ((d8 + s.V - 1) / s.V + 31) / 32 * 32;
+    s.rows = s.threads < cta ? cta / s.threads : 1;
+    return s;
+}
+
+RowShape bwd_shape(int d8) { return row_shape(d8, 512, 128); }
+
+// Rows in flight of the backward: CTAs for the SMs, no more than there are rows.
+int bwd_ctas(int T, const RowShape &s) {
+    const long long want = ((long long)T + s.rows - 1) / s.rows;
+    const long long most = (long long)num_sms() * (s.threads * s.rows <= 512 ? 4 : 2);
+    return (int)(want < most ? want : most);
+}
+
+}  // namespace
+
+moe_status launch_rmsnorm(const moe_norm_args *a, cudaStream_t st) {
+    const RowShape s = row_shape(a->d / 8, 1024, 128);
+    NormRows p;
+    std::memset(&p, 0, sizeof p);
+    p.T = a->T;
+    p.d8 = a->d / 8;
+    p.threads = s.threads;
+    p.eps = a->eps;
+    p.inv_d = 1.0f / (float)a->d;
+    p.format = a->format;
+    p.x = reinterpret_cast<const uint4 *>(a->x);
+    p.residual = reinterpret_cast<const uint4 *>(a->residual);
+    p.weight = a->weight;
+    p.residual_out = reinterpret_cast<uint4 *>(a->residual_out);
+    p.y = reinterpret_cast<uint4 *>(a->y);
+    p.rstd = a->rstd;
+    p.q = a->q;
+    p.scales = a->scales;
+    p.scale_pitch = a->format == MOE_ROWS_FP8 ? fp8_blocks(a->d) : mx_sf_pitch(a->d);
+    const dim3 grid((a->T + s.rows - 1) / s.rows);
+    const int threads = s.threads * s.rows;
+    if (s.V == 1) return launch_early(rmsnorm_kernel<1>, grid, threads, 0, st, p);
+    if (s.V == 2) return launch_early(rmsnorm_kernel<2>, grid, threads, 0, st, p);
+    return launch_early(rmsnorm_kernel<4>, grid, threads, 0, st, p);
+}
+
+size_t rmsnorm_bwd_workspace_bytes(int T, int d) {
+    const RowShape s = bwd_shape(d / 8);
+    return (size_t)bwd_ctas(T, s) * s.rows * d * sizeof(float);
+}
+
+moe_status launch_rmsnorm_bwd(const moe_norm_bwd_args *a, cudaStream_t st) {
+    const RowShape s = bwd_shape(a->d / 8);
+    NormBwd p;
+    std::memset(&p, 0, sizeof p);
+    p.T = a->T;
+    p.d8 = a->d / 8;
+    p.threads = s.threads;
+    p.inv_d = 1.0f / (float)a->d;
+    p.x = reinterpret_cast<const uint4 *>(a->x);
+    p.dy = reinterpret_cast<const uint4 *>(a->dy);
+    p.d_residual = reinterpret_cast<const uint4 *>(a->d_residual);
+    p.weight = a->weight;
+    p.rstd = a->rstd;
+    p.dx = reinterpret_cast<uint4 *>(a->dx);
+    p.part = static_cast<float *>(a->ws);
+    const int ctas = bwd_ctas(a->T, s), threads = s.threads * s.rows;
+    moe_status r = MOE_OK;
+    if (ctas > 0) {
+        if (s.V == 1) r = launch_early(rmsnorm_bwd_kernel<1>, dim3(ctas), threads, 0, st, p);
+        else if (s.V == 2) r = launch_early(rmsnorm_bwd_kernel<2>, dim3(ctas), threads, 0, st, p);
+        else if (s.V == 4) r = launch_early(rmsnorm_bwd_kernel<4>, dim3(ctas), threads, 0, st, p);
+        else r = launch_early(rmsnorm_bwd_kernel<8>, dim3(ctas), threads, 0, st, p);
+    }
+    if (r != MOE_OK) return r;
+    // without rows: zeros
+    const int d4 = a->d / 4;
+    return launch_early(rmsnorm_dw_kernel, dim3((d4 + 31) / 32), 256, 0, st,
+                        reinterpret_cast<const float4 *>(a->ws), ctas * s.rows, d4,
+                        reinterpret_cast<float4 *>(a->d_weight));
+}
+
+}  // namespace moe

@@ -1,0 +1,178 @@
+"""MXFP4 against the plain 64-bit implementation of tests/mx4_ref.py.
+
+Quantisation is a fixed rounding rule: codes and scales match bit for bit.  The products
+of the matmuls are exact and only their fp32 sums round.  Bound of an element, with A =
+sum |a| |b| over the contraction: K additions one after the other at worst, each off by at
+most one fp32 spacing of a partial sum (2^-23 A, truncation allowed), and the row weight's
+rounding: (K + 2) 2^-23 A.  A bf16 result has to be the rounding of a value that close: it
+lies between the roundings of the interval's two ends (rounding is monotonic)."""
+import numpy as np
+import pytest
+import torch
+
+from moe_expert_layer_04_gb300 import _lib
+from tests import fp8_ref as F
+from tests import mx4_ref as R
+from tests.test_gpu_fp8 import bf16, codes, counts_offsets, empty, f64, ok
+
+pytestmark = pytest.mark.gpu
+
+
+def dev(a):
+    return torch.from_numpy(np.ascontiguousarray(a)).cuda()
+
+
+def padded(s, K, fill):
+    """Scale codes with the bytes behind a row set to `fill`."""
+    out = np.full((s.shape[0], R.pitch(K)), fill, np.uint8)
+    out[:, :s.shape[1]] = s
+    return out
+
+
+def values(rng, rows, K):
+    """Values over many magnitudes, with the rule's edge cases at the start."""
+    v = rng.standard_normal((rows, K)) * np.exp(2 * rng.standard_normal((rows, 1)))
+    v[0, :32] = 0.0
+    v[0, :16] = -0.0
+    if rows > 4:
+        mid = (R.GRID[:7] + R.GRID[1:]) / 2                       # scale 1: every tie, signed
+        v[1, :32] = np.resize(np.concatenate([mid, -mid, [4.0, 7.5]]), 32)
+        v[2, :32] = np.resize(R.TABLE, 32)                        # on the grid
+        v[3, :32] = 2.0 ** -133 * np.resize([1, 3, -5, 0, 60], 32)  # bf16 subnormals
+        v[4, :32] = np.resize([3.3e38, -1e38, 1e30, 1.0], 32)
+    return v
+
+
+@pytest.mark.parametrize("rows,K", [(1, 32), (1, 512), (7, 96), (33, 1056), (300, 2048), (5, 4128)])
+def test_quantise_bit_exact(rows, K):
+    x = bf16(values(np.random.default_rng(rows * 31 + K), rows, K))
+    q, sf = empty(rows, K // 2), empty(rows, R.pitch(K), fill=0xA5)
+    _lib.moe_mx4_quantize(x.cuda(), rows, K, q, sf)
+    out = empty(rows, K, dtype=torch.bfloat16)
+    _lib.moe_mx4_dequantize(q, sf, rows, K, out)
+    ok()
+    c, s = R.quantise4(f64(x))
+    assert np.array_equal(codes(q), R.pack(c))
+    assert np.array_equal(codes(sf), padded(s, K, 0xA5))          # the padding stays
+    assert np.array_equal(f64(out), R.values4(c, s))
+
+
+def test_quantise_not_finite():
+    x = torch.ones(3, 96, dtype=torch.bfloat16)
+    x[0, 5], x[1, 40], x[2, 70] = float("nan"), float("inf"), float("-inf")
+    q, sf, out = empty(3, 48), empty(3, 16), empty(3, 96, dtype=torch.bfloat16)
+    _lib.moe_mx4_quantize(x.cuda(), 3, 96, q, sf)
+    _lib.moe_mx4_dequantize(q, sf, 3, 96, out)
+    ok()
+    assert codes(sf)[:, :3].tolist() == [[255, 125, 125], [125, 255, 125], [125, 125, 255]]
+    nan = np.isnan(f64(out)).reshape(3, 3, 32)
+    assert np.array_equal(nan.all(2), np.eye(3, dtype=bool)) and nan.sum() == 96
+
+
+def test_dequantise_every_code_and_scale():
+    c = np.tile(np.arange(16, dtype=np.uint8), (256, 2))
+    s = np.arange(256, dtype=np.uint8)[:, None]
+    out = empty(256, 32, dtype=torch.bfloat16)
+    _lib.moe_mx4_dequantize(dev(R.pack(c)), dev(padded(s, 32, 0)), 256, 32, out)
+    ok()
+    with np.errstate(over="ignore"):
+        want = R.values4(c, s)
+    big = np.abs(want) > 3.3895e38                                # past bf16's range
+    want[big] = np.copysign(np.inf, want[big])
+    got = f64(out)
+    assert np.array_equal(np.isnan(got), np.isnan(want))
+    assert np.array_equal(got[:255], want[:255])
+
+
+@pytest.mark.parametrize("T,d,k", [(1, 32, 1), (5, 288, 3), (130, 1152, 8), (64, 4096, 6), (3, 64, 32)])
+def test_gather_bit_exact(T, d, k):
+    x = bf16(values(np.random.default_rng(T + d + k), T, d))
+    slot_row = np.random.default_rng(1).permutation(T * k).astype(np.int32)
+    S = T * k
+    q, sf = empty(S + T, d // 2, fill=0xAA), empty(S + T, R.pitch(d), fill=0xA5)
+    _lib.moe_mx4_gather(x.cuda(), dev(slot_row), T, d, k, q, sf)
+    ok()
+    tok = np.empty(S + T, int)
+    tok[slot_row] = np.repeat(np.arange(T), k)
+    tok[S:] = np.arange(T)
+    c, s = R.quantise4(f64(x))
+    assert np.array_equal(codes(q), R.pack(c)[tok])
+    assert np.array_equal(codes(sf), padded(s, d, 0xA5)[tok])
+
+
+def test_quantise_behind_32_bit_places():
+    """Elements and code bytes whose places pass 2^31 and 2^32."""
+    K, rows = 8192, 530_000                                        # 4.3e9 elements
+    x = torch.zeros(rows, K, dtype=torch.bfloat16, device="cuda")
+    v = bf16(values(np.random.default_rng(1), 6, K))
+    x[-6:] = v.cuda()
+    q, sf = empty(rows, K // 2), empty(rows, R.pitch(K))
+    _lib.moe_mx4_quantize(x, rows, K, q, sf)
+    ok()
+    c, s = R.quantise4(f64(v))
+    assert np.array_equal(codes(q[-6:]), R.pack(c)) and np.array_equal(codes(sf[-6:]), s)
+    x.fill_(1.0)
+    _lib.moe_mx4_dequantize(q, sf, rows, K, x)
+    ok()
+    assert np.array_equal(f64(x[-6:]), R.values4(c, s))
+
+
+# ------------------------------------------------------------------ matmuls
+
+def between(got, ref, absdot, K, what):
+    g = f64(got)
+    lim = (K + 2) * 2.0 ** -23 * absdot + 1e-30
+    lo, hi = f64(bf16(ref - lim)), f64(bf16(ref + lim))
+    assert np.logical_and(lo <= g, g <= hi).all(), f"{what}: {float(np.max(np.abs(g - ref)))}"
+
+
+def rows_of(rng, rows, K, bits):
+    """Codes, scales and values of random rows."""
+    v = rng.standard_normal((rows, K)) * np.exp(rng.standard_normal((rows, 1)))
+    if bits == 4:
+        c, s = R.quantise4(v)
+        return R.pack(c), s, R.values4(c, s)
+    c, s = R.quantise8(v)
+    return c, s, R.values8(c, s)
+
+
+def weights_of(rng, G, N, K):
+    c, s = R.quantise4(rng.standard_normal((G * N, K)) / np.sqrt(K))
+    return R.pack(c), s, R.values4(c, s).reshape(G, N, K)
+
+
+SHAPES = [([1], 8, 32), ([1], 512, 4096), ([3], 136, 416), ([128], 256, 128), ([129, 0, 1, 260], 264, 288),
+          ([17, 40, 0, 200, 5], 640, 1152), ([0, 0], 64, 64), ([300], 1000, 2048), ([2] * 40, 72, 160),
+          ([32], 384, 512), ([31, 0, 1], 264, 672), ([650, 100, 0, 700], 520, 416), ([513], 264, 1056),
+          ([8], 24, 4128), ([9], 264, 544), ([1400, 0, 1201], 1032, 512), ([1], 4096, 128)]
+MATMULS = [(c, N, K, 4) for c, N, K in SHAPES]
+MATMULS += [(c, N, (K + 127) // 128 * 128, 8) for c, N, K in SHAPES]
+
+
+@pytest.mark.parametrize("counts,N,K,bits", MATMULS)
+@pytest.mark.parametrize("weighted", [False, True])
+def test_matmul(counts, N, K, bits, weighted):
+    rng = np.random.default_rng(N * 7 + K + len(counts))
+    G, rows = len(counts), sum(counts)
+    aq, asf, av = rows_of(rng, max(rows, 1) + 1, K, bits)          # one row behind the end
+    bq, bsf, bv = weights_of(rng, G, N, K)
+    w_rows = rows // 2
+    w = F.f32(rng.random(max(w_rows, 1)) + 0.5)
+    out = empty(max(rows, 1) + 1, N, dtype=torch.bfloat16, fill=77.0)
+    # the bytes behind a row's scales are anything: here the code of a NaN
+    _lib.moe_mx4_matmul(dev(aq), dev(padded(asf, K, 255)), bits, counts_offsets(counts), G,
+                        max(rows, 1), dev(bq), dev(padded(bsf, K, 255)),
+                        dev(w.astype(np.float32)) if weighted else None, w_rows if weighted else 0,
+                        N, K, out)
+    ok()
+    assert (out[rows:] == 77.0).all()
+    lo = 0
+    for g, n in enumerate(counts):
+        f_row = np.ones(n)
+        if weighted:
+            m = np.arange(lo, lo + n) < w_rows
+            f_row[m] = w[np.arange(lo, lo + n)[m]]
+        a = av[lo:lo + n]
+        between(out[lo:lo + n], (a @ bv[g].T) * f_row[:, None],
+                (np.abs(a) @ np.abs(bv[g]).T) * f_row[:, None], K, f"group {g}")
+        lo += n
