@@ -888,7 +888,7 @@ moe_status moe_rmsnorm_backward(const moe_norm_bwd_args *args, void *stream);
  * moe_balance_loss writes counts, tokens, load, seq_loss and loss (dloss and dlogits are
  * not read); moe_balance_loss_backward reads tokens and load of it and writes dlogits (ids,
  * counts, seq_loss, loss and ws are not read).
- * T >= 0, n_seq >= 1, 1 <= E <= 1024, 1 <= k <= 32 (else MOE_ERR_UNSUPPORTED),
+ * T >= 0, 1 <= n_seq <= 65535, 1 <= E <= 1024, 1 <= k <= 32 (else MOE_ERR_UNSUPPORTED),
  * (T + n_seq) E < 2^40.  seq_offsets int32 [n_seq+1] on the device, or NULL: one sequence of
  * all T tokens (n_seq = 1).  Offsets that descend or leave [0, T] are cut to it and recorded
  * as MOE_ERR_INVALID_ARG on the device, as are ids outside [0, E), which are not counted.

@@ -1469,7 +1469,7 @@ moe_status moe_rmsnorm_backward(const moe_norm_bwd_args *a, void *stream) {
 // Shapes of the balance loss: MOE_OK, or why not.
 static moe_status balance_shape(int T, int E, int k, int n_seq) {
     if (T < 0 || E < 1 || k < 1 || n_seq < 1) return MOE_ERR_INVALID_ARG;
-    if (E > 1024 || k > 32 || ((long long)T + n_seq) * E >= (1LL << 40))
+    if (E > 1024 || k > 32 || n_seq > 65535 || ((long long)T + n_seq) * E >= (1LL << 40))
         return MOE_ERR_UNSUPPORTED;
     return MOE_OK;
 }

@@ -11,15 +11,26 @@
 //
 // The tensor cores apply the scales: every product is exact, the sums are fp32.  A stage
 // is 128 bytes of each row's codes: 256 elements (4 bits) or 128 (8 bits).  The scales of
-// 512 elements of a row are 16 bytes; they come by TMA as rows, a warp turns 128 rows of
-// them in place into four blocks of 32 x 16 bytes (one for each word of four scales), and
-// the thread that issues a stage's MMAs first copies its blocks into tensor memory
-// (tcgen05.cp, which the MMAs behind it wait for).
+// 512 elements of a row are 16 bytes: a warp for each 128 rows of A or B loads them three
+// slots of 512 elements ahead, turns them in registers into four blocks of 32 x 16 bytes
+// (one for each word of four scales) and writes those to shared memory; the thread that
+// issues a stage's MMAs first copies its blocks into tensor memory (tcgen05.cp, which the
+// MMAs behind it wait for).  (Rows of 16 bytes by TMA take it about five cycles each: 8192
+// rows over 8 groups, 4864 x 4096, 80 us, and 61 without the codes' copies.)
 //
-// One CTA per SM, persistent, 12 warps: warp 0 TMA producer, warp 1 tensor memory owner
-// and MMA issuer, warps 2 and 3 the scales, warps 4-11 epilogue (thread = row; two warps
-// per lane quadrant, half of the columns each).  Every wait is bounded; on a timeout the
-// CTA records MOE_ERR_TIMEOUT, drains its copies and MMAs, frees tensor memory and returns.
+// One CTA per SM, persistent, 13 warps: warp 0 TMA producer, warp 1 tensor memory owner
+// and MMA issuer, warps 2-4 the scales, warps 5-12 epilogue (thread = row; two warps
+// per lane quadrant, half of the columns each).  Where groups hold many rows two CTAs form
+// a pair (CL = 2): MMAs of 256 rows, each CTA with its 128 rows of A and half of B in
+// shared memory, so that a stage brings 32 KB instead of 48 into each SM; the even CTA
+// issues, the scales of all of B are in both.
+//
+// Tensor memory: two accumulators.  Of 256 columns two and the scales do not fit: the
+// second begins where the first still has its last columns (48, or 24 with 8-bit rows), and
+// the epilogue reads those first, so that the next tile's MMAs wait for them alone.
+//
+// Every wait is bounded; on a timeout the CTA records MOE_ERR_TIMEOUT, drains its copies
+// and MMAs, frees tensor memory and returns.
 #include <cstring>
 
 #include "fp8_common.cuh"
@@ -34,9 +45,10 @@ enum Mx4Mode : int { MX4_ROWS = 0, MX4_FFN1 = 1 };
 struct Mx4Params {
     CUtensorMap tmA;    // A codes, 128 bytes of a row at a time, boxes of a_rows rows
     CUtensorMap tmB;    // B codes, boxes of BN rows (FFN1: BN / 2)
-    CUtensorMap tmSA;   // scale rows [.., pitch], boxes of 16 bytes x a_rows
-    CUtensorMap tmSB;   //                          16 bytes x BN (FFN1: BN / 2)
     CUtensorMap tmO;    // ROWS: output, boxes of 32 rows x 32 columns
+    const uint8_t *sa, *sb;          // scale rows of A and B, `pitch` bytes each
+    int pitch;
+    long long b_rows;
     const int32_t *offsets;
     int G, N, blocks, kb, n_tiles;   // blocks of 32 along K; stages of a tile
     int max_rows, a_rows;
@@ -51,50 +63,52 @@ struct Mx4Params {
     long long wait_limit;
 };
 
-constexpr int kEpi0 = 4, kEpi = 8;               // epilogue warps
+constexpr int kScale0 = 2;                       // scale warps
+constexpr int kEpi0 = 5, kEpi = 8;               // epilogue warps
+constexpr int kAhead = 3;                        // slots of scales on their way in registers
 constexpr int kThreads = 32 * (kEpi0 + kEpi);
 constexpr int kCodeA = 128 * 128;
 constexpr int kSfRegion = 128 * 16;              // scales of 512 elements of 128 rows
-constexpr int kSfSlots = 2;
-constexpr int kBars = 256;
+constexpr int kBars = 512;
 constexpr int kSmem = 232448;                    // of a CTA at most
 constexpr int kWideGroups = 700;                 // whose tables fit beside 256-wide stages
 constexpr int kPiece = 32 * 64;                  // 32 rows x 32 bf16 on their way out
 
-// Registers: the four warps that copy and issue hand most of theirs to the eight that
-// hold a tile's results (128 a thread); 4 x 40 + 8 x 232 is what 12 x 168 launch with.
-constexpr int kRegsFew = 40, kRegsMany = 232;
-static_assert(4 * kRegsFew + 8 * kRegsMany <= 12 * 168, "register split");
-
-template <int MODE, int AB, int BN, int ST>
+template <int MODE, int AB, int BN, int ST, int CL>
 struct Shape {
-    static constexpr int STAGE = kCodeA + BN * 128;
+    static constexpr int STAGE = kCodeA + BN / CL * 128;
     static constexpr int WORDS = AB == 4 ? 2 : 1;        // scale words of a row in a stage
     static constexpr int SPS = 4 / WORDS;                // stages of a scale slot
     static constexpr int NB = (BN + 127) / 128;
     static constexpr int SLOT = (1 + NB) * kSfRegion;
-    static constexpr int NACC = BN == 256 ? 1 : 2;
-    static constexpr int SF0 = NACC * BN;                // tensor memory: accumulators, then
-    static constexpr int SFC = WORDS * 4 * (1 + NB);     // two stages' scales
+    // tensor memory: two accumulators, then two stages' scales
+    static constexpr int SFC = WORDS * 4 * (1 + NB);
+    static constexpr int SF0 = 512 - 2 * SFC;
+    static constexpr int ACC1 = BN == 256 ? SF0 - 256 : BN;   // first column of the second
+    static constexpr int OVER = BN == 256 ? 256 - ACC1 : 0;   // columns that they share
     static constexpr bool TMA_OUT = MODE == MX4_ROWS && BN >= 64;
     static constexpr int OUT = TMA_OUT ? kEpi * kPiece : 0;
-    static constexpr int FIXED = ST * STAGE + kSfSlots * SLOT + OUT + kBars;
+    static constexpr int TABLES = 8 * ((BN == 256 ? kWideGroups : kMaxGroups) + 2);
+    static constexpr int SLOTS = ST * STAGE > 192 * 1024 - 1 ? 2 : 4;   // of scales
+    static constexpr int FIXED = ST * STAGE + SLOTS * SLOT + OUT + kBars;
     static constexpr int smem(int G) { return 1024 + FIXED + 8 * (G + 2); }
-    static_assert(SF0 + 2 * SFC <= 512, "tensor memory");
-    static_assert((2 * ST + 2 * kSfSlots + 3 * NACC + 2) * 8 + 16 <= kBars, "barriers");
+    static_assert(1024 + FIXED + TABLES <= kSmem, "shared memory");
+    static_assert(ACC1 + BN <= SF0 && OVER <= 64, "tensor memory");
+    static_assert((2 * ST + 2 * SLOTS + 6) * 8 + 16 <= kBars, "barriers");
+    static_assert(CL == 1 || BN == 256, "pairs");
 };
 
 struct Tile {
     int g, nt, row0, rows;
 };
 
-// The tiles of a CTA, gridDim.x apart: tile t = q n_tiles + nt.
+// The tiles of a CTA (or pair), as far apart as there are of them: tile t = q n_tiles + nt.
 struct Walk {
     int q, nt, dq, dn, n;
-    __device__ explicit Walk(int n_tiles)
-        : q(blockIdx.x / n_tiles), dq(gridDim.x / n_tiles), n(n_tiles) {
-        nt = blockIdx.x - q * n;
-        dn = gridDim.x - dq * n;
+    __device__ Walk(int n_tiles, int first, int step)
+        : q(first / n_tiles), dq(step / n_tiles), n(n_tiles) {
+        nt = first - q * n;
+        dn = step - dq * n;
     }
     __device__ void next() {
         q += dq;
@@ -103,10 +117,12 @@ struct Walk {
     }
 };
 
-// Row tile q, found by a whole warp: the last group that starts at or before it, 32 groups
-// a ballot from the group of the tile before (empty groups start where the next one does).
+// Row tile q (of CL x 128 rows), found by a whole warp: the last group that starts at or
+// before it, 32 groups a ballot from the group of the tile before (empty groups start where
+// the next one does).
+template <int CL>
 __device__ __forceinline__ Tile find_tile(const Mx4Params &p, int q, int nt, const int *mt_start,
-                                          const int *offs, int from) {
+                                          const int *offs, int from, int rank) {
     int g = from;
     while (true) {
         const int i = g + 1 + (threadIdx.x & 31);
@@ -117,8 +133,8 @@ __device__ __forceinline__ Tile find_tile(const Mx4Params &p, int q, int nt, con
     Tile ti;
     ti.g = g;
     ti.nt = nt;
-    ti.row0 = offs[g] + (q - mt_start[g]) * 128;
-    ti.rows = min(128, offs[g + 1] - ti.row0);
+    ti.row0 = offs[g] + ((q - mt_start[g]) * CL + rank) * 128;
+    ti.rows = min(128, offs[g + 1] - ti.row0);   // (none: a pair's second half)
     return ti;
 }
 
@@ -134,22 +150,21 @@ __device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[16]) {
         : "memory");
 }
 
-template <int MODE, int AB, int BN, int ST>   // ST: stages of codes in shared memory
+template <int MODE, int AB, int BN, int ST, int CL>   // ST: stages of codes in shared memory
 __global__ void __launch_bounds__(kThreads, 1) mx4_gemm_kernel(const __grid_constant__ Mx4Params p) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-    using SH = Shape<MODE, AB, BN, ST>;
-    constexpr int NACC = SH::NACC;
+    using SH = Shape<MODE, AB, BN, ST, CL>;
     uint8_t *sf = smem + ST * SH::STAGE;
-    uint8_t *out_s = sf + kSfSlots * SH::SLOT;
+    uint8_t *out_s = sf + SH::SLOTS * SH::SLOT;
     uint64_t *full = reinterpret_cast<uint64_t *>(out_s + SH::OUT);
     uint64_t *empty = full + ST;
-    uint64_t *sffull = empty + ST;          // a slot's scale rows have come
-    uint64_t *sfready = sffull + kSfSlots;  // ... and are turned
-    uint64_t *sfempty = sfready + kSfSlots; // ... and copied into tensor memory
-    uint64_t *tfull = sfempty + kSfSlots;
-    uint64_t *tempty = tfull + NACC;
-    uint64_t *done = tempty + NACC;
+    uint64_t *sfready = empty + ST;          // a slot's scales are there
+    uint64_t *sfempty = sfready + SH::SLOTS; // ... and copied into tensor memory
+    uint64_t *tfull = sfempty + SH::SLOTS;   // [2]
+    uint64_t *tempty = tfull + 2;           // [2]
+    uint64_t *tover = tempty + 2;           // a tile's shared columns have been read
+    uint64_t *done = tover + 1;
     uint32_t *tmem_base_s = reinterpret_cast<uint32_t *>(done + 1);
     volatile int *abort_s = reinterpret_cast<volatile int *>(tmem_base_s + 1);
     int *offs = reinterpret_cast<int *>(out_s + SH::OUT + kBars);
@@ -163,15 +178,15 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_gemm_kernel(const __grid_cons
             mbar_init(&full[s], 1);
             mbar_init(&empty[s], 1);
         }
-        for (int s = 0; s < kSfSlots; ++s) {
-            mbar_init(&sffull[s], 1);
-            mbar_init(&sfready[s], 2);
+        for (int s = 0; s < SH::SLOTS; ++s) {
+            mbar_init(&sfready[s], (1 + SH::NB) * CL);
             mbar_init(&sfempty[s], 1);
         }
-        for (int a = 0; a < NACC; ++a) {
+        for (int a = 0; a < 2; ++a) {
             mbar_init(&tfull[a], 1);
-            mbar_init(&tempty[a], kEpi);
+            mbar_init(&tempty[a], kEpi * CL);
         }
+        mbar_init(tover, kEpi / 2 * CL);
         mbar_init(done, 1);
         *abort_s = 0;
         fence_barrier_init();
@@ -179,16 +194,19 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_gemm_kernel(const __grid_cons
     if (warp == 0 && lane == 0) {
         tma_prefetch_desc(&p.tmA);
         tma_prefetch_desc(&p.tmB);
-        tma_prefetch_desc(&p.tmSA);
-        tma_prefetch_desc(&p.tmSB);
     }
     if (warp == 1) {
-        tmem_alloc(tmem_base_s, 512);
-        tmem_relinquish();
+        if constexpr (CL == 2) {
+            tmem_alloc_pair(tmem_base_s, 512);
+            tmem_relinquish_pair();
+        } else {
+            tmem_alloc(tmem_base_s, 512);
+            tmem_relinquish();
+        }
     }
     wait_for_kernels_ahead();
     if (warp == 2) {
-        // group offsets and the exclusive prefix of their 128-row tiles
+        // group offsets and the exclusive prefix of their row tiles
         int carry = 0;
         for (int base = 0; base <= p.G; base += 32) {
             const int g = base + lane;
@@ -201,7 +219,7 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_gemm_kernel(const __grid_cons
             if (g < p.G) {
                 const int end = row_offset(p.offsets[g + 1], p.max_rows);
                 ok = ok && end >= o;
-                mt = max(0, (end - o + 127) >> 7);
+                mt = max(0, (end - o + 128 * CL - 1) / (128 * CL));
             }
             if (!ok && blockIdx.x == 0) record_status(p.status, MOE_ERR_INVALID_ARG);
             int incl = mt;
@@ -217,53 +235,50 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_gemm_kernel(const __grid_cons
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    // a pair's commits and arrivals reach both CTAs' barriers, initialised by now
+    if constexpr (CL == 2) cluster_sync_all();
     let_kernels_behind_begin();
 
+    const int rank = CL == 2 ? (int)cluster_ctarank() : 0;
+    const int first = blockIdx.x / CL, step = gridDim.x / CL;
     const uint32_t tmem_base = *tmem_base_s;
     const WaitCtl wc{abort_s, p.status, p.wait_limit};
     const long long total = (long long)mt_start[p.G] * p.n_tiles;
 
-    if (warp < kEpi0) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsFew));
     if (warp == 0) {
         // ------------------------------------------------ TMA producer
-        uint32_t s = 0, ph = 0, j = 0, jph = 0;
-        uint32_t begun = 0, sf_begun = 0;   // stages and slots with a copy, and its parity
+        uint32_t s = 0, ph = 0;
+        uint32_t begun = 0;   // stages with a copy, and its parity
         bool ok = true;
         int g = 0;
-        Walk at(p.n_tiles);
-        for (long long t = blockIdx.x; ok && t < total; t += gridDim.x, at.next()) {
-            const Tile ti = find_tile(p, at.q, at.nt, mt_start, offs, g);
+        Walk at(p.n_tiles, first, step);
+        for (long long t = first; ok && t < total; t += step, at.next()) {
+            const Tile ti = find_tile<CL>(p, at.q, at.nt, mt_start, offs, g, rank);
             g = ti.g;
+            // B's first row; FFN1: of the gate, whose up row is I further on
             const int br = MODE == MX4_FFN1 ? g * 2 * p.I + ti.nt * (BN / 2) : g * p.N + ti.nt * BN;
             for (int kb = 0; kb < p.kb; ++kb) {
-                if (kb % SH::SPS == 0) {
-                    if (!mbar_wait_warp(&sfempty[j], jph ^ 1u, wc)) { ok = false; break; }
-                    if (lane == 0) {
-                        uint8_t *a = sf + j * SH::SLOT;
-                        uint8_t *b = a + kSfRegion;
-                        const int x = kb / SH::SPS * 16;
-                        mbar_arrive_expect_tx(&sffull[j], (p.a_rows + BN) * 16);
-                        tma_load_2d(a, &p.tmSA, &sffull[j], x, ti.row0);
-                        tma_load_2d(b, &p.tmSB, &sffull[j], x, br);
-                        if constexpr (MODE == MX4_FFN1)
-                            tma_load_2d(b + BN / 2 * 16, &p.tmSB, &sffull[j], x, br + p.I);
-                    }
-                    sf_begun = (sf_begun & ~(0x10001u << j)) | (0x10000u << j) | (jph << j);
-                    if (++j == kSfSlots) { j = 0; jph ^= 1u; }
-                }
                 if (!mbar_wait_warp(&empty[s], ph ^ 1u, wc)) { ok = false; break; }
                 if (lane == 0) {
                     uint8_t *a = smem + s * SH::STAGE;
                     uint8_t *b = a + kCodeA;
-                    // (a copy that expands counts the bytes that it reads)
-                    mbar_arrive_expect_tx(&full[s], p.a_rows * 128 + BN * (AB == 4 ? 128 : 64));
-                    tma_load_2d(a, &p.tmA, &full[s], kb * 128, ti.row0);
-                    // coordinates count elements: bytes for packed pairs, 4-bit elements
-                    // where the copy expands them
-                    tma_load_2d(b, &p.tmB, &full[s], kb * 128, br);
-                    if constexpr (MODE == MX4_FFN1)
-                        tma_load_2d(b + BN / 2 * 128, &p.tmB, &full[s], kb * 128, br + p.I);
+                    // Coordinates count elements: bytes for packed pairs, 4-bit elements where
+                    // the copy expands them (which counts the bytes that it reads).  A pair's
+                    // copies all arrive on the even CTA's barrier.
+                    if (CL == 1 || rank == 0)
+                        mbar_arrive_expect_tx(&full[s], CL * (p.a_rows * 128 +
+                                                              BN / CL * (AB == 4 ? 128 : 64)));
+                    if (CL == 2 && rank == 1) {
+                        const uint32_t bar = dsmem_map(&full[s], 0);
+                        tma_load_2d_pairbar(a, &p.tmA, bar, kb * 128, ti.row0);
+                        tma_load_2d_pairbar(b, &p.tmB, bar, kb * 128,
+                                            br + (MODE == MX4_FFN1 ? p.I : BN / 2));
+                    } else {
+                        tma_load_2d(a, &p.tmA, &full[s], kb * 128, ti.row0);
+                        tma_load_2d(b, &p.tmB, &full[s], kb * 128, br);
+                        if constexpr (MODE == MX4_FFN1 && CL == 1)
+                            tma_load_2d(b + BN / 2 * 128, &p.tmB, &full[s], kb * 128, br + p.I);
+                    }
                 }
                 begun = (begun & ~(0x10001u << s)) | (0x10000u << s) | (ph << s);
                 if (++s == ST) { s = 0; ph ^= 1u; }
@@ -271,12 +286,16 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_gemm_kernel(const __grid_cons
         }
         if (!ok) {
             // drain the copies still in flight before the CTA exits
-            for (int i = 0; i < ST; ++i)
-                if (begun >> (16 + i) & 1u)
-                    mbar_wait_teardown(&full[i], begun >> i & 1u, p.wait_limit);
-            for (int i = 0; i < kSfSlots; ++i)
-                if (sf_begun >> (16 + i) & 1u)
-                    mbar_wait_teardown(&sffull[i], sf_begun >> i & 1u, p.wait_limit);
+            if (CL == 2 && rank == 1) {
+                // (those of codes arrive on the even CTA's barriers, which this one cannot
+                // wait on: a copy takes microseconds, this about a millisecond)
+                const long long t0 = clock64();
+                while (clock64() - t0 < (1LL << 21)) __nanosleep(1000);
+            } else {
+                for (int i = 0; i < ST; ++i)
+                    if (begun >> (16 + i) & 1u)
+                        mbar_wait_teardown(&full[i], begun >> i & 1u, p.wait_limit);
+            }
         }
     } else if (warp == 1) {
         // ------------------------------------------------ MMA issuer
@@ -285,14 +304,24 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_gemm_kernel(const __grid_cons
         uint32_t s = 0, ph = 0, j = 0, jph = 0, turn = 0;
         int it = 0;
         bool ok = true;
-        for (long long t = blockIdx.x; ok && t < total; t += gridDim.x, ++it) {
-            const uint32_t acc = it % NACC, aph = (it / NACC) & 1u;
-            if (!mbar_wait_warp(&tempty[acc], aph ^ 1u, wc)) { ok = false; break; }
-            const uint32_t d = tmem_base + acc * BN;
+        auto commit = [&](uint64_t *bar) {
+            if constexpr (CL == 2) umma_commit_pair(bar, 0x3);
+            else umma_commit(bar);
+        };
+        for (long long t = first; rank == 0 && ok && t < total; t += step, ++it) {
+            if (!mbar_wait_warp(&tempty[it & 1], ((it >> 1) & 1u) ^ 1u, wc) ||
+                (SH::OVER > 0 && it > 0 && !mbar_wait_warp(tover, (it - 1) & 1u, wc))) {
+                ok = false;
+                break;
+            }
+            const uint32_t d = tmem_base + (it & 1) * SH::ACC1;
             for (int kb = 0; kb < p.kb; ++kb) {
                 const int w0 = kb % SH::SPS * SH::WORDS;   // first word of the slot's rows
-                if (w0 == 0 && !mbar_wait_warp(&sfready[j], jph, wc)) { ok = false; break; }
-                if (!mbar_wait_warp(&full[s], ph, wc)) { ok = false; break; }
+                if ((w0 == 0 && !mbar_wait_warp(&sfready[j], jph, wc)) ||
+                    !mbar_wait_warp(&full[s], ph, wc)) {
+                    ok = false;
+                    break;
+                }
                 tc_fence_after();
                 const bool last = kb + 1 == p.kb;
                 const bool slot_done = last || w0 + SH::WORDS == 4;
@@ -303,177 +332,240 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_gemm_kernel(const __grid_cons
 #pragma unroll
                     for (int w = 0; w < SH::WORDS; ++w) {
 #pragma unroll
-                        for (int r = 0; r < 1 + SH::NB; ++r)
-                            tmem_cp_scales(sfa + w * 4 * (1 + SH::NB) + 4 * r,
-                                           sd + w * 32 + r * (kSfRegion / 16));
+                        for (int r = 0; r < 1 + SH::NB; ++r) {
+                            const uint32_t col = sfa + 4 * (w * (1 + SH::NB) + r);
+                            const uint64_t src = sd + w * 32 + r * (kSfRegion / 16);
+                            if constexpr (CL == 2) tmem_cp_scales_pair(col, src);
+                            else tmem_cp_scales(col, src);
+                        }
                     }
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const uint32_t more = (kb | i) != 0 ? 1u : 0u;
+                        const uint32_t sa = AB == 4 ? sfa + i / 2 * 4 * (1 + SH::NB) : sfa;
+                        const uint64_t a = ad + 2 * i, b = bd + 2 * i;
                         if constexpr (AB == 4) {
-                            const uint32_t a = sfa + i / 2 * 4 * (1 + SH::NB);
-                            umma_mxf4(d, ad + 2 * i, bd + 2 * i, idesc_mxf4_f32(128, BN, i % 2 * 2),
-                                      a, a + 4, more);
+                            constexpr int M = 128 * CL;
+                            if constexpr (CL == 2)
+                                umma_mxf4_pair(d, a, b, idesc_mxf4_f32(M, BN, i % 2 * 2), sa, sa + 4, more);
+                            else
+                                umma_mxf4(d, a, b, idesc_mxf4_f32(M, BN, i % 2 * 2), sa, sa + 4, more);
                         } else {
-                            umma_mxf8(d, ad + 2 * i, bd + 2 * i, idesc_mxf8_e2m1_f32(128, BN, i),
-                                      sfa, sfa + 4, more);
+                            constexpr int M = 128 * CL;
+                            if constexpr (CL == 2)
+                                umma_mxf8_pair(d, a, b, idesc_mxf8_e2m1_f32(M, BN, i), sa, sa + 4, more);
+                            else
+                                umma_mxf8(d, a, b, idesc_mxf8_e2m1_f32(M, BN, i), sa, sa + 4, more);
                         }
                     }
-                    umma_commit(&empty[s]);
-                    if (slot_done) umma_commit(&sfempty[j]);
-                    if (last) umma_commit(&tfull[acc]);
+                    commit(&empty[s]);
+                    if (slot_done) commit(&sfempty[j]);
+                    if (last) commit(&tfull[it & 1]);
                 }
                 __syncwarp();
                 turn ^= 1u;
-                if (slot_done && ++j == kSfSlots) { j = 0; jph ^= 1u; }
+                if (slot_done && ++j == SH::SLOTS) { j = 0; jph ^= 1u; }
                 if (++s == ST) { s = 0; ph ^= 1u; }
             }
         }
-        if (!ok) {
-            // every MMA this thread issued must finish before TMEM is freed
-            if (elect_one()) umma_commit(done);
+        if (rank == 0 && (CL == 2 || !ok)) {
+            // every MMA of this thread must finish before TMEM is freed (a pair's, before
+            // either CTA's operands go away)
+            if (elect_one()) {
+                if constexpr (CL == 2) umma_commit_pair(done, 0x1);
+                else umma_commit(done);
+            }
             __syncwarp();
             mbar_wait_teardown(done, 0, p.wait_limit);
         }
-    } else {
+    } else if (warp < kEpi0) {
         // ------------------------------------------------ scales
-        // Regions of 128 rows x 16 bytes (A, then B), one warp each in turn: word w of row
-        // 32 c + l goes to byte 4 c of row l of block w.  In place: every lane has its four
-        // rows in registers before the first is written.
+        // Warp m: the region of 128 rows of A (m = 0) or of B.  Row 32 c + l is lane l's
+        // v[c]; its word w goes to word c of row l of block w.
+        const int m = warp - kScale0;
         uint32_t j = 0, jph = 0;
-        bool ok = true;
-        for (long long t = blockIdx.x; ok && t < total; t += gridDim.x) {
-            for (int k0 = 0; k0 < p.blocks; k0 += 16) {
-                if (!mbar_wait_warp(&sffull[j], jph, wc)) { ok = false; break; }
-                // scales behind the row's end (its padding may hold anything, a NaN too)
-                // multiply zeros: they become zeros
-                const int left = p.blocks - k0;
-                uint32_t mask[4];
+        Walk at(p.n_tiles, first, step);
+        int g = 0, slot = 0;
+        const int slots = (p.blocks + 15) / 16;
+        long long t = first;
+        const uint8_t *src[4];
+        // the rows of tile t (rows that are not there: any others, for products that go
+        // nowhere)
+        auto rows_of_tile = [&] {
+            if (t >= total) return;
+            const Tile ti = find_tile<CL>(p, at.q, at.nt, mt_start, offs, g, rank);
+            g = ti.g;
 #pragma unroll
-                for (int w = 0; w < 4; ++w) {
-                    const int n = min(4, max(0, left - 4 * w));
-                    mask[w] = n == 4 ? 0xFFFFFFFFu : (1u << (8 * n)) - 1u;
+            for (int c = 0; c < 4; ++c) {
+                if (m == 0) {
+                    src[c] = p.sa + (size_t)min(ti.row0 + 32 * c + lane, p.max_rows - 1) * p.pitch;
+                } else {
+                    long long r;
+                    if constexpr (MODE == MX4_FFN1) {
+                        const int i = (m - 1) * 128 + 32 * c;   // of the tile's B rows
+                        r = (long long)g * 2 * p.I + ti.nt * (BN / 2) + i % (BN / 2) +
+                            (i >= BN / 2 ? p.I : 0) + lane;
+                    } else {
+                        r = (long long)g * p.N + ti.nt * BN + (m - 1) * 128 + 32 * c + lane;
+                    }
+                    src[c] = p.sb + (size_t)min(r, p.b_rows - 1) * p.pitch;
                 }
+            }
+        };
+        uint4 v[kAhead][4];
+        int at_slot[kAhead];   // slot of the row that v[.] holds, or -1 behind the last tile
+        auto load = [&](int i) {
+            at_slot[i] = -1;
+            if (t >= total) return;
+            at_slot[i] = slot;
 #pragma unroll
-                for (int r = 0; r < 1 + SH::NB; ++r) {
-                    if ((r & 1) != warp - 2) continue;
-                    uint8_t *reg = sf + j * SH::SLOT + r * kSfRegion;
-                    uint4 v[4];
+            for (int c = 0; c < 4; ++c)
+                if (m == 0 || 32 * c < BN)
+                    v[i][c] = __ldg(reinterpret_cast<const uint4 *>(src[c]) + slot);
+                else
+                    v[i][c] = make_uint4(0, 0, 0, 0);
+            if (++slot == slots) {
+                slot = 0;
+                t += step;
+                at.next();
+                rows_of_tile();
+            }
+        };
+        if (m < 1 + SH::NB) {
+            rows_of_tile();
 #pragma unroll
-                    for (int c = 0; c < 4; ++c)
-                        v[c] = *reinterpret_cast<const uint4 *>(reg + (32 * c + lane) * 16);
+            for (int i = 0; i < kAhead; ++i) load(i);
+            bool ok = true;
+            while (ok) {
+#pragma unroll
+                for (int i = 0; i < kAhead; ++i) {
+                    if (!ok || at_slot[i] < 0) { ok = false; continue; }
+                    // scales behind the row's end (its padding may hold anything, a NaN too)
+                    // multiply zeros: they become zeros
+                    const int left = p.blocks - 16 * at_slot[i];
+                    uint32_t mask[4];
+#pragma unroll
+                    for (int w = 0; w < 4; ++w) {
+                        const int n = min(4, max(0, left - 4 * w));
+                        mask[w] = n == 4 ? 0xFFFFFFFFu : (1u << (8 * n)) - 1u;
+                    }
+                    ok = mbar_wait_warp(&sfempty[j], jph ^ 1u, wc);
+                    if (!ok) continue;
+                    const uint4(&x)[4] = v[i];
+                    const uint32_t a = smem_u32(sf + j * SH::SLOT + m * kSfRegion) + lane * 16;
+                    st_shared_v4(a, x[0].x & mask[0], x[1].x & mask[0], x[2].x & mask[0],
+                                 x[3].x & mask[0]);
+                    st_shared_v4(a + 512, x[0].y & mask[1], x[1].y & mask[1], x[2].y & mask[1],
+                                 x[3].y & mask[1]);
+                    st_shared_v4(a + 1024, x[0].z & mask[2], x[1].z & mask[2], x[2].z & mask[2],
+                                 x[3].z & mask[2]);
+                    st_shared_v4(a + 1536, x[0].w & mask[3], x[1].w & mask[3], x[2].w & mask[3],
+                                 x[3].w & mask[3]);
+                    fence_proxy_async_smem();   // the copies into tensor memory read them
                     __syncwarp();
-                    const uint32_t a = smem_u32(reg) + lane * 16;
-                    st_shared_v4(a, v[0].x & mask[0], v[1].x & mask[0], v[2].x & mask[0],
-                                 v[3].x & mask[0]);
-                    st_shared_v4(a + 512, v[0].y & mask[1], v[1].y & mask[1], v[2].y & mask[1],
-                                 v[3].y & mask[1]);
-                    st_shared_v4(a + 1024, v[0].z & mask[2], v[1].z & mask[2], v[2].z & mask[2],
-                                 v[3].z & mask[2]);
-                    st_shared_v4(a + 1536, v[0].w & mask[3], v[1].w & mask[3], v[2].w & mask[3],
-                                 v[3].w & mask[3]);
+                    if (lane == 0) {
+                        if (rank == 0) mbar_arrive(&sfready[j]);
+                        else mbar_arrive_remote_own(dsmem_map(&sfready[j], 0));
+                    }
+                    if (++j == SH::SLOTS) { j = 0; jph ^= 1u; }
+                    load(i);
                 }
-                fence_proxy_async_smem();   // the copies into tensor memory read them
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&sfready[j]);
-                if (++j == kSfSlots) { j = 0; jph ^= 1u; }
             }
         }
-    }
     } else {
         // ------------------------------------------------ epilogue
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsMany));
         const int q = warp & 3;                // TMEM lane quadrant
         const int part = (warp - kEpi0) >> 2;  // its half of the columns
         const int r_local = q * 32 + lane;
         uint8_t *piece = out_s + (warp - kEpi0) * kPiece;
+        // Up to 64 columns at a time: CN chunks of CH.  (FFN1: a chunk of gate columns and
+        // the up columns that go with it.)
+        constexpr int CW = BN / 2;                           // accumulator columns of this warp
+        constexpr int CH = CW < 32 ? CW : 32, CN = CW < 64 ? 1 : 2, PH = CW / (CH * CN);
         int it = 0, g = 0;
-        Walk at(p.n_tiles);
-        for (long long t = blockIdx.x; t < total; t += gridDim.x, at.next(), ++it) {
-            const Tile ti = find_tile(p, at.q, at.nt, mt_start, offs, g);
+        Walk at(p.n_tiles, first, step);
+        auto arrive = [&](uint64_t *bar) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                if (rank == 0) mbar_arrive(bar);
+                else mbar_arrive_remote_relaxed(dsmem_map(bar, 0));
+            }
+        };
+        for (long long t = first; t < total; t += step, at.next(), ++it) {
+            const Tile ti = find_tile<CL>(p, at.q, at.nt, mt_start, offs, g, rank);
             g = ti.g;
             const bool valid = r_local < ti.rows;
             const int row = ti.row0 + r_local;
             float w = 1.0f;
             if (MODE == MX4_ROWS && valid && p.row_w && row < p.w_rows) w = __ldg(p.row_w + row);
-            const uint32_t acc = it % NACC, aph = (it / NACC) & 1u;
-            if (!mbar_wait_warp(&tfull[acc], aph, wc)) break;
+            if (!mbar_wait_warp(&tfull[it & 1], (it >> 1) & 1u, wc)) break;
             tc_fence_after();
-            const uint32_t tb = tmem_base + ((uint32_t)(q * 32) << 16) + acc * BN;
-            auto release = [&] {
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&tempty[acc]);
-            };
-            if constexpr (MODE == MX4_FFN1) {
-                constexpr int HC = BN / 4;   // h columns of this warp
-                uint32_t rg[HC / 32][32], ru[HC / 32][32];
+            const uint32_t tb = tmem_base + ((uint32_t)(q * 32) << 16) + (it & 1) * SH::ACC1;
+            // the columns that the next accumulator takes first: the last ones of the first
+            // accumulator, the first ones of the second
+            const bool down = SH::OVER > 0 && (it & 1) == 0;
 #pragma unroll
-                for (int c = 0; c < HC / 32; ++c) {
-                    tmem_ld(tb + part * HC + 32 * c, rg[c]);
-                    tmem_ld(tb + BN / 2 + part * HC + 32 * c, ru[c]);
-                }
+            for (int i = 0; i < PH; ++i) {
+                const int ph = down ? PH - 1 - i : i;
+                const int c0 = MODE == MX4_FFN1 ? part * (CW / 2) + ph * CH
+                                                : part * CW + ph * CN * CH;
+                uint32_t r[CN][CH];
+#pragma unroll
+                for (int c = 0; c < CN; ++c)
+                    tmem_ld(tb + c0 + c * (MODE == MX4_FFN1 ? BN / 2 : CH), r[c]);
                 tmem_wait_ld();
-                release();
-                if (valid) {
-#pragma unroll
-                    for (int c = 0; c < HC / 32; ++c) {
+                if (SH::OVER > 0 && i == 0 && part == (down ? 1 : 0)) arrive(tover);
+                if (i == PH - 1) arrive(&tempty[it & 1]);
+                if constexpr (MODE == MX4_FFN1) {
+                    if (valid) {
                         float h[32];
 #pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            h[i] = swiglu_clamped_nan(__uint_as_float(rg[c][i]),
-                                                      __uint_as_float(ru[c][i]), p.clamp);
+                        for (int e = 0; e < 32; ++e)
+                            h[e] = swiglu_clamped_nan(__uint_as_float(r[0][e]),
+                                                      __uint_as_float(r[CN - 1][e]), p.clamp);
                         uint32_t wq[8];
                         const uint32_t code = mx_quantize_block(h, wq);
-                        const int col = ti.nt * (BN / 2) + part * HC + 32 * c;
+                        const int col = ti.nt * (BN / 2) + c0;
                         uint8_t *dst = p.hq + (size_t)row * p.I + col;
                         st_global_v4(dst, wq[0], wq[1], wq[2], wq[3]);
                         st_global_v4(dst + 16, wq[4], wq[5], wq[6], wq[7]);
                         p.hsf[(size_t)row * p.h_pitch + col / 32] = (uint8_t)code;
                     }
-                }
-            } else {
-                constexpr int CW = BN / 2, CH = CW < 32 ? CW : 32;   // columns of this warp
-                uint32_t o[CW / 2];
+                } else {
 #pragma unroll
-                for (int c = 0; c < CW / CH; ++c) {
-                    uint32_t r[CH];
-                    tmem_ld(tb + part * CW + CH * c, r);
-                    tmem_wait_ld();
+                    for (int c = 0; c < CN; ++c) {
+                        const int col = ti.nt * BN + c0 + c * CH;
+                        uint32_t o[CH / 2];
 #pragma unroll
-                    for (int i = 0; i < CH / 2; ++i)
-                        o[c * (CH / 2) + i] = pack_bf16x2(w * __uint_as_float(r[2 * i]),
-                                                          w * __uint_as_float(r[2 * i + 1]));
-                }
-                release();
-                const int col0 = ti.nt * BN + part * CW;
-                if (SH::TMA_OUT && q * 32 + 32 <= ti.rows) {
-                    // 32 columns at a time through shared memory, from where one thread's
-                    // TMA store takes all 32 rows
+                        for (int e = 0; e < CH / 2; ++e)
+                            o[e] = pack_bf16x2(w * __uint_as_float(r[c][2 * e]),
+                                               w * __uint_as_float(r[c][2 * e + 1]));
+                        if (SH::TMA_OUT && q * 32 + 32 <= ti.rows) {
+                            // through shared memory, from where one thread's TMA store takes
+                            // all 32 rows
+                            if (lane == 0) bulk_wait_group_read<0>();   // the last piece has left
+                            __syncwarp();
+                            const uint32_t sw = (uint32_t)((lane >> 1) & 3);
 #pragma unroll
-                    for (int c = 0; c < CW / CH; ++c) {
-                        if (lane == 0) bulk_wait_group_read<0>();   // the last piece has left
-                        __syncwarp();
-                        const uint32_t sw = (uint32_t)((lane >> 1) & 3);
+                            for (int e = 0; e < CH / 8; ++e)
+                                st_shared_v4(smem_u32(piece) + lane * 64 + (((uint32_t)e ^ sw) << 4),
+                                             o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+                            fence_proxy_async_smem();
+                            __syncwarp();
+                            if (lane == 0 && col < p.N) {
+                                tma_store_2d(&p.tmO, piece, col, row);
+                                bulk_commit_group();
+                            }
+                        } else if (valid) {
+                            uint16_t *dst = p.out + (size_t)row * p.N + col;
 #pragma unroll
-                        for (int i = 0; i < CH / 8; ++i)
-                            st_shared_v4(smem_u32(piece) + lane * 64 + (((uint32_t)i ^ sw) << 4),
-                                         o[c * (CH / 2) + 4 * i], o[c * (CH / 2) + 4 * i + 1],
-                                         o[c * (CH / 2) + 4 * i + 2], o[c * (CH / 2) + 4 * i + 3]);
-                        fence_proxy_async_smem();
-                        __syncwarp();
-                        if (lane == 0 && col0 + CH * c < p.N) {
-                            tma_store_2d(&p.tmO, piece, col0 + CH * c, row);
-                            bulk_commit_group();
+                            for (int e = 0; e < CH / 8; ++e)
+                                if (col + 8 * e < p.N)
+                                    st_global_v4(dst + 8 * e, o[4 * e], o[4 * e + 1], o[4 * e + 2],
+                                                 o[4 * e + 3]);
                         }
                     }
-                } else if (valid) {
-                    uint16_t *dst = p.out + (size_t)row * p.N + col0;
-#pragma unroll
-                    for (int i = 0; i < CW / 8; ++i)
-                        if (col0 + 8 * i < p.N)
-                            st_global_v4(dst + 8 * i, o[4 * i], o[4 * i + 1], o[4 * i + 2],
-                                         o[4 * i + 3]);
                 }
             }
         }
@@ -483,30 +575,56 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_gemm_kernel(const __grid_cons
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == 1) tmem_dealloc(tmem_base, 512);
+    if constexpr (CL == 2) {
+        // neither CTA leaves while the other may still signal it
+        cluster_sync_all();
+        if (warp == 1) tmem_dealloc_pair(tmem_base, 512);
+        cluster_sync_all();
+    } else {
+        if (warp == 1) tmem_dealloc(tmem_base, 512);
+    }
 }
 
-template <int MODE, int AB, int BN, int ST>
+// max_tiles: upper bound of the tiles (of 128 CL rows).
+template <int MODE, int AB, int BN, int ST, int CL>
 moe_status launch_mx4(Mx4Params &p, long long max_tiles, cudaStream_t st) {
-    using SH = Shape<MODE, AB, BN, ST>;
-    auto kern = mx4_gemm_kernel<MODE, AB, BN, ST>;
-    static bool attr_set[64] = {};
+    using SH = Shape<MODE, AB, BN, ST, CL>;
+    auto kern = mx4_gemm_kernel<MODE, AB, BN, ST, CL>;
+    static int resident[64] = {};   // CTAs or pairs at once
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return MOE_ERR_CUDA;
     if (dev < 0 || dev >= 64) return MOE_ERR_UNSUPPORTED;
-    if (!attr_set[dev]) {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = CL;
+    at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+    cfg.gridDim = dim3(num_sms() / CL * CL);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kSmem;
+    cfg.stream = st;
+    cfg.attrs = at;
+    cfg.numAttrs = CL == 1 ? 1 : 2;
+    if (!resident[dev]) {
         if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) !=
             cudaSuccess)
             return MOE_ERR_CUDA;
-        attr_set[dev] = true;
+        int n = num_sms();
+        if (CL == 2 && (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess || n < 1))
+            return MOE_ERR_CUDA;
+        resident[dev] = n;
     }
-    static_assert(SH::smem(BN == 256 ? kWideGroups : kMaxGroups) <= kSmem, "shared memory");
     if (max_tiles <= 0) return MOE_OK;
     p.status = device_status_ptr();
     if (!p.status) return MOE_ERR_CUDA;
     p.wait_limit = kWaitLimitCycles;
-    const int grid = max_tiles < num_sms() ? (int)max_tiles : num_sms();
-    return launch_early(kern, dim3(grid), kThreads, SH::smem(p.G), st, p);
+    const int n = max_tiles < resident[dev] ? (int)max_tiles : resident[dev];
+    cfg.gridDim = dim3(n * CL);
+    cfg.dynamicSmemBytes = SH::smem(p.G);
+    if (cudaLaunchKernelEx(&cfg, kern, p) != cudaSuccess) return MOE_ERR_CUDA;
+    return cuda_status(cudaGetLastError());
 }
 
 // Rows of A's boxes: no more than there are (the MMAs' other rows take whatever the
@@ -531,9 +649,15 @@ int rows_bn(int max_rows, int G, int N) {
     return best;
 }
 
+// Pairs of row tiles, where groups hold several.
+bool pairs(int max_rows, int G) { return max_rows >= 256LL * G; }
+
 bool encode_operands(Mx4Params &p, int bits, const uint8_t *aq, const uint8_t *asf, int max_rows,
                      const uint8_t *bq, const uint8_t *bsf, uint64_t brows, int b_box, int K) {
-    const int sfp = mx_sf_pitch(K);
+    p.sa = asf;
+    p.sb = bsf;
+    p.pitch = mx_sf_pitch(K);
+    p.b_rows = (long long)brows;
     p.max_rows = max_rows;
     p.a_rows = box_rows(max_rows);
     p.blocks = K / 32;
@@ -541,9 +665,7 @@ bool encode_operands(Mx4Params &p, int bits, const uint8_t *aq, const uint8_t *a
     const int row = bits == 4 ? K / 2 : K;
     return encode_tmap_u8_2d(&p.tmA, aq, row, max_rows, row, 128, p.a_rows, 128) &&
            (bits == 4 ? encode_tmap_u8_2d(&p.tmB, bq, K / 2, brows, K / 2, 128, b_box, 128)
-                      : encode_tmap_u4_expand_2d(&p.tmB, bq, K, brows, b_box)) &&
-           encode_tmap_u8_2d(&p.tmSA, asf, sfp, max_rows, sfp, 16, p.a_rows, 0) &&
-           encode_tmap_u8_2d(&p.tmSB, bsf, sfp, brows, sfp, 16, b_box, 0);
+                      : encode_tmap_u4_expand_2d(&p.tmB, bq, K, brows, b_box));
 }
 
 }  // namespace
@@ -555,7 +677,8 @@ moe_status launch_mx4_matmul(const uint8_t *aq, const uint8_t *asf, int bits,
     Mx4Params p;
     std::memset(&p, 0, sizeof p);
     const int BN = rows_bn(max_rows, G, N);
-    if (!encode_operands(p, bits, aq, asf, max_rows, bq, bsf, (uint64_t)G * N, BN, K) ||
+    const int b_box = BN == 256 && pairs(max_rows, G) ? 128 : BN;
+    if (!encode_operands(p, bits, aq, asf, max_rows, bq, bsf, (uint64_t)G * N, b_box, K) ||
         (BN >= 64 && !encode_tmap_bf16_2d_sw64(&p.tmO, out, N, max_rows, 2ULL * N, 32, 32)))
         return MOE_ERR_CUDA;
     p.offsets = offsets;
@@ -565,20 +688,25 @@ moe_status launch_mx4_matmul(const uint8_t *aq, const uint8_t *asf, int bits,
     p.row_w = row_w;
     p.w_rows = w_rows;
     p.out = out;
+    if (BN == 256 && pairs(max_rows, G)) {
+        const long long t = (long long)row_pair_bound(max_rows, G) * p.n_tiles;
+        return bits == 4 ? launch_mx4<MX4_ROWS, 4, 256, 5, 2>(p, t, st)
+                         : launch_mx4<MX4_ROWS, 8, 256, 6, 2>(p, t, st);
+    }
     const long long tiles = (long long)row_tile_bound(max_rows, G) * p.n_tiles;
     if (bits == 4) {
         switch (BN) {
-        case 256: return launch_mx4<MX4_ROWS, 4, 256, 4>(p, tiles, st);
-        case 128: return launch_mx4<MX4_ROWS, 4, 128, 5>(p, tiles, st);
-        case 64: return launch_mx4<MX4_ROWS, 4, 64, 7>(p, tiles, st);
-        default: return launch_mx4<MX4_ROWS, 4, 32, 8>(p, tiles, st);
+        case 256: return launch_mx4<MX4_ROWS, 4, 256, 4, 1>(p, tiles, st);
+        case 128: return launch_mx4<MX4_ROWS, 4, 128, 5, 1>(p, tiles, st);
+        case 64: return launch_mx4<MX4_ROWS, 4, 64, 7, 1>(p, tiles, st);
+        default: return launch_mx4<MX4_ROWS, 4, 32, 8, 1>(p, tiles, st);
         }
     }
     switch (BN) {
-    case 256: return launch_mx4<MX4_ROWS, 8, 256, 4>(p, tiles, st);
-    case 128: return launch_mx4<MX4_ROWS, 8, 128, 5>(p, tiles, st);
-    case 64: return launch_mx4<MX4_ROWS, 8, 64, 7>(p, tiles, st);
-    default: return launch_mx4<MX4_ROWS, 8, 32, 8>(p, tiles, st);
+    case 256: return launch_mx4<MX4_ROWS, 8, 256, 4, 1>(p, tiles, st);
+    case 128: return launch_mx4<MX4_ROWS, 8, 128, 5, 1>(p, tiles, st);
+    case 64: return launch_mx4<MX4_ROWS, 8, 64, 7, 1>(p, tiles, st);
+    default: return launch_mx4<MX4_ROWS, 8, 32, 8, 1>(p, tiles, st);
     }
 }
 
@@ -599,9 +727,12 @@ moe_status launch_mx4_ffn1(const uint8_t *xq, const uint8_t *xsf, const int32_t 
     p.hq = hq;
     p.hsf = hsf;
     p.h_pitch = mx_sf_pitch(I);
+    if (BN == 256 && pairs(max_rows, G))
+        return launch_mx4<MX4_FFN1, 8, 256, 6, 2>(
+            p, (long long)row_pair_bound(max_rows, G) * p.n_tiles, st);
     const long long tiles = (long long)row_tile_bound(max_rows, G) * p.n_tiles;
-    return BN == 256 ? launch_mx4<MX4_FFN1, 8, 256, 4>(p, tiles, st)
-                     : launch_mx4<MX4_FFN1, 8, 128, 5>(p, tiles, st);
+    return BN == 256 ? launch_mx4<MX4_FFN1, 8, 256, 4, 1>(p, tiles, st)
+                     : launch_mx4<MX4_FFN1, 8, 128, 5, 1>(p, tiles, st);
 }
 
 }  // namespace moe

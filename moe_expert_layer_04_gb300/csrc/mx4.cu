@@ -12,7 +12,7 @@
 namespace moe {
 namespace {
 
-constexpr int kU = 4;   // vectors of eight elements of a lane
+constexpr int kU = 4;   // vectors of eight elements of a lane (own_block() says four)
 
 // Codes and scale code of a vector; every lane of the warp calls it.
 __device__ __forceinline__ uint32_t quantise8(const uint4 v, uint32_t &code) {
@@ -33,36 +33,44 @@ __device__ __forceinline__ uint32_t quantise8(const uint4 v, uint32_t &code) {
     return e2m1x8(f, mx4_inv_scale(code));
 }
 
-// n8 = all vectors of the matrix; kb = blocks of a row.
+// A warp's scale codes: lane l holds that of its block l / 4 of each of kU = 4 vectors.
+// Block 8 u + l / 4 of the warp's 32 is stored (and, for the values, loaded) by lane
+// 4 (l / 4) + u: 32 consecutive bytes where the row's scales are.
+__device__ __forceinline__ int own_block(int lane) { return (lane & 3) * 8 + (lane >> 2); }
+
+// Place of the scale of block b (of all rows); kb blocks a row, sfp bytes.
+__device__ __forceinline__ long long scale_at(long long b, int kb, int sfp) {
+    if (kb == sfp) return b;
+    const long long r = b / kb;
+    return r * sfp + (b - r * kb);
+}
+
+// n8 = all vectors of the matrix; kb = blocks of a row.  A warp: 32 kU vectors.
 __global__ void __launch_bounds__(256)
     mx4_quantize_kernel(const uint4 *__restrict__ src, long long n8, int kb, int sfp,
                         uint32_t *__restrict__ q, uint8_t *__restrict__ sf) {
     wait_for_kernels_ahead();
     let_kernels_behind_begin();
     const int lane = threadIdx.x & 31;
-    const long long step = (long long)gridDim.x * 8 * 32 * kU;
-    // whole warps take the same steps: the shuffles need every lane
-    for (long long w0 = ((long long)blockIdx.x * 8 + (threadIdx.x >> 5)) * 32 * kU; w0 < n8;
-         w0 += step) {
-        uint4 v[kU];
+    const long long w0 = ((long long)blockIdx.x * 8 + (threadIdx.x >> 5)) * 32 * kU;
+    if (w0 >= n8) return;
+    uint4 v[kU];
 #pragma unroll
-        for (int u = 0; u < kU; ++u) {
-            const long long i = w0 + 32 * u + lane;
-            v[u] = i < n8 ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
-        }
-#pragma unroll
-        for (int u = 0; u < kU; ++u) {
-            const long long i = w0 + 32 * u + lane;
-            uint32_t code;
-            const uint32_t w = quantise8(v[u], code);
-            if (i >= n8) continue;
-            q[i] = w;
-            if ((lane & 3) == 0) {
-                const long long b = i >> 2, r = b / kb;
-                sf[r * sfp + (b - r * kb)] = (uint8_t)code;
-            }
-        }
+    for (int u = 0; u < kU; ++u) {
+        const long long i = w0 + 32 * u + lane;
+        v[u] = i < n8 ? __ldcs(src + i) : make_uint4(0, 0, 0, 0);
     }
+    uint32_t own = 0;
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+        const long long i = w0 + 32 * u + lane;
+        uint32_t code;
+        const uint32_t w = quantise8(v[u], code);
+        if (i < n8) q[i] = w;
+        if ((lane & 3) == u) own = code;
+    }
+    const long long b = w0 / 4 + own_block(lane);
+    if (4 * b < n8) sf[scale_at(b, kb, sfp)] = (uint8_t)own;
 }
 
 __global__ void __launch_bounds__(256)
@@ -71,34 +79,28 @@ __global__ void __launch_bounds__(256)
     wait_for_kernels_ahead();
     let_kernels_behind_begin();
     const int lane = threadIdx.x & 31;
-    const long long step = (long long)gridDim.x * 8 * 32 * kU;
-    for (long long w0 = ((long long)blockIdx.x * 8 + (threadIdx.x >> 5)) * 32 * kU; w0 < n8;
-         w0 += step) {
-        uint32_t w[kU], code[kU];
+    const long long w0 = ((long long)blockIdx.x * 8 + (threadIdx.x >> 5)) * 32 * kU;
+    if (w0 >= n8) return;
+    const long long b = w0 / 4 + own_block(lane);
+    uint32_t own = 0, w[kU];
+    if (4 * b < n8) own = __ldg(sf + scale_at(b, kb, sfp));
 #pragma unroll
-        for (int u = 0; u < kU; ++u) {
-            const long long i = w0 + 32 * u + lane;
-            w[u] = code[u] = 0;
-            if (i < n8) {
-                const long long b = i >> 2, r = b / kb;
-                w[u] = __ldg(q + i);
-                code[u] = __ldg(sf + r * sfp + (b - r * kb));
-            }
+    for (int u = 0; u < kU; ++u) {
+        const long long i = w0 + 32 * u + lane;
+        w[u] = i < n8 ? __ldcs(q + i) : 0u;
+    }
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+        const long long i = w0 + 32 * u + lane;
+        const float x = mx4_scale(__shfl_sync(0xffffffffu, own, (lane & ~3) + u));
+        uint32_t h[4], o[4];
+        e2m1x8_f16(w[u], h);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h[j]));
+            o[j] = pack_bf16x2(f.x * x, f.y * x);
         }
-#pragma unroll
-        for (int u = 0; u < kU; ++u) {
-            const long long i = w0 + 32 * u + lane;
-            if (i >= n8) continue;
-            uint32_t h[4], o[4];
-            e2m1x8_f16(w[u], h);
-            const float x = mx4_scale(code[u]);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h[j]));
-                o[j] = pack_bf16x2(f.x * x, f.y * x);
-            }
-            out[i] = make_uint4(o[0], o[1], o[2], o[3]);
-        }
+        if (i < n8) out[i] = make_uint4(o[0], o[1], o[2], o[3]);
     }
 }
 
@@ -152,17 +154,17 @@ unsigned blocks_for(long long warps) {
 
 moe_status launch_mx4_quantize(const uint16_t *src, long long rows, int K, uint8_t *q, uint8_t *sf,
                                cudaStream_t st) {
-    const long long n8 = rows * (K / 8);
-    return launch_early(mx4_quantize_kernel, dim3(blocks_for((n8 + 32 * kU - 1) / (32 * kU))), 256,
-                        0, st, reinterpret_cast<const uint4 *>(src), n8, K / 32, mx_sf_pitch(K),
+    const long long n8 = rows * (K / 8), ctas = (n8 + 256 * kU - 1) / (256 * kU);
+    if (ctas > 0x7FFFFFFFLL) return MOE_ERR_UNSUPPORTED;
+    return launch_early(mx4_quantize_kernel, dim3((unsigned)ctas), 256, 0, st, reinterpret_cast<const uint4 *>(src), n8, K / 32, mx_sf_pitch(K),
                         reinterpret_cast<uint32_t *>(q), sf);
 }
 
 moe_status launch_mx4_dequantize(const uint8_t *q, const uint8_t *sf, long long rows, int K,
                                  uint16_t *out, cudaStream_t st) {
-    const long long n8 = rows * (K / 8);
-    return launch_early(mx4_dequantize_kernel, dim3(blocks_for((n8 + 32 * kU - 1) / (32 * kU))),
-                        256, 0, st, reinterpret_cast<const uint32_t *>(q), sf, n8, K / 32,
+    const long long n8 = rows * (K / 8), ctas = (n8 + 256 * kU - 1) / (256 * kU);
+    if (ctas > 0x7FFFFFFFLL) return MOE_ERR_UNSUPPORTED;
+    return launch_early(mx4_dequantize_kernel, dim3((unsigned)ctas), 256, 0, st, reinterpret_cast<const uint32_t *>(q), sf, n8, K / 32,
                         mx_sf_pitch(K), reinterpret_cast<uint4 *>(out));
 }
 

@@ -39,14 +39,14 @@ def scale(code):
 
 def quantise4(v):
     """[rows, K] float64 (finite) -> element codes [rows, K], scale codes [rows, K/32]."""
-    b = v.reshape(v.shape[0], -1, BLOCK)
+    b = v.reshape(v.shape[0], v.shape[1] // BLOCK, BLOCK)
     s = _scale_codes(np.abs(b).max(2), 2)
     return e2m1_codes(b / scale(s)[:, :, None]).reshape(v.shape), s
 
 
 def quantise8(v):
     """The same in MXFP8 (E4M3): codes [rows, K], scale codes."""
-    b = v.reshape(v.shape[0], -1, BLOCK)
+    b = v.reshape(v.shape[0], v.shape[1] // BLOCK, BLOCK)
     s = _scale_codes(np.abs(b).max(2), 8)
     return F.e4m3_codes(b / scale(s)[:, :, None]).reshape(v.shape), s
 

@@ -82,7 +82,7 @@ def test_balance_refusals():
                dict(seq_offsets=None), dict(tokens=None), dict(load=None), dict(load=Q),
                dict(logits=None), dict(logits=Q)):
         assert both(**kw) == (BAD, BAD), kw
-    for kw in (dict(E=1025), dict(k=33)):
+    for kw in (dict(E=1025), dict(k=33), dict(n_seq=65536)):
         assert both(**kw) == (UNS, UNS), kw
     assert lib.moe_balance_loss(None, None) == BAD and lib.moe_balance_loss_backward(None, None) == BAD
 
