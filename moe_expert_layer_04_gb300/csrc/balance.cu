@@ -9,8 +9,10 @@
 // (Text and vision, or any other share of the tokens, are balanced apart by giving each
 // as sequences of its own: "HyperParallel加速DeepSeek-V4.1多模态1M长序列训练" §01 item 5.)
 //
-// Sums are fp32 within a chunk of tokens and fp64 over the chunks, in a fixed order, so
-// that results do not depend on the schedule.  Bound by HBM: the logits are read once in
+// Sums are fp32 in a fixed order, so that results do not depend on the schedule: a lane's
+// tokens, the warps of a chunk of tokens, the chunks of a sequence (32 interleaved sums).
+// (fp64 for the last two cost more than the rest of a small call: this GPU adds two of
+// them a cycle.)  Bound by HBM: the logits are read once in
 // each direction, and their gradient is written once.
 #include <cstring>
 
@@ -20,9 +22,11 @@ namespace moe {
 namespace {
 
 constexpr int kWarps = 8;
+constexpr int kOneWarps = 16, kOneTokens = 128, kOneSeqs = 4;
 
 struct BalanceParams {
     int T, E, k, n_seq, chunk, n_chunks;
+    bool one;   // one CTA takes all tokens
     float alpha;
     const float *logits;
     const int32_t *ids, *seq_offsets;
@@ -43,20 +47,35 @@ __device__ __forceinline__ int seq_begin(const BalanceParams &p, int q) {
     return p.seq_offsets ? min(max(__ldg(p.seq_offsets + q), 0), p.T) : q == 0 ? 0 : p.T;
 }
 
-// The first sequence that ends behind token t (n_seq: none).
+// The first sequence that ends behind token t (n_seq: none); called by a whole warp, which
+// looks at 32 places at a time (each look costs a trip to L2).
 __device__ __forceinline__ int first_seq(const BalanceParams &p, int t) {
     int lo = 0, hi = p.n_seq;
     while (lo < hi) {
-        const int mid = (lo + hi) >> 1;
-        if (seq_begin(p, mid + 1) <= t) lo = mid + 1; else hi = mid;
+        const int width = (hi - lo + 31) >> 5, at = lo + (threadIdx.x & 31) * width;
+        const bool before = at < hi && seq_begin(p, min(at + width, hi)) <= t;
+        lo += __popc(__ballot_sync(0xffffffffu, before)) * width;
+        if (width == 1) break;
+        hi = min(hi, lo + width);
     }
-    return lo;
+    return min(lo, p.n_seq);
 }
 
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     return v;
+}
+
+// Writes expert e's count and load in sequence q of n valid tokens; returns its term of the
+// loss, from its count and the sum of its shares.
+__device__ __forceinline__ float finish(const BalanceParams &p, int q, int e, int n, int count,
+                                        float shares) {
+    const float inv = n ? 1.0f / (float)n : 0.0f;
+    const float f = (float)count * inv * ((float)p.E / (float)p.k);
+    p.counts[(size_t)q * p.E + e] = count;
+    p.load[(size_t)q * p.E + e] = f;
+    return n ? f * (shares * inv) : 0.0f;   // (no token: no share, whatever they hold)
 }
 
 // A lane's columns: VEC consecutive ones from VEC (lane + 32 i), i < N.
@@ -129,12 +148,17 @@ __device__ __forceinline__ void shares(const Row<VEC, N> &r, float (&p)[N][VEC],
         for (int j = 0; j < VEC; ++j) p[i][j] *= inv;
 }
 
-// CTA: one chunk of tokens, sequence by sequence; its warps take tokens in turn, a lane
-// sums its columns' shares in registers.
-template <bool SOFTMAX, int VEC, int N>
-__global__ void __launch_bounds__(32 * kWarps) balance_part_kernel(const BalanceParams p) {
+// CTA: one chunk of tokens, sequence by sequence; its warps take tokens in turn (UNROLL
+// of them at a time, whose loads are issued together), a lane sums its columns' shares in
+// registers.  ONE: the chunk is all there is, and the CTA finishes its sums itself.
+template <bool SOFTMAX, int VEC, int N, bool ONE>
+__global__ void __launch_bounds__(32 * (ONE ? kOneWarps : kWarps), !ONE && N * VEC <= 16 ? 4 : 1)
+    balance_part_kernel(const BalanceParams p) {
+    constexpr int WARPS = ONE ? kOneWarps : kWarps;
+    constexpr int UNROLL = N * VEC <= 16 ? 2 : 1;
     extern __shared__ float sm[];   // [kWarps, E] shares, [E] counts
     __shared__ int n_valid;
+    __shared__ float term[WARPS];
     wait_for_kernels_ahead();
     let_kernels_behind_begin();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -148,53 +172,101 @@ __global__ void __launch_bounds__(32 * kWarps) balance_part_kernel(const Balance
     }
     const int end = min(p.T, (int)(blockIdx.x + 1) * p.chunk);
     int a = blockIdx.x * p.chunk;
-    for (int q = first_seq(p, a); q < p.n_seq && a < end; ++q) {
-        const int b = min(end, seq_begin(p, q + 1));
-        a = max(a, seq_begin(p, q));
-        if (a >= b) continue;
+    float loss = 0.0f;
+    for (int q = ONE ? 0 : first_seq(p, a); q < p.n_seq && (ONE || a < end); ++q) {
+        const int b = max(a, min(end, seq_begin(p, q + 1)));
+        a = min(b, max(a, seq_begin(p, q)));
+        if (!ONE && a >= b) continue;
         __syncthreads();   // the last sequence's sums have been read
         for (int e = threadIdx.x; e < p.E; e += blockDim.x) hist[e] = 0;
         if (threadIdx.x == 0) n_valid = 0;
         __syncthreads();
         float acc[N][VEC] = {};
         int n = 0;
-        for (int t = a + warp; t < b; t += kWarps) {
-            if (p.valid && !__ldg(p.valid + t)) continue;
-            ++n;
-            Row<VEC, N> r;
-            r.load(p.logits + (size_t)t * p.E, p.E);
-            float s[N][VEC], slope[N][VEC];
-            shares<SOFTMAX>(r, s, slope);
+        for (int t0 = a + warp; t0 < b; t0 += WARPS * 32) {
+            // the valid ones of the warp's next 32 tokens (a flag each before its row would
+            // be a second trip to memory for every token)
+            const int tl = t0 + lane * WARPS;
+            unsigned left = __ballot_sync(0xffffffffu, tl < b && (!p.valid || __ldg(p.valid + tl)));
+            n += __popc(left);
+            while (left) {
+                Row<VEC, N> r[UNROLL];
+                bool live[UNROLL];
+                int id[UNROLL];
 #pragma unroll
-            for (int i = 0; i < N; ++i)
+                for (int u = 0; u < UNROLL; ++u) {
+                    live[u] = left != 0;
+                    if (!live[u]) continue;
+                    const int t = t0 + (__ffs(left) - 1) * WARPS;
+                    left &= left - 1;
+                    r[u].load(p.logits + (size_t)t * p.E, p.E);
+                    id[u] = lane < p.k ? __ldg(p.ids + (size_t)t * p.k + lane) : 0;
+                }
 #pragma unroll
-                for (int j = 0; j < VEC; ++j) acc[i][j] += s[i][j];
-            if (lane < p.k) {
-                const int e = __ldg(p.ids + (size_t)t * p.k + lane);
-                if ((unsigned)e < (unsigned)p.E) atomicAdd(hist + e, 1);
-                else record_status(p.status, MOE_ERR_INVALID_ARG);
+                for (int u = 0; u < UNROLL; ++u) {
+                    if (!live[u]) continue;
+                    float s[N][VEC], slope[N][VEC];
+                    shares<SOFTMAX>(r[u], s, slope);
+#pragma unroll
+                    for (int i = 0; i < N; ++i)
+#pragma unroll
+                        for (int j = 0; j < VEC; ++j) acc[i][j] += s[i][j];
+                    if (lane < p.k) {
+                        if ((unsigned)id[u] < (unsigned)p.E) atomicAdd(hist + id[u], 1);
+                        else record_status(p.status, MOE_ERR_INVALID_ARG);
+                    }
+                }
             }
         }
         if (lane == 0 && n) atomicAdd(&n_valid, n);
+        // (eight warps' worth of shared memory: further warps add to the first ones')
+        for (int w0 = 0; w0 < WARPS; w0 += kWarps) {
+            if (warp >= w0 && warp < w0 + kWarps) {
 #pragma unroll
-        for (int i = 0; i < N; ++i)
+                for (int i = 0; i < N; ++i)
 #pragma unroll
-            for (int j = 0; j < VEC; ++j) {
-                const int c = VEC * (lane + 32 * i) + j;
-                if (c < p.E) sm[warp * p.E + c] = acc[i][j];
+                    for (int j = 0; j < VEC; ++j) {
+                        const int c = VEC * (lane + 32 * i) + j;
+                        if (c >= p.E) continue;
+                        float *dst = sm + (warp - w0) * p.E + c;
+                        *dst = w0 ? *dst + acc[i][j] : acc[i][j];
+                    }
             }
-        __syncthreads();
-        const size_t slot = (size_t)blockIdx.x + q;
-        for (int e = threadIdx.x; e < p.E; e += blockDim.x) {
-            float s = 0.0f;
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) s += sm[w * p.E + e];
-            p.part_p[slot * p.E + e] = s;
-            p.part_c[slot * p.E + e] = hist[e];
+            __syncthreads();
         }
-        if (threadIdx.x == 0) p.part_n[slot] = n_valid;
+        n = n_valid;
+        if constexpr (ONE) {
+            float mine = 0.0f;
+            for (int e = threadIdx.x; e < p.E; e += blockDim.x) {
+                float v = 0.0f;
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w) v += sm[w * p.E + e];
+                mine += finish(p, q, e, n, hist[e], v);
+            }
+            mine = warp_sum(mine);
+            if (lane == 0) term[warp] = mine;
+            __syncthreads();
+            if (threadIdx.x == 0) {
+                float t = 0.0f;
+                for (int w = 0; w < WARPS; ++w) t += term[w];
+                p.seq_loss[q] = t;
+                p.tokens[q] = n;
+                loss += t;
+            }
+        } else {
+            const size_t slot = (size_t)blockIdx.x + q;
+            for (int e = threadIdx.x; e < p.E; e += blockDim.x) {
+                float s = 0.0f;
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w) s += sm[w * p.E + e];
+                p.part_p[slot * p.E + e] = s;
+                p.part_c[slot * p.E + e] = hist[e];
+            }
+            if (threadIdx.x == 0) p.part_n[slot] = n;
+        }
         a = b;
     }
+    if (ONE && threadIdx.x == 0) p.loss[0] = p.alpha * loss / (float)p.n_seq;
 }
 
 // A cluster for each sequence, a CTA of it for 128 columns: 32 warps take the sequence's
@@ -206,8 +278,8 @@ constexpr int kSeqWarps = 32, kSeqCols = 128;
 __global__ void __launch_bounds__(32 * kSeqWarps) balance_seq_kernel(const BalanceParams p) {
     __shared__ float sum[kSeqWarps][kSeqCols];
     __shared__ int32_t cnt[kSeqWarps][kSeqCols];
-    __shared__ double term[kSeqCols / 32];
-    __shared__ double terms[8];   // of the first CTA: one for each CTA of the cluster
+    __shared__ float term[kSeqCols / 32];
+    __shared__ float terms[8];   // of the first CTA: one for each CTA of the cluster
     __shared__ int n_all;
     wait_for_kernels_ahead();
     let_kernels_behind_begin();
@@ -241,50 +313,44 @@ __global__ void __launch_bounds__(32 * kSeqWarps) balance_seq_kernel(const Balan
     n = n_all;
     if (threadIdx.x < kSeqCols) {
         const int e = blockIdx.x * kSeqCols + threadIdx.x;
-        double v = 0.0;
+        float v = 0.0f;
         int32_t c = 0;
 #pragma unroll
         for (int w = 0; w < kSeqWarps; ++w) {
             v += sum[w][threadIdx.x];
             c += cnt[w][threadIdx.x];
         }
-        const float f = n ? (float)((double)c * p.E / ((double)p.k * n)) : 0.0f;
-        double mine = 0.0;
-        if (e < p.E) {
-            p.counts[(size_t)q * p.E + e] = c;
-            p.load[(size_t)q * p.E + e] = f;
-            if (n) mine = f * (v / n);
-        }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
+        const float mine = warp_sum(e < p.E ? finish(p, q, e, n, c, v) : 0.0f);
         if (lane == 0) term[warp] = mine;
     }
     __syncthreads();
     if (threadIdx.x == 0) {
-        double t = 0.0;
+        float t = 0.0f;
         for (int i = 0; i < kSeqCols / 32; ++i) t += term[i];
-        const uint32_t dst = dsmem_map(&terms[blockIdx.x], 0);
-        asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(dst), "d"(t) : "memory");
+        dsmem_st_u32(dsmem_map(&terms[blockIdx.x], 0), __float_as_uint(t));
     }
     cluster_sync_all();
     if (blockIdx.x == 0 && threadIdx.x == 0) {
-        double t = 0.0;
+        float t = 0.0f;
         for (int i = 0; i < (int)gridDim.x; ++i) t += terms[i];
-        p.seq_loss[q] = (float)t;
+        p.seq_loss[q] = t;
         p.tokens[q] = n;
-        if (p.n_seq == 1) p.loss[0] = (float)(p.alpha * t);
+        if (p.n_seq == 1) p.loss[0] = p.alpha * t;
     }
 }
 
-// The mean of the sequences' losses; one warp.
+// The mean of the sequences' losses; one warp, each lane's sum compensated (it can be long).
 __global__ void balance_loss_kernel(const BalanceParams p) {
     wait_for_kernels_ahead();
     let_kernels_behind_begin();
-    double s = 0.0;
-    for (int q = threadIdx.x; q < p.n_seq; q += 32) s += p.seq_loss[q];
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    if (threadIdx.x == 0) p.loss[0] = (float)(p.alpha * s / p.n_seq);
+    float s = 0.0f, c = 0.0f;
+    for (int q = threadIdx.x; q < p.n_seq; q += 32) {
+        const float v = p.seq_loss[q] - c, u = s + v;
+        c = (u - s) - v;
+        s = u;
+    }
+    s = warp_sum(s);
+    if (threadIdx.x == 0) p.loss[0] = p.alpha * s / (float)p.n_seq;
 }
 
 // A warp takes `chunk` consecutive tokens; a sequence's load stays in its registers.
@@ -406,8 +472,11 @@ moe_status by_columns(const moe_balance_args *a, const BalanceParams &p, cudaStr
 template <bool S, int V, int N>
 struct PartLaunch {
     static moe_status go(const BalanceParams &p, cudaStream_t st) {
-        return launch_early(balance_part_kernel<S, V, N>, dim3(p.n_chunks), 32 * kWarps,
-                            (kWarps + 1) * p.E * 4, st, p);
+        const int smem = (kWarps + 1) * p.E * 4;
+        if (p.one) return launch_early(balance_part_kernel<S, V, N, true>, dim3(1), 32 * kOneWarps,
+                                       smem, st, p);
+        return launch_early(balance_part_kernel<S, V, N, false>, dim3(p.n_chunks), 32 * kWarps,
+                            smem, st, p);
     }
 };
 template <bool S, int V, int N>
@@ -433,6 +502,12 @@ moe_status launch_balance(const moe_balance_args *a, cudaStream_t st) {
     p.status = device_status_ptr();
     if (!p.status) return MOE_ERR_CUDA;
     p.chunk = part_chunk(a->T);
+    // few tokens and sequences: one launch of one CTA instead of two of many
+    p.one = a->T <= kOneTokens && a->n_seq <= kOneSeqs;
+    if (p.one) {
+        p.chunk = kOneTokens;
+        return by_columns<PartLaunch>(a, p, st);
+    }
     p.n_chunks = (a->T + p.chunk - 1) / p.chunk;
     const size_t slots = (size_t)p.n_chunks + a->n_seq;
     p.part_p = static_cast<float *>(a->ws);

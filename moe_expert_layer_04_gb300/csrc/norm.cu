@@ -179,8 +179,8 @@ struct NormBwd {
 
 // The rows slot, slot + slots, ... of one slot; the next row's loads are issued before
 // this row's sum.
-template <int V>
-__global__ void __launch_bounds__(512) rmsnorm_bwd_kernel(const NormBwd p) {
+template <int V, int MOST, int CTAS>
+__global__ void __launch_bounds__(MOST, CTAS) rmsnorm_bwd_kernel(const NormBwd p) {
     __shared__ float part[2][32];
     wait_for_kernels_ahead();
     let_kernels_behind_begin();
@@ -298,32 +298,38 @@ __global__ void __launch_bounds__(256)
     dw[c] = s;
 }
 
-// Threads of a row of d8 vectors, V each, and rows of a CTA.
+// Threads of a row of d8 vectors, V of them each, and rows of a CTA: V a power of two, no
+// more than `most` threads a row, CTAs of 128 at least.
 struct RowShape {
     int V, threads, rows;
 };
-RowShape row_shape(int d8, int most, int cta) {
+RowShape row_shape(int d8, int most) {
     RowShape s;
     s.V = 1;
     while (d8 > s.V * most) s.V *= 2;
     s.threads = ((d8 + s.V - 1) / s.V + 31) / 32 * 32;
-    s.rows = s.threads < cta ? cta / s.threads : 1;
+    s.rows = s.threads < 128 ? 128 / s.threads : 1;
     return s;
 }
 
-RowShape bwd_shape(int d8) { return row_shape(d8, 512, 128); }
+// Backward: two vectors a thread up to d = 4096 (256 threads, CTAs to an SM as their
+// registers allow), more beyond.
+constexpr int kBwdCtas = 2;
+RowShape bwd_shape(int d8) { return d8 <= 512 ? row_shape(d8, 256) : row_shape(d8, 512); }
 
 // Rows in flight of the backward: CTAs for the SMs, no more than there are rows.
-int bwd_ctas(int T, const RowShape &s) {
+int bwd_ctas(int T, int d8, const RowShape &s) {
     const long long want = ((long long)T + s.rows - 1) / s.rows;
-    const long long most = (long long)num_sms() * (s.threads * s.rows <= 512 ? 4 : 2);
+    const long long most = (long long)num_sms() * (d8 <= 512 ? kBwdCtas : 1);
     return (int)(want < most ? want : most);
 }
 
 }  // namespace
 
 moe_status launch_rmsnorm(const moe_norm_args *a, cudaStream_t st) {
-    const RowShape s = row_shape(a->d / 8, 1024, 128);
+    // few rows: one vector a thread, for the latency; many: two, for more rows in flight
+    const int d8 = a->d / 8;
+    const RowShape s = row_shape(d8, a->T > 2 * num_sms() && d8 > 256 && d8 <= 2048 ? (d8 + 1) / 2 : 1024);
     NormRows p;
     std::memset(&p, 0, sizeof p);
     p.T = a->T;
@@ -350,7 +356,7 @@ moe_status launch_rmsnorm(const moe_norm_args *a, cudaStream_t st) {
 
 size_t rmsnorm_bwd_workspace_bytes(int T, int d) {
     const RowShape s = bwd_shape(d / 8);
-    return (size_t)bwd_ctas(T, s) * s.rows * d * sizeof(float);
+    return (size_t)bwd_ctas(T, d / 8, s) * s.rows * d * sizeof(float);
 }
 
 moe_status launch_rmsnorm_bwd(const moe_norm_bwd_args *a, cudaStream_t st) {
@@ -368,13 +374,20 @@ moe_status launch_rmsnorm_bwd(const moe_norm_bwd_args *a, cudaStream_t st) {
     p.rstd = a->rstd;
     p.dx = reinterpret_cast<uint4 *>(a->dx);
     p.part = static_cast<float *>(a->ws);
-    const int ctas = bwd_ctas(a->T, s), threads = s.threads * s.rows;
+    const int ctas = bwd_ctas(a->T, p.d8, s), threads = s.threads * s.rows;
     moe_status r = MOE_OK;
     if (ctas > 0) {
-        if (s.V == 1) r = launch_early(rmsnorm_bwd_kernel<1>, dim3(ctas), threads, 0, st, p);
-        else if (s.V == 2) r = launch_early(rmsnorm_bwd_kernel<2>, dim3(ctas), threads, 0, st, p);
-        else if (s.V == 4) r = launch_early(rmsnorm_bwd_kernel<4>, dim3(ctas), threads, 0, st, p);
-        else r = launch_early(rmsnorm_bwd_kernel<8>, dim3(ctas), threads, 0, st, p);
+        const dim3 grid(ctas);
+        if (p.d8 <= 256)
+            r = launch_early(rmsnorm_bwd_kernel<1, 256, kBwdCtas>, grid, threads, 0, st, p);
+        else if (p.d8 <= 512)
+            r = launch_early(rmsnorm_bwd_kernel<2, 256, kBwdCtas>, grid, threads, 0, st, p);
+        else if (s.V == 2)
+            r = launch_early(rmsnorm_bwd_kernel<2, 512, 1>, grid, threads, 0, st, p);
+        else if (s.V == 4)
+            r = launch_early(rmsnorm_bwd_kernel<4, 512, 1>, grid, threads, 0, st, p);
+        else
+            r = launch_early(rmsnorm_bwd_kernel<8, 512, 1>, grid, threads, 0, st, p);
     }
     if (r != MOE_OK) return r;
     // without rows: zeros
