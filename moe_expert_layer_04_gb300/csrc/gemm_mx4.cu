@@ -138,6 +138,82 @@ __device__ __forceinline__ Tile find_tile(const Mx4Params &p, int q, int nt, con
     return ti;
 }
 
+// tcgen05 instructions of one thread, elected inside each: called by a whole warp in uniform
+// control flow, where descriptors and addresses stay in uniform registers.  (Inside a
+// branch for the one thread a stage's instructions took the warp up to 400 cycles, as long
+// as narrow tiles' MMAs.)  CL = 2: the forms of a pair of CTAs.
+
+// 32 rows of 16 bytes (row j: the scale words of rows j, 32 + j, 64 + j and 96 + j of an
+// operand) to four columns of each lane quadrant, as the block-scaled MMAs read them; a pair:
+// in both CTAs, each from its own shared memory.  In order with the MMAs of the thread.
+template <int CL>
+__device__ __forceinline__ void cp_scales(uint32_t taddr, uint64_t desc) {
+    if constexpr (CL == 2)
+        asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+                     "@e tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;\n\t}" ::"r"(taddr),
+                     "l"(desc)
+                     : "memory");
+    else
+        asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+                     "@e tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;\n\t}" ::"r"(taddr),
+                     "l"(desc)
+                     : "memory");
+}
+
+// Descriptor of those 512 bytes (no swizzle, groups of eight rows 128 bytes apart).
+__device__ __forceinline__ uint64_t sdesc_scales(uint32_t saddr) {
+    return (uint64_t)((saddr >> 4) & 0x3FFFu) | ((uint64_t)(128u >> 4) << 32) | ((uint64_t)1 << 46);
+}
+
+// D[tmem] (+)= (A[smem] * SFA) (B[smem] * SFB)^T, fp32.  AB = 4: E2M1 operands, two elements
+// a byte (K = 64, 32 bytes), two E8M0 scales of each row.  AB = 8: E4M3 rows and E2M1
+// weights, in shared memory sixteen elements in eight bytes and eight bytes of padding (K =
+// 32, 32 bytes), one scale.  Of a pair: M = 256, A's scales of its own rows in each CTA.
+#define MOE_MX4_MMA(GROUP, KIND)                                                               \
+    asm volatile(                                                                              \
+        "{\n\t.reg .pred e, p;\n\telect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 p, %6, 0;\n\t"      \
+        "@e tcgen05.mma.cta_group::" GROUP "." KIND " [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::\
+            "r"(d), "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(more)                  \
+        : "memory")
+template <int AB, int CL>
+__device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                    uint32_t sfa, uint32_t sfb, uint32_t more) {
+    if constexpr (AB == 4 && CL == 2) MOE_MX4_MMA("2", "kind::mxf4.block_scale.scale_vec::2X");
+    else if constexpr (AB == 4) MOE_MX4_MMA("1", "kind::mxf4.block_scale.scale_vec::2X");
+    else if constexpr (CL == 2) MOE_MX4_MMA("2", "kind::mxf8f6f4.block_scale.scale_vec::1X");
+    else MOE_MX4_MMA("1", "kind::mxf8f6f4.block_scale.scale_vec::1X");
+}
+#undef MOE_MX4_MMA
+
+// The instruction descriptor of a stage's i-th MMA: A / B format [7,10) / [10,13), E2M1 = 1
+// where both are packed, E4M3 = 0 and E2M1 = 5 otherwise; N >> 3 at [17,23); scale format
+// [23] = 1 (E8M0); M >> 4 at [24,29) (packed: M >> 7 at [27,29)); which scale byte (packed:
+// pair of bytes) of each word, B's at [4,6) and A's at [29,31); K-major operands.
+template <int AB>
+__host__ __device__ constexpr uint32_t mma_desc(int M, int N, int i) {
+    const uint32_t byte = AB == 4 ? i % 2 * 2 : i;
+    return (byte << 4) | (AB == 4 ? (1u << 7) | (1u << 10) : 5u << 10) |
+           ((uint32_t)(N >> 3) << 17) | (1u << 23) | ((uint32_t)(M >> 4) << 24) | (byte << 29);
+}
+
+// Arrives on `bar` (a pair: at the same place in both CTAs) when all before has completed.
+template <int CL>
+__device__ __forceinline__ void commit(uint64_t *bar) {
+    if constexpr (CL == 2)
+        asm volatile(
+            "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+            "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::"
+            "cluster.b64 [%0], %1;\n\t}" ::"r"(smem_u32(bar)),
+            "h"((uint16_t)0x3)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+            "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::
+                "r"(smem_u32(bar))
+            : "memory");
+}
+
 __device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[32]) { tmem_ld32(taddr, r); }
 __device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[16]) {
     asm volatile(
@@ -304,10 +380,6 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_gemm_kernel(const __grid_cons
         uint32_t s = 0, ph = 0, j = 0, jph = 0, turn = 0;
         int it = 0;
         bool ok = true;
-        auto commit = [&](uint64_t *bar) {
-            if constexpr (CL == 2) umma_commit_pair(bar, 0x3);
-            else umma_commit(bar);
-        };
         for (long long t = first; rank == 0 && ok && t < total; t += step, ++it) {
             if (!mbar_wait_warp(&tempty[it & 1], ((it >> 1) & 1u) ^ 1u, wc) ||
                 (SH::OVER > 0 && it > 0 && !mbar_wait_warp(tover, (it - 1) & 1u, wc))) {
@@ -325,44 +397,24 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_gemm_kernel(const __grid_cons
                 tc_fence_after();
                 const bool last = kb + 1 == p.kb;
                 const bool slot_done = last || w0 + SH::WORDS == 4;
-                if (elect_one()) {
-                    const uint64_t ad = ad0 + s * (SH::STAGE / 16), bd = ad + kCodeA / 16;
-                    const uint64_t sd = sd0 + j * (SH::SLOT / 16) + w0 * 32;
-                    const uint32_t sfa = tmem_base + SH::SF0 + turn * SH::SFC;
+                const uint64_t ad = ad0 + s * (SH::STAGE / 16), bd = ad + kCodeA / 16;
+                const uint64_t sd = sd0 + j * (SH::SLOT / 16) + w0 * 32;
+                const uint32_t sfa = tmem_base + SH::SF0 + turn * SH::SFC;
 #pragma unroll
-                    for (int w = 0; w < SH::WORDS; ++w) {
+                for (int w = 0; w < SH::WORDS; ++w)
 #pragma unroll
-                        for (int r = 0; r < 1 + SH::NB; ++r) {
-                            const uint32_t col = sfa + 4 * (w * (1 + SH::NB) + r);
-                            const uint64_t src = sd + w * 32 + r * (kSfRegion / 16);
-                            if constexpr (CL == 2) tmem_cp_scales_pair(col, src);
-                            else tmem_cp_scales(col, src);
-                        }
-                    }
+                    for (int r = 0; r < 1 + SH::NB; ++r)
+                        cp_scales<CL>(sfa + 4 * (w * (1 + SH::NB) + r),
+                                      sd + w * 32 + r * (kSfRegion / 16));
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const uint32_t more = (kb | i) != 0 ? 1u : 0u;
-                        const uint32_t sa = AB == 4 ? sfa + i / 2 * 4 * (1 + SH::NB) : sfa;
-                        const uint64_t a = ad + 2 * i, b = bd + 2 * i;
-                        if constexpr (AB == 4) {
-                            constexpr int M = 128 * CL;
-                            if constexpr (CL == 2)
-                                umma_mxf4_pair(d, a, b, idesc_mxf4_f32(M, BN, i % 2 * 2), sa, sa + 4, more);
-                            else
-                                umma_mxf4(d, a, b, idesc_mxf4_f32(M, BN, i % 2 * 2), sa, sa + 4, more);
-                        } else {
-                            constexpr int M = 128 * CL;
-                            if constexpr (CL == 2)
-                                umma_mxf8_pair(d, a, b, idesc_mxf8_e2m1_f32(M, BN, i), sa, sa + 4, more);
-                            else
-                                umma_mxf8(d, a, b, idesc_mxf8_e2m1_f32(M, BN, i), sa, sa + 4, more);
-                        }
-                    }
-                    commit(&empty[s]);
-                    if (slot_done) commit(&sfempty[j]);
-                    if (last) commit(&tfull[it & 1]);
+                for (int i = 0; i < 4; ++i) {
+                    const uint32_t sa = AB == 4 ? sfa + i / 2 * 4 * (1 + SH::NB) : sfa;
+                    mma<AB, CL>(d, ad + 2 * i, bd + 2 * i, mma_desc<AB>(128 * CL, BN, i), sa, sa + 4,
+                                (kb | i) != 0 ? 1u : 0u);
                 }
-                __syncwarp();
+                commit<CL>(&empty[s]);
+                if (slot_done) commit<CL>(&sfempty[j]);
+                if (last) commit<CL>(&tfull[it & 1]);
                 turn ^= 1u;
                 if (slot_done && ++j == SH::SLOTS) { j = 0; jph ^= 1u; }
                 if (++s == ST) { s = 0; ph ^= 1u; }
@@ -371,11 +423,7 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_gemm_kernel(const __grid_cons
         if (rank == 0 && (CL == 2 || !ok)) {
             // every MMA of this thread must finish before TMEM is freed (a pair's, before
             // either CTA's operands go away)
-            if (elect_one()) {
-                if constexpr (CL == 2) umma_commit_pair(done, 0x1);
-                else umma_commit(done);
-            }
-            __syncwarp();
+            commit<CL>(done);
             mbar_wait_teardown(done, 0, p.wait_limit);
         }
     } else if (warp < kEpi0) {

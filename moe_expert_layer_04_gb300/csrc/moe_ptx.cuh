@@ -388,61 +388,6 @@ __host__ __device__ constexpr uint32_t idesc_mxf8_f32(int M, int N, uint32_t sf_
            ((uint32_t)(M >> 4) << 24) | (sf_byte << 29);
 }
 
-// The same with E2M1 weights as B: packed in memory, in shared memory sixteen elements in
-// eight bytes with eight bytes of padding behind them (tma_load_2d through a 16U4_ALIGN16B
-// map), so that a K step is 32 bytes for both operands.  B format [10,13) = 5 (E2M1).
-__host__ __device__ constexpr uint32_t idesc_mxf8_e2m1_f32(int M, int N, uint32_t sf_byte) {
-    return idesc_mxf8_f32(M, N, sf_byte) | (5u << 10);
-}
-
-// D[tmem] (+)= (A[smem] * SFA) (B[smem] * SFB)^T: E2M1 operands, two elements a byte in
-// shared memory too (K = 64 per instruction, 32 bytes), one E8M0 scale for 32 elements:
-// two scale bytes of each row.
-__device__ __forceinline__ void umma_mxf4(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
-                                          uint32_t idesc, uint32_t sfa_tmem, uint32_t sfb_tmem,
-                                          uint32_t accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %6, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, "
-        "[%4], [%5], p;\n\t}" ::"r"(d_tmem),
-        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sfa_tmem), "r"(sfb_tmem), "r"(accumulate)
-        : "memory");
-}
-
-// Its instruction descriptor: B scale byte pair [4,6) (0 or 2); A / B format [7,10) /
-// [10,12) = 1 (E2M1); N >> 3 at [17,23); scale format [23] = 1 (E8M0); M >> 7 at [27,29);
-// A scale byte pair [29,31); K = 64 [31] = 0.
-__host__ __device__ constexpr uint32_t idesc_mxf4_f32(int M, int N, uint32_t sf_byte) {
-    return (sf_byte << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(N >> 3) << 17) | (1u << 23) |
-           ((uint32_t)(M >> 7) << 27) | (sf_byte << 29);
-}
-
-// Scales from shared memory into TMEM: 32 rows of 16 bytes (row j: the scale words of rows
-// j, 32 + j, 64 + j and 96 + j of an operand) to four columns of each lane quadrant, as the
-// block-scaled MMAs read them.  In order with the MMAs of the issuing thread.
-__device__ __forceinline__ void tmem_cp_scales(uint32_t taddr, uint64_t desc) {
-    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc)
-                 : "memory");
-}
-
-// Shared-memory descriptor of those 512 bytes (no swizzle, groups of eight rows 128 bytes
-// apart).
-__device__ __forceinline__ uint64_t sdesc_scales(uint32_t saddr) {
-    return (uint64_t)((saddr >> 4) & 0x3FFFu) | ((uint64_t)(128u >> 4) << 32) | ((uint64_t)1 << 46);
-}
-
-// One lane of a converged warp, the same one each time.
-__device__ __forceinline__ bool elect_one() {
-    uint32_t p;
-    asm volatile(
-        "{\n\t.reg .pred e;\n\t"
-        "elect.sync _|e, 0xffffffff;\n\t"
-        "selp.u32 %0, 1, 0, e;\n\t}"
-        : "=r"(p)::"memory");
-    return p != 0;
-}
-
 // Stores one 32-bit word per thread into TMEM (32x32b shape: warp w writes
 // lanes 32*(w%4) .. +31 at column taddr & 0xFFFF).  tmem_wait_st() before the
 // words may be read by an MMA.
@@ -531,38 +476,6 @@ __device__ __forceinline__ void umma_commit_pair(uint64_t *bar, uint16_t mask) {
         "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
         " [%0], %1;" ::"r"(smem_u32(bar)), "h"(mask)
         : "memory");
-}
-
-// The block-scaled MMAs of a pair (umma_mxf8, umma_mxf4 with M = 256): A's scales of its
-// own 128 rows and B's of all N columns are in each CTA's tensor memory.
-__device__ __forceinline__ void umma_mxf8_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
-                                               uint32_t idesc, uint32_t sfa_tmem,
-                                               uint32_t sfb_tmem, uint32_t accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %6, 0;\n\t"
-        "tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, "
-        "[%4], [%5], p;\n\t}" ::"r"(d_tmem),
-        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sfa_tmem), "r"(sfb_tmem), "r"(accumulate)
-        : "memory");
-}
-
-__device__ __forceinline__ void umma_mxf4_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
-                                               uint32_t idesc, uint32_t sfa_tmem,
-                                               uint32_t sfb_tmem, uint32_t accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %6, 0;\n\t"
-        "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, "
-        "[%4], [%5], p;\n\t}" ::"r"(d_tmem),
-        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sfa_tmem), "r"(sfb_tmem), "r"(accumulate)
-        : "memory");
-}
-
-// tmem_cp_scales in both CTAs, each from its own shared memory at the same offset.
-__device__ __forceinline__ void tmem_cp_scales_pair(uint32_t taddr, uint64_t desc) {
-    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc)
-                 : "memory");
 }
 
 // Shared-memory matrix descriptor for a 128-byte-swizzled operand tile.
