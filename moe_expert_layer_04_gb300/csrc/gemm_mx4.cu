@@ -679,26 +679,42 @@ moe_status launch_mx4(Mx4Params &p, long long max_tiles, cudaStream_t st) {
 // stage holds, and what comes of them is not written).
 int box_rows(int max_rows) { return max_rows < 128 ? (max_rows + 7) & ~7 : 128; }
 
-int rows_bn(int max_rows, int G, int N) {
+// The tile of a call: wide ones read fewer operand bytes for a product, narrow ones spread
+// over the SMs where there are few; pairs of CTAs (256 rows) only where groups hold 256 rows
+// on average, as a group's last pair is half empty more often than not.  The least of (rounds
+// of tiles over the SMs) x (ns of a stage, measured with many rounds: 8192 x 4096 x 4096 in
+// pairs 45 us, and 256 / 128 / 64 / 32 wide 54 / 59 / 95 / 182 with 4-bit rows, 74 and 91 / 106 /
+// 162 / 298 with 8-bit ones).  4-bit rows, pairs 256 / 256 / 128 / 64 / 32 wide, us, the rule's
+// choice in brackets: 1 row - / 8.6 / 7.0 / 6.6 / [6.2], 512 rows 10.8 / 10.4 / [7.6] / 10.1 / 16.0,
+// 1024 rows [11.5] / 11.4 / 11.7 / 17.3 / 26.3; 4096 x 2048 weights of 33 groups: 500 rows 29.8 / 26.9
+// / [25.9] / 30.9 / 47.1, 6000 rows 40.9 / [35.8] / 40.5 / 54.7 / 96, 12345 rows [53.5] / 52.9 / 61.2 /
+// 87.3 / 158; of 9 groups, 288 rows 12.3 / [10.8] / 9.6 / 11.6 / 16.9 (not the fastest).
+struct TileChoice {
+    int bn;
+    bool pair;
+};
+TileChoice tile_shape(int max_rows, int G, int N, int bits, int narrowest) {
+    // row tiles: one for each group, or half a tile more than its rows fill
     const int groups = G < max_rows ? G : max_rows;
-    const long long filled = (max_rows + 127) / 128 + (groups - 1) / 2;
-    const long long rows = filled > groups ? filled : groups;
-    int best = 256;
+    const int width[5] = {256, 256, 128, 64, 32};
+    const int ns[2][5] = {{310, 500, 265, 215, 200}, {330, 410, 240, 185, 170}};
+    TileChoice best = {narrowest, false};
     long long least = -1;
-    const int width[4] = {256, 128, 64, 32}, cycles[4] = {600, 400, 320, 300};
-    for (int i = G > kWideGroups ? 1 : 0; i < 4; ++i) {
-        const long long tiles = rows * ((N + width[i] - 1) / width[i]);
-        const long long cost = (tiles + num_sms() - 1) / num_sms() * cycles[i];
+    for (int i = 0; i < 5 && width[i] >= narrowest; ++i) {
+        const bool pair = i == 0;
+        const int rows = pair ? 256 : 128, units = pair ? num_sms() / 2 : num_sms();
+        if ((pair && max_rows < 256LL * G) || (width[i] == 256 && G > kWideGroups)) continue;
+        const long long filled = (max_rows + rows - 1) / rows + (groups - 1) / 2;
+        const long long tiles =
+            (filled > groups ? filled : groups) * ((N + width[i] - 1) / width[i]);
+        const long long cost = (tiles + units - 1) / units * ns[bits == 8][i];
         if (least < 0 || cost < least) {
             least = cost;
-            best = width[i];
+            best = {width[i], pair};
         }
     }
     return best;
 }
-
-// Pairs of row tiles, where groups hold several.
-bool pairs(int max_rows, int G) { return max_rows >= 256LL * G; }
 
 bool encode_operands(Mx4Params &p, int bits, const uint8_t *aq, const uint8_t *asf, int max_rows,
                      const uint8_t *bq, const uint8_t *bsf, uint64_t brows, int b_box, int K) {
@@ -724,8 +740,9 @@ moe_status launch_mx4_matmul(const uint8_t *aq, const uint8_t *asf, int bits,
                              uint16_t *out, cudaStream_t st) {
     Mx4Params p;
     std::memset(&p, 0, sizeof p);
-    const int BN = rows_bn(max_rows, G, N);
-    const int b_box = BN == 256 && pairs(max_rows, G) ? 128 : BN;
+    const TileChoice ts = tile_shape(max_rows, G, N, bits, 32);
+    const int BN = ts.bn;
+    const int b_box = ts.pair ? 128 : BN;
     if (!encode_operands(p, bits, aq, asf, max_rows, bq, bsf, (uint64_t)G * N, b_box, K) ||
         (BN >= 64 && !encode_tmap_bf16_2d_sw64(&p.tmO, out, N, max_rows, 2ULL * N, 32, 32)))
         return MOE_ERR_CUDA;
@@ -736,7 +753,7 @@ moe_status launch_mx4_matmul(const uint8_t *aq, const uint8_t *asf, int bits,
     p.row_w = row_w;
     p.w_rows = w_rows;
     p.out = out;
-    if (BN == 256 && pairs(max_rows, G)) {
+    if (ts.pair) {
         const long long t = (long long)row_pair_bound(max_rows, G) * p.n_tiles;
         return bits == 4 ? launch_mx4<MX4_ROWS, 4, 256, 5, 2>(p, t, st)
                          : launch_mx4<MX4_ROWS, 8, 256, 6, 2>(p, t, st);
@@ -763,7 +780,8 @@ moe_status launch_mx4_ffn1(const uint8_t *xq, const uint8_t *xsf, const int32_t 
                            float clamp, uint8_t *hq, uint8_t *hsf, cudaStream_t st) {
     Mx4Params p;
     std::memset(&p, 0, sizeof p);
-    const int BN = rows_bn(max_rows, G, 2 * I) == 256 ? 256 : 128;
+    const TileChoice ts = tile_shape(max_rows, G, 2 * I, 8, 128);
+    const int BN = ts.bn;
     if (!encode_operands(p, 8, xq, xsf, max_rows, W13q, W13sf, (uint64_t)G * 2 * I, BN / 2, d))
         return MOE_ERR_CUDA;
     p.offsets = offsets;
@@ -775,7 +793,7 @@ moe_status launch_mx4_ffn1(const uint8_t *xq, const uint8_t *xsf, const int32_t 
     p.hq = hq;
     p.hsf = hsf;
     p.h_pitch = mx_sf_pitch(I);
-    if (BN == 256 && pairs(max_rows, G))
+    if (ts.pair)
         return launch_mx4<MX4_FFN1, 8, 256, 6, 2>(
             p, (long long)row_pair_bound(max_rows, G) * p.n_tiles, st);
     const long long tiles = (long long)row_tile_bound(max_rows, G) * p.n_tiles;
