@@ -31,7 +31,8 @@
  *   - bf16 tensors are passed as uint16_t bit patterns.  Every matrix is
  *     row-major and densely packed; base pointers must be 16-byte aligned.
  *   - Every call is asynchronous on `stream` (a cudaStream_t; NULL = legacy
- *     default stream).  Outputs are overwritten, never accumulated.
+ *     default stream).  Outputs are overwritten, never accumulated (but for
+ *     moe_gate_backward's, which says so).
  *   - Arguments are validated on the host before anything is launched; a
  *     failure returns MOE_ERR_INVALID_ARG or MOE_ERR_UNSUPPORTED and launches
  *     nothing.  A CUDA launch error returns MOE_ERR_CUDA.  Errors found on the
@@ -916,6 +917,19 @@ typedef struct {
 size_t moe_balance_workspace_size(int T, int E, int n_seq);
 moe_status moe_balance_loss(const moe_balance_args *args, void *stream);
 moe_status moe_balance_loss_backward(const moe_balance_args *args, void *stream);
+
+/* A dense gradient at the gate's logits (the balance loss's) into the gradients that
+ * moe_backward or moe_backward_mx wrote, which it ADDS to:
+ *   dX[t]   = bf16( dX[t] + bf16( sum_e dz[t,e] W_g[e] ) )
+ *   dW_g[e] = dW_g[e] + sum_t dz[t,e] x[t]            dz = bf16(dlogits), fp32 sums
+ * dlogits [T,E] fp32, x [T,d] and W_g [E,d] bf16 (the gate projection's), dX [T,d] bf16 and
+ * dW_g [E,d] fp32, either of them NULL.  T >= 0; d % 128 == 0, E <= 1024, T max(d, 1024) < 2^31
+ * (else MOE_ERR_UNSUPPORTED).  Workspace: moe_gate_bwd_workspace_size(T, d, E) bytes, 256-byte
+ * aligned (0: not supported, or T = 0). */
+size_t moe_gate_bwd_workspace_size(int T, int d, int E);
+moe_status moe_gate_backward(const float *dlogits, const uint16_t *x, const uint16_t *W_g, int T,
+                             int d, int E, uint16_t *dX, float *dW_g, void *ws, size_t ws_bytes,
+                             void *stream);
 
 /* Text of a status code (static storage). */
 const char *moe_status_string(moe_status s);

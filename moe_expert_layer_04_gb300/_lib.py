@@ -52,7 +52,7 @@ EXPORTS = ["moe_workspace_size", "moe_route", "moe_route_logits", "moe_gate_rout
            "moe_mx4_quantize", "moe_mx4_dequantize", "moe_mx4_gather", "moe_mx4_matmul",
            "moe_expert_ffn_mx4", "moe_rmsnorm", "moe_rmsnorm_bwd_workspace_size",
            "moe_rmsnorm_backward", "moe_balance_workspace_size", "moe_balance_loss",
-           "moe_balance_loss_backward"]
+           "moe_balance_loss_backward", "moe_gate_bwd_workspace_size", "moe_gate_backward"]
 
 
 class MoeError(RuntimeError):
@@ -278,6 +278,8 @@ _SIGS = {
     "moe_rmsnorm_bwd_workspace_size": ([_I, _I], _Z),
     "moe_rmsnorm_backward": ([_P, _P], _I),
     "moe_balance_workspace_size": ([_I, _I, _I], _Z),
+    "moe_gate_bwd_workspace_size": ([_I, _I, _I], _Z),
+    "moe_gate_backward": ([_P, _P, _P, _I, _I, _I, _P, _P, _P, _Z, _P], _I),
     "moe_balance_loss": ([_P, _P], _I),
     "moe_balance_loss_backward": ([_P, _P], _I),
     "moe_expert_gemm2_mx": ([_P, _P, _P, _I, _I, _P, _P, _P, _I, _I, _I, _P, _P], _I),
@@ -949,3 +951,15 @@ def moe_balance_loss_backward(args: dict, stream=None):
     """args: the fields of moe_balance_args (of the forward)."""
     _check("moe_balance_loss_backward",
            load().moe_balance_loss_backward(_balance_bwd(args), _stream(stream)))
+
+
+def moe_gate_bwd_workspace_size(T, d, E) -> int:
+    return int(load().moe_gate_bwd_workspace_size(T, d, E))
+
+
+def moe_gate_backward(dlogits, x, W_g, T, d, E, dX, dW_g, ws, stream=None):
+    st = load().moe_gate_backward(_ptr(dlogits, F32, "dlogits"), _ptr(x, BF16, "x"),
+                                  _ptr(W_g, BF16, "W_g"), T, d, E, _ptr(dX, BF16, "dX"),
+                                  _ptr(dW_g, F32, "dW_g"), _ptr(ws, U8, "ws"),
+                                  0 if ws is None else ws.numel(), _stream(stream))
+    _check("moe_gate_backward", st)

@@ -1508,6 +1508,32 @@ moe_status moe_balance_loss_backward(const moe_balance_args *a, void *stream) {
     return launch_balance_bwd(a, static_cast<cudaStream_t>(stream));
 }
 
+static moe_status gate_bwd_shape(int T, int d, int E) {
+    if (T < 0 || d < 1 || E < 1) return MOE_ERR_INVALID_ARG;
+    if (d % 128 != 0 || E > 1024 || (long long)T * (d > 1024 ? d : 1024) >= (1LL << 31))
+        return MOE_ERR_UNSUPPORTED;
+    return MOE_OK;
+}
+
+size_t moe_gate_bwd_workspace_size(int T, int d, int E) {
+    return T > 0 && gate_bwd_shape(T, d, E) == MOE_OK ? gate_bwd_workspace_bytes(T, d, E) : 0;
+}
+
+moe_status moe_gate_backward(const float *dlogits, const uint16_t *x, const uint16_t *W_g, int T,
+                             int d, int E, uint16_t *dX, float *dW_g, void *ws, size_t ws_bytes,
+                             void *stream) {
+    const moe_status s = gate_bwd_shape(T, d, E);
+    if (s != MOE_OK) return s;
+    if (T == 0 || (!dX && !dW_g)) return MOE_OK;
+    if (!all_aligned16({dlogits, x, W_g}) || !aligned16(dX) || !aligned16(dW_g))
+        return MOE_ERR_INVALID_ARG;
+    if (!ws || (reinterpret_cast<uintptr_t>(ws) & 255u) != 0 ||
+        ws_bytes < gate_bwd_workspace_bytes(T, d, E))
+        return MOE_ERR_WORKSPACE;
+    return launch_gate_bwd(dlogits, x, W_g, T, d, E, dX, dW_g, ws,
+                           static_cast<cudaStream_t>(stream));
+}
+
 size_t moe_few_workspace_size(int T, int d, int E, int k, int I) {
     return few_supported(T, d, E, k, I) ? few_workspace_bytes(T, d, E, k, I) : 0;
 }

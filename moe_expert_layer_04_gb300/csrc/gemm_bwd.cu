@@ -63,14 +63,16 @@ moe_status launch_dgrad2(const uint16_t *dY_perm, const int32_t *offsets, int G,
 }
 
 moe_status launch_dgrad1(const uint16_t *dGU, const int32_t *offsets, int G, int max_rows,
-                         const uint16_t *W13, int d, int I, uint16_t *dX_perm, cudaStream_t st) {
+                         const uint16_t *W13, int d, int I, uint16_t *dX_perm, cudaStream_t st,
+                         uint64_t w_rows) {
     GemmParams p;
     std::memset(&p, 0, sizeof p);
     const int BN = (d % 256 == 0) ? 256 : 128;
     if (!encode_tmap_bf16_2d(&p.tmA, dGU, 2 * I, max_rows, (uint64_t)4 * I, 64, 128))
         return MOE_ERR_CUDA;
     // W13 as [G*2I rows (contraction), d columns (output)], MN-major boxes
-    if (!encode_tmap_bf16_2d(&p.tmB, W13, d, (uint64_t)G * 2 * I, (uint64_t)d * 2, 64, 64))
+    if (!encode_tmap_bf16_2d(&p.tmB, W13, d, w_rows ? w_rows : (uint64_t)G * 2 * I,
+                             (uint64_t)d * 2, 64, 64))
         return MOE_ERR_CUDA;
     p.offsets = offsets;
     p.G = G;

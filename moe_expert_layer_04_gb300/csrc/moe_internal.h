@@ -95,7 +95,9 @@ moe_status launch_dgrad2(const uint16_t *dY_perm, const int32_t *offsets, int G,
                          int *dw_tiles, int *tile_counter, cudaStream_t st);
 int dgrad2_n_tiles(int I);
 moe_status launch_dgrad1(const uint16_t *dGU, const int32_t *offsets, int G, int max_rows,
-                         const uint16_t *W13, int d, int I, uint16_t *dX_perm, cudaStream_t st);
+                         const uint16_t *W13, int d, int I, uint16_t *dX_perm, cudaStream_t st,
+                         uint64_t w_rows = 0);   // W13's rows, where fewer than G * 2I: the
+                                                 // others count as zeros
 // dW[g] (M x N, fp32) = A[rows of g]^T B[rows of g]; A [R, M] and B [R, N] bf16.
 // scratch: kWgradScratchBytes of device memory (64-byte aligned) for the
 // per-group tensor maps of A, the schedule's group order and its tile
@@ -210,6 +212,11 @@ moe_status launch_rmsnorm_bwd(const moe_norm_bwd_args *a, cudaStream_t st);
 size_t balance_workspace_bytes(int T, int E, int n_seq);
 moe_status launch_balance(const moe_balance_args *a, cudaStream_t st);
 moe_status launch_balance_bwd(const moe_balance_args *a, cudaStream_t st);
+
+// A dense gradient at the gate's logits into dX and dW_g (gate_bwd.cu).
+size_t gate_bwd_workspace_bytes(int T, int d, int E);
+moe_status launch_gate_bwd(const float *dlogits, const uint16_t *x, const uint16_t *W_g, int T,
+                           int d, int E, uint16_t *dX, float *dW_g, void *ws, cudaStream_t st);
 
 // The whole layer for a few tokens (few.cu).
 bool few_supported(int T, int d, int E, int k, int I);

@@ -7,6 +7,9 @@ library in order; every step of the layer runs in the library's kernels:
             (or the one-launch moe_expert_ffn_fused) -> moe_combine
   backward  moe_backward
   decoding  moe_layer_few (at most 32 tokens, two launches)
+  around it moe_rmsnorm ahead of the routing, moe_balance_loss behind it, and
+            their backward (moe_gate_backward carries the loss's gradient into dX
+            and dW_g)
 
 ("HyperParallel加速DeepSeek-V4.1多模态1M长序列训练" §2.3: MegaGate routing
 pipeline, then MegaMoE dispatch, two expert matmuls around the clamped
@@ -33,6 +36,11 @@ def gate_route_supported(d: int, E: int, k: int) -> bool:
 def mx_supported(d: int, I: int) -> bool:
     """Shapes the MXFP8 expert matmuls (moe_expert_ffn_mx) take."""
     return d % 256 == 0 and I % 128 == 0
+
+
+def mx4_supported(d: int, I: int) -> bool:
+    """Shapes the expert FFN with MXFP4 weights (moe_expert_ffn_mx4) takes."""
+    return d % 128 == 0 and I % 128 == 0
 
 
 def fp8_supported(d: int, I: int) -> bool:
@@ -106,13 +114,41 @@ class MoELayer:
     step's token rows in the dispatch (moe_fp8_gather) and runs
     moe_expert_ffn_fp8; forward_few() decodes from the same weights.  Forward
     only (GroupedLinearFP8 has the matmul's gradients).
+    mx4: the serving variant whose expert weights are MXFP4 (4-bit elements, one
+    power of two per 32), quantised here (moe_mx4_quantize; again with
+    quantize_weights() after they change), or given so: weights then has W13_q
+    [E+1,2I,d/2], W2_q [E+1,d,I/2], W13_sf [E+1,2I,moe_mx_sf_pitch(d)] and W2_sf
+    [E+1,d,moe_mx_sf_pitch(I)] (uint8) in place of W13 and W2.  forward() quantises
+    each step's token rows to MXFP8 in the dispatch and runs moe_expert_ffn_mx4.
+    Forward only.
+    norm_eps: the root-mean-square norm ahead of the layer, of weight weights["norm"]
+    (fp32 [d]).  forward() then takes rows of the residual stream's update x and, with
+    `residual`, adds them to it first; self.residual is the stream after the addition
+    (x itself without one).  In the MX, MXFP4 and FP8 layers the same kernel quantises
+    the rows (of the norm's fp32 result) and the dispatch moves their codes.  backward()
+    returns the gradient of x and of the residual (self.dnorm: the weight's).
+    forward_few() takes rows that norm() has been through.
+    balance: alpha of the router's balance loss over `sequences` sequences (softmax
+    shares with balance_softmax, of sigmoid scores without).  forward() writes
+    self.balance_loss [1], self.balance_counts [sequences, E] and balance_load; backward()
+    adds its gradient (times d_balance) to dX and dW_g.
     """
+
+    mx4 = False
+    norm_eps = balance_alpha = None
 
     def __init__(self, dims: Dims, weights: dict, scaling: float, clamp: float = 7.0,
                  backward: bool = False, recompute: bool = False, device="cuda",
                  fused_route: bool | None = None, fused_ffn: bool = False, mx: bool = False,
-                 fp8: bool = False):
+                 fp8: bool = False, mx4: bool = False, norm_eps: float | None = None,
+                 balance: float | None = None, sequences: int = 1,
+                 balance_softmax: bool = False):
         self.dims = dims
+        if mx4 and (mx or fp8 or fused_ffn or backward or not mx4_supported(dims.d, dims.I)):
+            raise ValueError(f"the MXFP4 layer runs the forward in two launches and needs "
+                             f"d % 128 == 0, I % 128 == 0 (got {dims})")
+        if mx4:
+            self.mx4 = True
         if fp8 and (mx or fused_ffn or backward or not fp8_supported(dims.d, dims.I)):
             raise ValueError(f"the FP8 layer runs the forward in two launches and needs "
                              f"d % 128 == 0, I % 128 == 0 (got {dims})")
@@ -150,6 +186,8 @@ class MoELayer:
         self.row_weight = torch.empty(D.S, dtype=torch.float32, **e)
         if self.mx:
             self._init_mx(weights, e)
+        elif self.mx4:
+            self._init_mx4(e)
         elif self.fp8:
             self._init_fp8(e)
         else:
@@ -179,6 +217,79 @@ class MoELayer:
             self.dlogits = None
             self.dweights = None
         self._few_ws = {}   # forward_few: a workspace for each number of tokens and stream
+        if norm_eps is not None:
+            self.norm_eps = float(norm_eps)
+            self._init_norm(e)
+        if balance is not None:
+            self.balance_alpha = float(balance)
+            self._init_balance(int(sequences), bool(balance_softmax), e)
+
+    def _init_norm(self, e):
+        D = self.dims
+        w = self.w.get("norm")
+        if w is None or tuple(w.shape) != (D.d,) or w.dtype != torch.float32:
+            raise ValueError(f"a layer with norm_eps needs weights['norm'], fp32 [{D.d}]")
+        self.xn = torch.empty(D.T, D.d, dtype=torch.bfloat16, **e)
+        self.rstd = torch.empty(D.T, dtype=torch.float32, **e)
+        self.residual = self._stream_rows = torch.empty(D.T, D.d, dtype=torch.bfloat16, **e)
+        self.xn_q = self.xn_s = None
+        if self.mx or self.mx4:
+            self._row_format = _lib.MOE_ROWS_MXFP8
+            self.xn_q = torch.empty(D.T, D.d, dtype=torch.uint8, **e)
+            self.xn_s = torch.empty(D.T, _lib.moe_mx_sf_pitch(D.d), dtype=torch.uint8, **e)
+        elif self.fp8:
+            self._row_format = _lib.MOE_ROWS_FP8
+            self.xn_q = torch.empty(D.T, D.d, dtype=torch.uint8, **e)
+            self.xn_s = torch.empty(D.T, _lib.moe_fp8_scale_cols(D.d), dtype=torch.float32, **e)
+        else:
+            self._row_format = _lib.MOE_ROWS_NONE
+        if self.backward_enabled:
+            self.dnorm = torch.empty(D.d, dtype=torch.float32, **e)
+            self.ws_norm = torch.empty(_lib.moe_rmsnorm_bwd_workspace_size(D.T, D.d),
+                                       dtype=torch.uint8, **e)
+
+    def _init_balance(self, n, softmax, e):
+        D = self.dims
+        f32, i32 = dict(dtype=torch.float32, **e), dict(dtype=torch.int32, **e)
+        size = _lib.moe_balance_workspace_size(D.T, D.E, n)
+        if size == 0:
+            raise ValueError(f"unsupported balance loss of {n} sequences of {D}")
+        self.balance_loss = torch.empty(1, **f32)
+        self.balance_counts = torch.empty(n, D.E, **i32)
+        self.balance_load = torch.empty(n, D.E, **f32)
+        self.balance_seq_loss = torch.empty(n, **f32)
+        score = _lib.MOE_SCORE_SOFTMAX if softmax else _lib.MOE_SCORE_SIGMOID
+        self._balance = dict(
+            T=D.T, E=D.E, k=D.k, n_seq=n, score=score, alpha=self.balance_alpha,
+            logits=self.logits, ids=self.ids, counts=self.balance_counts,
+            tokens=torch.empty(n, **i32), load=self.balance_load, seq_loss=self.balance_seq_loss,
+            loss=self.balance_loss, ws=torch.empty(size, dtype=torch.uint8, **e))
+        if self.backward_enabled:
+            self._balance["dlogits"] = torch.empty(D.T, D.E, **f32)
+            self.ws_gate = torch.empty(_lib.moe_gate_bwd_workspace_size(D.T, D.d, D.E),
+                                       dtype=torch.uint8, **e)
+
+    def _init_mx4(self, e):
+        D = self.dims
+        u8 = dict(dtype=torch.uint8, **e)
+        pd, pi = _lib.moe_mx_sf_pitch(D.d), _lib.moe_mx_sf_pitch(D.I)
+        G = D.E + 1
+        shapes = dict(W13_q=(G, 2 * D.I, D.d // 2), W13_sf=(G, 2 * D.I, pd),
+                      W2_q=(G, D.d, D.I // 2), W2_sf=(G, D.d, pi))
+        given = [n for n in shapes if n in self.w]
+        if given and (len(given) < 4 or "W13" in self.w or "W2" in self.w):
+            raise ValueError("MXFP4 weights are W13 and W2, or W13_q, W13_sf, W2_q and W2_sf")
+        for name, shape in shapes.items():
+            t = self.w[name] if given else torch.empty(*shape, **u8)
+            if tuple(t.shape) != shape or t.dtype != torch.uint8:
+                raise ValueError(f"{name}: {t.dtype} {tuple(t.shape)}, expected uint8 {shape}")
+            setattr(self, name, t)
+        if not given:
+            self.quantize_weights()
+        self.x_perm_q = torch.empty(D.R, D.d, **u8)
+        self.x_perm_sf = torch.empty(D.R, pd, **u8)
+        self.h_q = torch.empty(D.R, D.I, **u8)
+        self.h_sf = torch.empty(D.R, pi, **u8)
 
     def _init_fp8(self, e):
         D = self.dims
@@ -230,14 +341,18 @@ class MoELayer:
         self.h_sf = torch.empty(D.R, pi, **u8)
 
     def quantize_weights(self, stream=None):
-        """(MX and FP8 layers) Quantise the expert weights from self.w into the
-        copies the matmuls read.  MX: along d and I for the forward, and with
+        """(MX, MXFP4 and FP8 layers) Quantise the expert weights from self.w into
+        the copies the matmuls read.  MX: along d and I for the forward, and with
         backward also along d (W2) and 2I (W13) for the dgrad matmuls."""
         D = self.dims
         G = D.E + 1
         if "W13" not in self.w:
-            raise RuntimeError("the layer was given FP8 weights: there are none to quantise")
+            raise RuntimeError("the layer was given quantised weights: there are none to quantise")
         W13, W2 = self.w["W13"], self.w["W2"]
+        if self.mx4:
+            _lib.moe_mx4_quantize(W13, G * 2 * D.I, D.d, self.W13_q, self.W13_sf, stream)
+            _lib.moe_mx4_quantize(W2, G * D.d, D.I, self.W2_q, self.W2_sf, stream)
+            return
         if self.fp8:
             _lib.moe_fp8_quantize_weights(W13, G, 2 * D.I, D.d, self.W13_q, self.W13_s,
                                           stream=stream)
@@ -279,14 +394,20 @@ class MoELayer:
     def dispatch(self, x, stream=None):
         D = self.dims
         self._rows("x", x)
-        low = self.mx or self.fp8
+        low = self.mx or self.fp8 or self.mx4
         _lib.moe_permute(self.ids, self.weights, None if low else x, D.T, D.d, D.E, D.k,
                          self.counts, self.offsets, self.row_token, self.slot_row,
                          self.row_weight, None if low else self.x_perm, self.ws, stream)
+        if low and self.norm_eps is not None and x is self.xn:
+            # the norm has quantised the rows: their codes and scales move
+            for src, dst in ((self.xn_q, self.x_perm_q),
+                             (self.xn_s, self.x_perm_s if self.fp8 else self.x_perm_sf)):
+                _lib.moe_gather_rows(src, self.row_token, dst, stream)
+            return
         if self.fp8:
             _lib.moe_fp8_gather(x, self.slot_row, D.T, D.d, D.k, self.x_perm_q, self.x_perm_s,
                                 stream)
-        if self.mx:
+        if self.mx or self.mx4:
             _lib.moe_mx_gather(x, self.slot_row, D.T, D.d, D.k, self.x_perm_q, self.x_perm_sf,
                                stream)
 
@@ -297,6 +418,12 @@ class MoELayer:
                                    self.W13_q, self.W13_sf, self.W2_q, self.W2_sf,
                                    self.row_weight, D.S, D.d, D.I, self.clamp, self.h_q,
                                    self.h_sf, self.y_perm, self.gu_save, stream)
+            return
+        if self.mx4:
+            _lib.moe_expert_ffn_mx4(self.x_perm_q, self.x_perm_sf, self.offsets, D.E + 1, D.R,
+                                    self.W13_q, self.W13_sf, self.W2_q, self.W2_sf,
+                                    self.row_weight, D.S, D.d, D.I, self.clamp, self.h_q,
+                                    self.h_sf, self.y_perm, stream)
             return
         if self.fp8:
             _lib.moe_expert_ffn_fp8(self.x_perm_q, self.x_perm_s, self.offsets, D.E + 1, D.R,
@@ -315,8 +442,8 @@ class MoELayer:
 
     def expert_gemm1(self, stream=None):
         D = self.dims
-        if self.fp8:
-            raise RuntimeError("the FP8 layer's expert matmuls are one call (experts())")
+        if self.fp8 or self.mx4:
+            raise RuntimeError("this layer's expert matmuls are one call (experts())")
         if self.mx:
             _lib.moe_expert_gemm1_mx(self.x_perm_q, self.x_perm_sf, self.offsets, D.E + 1, D.R,
                                      self.W13_q, self.W13_sf, D.d, D.I, self.clamp, self.h_q,
@@ -327,8 +454,8 @@ class MoELayer:
 
     def expert_gemm2(self, stream=None):
         D = self.dims
-        if self.fp8:
-            raise RuntimeError("the FP8 layer's expert matmuls are one call (experts())")
+        if self.fp8 or self.mx4:
+            raise RuntimeError("this layer's expert matmuls are one call (experts())")
         if self.mx:
             _lib.moe_expert_gemm2_mx(self.h_q, self.h_sf, self.offsets, D.E + 1, D.R, self.W2_q,
                                      self.W2_sf, self.row_weight, D.S, D.d, D.I, self.y_perm,
@@ -343,12 +470,59 @@ class MoELayer:
         _lib.moe_combine(self.y_perm, self.slot_row, D.T, D.d, D.k, 1,
                          self.y if y is None else y, stream)
 
+    def norm(self, x, residual=None, stream=None):
+        """The norm ahead of the layer: (rows [T, d] bf16, the residual stream after the
+        addition).  Of dims.T rows into the layer's own buffers (with the codes of a
+        low-precision layer); of any other number, for forward_few(), new tensors."""
+        D = self.dims
+        if self.norm_eps is None:
+            raise RuntimeError("layer built without norm_eps")
+        T = int(x.shape[0])
+        _expect("x", x, T, D.d)
+        _expect("residual", residual, T, D.d)
+        own = T == D.T
+        xn = self.xn if own else _result(stream, x.device, T, D.d)
+        out = None
+        if residual is not None:
+            out = self._stream_rows if own else _result(stream, x.device, T, D.d)
+        _lib.moe_rmsnorm(dict(
+            T=T, d=D.d, eps=self.norm_eps, format=self._row_format if own else _lib.MOE_ROWS_NONE,
+            x=x, residual=residual, weight=self.w["norm"], residual_out=out, y=xn,
+            rstd=self.rstd if own else None, q=self.xn_q if own else None,
+            scales=self.xn_s if own else None), stream)
+        out = x if out is None else out
+        if own:
+            self.residual = out       # the backward reads it
+        return xn, out
+
     def forward(self, x, bias, is_vision=None, logit_offset=None, mode=MOE_ROUTE_TOPK,
-                input_ids=None, tid2eid=None, stream=None, y=None):
+                input_ids=None, tid2eid=None, stream=None, y=None, residual=None,
+                seq_offsets=None, valid=None):
         """One forward pass; the output goes to self.y, or to `y` ([T, d] bf16)
-        when given."""
+        when given.  residual [T, d] bf16 (norm_eps layers): the residual stream that x is
+        added to.  seq_offsets int32 [sequences + 1], valid uint8 [T] (balance layers): the
+        loss's sequences, and which tokens count."""
+        D = self.dims
         self._rows("y", y)
+        if residual is not None and self.norm_eps is None:
+            raise ValueError("residual: the layer was built without norm_eps")
+        if self.balance_alpha is None and (seq_offsets is not None or valid is not None):
+            raise ValueError("seq_offsets, valid: the layer was built without balance")
+        if self.balance_alpha is not None:
+            n = self._balance["n_seq"]
+            if n != 1 or seq_offsets is not None:
+                if seq_offsets is None:
+                    raise ValueError(f"seq_offsets: the layer was built for {n} sequences")
+                _expect("seq_offsets", seq_offsets, n + 1)
+            _expect("valid", valid, D.T)
+        if self.norm_eps is not None:
+            if int(x.shape[0]) != D.T:
+                raise ValueError(f"x: {int(x.shape[0])} rows, the layer has T = {D.T}")
+            x, _ = self.norm(x, residual, stream)
         self.route(x, bias, is_vision, logit_offset, mode, input_ids, tid2eid, stream)
+        if self.balance_alpha is not None:
+            self._balance.update(seq_offsets=seq_offsets, valid=valid)   # (the backward's too)
+            _lib.moe_balance_loss(self._balance, stream)
         self.dispatch(x, stream)
         self.experts(stream)
         self.combine(stream, y)
@@ -365,7 +539,7 @@ class MoELayer:
         with that stream's calls); else the graph gets its own, which it zeroes on
         every replay.  See reset_few()."""
         D = self.dims
-        if self.mx:
+        if self.mx or self.mx4:
             raise RuntimeError("moe_layer_few takes bf16 or FP8 weights")
         T = int(x.shape[0])
         _expect("x", x, T, D.d)
@@ -411,14 +585,37 @@ class MoELayer:
 
     # ----------------------------------------------------------- backward
     def backward(self, dY, want_dlogits=False, want_dweights=False, stream=None,
-                 stage_events=None):
+                 stage_events=None, d_balance=None, d_residual=None):
         """Backward of the last forward; returns dX.  stage_events: optional
         list of MOE_BWD_STAGES + 1 torch.cuda.Event (recorded once before) that
-        the library records around each of its stages."""
+        the library records around each of its stages.  d_balance fp32 [1] (balance
+        layers; None: 1): the gradient of the balance loss.  d_residual [T, d] bf16
+        (norm_eps layers): the gradient that reaches self.residual past the layer.
+        want_dlogits gives the routing weights' part alone."""
         D = self.dims
         if not self.backward_enabled:
             raise RuntimeError("layer built without backward buffers")
         self._rows("dY", dY)
+        if d_residual is not None and self.norm_eps is None:
+            raise ValueError("d_residual: the layer was built without norm_eps")
+        if d_balance is not None and self.balance_alpha is None:
+            raise ValueError("d_balance: the layer was built without balance")
+        self._rows("d_residual", d_residual)
+        _expect("d_balance", d_balance, 1)
+        self._experts_backward(dY, want_dlogits, want_dweights, stream, stage_events)
+        if self.balance_alpha is not None:
+            a = dict(self._balance, dloss=d_balance)
+            _lib.moe_balance_loss_backward(a, stream)
+            _lib.moe_gate_backward(a["dlogits"], self.x, self.w["W_g"], D.T, D.d, D.E, self.dX,
+                                   self.dW_g, self.ws_gate, stream)
+        if self.norm_eps is not None:
+            _lib.moe_rmsnorm_backward(dict(
+                T=D.T, d=D.d, x=self.residual, weight=self.w["norm"], rstd=self.rstd, dy=self.dX,
+                d_residual=d_residual, dx=self.dX, d_weight=self.dnorm, ws=self.ws_norm), stream)
+        return self.dX
+
+    def _experts_backward(self, dY, want_dlogits, want_dweights, stream, stage_events):
+        D = self.dims
         if want_dlogits and self.dlogits is None:
             self.dlogits = torch.empty(D.T, D.E, dtype=torch.float32, device=dY.device)
         if want_dweights and self.dweights is None:
@@ -437,7 +634,7 @@ class MoELayer:
                 dlogits=self.dlogits if want_dlogits else None,
                 dweights=self.dweights if want_dweights else None, ws=self.ws_bwd,
                 stage_events=stage_events), stream)
-            return self.dX
+            return
         args = dict(T=D.T, d=D.d, E=D.E, k=D.k, I=D.I, scaling=self.scaling, clamp=self.clamp,
                     flags=MOE_FLAG_RECOMPUTE if self.recompute else 0,
                     x=self.x, W_g=self.w["W_g"], W13=self.w["W13"], W2=self.w["W2"],
@@ -451,8 +648,6 @@ class MoELayer:
                     dweights=self.dweights if want_dweights else None, ws=self.ws,
                     stage_events=stage_events)
         _lib.moe_backward(args, stream)
-        return self.dX
-
 
     # ------------------------------------------------- steps from host memory
     def step_host(self, x_host, y_host, dY_host=None, dX_host=None, bias=None, is_vision=None,
@@ -488,8 +683,9 @@ class MoELayer:
     def _ensure_host_struct(self, train, bias, is_vision, logit_offset, mode, input_ids,
                             tid2eid):
         D = self.dims
-        if self.mx or self.fp8:
-            raise RuntimeError("the host-memory steps run the bf16 layer")
+        if self.mx or self.fp8 or self.mx4 or self.norm_eps is not None \
+                or self.balance_alpha is not None:
+            raise RuntimeError("the host-memory steps run the plain bf16 layer")
         if train and not self.backward_enabled:
             raise RuntimeError("layer built without backward buffers")
         key = (id(bias), id(is_vision), id(logit_offset), mode, id(input_ids), id(tid2eid))
@@ -592,7 +788,64 @@ class GroupedLinearFP8:
         return dx
 
 
-__all__ = ["Dims", "GroupedLinearFP8", "MoELayer", "MOE_ROUTE_TOPK", "MOE_ROUTE_HASH"]
+class GroupedLinearMX4:
+    """One projection per group (expert) for serving, y[r] = x[r] W[g]^T for the rows of
+    group g, with MXFP4 weights (4-bit elements, one power of two per 32).
+
+    weight: bf16 [G, N, K] (CUDA), quantised here; again with quantize_weights() after it
+    changes.  Or codes=(w_q, w_sf), uint8 [G, N, K/2] and [G, N, moe_mx_sf_pitch(K)], with
+    weight None.  G = 1 is a dense layer.  rows: the most rows of a call.  bits: of the rows,
+    which each call quantises: 8 (MXFP8, K % 128 == 0) or 4 (MXFP4, K % 32 == 0: twice the
+    tensor rate, with the rows' rounding errors those of the weights)."""
+
+    def __init__(self, weight, rows: int, bits: int = 8, codes=None):
+        if (weight is None) == (codes is None):
+            raise ValueError("GroupedLinearMX4 takes a weight, or its codes and scales")
+        if bits not in (4, 8):
+            raise ValueError(f"rows of {bits} bits: 4 or 8")
+        G, N, K = map(int, weight.shape if codes is None else codes[0].shape)
+        if codes is not None:
+            K *= 2
+        if G < 1 or G > 1025 or N % 8 or K < 32 or K % (32 if bits == 4 else 128):
+            raise ValueError(f"unsupported MXFP4 projection [{G}, {N}, {K}] on {bits}-bit rows")
+        self.weight, self.G, self.N, self.K, self.rows, self.bits = weight, G, N, K, int(rows), bits
+        pitch = _lib.moe_mx_sf_pitch(K)
+        u8 = dict(dtype=torch.uint8, device=(codes[0] if weight is None else weight).device)
+        if codes is None:
+            self.w_q, self.w_sf = torch.empty(G, N, K // 2, **u8), torch.empty(G, N, pitch, **u8)
+            self.quantize_weights()
+        else:
+            self.w_q, self.w_sf = codes
+            _expect("codes", self.w_sf, G, N, pitch)
+        self.x_q = torch.empty(self.rows, K if bits == 8 else K // 2, **u8)
+        self.x_sf = torch.empty(self.rows, pitch, **u8)
+
+    def quantize_weights(self, stream=None):
+        if self.weight is None:
+            raise RuntimeError("the projection was given quantised weights")
+        _lib.moe_mx4_quantize(self.weight, self.G * self.N, self.K, self.w_q, self.w_sf, stream)
+
+    def forward(self, x, offsets, stream=None, row_weight=None):
+        """y [R, N] bf16 of the rows x [R, K] bf16, R <= rows; offsets int32 [G+1] on the
+        device, the groups' first rows, the last one R.  row_weight fp32 [R]: factors of the
+        rows.  With `stream` the work and y's memory belong to that stream."""
+        R = int(x.shape[0])
+        _expect("x", x, R, self.K)
+        _expect("offsets", offsets, self.G + 1)
+        _expect("row_weight", row_weight, R)
+        if R > self.rows:
+            raise ValueError(f"{R} rows, the buffers hold {self.rows}")
+        y = _result(stream, x.device, R, self.N)
+        if R == 0:
+            return y
+        quantize = _lib.moe_mx_quantize if self.bits == 8 else _lib.moe_mx4_quantize
+        quantize(x, R, self.K, self.x_q, self.x_sf, stream)
+        _lib.moe_mx4_matmul(self.x_q, self.x_sf, self.bits, offsets, self.G, R, self.w_q, self.w_sf,
+                            row_weight, R, self.N, self.K, y, stream)
+        return y
+
+
+__all__ = ["Dims", "GroupedLinearFP8", "GroupedLinearMX4", "MoELayer", "MOE_ROUTE_TOPK", "MOE_ROUTE_HASH"]
 
 
 class HostPipeline:
