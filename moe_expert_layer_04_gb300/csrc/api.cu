@@ -1398,7 +1398,7 @@ moe_status moe_mx4_matmul(const uint8_t *a_q, const uint8_t *a_sf, int a_bits,
     if (!fp8_groups_ok(G, max_rows) || N < 8 || N % 8 != 0 || K < 32 || K % 32 != 0 ||
         w_rows < 0 || (a_bits != 4 && a_bits != 8))
         return MOE_ERR_INVALID_ARG;
-    if ((long long)G * N >= (1LL << 31) || (a_bits == 8 && K % 128 != 0))
+    if ((long long)G * N >= (1LL << 31) - 256 || (a_bits == 8 && K % 128 != 0))
         return MOE_ERR_UNSUPPORTED;
     if (!offsets || !all_aligned16({a_q, a_sf, b_q, b_sf, out}) || (a_bits == 8 && !aligned32(b_q)))
         return MOE_ERR_INVALID_ARG;

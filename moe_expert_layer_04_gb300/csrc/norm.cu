@@ -54,6 +54,7 @@ struct NormRows {
     int T, d8, threads;   // threads of a row, a multiple of 32
     float eps, inv_d;
     int format;
+    int *status;
     const uint4 *x, *residual;
     const float *weight;
     uint4 *residual_out, *y;
@@ -113,7 +114,8 @@ __device__ __forceinline__ void store_codes(const NormRows &p, size_t row, int c
         static_cast<uint8_t *>(p.scales)[row * p.scale_pitch + (c >> 2)] = (uint8_t)code;
 }
 
-// A row's `threads` threads hold V vectors of eight elements each.
+// Few rows, or long ones: a CTA for each (or for a few short ones).  A row's `threads`
+// threads hold V vectors of eight elements each.
 template <int V>
 __global__ void __launch_bounds__(1024) rmsnorm_kernel(const NormRows p) {
     __shared__ float part[32];
@@ -168,8 +170,133 @@ __global__ void __launch_bounds__(1024) rmsnorm_kernel(const NormRows p) {
     }
 }
 
+// ------------------------------------------------------- many rows, in a ring
+//
+// A CTA takes every gridDim.x-th group of rows (one row, or as many short ones as its threads
+// hold) and has the next kRing groups on their way into shared memory by bulk copies, so that
+// the loads do not stop while a row is summed and written, and the weight stays in
+// registers.  The barrier of a row's sum is also what frees its place in the ring.
+constexpr int kRing = 4;
+constexpr int kRingRows = 2;   // rows for each SM, from where the ring pays
+constexpr int kRingThreads = 256;
+
+struct Ring {
+    uint64_t *full;      // [kRing]
+    volatile int *abort;
+    int *status;
+    int arrays;          // rows of so many arrays make a group
+    const uint4 *src[3];
+    uint4 *smem;
+    int group;           // vectors of a group of one array
+};
+
+__device__ __forceinline__ void ring_load(const Ring &r, int slot, long long row, int rows, int d8) {
+    const uint32_t bytes = (uint32_t)rows * d8 * 16;
+    mbar_arrive_expect_tx(&r.full[slot], r.arrays * bytes);
+    for (int i = 0; i < r.arrays; ++i)
+        bulk_load(r.smem + (slot * r.arrays + i) * r.group, r.src[i] + row * d8, bytes,
+                  &r.full[slot]);
+}
+
+// The group in `slot` has come: the same answer for the whole CTA.  Where the wait ran out,
+// the copies still in flight (of the groups from row `base` on) are waited for as well.
+__device__ __forceinline__ bool ring_wait(const Ring &r, int slot, uint32_t parity, long long base,
+                                          long long step, long long T) {
+    const WaitCtl wc{r.abort, r.status, kWaitLimitCycles};
+    if (__syncthreads_and(mbar_wait(&r.full[slot], parity, wc))) return true;
+    if (threadIdx.x == 0)
+        for (int i = 0; i < kRing; ++i)
+            if (base + i * step < T)
+                mbar_wait_teardown(&r.full[(slot + i) % kRing],
+                                   slot + i < kRing ? parity : parity ^ 1u, kWaitLimitCycles);
+    __syncthreads();
+    return false;
+}
+
+template <int V>
+__global__ void __launch_bounds__(kRingThreads, 3) rmsnorm_ring_kernel(const NormRows p) {
+    extern __shared__ uint4 ring_smem[];
+    __shared__ uint64_t full[kRing];
+    __shared__ int abort_s;
+    __shared__ float part[2][8];
+    const int per = blockDim.x / p.threads;
+    const int in_row = threadIdx.x % p.threads, my = threadIdx.x / p.threads;
+    const Ring r{full, &abort_s, p.status, p.residual ? 2 : 1, {p.x, p.residual, nullptr}, ring_smem,
+                 per * p.d8};
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kRing; ++i) mbar_init(&full[i], 1);
+        abort_s = 0;
+        fence_barrier_init();
+    }
+    __syncthreads();
+    wait_for_kernels_ahead();
+    let_kernels_behind_begin();
+    const long long first = (long long)blockIdx.x * per, step = (long long)gridDim.x * per;
+    auto load = [&](int slot, long long base) {
+        if (base < p.T) ring_load(r, slot, base, (int)min((long long)per, p.T - base), p.d8);
+    };
+    if (threadIdx.x == 0)
+        for (int i = 0; i < kRing; ++i) load(i, first + i * step);
+    float w[V][8];
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+        const int c = in_row + j * p.threads;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[j][i] = c < p.d8 ? __ldg(p.weight + 8 * c + i) : 0.0f;
+    }
+    int slot = 0, turn = 0;
+    uint32_t ph = 0;
+    for (long long base = first; base < p.T; base += step, turn ^= 1) {
+        const long long row = base + my;
+        const bool has = row < p.T;
+        if (!ring_wait(r, slot, ph, base, step, p.T)) return;
+        const uint4 *at = ring_smem + slot * r.arrays * r.group + my * p.d8;
+        uint4 v[V];
+        float ss = 0.0f;
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            const int c = in_row + j * p.threads;
+            v[j] = make_uint4(0, 0, 0, 0);
+            float f[8];
+            if (has && c < p.d8) {
+                v[j] = at[c];
+                if (p.residual) {
+                    float g[8];
+                    unpack8(v[j], f);
+                    unpack8(at[r.group + c], g);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) f[i] += g[i];
+                    v[j] = pack8(f);
+                    p.residual_out[row * p.d8 + c] = v[j];
+                }
+            }
+            unpack8(v[j], f);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) ss = fmaf(f[i], f[i], ss);
+        }
+        ss = row_sum(ss, p.threads >> 5, part[turn]);
+        if (p.threads == 32) __syncthreads();   // (the sum has none)
+        if (threadIdx.x == 0) load(slot, base + kRing * step);
+        if (++slot == kRing) { slot = 0; ph ^= 1u; }
+        const float rs = 1.0f / sqrtf(fmaf(ss, p.inv_d, p.eps));
+        if (has && in_row == 0 && p.rstd) p.rstd[row] = rs;
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            const int c = in_row + j * p.threads;
+            const bool live = has && c < p.d8;
+            float f[8];
+            unpack8(v[j], f);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) f[i] = f[i] * rs * w[j][i];
+            if (live && p.y) p.y[row * p.d8 + c] = pack8(f);
+            if (p.format != MOE_ROWS_NONE) store_codes(p, (size_t)row, c, live, f);
+        }
+    }
+}
+
 struct NormBwd {
     int T, d8, threads;
+    int *status;
     float inv_d;
     const uint4 *x, *dy, *d_residual;
     const float *weight, *rstd;
@@ -177,10 +304,104 @@ struct NormBwd {
     float *part;   // [slots, d]: a row of partial sums for each row in flight
 };
 
-// The rows slot, slot + slots, ... of one slot; the next row's loads are issued before
-// this row's sum.
-template <int V, int MOST, int CTAS>
-__global__ void __launch_bounds__(MOST, CTAS) rmsnorm_bwd_kernel(const NormBwd p) {
+template <int V>
+__global__ void __launch_bounds__(kRingThreads, 2) rmsnorm_bwd_ring_kernel(const NormBwd p) {
+    extern __shared__ uint4 ring_smem[];
+    __shared__ uint64_t full[kRing];
+    __shared__ int abort_s;
+    __shared__ float part[2][8];
+    const int per = blockDim.x / p.threads;
+    const int in_row = threadIdx.x % p.threads, my = threadIdx.x / p.threads;
+    const Ring r{full, &abort_s, p.status, p.d_residual ? 3 : 2, {p.x, p.dy, p.d_residual}, ring_smem,
+                 per * p.d8};
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kRing; ++i) mbar_init(&full[i], 1);
+        abort_s = 0;
+        fence_barrier_init();
+    }
+    __syncthreads();
+    wait_for_kernels_ahead();
+    let_kernels_behind_begin();
+    const long long first = (long long)blockIdx.x * per, step = (long long)gridDim.x * per;
+    auto load = [&](int slot, long long base) {
+        if (base < p.T) ring_load(r, slot, base, (int)min((long long)per, p.T - base), p.d8);
+    };
+    if (threadIdx.x == 0)
+        for (int i = 0; i < kRing; ++i) load(i, first + i * step);
+    float w[V][8], dw[V][8];
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+        const int c = in_row + j * p.threads;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            w[j][i] = c < p.d8 ? __ldg(p.weight + 8 * c + i) : 0.0f;
+            dw[j][i] = 0.0f;
+        }
+    }
+    int slot = 0, turn = 0;
+    uint32_t ph = 0;
+    for (long long base = first; base < p.T; base += step, turn ^= 1) {
+        const long long row = base + my;
+        const bool has = row < p.T;
+        const float rs = has ? __ldg(p.rstd + row) : 0.0f;
+        if (!ring_wait(r, slot, ph, base, step, p.T)) return;
+        const uint4 *at = ring_smem + slot * r.arrays * r.group + my * p.d8;
+        uint4 v[V], dr[V];
+        float a[V][8];
+        float dot = 0.0f;
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            const int c = in_row + j * p.threads;
+            const bool live = has && c < p.d8;
+            v[j] = dr[j] = make_uint4(0, 0, 0, 0);
+            uint4 dy = make_uint4(0, 0, 0, 0);
+            if (live) {
+                v[j] = at[c];
+                dy = at[r.group + c];
+                if (p.d_residual) dr[j] = at[2 * r.group + c];
+            }
+            float f[8], g[8];
+            unpack8(v[j], f);
+            unpack8(dy, g);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float vh = f[i] * rs;
+                dw[j][i] = fmaf(g[i], vh, dw[j][i]);
+                a[j][i] = g[i] * w[j][i];
+                dot = fmaf(a[j][i], vh, dot);
+            }
+        }
+        const float m = row_sum(dot, p.threads >> 5, part[turn]) * p.inv_d;
+        if (p.threads == 32) __syncthreads();
+        if (threadIdx.x == 0) load(slot, base + kRing * step);
+        if (++slot == kRing) { slot = 0; ph ^= 1u; }
+        if (!has) continue;
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            const int c = in_row + j * p.threads;
+            if (c >= p.d8) continue;
+            float f[8], g[8];
+            unpack8(v[j], f);
+            unpack8(dr[j], g);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) g[i] += rs * (a[j][i] - f[i] * rs * m);
+            p.dx[row * p.d8 + c] = pack8(g);
+        }
+    }
+    float4 *dst = reinterpret_cast<float4 *>(p.part + (first + my) * p.d8 * 8);
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+        const int c = in_row + j * p.threads;
+        if (c >= p.d8) continue;
+        dst[2 * c] = make_float4(dw[j][0], dw[j][1], dw[j][2], dw[j][3]);
+        dst[2 * c + 1] = make_float4(dw[j][4], dw[j][5], dw[j][6], dw[j][7]);
+    }
+}
+
+// Long rows.  The rows slot, slot + slots, ... of one slot; the next row's loads are issued
+// before this row's sum.
+template <int V>
+__global__ void __launch_bounds__(512) rmsnorm_bwd_kernel(const NormBwd p) {
     __shared__ float part[2][32];
     wait_for_kernels_ahead();
     let_kernels_behind_begin();
@@ -312,24 +533,43 @@ RowShape row_shape(int d8, int most) {
     return s;
 }
 
-// Backward: two vectors a thread up to d = 4096 (256 threads, CTAs to an SM as their
-// registers allow), more beyond.
-constexpr int kBwdCtas = 2;
-RowShape bwd_shape(int d8) { return d8 <= 512 ? row_shape(d8, 256) : row_shape(d8, 512); }
+// Rows that the ring kernels take: V <= 2 vectors for each of 256 threads.
+constexpr int kRingVecs = 2 * kRingThreads;
+RowShape ring_shape(int d8) {
+    RowShape s = row_shape(d8, kRingThreads);
+    s.rows = kRingThreads / s.threads;
+    return s;
+}
+
+RowShape bwd_shape(int d8) { return d8 <= kRingVecs ? ring_shape(d8) : row_shape(d8, 512); }
 
 // Rows in flight of the backward: CTAs for the SMs, no more than there are rows.
 int bwd_ctas(int T, int d8, const RowShape &s) {
     const long long want = ((long long)T + s.rows - 1) / s.rows;
-    const long long most = (long long)num_sms() * (d8 <= 512 ? kBwdCtas : 1);
+    const long long most = (long long)num_sms() * (d8 <= kRingVecs ? 2 : 1);
     return (int)(want < most ? want : most);
+}
+
+template <auto KERN, typename P>
+moe_status launch_ring(int ctas, const RowShape &s, int arrays, int d, cudaStream_t st, const P &p) {
+    static bool attr_set[64] = {};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return MOE_ERR_CUDA;
+    if (dev < 0 || dev >= 64) return MOE_ERR_UNSUPPORTED;
+    if (!attr_set[dev]) {
+        if (cudaFuncSetAttribute(KERN, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 kRing * 3 * kRingVecs * 16) != cudaSuccess)
+            return MOE_ERR_CUDA;
+        attr_set[dev] = true;
+    }
+    return launch_early(KERN, dim3(ctas), s.threads * s.rows, kRing * arrays * s.rows * d * 2, st, p);
 }
 
 }  // namespace
 
 moe_status launch_rmsnorm(const moe_norm_args *a, cudaStream_t st) {
-    // few rows: one vector a thread, for the latency; many: two, for more rows in flight
     const int d8 = a->d / 8;
-    const RowShape s = row_shape(d8, a->T > 2 * num_sms() && d8 > 256 && d8 <= 2048 ? (d8 + 1) / 2 : 1024);
+    const RowShape s = row_shape(d8, 1024);
     NormRows p;
     std::memset(&p, 0, sizeof p);
     p.T = a->T;
@@ -347,6 +587,17 @@ moe_status launch_rmsnorm(const moe_norm_args *a, cudaStream_t st) {
     p.q = a->q;
     p.scales = a->scales;
     p.scale_pitch = a->format == MOE_ROWS_FP8 ? fp8_blocks(a->d) : mx_sf_pitch(a->d);
+    p.status = device_status_ptr();
+    if (!p.status) return MOE_ERR_CUDA;
+    // Many rows go through the ring (RING_FIGURES).
+    if (d8 <= kRingVecs && a->T > kRingRows * num_sms()) {
+        const RowShape r = ring_shape(d8);
+        p.threads = r.threads;
+        const long long want = ((long long)a->T + r.rows - 1) / r.rows, most = 3LL * num_sms();
+        const int ctas = (int)(want < most ? want : most), arrays = a->residual ? 2 : 1;
+        return r.V == 1 ? launch_ring<rmsnorm_ring_kernel<1>>(ctas, r, arrays, a->d, st, p)
+                        : launch_ring<rmsnorm_ring_kernel<2>>(ctas, r, arrays, a->d, st, p);
+    }
     const dim3 grid((a->T + s.rows - 1) / s.rows);
     const int threads = s.threads * s.rows;
     if (s.V == 1) return launch_early(rmsnorm_kernel<1>, grid, threads, 0, st, p);
@@ -374,20 +625,21 @@ moe_status launch_rmsnorm_bwd(const moe_norm_bwd_args *a, cudaStream_t st) {
     p.rstd = a->rstd;
     p.dx = reinterpret_cast<uint4 *>(a->dx);
     p.part = static_cast<float *>(a->ws);
+    p.status = device_status_ptr();
+    if (!p.status) return MOE_ERR_CUDA;
     const int ctas = bwd_ctas(a->T, p.d8, s), threads = s.threads * s.rows;
     moe_status r = MOE_OK;
     if (ctas > 0) {
-        const dim3 grid(ctas);
-        if (p.d8 <= 256)
-            r = launch_early(rmsnorm_bwd_kernel<1, 256, kBwdCtas>, grid, threads, 0, st, p);
-        else if (p.d8 <= 512)
-            r = launch_early(rmsnorm_bwd_kernel<2, 256, kBwdCtas>, grid, threads, 0, st, p);
-        else if (s.V == 2)
-            r = launch_early(rmsnorm_bwd_kernel<2, 512, 1>, grid, threads, 0, st, p);
+        if (p.d8 <= kRingVecs) {
+            const int arrays = a->d_residual ? 3 : 2;
+            r = s.V == 1 ? launch_ring<rmsnorm_bwd_ring_kernel<1>>(ctas, s, arrays, a->d, st, p)
+                         : launch_ring<rmsnorm_bwd_ring_kernel<2>>(ctas, s, arrays, a->d, st, p);
+        } else if (s.V == 2)
+            r = launch_early(rmsnorm_bwd_kernel<2>, dim3(ctas), threads, 0, st, p);
         else if (s.V == 4)
-            r = launch_early(rmsnorm_bwd_kernel<4, 512, 1>, grid, threads, 0, st, p);
+            r = launch_early(rmsnorm_bwd_kernel<4>, dim3(ctas), threads, 0, st, p);
         else
-            r = launch_early(rmsnorm_bwd_kernel<8, 512, 1>, grid, threads, 0, st, p);
+            r = launch_early(rmsnorm_bwd_kernel<8>, dim3(ctas), threads, 0, st, p);
     }
     if (r != MOE_OK) return r;
     // without rows: zeros

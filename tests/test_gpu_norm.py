@@ -59,7 +59,9 @@ def reference(x, w, residual=None):
 
 
 SHAPES = [(1, 8), (1, 4096), (3, 40), (7, 1184), (130, 256), (65, 2056), (5, 8200), (2, 16392),
-          (3, 32768), (4099, 128), (300, 7168)]
+          (3, 32768), (4099, 128), (300, 7168),
+          # more rows than the SMs hold at once
+          (1000, 4096), (700, 1184), (311, 256), (5000, 8), (1231, 2056), (613, 4088)]
 
 
 @pytest.mark.parametrize("T,d", SHAPES)
@@ -110,7 +112,7 @@ def check_codes(a, u, fmt):
 
 
 @pytest.mark.parametrize("T,d", [(1, 32), (1, 4096), (5, 1184), (130, 288), (33, 8224), (3, 32768),
-                                 (4099, 128)])
+                                 (4099, 128), (700, 4096), (1000, 96), (901, 2080)])
 @pytest.mark.parametrize("fmt", [_lib.MOE_ROWS_FP8, _lib.MOE_ROWS_MXFP8, _lib.MOE_ROWS_MXFP4])
 def test_forward_codes(T, d, fmt):
     rng = np.random.default_rng(T * 5 + d + fmt)
@@ -210,6 +212,36 @@ def test_backward_is_the_gradient():
         # dx is bf16 (2^-8 of each element), differences are off by O(h^2)
         lim = 2.0 ** -8 * np.abs(parts).sum() + 1e-4
         assert abs(parts.sum() + (f64(o["d_weight"]) * b).sum() - num) <= lim
+
+
+def test_places_behind_32_bits():
+    """Elements past 2^31, the last rows of a long list, both directions."""
+    T, d, n = 600_000, 4096, 64
+    rng = np.random.default_rng(2)
+    w = torch.from_numpy(rng.standard_normal(d).astype(np.float32))
+    last, g = rows(rng, n, d), rows(rng, n, d)
+    x = torch.zeros(T, d, dtype=torch.bfloat16, device="cuda")
+    x[-n:] = last.cuda()
+    y, rstd = torch.empty_like(x), torch.empty(T, device="cuda")
+    q, s = torch.empty(T, d, dtype=torch.uint8, device="cuda"), torch.empty(T, 32, device="cuda")
+    _lib.moe_rmsnorm(dict(T=T, d=d, eps=EPS, format=_lib.MOE_ROWS_FP8, x=x, weight=w.cuda(), y=y, rstd=rstd,
+                          q=q, scales=s))
+    ok()
+    v, r, u = reference(last, w)
+    between(y[-n:], u, E * np.abs(u))
+    check_codes(dict(q=q[-n:], scales=s[-n:]), u, _lib.MOE_ROWS_FP8)
+    assert (y[:-n] == 0).all() and (q[:-n] & 127 == 0).all()        # (zeros of either sign)
+    y.zero_()
+    y[-n:] = g.cuda()
+    ws = empty(_lib.moe_rmsnorm_bwd_workspace_size(T, d))
+    dw = torch.empty(d, device="cuda")
+    _lib.moe_rmsnorm_backward(dict(T=T, d=d, x=x, weight=w.cuda(), rstd=rstd, dy=y, dx=y, d_weight=dw, ws=ws))
+    ok()
+    r = f64(rstd[-n:])[:, None]
+    a, vh = f64(g) * f64(w), v * r
+    dot = (a * vh).mean(1, keepdims=True)
+    between(y[-n:], r * (a - vh * dot), E * r * (np.abs(a) + np.abs(vh) * np.abs(a * vh).mean(1, keepdims=True)))
+    assert (y[:-n] == 0).all()
 
 
 def test_no_rows():
