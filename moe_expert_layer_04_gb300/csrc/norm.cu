@@ -178,14 +178,18 @@ __global__ void __launch_bounds__(1024) rmsnorm_kernel(const NormRows p) {
 // bulk copies, so that the loads do not stop while a row is summed and written, and the
 // weight stays in registers.  The barrier of a row's sum is also what frees its place in the
 // ring.  Measured, of the copy bandwidth: backward of 16384 x 4096 83 us, 96 % (103 with a
-// row's loads into registers); forward of 4096 x 4096 with the residual 23 us, 86 %, with FP8
-// rows 28 us, 79 %: half of what the codes add is their bytes, half the instructions that
-// make them.  One vector a thread and fewer rows a barrier: 4096 x 2048 17 us against 12.5.
-// Three CTAs an SM and four groups ahead; 4 and 3, 4 and 2, 3 and 2 are 1 to 6 % slower.
+// row's loads into registers), of 4096 x 512 7.2 us (23 with one row a CTA); forward of
+// 4096 x 4096 with the residual 23 us, 86 %, with FP8 rows 28 us, 79 %: half of what the codes
+// add is their bytes, half the instructions that make them.  The forward takes three CTAs an
+// SM and four rows ahead (23.2 and 28.3 us; four CTAs and two ahead 23.3 and 28.7, four and
+// three 24.0 and 29.1, three and two 24.0 and 30.0).
 constexpr int kRing = 4;
 constexpr int kFwdCtas = 3, kBwdCtas = 2;   // to an SM
-constexpr int kRingRows = 2;   // rows for each SM, from where the ring pays
 constexpr int kRingThreads = 256;
+// The forward's ring takes rows that nearly fill its threads' two vectors, where there are more
+// of them than the SMs hold CTAs of the other kernel at once, and not so many that its
+// waves' ends no longer count.
+constexpr int kFwdVecs = 7 * kRingThreads / 4, kFwdMore = 6, kFwdMost = 64;   // rows to an SM
 
 struct Ring {
     uint64_t *full;      // [kRing]
@@ -263,10 +267,8 @@ __global__ void __launch_bounds__(kRingThreads, kFwdCtas) rmsnorm_ring_kernel(co
     __shared__ uint64_t full[kRing];
     __shared__ int abort_s;
     __shared__ float part[2][8];
-    const int per = blockDim.x / p.threads;
-    const int in_row = threadIdx.x % p.threads, my = threadIdx.x / p.threads;
     const Ring r{full, &abort_s, p.status, p.residual ? 2 : 1, {p.x, p.residual, nullptr}, ring_smem,
-                 per * p.d8};
+                 p.d8};
     if (threadIdx.x == 0) {
         for (int i = 0; i < kRing; ++i) mbar_init(&full[i], 1);
         abort_s = 0;
@@ -275,16 +277,16 @@ __global__ void __launch_bounds__(kRingThreads, kFwdCtas) rmsnorm_ring_kernel(co
     __syncthreads();
     wait_for_kernels_ahead();
     let_kernels_behind_begin();
-    const long long first = (long long)blockIdx.x * per, step = (long long)gridDim.x * per;
-    auto load = [&](int slot, long long base) {
-        if (base < p.T) ring_load(r, slot, base, (int)min((long long)per, p.T - base), p.d8);
+    const long long step = gridDim.x;
+    auto load = [&](int slot, long long row) {
+        if (row < p.T) ring_load(r, slot, row, 1, p.d8);
     };
     if (threadIdx.x == 0)
-        for (int i = 0; i < kRing; ++i) load(i, first + i * step);
+        for (int i = 0; i < kRing; ++i) load(i, blockIdx.x + i * step);
     uint64_t w[V][4];
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-        const int c = in_row + j * p.threads;
+        const int c = threadIdx.x + j * blockDim.x;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const float2 f = c < p.d8 ? __ldg(reinterpret_cast<const float2 *>(p.weight) + 4 * c + i)
@@ -294,16 +296,14 @@ __global__ void __launch_bounds__(kRingThreads, kFwdCtas) rmsnorm_ring_kernel(co
     }
     int slot = 0, turn = 0;
     uint32_t ph = 0;
-    for (long long base = first; base < p.T; base += step, turn ^= 1) {
-        const long long row = base + my;
-        const bool has = row < p.T;
-        if (!ring_wait(r, slot, ph, base, step, p.T)) return;
-        const uint4 *at = ring_smem + slot * r.arrays * r.group + my * p.d8;
+    for (long long row = blockIdx.x; row < p.T; row += step, turn ^= 1) {
+        if (!ring_wait(r, slot, ph, row, step, p.T)) return;
+        const uint4 *at = ring_smem + slot * r.arrays * r.group;
         uint64_t f[V][4], ss = 0;
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-            const int c = in_row + j * p.threads;
-            const bool live = has && c < p.d8;
+            const int c = threadIdx.x + j * blockDim.x;
+            const bool live = c < p.d8;
             uint4 v = live ? at[c] : make_uint4(0, 0, 0, 0);
             if (p.residual && live) {
                 const uint4 b = at[r.group + c];
@@ -321,17 +321,16 @@ __global__ void __launch_bounds__(kRingThreads, kFwdCtas) rmsnorm_ring_kernel(co
             for (int i = 0; i < 4; ++i) ss = fma2(f[j][i], f[j][i], ss);
         }
         const float2 s2 = two(ss);
-        const float sum = row_sum(s2.x + s2.y, p.threads >> 5, part[turn]);
-        if (p.threads == 32) __syncthreads();   // (the sum has none)
-        if (threadIdx.x == 0) load(slot, base + kRing * step);
+        const float sum = row_sum(s2.x + s2.y, blockDim.x >> 5, part[turn]);
+        if (threadIdx.x == 0) load(slot, row + kRing * step);
         if (++slot == kRing) { slot = 0; ph ^= 1u; }
         const float rs = 1.0f / sqrtf(fmaf(sum, p.inv_d, p.eps));
-        if (has && in_row == 0 && p.rstd) p.rstd[row] = rs;
+        if (threadIdx.x == 0 && p.rstd) p.rstd[row] = rs;
         const uint64_t rs2 = pair_f(rs, rs);
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-            const int c = in_row + j * p.threads;
-            const bool live = has && c < p.d8;
+            const int c = threadIdx.x + j * blockDim.x;
+            const bool live = c < p.d8;
             uint64_t u2[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) u2[i] = mul2(mul2(f[j][i], rs2), w[j][i]);
@@ -634,7 +633,12 @@ moe_status launch_ring(int ctas, const RowShape &s, int arrays, int d, cudaStrea
 
 moe_status launch_rmsnorm(const moe_norm_args *a, cudaStream_t st) {
     const int d8 = a->d / 8;
-    const RowShape s = row_shape(d8, 1024);
+    // Rows of 3584 to 4096: with many of them a thread holds two vectors, so that more rows are
+    // on their way in an SM (700 rows of 4096 4.1 us against 5.3, with FP8 rows 16384
+    // 102 us against 106), with few of them one (300 rows 2.9 us against 3.1; other
+    // widths: 2000 rows of 2304 7.9 us against 8.5).
+    const bool wide = d8 >= kFwdVecs && d8 <= kRingVecs;
+    const RowShape s = row_shape(d8, wide && a->T > 2 * num_sms() ? kRingThreads : 1024);
     NormRows p;
     std::memset(&p, 0, sizeof p);
     p.T = a->T;
@@ -654,13 +658,12 @@ moe_status launch_rmsnorm(const moe_norm_args *a, cudaStream_t st) {
     p.scale_pitch = a->format == MOE_ROWS_FP8 ? fp8_blocks(a->d) : mx_sf_pitch(a->d);
     p.status = device_status_ptr();
     if (!p.status) return MOE_ERR_CUDA;
-    // Many rows go through the ring: 4096 rows of 4096 with FP8 rows 28 us there, 29.5 a CTA
-    // for each row (without codes 23 and 26); few do not: 300 rows 3.3 us against 3.9.
-    if (d8 <= kRingVecs && a->T > kRingRows * num_sms()) {
+    // The ring: 2000 rows of 4096 12.2 us there, 14.4 in the other kernel (with FP8 rows 14.9
+    // and 16.5), 4096 rows 23.3 and 25.4 (28.3 and 29.3), 16384 rows 90 and 88 (111 and 102);
+    // narrower rows leave threads idle: 2000 rows of 1536 5.5 and 5.0.
+    if (wide && a->T > kFwdMore * num_sms() && a->T <= kFwdMost * num_sms()) {
         const RowShape r = ring_shape(d8);
-        p.threads = r.threads;
-        const long long want = ((long long)a->T + r.rows - 1) / r.rows, most = (long long)kFwdCtas * num_sms();
-        const int ctas = (int)(want < most ? want : most), arrays = a->residual ? 2 : 1;
+        const int ctas = kFwdCtas * num_sms(), arrays = a->residual ? 2 : 1;
 #define MOE_RING(F) return launch_ring<rmsnorm_ring_kernel<2, F>>(ctas, r, arrays, a->d, st, p)
         switch (a->format) {
         case MOE_ROWS_FP8: MOE_RING(MOE_ROWS_FP8);

@@ -61,7 +61,8 @@ def reference(x, w, residual=None):
 SHAPES = [(1, 8), (1, 4096), (3, 40), (7, 1184), (130, 256), (65, 2056), (5, 8200), (2, 16392),
           (3, 32768), (4099, 128), (300, 7168),
           # more rows than the SMs hold at once
-          (1000, 4096), (700, 1184), (311, 256), (5000, 8), (1231, 2056), (613, 4088)]
+          (1000, 4096), (700, 1184), (311, 256), (5000, 8), (1231, 2056), (613, 4088),
+          (913, 3592), (1300, 3584)]
 
 
 @pytest.mark.parametrize("T,d", SHAPES)
@@ -112,7 +113,8 @@ def check_codes(a, u, fmt):
 
 
 @pytest.mark.parametrize("T,d", [(1, 32), (1, 4096), (5, 1184), (130, 288), (33, 8224), (3, 32768),
-                                 (4099, 128), (700, 4096), (1000, 96), (901, 2080)])
+                                 (4099, 128), (700, 4096), (1000, 96), (901, 2080),
+                                 (1000, 4096), (1300, 3616)])
 @pytest.mark.parametrize("fmt", [_lib.MOE_ROWS_FP8, _lib.MOE_ROWS_MXFP8, _lib.MOE_ROWS_MXFP4])
 def test_forward_codes(T, d, fmt):
     rng = np.random.default_rng(T * 5 + d + fmt)
@@ -125,8 +127,8 @@ def test_forward_codes(T, d, fmt):
 
 def test_fp8_short_last_block():
     rng = np.random.default_rng(3)
-    for d in (16, 144, 1040):
-        x, w = rows(rng, 9, d), torch.ones(d)
+    for T, d in ((9, 16), (9, 144), (9, 1040), (1000, 3600)):
+        x, w = rows(rng, T, d), torch.ones(d)
         check_codes(forward(x, w, None, _lib.MOE_ROWS_FP8), reference(x, w)[2], _lib.MOE_ROWS_FP8)
 
 
