@@ -795,9 +795,10 @@ moe_status moe_mx4_gather(const uint16_t *x, const int32_t *slot_row, int T, int
  * them), a_sf [R, moe_mx_sf_pitch(K)]; b_q [G, N, K/2], b_sf [G, N, moe_mx_sf_pitch(K)];
  * offsets int32 [G+1] on the device with R = offsets[G] <= max_rows (offsets that descend
  * or leave [0, max_rows] are cut to it and recorded as MOE_ERR_INVALID_ARG on the device);
- * out [R, N] bf16, rows outside every group are left as they were.  G = 1 is a dense
- * product.  N % 8 == 0, 1 <= G <= 1025, K % 32 == 0; with a_bits 8 also K % 128 == 0 (else
- * MOE_ERR_UNSUPPORTED) and b_q 32-byte aligned. */
+ * out [R, N] bf16, rows outside every group are left as they were.  a_q, a_sf and out have
+ * max_rows rows of memory, also where R is less.  G = 1 is a dense product.  N % 8 == 0,
+ * 1 <= G <= 1025, K % 32 == 0, with a_bits 8 b_q 32-byte aligned; G N < 2^31 - 256, with
+ * a_bits 8 K % 128 == 0 (else MOE_ERR_UNSUPPORTED). */
 moe_status moe_mx4_matmul(const uint8_t *a_q, const uint8_t *a_sf, int a_bits,
                           const int32_t *offsets, int G, int max_rows, const uint8_t *b_q,
                           const uint8_t *b_sf, const float *row_weight, int w_rows, int N, int K,
@@ -809,7 +810,8 @@ moe_status moe_mx4_matmul(const uint8_t *a_q, const uint8_t *a_sf, int a_bits,
  *   y[r]    = bf16( row_weight[r] * (h~[r] W2~[g]^T) )
  * x_perm_q [R, d] / x_perm_sf (moe_mx_gather); W13_q [G, 2I, d/2] / W13_sf, W2_q
  * [G, d, I/2] / W2_sf (MXFP4, codes 32-byte aligned); outputs h_q [R, I], h_sf, y_perm
- * [R, d] bf16.  d % 128 == 0, I % 128 == 0 (else MOE_ERR_UNSUPPORTED).  No workspace. */
+ * [R, d] bf16; buffers of rows have max_rows of them.  d % 128 == 0, I % 128 == 0,
+ * G max(2I, d) < 2^31 - 256 (else MOE_ERR_UNSUPPORTED).  No workspace. */
 moe_status moe_expert_ffn_mx4(const uint8_t *x_perm_q, const uint8_t *x_perm_sf,
                               const int32_t *offsets, int G, int max_rows, const uint8_t *W13_q,
                               const uint8_t *W13_sf, const uint8_t *W2_q, const uint8_t *W2_sf,
@@ -889,8 +891,8 @@ moe_status moe_rmsnorm_backward(const moe_norm_bwd_args *args, void *stream);
  * moe_balance_loss writes counts, tokens, load, seq_loss and loss (dloss and dlogits are
  * not read); moe_balance_loss_backward reads tokens and load of it and writes dlogits (ids,
  * counts, seq_loss, loss and ws are not read).
- * T >= 0, 1 <= n_seq <= 65535, 1 <= E <= 1024, 1 <= k <= 32 (else MOE_ERR_UNSUPPORTED),
- * (T + n_seq) E < 2^40.  seq_offsets int32 [n_seq+1] on the device, or NULL: one sequence of
+ * 0 <= T <= 2^30, 1 <= n_seq <= 65535, 1 <= E <= 1024, 1 <= k <= 32 (above:
+ * MOE_ERR_UNSUPPORTED).  seq_offsets int32 [n_seq+1] on the device, or NULL: one sequence of
  * all T tokens (n_seq = 1).  Offsets that descend or leave [0, T] are cut to it and recorded
  * as MOE_ERR_INVALID_ARG on the device, as are ids outside [0, E), which are not counted.
  * logits and dlogits 16-byte aligned; dlogits may be logits.  Workspace:

@@ -342,6 +342,28 @@ def _stream(stream):
     return _raw_stream(_get_device())
 
 
+_Tensor = torch.Tensor
+
+
+def _device():
+    """The current device; none that a tensor could be on where there is no GPU."""
+    try:
+        return _get_device()
+    except RuntimeError:
+        return -2
+
+
+def _here(t, dtype=None, name="tensor"):
+    """_ptr of a tensor of the current device, where the call runs."""
+    if t.__class__ is _Tensor and t.dtype is dtype and t.is_contiguous():
+        at = t.get_device()
+        if at >= 0 and at == _get_device():
+            return t.data_ptr()
+    if isinstance(t, torch.Tensor) and t.is_cuda and t.get_device() != _device():
+        raise ValueError(f"{name}: on {t.device}, the current device is cuda:{_device()}")
+    return _ptr(t, dtype, name)
+
+
 def _check(fn, st):
     if st != MOE_OK:
         raise MoeError(fn, st)
@@ -843,42 +865,42 @@ def moe_layer_few(args: dict, stream=None):
 # ------------------------------------------------------------------- MXFP4
 
 def moe_mx4_quantize(src, rows, K, q, sf, stream=None):
-    st = load().moe_mx4_quantize(_ptr(src, BF16, "src"), int(rows), int(K), _ptr(q, U8, "q"),
-                                 _ptr(sf, U8, "sf"), _stream(stream))
+    st = load().moe_mx4_quantize(_here(src, BF16, "src"), int(rows), int(K), _here(q, U8, "q"),
+                                 _here(sf, U8, "sf"), _stream(stream))
     _check("moe_mx4_quantize", st)
 
 
 def moe_mx4_dequantize(q, sf, rows, K, out, stream=None):
-    st = load().moe_mx4_dequantize(_ptr(q, U8, "q"), _ptr(sf, U8, "sf"), int(rows), int(K),
-                                   _ptr(out, BF16, "out"), _stream(stream))
+    st = load().moe_mx4_dequantize(_here(q, U8, "q"), _here(sf, U8, "sf"), int(rows), int(K),
+                                   _here(out, BF16, "out"), _stream(stream))
     _check("moe_mx4_dequantize", st)
 
 
 def moe_mx4_gather(x, slot_row, T, d, k, x_perm_q, x_perm_sf, stream=None):
-    st = load().moe_mx4_gather(_ptr(x, BF16, "x"), _ptr(slot_row, I32, "slot_row"), T, d, k,
-                               _ptr(x_perm_q, U8, "x_perm_q"), _ptr(x_perm_sf, U8, "x_perm_sf"),
+    st = load().moe_mx4_gather(_here(x, BF16, "x"), _here(slot_row, I32, "slot_row"), T, d, k,
+                               _here(x_perm_q, U8, "x_perm_q"), _here(x_perm_sf, U8, "x_perm_sf"),
                                _stream(stream))
     _check("moe_mx4_gather", st)
 
 
 def moe_mx4_matmul(a_q, a_sf, a_bits, offsets, G, max_rows, b_q, b_sf, row_weight, w_rows, N, K,
                    out, stream=None):
-    st = load().moe_mx4_matmul(_ptr(a_q, U8, "a_q"), _ptr(a_sf, U8, "a_sf"), a_bits,
-                               _ptr(offsets, I32, "offsets"), G, max_rows, _ptr(b_q, U8, "b_q"),
-                               _ptr(b_sf, U8, "b_sf"), _ptr(row_weight, F32, "row_weight"),
-                               w_rows, N, K, _ptr(out, BF16, "out"), _stream(stream))
+    st = load().moe_mx4_matmul(_here(a_q, U8, "a_q"), _here(a_sf, U8, "a_sf"), a_bits,
+                               _here(offsets, I32, "offsets"), G, max_rows, _here(b_q, U8, "b_q"),
+                               _here(b_sf, U8, "b_sf"), _here(row_weight, F32, "row_weight"),
+                               w_rows, N, K, _here(out, BF16, "out"), _stream(stream))
     _check("moe_mx4_matmul", st)
 
 
 def moe_expert_ffn_mx4(x_perm_q, x_perm_sf, offsets, G, max_rows, W13_q, W13_sf, W2_q, W2_sf,
                        row_weight, S, d, I, clamp, h_q, h_sf, y_perm, stream=None):
-    st = load().moe_expert_ffn_mx4(_ptr(x_perm_q, U8, "x_perm_q"), _ptr(x_perm_sf, U8, "x_perm_sf"),
-                                   _ptr(offsets, I32, "offsets"), G, max_rows,
-                                   _ptr(W13_q, U8, "W13_q"), _ptr(W13_sf, U8, "W13_sf"),
-                                   _ptr(W2_q, U8, "W2_q"), _ptr(W2_sf, U8, "W2_sf"),
-                                   _ptr(row_weight, F32, "row_weight"), S, d, I, float(clamp),
-                                   _ptr(h_q, U8, "h_q"), _ptr(h_sf, U8, "h_sf"),
-                                   _ptr(y_perm, BF16, "y_perm"), _stream(stream))
+    st = load().moe_expert_ffn_mx4(_here(x_perm_q, U8, "x_perm_q"), _here(x_perm_sf, U8, "x_perm_sf"),
+                                   _here(offsets, I32, "offsets"), G, max_rows,
+                                   _here(W13_q, U8, "W13_q"), _here(W13_sf, U8, "W13_sf"),
+                                   _here(W2_q, U8, "W2_q"), _here(W2_sf, U8, "W2_sf"),
+                                   _here(row_weight, F32, "row_weight"), S, d, I, float(clamp),
+                                   _here(h_q, U8, "h_q"), _here(h_sf, U8, "h_sf"),
+                                   _here(y_perm, BF16, "y_perm"), _stream(stream))
     _check("moe_expert_ffn_mx4", st)
 
 
@@ -889,8 +911,10 @@ def _packer(mirror, **types):
     as they are, the tensors of `types` checked (dtype, device, contiguity) and replaced by
     their pointers, fields of neither zero; ws_bytes, where there is one, is ws's size.
     It is written out field by field: a loop over them with a ctypes.Structure takes twice as
-    long (7 of the 14 us of the smallest call)."""
-    fields, fmt, lines, names, env = mirror._fields_, "@", [], [], dict(_ptr=_ptr)
+    long (7 of the 14 us of the smallest call); so does a call for each tensor (4.4 us for
+    the norm's eight)."""
+    fields, fmt, lines, names, env = mirror._fields_, "@", [], [], dict(
+        here=_here, device=_device, Tensor=_Tensor)
     for i, (name, ctype) in enumerate(fields):
         fmt += {_I: "i", _F: "f", _P: "P", _Z: "N"}[ctype]
         if ctype in (_I, _F):
@@ -899,14 +923,16 @@ def _packer(mirror, **types):
             env[f"t{i}"] = types[name]
             names.append(f"v{i}")
             lines += [f"    v{i} = get({name!r})",
-                      f"    v{i} = 0 if v{i} is None else _ptr(v{i}, t{i}, {name!r})"]
+                      f"    v{i} = (0 if v{i} is None else v{i}.data_ptr() if v{i}.__class__ is Tensor "
+                      f"and v{i}.dtype is t{i} and v{i}.get_device() == dev and v{i}.is_contiguous() "
+                      f"else here(v{i}, t{i}, {name!r}))"]
         elif name == "ws_bytes":
             names.append("0 if get('ws') is None else get('ws').numel()")
         else:
             names.append("0")
     assert struct.calcsize(fmt) == ctypes.sizeof(mirror)
     env["pack"] = struct.Struct(fmt).pack
-    exec("def f(args):\n    get = args.get\n" + "\n".join(lines)
+    exec("def f(args):\n    get, dev = args.get, device()\n" + "\n".join(lines)
          + f"\n    return pack({', '.join(names)})", env)
     return env["f"]
 
@@ -958,8 +984,8 @@ def moe_gate_bwd_workspace_size(T, d, E) -> int:
 
 
 def moe_gate_backward(dlogits, x, W_g, T, d, E, dX, dW_g, ws, stream=None):
-    st = load().moe_gate_backward(_ptr(dlogits, F32, "dlogits"), _ptr(x, BF16, "x"),
-                                  _ptr(W_g, BF16, "W_g"), T, d, E, _ptr(dX, BF16, "dX"),
-                                  _ptr(dW_g, F32, "dW_g"), _ptr(ws, U8, "ws"),
+    st = load().moe_gate_backward(_here(dlogits, F32, "dlogits"), _here(x, BF16, "x"),
+                                  _here(W_g, BF16, "W_g"), T, d, E, _here(dX, BF16, "dX"),
+                                  _here(dW_g, F32, "dW_g"), _here(ws, U8, "ws"),
                                   0 if ws is None else ws.numel(), _stream(stream))
     _check("moe_gate_backward", st)

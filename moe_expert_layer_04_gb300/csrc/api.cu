@@ -1347,7 +1347,7 @@ moe_status moe_expert_ffn_fp8(const uint8_t *x_perm_q, const float *x_perm_s,
                               const float *row_weight, int S, int d, int I, float clamp,
                               uint8_t *h_q, float *h_s, uint16_t *y_perm, void *stream) {
     if (!fp8_groups_ok(G, max_rows) || d < 1 || I < 1 || S < 0) return MOE_ERR_INVALID_ARG;
-    if (d % 128 != 0 || I % 128 != 0 || (long long)G * (2LL * I > d ? 2LL * I : d) >= (1LL << 31))
+    if (d % 128 != 0 || I % 128 != 0 || (long long)G * (2LL * I > d ? 2LL * I : d) >= (1LL << 31) - 256)
         return MOE_ERR_UNSUPPORTED;
     if (!offsets || !(clamp > 0.0f) ||
         !all_aligned16({x_perm_q, x_perm_s, W13_q, W13_s, W2_q, W2_s, h_q, h_s, y_perm}))
@@ -1413,7 +1413,7 @@ moe_status moe_expert_ffn_mx4(const uint8_t *x_perm_q, const uint8_t *x_perm_sf,
                               const float *row_weight, int S, int d, int I, float clamp,
                               uint8_t *h_q, uint8_t *h_sf, uint16_t *y_perm, void *stream) {
     if (!fp8_groups_ok(G, max_rows) || d < 1 || I < 1 || S < 0) return MOE_ERR_INVALID_ARG;
-    if (d % 128 != 0 || I % 128 != 0 || (long long)G * (2LL * I > d ? 2LL * I : d) >= (1LL << 31))
+    if (d % 128 != 0 || I % 128 != 0 || (long long)G * (2LL * I > d ? 2LL * I : d) >= (1LL << 31) - 256)
         return MOE_ERR_UNSUPPORTED;
     if (!offsets || !(clamp > 0.0f) || !aligned32(W13_q) || !aligned32(W2_q) ||
         !all_aligned16({x_perm_q, x_perm_sf, W13_q, W13_sf, W2_q, W2_sf, h_q, h_sf, y_perm}))
@@ -1469,7 +1469,7 @@ moe_status moe_rmsnorm_backward(const moe_norm_bwd_args *a, void *stream) {
 // Shapes of the balance loss: MOE_OK, or why not.
 static moe_status balance_shape(int T, int E, int k, int n_seq) {
     if (T < 0 || E < 1 || k < 1 || n_seq < 1) return MOE_ERR_INVALID_ARG;
-    if (E > 1024 || k > 32 || n_seq > 65535 || ((long long)T + n_seq) * E >= (1LL << 40))
+    if (E > 1024 || k > 32 || n_seq > 65535 || T > 1 << 30)
         return MOE_ERR_UNSUPPORTED;
     return MOE_OK;
 }

@@ -673,7 +673,7 @@ moe_status launch_rmsnorm(const moe_norm_args *a, cudaStream_t st) {
         }
 #undef MOE_RING
     }
-    const dim3 grid((a->T + s.rows - 1) / s.rows);
+    const dim3 grid((unsigned)(((long long)a->T + s.rows - 1) / s.rows));
     const int threads = s.threads * s.rows;
     if (s.V == 1) return launch_early(rmsnorm_kernel<1>, grid, threads, 0, st, p);
     if (s.V == 2) return launch_early(rmsnorm_kernel<2>, grid, threads, 0, st, p);

@@ -473,7 +473,8 @@ class MoELayer:
     def norm(self, x, residual=None, stream=None):
         """The norm ahead of the layer: (rows [T, d] bf16, the residual stream after the
         addition).  Of dims.T rows into the layer's own buffers (with the codes of a
-        low-precision layer); of any other number, for forward_few(), new tensors."""
+        low-precision layer, which dispatch() of these rows moves: they are not changed in
+        between); of any other number, for forward_few(), new tensors."""
         D = self.dims
         if self.norm_eps is None:
             raise RuntimeError("layer built without norm_eps")

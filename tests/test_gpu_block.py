@@ -327,3 +327,15 @@ def test_step_in_graphs_and_streams():
     for n, a, b in zip(names, kept(), first):
         assert torch.equal(a, b), n
     ok()
+
+
+def test_tensors_of_another_device_are_refused(monkeypatch):
+    """Refused by the binding, ahead of any launch (the tensors are on device 0)."""
+    x, w = torch.ones(4, 128, dtype=torch.bfloat16, device="cuda"), torch.ones(128, device="cuda")
+    y = torch.empty_like(x)
+    q, sf = (torch.empty(4, c, dtype=torch.uint8, device="cuda") for c in (64, 16))
+    monkeypatch.setattr(_lib, "_get_device", lambda: 1)
+    with pytest.raises(ValueError, match="current device"):
+        _lib.moe_rmsnorm(dict(T=4, d=128, eps=1e-6, x=x, weight=w, y=y))
+    with pytest.raises(ValueError, match="current device"):
+        _lib.moe_mx4_quantize(x, 4, 128, q, sf)
