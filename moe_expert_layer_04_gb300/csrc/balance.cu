@@ -40,6 +40,7 @@ struct BalanceParams {
     float *part_p;     // [slots, E]
     int32_t *part_c;   // [slots, E]
     int32_t *part_n;   // [slots]
+    unsigned *done;    // sequences that are finished
     int *status;
 };
 
@@ -163,6 +164,7 @@ __global__ void __launch_bounds__(32 * (ONE ? kOneWarps : kWarps), !ONE && N * V
     let_kernels_behind_begin();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     int32_t *hist = reinterpret_cast<int32_t *>(sm + kWarps * p.E);
+    if (!ONE && blockIdx.x == 0 && threadIdx.x == 0) *p.done = 0;
     if (blockIdx.x == 0 && p.seq_offsets) {
         for (int q = threadIdx.x; q <= p.n_seq; q += blockDim.x) {
             const int o = p.seq_offsets[q];
@@ -330,27 +332,28 @@ __global__ void __launch_bounds__(32 * kSeqWarps) balance_seq_kernel(const Balan
         dsmem_st_u32(dsmem_map(&terms[blockIdx.x], 0), __float_as_uint(t));
     }
     cluster_sync_all();
-    if (blockIdx.x == 0 && threadIdx.x == 0) {
+    if (blockIdx.x != 0 || warp != 0) return;
+    bool last = false;
+    if (lane == 0) {
         float t = 0.0f;
         for (int i = 0; i < (int)gridDim.x; ++i) t += terms[i];
         p.seq_loss[q] = t;
         p.tokens[q] = n;
-        if (p.n_seq == 1) p.loss[0] = p.alpha * t;
+        __threadfence();
+        last = atomicAdd(p.done, 1u) == (unsigned)p.n_seq - 1;
     }
-}
-
-// The mean of the sequences' losses; one warp, each lane's sum compensated (it can be long).
-__global__ void balance_loss_kernel(const BalanceParams p) {
-    wait_for_kernels_ahead();
-    let_kernels_behind_begin();
-    float s = 0.0f, c = 0.0f;
-    for (int q = threadIdx.x; q < p.n_seq; q += 32) {
-        const float v = p.seq_loss[q] - c, u = s + v;
-        c = (u - s) - v;
-        s = u;
+    if (!__any_sync(0xffffffffu, last)) return;
+    // the sequence that is finished last takes the mean of all, in their order: each lane's sum
+    // compensated, as it can be long
+    __threadfence();
+    float sum_q = 0.0f, c = 0.0f;
+    for (int i = lane; i < p.n_seq; i += 32) {
+        const float v = __ldcg(p.seq_loss + i) - c, u = sum_q + v;
+        c = (u - sum_q) - v;
+        sum_q = u;
     }
-    s = warp_sum(s);
-    if (threadIdx.x == 0) p.loss[0] = p.alpha * s / (float)p.n_seq;
+    sum_q = warp_sum(sum_q);
+    if (lane == 0) p.loss[0] = p.alpha * sum_q / (float)p.n_seq;
 }
 
 // A warp takes `chunk` consecutive tokens; a sequence's load stays in its registers.
@@ -494,7 +497,7 @@ struct BwdLaunch {
 size_t balance_workspace_bytes(int T, int E, int n_seq) {
     const int C = part_chunk(T);
     const size_t slots = (size_t)((T + C - 1) / C) + n_seq;
-    return slots * E * 8 + slots * 4;
+    return slots * E * 8 + slots * 4 + 4;
 }
 
 moe_status launch_balance(const moe_balance_args *a, cudaStream_t st) {
@@ -513,10 +516,10 @@ moe_status launch_balance(const moe_balance_args *a, cudaStream_t st) {
     p.part_p = static_cast<float *>(a->ws);
     p.part_c = reinterpret_cast<int32_t *>(p.part_p + slots * a->E);
     p.part_n = p.part_c + slots * a->E;
-    if (p.n_chunks > 0) {
-        const moe_status s = by_columns<PartLaunch>(a, p, st);
-        if (s != MOE_OK) return s;
-    }
+    p.done = reinterpret_cast<unsigned *>(p.part_n + slots);
+    if (p.n_chunks == 0) p.n_chunks = 1;   // (no token: it sets `done`)
+    const moe_status s = by_columns<PartLaunch>(a, p, st);
+    if (s != MOE_OK) return s;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute at[2];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -530,8 +533,7 @@ moe_status launch_balance(const moe_balance_args *a, cudaStream_t st) {
     cfg.attrs = at;
     cfg.numAttrs = 2;
     if (cudaLaunchKernelEx(&cfg, balance_seq_kernel, p) != cudaSuccess) return MOE_ERR_CUDA;
-    if (a->n_seq == 1) return cuda_status(cudaGetLastError());
-    return launch_early(balance_loss_kernel, dim3(1), 32, 0, st, p);
+    return cuda_status(cudaGetLastError());
 }
 
 moe_status launch_balance_bwd(const moe_balance_args *a, cudaStream_t st) {
