@@ -106,9 +106,10 @@ struct Row {
     }
 };
 
-// z -> p (columns outside E: zeros); slope = 1 - s for the sigmoid, 1 otherwise.
+// z -> s (columns outside E: zeros), p is s times what it returns; slope = 1 - s for the
+// sigmoid, 1 otherwise.
 template <bool SOFTMAX, int VEC, int N>
-__device__ __forceinline__ void shares(const Row<VEC, N> &r, float (&p)[N][VEC],
+__device__ __forceinline__ float shares(const Row<VEC, N> &r, float (&p)[N][VEC],
                                        float (&slope)[N][VEC]) {
     float sum = 0.0f;
     if constexpr (SOFTMAX) {
@@ -142,11 +143,7 @@ __device__ __forceinline__ void shares(const Row<VEC, N> &r, float (&p)[N][VEC],
             }
     }
     sum = warp_sum(sum);
-    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-#pragma unroll
-    for (int i = 0; i < N; ++i)
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) p[i][j] *= inv;
+    return sum == 0.0f ? 0.0f : 1.0f / sum;
 }
 
 // CTA: one chunk of tokens, sequence by sequence; its warps take tokens in turn (UNROLL
@@ -208,11 +205,11 @@ __global__ void __launch_bounds__(32 * (ONE ? kOneWarps : kWarps), !ONE && N * V
                 for (int u = 0; u < UNROLL; ++u) {
                     if (!live[u]) continue;
                     float s[N][VEC], slope[N][VEC];
-                    shares<SOFTMAX>(r[u], s, slope);
+                    const float inv = shares<SOFTMAX>(r[u], s, slope);
 #pragma unroll
                     for (int i = 0; i < N; ++i)
 #pragma unroll
-                        for (int j = 0; j < VEC; ++j) acc[i][j] += s[i][j];
+                        for (int j = 0; j < VEC; ++j) acc[i][j] = fmaf(s[i][j], inv, acc[i][j]);
                     if (lane < p.k) {
                         if ((unsigned)id[u] < (unsigned)p.E) atomicAdd(hist + id[u], 1);
                         else record_status(p.status, MOE_ERR_INVALID_ARG);
@@ -397,7 +394,11 @@ __global__ void __launch_bounds__(32 * kWarps) balance_bwd_kernel(const BalanceP
             Row<VEC, N> r;
             r.load(p.logits + (size_t)t * p.E, p.E);
             float s[N][VEC], slope[N][VEC];
-            shares<SOFTMAX>(r, s, slope);
+            const float inv = shares<SOFTMAX>(r, s, slope);
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+#pragma unroll
+                for (int j = 0; j < VEC; ++j) s[i][j] *= inv;
             float dot = 0.0f;
 #pragma unroll
             for (int i = 0; i < N; ++i)
