@@ -4,9 +4,9 @@
 // Both products run on the tensor cores, as one group of the layer's data-gradient and
 // weight-gradient matmuls.  dz is their bf16 operand (2^-9 of itself; sums over the tokens
 // average that out), padded with zeros to whole tiles of 128 experts; dz W_g is rounded to
-// bf16 before it is added.  Against the layer's backward (65 ms at 65536 tokens, d = 4096,
-// E = 384) the 0.4 TFLOP and 2.6 GB here are under one per cent, so the sums are a pass of
-// their own.
+// bf16 before it is added.  Measured: 0.87 ms at 65536 tokens, d = 4096, E = 384 (127 us at
+// 8192), 1.3 % of the layer's backward there; so the sums stay a pass of their own, which
+// leaves that backward as it is.
 #include "fp8_common.cuh"
 
 namespace moe {

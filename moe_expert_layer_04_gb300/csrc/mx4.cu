@@ -5,7 +5,10 @@
 // A lane owns eight consecutive elements, 16 bytes of bf16 and a word of codes, four
 // lanes a block: every load and store of a warp is contiguous, and a block's largest
 // magnitude is two shuffles away.  All loads of a lane are issued before the first use.
-// Bound by HBM: 2 bytes read, 1/2 + 1/32 written an element, and the reverse.
+// Bound by HBM: 2 bytes read, 1/2 + 1/32 written an element, and the reverse.  Measured at
+// 36864 rows of 4096: quantised in 55.6 us, the values in 56.1, 101 and 100 % of the copy
+// bandwidth (70 and 61 with a grid-stride loop and a scale's byte stored by each fourth lane);
+// one row of 4096 1.6 us.
 #include "fp8_common.cuh"
 #include "mx_common.cuh"
 
