@@ -229,3 +229,62 @@ def test_same_bits_every_time():
     ok()
     for n in ("loss", "seq_loss", "load", "counts", "dlogits"):
         assert torch.equal(a[n], b[n]), n
+
+
+@pytest.mark.parametrize("score", [SIG, SOFT])
+def test_most_sequences(score):
+    """As many sequences as a call takes, of a token or none, some of two."""
+    T, E, k, n = 70000, 8, 2, 65535
+    rng = np.random.default_rng(9)
+    z, ids = inputs(rng, T, E, k)
+    offs = np.sort(np.concatenate([[0, T], rng.integers(0, T + 1, n - 1)])).astype(np.int32)
+    a = call(z, ids, score, offs)
+    ok()
+    check(a, reference(z.astype(np.float64), ids, score, offs), z)
+
+
+def test_places_behind_32_bits():
+    """More than 2^31 logits, of which the last 70 tokens count; the gradient in their place."""
+    T, E, k, m = (1 << 21) + 70, 1024, 2, 70
+    z, ids = inputs(np.random.default_rng(4), m, E, k)
+    logits = torch.ones(T, E, device="cuda")
+    logits[-m:] = dev(z)
+    all_ids, valid = torch.zeros(T, k, dtype=torch.int32, device="cuda"), torch.zeros(
+        T, dtype=torch.uint8, device="cuda")
+    all_ids[-m:], valid[-m:] = dev(ids), 1
+    f = lambda *s, t=torch.float32: torch.empty(s, dtype=t, device="cuda")
+    a = dict(T=T, E=E, k=k, n_seq=1, score=SIG, alpha=ALPHA, logits=logits, ids=all_ids, valid=valid,
+             counts=f(1, E, t=torch.int32), tokens=f(1, t=torch.int32), load=f(1, E), seq_loss=f(1),
+             loss=f(1), dlogits=logits,
+             ws=f(_lib.moe_balance_workspace_size(T, E), t=torch.uint8))
+    _lib.moe_balance_loss(a)
+    _lib.moe_balance_loss_backward(a)
+    ok()
+    for part in (logits[:5000], logits[T // 2:T // 2 + 5000], logits[-m - 5000:-m]):
+        assert not part.any()
+    check(dict(a, dlogits=logits[-m:]), reference(z.astype(np.float64), ids, SIG), z)
+
+
+def test_one_workspace_in_a_graph():
+    """Captured and replayed on a workspace that calls of other sizes have used."""
+    rng = np.random.default_rng(6)
+    z, ids = inputs(rng, 3000, 40, 4)
+    offs = np.array([0, 10, 1700, 1700, 2990], np.int32)
+    a = call(z, ids, SIG, offs, backward=False)
+    r = reference(z.astype(np.float64), ids, SIG, offs)
+    torch.cuda.synchronize()
+    st = torch.cuda.Stream()
+    with torch.cuda.stream(st):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=st):
+            for _ in range(2):
+                _lib.moe_balance_loss(a)
+                _lib.moe_balance_loss_backward(a)
+        for fill in (0, 255, 77):
+            a["ws"].fill_(fill)
+            a["loss"].fill_(-1.0)
+            a["dlogits"].fill_(-1.0)
+            g.replay()
+            st.synchronize()
+            check(a, r, z)
+    ok()

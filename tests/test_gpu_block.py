@@ -339,3 +339,20 @@ def test_tensors_of_another_device_are_refused(monkeypatch):
         _lib.moe_rmsnorm(dict(T=4, d=128, eps=1e-6, x=x, weight=w, y=y))
     with pytest.raises(ValueError, match="current device"):
         _lib.moe_mx4_quantize(x, 4, 128, q, sf)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "mx4", "fp8"])
+def test_balance_without_a_backward(kind):
+    T, d, E, k, I = 70, 256, 32, 4, 128
+    kw = {} if kind == "bf16" else {kind: True}
+    layer, w, bias, x, res = block(T, d, E, k, I, balance=0.5, **kw)
+    layer.forward(x, bias, residual=res)
+    ok()
+    s = 1 / (1 + np.exp(-f64(layer.logits)[:T]))
+    counts = np.bincount(layer.ids.cpu().numpy().ravel(), minlength=E)
+    assert np.array_equal(layer.balance_counts.cpu().numpy()[0], counts)
+    want = 0.5 * (E * counts / (k * T)) @ (s / s.sum(1, keepdims=True)).mean(0)
+    # 2^-16: what an exponential of these logits, a sum of 32 and a mean of 70 can be off by, and more
+    assert abs(f64(layer.balance_loss)[0] - want) <= 2.0 ** -16 * want
+    with pytest.raises(RuntimeError):
+        layer.backward(x)

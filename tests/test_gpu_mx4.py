@@ -148,7 +148,9 @@ SHAPES = [([1], 8, 32), ([1], 512, 4096), ([3], 136, 416), ([128], 256, 128), ([
           # enough rows for pairs of row tiles: one tile each, many each, a group's last pair
           # with one row tile, one row, or a row of its second tile
           ([2048], 2048, 640), ([700, 1, 0, 900, 300], 4104, 288), ([4000, 129, 257, 127], 2304, 1120),
-          ([1, 3333], 8200, 64)]
+          ([1, 3333], 8200, 64),
+          # as many groups as there can be, and more than wide tiles' tables hold
+          ([1] * 1024 + [3], 16, 64), ([40] * 400 + [0, 2] * 200, 264, 64)]
 MATMULS = [(c, N, K, 4) for c, N, K in SHAPES]
 MATMULS += [(c, N, (K + 127) // 128 * 128, 8) for c, N, K in SHAPES]
 
