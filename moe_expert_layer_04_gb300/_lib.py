@@ -864,44 +864,36 @@ def moe_layer_few(args: dict, stream=None):
 
 # ------------------------------------------------------------------- MXFP4
 
-def moe_mx4_quantize(src, rows, K, q, sf, stream=None):
-    st = load().moe_mx4_quantize(_here(src, BF16, "src"), int(rows), int(K), _here(q, U8, "q"),
-                                 _here(sf, U8, "sf"), _stream(stream))
-    _check("moe_mx4_quantize", st)
+_KINDS = dict(bf16=BF16, f32=F32, i32=I32, u8=U8)
+_CHECKED = ("{0}.data_ptr() if {0}.__class__ is Tensor and {0}.dtype is {1} and "
+            "{0}.get_device() == dev and {0}.is_contiguous() else here({0}, {1}, {0!r})")
 
 
-def moe_mx4_dequantize(q, sf, rows, K, out, stream=None):
-    st = load().moe_mx4_dequantize(_here(q, U8, "q"), _here(sf, U8, "sf"), int(rows), int(K),
-                                   _here(out, BF16, "out"), _stream(stream))
-    _check("moe_mx4_dequantize", st)
+def _call(name, params):
+    """The call `name` of the library with its arguments in order ("x:bf16" a tensor of that
+    type on the current device, or None; "x:int" a number that is converted; "x" one that is
+    not), then stream=None.  The checks are written out: a call for each tensor costs the host
+    a microsecond of the seven that a matmul of one row takes."""
+    names, args = [], []
+    for param in params.split():
+        n, _, kind = param.partition(":")
+        names.append(n)
+        args.append(_CHECKED.format(n, kind) if kind in _KINDS else f"{kind}({n})" if kind else n)
+    env = dict(_KINDS, load=load, here=_here, device=_device, Tensor=_Tensor, stream_of=_stream,
+               check=_check)
+    exec(f"def {name}({', '.join(names)}, stream=None):\n    dev = device()\n"
+         f"    check({name!r}, load().{name}({', '.join(args)}, stream_of(stream)))", env)
+    return env[name]
 
 
-def moe_mx4_gather(x, slot_row, T, d, k, x_perm_q, x_perm_sf, stream=None):
-    st = load().moe_mx4_gather(_here(x, BF16, "x"), _here(slot_row, I32, "slot_row"), T, d, k,
-                               _here(x_perm_q, U8, "x_perm_q"), _here(x_perm_sf, U8, "x_perm_sf"),
-                               _stream(stream))
-    _check("moe_mx4_gather", st)
-
-
-def moe_mx4_matmul(a_q, a_sf, a_bits, offsets, G, max_rows, b_q, b_sf, row_weight, w_rows, N, K,
-                   out, stream=None):
-    st = load().moe_mx4_matmul(_here(a_q, U8, "a_q"), _here(a_sf, U8, "a_sf"), a_bits,
-                               _here(offsets, I32, "offsets"), G, max_rows, _here(b_q, U8, "b_q"),
-                               _here(b_sf, U8, "b_sf"), _here(row_weight, F32, "row_weight"),
-                               w_rows, N, K, _here(out, BF16, "out"), _stream(stream))
-    _check("moe_mx4_matmul", st)
-
-
-def moe_expert_ffn_mx4(x_perm_q, x_perm_sf, offsets, G, max_rows, W13_q, W13_sf, W2_q, W2_sf,
-                       row_weight, S, d, I, clamp, h_q, h_sf, y_perm, stream=None):
-    st = load().moe_expert_ffn_mx4(_here(x_perm_q, U8, "x_perm_q"), _here(x_perm_sf, U8, "x_perm_sf"),
-                                   _here(offsets, I32, "offsets"), G, max_rows,
-                                   _here(W13_q, U8, "W13_q"), _here(W13_sf, U8, "W13_sf"),
-                                   _here(W2_q, U8, "W2_q"), _here(W2_sf, U8, "W2_sf"),
-                                   _here(row_weight, F32, "row_weight"), S, d, I, float(clamp),
-                                   _here(h_q, U8, "h_q"), _here(h_sf, U8, "h_sf"),
-                                   _here(y_perm, BF16, "y_perm"), _stream(stream))
-    _check("moe_expert_ffn_mx4", st)
+moe_mx4_quantize = _call("moe_mx4_quantize", "src:bf16 rows:int K:int q:u8 sf:u8")
+moe_mx4_dequantize = _call("moe_mx4_dequantize", "q:u8 sf:u8 rows:int K:int out:bf16")
+moe_mx4_gather = _call("moe_mx4_gather", "x:bf16 slot_row:i32 T d k x_perm_q:u8 x_perm_sf:u8")
+moe_mx4_matmul = _call("moe_mx4_matmul", "a_q:u8 a_sf:u8 a_bits offsets:i32 G max_rows b_q:u8 b_sf:u8 "
+                                         "row_weight:f32 w_rows N K out:bf16")
+moe_expert_ffn_mx4 = _call("moe_expert_ffn_mx4", "x_perm_q:u8 x_perm_sf:u8 offsets:i32 G max_rows "
+                           "W13_q:u8 W13_sf:u8 W2_q:u8 W2_sf:u8 row_weight:f32 S d I clamp:float "
+                           "h_q:u8 h_sf:u8 y_perm:bf16")
 
 
 # ------------------------------------- calls that take their fields as a dict
@@ -922,10 +914,8 @@ def _packer(mirror, **types):
         elif name in types:
             env[f"t{i}"] = types[name]
             names.append(f"v{i}")
-            lines += [f"    v{i} = get({name!r})",
-                      f"    v{i} = (0 if v{i} is None else v{i}.data_ptr() if v{i}.__class__ is Tensor "
-                      f"and v{i}.dtype is t{i} and v{i}.get_device() == dev and v{i}.is_contiguous() "
-                      f"else here(v{i}, t{i}, {name!r}))"]
+            checked = _CHECKED.format(f"v{i}", f"t{i}").replace(f"'v{i}'", repr(name))
+            lines += [f"    v{i} = get({name!r})", f"    v{i} = 0 if v{i} is None else {checked}"]
         elif name == "ws_bytes":
             names.append("0 if get('ws') is None else get('ws').numel()")
         else:
