@@ -471,24 +471,29 @@ __global__ void __launch_bounds__(kRingThreads, kBwdCtas) rmsnorm_bwd_ring_kerne
     }
 }
 
-// Long rows.  The rows slot, slot + slots, ... of one slot; the next row's loads are issued
-// before this row's sum.
-template <int V>
+// Long rows: a cluster of CL CTAs takes each gridDim.x / CL-th row, a CTA up to 1024 vectors of
+// it, two a thread.  The next row's loads are issued before this row's sum, which goes
+// through the CTAs' shared memory.  Measured, of the copy bandwidth: 4096 x 7168 43 us, 80 %, 2048 x
+// 16384 62 us, 64 %, 1024 x 32768 68 us, 58 % (115 and 476 us with a CTA a row, whose four or
+// eight vectors a thread spill).
+template <int CL>
 __global__ void __launch_bounds__(512) rmsnorm_bwd_kernel(const NormBwd p) {
-    __shared__ float part[2][32];
+    constexpr int V = 2;
+    __shared__ float part[2][16];
+    __shared__ float sums[2][CL];   // of the cluster's CTAs
+    if constexpr (CL > 1) cluster_sync_all();   // they have begun
     wait_for_kernels_ahead();
     let_kernels_behind_begin();
-    const int in_row = threadIdx.x % p.threads;
-    const int per = blockDim.x / p.threads;
-    const long long slots = (long long)gridDim.x * per;
-    const long long slot = (long long)blockIdx.x * per + threadIdx.x / p.threads;
+    const int slots = gridDim.x / CL, slot = blockIdx.x / CL;
+    const int rank = CL > 1 ? (int)cluster_ctarank() : 0, slice = (p.d8 + CL - 1) / CL;
+    const int c0 = rank * slice, c1 = min(p.d8, c0 + slice);
     float w[V][8], dw[V][8];
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-        const int c = in_row + j * p.threads;
+        const int c = c0 + threadIdx.x + j * blockDim.x;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            w[j][i] = c < p.d8 ? __ldg(p.weight + 8 * c + i) : 0.0f;
+            w[j][i] = c < c1 ? __ldg(p.weight + 8 * c + i) : 0.0f;
             dw[j][i] = 0.0f;
         }
     }
@@ -500,19 +505,16 @@ __global__ void __launch_bounds__(512) rmsnorm_bwd_kernel(const NormBwd p) {
         nrstd = has ? __ldg(p.rstd + row) : 0.0f;
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-            const int c = in_row + j * p.threads;
-            const bool live = has && c < p.d8;
+            const int c = c0 + threadIdx.x + j * blockDim.x;
+            const bool live = has && c < c1;
             nv[j] = live ? __ldg(p.x + row * p.d8 + c) : zero;
             nd[j] = live ? __ldg(p.dy + row * p.d8 + c) : zero;
             nr[j] = live && p.d_residual ? __ldg(p.d_residual + row * p.d8 + c) : zero;
         }
     };
     load(slot);
-    // all rows of a CTA take the same number of steps (its sums are barriers)
-    const long long first = (long long)blockIdx.x * per;
     int turn = 0;
-    for (long long base = first; base < p.T; base += slots, turn ^= 1) {
-        const long long row = base + threadIdx.x / p.threads;
+    for (long long row = slot; row < p.T; row += slots, turn ^= 1) {
         const float r = nrstd;
         uint4 v[V], dr[V];
         float a[V][8];
@@ -533,26 +535,33 @@ __global__ void __launch_bounds__(512) rmsnorm_bwd_kernel(const NormBwd p) {
             }
         }
         load(row + slots);
-        const float m = row_sum(dot, p.threads >> 5, part[turn]) * p.inv_d;
-        if (row < p.T) {
+        float m = row_sum(dot, blockDim.x >> 5, part[turn]);
+        if constexpr (CL > 1) {
+            if (threadIdx.x < CL)
+                dsmem_st_u32(dsmem_map(&sums[turn][rank], threadIdx.x), __float_as_uint(m));
+            cluster_sync_all();
+            m = 0.0f;
 #pragma unroll
-            for (int j = 0; j < V; ++j) {
-                const int c = in_row + j * p.threads;
-                if (c >= p.d8) continue;
-                float f[8], g[8];
-                unpack8(v[j], f);
-                unpack8(dr[j], g);
+            for (int i = 0; i < CL; ++i) m += sums[turn][i];
+        }
+        m *= p.inv_d;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) g[i] += r * (a[j][i] - f[i] * r * m);
-                p.dx[row * p.d8 + c] = pack8(g);
-            }
+        for (int j = 0; j < V; ++j) {
+            const int c = c0 + threadIdx.x + j * blockDim.x;
+            if (c >= c1) continue;
+            float f[8], g[8];
+            unpack8(v[j], f);
+            unpack8(dr[j], g);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) g[i] += r * (a[j][i] - f[i] * r * m);
+            p.dx[row * p.d8 + c] = pack8(g);
         }
     }
-    float4 *dst = reinterpret_cast<float4 *>(p.part + slot * p.d8 * 8);
+    float4 *dst = reinterpret_cast<float4 *>(p.part + (size_t)slot * p.d8 * 8);
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-        const int c = in_row + j * p.threads;
-        if (c >= p.d8) continue;
+        const int c = c0 + threadIdx.x + j * blockDim.x;
+        if (c >= c1) continue;
         dst[2 * c] = make_float4(dw[j][0], dw[j][1], dw[j][2], dw[j][3]);
         dst[2 * c + 1] = make_float4(dw[j][4], dw[j][5], dw[j][6], dw[j][7]);
     }
@@ -605,13 +614,52 @@ RowShape ring_shape(int d8) {
     return s;
 }
 
-RowShape bwd_shape(int d8) { return d8 <= kRingVecs ? ring_shape(d8) : row_shape(d8, 512); }
+// CTAs that share a row of the backward.
+int wide_cluster(int d8) { return d8 <= 1024 ? 1 : d8 <= 2048 ? 2 : 4; }
 
-// Rows in flight of the backward: CTAs for the SMs, no more than there are rows.
-int bwd_ctas(int T, int d8, const RowShape &s) {
-    const long long want = ((long long)T + s.rows - 1) / s.rows;
-    const long long most = (long long)num_sms() * (d8 <= kRingVecs ? kBwdCtas : 1);
+// Rows of partial sums of the backward, one for each CTA or cluster: as many as the SMs take at
+// once, no more than there are groups of rows.
+int bwd_parts(int T, int d8) {
+    const bool ring = d8 <= kRingVecs;
+    const int rows = ring ? ring_shape(d8).rows : 1;
+    const long long want = ((long long)T + rows - 1) / rows;
+    const long long most = ring ? (long long)num_sms() * kBwdCtas : num_sms() / wide_cluster(d8);
     return (int)(want < most ? want : most);
+}
+
+// The clusters that the GPU holds at once, where they are fewer than `parts`, become it.
+template <int CL>
+moe_status launch_wide(int &parts, const NormBwd &p, cudaStream_t st) {
+    static int resident[64] = {};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return MOE_ERR_CUDA;
+    if (dev < 0 || dev >= 64) return MOE_ERR_UNSUPPORTED;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = CL;
+    at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+    cfg.gridDim = dim3(num_sms() / CL * CL);
+    cfg.blockDim = dim3(512);
+    cfg.stream = st;
+    cfg.attrs = at;
+    cfg.numAttrs = 2;
+    if (!resident[dev]) {
+        int n = num_sms();
+        if (CL > 1 && (cudaOccupancyMaxActiveClusters(&n, rmsnorm_bwd_kernel<CL>, &cfg) !=
+                           cudaSuccess ||
+                       n < 1))
+            return MOE_ERR_CUDA;
+        resident[dev] = n;
+    }
+    if (parts > resident[dev]) parts = resident[dev];
+    const int slice = (p.d8 + CL - 1) / CL;
+    cfg.gridDim = dim3(parts * CL);
+    cfg.blockDim = dim3((slice + 63) / 64 * 32);
+    if (cudaLaunchKernelEx(&cfg, rmsnorm_bwd_kernel<CL>, p) != cudaSuccess) return MOE_ERR_CUDA;
+    return cuda_status(cudaGetLastError());
 }
 
 template <auto KERN, typename P>
@@ -681,17 +729,14 @@ moe_status launch_rmsnorm(const moe_norm_args *a, cudaStream_t st) {
 }
 
 size_t rmsnorm_bwd_workspace_bytes(int T, int d) {
-    const RowShape s = bwd_shape(d / 8);
-    return (size_t)bwd_ctas(T, d / 8, s) * d * sizeof(float);
+    return (size_t)bwd_parts(T, d / 8) * d * sizeof(float);
 }
 
 moe_status launch_rmsnorm_bwd(const moe_norm_bwd_args *a, cudaStream_t st) {
-    const RowShape s = bwd_shape(a->d / 8);
     NormBwd p;
     std::memset(&p, 0, sizeof p);
     p.T = a->T;
     p.d8 = a->d / 8;
-    p.threads = s.threads;
     p.inv_d = 1.0f / (float)a->d;
     p.x = reinterpret_cast<const uint4 *>(a->x);
     p.dy = reinterpret_cast<const uint4 *>(a->dy);
@@ -702,24 +747,22 @@ moe_status launch_rmsnorm_bwd(const moe_norm_bwd_args *a, cudaStream_t st) {
     p.part = static_cast<float *>(a->ws);
     p.status = device_status_ptr();
     if (!p.status) return MOE_ERR_CUDA;
-    const int ctas = bwd_ctas(a->T, p.d8, s), threads = s.threads * s.rows;
+    int parts = bwd_parts(a->T, p.d8);
     moe_status r = MOE_OK;
-    if (ctas > 0) {
-        if (p.d8 <= kRingVecs) {
-            const int arrays = a->d_residual ? 3 : 2;
-            r = launch_ring<rmsnorm_bwd_ring_kernel<2>>(ctas, s, arrays, a->d, st, p);
-        } else if (s.V == 2)
-            r = launch_early(rmsnorm_bwd_kernel<2>, dim3(ctas), threads, 0, st, p);
-        else if (s.V == 4)
-            r = launch_early(rmsnorm_bwd_kernel<4>, dim3(ctas), threads, 0, st, p);
-        else
-            r = launch_early(rmsnorm_bwd_kernel<8>, dim3(ctas), threads, 0, st, p);
+    if (parts > 0 && p.d8 <= kRingVecs) {
+        const RowShape s = ring_shape(p.d8);
+        p.threads = s.threads;
+        r = launch_ring<rmsnorm_bwd_ring_kernel<2>>(parts, s, a->d_residual ? 3 : 2, a->d, st, p);
+    } else if (parts > 0) {
+        const int cl = wide_cluster(p.d8);
+        r = cl == 1 ? launch_wide<1>(parts, p, st)
+                    : cl == 2 ? launch_wide<2>(parts, p, st) : launch_wide<4>(parts, p, st);
     }
     if (r != MOE_OK) return r;
     // without rows: zeros
     const int d4 = a->d / 4;
     return launch_early(rmsnorm_dw_kernel, dim3((d4 + 31) / 32), 32 * kDwWarps, 0, st,
-                        reinterpret_cast<const float4 *>(a->ws), ctas, d4,
+                        reinterpret_cast<const float4 *>(a->ws), parts, d4,
                         reinterpret_cast<float4 *>(a->d_weight));
 }
 

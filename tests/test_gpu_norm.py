@@ -168,7 +168,8 @@ def backward(x, w, rstd, dy, dres, in_place=False, ws_fill=None):
     return a
 
 
-@pytest.mark.parametrize("T,d", SHAPES + [(2000, 512), (1500, 32)])
+@pytest.mark.parametrize("T,d", SHAPES + [(2000, 512), (1500, 32), (200, 16392), (170, 20480),
+                                          (90, 32768), (333, 9000)])
 @pytest.mark.parametrize("res", [False, True])
 def test_backward(T, d, res):
     """dx: the sum of a vh over d rounds like the forward's (at most 50 2^-24 of the sum of
