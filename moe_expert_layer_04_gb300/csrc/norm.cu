@@ -686,7 +686,15 @@ moe_status launch_rmsnorm(const moe_norm_args *a, cudaStream_t st) {
     // 102 us against 106), with few of them one (300 rows 2.9 us against 3.1; other
     // widths: 2000 rows of 2304 7.9 us against 8.5).
     const bool wide = d8 >= kFwdVecs && d8 <= kRingVecs;
-    const RowShape s = row_shape(d8, wide && a->T > 2 * num_sms() ? kRingThreads : 1024);
+    // Longer rows likewise, four vectors a thread where that leaves 192 threads or more (2048
+    // rows of 8192 28.1 us, two 30.3, one 32.0; of 16384 53.0 and, two, 68.0; 4096 rows of 7168
+    // 47.1, 52.7 and 52.6, but of 5120 33.8, 32.2 and 33.6).
+    const bool many = a->T > 2 * num_sms();
+    const int most = !many ? 1024
+                     : wide || (d8 > 3 * kRingThreads && d8 <= 4 * kRingThreads) ? kRingThreads
+                     : d8 > kRingVecs && d8 <= 4 * 512 ? 512
+                                                       : 1024;
+    const RowShape s = row_shape(d8, most);
     NormRows p;
     std::memset(&p, 0, sizeof p);
     p.T = a->T;

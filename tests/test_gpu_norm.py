@@ -62,7 +62,7 @@ SHAPES = [(1, 8), (1, 4096), (3, 40), (7, 1184), (130, 256), (65, 2056), (5, 820
           (3, 32768), (4099, 128), (300, 7168),
           # more rows than the SMs hold at once
           (1000, 4096), (700, 1184), (311, 256), (5000, 8), (1231, 2056), (613, 4088),
-          (913, 3592), (1300, 3584)]
+          (913, 3592), (1300, 3584), (310, 7168), (320, 5128), (330, 16384)]
 
 
 @pytest.mark.parametrize("T,d", SHAPES)
@@ -114,7 +114,7 @@ def check_codes(a, u, fmt):
 
 @pytest.mark.parametrize("T,d", [(1, 32), (1, 4096), (5, 1184), (130, 288), (33, 8224), (3, 32768),
                                  (4099, 128), (700, 4096), (1000, 96), (901, 2080),
-                                 (1000, 4096), (1300, 3616)])
+                                 (1000, 4096), (1300, 3616), (310, 8192), (306, 10016)])
 @pytest.mark.parametrize("fmt", [_lib.MOE_ROWS_FP8, _lib.MOE_ROWS_MXFP8, _lib.MOE_ROWS_MXFP4])
 def test_forward_codes(T, d, fmt):
     rng = np.random.default_rng(T * 5 + d + fmt)
