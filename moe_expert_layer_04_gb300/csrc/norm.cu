@@ -64,6 +64,31 @@ struct NormRows {
     int scale_pitch;      // scales of a row
 };
 
+// The largest of |u| as bits, over the `lanes` lanes of a block.  NAN_COUNTS: a NaN is larger than
+// every number (0x7FFFFFFF), else it is left out.  (Three inputs an instruction: as integer
+// maxima of masked bits these were a seventh of the norm's instructions.)
+template <bool NAN_COUNTS>
+__device__ __forceinline__ uint32_t block_max(const float (&u)[8], int lanes) {
+    float m = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; i += 2) {
+        if constexpr (NAN_COUNTS)
+            asm("max.NaN.abs.f32 %0, %0, %1, %2;" : "+f"(m) : "f"(u[i]), "f"(u[i + 1]));
+        else
+            asm("max.abs.f32 %0, %0, %1, %2;" : "+f"(m) : "f"(u[i]), "f"(u[i + 1]));
+    }
+    uint32_t b = __float_as_uint(m);
+#pragma unroll
+    for (int o = 1; o < lanes; o <<= 1) b = max(b, __shfl_xor_sync(0xffffffffu, b, o));
+    return b;
+}
+
+// u times r in E4M3.
+__device__ __forceinline__ uint2 e4m3_of(const float (&u)[8], float r) {
+    return make_uint2(e4m3x4(u[0] * r, u[1] * r, u[2] * r, u[3] * r),
+                      e4m3x4(u[4] * r, u[5] * r, u[6] * r, u[7] * r));
+}
+
 // Codes and scales of the eight values u, elements 8 c .. of row `row`; called by
 // whole warps, whose lanes hold consecutive vectors (a block of 128 is sixteen lanes,
 // one of 32 four).
@@ -71,41 +96,19 @@ template <int FORMAT>
 __device__ __forceinline__ void store_codes(const NormRows &p, size_t row, int c, bool live,
                                             const float (&u)[8]) {
     if constexpr (FORMAT == MOE_ROWS_FP8) {
-        uint32_t m = 0;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(u[i]) & 0x7FFFFFFFu);
-#pragma unroll
-        for (int o = 1; o < 16; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-        const Fp8Scale f = fp8_scale(m);
+        const Fp8Scale f = fp8_scale(block_max<true>(u, 16));
         if (!live) return;
-        uint2 w;
-        w.x = e4m3x4(u[0] * f.r, u[1] * f.r, u[2] * f.r, u[3] * f.r);
-        w.y = e4m3x4(u[4] * f.r, u[5] * f.r, u[6] * f.r, u[7] * f.r);
-        *reinterpret_cast<uint2 *>(p.q + (row * p.d8 + c) * 8) = w;
+        *reinterpret_cast<uint2 *>(p.q + (row * p.d8 + c) * 8) = e4m3_of(u, f.r);
         if ((c & 15) == 0)
             static_cast<float *>(p.scales)[row * p.scale_pitch + (c >> 4)] = f.s;
     } else if constexpr (FORMAT == MOE_ROWS_MXFP8) {
-        float m = 0.0f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(u[i]));
-#pragma unroll
-        for (int o = 1; o < 4; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-        const uint32_t code = mx_scale_code(m);
-        const float r = mx_inv_scale(code);
+        const uint32_t code = mx_scale_code(__uint_as_float(block_max<false>(u, 4)));
         if (!live) return;
-        uint2 w;
-        w.x = e4m3x4(u[0] * r, u[1] * r, u[2] * r, u[3] * r);
-        w.y = e4m3x4(u[4] * r, u[5] * r, u[6] * r, u[7] * r);
-        *reinterpret_cast<uint2 *>(p.q + (row * p.d8 + c) * 8) = w;
+        *reinterpret_cast<uint2 *>(p.q + (row * p.d8 + c) * 8) = e4m3_of(u, mx_inv_scale(code));
         if ((c & 3) == 0)
             static_cast<uint8_t *>(p.scales)[row * p.scale_pitch + (c >> 2)] = (uint8_t)code;
     } else {
-        uint32_t m = 0;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(u[i]) & 0x7FFFFFFFu);
-#pragma unroll
-        for (int o = 1; o < 4; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-        const uint32_t code = mx4_scale_code(m);
+        const uint32_t code = mx4_scale_code(block_max<true>(u, 4));
         if (!live) return;
         *reinterpret_cast<uint32_t *>(p.q + (row * p.d8 + c) * 4) = e2m1x8(u, mx4_inv_scale(code));
         if ((c & 3) == 0)
@@ -179,7 +182,7 @@ __global__ void __launch_bounds__(1024) rmsnorm_kernel(const NormRows p) {
 // weight stays in registers.  The barrier of a row's sum is also what frees its place in the
 // ring.  Measured, of the copy bandwidth: backward of 16384 x 4096 83 us, 96 % (103 with a
 // row's loads into registers), of 4096 x 512 7.2 us (23 with one row a CTA); forward of
-// 4096 x 4096 with the residual 23 us, 86 %, with FP8 rows 28 us, 79 %: half of what the codes
+// 4096 x 4096 with the residual 23 us, 86 %, with FP8 rows 27.7 us, 81 %: half of what the codes
 // add is their bytes, half the instructions that make them.  The forward takes three CTAs an
 // SM and four rows ahead (23.2 and 28.3 us; four CTAs and two ahead 23.3 and 28.7, four and
 // three 24.0 and 29.1, three and two 24.0 and 30.0).
