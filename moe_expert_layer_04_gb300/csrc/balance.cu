@@ -14,7 +14,7 @@
 // (fp64 for the last two cost more than the rest of a small call: this GPU adds two of
 // them a cycle.)  Bound by HBM: the logits are read once in
 // each direction, and their gradient is written once.  Measured at 65536 x 384 in 16 sequences,
-// sigmoid: backward 34 us (87 % of the copy bandwidth by the rows of all tokens), forward 28: 21
+// sigmoid: backward 34 us (87 % of the copy bandwidth by the rows of all tokens), forward 27: 21
 // of the pass over the tokens, 70 % (it issues in 62 % of its cycles and waits for its loads in most others), the
 // rest of the sequences' sums, which begin when the last chunk ends.  Smallest call: 3.8 and
 // 2.4 us.
@@ -284,16 +284,17 @@ __global__ void __launch_bounds__(32 * kSeqWarps) balance_seq_kernel(const Balan
     __shared__ float term[kSeqCols / 32];
     __shared__ float terms[8];   // of the first CTA: one for each CTA of the cluster
     __shared__ int n_all;
-    wait_for_kernels_ahead();
-    let_kernels_behind_begin();
+    // (the kernel ahead lets this one begin when all its CTAs have waited for what came before
+    // it: the offsets are there)
     const int q = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int a = seq_begin(p, q), b = seq_begin(p, q + 1);
     const int c0 = a / p.chunk, c1 = b > a ? (b - 1) / p.chunk : c0 - 1;
     if (threadIdx.x == 0) n_all = 0;
     __syncthreads();
+    wait_for_kernels_ahead();
+    let_kernels_behind_begin();
     int n = 0;
     for (int c = c0 + threadIdx.x; c <= c1; c += blockDim.x) n += p.part_n[c + q];
-    if (n) atomicAdd(&n_all, n);
     float s[4] = {};
     int32_t k[4] = {};
     const int col = blockIdx.x * kSeqCols + lane;
@@ -312,6 +313,7 @@ __global__ void __launch_bounds__(32 * kSeqWarps) balance_seq_kernel(const Balan
         sum[warp][lane + 32 * j] = s[j];
         cnt[warp][lane + 32 * j] = k[j];
     }
+    if (n) atomicAdd(&n_all, n);
     __syncthreads();
     n = n_all;
     if (threadIdx.x < kSeqCols) {
