@@ -331,3 +331,32 @@ def test_offsets_that_do_not_fit():
                 assert (out[R_:] == 3.0).all()
                 got.append(out)
             assert torch.equal(got[0], got[1])
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("cuts,R,N,K", [([], 512, 512, 2048), ([700, 701, 1700], 2600, 768, 640),
+                                        ([60, 61], 200, 512, 1024), ([], 1, 2048, 4096)])
+def test_inputs_in_turn(cuts, R, N, K, bits):
+    """Three inputs in turn, launched behind one another: every product as it is alone, bit for
+    bit (a stage with another call's codes or scales would show)."""
+    G = len(cuts) + 1
+    g = torch.Generator(device="cuda").manual_seed(R)
+    u8 = lambda lo, hi, *s: torch.randint(lo, hi, s, generator=g, dtype=torch.uint8, device="cuda")
+    offs = torch.tensor([0] + cuts + [R], dtype=torch.int32, device="cuda")
+    sets = [(u8(0, 120 if bits == 8 else 256, R, K if bits == 8 else K // 2), u8(117, 132, R, _lib.moe_mx_sf_pitch(K)),
+             u8(0, 256, G, N, K // 2), u8(117, 132, G, N, _lib.moe_mx_sf_pitch(K))) for _ in range(3)]
+    out = torch.empty(R, N, dtype=torch.bfloat16, device="cuda")
+
+    def run(s):
+        _lib.moe_mx4_matmul(s[0], s[1], bits, offs, G, R, s[2], s[3], None, 0, N, K, out)
+        return out.view(torch.int16)
+    alone = []
+    for s in sets:
+        torch.cuda.synchronize()
+        alone.append(run(s).clone())
+    wrong = torch.zeros((), dtype=torch.int64, device="cuda")
+    for i in range(400):
+        out.zero_()
+        wrong += (run(sets[i % 3]) != alone[i % 3]).sum()
+    ok()
+    assert int(wrong) == 0

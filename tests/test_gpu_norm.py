@@ -253,3 +253,29 @@ def test_no_rows():
     forward(x, w, x)
     o = backward(x, w, empty(0, dtype=torch.float32), x, None)
     assert (f64(o["d_weight"]) == 0).all()
+
+
+@pytest.mark.parametrize("T,d,fmt", [(1500, 4096, _lib.MOE_ROWS_FP8), (1300, 3616, _lib.MOE_ROWS_MXFP4),
+                                     (700, 512, _lib.MOE_ROWS_MXFP8), (5, 2048, _lib.MOE_ROWS_FP8)])
+def test_inputs_in_turn(T, d, fmt):
+    """Both directions of three inputs in turn, launched behind one another: every result as it
+    is alone, bit for bit."""
+    rng = np.random.default_rng(d)
+    w = torch.from_numpy(rng.standard_normal(d).astype(np.float32))
+    calls = []
+    for _ in range(3):
+        a = forward(rows(rng, T, d), w, rows(rng, T, d), fmt)
+        b = backward(a["residual_out"], w, a["rstd"], rows(rng, T, d), rows(rng, T, d))
+        calls.append((a, b, [t.clone() for t in (a["y"], a["q"], a["rstd"], b["dx"], b["d_weight"])]))
+    wrong = torch.zeros((), dtype=torch.int64, device="cuda")
+    for i in range(200):
+        a, b, want = calls[i % 3]
+        got = a["y"], a["q"], a["rstd"], b["dx"], b["d_weight"]
+        for t in got:
+            t.zero_()
+        _lib.moe_rmsnorm(a)
+        _lib.moe_rmsnorm_backward(b)
+        for x, y in zip(got, want):
+            wrong += (x != y).sum()
+    ok()
+    assert int(wrong) == 0
