@@ -290,7 +290,7 @@ __global__ void __launch_bounds__(32 * kSeqWarps) balance_seq_kernel(const Balan
     const int a = seq_begin(p, q), b = seq_begin(p, q + 1);
     const int c0 = a / p.chunk, c1 = b > a ? (b - 1) / p.chunk : c0 - 1;
     if (threadIdx.x == 0) n_all = 0;
-    __syncthreads();
+    cluster_sync_all();   // the cluster's CTAs have begun: the first one's memory takes the terms
     wait_for_kernels_ahead();
     let_kernels_behind_begin();
     int n = 0;
