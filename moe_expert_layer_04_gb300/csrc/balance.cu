@@ -284,15 +284,13 @@ __global__ void __launch_bounds__(32 * kSeqWarps) balance_seq_kernel(const Balan
     __shared__ float term[kSeqCols / 32];
     __shared__ float terms[8];   // of the first CTA: one for each CTA of the cluster
     __shared__ int n_all;
-    // (the kernel ahead lets this one begin when all its CTAs have waited for what came before
-    // it: the offsets are there)
     const int q = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int a = seq_begin(p, q), b = seq_begin(p, q + 1);
-    const int c0 = a / p.chunk, c1 = b > a ? (b - 1) / p.chunk : c0 - 1;
     if (threadIdx.x == 0) n_all = 0;
     cluster_sync_all();   // the cluster's CTAs have begun: the first one's memory takes the terms
     wait_for_kernels_ahead();
     let_kernels_behind_begin();
+    const int a = seq_begin(p, q), b = seq_begin(p, q + 1);
+    const int c0 = a / p.chunk, c1 = b > a ? (b - 1) / p.chunk : c0 - 1;
     int n = 0;
     for (int c = c0 + threadIdx.x; c <= c1; c += blockDim.x) n += p.part_n[c + q];
     float s[4] = {};
