@@ -893,8 +893,9 @@ moe_status moe_rmsnorm_backward(const moe_norm_bwd_args *args, void *stream);
  * counts, seq_loss, loss and ws are not read).
  * 0 <= T <= 2^30, 1 <= n_seq <= 65535, 1 <= E <= 1024, 1 <= k <= 32 (above:
  * MOE_ERR_UNSUPPORTED).  seq_offsets int32 [n_seq+1] on the device, or NULL: one sequence of
- * all T tokens (n_seq = 1).  Offsets that descend or leave [0, T] are cut to it and recorded
- * as MOE_ERR_INVALID_ARG on the device, as are ids outside [0, E), which are not counted.
+ * all T tokens (n_seq = 1).  Offsets that leave [0, T] are cut to it and recorded as
+ * MOE_ERR_INVALID_ARG on the device, as are ids outside [0, E), which are not counted, and
+ * offsets that descend: nothing is counted then, and every output is zero.
  * logits and dlogits 16-byte aligned; dlogits may be logits.  Workspace:
  * moe_balance_workspace_size(T, E, n_seq) bytes, 16-byte aligned (0: not supported). */
 typedef enum { MOE_SCORE_SIGMOID = 0, MOE_SCORE_SOFTMAX = 1 } moe_score;

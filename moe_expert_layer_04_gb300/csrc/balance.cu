@@ -45,6 +45,7 @@ struct BalanceParams {
     int32_t *part_c;   // [slots, E]
     int32_t *part_n;   // [slots]
     unsigned *done;    // sequences that are finished
+    unsigned *descend; // the sequences' offsets do
     int *status;
 };
 
@@ -166,11 +167,15 @@ __global__ void __launch_bounds__(32 * (ONE ? kOneWarps : kWarps), !ONE && N * V
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     int32_t *hist = reinterpret_cast<int32_t *>(sm + kWarps * p.E);
     if (!ONE && blockIdx.x == 0 && threadIdx.x == 0) *p.done = 0;
+    // Offsets that descend leave the slots of some (chunk, sequence) unwritten and give others
+    // to two of them: nothing is counted then.
+    bool descend = false;
     if (blockIdx.x == 0 && p.seq_offsets) {
         for (int q = threadIdx.x; q <= p.n_seq; q += blockDim.x) {
             const int o = p.seq_offsets[q];
-            if (o < 0 || o > p.T || (q > 0 && p.seq_offsets[q - 1] > o))
-                record_status(p.status, MOE_ERR_INVALID_ARG);
+            const bool down = q > 0 && seq_begin(p, q - 1) > seq_begin(p, q);
+            if (o < 0 || o > p.T || down) record_status(p.status, MOE_ERR_INVALID_ARG);
+            descend = descend || down;
         }
     }
     const int end = min(p.T, (int)(blockIdx.x + 1) * p.chunk);
@@ -237,14 +242,16 @@ __global__ void __launch_bounds__(32 * (ONE ? kOneWarps : kWarps), !ONE && N * V
             }
             __syncthreads();
         }
-        n = n_valid;
+        bool counted = true;
+        if constexpr (ONE) counted = !__syncthreads_or(descend);
+        n = counted ? n_valid : 0;
         if constexpr (ONE) {
             float mine = 0.0f;
             for (int e = threadIdx.x; e < p.E; e += blockDim.x) {
                 float v = 0.0f;
 #pragma unroll
                 for (int w = 0; w < kWarps; ++w) v += sm[w * p.E + e];
-                mine += finish(p, q, e, n, hist[e], v);
+                mine += finish(p, q, e, n, counted ? hist[e] : 0, v);
             }
             mine = warp_sum(mine);
             if (lane == 0) term[warp] = mine;
@@ -269,7 +276,12 @@ __global__ void __launch_bounds__(32 * (ONE ? kOneWarps : kWarps), !ONE && N * V
         }
         a = b;
     }
-    if (ONE && threadIdx.x == 0) p.loss[0] = p.alpha * loss / (float)p.n_seq;
+    if constexpr (ONE) {
+        if (threadIdx.x == 0) p.loss[0] = p.alpha * loss / (float)p.n_seq;
+    } else if (blockIdx.x == 0) {
+        descend = __syncthreads_or(descend);
+        if (threadIdx.x == 0) *p.descend = descend;
+    }
 }
 
 // A cluster for each sequence, a CTA of it for 128 columns: 32 warps take the sequence's
@@ -290,7 +302,8 @@ __global__ void __launch_bounds__(32 * kSeqWarps) balance_seq_kernel(const Balan
     wait_for_kernels_ahead();
     let_kernels_behind_begin();
     const int a = seq_begin(p, q), b = seq_begin(p, q + 1);
-    const int c0 = a / p.chunk, c1 = b > a ? (b - 1) / p.chunk : c0 - 1;
+    const bool counted = *p.descend == 0;
+    const int c0 = a / p.chunk, c1 = counted && b > a ? (b - 1) / p.chunk : c0 - 1;
     int n = 0;
     for (int c = c0 + threadIdx.x; c <= c1; c += blockDim.x) n += p.part_n[c + q];
     float s[4] = {};
@@ -502,7 +515,7 @@ struct BwdLaunch {
 size_t balance_workspace_bytes(int T, int E, int n_seq) {
     const int C = part_chunk(T);
     const size_t slots = (size_t)((T + C - 1) / C) + n_seq;
-    return slots * E * 8 + slots * 4 + 4;
+    return slots * E * 8 + slots * 4 + 8;
 }
 
 moe_status launch_balance(const moe_balance_args *a, cudaStream_t st) {
@@ -522,7 +535,8 @@ moe_status launch_balance(const moe_balance_args *a, cudaStream_t st) {
     p.part_c = reinterpret_cast<int32_t *>(p.part_p + slots * a->E);
     p.part_n = p.part_c + slots * a->E;
     p.done = reinterpret_cast<unsigned *>(p.part_n + slots);
-    if (p.n_chunks == 0) p.n_chunks = 1;   // (no token: it sets `done`)
+    p.descend = p.done + 1;
+    if (p.n_chunks == 0) p.n_chunks = 1;   // (no token: it sets `done` and `descend`)
     const moe_status s = by_columns<PartLaunch>(a, p, st);
     if (s != MOE_OK) return s;
     cudaLaunchConfig_t cfg = {};
