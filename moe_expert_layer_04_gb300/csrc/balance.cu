@@ -111,11 +111,38 @@ struct Row {
     }
 };
 
+// Sigmoids that are all small lose bits below fp32's normal range, and their sum's reciprocal
+// may be none (logits of -88 and less).  Below this sum (above it a score that fp32 cannot
+// hold is a share below 2^-105) the scores of the row r of such a token are taken relative to
+// the largest, s e^-m = e^(z - m) (1 - s), whose common factor leaves p as it is.
+constexpr float kLowSum = 0x1p-20f;
+template <int VEC, int N>
+__device__ __forceinline__ float low_shares(const Row<VEC, N> &r, float (&p)[N][VEC]) {
+    float m = -INFINITY, sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) m = fmaxf(m, r.z[i][j]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    if (m == -INFINITY) m = 0.0f;   // nothing is left: every term is zero
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) {
+            const float z = r.z[i][j];   // (below zero)
+            p[i][j] = __fdividef(__expf(z - m), 1.0f + __expf(z));
+            sum += p[i][j];
+        }
+    sum = warp_sum(sum);
+    return sum == 0.0f ? 0.0f : 1.0f / sum;
+}
+
 // z -> s (columns outside E: zeros), p is s times what it returns; slope = 1 - s for the
-// sigmoid, 1 otherwise.
+// sigmoid, 1 otherwise.  low: the scores have to be low_shares().
 template <bool SOFTMAX, int VEC, int N>
 __device__ __forceinline__ float shares(const Row<VEC, N> &r, float (&p)[N][VEC],
-                                       float (&slope)[N][VEC]) {
+                                       float (&slope)[N][VEC], bool &low) {
     float sum = 0.0f;
     if constexpr (SOFTMAX) {
         float m = -INFINITY;   // (a NaN makes the sum one)
@@ -148,6 +175,7 @@ __device__ __forceinline__ float shares(const Row<VEC, N> &r, float (&p)[N][VEC]
             }
     }
     sum = warp_sum(sum);
+    low = !SOFTMAX && sum < kLowSum;
     return sum == 0.0f ? 0.0f : 1.0f / sum;
 }
 
@@ -196,6 +224,7 @@ __global__ void __launch_bounds__(32 * (ONE ? kOneWarps : kWarps), !ONE && N * V
             // be a second trip to memory for every token)
             const int tl = t0 + lane * WARPS;
             unsigned left = __ballot_sync(0xffffffffu, tl < b && (!p.valid || __ldg(p.valid + tl)));
+            [[maybe_unused]] bool any_low = false;
             n += __popc(left);
             while (left) {
                 Row<VEC, N> r[UNROLL];
@@ -214,7 +243,12 @@ __global__ void __launch_bounds__(32 * (ONE ? kOneWarps : kWarps), !ONE && N * V
                 for (int u = 0; u < UNROLL; ++u) {
                     if (!live[u]) continue;
                     float s[N][VEC], slope[N][VEC];
-                    const float inv = shares<SOFTMAX>(r[u], s, slope);
+                    bool is_low;
+                    float inv = shares<SOFTMAX>(r[u], s, slope, is_low);
+                    if (is_low) {
+                        any_low = true;
+                        inv = 0.0f;
+                    }
 #pragma unroll
                     for (int i = 0; i < N; ++i)
 #pragma unroll
@@ -223,6 +257,26 @@ __global__ void __launch_bounds__(32 * (ONE ? kOneWarps : kWarps), !ONE && N * V
                         if ((unsigned)id[u] < (unsigned)p.E) atomicAdd(hist + id[u], 1);
                         else record_status(p.status, MOE_ERR_INVALID_ARG);
                     }
+                }
+            }
+            if constexpr (!SOFTMAX) {
+                // the low ones, all of them looked at again (which leaves the loop above its
+                // registers)
+                left = any_low ? __ballot_sync(0xffffffffu, tl < b && (!p.valid || __ldg(p.valid + tl)))
+                               : 0;
+                for (; left; left &= left - 1) {
+                    const int t = t0 + (__ffs(left) - 1) * WARPS;
+                    Row<VEC, N> r;
+                    r.load(p.logits + (size_t)t * p.E, p.E);
+                    float s[N][VEC], slope[N][VEC];
+                    bool is_low;
+                    shares<false>(r, s, slope, is_low);
+                    if (!is_low) continue;
+                    const float inv = low_shares(r, s);
+#pragma unroll
+                    for (int i = 0; i < N; ++i)
+#pragma unroll
+                        for (int j = 0; j < VEC; ++j) acc[i][j] = fmaf(s[i][j], inv, acc[i][j]);
                 }
             }
         }
@@ -370,9 +424,11 @@ __global__ void __launch_bounds__(32 * kSeqWarps) balance_seq_kernel(const Balan
     if (lane == 0) p.loss[0] = p.alpha * sum_q / (float)p.n_seq;
 }
 
-// A warp takes `chunk` consecutive tokens; a sequence's load stays in its registers.
+// A warp takes `chunk` consecutive tokens; a sequence's load stays in its registers.  (Narrow
+// rows at 32 registers a thread: 30000 x 128 8.9 us, at the 39 that the compiler takes 10.9.)
 template <bool SOFTMAX, int VEC, int N>
-__global__ void __launch_bounds__(32 * kWarps) balance_bwd_kernel(const BalanceParams p) {
+__global__ void __launch_bounds__(32 * kWarps, N * VEC <= 4 ? 8 : 0)
+    balance_bwd_kernel(const BalanceParams p) {
     wait_for_kernels_ahead();
     let_kernels_behind_begin();
     const int lane = threadIdx.x & 31;
@@ -411,7 +467,12 @@ __global__ void __launch_bounds__(32 * kWarps) balance_bwd_kernel(const BalanceP
             Row<VEC, N> r;
             r.load(p.logits + (size_t)t * p.E, p.E);
             float s[N][VEC], slope[N][VEC];
-            const float inv = shares<SOFTMAX>(r, s, slope);
+            bool low;
+            float inv = shares<SOFTMAX>(r, s, slope, low);
+            if (low) {
+                r.load(p.logits + (size_t)t * p.E, p.E);   // (again, for fewer registers)
+                inv = low_shares(r, s);
+            }
 #pragma unroll
             for (int i = 0; i < N; ++i)
 #pragma unroll
