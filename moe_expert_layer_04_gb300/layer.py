@@ -65,6 +65,14 @@ def _result(stream, device, *shape):
     return t
 
 
+def _capturing(stream):
+    """Whether calls on `stream` (None: the current one) go into a graph."""
+    if stream is None:
+        return torch.cuda.is_current_stream_capturing()
+    with torch.cuda.stream(stream):
+        return torch.cuda.is_current_stream_capturing()
+
+
 def ffn_fused_supported(d: int, I: int) -> bool:
     """Shapes the one-launch expert FFN (moe_expert_ffn_fused) takes: 256-wide
     tiles in both matmuls."""
@@ -797,7 +805,9 @@ class GroupedLinearMX4:
     changes.  Or codes=(w_q, w_sf), uint8 [G, N, K/2] and [G, N, moe_mx_sf_pitch(K)], with
     weight None.  G = 1 is a dense layer.  rows: the most rows of a call.  bits: of the rows,
     which each call quantises: 8 (MXFP8, K % 128 == 0) or 4 (MXFP4, K % 32 == 0: twice the
-    tensor rate, with the rows' rounding errors those of the weights)."""
+    tensor rate, with the rows' rounding errors those of the weights).  The buffers for the
+    quantised rows of a stream are made at its first call and kept, so that calls on several
+    streams may run at once; a captured call has its own."""
 
     def __init__(self, weight, rows: int, bits: int = 8, codes=None):
         if (weight is None) == (codes is None):
@@ -818,8 +828,23 @@ class GroupedLinearMX4:
         else:
             self.w_q, self.w_sf = codes
             _expect("codes", self.w_sf, G, N, pitch)
-        self.x_q = torch.empty(self.rows, K if bits == 8 else K // 2, **u8)
-        self.x_sf = torch.empty(self.rows, pitch, **u8)
+        self._row_buffers = {}   # codes and scales of the rows, by stream
+
+    def _rows_of(self, stream):
+        """Codes and scales of the rows that a call on `stream` quantises, memory of that
+        stream."""
+        cuda = self.w_q.is_cuda
+        key = _lib._stream(stream) if cuda else stream
+        got = self._row_buffers.get(key)
+        capturing = cuda and _capturing(stream)
+        if got is None or capturing:
+            u8 = dict(dtype=torch.uint8, device=self.w_q.device)
+            with torch.cuda.stream(stream if cuda else None):   # (None: the current one)
+                got = (torch.empty(self.rows, self.K if self.bits == 8 else self.K // 2, **u8),
+                       torch.empty(self.rows, _lib.moe_mx_sf_pitch(self.K), **u8))
+            if not capturing:
+                self._row_buffers[key] = got
+        return got
 
     def quantize_weights(self, stream=None):
         if self.weight is None:
@@ -840,8 +865,9 @@ class GroupedLinearMX4:
         if R == 0:
             return y
         quantize = _lib.moe_mx_quantize if self.bits == 8 else _lib.moe_mx4_quantize
-        quantize(x, R, self.K, self.x_q, self.x_sf, stream)
-        _lib.moe_mx4_matmul(self.x_q, self.x_sf, self.bits, offsets, self.G, R, self.w_q, self.w_sf,
+        x_q, x_sf = self._rows_of(stream)
+        quantize(x, R, self.K, x_q, x_sf, stream)
+        _lib.moe_mx4_matmul(x_q, x_sf, self.bits, offsets, self.G, R, self.w_q, self.w_sf,
                             row_weight, R, self.N, self.K, y, stream)
         return y
 
