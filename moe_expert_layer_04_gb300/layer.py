@@ -65,12 +65,31 @@ def _result(stream, device, *shape):
     return t
 
 
-def _capturing(stream):
-    """Whether calls on `stream` (None: the current one) go into a graph."""
-    if stream is None:
-        return torch.cuda.is_current_stream_capturing()
-    with torch.cuda.stream(stream):
-        return torch.cuda.is_current_stream_capturing()
+class _StreamBuffers:
+    """Tensors of the given (shape, dtype)s for the calls of each stream, made at its first
+    one and kept; a captured call gets its own."""
+
+    def __init__(self, device, *specs):
+        self.device, self.specs, self.kept = device, specs, {}
+
+    def of(self, stream):
+        """Those of `stream` (None: the current one), memory of that stream."""
+        if self.device.type != "cuda":
+            return self._of_current(stream)
+        if stream is None:
+            return self._of_current(_lib._stream(None))
+        with torch.cuda.stream(stream):
+            return self._of_current(stream.cuda_stream)
+
+    def _of_current(self, key):
+        capturing = self.device.type == "cuda" and torch.cuda.is_current_stream_capturing()
+        got = None if capturing else self.kept.get(key)
+        if got is None:
+            got = tuple(torch.empty(*shape, dtype=t, device=self.device)
+                        for shape, t in self.specs)
+            if not capturing:
+                self.kept[key] = got
+        return got
 
 
 def ffn_fused_supported(d: int, I: int) -> bool:
@@ -734,6 +753,9 @@ class GroupedLinearFP8:
     with quantize_weights() after it changes.  G = 1 is a dense layer.  rows:
     the most rows of a call.  offsets: int32 [G+1] on the device, the groups'
     first rows (as moe_permute writes them), the last one the number of rows.
+    The buffers for the quantised rows x of a stream are made at its first call and
+    kept, so that forward calls on several streams may run at once; a captured call
+    has its own.  The backward is that of the last forward, whichever its stream.
     """
 
     def __init__(self, weight, rows: int):
@@ -748,7 +770,8 @@ class GroupedLinearFP8:
         u8, f32 = dict(dtype=torch.uint8, device=dev), dict(dtype=torch.float32, device=dev)
         self.w_q, self.w_s = torch.empty(G, N, K, **u8), torch.empty(G, bn, bk, **f32)
         self.wt_q, self.wt_s = torch.empty(G, K, N, **u8), torch.empty(G, bk, bn, **f32)
-        self.x_q, self.x_s = torch.empty(rows, K, **u8), torch.empty(rows, bk, **f32)
+        self._buffers = _StreamBuffers(dev, ((self.rows, K), torch.uint8),
+                                       ((self.rows, bk), torch.float32))
         self.dy_q, self.dy_s = torch.empty(rows, N, **u8), torch.empty(rows, bn, **f32)
         self.dW = torch.empty(G, N, K, **f32)
         self.ws = torch.empty(n, **u8)
@@ -771,9 +794,10 @@ class GroupedLinearFP8:
         y = _result(stream, x.device, R, self.N)
         if R == 0:
             return y
-        _lib.moe_fp8_quantize(x, R, self.K, self.x_q, self.x_s, stream)
-        _lib.moe_fp8_matmul(self.x_q, self.x_s, offsets, self.G, R, self.w_q, self.w_s, None, 0,
-                            self.N, self.K, y, stream)
+        x_q, x_s = self._buffers.of(stream)
+        _lib.moe_fp8_quantize(x, R, self.K, x_q, x_s, stream)
+        _lib.moe_fp8_matmul(x_q, x_s, offsets, self.G, R, self.w_q, self.w_s, None, 0, self.N,
+                            self.K, y, stream)
         return y
 
     def backward(self, dy, stream=None):
@@ -828,23 +852,9 @@ class GroupedLinearMX4:
         else:
             self.w_q, self.w_sf = codes
             _expect("codes", self.w_sf, G, N, pitch)
-        self._row_buffers = {}   # codes and scales of the rows, by stream
-
-    def _rows_of(self, stream):
-        """Codes and scales of the rows that a call on `stream` quantises, memory of that
-        stream."""
-        cuda = self.w_q.is_cuda
-        key = _lib._stream(stream) if cuda else stream
-        got = self._row_buffers.get(key)
-        capturing = cuda and _capturing(stream)
-        if got is None or capturing:
-            u8 = dict(dtype=torch.uint8, device=self.w_q.device)
-            with torch.cuda.stream(stream if cuda else None):   # (None: the current one)
-                got = (torch.empty(self.rows, self.K if self.bits == 8 else self.K // 2, **u8),
-                       torch.empty(self.rows, _lib.moe_mx_sf_pitch(self.K), **u8))
-            if not capturing:
-                self._row_buffers[key] = got
-        return got
+        self._buffers = _StreamBuffers(
+            self.w_q.device, ((self.rows, K if bits == 8 else K // 2), torch.uint8),
+            ((self.rows, pitch), torch.uint8))
 
     def quantize_weights(self, stream=None):
         if self.weight is None:
@@ -865,7 +875,7 @@ class GroupedLinearMX4:
         if R == 0:
             return y
         quantize = _lib.moe_mx_quantize if self.bits == 8 else _lib.moe_mx4_quantize
-        x_q, x_sf = self._rows_of(stream)
+        x_q, x_sf = self._buffers.of(stream)
         quantize(x, R, self.K, x_q, x_sf, stream)
         _lib.moe_mx4_matmul(x_q, x_sf, self.bits, offsets, self.G, R, self.w_q, self.w_sf,
                             row_weight, R, self.N, self.K, y, stream)
