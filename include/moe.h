@@ -707,7 +707,7 @@ moe_status moe_fp8_wgrad(const uint16_t *a, const uint16_t *b, const int32_t *of
  *   y[r]    = bf16( row_weight[r] * (h~[r] W2~[g]^T) )
  * x_perm_q [R, d] / x_perm_s, W13_q [G, 2I, d] / W13_s, W2_q [G, d, I] / W2_s;
  * outputs h_q [R, I], h_s [R, I/128] and y_perm [R, d] bf16.  d % 128 == 0,
- * I % 128 == 0 (else MOE_ERR_UNSUPPORTED).  No workspace. */
+ * I % 128 == 0, G max(2I, d) < 2^31 (else MOE_ERR_UNSUPPORTED).  No workspace. */
 moe_status moe_expert_ffn_fp8(const uint8_t *x_perm_q, const float *x_perm_s,
                               const int32_t *offsets, int G, int max_rows, const uint8_t *W13_q,
                               const float *W13_s, const uint8_t *W2_q, const float *W2_s,

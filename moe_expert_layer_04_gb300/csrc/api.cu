@@ -1347,7 +1347,7 @@ moe_status moe_expert_ffn_fp8(const uint8_t *x_perm_q, const float *x_perm_s,
                               const float *row_weight, int S, int d, int I, float clamp,
                               uint8_t *h_q, float *h_s, uint16_t *y_perm, void *stream) {
     if (!fp8_groups_ok(G, max_rows) || d < 1 || I < 1 || S < 0) return MOE_ERR_INVALID_ARG;
-    if (d % 128 != 0 || I % 128 != 0 || (long long)G * (2LL * I > d ? 2LL * I : d) >= (1LL << 31) - 256)
+    if (d % 128 != 0 || I % 128 != 0 || (long long)G * (2LL * I > d ? 2LL * I : d) >= (1LL << 31))
         return MOE_ERR_UNSUPPORTED;
     if (!offsets || !(clamp > 0.0f) ||
         !all_aligned16({x_perm_q, x_perm_s, W13_q, W13_s, W2_q, W2_s, h_q, h_s, y_perm}))
