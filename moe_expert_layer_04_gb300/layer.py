@@ -418,17 +418,27 @@ class MoELayer:
         if t is not None and t.numel() < D.T * D.d:
             raise ValueError(f"{name}: shape {tuple(t.shape)}, the layer has T = {D.T}, d = {D.d}")
 
-    def dispatch(self, x, stream=None):
+    def dispatch(self, x, stream=None, codes=None):
+        """The rows x [T, d] to their experts, in the type that the expert matmuls read.
+        codes: (codes, scales) of these rows where they are there already, as norm() of
+        dims.T rows writes them to (self.xn_q, self.xn_s): those move, and x is not read."""
         D = self.dims
         self._rows("x", x)
         low = self.mx or self.fp8 or self.mx4
+        if codes is not None:
+            if not low:
+                raise ValueError("codes: this layer's expert matmuls read bf16 rows")
+            moves = list(zip(codes, (self.x_perm_q,
+                                     self.x_perm_s if self.fp8 else self.x_perm_sf)))
+            for src, dst in moves:
+                if tuple(src.shape) != (D.T, dst.shape[1]) or src.dtype != dst.dtype:
+                    raise ValueError(f"codes: {src.dtype} {tuple(src.shape)}, expected "
+                                     f"{dst.dtype} {(D.T, dst.shape[1])}")
         _lib.moe_permute(self.ids, self.weights, None if low else x, D.T, D.d, D.E, D.k,
                          self.counts, self.offsets, self.row_token, self.slot_row,
                          self.row_weight, None if low else self.x_perm, self.ws, stream)
-        if low and self.norm_eps is not None and x is self.xn:
-            # the norm has quantised the rows: their codes and scales move
-            for src, dst in ((self.xn_q, self.x_perm_q),
-                             (self.xn_s, self.x_perm_s if self.fp8 else self.x_perm_sf)):
+        if codes is not None:
+            for src, dst in moves:
                 _lib.moe_gather_rows(src, self.row_token, dst, stream)
             return
         if self.fp8:
@@ -499,9 +509,9 @@ class MoELayer:
 
     def norm(self, x, residual=None, stream=None):
         """The norm ahead of the layer: (rows [T, d] bf16, the residual stream after the
-        addition).  Of dims.T rows into the layer's own buffers (with the codes of a
-        low-precision layer, which dispatch() of these rows moves: they are not changed in
-        between); of any other number, for forward_few(), new tensors."""
+        addition).  Of dims.T rows into the layer's own buffers, in a low-precision layer
+        with their codes and scales (self.xn_q and self.xn_s, for dispatch()); of any other
+        number, for forward_few(), new tensors."""
         D = self.dims
         if self.norm_eps is None:
             raise RuntimeError("layer built without norm_eps")
@@ -551,7 +561,8 @@ class MoELayer:
         if self.balance_alpha is not None:
             self._balance.update(seq_offsets=seq_offsets, valid=valid)   # (the backward's too)
             _lib.moe_balance_loss(self._balance, stream)
-        self.dispatch(x, stream)
+        self.dispatch(x, stream, None if self.norm_eps is None or self.xn_q is None
+                      else (self.xn_q, self.xn_s))
         self.experts(stream)
         self.combine(stream, y)
         return self.y if y is None else y
