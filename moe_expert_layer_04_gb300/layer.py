@@ -48,6 +48,11 @@ def fp8_supported(d: int, I: int) -> bool:
     return d % 128 == 0 and I % 128 == 0
 
 
+def norm_supported(d: int) -> bool:
+    """Row lengths the norm ahead of the layer (moe_rmsnorm) takes."""
+    return d % 8 == 0 and 8 <= d <= 32768
+
+
 def _expect(name, t, *shape):
     """A tensor, where it is given, has the elements that a call reads or writes."""
     if t is not None and t.numel() != math.prod(shape):
@@ -256,6 +261,8 @@ class MoELayer:
         w = self.w.get("norm")
         if w is None or tuple(w.shape) != (D.d,) or w.dtype != torch.float32:
             raise ValueError(f"a layer with norm_eps needs weights['norm'], fp32 [{D.d}]")
+        if not norm_supported(D.d):
+            raise ValueError(f"moe_rmsnorm does not take rows of {D.d}")
         self.xn = torch.empty(D.T, D.d, dtype=torch.bfloat16, **e)
         self.rstd = torch.empty(D.T, dtype=torch.float32, **e)
         self.residual = self._stream_rows = torch.empty(D.T, D.d, dtype=torch.bfloat16, **e)
@@ -293,8 +300,10 @@ class MoELayer:
             loss=self.balance_loss, ws=torch.empty(size, dtype=torch.uint8, **e))
         if self.backward_enabled:
             self._balance["dlogits"] = torch.empty(D.T, D.E, **f32)
-            self.ws_gate = torch.empty(_lib.moe_gate_bwd_workspace_size(D.T, D.d, D.E),
-                                       dtype=torch.uint8, **e)
+            size = _lib.moe_gate_bwd_workspace_size(D.T, D.d, D.E)
+            if size == 0:
+                raise ValueError(f"unsupported balance loss of a training layer of {D}")
+            self.ws_gate = torch.empty(size, dtype=torch.uint8, **e)
 
     def _init_mx4(self, e):
         D = self.dims
