@@ -265,7 +265,7 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_gemm_kernel(const __grid_cons
             mbar_init(&empty[s], 1);
         }
         for (int s = 0; s < SH::SLOTS; ++s) {
-            mbar_init(&sfready[s], (1 + SH::NB) * CL);
+            mbar_init(&sfready[s], 1 + SH::NB);
             mbar_init(&sfempty[s], 1);
         }
         for (int a = 0; a < 2; ++a) {
@@ -337,6 +337,7 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_gemm_kernel(const __grid_cons
         uint32_t begun = 0;   // stages with a copy, and its parity
         bool ok = true;
         int g = 0;
+        uint32_t j = 0, jph = 0;   // scale slot
         Walk at(p.n_tiles, first, step);
         for (long long t = first; ok && t < total; t += step, at.next()) {
             const Tile ti = find_tile<CL>(p, at.q, at.nt, mt_start, offs, g, rank);
@@ -345,6 +346,16 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_gemm_kernel(const __grid_cons
             const int br = MODE == MX4_FFN1 ? g * 2 * p.I + ti.nt * (BN / 2) : g * p.N + ti.nt * BN;
             for (int kb = 0; kb < p.kb; ++kb) {
                 if (!mbar_wait_warp(&empty[s], ph ^ 1u, wc)) { ok = false; break; }
+                // A pair's odd CTA: its scales of a slot are in its shared memory before the
+                // slot's first codes are asked for, whose arrival in the even CTA, which
+                // issues the pair's MMAs, so tells of both.  (An arrival of its own there,
+                // released at cluster scope, takes a warp a microsecond, more than a slot
+                // lasts: 12345 rows of 33 groups 66.7 us, by two more warps in turn 56.8, so
+                // 55.5; the long FFN 609, 627 and 590.)
+                if (CL == 2 && rank == 1 && kb % SH::SPS == 0) {
+                    if (!mbar_wait_warp(&sfready[j], jph, wc)) { ok = false; break; }
+                    if (++j == SH::SLOTS) { j = 0; jph ^= 1u; }
+                }
                 if (lane == 0) {
                     uint8_t *a = smem + s * SH::STAGE;
                     uint8_t *b = a + kCodeA;
@@ -400,7 +411,8 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_gemm_kernel(const __grid_cons
             for (int kb = 0; kb < p.kb; ++kb) {
                 const int w0 = kb % SH::SPS * SH::WORDS;   // first word of the slot's rows
                 if ((w0 == 0 && !mbar_wait_warp(&sfready[j], jph, wc)) ||
-                    !mbar_wait_warp(&full[s], ph, wc)) {
+                    !(CL == 2 && w0 == 0 ? mbar_wait_cluster_warp(&full[s], ph, wc)
+                                         : mbar_wait_warp(&full[s], ph, wc))) {
                     ok = false;
                     break;
                 }
@@ -521,10 +533,7 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_gemm_kernel(const __grid_cons
                                  x[3].w & mask[3]);
                     fence_proxy_async_smem();   // the copies into tensor memory read them
                     __syncwarp();
-                    if (lane == 0) {
-                        if (rank == 0) mbar_arrive(&sfready[j]);
-                        else mbar_arrive_remote_own(dsmem_map(&sfready[j], 0));
-                    }
+                    if (lane == 0) mbar_arrive(&sfready[j]);
                     if (++j == SH::SLOTS) { j = 0; jph ^= 1u; }
                     load(i);
                 }

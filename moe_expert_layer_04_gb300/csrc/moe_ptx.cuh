@@ -177,14 +177,6 @@ __device__ __forceinline__ void mbar_arrive_remote_relaxed(uint32_t addr) {
                  : "memory");
 }
 
-// The same arrival with release semantics among this CTA's threads: for a signal behind
-// writes to this CTA's own shared memory that this SM reads itself, through the async proxy
-// (fence_proxy_async_smem first), when the pair's other CTA issues the pair's MMAs.  A
-// release at cluster scope takes a microsecond of the warp.
-__device__ __forceinline__ void mbar_arrive_remote_own(uint32_t addr) {
-    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
-}
-
 __device__ __forceinline__ bool mbar_try_wait_cluster(uint32_t bar, uint32_t parity) {
     uint32_t ok;
     asm volatile(
@@ -213,6 +205,12 @@ __device__ __forceinline__ bool mbar_wait_cluster(uint64_t *bar, uint32_t parity
             return false;
         }
     }
+}
+
+// The same for a whole warp, with one answer for all its lanes.
+__device__ __forceinline__ bool mbar_wait_cluster_warp(uint64_t *bar, uint32_t parity,
+                                                       const WaitCtl &w) {
+    return __all_sync(0xffffffffu, mbar_wait_cluster(bar, parity, w));
 }
 
 // -------------------------------------------- counters between CTAs
