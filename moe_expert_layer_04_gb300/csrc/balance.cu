@@ -26,7 +26,7 @@ namespace moe {
 namespace {
 
 constexpr int kWarps = 8;
-constexpr int kOneWarps = 16, kOneTokens = 128, kOneSeqs = 4;
+constexpr int kOneWarps = 16, kOneTokens = 128;   // of the one CTA that takes a small call
 
 struct BalanceParams {
     int T, E, k, n_seq, chunk, n_chunks;
@@ -584,8 +584,12 @@ moe_status launch_balance(const moe_balance_args *a, cudaStream_t st) {
     p.status = device_status_ptr();
     if (!p.status) return MOE_ERR_CUDA;
     p.chunk = part_chunk(a->T);
-    // few tokens and sequences: one launch of one CTA instead of two of many
-    p.one = a->T <= kOneTokens && a->n_seq <= kOneSeqs;
+    // Few tokens and sequences: one launch of one CTA instead of two of many.  A token takes the
+    // one CTA as long as E + 300 numbers, a sequence as long as 28 tokens.  Measured, one sequence,
+    // us in one launch / in two: 64 tokens of 16 experts 3.7 / 7.3, 128 tokens of 384 7.7 / 7.9,
+    // 64 of 1024 8.7 / 8.6, 128 of 1024 13.4 / 8.6; four: 128 of 16 8.7 / 8.7, 32 of 384 9.3 / 9.8,
+    // 64 of 384 10.8 / 10.6, 8 of 1024 12.7 / 9.4.
+    p.one = a->T <= kOneTokens && (a->T + 28LL * (a->n_seq - 1)) * (a->E + 300) <= 88000;
     if (p.one) {
         p.chunk = kOneTokens;
         return by_columns<PartLaunch>(a, p, st);
