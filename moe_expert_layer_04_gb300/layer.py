@@ -385,6 +385,8 @@ class MoELayer:
         if "W13" not in self.w:
             raise RuntimeError("the layer was given quantised weights: there are none to quantise")
         W13, W2 = self.w["W13"], self.w["W2"]
+        _expect("W13", W13, G, 2 * D.I, D.d)
+        _expect("W2", W2, G, D.d, D.I)
         if self.mx4:
             _lib.moe_mx4_quantize(W13, G * 2 * D.I, D.d, self.W13_q, self.W13_sf, stream)
             _lib.moe_mx4_quantize(W2, G * D.d, D.I, self.W2_q, self.W2_sf, stream)
@@ -799,6 +801,7 @@ class GroupedLinearFP8:
         self.quantize_weights()
 
     def quantize_weights(self, stream=None):
+        _expect("weight", self.weight, self.G, self.N, self.K)
         _lib.moe_fp8_quantize_weights(self.weight, self.G, self.N, self.K, self.w_q, self.w_s,
                                       self.wt_q, self.wt_s, stream)
 
@@ -879,6 +882,7 @@ class GroupedLinearMX4:
     def quantize_weights(self, stream=None):
         if self.weight is None:
             raise RuntimeError("the projection was given quantised weights")
+        _expect("weight", self.weight, self.G, self.N, self.K)
         _lib.moe_mx4_quantize(self.weight, self.G * self.N, self.K, self.w_q, self.w_sf, stream)
 
     def forward(self, x, offsets, stream=None, row_weight=None):
