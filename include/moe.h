@@ -777,7 +777,8 @@ moe_status moe_layer_few(const moe_few_args *args, void *stream);
 moe_status moe_mx4_quantize(const uint16_t *src, long long rows, int K, uint8_t *q, uint8_t *sf,
                             void *stream);
 
-/* The values of an MXFP4 matrix in bf16 (exact), out [rows, K]. */
+/* The values of an MXFP4 matrix in bf16, out [rows, K]: exact, but for those beyond bf16's
+ * range (of scale codes 253 and 254), which are infinite. */
 moe_status moe_mx4_dequantize(const uint8_t *q, const uint8_t *sf, long long rows, int K,
                               uint16_t *out, void *stream);
 
@@ -827,7 +828,7 @@ moe_status moe_expert_ffn_mx4(const uint8_t *x_perm_q, const uint8_t *x_perm_sf,
  *   y    = bf16(u);  q, scales = u in the format's blocks (not of the rounded y)
  * x, residual, residual_out, y [T, d] bf16; weight [d] fp32; rstd [T] fp32.  residual and
  * residual_out (= v) are both given or both NULL; residual_out may be x or residual.
- * y and rstd may be NULL, and y too may be x.  format: MOE_ROWS_NONE (q and scales
+ * y and rstd may be NULL, and y too may be x (but not residual_out).  format: MOE_ROWS_NONE (q and scales
  * NULL), MOE_ROWS_FP8 (q [T, d], scales fp32 [T, ceil(d/128)], the rule of
  * moe_fp8_quantize), MOE_ROWS_MXFP8 (q [T, d], scales uint8 [T, moe_mx_sf_pitch(d)], as
  * moe_mx_quantize) or MOE_ROWS_MXFP4 (q [T, d/2], scales likewise, as moe_mx4_quantize).

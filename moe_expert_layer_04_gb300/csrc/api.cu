@@ -1439,6 +1439,7 @@ moe_status moe_rmsnorm(const moe_norm_args *a, void *stream) {
         (a->scales != nullptr) != coded)
         return MOE_ERR_INVALID_ARG;
     if (a->T == 0) return MOE_OK;
+    if (a->y && a->y == a->residual_out) return MOE_ERR_INVALID_ARG;
     if (!all_aligned16({a->x, a->weight}) || !aligned16(a->residual) ||
         !aligned16(a->residual_out) || !aligned16(a->y) || !aligned16(a->q) ||
         !aligned16(a->scales))
