@@ -176,7 +176,7 @@ __device__ __forceinline__ float shares(const Row<VEC, N> &r, float (&p)[N][VEC]
     }
     sum = warp_sum(sum);
     low = !SOFTMAX && sum < kLowSum;
-    return sum == 0.0f ? 0.0f : 1.0f / sum;
+    return (SOFTMAX ? sum == 0.0f : low) ? 0.0f : 1.0f / sum;
 }
 
 // CTA: one chunk of tokens, sequence by sequence; its warps take tokens in turn (UNROLL
@@ -244,11 +244,8 @@ __global__ void __launch_bounds__(32 * (ONE ? kOneWarps : kWarps), !ONE && N * V
                     if (!live[u]) continue;
                     float s[N][VEC], slope[N][VEC];
                     bool is_low;
-                    float inv = shares<SOFTMAX>(r[u], s, slope, is_low);
-                    if (is_low) {
-                        any_low = true;
-                        inv = 0.0f;
-                    }
+                    const float inv = shares<SOFTMAX>(r[u], s, slope, is_low);
+                    any_low |= is_low;
 #pragma unroll
                     for (int i = 0; i < N; ++i)
 #pragma unroll
