@@ -2,10 +2,10 @@
 // and the gate weight's:
 //   dX += dz W_g,   dW_g += dz^T x
 // Both products run on the tensor cores, as one group of the layer's data-gradient and
-// weight-gradient matmuls.  dz is their bf16 operand (2^-9 of itself; sums over the tokens
-// average that out), padded with zeros to whole tiles of 128 experts; dz W_g is rounded to
+// weight-gradient matmuls.  dz is their bf16 operand (off by at most 2^-8 of itself; sums over
+// the tokens average that out), padded with zeros to whole tiles of 128 experts; dz W_g is rounded to
 // bf16 before it is added.  Measured: 0.87 ms at 65536 tokens, d = 4096, E = 384 (127 us at
-// 8192), 1.3 % of the layer's backward there; so the sums stay a pass of their own, which
+// 8192), 1.3 % of the layer's step there; so the sums stay a pass of their own, which
 // leaves that backward as it is.
 #include "fp8_common.cuh"
 

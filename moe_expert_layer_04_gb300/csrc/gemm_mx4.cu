@@ -351,7 +351,7 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_gemm_kernel(const __grid_cons
                 // issues the pair's MMAs, so tells of both.  (An arrival of its own there,
                 // released at cluster scope, takes a warp a microsecond, more than a slot
                 // lasts: 12345 rows of 33 groups 66.7 us, by two more warps in turn 56.8, so
-                // 55.5; the long FFN 609, 627 and 590.)
+                // 55.1; the long FFN 609, 627 and 590.)
                 if (CL == 2 && rank == 1 && kb % SH::SPS == 0) {
                     if (!mbar_wait_warp(&sfready[j], jph, wc)) { ok = false; break; }
                     if (++j == SH::SLOTS) { j = 0; jph ^= 1u; }
@@ -702,12 +702,13 @@ int box_rows(int max_rows) { return max_rows < 128 ? (max_rows + 7) & ~7 : 128; 
 // over the SMs where there are few; pairs of CTAs (256 rows) only where groups hold 256 rows
 // on average, as a group's last pair is half empty more often than not.  The least of (rounds
 // of tiles over the SMs) x (ns of a stage, measured with many rounds: 8192 x 4096 x 4096 in
-// pairs 45 us, and 256 / 128 / 64 / 32 wide 54 / 59 / 95 / 182 with 4-bit rows, 74 and 91 / 106 /
+// pairs 46 us, and 256 / 128 / 64 / 32 wide 54 / 59 / 95 / 182 with 4-bit rows, 76 and 83 / 106 /
 // 162 / 298 with 8-bit ones).  4-bit rows, pairs 256 / 256 / 128 / 64 / 32 wide, us, the rule's
 // choice in brackets: 1 row - / 8.6 / 7.0 / 6.6 / [6.2], 512 rows 10.8 / 10.4 / [7.6] / 10.1 / 16.0,
-// 1024 rows [11.5] / 11.4 / 11.7 / 17.3 / 26.3; 4096 x 2048 weights of 33 groups: 500 rows 29.8 / 26.9
-// / [25.9] / 30.9 / 47.1, 6000 rows 40.9 / [35.8] / 40.5 / 54.7 / 96, 12345 rows [53.5] / 52.9 / 61.2 /
-// 87.3 / 158; of 9 groups, 288 rows 12.3 / [10.8] / 9.6 / 11.6 / 16.9 (not the fastest).
+// 1024 rows [11.5] / 11.4 / 11.7 / 17.3 / 26.3, 1280 rows 16.4 / 17.5 / [15.2]; 4096 x 2048 weights of
+// 33 groups: 500 rows 29.8 / 26.9 / [25.9] / 30.9 / 47.1, 6000 rows 40.9 / [35.8] / 40.5 / 54.7 / 96, 12345
+// rows 55.1 / [52.9] / 61.2 / 87.3 / 158; of 9 groups, 288 rows 12.3 / [10.8] / 9.6 / 11.6 / 16.9 (not
+// the fastest).
 struct TileChoice {
     int bn;
     bool pair;
@@ -716,7 +717,7 @@ TileChoice tile_shape(int max_rows, int G, int N, int bits, int narrowest) {
     // row tiles: one for each group, or half a tile more than its rows fill
     const int groups = G < max_rows ? G : max_rows;
     const int width[5] = {256, 256, 128, 64, 32};
-    const int ns[2][5] = {{310, 500, 265, 215, 200}, {330, 410, 240, 185, 170}};
+    const int ns[2][5] = {{430, 500, 270, 220, 210}, {354, 384, 246, 188, 173}};
     TileChoice best = {narrowest, false};
     long long least = -1;
     for (int i = 0; i < 5 && width[i] >= narrowest; ++i) {

@@ -33,7 +33,8 @@ def test_scales_of_a_pair_are_there_before_their_codes_are_asked_for():
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("cuts,R,N,K", [([], 512, 512, 2048), ([], 1024, 640, 544), ([900], 2600, 768, 8192),
-                                        ([300, 301, 900], 1500, 256, 1024)])
+                                        ([300, 301, 900], 1500, 256, 1024), ([], 2048, 2048, 544),
+                                        ([900], 2600, 1032, 4096), ([300, 301, 900], 2048, 4096, 1024)])
 @pytest.mark.parametrize("bits", [4, 8])
 def test_scales_alone_differ(cuts, R, N, K, bits):
     """Pairs of CTAs: calls in a row whose codes are the same and whose scales are not."""
@@ -61,3 +62,13 @@ def test_scales_alone_differ(cuts, R, N, K, bits):
         wrong += (run(scales[i % 3]) != alone[i % 3]).sum()
     ok()
     assert int(wrong) == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("counts,N,K", [([700, 1, 0, 900, 300], 1032, 288), ([1, 3333], 1032, 64),
+                                        ([255, 257, 1, 2000, 0, 300], 1032, 1120), ([2500, 1, 129], 4104, 96)])
+@pytest.mark.parametrize("bits", [4, 8])
+def test_pairs_where_groups_end(counts, N, K, bits):
+    """Groups that end in a pair's first row tile, with one row, or in its second."""
+    from tests.test_gpu_mx4 import test_matmul as check
+    check(counts, N, K if bits == 4 else (K + 127) // 128 * 128, bits, False)
