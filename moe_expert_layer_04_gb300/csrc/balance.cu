@@ -15,7 +15,7 @@
 // them a cycle.)  Bound by HBM: the logits are read once in
 // each direction, and their gradient is written once.  Measured at 65536 x 384 in 16 sequences,
 // sigmoid: backward 34 us (87 % of the copy bandwidth by the rows of all tokens), forward 28.5: 22
-// of the pass over the tokens, 67 % (it issues in 62 % of its cycles and waits for its loads in
+// of the pass over the tokens, 67 % (it issues in 60 % of its cycles and waits for its loads in
 // most others), the rest of the sequences' sums, which begin when the last chunk ends.
 // Smallest call: 3.9 and 2.4 us.
 #include <cstring>
