@@ -168,7 +168,9 @@ __device__ __forceinline__ float shares(const Row<VEC, N> &r, float (&p)[N][VEC]
             for (int j = 0; j < VEC; ++j) {
                 // both s and 1 - s without cancellation or overflow
                 const float z = r.z[i][j], t = __expf(-fabsf(z));
-                const float big = __fdividef(1.0f, 1.0f + t), small = t * big;
+                const float big = __fdividef(1.0f, 1.0f + t);
+                // (its own rounding wherever this is used: `low` below has one answer for a row)
+                const float small = __fmul_rn(t, big);
                 p[i][j] = z < 0.0f ? small : big;
                 slope[i][j] = z < 0.0f ? big : small;
                 sum += p[i][j];

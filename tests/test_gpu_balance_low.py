@@ -75,3 +75,17 @@ def test_equal_logits_have_equal_shares(value):
     r = B.reference(z.astype(np.float64), ids, B.SIG)
     assert abs(r["seq_loss"][0] - 1) < 1e-12
     B.check(a, r, np.where(np.abs(z) > 250, 0.0, z))
+
+
+@pytest.mark.parametrize("E", [16, 97, 384])
+def test_rows_on_the_border_count_once(E):
+    """Scores whose sum is about the one from which shares are taken relative to the largest
+    (2^-20), spread over some of fp32's steps around it: every row once."""
+    T, k = 1500, 2
+    mid = np.float32(np.log(2.0 ** -20 / E))
+    z = (mid + np.float32(2.0 ** -19) * np.arange(-T // 2, T - T // 2, dtype=np.float32))[:, None]
+    z = np.repeat(z, E, 1) + np.float32(2.0 ** -19) * np.random.default_rng(E).integers(-3, 4, (T, E)).astype(np.float32)
+    ids = (np.arange(k * T).reshape(T, k) % E).astype(np.int32)
+    a = B.call(z, ids, B.SIG)
+    ok()
+    B.check(a, B.reference(z.astype(np.float64), ids, B.SIG), z)
