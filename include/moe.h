@@ -828,12 +828,13 @@ moe_status moe_expert_ffn_mx4(const uint8_t *x_perm_q, const uint8_t *x_perm_sf,
  *   y    = bf16(u);  q, scales = u in the format's blocks (not of the rounded y)
  * x, residual, residual_out, y [T, d] bf16; weight [d] fp32; rstd [T] fp32.  residual and
  * residual_out (= v) are both given or both NULL; residual_out may be x or residual.
- * y and rstd may be NULL, and y too may be x (but not residual_out).  format: MOE_ROWS_NONE (q and scales
- * NULL), MOE_ROWS_FP8 (q [T, d], scales fp32 [T, ceil(d/128)], the rule of
- * moe_fp8_quantize), MOE_ROWS_MXFP8 (q [T, d], scales uint8 [T, moe_mx_sf_pitch(d)], as
- * moe_mx_quantize) or MOE_ROWS_MXFP4 (q [T, d/2], scales likewise, as moe_mx4_quantize).
+ * y and rstd may be NULL, and y too may be x, but not what residual_out is.  format:
+ * MOE_ROWS_NONE (q and scales NULL), MOE_ROWS_FP8 (q [T, d], scales fp32
+ * [T, ceil(d/128)], the rule of moe_fp8_quantize), MOE_ROWS_MXFP8 (q [T, d], scales uint8
+ * [T, moe_mx_sf_pitch(d)], as moe_mx_quantize) or MOE_ROWS_MXFP4 (q [T, d/2], scales
+ * likewise, as moe_mx4_quantize).
  * T >= 0; d % 8 == 0, with FP8 d % 16 == 0, with MX d % 32 == 0; d <= 32768 (else
- * MOE_ERR_UNSUPPORTED); eps > 0, finite.  A row whose squares leave fp32's range has
+ * MOE_ERR_UNSUPPORTED); 0 < eps < 1e30.  A row whose squares leave fp32's range has
  * rstd 0. */
 typedef enum {
     MOE_ROWS_NONE = 0, MOE_ROWS_FP8 = 1, MOE_ROWS_MXFP8 = 2, MOE_ROWS_MXFP4 = 3
